@@ -2,7 +2,8 @@
  * tcg.h -- C ABI of libtcg, a mixed-precision tensor-core GEMM for GB300
  * (sm_103a).
  *
- * The one operation (every entry point below serves it):
+ * The one operation (every entry point up to the section "Language-model products"
+ * serves it):
  *
  *     D = alpha * op(A) * op(B) + beta * C
  *
@@ -55,7 +56,7 @@
  * kernel has completed, so stream order is kept.  A handle is not thread-safe: use
  * one per host thread.  C must not overlap A or
  * B.  The first GEMM call on a handle binds it to the current device and
- * allocates a 4-byte device error word; make that call before any stream
+ * allocates a few KiB of device words (the error word, split counters); make that call before any stream
  * capture.  The TF32 path and split-K calls need a workspace (see
  * tcg_set_workspace).  Once bound, and with its workspace large enough, a
  * handle's device-buffer calls can be captured in a CUDA graph: they then make
@@ -400,6 +401,128 @@ tcgStatus_t tcg_gemm_split_k(tcgHandle_t h, int64_t m, int64_t n, int64_t k,
 /* Number of GEMM-path kernel launches this handle has made (for the
  * benchmark's launch count).  Returns 0 for NULL. */
 uint64_t tcg_launch_count(tcgHandle_t h);
+
+/* ---------------------------------------------------------- Language-model products
+ *
+ * The products of a transformer's layers with what surrounds them, on the same handles,
+ * streams, workspaces and errors as the GEMM calls above, and asynchronous like them.
+ * The pages have no counterpart to these: they are the library's own additions.
+ *
+ * Column-major as above: a row-major matrix of tokens x features (one row per token) is
+ * a column-major features x tokens matrix with one column per token.  A and B are FP16 or
+ * BF16 (both the same; ABtype), products exact, accumulation FP32; D is FP32 or ABtype
+ * (rounded to nearest even once, after the whole epilogue).  Matrices must be 16-byte
+ * aligned with leading dimensions (times the element size) a multiple of 16 bytes; m, n
+ * and k are arbitrary, zero included.  Element offsets are 64-bit.  The calls run on SM
+ * pairs (tcg_set_kernel_options' cta_group does not apply; its group_m does).
+ *
+ * Accuracy: the bound of tcg_gemm_ex on the accumulator; the epilogue runs in FP32 with
+ * exp and erfc to 1.5e-7 absolute or better; a D of ABtype adds one rounding.
+ *
+ * Errors: INVALID_VALUE (NULL handle or needed pointer, misalignment, negative sizes, a
+ * leading dimension too small, an unknown enumerator, host memory), NOT_SUPPORTED (type
+ * combination, extents near 2^31, more than 384 groups), and the CUDA errors of
+ * tcg_gemm_ex.  Nothing is launched after a failed check.  A device wait that runs out
+ * is reported by tcg_get_device_error, which also clears the split counters. */
+
+typedef enum {
+    TCG_ACT_NONE = 0,
+    TCG_ACT_RELU = 1,      /* max(x, 0) */
+    TCG_ACT_GELU = 2,      /* x Phi(x), Phi the normal distribution function */
+    TCG_ACT_GELU_TANH = 3, /* x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) / 2 */
+    TCG_ACT_SILU = 4       /* x / (1 + exp(-x)) */
+} tcgActivation_t;
+
+/* What happens to an accumulator: z = alpha * acc + bias, D = act(z) + beta * C. */
+typedef struct {
+    tcgActivation_t activation;
+    const void *bias;        /* m entries, one per row of D (per group: the next m); NULL: 0 */
+    tcgDataType_t bias_type; /* TCG_R_32F or ABtype */
+    float beta;              /* 0: C is not read */
+    const void *C;           /* m x n, type of D; may be D itself */
+    int64_t ldc;
+    void *Z;                 /* m x n, ABtype: receives z rounded; NULL: not kept */
+    int64_t ldz;
+} tcgEpilogue_t;
+
+/* D = act(alpha * op(A) * op(B) + bias) + beta * C, with op as in tcg_gemm_ex: the forward
+ * pass of a linear layer (row-major Y = X W^T: A = W with OP_T, B = X with OP_N, m = out
+ * features, n = tokens).  epilogue NULL: D = alpha * op(A) * op(B).  D and Z must not
+ * overlap A, B or each other.  Products with few tiles split K over the SMs and join the
+ * FP32 partial sums in a fixed order (workspace: tcg_gemm_epilogue_workspace_size). */
+tcgStatus_t tcg_gemm_epilogue(tcgHandle_t h, tcgOp_t transa, tcgOp_t transb, int64_t m, int64_t n,
+                              int64_t k, float alpha, const void *A, int64_t lda, const void *B,
+                              int64_t ldb, tcgDataType_t ABtype, void *D, tcgDataType_t Dtype,
+                              int64_t ldd, const tcgEpilogue_t *epilogue);
+
+/* Products grouped by expert.  The n columns of B and D (tokens, sorted by expert) fall
+ * into `groups` ranges offsets[g] .. offsets[g + 1] - 1, some possibly empty; offsets is a
+ * DEVICE array of groups + 1 non-decreasing entries in 0 .. n, read when the kernel runs.
+ *     D[:, range g] = act(alpha * op(A_g) * B[:, range g] + bias_g) + beta * C[:, range g]
+ * with A_g = A + g * strideA (elements) and bias_g = bias + g * m.  Columns in no range
+ * (before offsets[0], from offsets[groups] on) come out zero, in D and in Z.  Entries
+ * outside 0 .. n are taken as the nearest of the two; decreasing ones give an undefined D
+ * (no access out of bounds). */
+tcgStatus_t tcg_gemm_grouped(tcgHandle_t h, tcgOp_t transa, int64_t m, int64_t n, int64_t k,
+                             int64_t groups, const int64_t *offsets, float alpha, const void *A,
+                             int64_t lda, int64_t strideA, const void *B, int64_t ldb,
+                             tcgDataType_t ABtype, void *D, tcgDataType_t Dtype, int64_t ldd,
+                             const tcgEpilogue_t *epilogue);
+
+/* Workspace of the two calls above on h's device (binds h), groups = 0 for
+ * tcg_gemm_epilogue.  transb as in tcg_gemm_epilogue (OP_N for a grouped call). */
+tcgStatus_t tcg_gemm_epilogue_workspace_size(tcgHandle_t h, tcgOp_t transb, int64_t m, int64_t n,
+                                             int64_t k, int64_t groups, size_t *bytes);
+
+/* The weight gradients of a grouped product: one m x n matrix per group, summed over the
+ * group's tokens,
+ *     D_g = alpha * A[:, range g] * B[:, range g]^T,      D_g = D + g * strideD,
+ * A m x k and B n x k column-major, one column per token (k tokens), offsets as above with
+ * n = k.  A group without tokens gets zeros.  Tokens of other groups are never part of a
+ * sum, whatever they hold (NaN included).  No workspace. */
+tcgStatus_t tcg_gemm_grouped_k(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int64_t groups,
+                               const int64_t *offsets, float alpha, const void *A, int64_t lda,
+                               const void *B, int64_t ldb, tcgDataType_t ABtype, void *D,
+                               tcgDataType_t Dtype, int64_t ldd, int64_t strideD);
+
+/* The gradient of an epilogue: dZ = dD * act'(Z) (m x n, all of one 16-bit type, rounded
+ * once) and dbias[g * m + i] = the FP32 sum of row i of the unrounded dZ over group g's
+ * columns, in an order that depends only on the sizes.  offsets NULL with groups = 1: one
+ * group of all columns.  dZ or dbias may be NULL; dZ may be dD.  Z is not read for
+ * TCG_ACT_NONE.  Columns in no group get dZ = 0.  Workspace with dbias: at most
+ * 4 * m * groups * (n / (16 * groups) + 1) bytes. */
+tcgStatus_t tcg_epilogue_backward(tcgHandle_t h, tcgActivation_t activation, int64_t m, int64_t n,
+                                  int64_t groups, const int64_t *offsets, const void *dD,
+                                  int64_t lddd, const void *Z, int64_t ldz, tcgDataType_t type,
+                                  void *dZ, int64_t lddz, float *dbias);
+
+/* Softmax cross entropy of a linear head, without keeping the logits L = X W^T (rows x
+ * vocab).  X is row-major rows x k (leading dimension ldx >= k), W row-major vocab x k.
+ *     lse[i]  = log sum_v exp L[i, v]
+ *     loss[i] = lse[i] - L[i, targets[i]]
+ * both FP32.  targets is a device array of int64; a row whose target is ignore_index or
+ * outside 0 .. vocab - 1 does not count: loss 0 (lse is written all the same). */
+tcgStatus_t tcg_xent_forward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_t k, const void *X,
+                             int64_t ldx, const void *W, int64_t ldw, tcgDataType_t type,
+                             const int64_t *targets, int64_t ignore_index, float *loss, float *lse);
+
+/* Its gradient, with dloss[i] the upstream gradient of loss[i] and lse from the forward
+ * call (the gradient of lse itself is not taken):
+ *     G = dloss (exp(L - lse) - [v = target]),   dX = G W (rows x k),   dW = G^T X (vocab x k)
+ * rounded to `type`; either may be NULL.  The logits are formed again, a piece of the
+ * vocabulary at a time; a piece of G is held in `type` (256 MiB at most, or 256 columns).
+ * For FP16 it is held times a power of two chosen from max |dloss|, so that small
+ * probabilities keep their bits.  dX is summed over the pieces in FP32.  Rows that do not
+ * count contribute nothing, whatever they hold in dloss or lse. */
+tcgStatus_t tcg_xent_backward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_t k, const void *X,
+                              int64_t ldx, const void *W, int64_t ldw, tcgDataType_t type,
+                              const int64_t *targets, int64_t ignore_index, const float *lse,
+                              const float *dloss, void *dX, int64_t lddx, void *dW, int64_t lddw);
+
+/* Workspace of tcg_xent_forward (backward = 0) or tcg_xent_backward (1) on h's device
+ * (binds h).  INVALID_VALUE: NULL pointers, bad sizes or type. */
+tcgStatus_t tcg_xent_workspace_size(tcgHandle_t h, int64_t rows, int64_t vocab, int64_t k,
+                                    tcgDataType_t type, int backward, size_t *bytes);
 
 #ifdef __cplusplus
 }

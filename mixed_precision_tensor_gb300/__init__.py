@@ -12,6 +12,9 @@ Names mirror the C ABI: ``tcg_create``, ``tcg_destroy``, ``tcg_set_stream``,
 ``tcg_gemm_strided_batched``, ``tcg_get_device_error``, ``tcg_status_string``,
 ``tcg_set_debug``, ``tcg_launch_count``.  ``Handle`` and ``gemm_rowmajor`` are
 conveniences on top of them.
+
+``linear``, ``grouped_linear`` and ``linear_cross_entropy`` with their backward passes
+(module ``lm``) are the language-model products on torch tensors.
 """
 from __future__ import annotations
 
@@ -34,6 +37,7 @@ TCG_STATUS_ALLOC_FAILED = 7
 TCG_OP_N, TCG_OP_T = 0, 1
 TCG_R_16F, TCG_R_16BF, TCG_R_32F, TCG_R_8F_E4M3, TCG_R_8F_E5M2 = 0, 1, 2, 3, 4
 TCG_COMPUTE_32F, TCG_COMPUTE_32F_FAST_TF32, TCG_COMPUTE_32F_3XTF32 = 0, 1, 2
+TCG_ACT_NONE, TCG_ACT_RELU, TCG_ACT_GELU, TCG_ACT_GELU_TANH, TCG_ACT_SILU = 0, 1, 2, 3, 4
 
 EXPORTS = ("tcg_create", "tcg_destroy", "tcg_set_stream", "tcg_set_workspace",
            "tcg_gemm_workspace_size", "tcg_gemm_ex", "tcg_gemm_strided_batched",
@@ -43,10 +47,19 @@ EXPORTS = ("tcg_create", "tcg_destroy", "tcg_set_stream", "tcg_set_workspace",
            "tcg_read_clock_probe", "tcg_set_split_k", "tcg_split_k_plan",
            "tcg_gemm_split_k", "tcg_gemm_ex_host", "tcg_gemm_strided_batched_host",
            "tcg_tail_split_plan", "tcg_gemm_tile_plan", "tcg_set_tile_n",
-           "tcg_set_tf32_rounding")
+           "tcg_set_tf32_rounding", "tcg_gemm_epilogue", "tcg_gemm_grouped",
+           "tcg_gemm_grouped_k", "tcg_gemm_epilogue_workspace_size", "tcg_epilogue_backward",
+           "tcg_xent_forward", "tcg_xent_backward", "tcg_xent_workspace_size")
 
 _lock = threading.Lock()
 _lib = None
+
+
+class Epilogue(ctypes.Structure):
+    """tcgEpilogue_t of include/tcg.h: z = alpha * acc + bias, D = act(z) + beta * C."""
+    _fields_ = [("activation", ctypes.c_int), ("bias", ctypes.c_void_p),
+                ("bias_type", ctypes.c_int), ("beta", ctypes.c_float), ("C", ctypes.c_void_p),
+                ("ldc", ctypes.c_int64), ("Z", ctypes.c_void_p), ("ldz", ctypes.c_int64)]
 
 
 class TcgError(RuntimeError):
@@ -131,6 +144,30 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.tcg_gemm_tf32_noalloc.restype = st
         lib.tcg_gemm_tf32_noalloc.argtypes = [vp, ci, ci, i64, i64, i64, f32, vp, i64, vp, i64,
                                               f32, vp, i64]
+        pep = ctypes.POINTER(Epilogue)
+        lib.tcg_gemm_epilogue.restype = st
+        lib.tcg_gemm_epilogue.argtypes = [vp, ci, ci, i64, i64, i64, f32, vp, i64, vp, i64, ci, vp,
+                                          ci, i64, pep]
+        lib.tcg_gemm_grouped.restype = st
+        lib.tcg_gemm_grouped.argtypes = [vp, ci, i64, i64, i64, i64, vp, f32, vp, i64, i64, vp, i64,
+                                         ci, vp, ci, i64, pep]
+        lib.tcg_gemm_grouped_k.restype = st
+        lib.tcg_gemm_grouped_k.argtypes = [vp, i64, i64, i64, i64, vp, f32, vp, i64, vp, i64, ci,
+                                           vp, ci, i64, i64]
+        lib.tcg_gemm_epilogue_workspace_size.restype = st
+        lib.tcg_gemm_epilogue_workspace_size.argtypes = [vp, ci, i64, i64, i64, i64,
+                                                         ctypes.POINTER(ctypes.c_size_t)]
+        lib.tcg_epilogue_backward.restype = st
+        lib.tcg_epilogue_backward.argtypes = [vp, ci, i64, i64, i64, vp, vp, i64, vp, i64, ci, vp,
+                                              i64, vp]
+        lib.tcg_xent_forward.restype = st
+        lib.tcg_xent_forward.argtypes = [vp, i64, i64, i64, vp, i64, vp, i64, ci, vp, i64, vp, vp]
+        lib.tcg_xent_backward.restype = st
+        lib.tcg_xent_backward.argtypes = [vp, i64, i64, i64, vp, i64, vp, i64, ci, vp, i64, vp, vp,
+                                          vp, i64, vp, i64]
+        lib.tcg_xent_workspace_size.restype = st
+        lib.tcg_xent_workspace_size.argtypes = [vp, i64, i64, i64, ci, ci,
+                                                ctypes.POINTER(ctypes.c_size_t)]
         _lib = lib
         return lib
 
@@ -318,6 +355,60 @@ def tcg_noalloc_device_error(stream) -> int:
     return load_library().tcg_noalloc_device_error(stream)
 
 
+def tcg_gemm_epilogue(h, transa, transb, m, n, k, alpha, A, lda, B, ldb, ABtype, D, Dtype, ldd,
+                      epilogue: Epilogue | None = None) -> int:
+    return load_library().tcg_gemm_epilogue(h, transa, transb, m, n, k, alpha, _ptr(A), lda,
+                                            _ptr(B), ldb, ABtype, _ptr(D), Dtype, ldd, epilogue)
+
+
+def tcg_gemm_grouped(h, transa, m, n, k, groups, offsets, alpha, A, lda, strideA, B, ldb, ABtype, D,
+                     Dtype, ldd, epilogue: Epilogue | None = None) -> int:
+    return load_library().tcg_gemm_grouped(h, transa, m, n, k, groups, _ptr(offsets), alpha,
+                                           _ptr(A), lda, strideA, _ptr(B), ldb, ABtype, _ptr(D),
+                                           Dtype, ldd, epilogue)
+
+
+def tcg_gemm_grouped_k(h, m, n, k, groups, offsets, alpha, A, lda, B, ldb, ABtype, D, Dtype, ldd,
+                       strideD) -> int:
+    return load_library().tcg_gemm_grouped_k(h, m, n, k, groups, _ptr(offsets), alpha, _ptr(A),
+                                             lda, _ptr(B), ldb, ABtype, _ptr(D), Dtype, ldd, strideD)
+
+
+def tcg_gemm_epilogue_workspace_size(h, transb, m, n, k, groups=0) -> int:
+    out = ctypes.c_size_t(0)
+    check(load_library().tcg_gemm_epilogue_workspace_size(h, transb, m, n, k, groups,
+                                                          ctypes.byref(out)),
+          "tcg_gemm_epilogue_workspace_size")
+    return out.value
+
+
+def tcg_epilogue_backward(h, activation, m, n, groups, offsets, dD, lddd, Z, ldz, type, dZ, lddz,
+                          dbias) -> int:
+    return load_library().tcg_epilogue_backward(h, activation, m, n, groups, _ptr(offsets),
+                                                _ptr(dD), lddd, _ptr(Z), ldz, type, _ptr(dZ), lddz,
+                                                _ptr(dbias))
+
+
+def tcg_xent_forward(h, rows, vocab, k, X, ldx, W, ldw, type, targets, ignore_index, loss,
+                     lse) -> int:
+    return load_library().tcg_xent_forward(h, rows, vocab, k, _ptr(X), ldx, _ptr(W), ldw, type,
+                                           _ptr(targets), ignore_index, _ptr(loss), _ptr(lse))
+
+
+def tcg_xent_backward(h, rows, vocab, k, X, ldx, W, ldw, type, targets, ignore_index, lse, dloss,
+                      dX, lddx, dW, lddw) -> int:
+    return load_library().tcg_xent_backward(h, rows, vocab, k, _ptr(X), ldx, _ptr(W), ldw, type,
+                                            _ptr(targets), ignore_index, _ptr(lse), _ptr(dloss),
+                                            _ptr(dX), lddx, _ptr(dW), lddw)
+
+
+def tcg_xent_workspace_size(h, rows, vocab, k, type, backward) -> int:
+    out = ctypes.c_size_t(0)
+    check(load_library().tcg_xent_workspace_size(h, rows, vocab, k, type, int(backward),
+                                                 ctypes.byref(out)), "tcg_xent_workspace_size")
+    return out.value
+
+
 # ------------------------------------------------------------ conveniences
 _TORCH_TYPE = {}
 
@@ -419,3 +510,7 @@ def gemm_rowmajor(handle: Handle, A, B, C, alpha=1.0, beta=0.0, tf32=False,
         s = many(handle.h, TCG_OP_N, TCG_OP_N, n, m, k, alpha, B, at, n, k * n, A, at, k, m * k,
                  beta, C, ct, n, m * n, batch, comp)
     check(s, "gemm_rowmajor")
+
+
+from .lm import (grouped_linear, grouped_linear_backward, linear, linear_backward,  # noqa: E402
+                 linear_cross_entropy, linear_cross_entropy_backward)

@@ -16,79 +16,11 @@
 #include <cstring>
 #include <new>
 
-#include "tcg.h"
-#include "tcg_internal.h"
+#include "tcg_host.h"
 
 using namespace tcg;
 
-namespace {
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-constexpr unsigned long long kDefaultWaitNs = 2000000000ull;
-constexpr int kMapCacheSize = 32;
-constexpr int kPtrCacheSize = 16;
-
-struct MapKey {
-    const void *ptr;
-    int dtype;
-    int rank;
-    int swizzle;
-    uint64_t dims[5];
-    uint64_t strides[4];
-    uint32_t box[5];
-    bool operator==(const MapKey &o) const { return std::memcmp(this, &o, sizeof(MapKey)) == 0; }
-};
-
-constexpr int kHostChunks = 16;     // chunks of a host-buffer call (events per handle)
-constexpr int kHostPanels = 4;      // chunks of the panel / batch-group split
-
-struct MapEntry {
-    MapKey key;
-    CUtensorMap map;
-    bool valid;
-};
-
-}  // namespace
-
-struct tcgContext {
-    int device = -1;
-    int num_sms = 0;
-    cudaStream_t stream = nullptr;
-    uint32_t *d_err = nullptr;
-    unsigned long long *d_clk = nullptr;   // clock probe counters (tcg_set_clock_probe)
-    bool clk_on = false;
-    void *ws_user = nullptr;
-    size_t ws_user_bytes = 0;
-    void *ws_own = nullptr;
-    size_t ws_own_bytes = 0;
-    unsigned long long wait_limit_ns = kDefaultWaitNs;
-    int fault_inject = 0;
-    uint64_t launches = 0;
-    uint32_t last_err_bits = 0;
-    int cta_group = 2;
-    int group_m = 0;           // 0: choose per problem
-    int split_k = 0;           // 0: choose per problem, 1: never split, >= 2: that many ranges
-    int tile_n = 0;            // 0: choose per problem, or kBN / kBNNarrow
-    int tf32_round = 0;        // TF32 rounding: 0 choose, 1 pre-pass kernels, 2 in the GEMM
-    // Host-buffer calls: device copies of A, B, C (grown on demand) and two copy streams.
-    void *stage_buf[3] = {nullptr, nullptr, nullptr};
-    size_t stage_bytes[3] = {0, 0, 0};
-    cudaStream_t h2d = nullptr, d2h = nullptr;
-    cudaEvent_t ev_in[kHostChunks] = {}, ev_out[kHostChunks] = {};
-    int max_ctas[3] = {0, 0, 0};
-    bool used = false;
-    EncodeTiledFn encode = nullptr;
-    MapEntry cache[kMapCacheSize];
-    int cache_next = 0;
-    const void *ptr_ok[kPtrCacheSize] = {};   // pointers already found to be device memory
-    int ptr_next = 0;
-};
-
-namespace {
+namespace tcg {
 
 int elem_size(tcgDataType_t t)
 {
@@ -105,19 +37,6 @@ bool valid_type(int t)
 int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Problem {
-    tcgOp_t transa, transb;
-    int64_t m, n, k;
-    float alpha, beta;
-    const void *A; tcgDataType_t Atype; int64_t lda; int64_t strideA;
-    const void *B; tcgDataType_t Btype; int64_t ldb; int64_t strideB;
-    void *C; tcgDataType_t Ctype; int64_t ldc; int64_t strideC;
-    int64_t batch;
-    tcgComputeType_t compute;
-    bool batched;
-    bool staged = false;       // A, B, C are the handle's own staging buffers (host-buffer calls)
-};
 
 // Pure host argument checks: no CUDA call is made before they pass.
 tcgStatus_t check_args(const Problem &p)
@@ -208,17 +127,19 @@ tcgStatus_t bind_device(tcgContext *h)
         return TCG_STATUS_NOT_INITIALIZED;
     }
     uint32_t *err = nullptr;
-    if (cudaMalloc(&err, sizeof(uint32_t)) != cudaSuccess) {
+    // the error word, then the split counters on a line of their own
+    if (cudaMalloc(&err, kErrAreaBytes) != cudaSuccess) {
         cudaGetLastError();
         return TCG_STATUS_ALLOC_FAILED;
     }
-    if (cudaMemset(err, 0, sizeof(uint32_t)) != cudaSuccess) {
+    if (cudaMemset(err, 0, kErrAreaBytes) != cudaSuccess) {
         cudaFree(err);
         cudaGetLastError();
         return TCG_STATUS_EXECUTION_FAILED;
     }
     h->encode = reinterpret_cast<EncodeTiledFn>(fn);
     h->d_err = err;
+    h->d_cnt = err + kErrAreaWords;
     h->num_sms = sms;
     h->device = dev;
     return TCG_STATUS_SUCCESS;
@@ -288,7 +209,7 @@ CUtensorMapDataType map_type(tcgDataType_t t)
 // per (pointer, type, dims, strides, box).
 tcgStatus_t get_map(tcgContext *h, const void *ptr, tcgDataType_t t, int rank,
                     const uint64_t *dims, const uint64_t *strides, const uint32_t *box,
-                    CUtensorMap *out, bool swizzle = true)
+                    CUtensorMap *out, bool swizzle)
 {
     MapKey key;
     std::memset(&key, 0, sizeof key);
@@ -516,6 +437,10 @@ tcgStatus_t acquire_ws(tcgContext *h, size_t need, void **ws)
     *ws = h->ws_own;
     return TCG_STATUS_SUCCESS;
 }
+
+}  // namespace tcg
+
+namespace {
 
 tcgStatus_t run(tcgContext *h, const Problem &p)
 {
@@ -1324,7 +1249,8 @@ tcgStatus_t tcg_get_device_error(tcgHandle_t h)
     uint32_t bits = 0;
     if (cudaStreamSynchronize(h->stream) != cudaSuccess ||
         cudaMemcpy(&bits, h->d_err, sizeof bits, cudaMemcpyDeviceToHost) != cudaSuccess ||
-        cudaMemset(h->d_err, 0, sizeof(uint32_t)) != cudaSuccess) {
+        // a kernel that stopped early may have left split counters behind
+        cudaMemset(h->d_err, 0, bits ? kErrAreaBytes : sizeof(uint32_t)) != cudaSuccess) {
         cudaGetLastError();
         return TCG_STATUS_EXECUTION_FAILED;
     }

@@ -40,7 +40,7 @@
 #include <type_traits>
 
 #include "tcg_internal.h"
-#include "tcg_ptx.cuh"
+#include "tcg_pipe.cuh"
 
 namespace tcg {
 
@@ -59,41 +59,6 @@ struct SmemCtl {
     volatile int cv_slot[2];           // epilogue half: the sub-unit its leader claimed
 };
 static_assert(sizeof(SmemCtl) <= kBarrierBytes, "barrier area too small");
-
-// Raise the abort flag in this CTA and, for a pair, in the peer CTA.
-template <int CG>
-__device__ __forceinline__ void raise_abort(SmemCtl *ctl, const GemmArgs &p, uint32_t err_bit)
-{
-    ctl->abort_flag = 1;
-    if constexpr (CG == 2)
-        st_shared_cluster_u32(mapa_shared(smem_u32(const_cast<int *>(&ctl->abort_flag)),
-                                          cluster_ctarank() ^ 1u),
-                              1u);
-    atomicOr(p.err, err_bit);
-}
-
-// Bounded wait on an mbarrier phase.  Returns false if the kernel was aborted or the
-// limit ran out (then the error bit is recorded and the abort flag raised).
-template <int CG>
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, SmemCtl *ctl,
-                                             const GemmArgs &p, uint32_t err_bit,
-                                             bool honour_abort = true)
-{
-    if (mbar_try_wait(bar, parity))
-        return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (;;) {
-        if (mbar_try_wait(bar, parity))
-            return true;
-        if (honour_abort && ctl->abort_flag)
-            return false;
-        if (globaltimer_ns() - t0 > p.wait_limit_ns) {
-            raise_abort<CG>(ctl, p, err_bit);
-            return false;
-        }
-    }
-}
-
 
 // Work unit u -> its tile (b, mt, nt), its K blocks [kb0, kb1), and -- for a unit of a
 // split tail tile -- its partial-sum slice (-1 otherwise).  Units [0, full_units) are

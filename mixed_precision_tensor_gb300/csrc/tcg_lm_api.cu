@@ -1,0 +1,774 @@
+// tcg_lm_api.cu -- host runtime and C ABI of the language-model products (declared in
+// include/tcg.h): products with a bias, activation and residual in their epilogue,
+// products grouped by expert, and the cross entropy of a linear head.
+//
+// Every call checks its arguments on the host, binds the handle, checks that its pointers
+// are device memory, and queues kernels of tcg_lm.cu on the handle's stream.
+
+#include <cstring>
+#include <initializer_list>
+
+#include "tcg_host.h"
+
+using namespace tcg;
+
+namespace {
+
+constexpr int64_t kMaxExtent = (int64_t(1) << 31) - 1024;   // 32-bit tile and TMA coordinates
+
+int out_kind_of(tcgDataType_t t)
+{
+    return t == TCG_R_32F ? kOutF32 : (t == TCG_R_16F ? kOutF16 : kOutBF16);
+}
+
+bool is_16bit(int t) { return t == TCG_R_16F || t == TCG_R_16BF; }
+
+bool bad_ld(int64_t ld, int64_t rows, int es)
+{
+    return ld < (rows > 1 ? rows : 1) || (ld * es) % 16;
+}
+
+int clusters_of(tcgContext *h)
+{
+    if (h->max_ctas[0] == 0)
+        h->max_ctas[0] = lm_max_resident_ctas(h->num_sms);
+    return h->max_ctas[0] / 2;
+}
+
+// One product of the kernel: D (m x cols) per group, see LmArgs.
+struct Product {
+    int64_t m = 0, cols = 0, k = 0;
+    bool a_kmajor = true, b_kmajor = true;
+    const void *A = nullptr, *B = nullptr;
+    int64_t lda = 0, strideA = 0, ldb = 0;
+    tcgDataType_t in = TCG_R_16BF, out = TCG_R_16BF;
+    int64_t groups = 1;
+    const int64_t *offsets = nullptr;
+    bool ragged_k = false;
+    int64_t n = 0;                          // K ragged
+    float alpha = 1.0f;
+    const float *alpha_dev = nullptr;
+    void *D = nullptr;
+    int64_t ldd = 0, strideD = 0;
+    tcgEpilogue_t epi = {};
+    int lm_epi = kEpiLinear;
+};
+
+int64_t m_tiles_of(int64_t m) { return (m + 2 * kBM - 1) / (2 * kBM); }
+
+// The most tiles a call can have (a grouped call's column tiles depend on its offsets).
+int64_t max_tiles(const Product &p, int bn)
+{
+    int64_t nt = (p.cols + bn - 1) / bn;
+    if (p.offsets)
+        nt = p.cols / bn + (p.groups + 2 < p.cols ? p.groups + 2 : p.cols);
+    return m_tiles_of(p.m) * nt;
+}
+
+// Tile width of an N-ragged product.
+int width_of(tcgContext *h, const Product &p)
+{
+    const int64_t per = p.offsets ? p.cols / p.groups : p.cols;
+    int bn = per <= 32 ? 32 : (per <= 64 ? 64 : (per <= 128 ? 128 : 256));
+    if (!p.b_kmajor && bn < 128)
+        bn = 128;                           // a 64-column chunk per CTA at least
+    if (bn == 256 && max_tiles(p, 256) * 2 <= clusters_of(h))
+        bn = 128;
+    return bn;
+}
+
+// K ranges of an N-ragged product: as many as fill the SM pairs once when the tiles fill
+// at most half of them, at least four K blocks each.
+void split_of(tcgContext *h, const Product &p, int bn, int *splits, int *per)
+{
+    const int nkb = static_cast<int>((p.k + 63) / 64);
+    const int64_t tiles = max_tiles(p, bn);
+    const int clusters = clusters_of(h);
+    int64_t s = 1;
+    if (tiles > 0 && tiles * 2 <= clusters && tiles * 4 <= kLmCounters)
+        s = clusters / tiles;
+    if (s > nkb / 4)
+        s = nkb / 4;
+    if (s > kLmMaxSplits)
+        s = kLmMaxSplits;
+    if (s < 1)
+        s = 1;
+    *per = nkb > 0 ? static_cast<int>((nkb + s - 1) / s) : 1;
+    *splits = nkb > 0 ? (nkb + *per - 1) / *per : 1;
+}
+
+size_t product_ws(tcgContext *h, const Product &p)
+{
+    if (p.ragged_k || p.lm_epi != kEpiLinear)
+        return 0;
+    const int bn = width_of(h, p);
+    int splits, per;
+    split_of(h, p, bn, &splits, &per);
+    return splits > 1 ? lm_part_bytes(max_tiles(p, bn), bn, splits) : 0;
+}
+
+// Queue one product.  ws: workspace of at least product_ws bytes.
+tcgStatus_t queue(tcgContext *h, const Product &p, void *ws, LmArgs a = LmArgs{})
+{
+    LmMaps maps;
+    std::memset(&maps, 0, sizeof maps);
+    const int bn = p.ragged_k || p.lm_epi != kEpiLinear ? 256 : width_of(h, p);
+    a.m = static_cast<int>(p.m);
+    a.cols = static_cast<int>(p.cols);
+    a.n = static_cast<int>(p.n);
+    a.ragged_k = p.ragged_k;
+    a.groups = static_cast<int>(p.groups);
+    a.offsets = p.offsets;
+    a.num_m_tiles = static_cast<int>(m_tiles_of(p.m));
+    a.num_n_tiles = static_cast<int>(((p.ragged_k ? p.n : p.cols) + bn - 1) / bn);
+    a.num_k_blocks = static_cast<int>((p.k + 63) / 64);
+    a.k_splits = 1;
+    a.kb_per_split = a.num_k_blocks;
+    if (!p.ragged_k && p.lm_epi == kEpiLinear)
+        split_of(h, p, bn, &a.k_splits, &a.kb_per_split);
+    a.group_m = h->group_m > 0 ? h->group_m : 8;
+    a.in_bf16 = p.in == TCG_R_16BF;
+    a.idesc = (1u << 4) | (static_cast<uint32_t>(a.in_bf16) << 7) |
+              (static_cast<uint32_t>(a.in_bf16) << 10) | ((p.a_kmajor ? 0u : 1u) << 15) |
+              ((p.b_kmajor ? 0u : 1u) << 16) | (static_cast<uint32_t>(bn >> 3) << 17) |
+              (static_cast<uint32_t>((2 * kBM) >> 4) << 24);
+    a.alpha = p.alpha;
+    a.alpha_dev = p.alpha_dev;
+    a.D = p.D;
+    a.ldd = p.ldd;
+    a.strideD = p.strideD;
+    a.bias = p.epi.bias;
+    a.bias_f32 = p.epi.bias_type == TCG_R_32F;
+    a.C = p.epi.beta != 0.0f ? p.epi.C : nullptr;
+    a.ldc = p.epi.ldc;
+    a.beta = p.epi.beta;
+    a.Z = p.epi.Z;
+    a.ldz = p.epi.ldz;
+    a.act = p.epi.activation;
+    a.part = static_cast<float *>(ws);
+    a.cnt = h->d_cnt;
+    a.err = h->d_err;
+    a.wait_limit_ns = h->wait_limit_ns;
+    a.fault_inject = h->fault_inject;
+
+    // Operands (none where nothing is summed).  A K-ragged call's are both M/N-major over
+    // all tokens.
+    tcgStatus_t st;
+    bool bc;
+    const int64_t ka = p.ragged_k ? p.cols : p.k;
+    if (ka > 0) {
+        st = operand_map(h, p.A, p.in, p.a_kmajor, p.m, ka, p.lda, p.strideA,
+                         p.ragged_k || !p.offsets ? 1 : p.groups, kBM, 64, &bc, &a.a_mode, &maps.A);
+        if (st != TCG_STATUS_SUCCESS)
+            return st;
+        st = operand_map(h, p.B, p.in, p.b_kmajor, p.ragged_k ? p.n : p.cols, ka, p.ldb, 0, 1,
+                         bn / 2, 64, &bc, &a.b_mode, &maps.B);
+        if (st != TCG_STATUS_SUCCESS)
+            return st;
+    }
+    if (p.ragged_k && ka > 0) {
+        const int boxes[3] = {16, 4, 1};
+        for (int i = 0; i < 3; ++i)
+            for (int x = 0; x < 2; ++x) {
+                const int64_t rows = x ? p.n : p.m, ld = x ? p.ldb : p.lda;
+                const uint64_t dims[3] = {static_cast<uint64_t>(rows), static_cast<uint64_t>(p.cols), 1};
+                const uint64_t str[2] = {static_cast<uint64_t>(ld) * 2,
+                                         static_cast<uint64_t>(ld) * 2 * static_cast<uint64_t>(p.cols)};
+                const uint32_t box[3] = {64, static_cast<uint32_t>(boxes[i]), 1};
+                st = get_map(h, x ? p.B : p.A, p.in, 3, dims, str, box,
+                             x ? &maps.B_tail[i] : &maps.A_tail[i]);
+                if (st != TCG_STATUS_SUCCESS)
+                    return st;
+            }
+    }
+    const int64_t units = p.ragged_k ? p.groups * a.num_m_tiles * a.num_n_tiles
+                                     : max_tiles(p, bn) * a.k_splits;
+    if (units > INT32_MAX)
+        return TCG_STATUS_NOT_SUPPORTED;
+    const int64_t most = clusters_of(h);
+    const int grid = 2 * static_cast<int>(units < most ? units : most);
+    const cudaError_t e = launch_lm(maps, a, p.lm_epi, out_kind_of(p.out), bn, grid, h->stream);
+    h->launches += 1;
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return TCG_STATUS_EXECUTION_FAILED;
+    }
+    return TCG_STATUS_SUCCESS;
+}
+
+tcgStatus_t check_epilogue(const tcgEpilogue_t &e, int64_t m, int64_t n, tcgDataType_t in,
+                           tcgDataType_t out)
+{
+    if (e.activation < TCG_ACT_NONE || e.activation > TCG_ACT_SILU)
+        return TCG_STATUS_INVALID_VALUE;
+    if (e.bias) {
+        if (!valid_type(e.bias_type))
+            return TCG_STATUS_INVALID_VALUE;
+        if (e.bias_type != TCG_R_32F && e.bias_type != in)
+            return TCG_STATUS_NOT_SUPPORTED;
+        if (reinterpret_cast<uintptr_t>(e.bias) % elem_size(e.bias_type))
+            return TCG_STATUS_INVALID_VALUE;
+    }
+    if (e.beta != 0.0f && ((!e.C && m > 0 && n > 0) || !aligned16(e.C) ||
+                           bad_ld(e.ldc, m, elem_size(out))))
+        return TCG_STATUS_INVALID_VALUE;
+    if (e.Z && (!aligned16(e.Z) || bad_ld(e.ldz, m, 2)))
+        return TCG_STATUS_INVALID_VALUE;
+    return TCG_STATUS_SUCCESS;
+}
+
+tcgStatus_t check_types(tcgDataType_t in, tcgDataType_t out)
+{
+    if (!valid_type(in) || !valid_type(out))
+        return TCG_STATUS_INVALID_VALUE;
+    if (!is_16bit(in) || (out != in && out != TCG_R_32F))
+        return TCG_STATUS_NOT_SUPPORTED;
+    return TCG_STATUS_SUCCESS;
+}
+
+tcgStatus_t check_groups(int64_t groups, const int64_t *offsets)
+{
+    if (groups < 1 || !offsets || reinterpret_cast<uintptr_t>(offsets) % 8)
+        return TCG_STATUS_INVALID_VALUE;
+    return groups > kLmMaxGroups ? TCG_STATUS_NOT_SUPPORTED : TCG_STATUS_SUCCESS;
+}
+
+tcgStatus_t check_device(tcgContext *h, std::initializer_list<const void *> ptrs)
+{
+    for (const void *q : ptrs)
+        if (q) {
+            const tcgStatus_t st = device_ptr_ok(h->device, q);
+            if (st != TCG_STATUS_SUCCESS)
+                return st;
+        }
+    return TCG_STATUS_SUCCESS;
+}
+
+// The N-ragged product behind tcg_gemm_epilogue and tcg_gemm_grouped.
+tcgStatus_t run_product(tcgContext *h, Product &p, const tcgEpilogue_t *e)
+{
+    if (e)
+        p.epi = *e;
+    tcgStatus_t st = check_types(p.in, p.out);
+    if (st == TCG_STATUS_SUCCESS)
+        st = check_epilogue(p.epi, p.m, p.cols, p.in, p.out);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    if (p.m < 0 || p.cols < 0 || p.k < 0)
+        return TCG_STATUS_INVALID_VALUE;
+    if (bad_ld(p.lda, p.a_kmajor ? p.k : p.m, 2) || bad_ld(p.ldb, p.b_kmajor ? p.k : p.cols, 2) ||
+        bad_ld(p.ldd, p.m, elem_size(p.out)))
+        return TCG_STATUS_INVALID_VALUE;
+    if (p.offsets && ((p.groups > 1 && p.strideA <= 0) || (p.strideA * 2) % 16))
+        return TCG_STATUS_INVALID_VALUE;
+    if (p.m > kMaxExtent || p.cols > kMaxExtent || p.k > kMaxExtent)
+        return TCG_STATUS_NOT_SUPPORTED;
+    if (p.m == 0 || p.cols == 0)
+        return TCG_STATUS_SUCCESS;
+    if (!p.D || !aligned16(p.D) ||
+        (p.k > 0 && (!p.A || !p.B || !aligned16(p.A) || !aligned16(p.B))))
+        return TCG_STATUS_INVALID_VALUE;
+    st = bind_device(h);
+    if (st == TCG_STATUS_SUCCESS)
+        st = check_device(h, {p.D, p.k > 0 ? p.A : nullptr, p.k > 0 ? p.B : nullptr, p.offsets,
+                              p.epi.bias, p.epi.beta != 0.0f ? p.epi.C : nullptr, p.epi.Z});
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    h->used = true;
+    void *ws = nullptr;
+    const size_t need = product_ws(h, p);
+    if (need) {
+        st = acquire_ws(h, need, &ws);
+        if (st != TCG_STATUS_SUCCESS)
+            return st;
+    }
+    return queue(h, p, ws);
+}
+
+// ----------------------------------------------------------------------- cross entropy
+size_t pad256(size_t b) { return (b + 255) / 256 * 256; }
+
+// Workspace of the forward pass: two (maximum, sum) slots per 256 vocabulary entries and
+// row, and the target logits.
+int64_t xent_slots(int64_t vocab) { return (vocab + 255) / 256 * 2; }
+size_t xent_stats_bytes(int64_t rows, int64_t vocab)
+{
+    return pad256(static_cast<size_t>(xent_slots(vocab) * rows) * sizeof(float2));
+}
+
+// Vocabulary entries whose gradient is held at a time, a multiple of 256: 256 MiB of it.
+constexpr int64_t kGradPieceBytes = int64_t(256) << 20;
+int64_t xent_piece(int64_t rows, int64_t vocab)
+{
+    int64_t w = kGradPieceBytes / (2 * rows) / 256 * 256;
+    w = w < 256 ? 256 : w;
+    const int64_t all = (vocab + 255) / 256 * 256;
+    return w < all ? w : all;
+}
+
+struct XentBackwardPlan {
+    int64_t piece, pieces;
+    size_t grad_bytes, acc_bytes, scale_bytes, split_bytes, total;
+};
+
+Product xent_dx(int64_t rows, int64_t k, int64_t width, int64_t piece, tcgDataType_t in, bool one)
+{
+    Product p;
+    p.m = k;
+    p.cols = rows;
+    p.k = width;
+    p.a_kmajor = false;
+    p.ldb = piece;
+    p.in = in;
+    p.out = one ? in : TCG_R_32F;
+    return p;
+}
+
+Product xent_dw(int64_t rows, int64_t k, int64_t width, int64_t piece, tcgDataType_t in)
+{
+    Product p;
+    p.m = k;
+    p.cols = width;
+    p.k = rows;
+    p.a_kmajor = p.b_kmajor = false;
+    p.ldb = piece;
+    p.in = p.out = in;
+    return p;
+}
+
+XentBackwardPlan xent_plan(tcgContext *h, int64_t rows, int64_t vocab, int64_t k, tcgDataType_t in)
+{
+    XentBackwardPlan pl;
+    pl.piece = xent_piece(rows, vocab);
+    pl.pieces = (vocab + pl.piece - 1) / pl.piece;
+    pl.grad_bytes = pad256(static_cast<size_t>(rows * pl.piece) * 2);
+    pl.acc_bytes = pl.pieces > 1 ? pad256(static_cast<size_t>(rows * ((k + 3) / 4 * 4)) * 4) : 0;
+    pl.scale_bytes = 256;
+    pl.split_bytes = 0;
+    for (int last = 0; last < 2; ++last) {
+        const int64_t w = last ? vocab - (pl.pieces - 1) * pl.piece : (pl.pieces > 1 ? pl.piece : 0);
+        if (w <= 0)
+            continue;
+        const size_t a = product_ws(h, xent_dx(rows, k, w, pl.piece, in, pl.pieces == 1));
+        const size_t b = product_ws(h, xent_dw(rows, k, w, pl.piece, in));
+        const size_t c = a > b ? a : b;
+        pl.split_bytes = c > pl.split_bytes ? c : pl.split_bytes;
+    }
+    pl.split_bytes = pad256(pl.split_bytes);
+    pl.total = pl.grad_bytes + pl.acc_bytes + pl.scale_bytes + pl.split_bytes;
+    return pl;
+}
+
+struct Xent {
+    int64_t rows, vocab, k;
+    const void *X; int64_t ldx;
+    const void *W; int64_t ldw;
+    tcgDataType_t in;
+    const int64_t *targets;
+    int64_t ignore;
+};
+
+tcgStatus_t check_xent(const Xent &x)
+{
+    if (!valid_type(x.in))
+        return TCG_STATUS_INVALID_VALUE;
+    if (!is_16bit(x.in))
+        return TCG_STATUS_NOT_SUPPORTED;
+    if (x.rows < 0 || x.vocab < 1 || x.k < 1)
+        return TCG_STATUS_INVALID_VALUE;
+    if (bad_ld(x.ldx, x.k, 2) || bad_ld(x.ldw, x.k, 2))
+        return TCG_STATUS_INVALID_VALUE;
+    if (x.rows > kMaxExtent || x.vocab > kMaxExtent || x.k > kMaxExtent)
+        return TCG_STATUS_NOT_SUPPORTED;
+    if (x.rows == 0)
+        return TCG_STATUS_SUCCESS;
+    if (!x.X || !x.W || !x.targets || !aligned16(x.X) || !aligned16(x.W) ||
+        reinterpret_cast<uintptr_t>(x.targets) % 8)
+        return TCG_STATUS_INVALID_VALUE;
+    return TCG_STATUS_SUCCESS;
+}
+
+Product xent_logits(const Xent &x, int64_t col0, int64_t width, int epi)
+{
+    Product p;
+    p.m = x.rows;
+    p.cols = width;
+    p.k = x.k;
+    p.A = x.X;
+    p.lda = x.ldx;
+    p.B = static_cast<const uint16_t *>(x.W) + col0 * x.ldw;
+    p.ldb = x.ldw;
+    p.in = x.in;
+    p.lm_epi = epi;
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+tcgStatus_t tcg_gemm_epilogue(tcgHandle_t h, tcgOp_t transa, tcgOp_t transb, int64_t m, int64_t n,
+                              int64_t k, float alpha, const void *A, int64_t lda, const void *B,
+                              int64_t ldb, tcgDataType_t ABtype, void *D, tcgDataType_t Dtype,
+                              int64_t ldd, const tcgEpilogue_t *epilogue)
+{
+    if (!h || (transa != TCG_OP_N && transa != TCG_OP_T) || (transb != TCG_OP_N && transb != TCG_OP_T))
+        return TCG_STATUS_INVALID_VALUE;
+    Product p;
+    p.m = m;
+    p.cols = n;
+    p.k = k;
+    p.a_kmajor = transa == TCG_OP_T;
+    p.b_kmajor = transb == TCG_OP_N;
+    p.A = A;
+    p.lda = lda;
+    p.B = B;
+    p.ldb = ldb;
+    p.in = ABtype;
+    p.out = Dtype;
+    p.alpha = alpha;
+    p.D = D;
+    p.ldd = ldd;
+    return run_product(h, p, epilogue);
+}
+
+tcgStatus_t tcg_gemm_grouped(tcgHandle_t h, tcgOp_t transa, int64_t m, int64_t n, int64_t k,
+                             int64_t groups, const int64_t *offsets, float alpha, const void *A,
+                             int64_t lda, int64_t strideA, const void *B, int64_t ldb,
+                             tcgDataType_t ABtype, void *D, tcgDataType_t Dtype, int64_t ldd,
+                             const tcgEpilogue_t *epilogue)
+{
+    if (!h || (transa != TCG_OP_N && transa != TCG_OP_T))
+        return TCG_STATUS_INVALID_VALUE;
+    const tcgStatus_t st = check_groups(groups, offsets);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    Product p;
+    p.m = m;
+    p.cols = n;
+    p.k = k;
+    p.a_kmajor = transa == TCG_OP_T;
+    p.A = A;
+    p.lda = lda;
+    p.strideA = strideA;
+    p.B = B;
+    p.ldb = ldb;
+    p.in = ABtype;
+    p.out = Dtype;
+    p.groups = groups;
+    p.offsets = offsets;
+    p.alpha = alpha;
+    p.D = D;
+    p.ldd = ldd;
+    return run_product(h, p, epilogue);
+}
+
+tcgStatus_t tcg_gemm_epilogue_workspace_size(tcgHandle_t h, tcgOp_t transb, int64_t m, int64_t n,
+                                             int64_t k, int64_t groups, size_t *bytes)
+{
+    if (!h || !bytes || (transb != TCG_OP_N && transb != TCG_OP_T) || m < 0 || n < 0 || k < 0 ||
+        groups < 0 || groups > kLmMaxGroups)
+        return TCG_STATUS_INVALID_VALUE;
+    *bytes = 0;
+    if (m == 0 || n == 0)
+        return TCG_STATUS_SUCCESS;
+    const tcgStatus_t st = bind_device(h);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    static const int64_t some = 0;
+    Product p;
+    p.m = m;
+    p.cols = n;
+    p.k = k;
+    p.b_kmajor = transb == TCG_OP_N;
+    if (groups > 0) {
+        p.groups = groups;
+        p.offsets = &some;                  // grouped: only whether it is set matters here
+    }
+    *bytes = product_ws(h, p);
+    return TCG_STATUS_SUCCESS;
+}
+
+tcgStatus_t tcg_gemm_grouped_k(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int64_t groups,
+                               const int64_t *offsets, float alpha, const void *A, int64_t lda,
+                               const void *B, int64_t ldb, tcgDataType_t ABtype, void *D,
+                               tcgDataType_t Dtype, int64_t ldd, int64_t strideD)
+{
+    if (!h)
+        return TCG_STATUS_INVALID_VALUE;
+    tcgStatus_t st = check_groups(groups, offsets);
+    if (st == TCG_STATUS_SUCCESS)
+        st = check_types(ABtype, Dtype);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    if (m < 0 || n < 0 || k < 0)
+        return TCG_STATUS_INVALID_VALUE;
+    if (bad_ld(lda, m, 2) || bad_ld(ldb, n, 2) || bad_ld(ldd, m, elem_size(Dtype)) || strideD < 0 ||
+        (strideD * elem_size(Dtype)) % 16 || (groups > 1 && strideD < (n > 0 ? (n - 1) * ldd + m : 0)))
+        return TCG_STATUS_INVALID_VALUE;
+    if (m > kMaxExtent || n > kMaxExtent || k > kMaxExtent)
+        return TCG_STATUS_NOT_SUPPORTED;
+    if (m == 0 || n == 0)
+        return TCG_STATUS_SUCCESS;
+    if (!D || !aligned16(D) || (k > 0 && (!A || !B || !aligned16(A) || !aligned16(B))))
+        return TCG_STATUS_INVALID_VALUE;
+    st = bind_device(h);
+    if (st == TCG_STATUS_SUCCESS)
+        st = check_device(h, {D, k > 0 ? A : nullptr, k > 0 ? B : nullptr, offsets});
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    h->used = true;
+    Product p;
+    p.m = m;
+    p.n = n;
+    p.cols = k;
+    p.ragged_k = true;
+    p.a_kmajor = p.b_kmajor = false;
+    p.A = A;
+    p.B = B;
+    p.lda = lda;
+    p.ldb = ldb;
+    p.in = ABtype;
+    p.out = Dtype;
+    p.groups = groups;
+    p.offsets = offsets;
+    p.alpha = alpha;
+    p.D = D;
+    p.ldd = ldd;
+    p.strideD = strideD;
+    return queue(h, p, nullptr);
+}
+
+tcgStatus_t tcg_epilogue_backward(tcgHandle_t h, tcgActivation_t activation, int64_t m, int64_t n,
+                                  int64_t groups, const int64_t *offsets, const void *dD,
+                                  int64_t lddd, const void *Z, int64_t ldz, tcgDataType_t type,
+                                  void *dZ, int64_t lddz, float *dbias)
+{
+    if (!h || activation < TCG_ACT_NONE || activation > TCG_ACT_SILU || !valid_type(type))
+        return TCG_STATUS_INVALID_VALUE;
+    if (!is_16bit(type))
+        return TCG_STATUS_NOT_SUPPORTED;
+    if (offsets) {
+        const tcgStatus_t st = check_groups(groups, offsets);
+        if (st != TCG_STATUS_SUCCESS)
+            return st;
+    } else if (groups != 1) {
+        return TCG_STATUS_INVALID_VALUE;
+    }
+    const bool need_z = activation != TCG_ACT_NONE;
+    if (m < 0 || n < 0 || bad_ld(lddd, m, 2) || (need_z && bad_ld(ldz, m, 2)) ||
+        (dZ && bad_ld(lddz, m, 2)))
+        return TCG_STATUS_INVALID_VALUE;
+    if (m > kMaxExtent || n > kMaxExtent)
+        return TCG_STATUS_NOT_SUPPORTED;
+    if (m == 0 || (!dZ && !dbias))
+        return TCG_STATUS_SUCCESS;
+    if (n > 0 && (!dD || !aligned16(dD) || (need_z && (!Z || !aligned16(Z))) || (dZ && !aligned16(dZ))))
+        return TCG_STATUS_INVALID_VALUE;
+    if (dbias && reinterpret_cast<uintptr_t>(dbias) % 4)
+        return TCG_STATUS_INVALID_VALUE;
+    tcgStatus_t st = bind_device(h);
+    if (st == TCG_STATUS_SUCCESS)
+        st = check_device(h, {n > 0 ? dD : nullptr, n > 0 && need_z ? Z : nullptr,
+                              n > 0 ? dZ : nullptr, dbias, offsets});
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    h->used = true;
+    // column ranges per group: about four blocks of 256 rows per SM, 16 columns each at least
+    const int64_t row_blocks = (m + 255) / 256;
+    int64_t parts = 4 * static_cast<int64_t>(h->num_sms) / (row_blocks * groups);
+    const int64_t most = (n / groups + 15) / 16;
+    parts = parts > most ? most : parts;
+    parts = parts < 1 ? 1 : parts;
+    void *ws = nullptr;
+    if (dbias) {
+        st = acquire_ws(h, static_cast<size_t>(groups * parts * m) * 4, &ws);
+        if (st != TCG_STATUS_SUCCESS)
+            return st;
+    }
+    const cudaError_t e = launch_epi_backward(
+        activation, type == TCG_R_16BF, static_cast<int>(m), static_cast<int>(n),
+        static_cast<int>(groups), offsets, dD, lddd, need_z ? Z : nullptr, ldz, n > 0 ? dZ : nullptr,
+        lddz, dbias, static_cast<float *>(ws), static_cast<int>(parts), h->stream);
+    h->launches += dbias ? 2 : 1;
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return TCG_STATUS_EXECUTION_FAILED;
+    }
+    return TCG_STATUS_SUCCESS;
+}
+
+tcgStatus_t tcg_xent_workspace_size(tcgHandle_t h, int64_t rows, int64_t vocab, int64_t k,
+                                    tcgDataType_t type, int backward, size_t *bytes)
+{
+    if (!h || !bytes || rows < 0 || vocab < 1 || k < 1 || !is_16bit(type))
+        return TCG_STATUS_INVALID_VALUE;
+    *bytes = 0;
+    if (rows == 0)
+        return TCG_STATUS_SUCCESS;
+    const tcgStatus_t st = bind_device(h);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    *bytes = backward ? xent_plan(h, rows, vocab, k, type).total
+                      : xent_stats_bytes(rows, vocab) + pad256(static_cast<size_t>(rows) * 4);
+    return TCG_STATUS_SUCCESS;
+}
+
+tcgStatus_t tcg_xent_forward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_t k, const void *X,
+                             int64_t ldx, const void *W, int64_t ldw, tcgDataType_t type,
+                             const int64_t *targets, int64_t ignore_index, float *loss, float *lse)
+{
+    const Xent x{rows, vocab, k, X, ldx, W, ldw, type, targets, ignore_index};
+    if (!h)
+        return TCG_STATUS_INVALID_VALUE;
+    tcgStatus_t st = check_xent(x);
+    if (st != TCG_STATUS_SUCCESS || rows == 0)
+        return st;
+    if (!loss || !lse || reinterpret_cast<uintptr_t>(loss) % 4 || reinterpret_cast<uintptr_t>(lse) % 4)
+        return TCG_STATUS_INVALID_VALUE;
+    st = bind_device(h);
+    if (st == TCG_STATUS_SUCCESS)
+        st = check_device(h, {X, W, targets, loss, lse});
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    h->used = true;
+    void *ws = nullptr;
+    const size_t stats_bytes = xent_stats_bytes(rows, vocab);
+    st = acquire_ws(h, stats_bytes + pad256(static_cast<size_t>(rows) * 4), &ws);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    LmArgs a{};
+    a.targets = targets;
+    a.ignore = ignore_index;
+    a.vocab = vocab;
+    a.stats = static_cast<float2 *>(ws);
+    a.target_logit = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + stats_bytes);
+    st = queue(h, xent_logits(x, 0, vocab, kEpiXentStats), nullptr, a);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    const cudaError_t e = launch_xent_combine(a.stats, static_cast<int>(xent_slots(vocab)),
+                                              static_cast<int>(rows), a.target_logit, targets, vocab,
+                                              ignore_index, loss, lse, h->stream);
+    h->launches += 1;
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return TCG_STATUS_EXECUTION_FAILED;
+    }
+    return TCG_STATUS_SUCCESS;
+}
+
+tcgStatus_t tcg_xent_backward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_t k, const void *X,
+                              int64_t ldx, const void *W, int64_t ldw, tcgDataType_t type,
+                              const int64_t *targets, int64_t ignore_index, const float *lse,
+                              const float *dloss, void *dX, int64_t lddx, void *dW, int64_t lddw)
+{
+    const Xent x{rows, vocab, k, X, ldx, W, ldw, type, targets, ignore_index};
+    if (!h)
+        return TCG_STATUS_INVALID_VALUE;
+    tcgStatus_t st = check_xent(x);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    if ((dX && (!aligned16(dX) || bad_ld(lddx, k, 2))) || (dW && (!aligned16(dW) || bad_ld(lddw, k, 2))))
+        return TCG_STATUS_INVALID_VALUE;
+    if (rows > 0 && (!lse || !dloss || reinterpret_cast<uintptr_t>(lse) % 4 ||
+                     reinterpret_cast<uintptr_t>(dloss) % 4))
+        return TCG_STATUS_INVALID_VALUE;
+    if ((rows == 0 && !dW) || (!dX && !dW))
+        return TCG_STATUS_SUCCESS;
+    st = bind_device(h);
+    if (st == TCG_STATUS_SUCCESS)
+        st = rows > 0 ? check_device(h, {X, W, targets, lse, dloss, dX, dW}) : check_device(h, {dW});
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    h->used = true;
+    if (rows == 0) {                                       // no rows: dW is zero
+        Product p = xent_dw(0, k, vocab, vocab, type);
+        p.lda = ldx;
+        p.D = dW;
+        p.ldd = lddw;
+        return queue(h, p, nullptr);
+    }
+    const XentBackwardPlan pl = xent_plan(h, rows, vocab, k, type);
+    void *ws = nullptr;
+    st = acquire_ws(h, pl.total, &ws);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    uint8_t *at = static_cast<uint8_t *>(ws);
+    void *G = at;
+    float *acc = reinterpret_cast<float *>(at + pl.grad_bytes);
+    float *scale = reinterpret_cast<float *>(at + pl.grad_bytes + pl.acc_bytes);
+    void *split_ws = at + pl.grad_bytes + pl.acc_bytes + pl.scale_bytes;
+    const int64_t ldacc = (k + 3) / 4 * 4;
+    const bool scaled = type == TCG_R_16F;                  // FP16 gradients need range
+    cudaError_t e = cudaSuccess;
+    if (scaled) {
+        e = launch_xent_scale(dloss, targets, static_cast<int>(rows), vocab, ignore_index, scale,
+                              h->stream);
+        h->launches += 1;
+    }
+    for (int64_t i = 0; e == cudaSuccess && i < pl.pieces; ++i) {
+        const int64_t c0 = i * pl.piece, width = vocab - c0 < pl.piece ? vocab - c0 : pl.piece;
+        LmArgs a{};
+        a.targets = targets;
+        a.ignore = ignore_index;
+        a.vocab = vocab;
+        a.col0 = static_cast<int>(c0);
+        a.lse = lse;
+        a.dloss = dloss;
+        a.gscale = scaled ? scale : nullptr;
+        Product g = xent_logits(x, c0, width, kEpiXentGrad);
+        g.D = G;
+        g.ldd = pl.piece;
+        st = queue(h, g, nullptr, a);
+        if (st != TCG_STATUS_SUCCESS)
+            return st;
+        if (dX) {
+            Product p = xent_dx(rows, k, width, pl.piece, type, pl.pieces == 1);
+            p.A = static_cast<const uint16_t *>(W) + c0 * ldw;
+            p.lda = ldw;
+            p.B = G;
+            if (pl.pieces == 1) {
+                p.D = dX;
+                p.ldd = lddx;
+                p.alpha_dev = scaled ? scale + 1 : nullptr;
+            } else {
+                p.D = acc;
+                p.ldd = ldacc;
+                p.epi.C = acc;
+                p.epi.ldc = ldacc;
+                p.epi.beta = i > 0 ? 1.0f : 0.0f;
+            }
+            st = queue(h, p, split_ws);
+            if (st != TCG_STATUS_SUCCESS)
+                return st;
+        }
+        if (dW) {
+            Product p = xent_dw(rows, k, width, pl.piece, type);
+            p.A = X;
+            p.lda = ldx;
+            p.B = G;
+            p.D = static_cast<uint16_t *>(dW) + c0 * lddw;
+            p.ldd = lddw;
+            p.alpha_dev = scaled ? scale + 1 : nullptr;
+            st = queue(h, p, split_ws);
+            if (st != TCG_STATUS_SUCCESS)
+                return st;
+        }
+    }
+    if (e == cudaSuccess && dX && pl.pieces > 1) {
+        const int64_t work = (k + 3) / 4 * rows;
+        const int64_t cap = static_cast<int64_t>(h->num_sms) * 8;
+        const int64_t blocks = (work + 255) / 256;
+        e = launch_round_out(acc, ldacc, static_cast<int>(k), static_cast<int>(rows),
+                             scaled ? scale + 1 : nullptr, dX, lddx, out_kind_of(type),
+                             static_cast<int>(blocks < cap ? blocks : cap), h->stream);
+        h->launches += 1;
+    }
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return TCG_STATUS_EXECUTION_FAILED;
+    }
+    return TCG_STATUS_SUCCESS;
+}
+
+}  // extern "C"

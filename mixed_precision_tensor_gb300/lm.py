@@ -1,0 +1,335 @@
+"""Language-model products on torch CUDA tensors: linear layers, layers of experts, and the
+cross entropy of a linear head, forward and backward (include/tcg.h, section "Language-model
+products").
+
+Row-major: a row is a token.  Inputs are FP16 or BF16, two-dimensional with unit stride
+along the features; rows may be any multiple of 16 bytes apart, so feature counts that are
+no multiple of 8 need padded rows.  Every call queues on the handle's stream and does not
+wait; inputs must be ready there.  Tensors that a call allocates belong to that stream.
+This module checks and marshals; all arithmetic is in the library's kernels.
+"""
+from __future__ import annotations
+
+import torch
+
+import mixed_precision_tensor_gb300 as _tcg
+
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+_IN = {torch.float16: 0, torch.bfloat16: 1}                  # TCG_R_16F, TCG_R_16BF
+_TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def _rows(t, what, rows, cols, dtype, device):
+    """Leading dimension of a rows x cols matrix, checked."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{what} must be {rows} x {cols}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{what} must be on {device}, got {t.device}")
+    s0, s1 = t.stride()
+    if cols > 1 and s1 != 1:
+        raise ValueError(f"{what} must have unit stride along its last dimension")
+    per = 16 // t.element_size()
+    if rows <= 1:
+        return max(1, -(-cols // per)) * per
+    if s0 < cols or s0 % per:
+        raise ValueError(f"{what}: rows must be a multiple of 16 bytes apart, got {s0} elements")
+    return s0
+
+
+def _input(x, what="x"):
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise ValueError(f"{what} must be a two-dimensional tensor")
+    if not x.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if x.dtype not in _IN:
+        raise ValueError(f"{what} must be float16 or bfloat16, got {x.dtype}")
+    return x.shape[0], x.shape[1], x.dtype, x.device
+
+
+def _act(act):
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
+def _empty(handle, shape, dtype, device):
+    """A new tensor of the handle's stream."""
+    if handle.stream is None or torch.cuda.current_stream(device) == handle.stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(handle.stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _matrix(handle, rows, cols, dtype, device):
+    """A new rows x cols matrix whose rows are a multiple of 16 bytes apart."""
+    per = 8 if dtype != torch.float32 else 4
+    if cols % per == 0:
+        return _empty(handle, (rows, cols), dtype, device)
+    return _empty(handle, (rows, -(-cols // per) * per), dtype, device)[:, :cols]
+
+
+def _experts(w, what, e, n, k, dtype, device):
+    """(leading dimension, stride between experts) of an e x n x k tensor, checked."""
+    if w.dim() != 3 or tuple(w.shape) != (e, n, k):
+        raise ValueError(f"{what} must be {e} x {n} x {k}, got {tuple(w.shape)}")
+    ld = _rows(w[0], what, n, k, dtype, device) if e else 8
+    stride = w.stride(0) if e > 1 else n * ld
+    if e > 1 and (stride <= 0 or stride % 8):
+        raise ValueError(f"{what}: experts must be a multiple of 16 bytes apart")
+    return ld, stride
+
+
+def _vector(t, what, shape, dtypes, device):
+    if tuple(t.shape) != shape or t.dtype not in dtypes or t.device != device or \
+            not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {shape} tensor of "
+                         f"{' or '.join(map(str, dtypes))} on {device}")
+    return t
+
+
+def _epilogue(act, bias, bias_shape, residual, beta, z, rows, n, dtype, out_dtype, device):
+    e = _tcg.Epilogue(activation=act)
+    if bias is not None:
+        _vector(bias, "bias", bias_shape, (dtype, torch.float32), device)
+        e.bias, e.bias_type = bias.data_ptr(), _TYPES[bias.dtype]
+    if residual is not None and beta != 0.0:
+        e.ldc = _rows(residual, "residual", rows, n, out_dtype, device)
+        e.C, e.beta = residual.data_ptr(), beta
+    if z is not None:
+        e.ldz = _rows(z, "z", rows, n, dtype, device)
+        e.Z = z.data_ptr()
+    return e
+
+
+def _out(handle, out, out_dtype, rows, n, dtype, device):
+    if out is None:
+        out = _matrix(handle, rows, n, out_dtype or dtype, device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out and out_dtype disagree")
+    if out.dtype not in (dtype, torch.float32):
+        raise ValueError(f"the output must be {dtype} or torch.float32, got {out.dtype}")
+    return out, _rows(out, "out", rows, n, out.dtype, device)
+
+
+def linear(handle, x, w, bias=None, act="none", residual=None, beta=1.0, alpha=1.0, out=None,
+           out_dtype=None, z=None):
+    """out = act(alpha * x @ w.T + bias) + beta * residual.
+
+    x: (tokens, k); w: (n, k); bias: (n,) of x's type or FP32; residual: (tokens, n) of the
+    output's type (it may be ``out`` itself); out: (tokens, n) of x's type or FP32, made if
+    None; z: (tokens, n) of x's type, receives the pre-activation that
+    :func:`linear_backward` wants.  act: "none", "relu", "gelu", "gelu_tanh" or "silu".
+    Returns out.
+    """
+    t, k, dtype, dev = _input(x)
+    n = w.shape[0]
+    ldw = _rows(w, "w", n, k, dtype, dev)
+    ldx = _rows(x, "x", t, k, dtype, dev)
+    out, ldo = _out(handle, out, out_dtype, t, n, dtype, dev)
+    e = _epilogue(_act(act), bias, (n,), residual, beta, z, t, n, dtype, out.dtype, dev)
+    code = _IN[dtype]
+    s = _tcg.load_library().tcg_gemm_epilogue(
+        handle.h, 1, 0, n, t, k, alpha, w.data_ptr(), ldw, x.data_ptr(), ldx, code, out.data_ptr(),
+        _TYPES[out.dtype], ldo, e)
+    if s:
+        raise _tcg.TcgError(s, "linear")
+    return out
+
+
+def _grad_z(handle, dout, z, act, want_dz, want_dbias, groups, offsets, dbias, ld_dout, rows, n):
+    """dz (dout itself where nothing has to be computed) and dbias."""
+    dtype, dev = dout.dtype, dout.device
+    dz = dout
+    if want_dbias:
+        shape = (n,) if offsets is None else (groups, n)
+        if dbias is None:
+            dbias = _empty(handle, shape, torch.float32, dev)
+        _vector(dbias, "dbias", shape, (torch.float32,), dev)
+    compute_dz = want_dz and act != 0
+    if compute_dz:
+        dz = _matrix(handle, rows, n, dtype, dev)
+    if compute_dz or want_dbias:
+        ldz = _rows(z, "z", rows, n, dtype, dev) if act else 0
+        s = _tcg.load_library().tcg_epilogue_backward(
+            handle.h, act, n, rows, groups, None if offsets is None else offsets.data_ptr(),
+            dout.data_ptr(), ld_dout, z.data_ptr() if act else None, ldz, _IN[dtype],
+            dz.data_ptr() if compute_dz else None,
+            _rows(dz, "dz", rows, n, dtype, dev), dbias.data_ptr() if want_dbias else None)
+        if s:
+            raise _tcg.TcgError(s, "epilogue_backward")
+    return dz, dbias
+
+
+def _backward_args(dout, x, z, act, n):
+    t, k, dtype, dev = _input(x)
+    ldx = _rows(x, "x", t, k, dtype, dev)
+    ldd = _rows(dout, "dout", t, n, dtype, dev)
+    code = _act(act)
+    if code and z is None:
+        raise ValueError("z, the pre-activation of the forward pass, is needed for act="
+                         f"{act!r}")
+    return t, k, dtype, dev, ldx, ldd, code
+
+
+def _want(want):
+    if not set(want) <= {"dx", "dw", "dbias"}:
+        raise ValueError("want names dx, dw and dbias only")
+    return "dx" in want, "dw" in want, "dbias" in want
+
+
+def linear_backward(handle, dout, x, w, z=None, act="none", want=("dx", "dw", "dbias"), dx=None,
+                    dw=None, dbias=None):
+    """Gradients of :func:`linear` (alpha = 1) for dout, the gradient of its output.
+
+    With dz = dout * act'(z): dx = dz @ w, dw = dz.T @ x, dbias = dz.sum(0) (FP32, from the
+    unrounded dz).  The residual's gradient is beta * dout.  ``want`` names what is computed;
+    the result is (dx, dw, dbias) with None for the others.  Outputs are made where not given.
+    """
+    n = w.shape[0]
+    t, k, dtype, dev, ldx, ldd, code = _backward_args(dout, x, z, act, n)
+    ldw = _rows(w, "w", n, k, dtype, dev)
+    want_dx, want_dw, want_db = _want(want)
+    dz, dbias = _grad_z(handle, dout, z, code, want_dx or want_dw, want_db, 1, None, dbias, ldd, t, n)
+    ldz = _rows(dz, "dz", t, n, dtype, dev)
+    ty, lib = _IN[dtype], _tcg.load_library()
+    if want_dx:
+        if dx is None:
+            dx = _matrix(handle, t, k, dtype, dev)
+        s = lib.tcg_gemm_ex(handle.h, 0, 0, k, t, n, 1.0, w.data_ptr(), ty, ldw, dz.data_ptr(), ty,
+                            ldz, 0.0, dx.data_ptr(), ty, _rows(dx, "dx", t, k, dtype, dev), 0)
+        if s:
+            raise _tcg.TcgError(s, "linear_backward dx")
+    if want_dw:
+        if dw is None:
+            dw = _matrix(handle, n, k, dtype, dev)
+        s = lib.tcg_gemm_ex(handle.h, 0, 1, k, n, t, 1.0, x.data_ptr(), ty, ldx, dz.data_ptr(), ty,
+                            ldz, 0.0, dw.data_ptr(), ty, _rows(dw, "dw", n, k, dtype, dev), 0)
+        if s:
+            raise _tcg.TcgError(s, "linear_backward dw")
+    return (dx if want_dx else None, dw if want_dw else None, dbias if want_db else None)
+
+
+def _check_offsets(offsets, e, device):
+    _vector(offsets, "offsets", (e + 1,), (torch.int64,), device)
+
+
+def grouped_linear(handle, x, w, offsets, bias=None, act="none", residual=None, beta=1.0, alpha=1.0,
+                   out=None, out_dtype=None, z=None):
+    """A layer of experts on rows sorted by expert: for every expert e and its rows
+    offsets[e] .. offsets[e + 1] - 1 of x,
+
+        out[rows] = act(alpha * x[rows] @ w[e].T + bias[e]) + beta * residual[rows].
+
+    x: (rows, k); w: (experts, n, k); offsets: int64 CUDA tensor of experts + 1
+    non-decreasing entries in 0 .. rows, read when the kernel runs (no host
+    synchronisation); bias: (experts, n).  Rows of no expert come out zero.  The rest as in
+    :func:`linear`.  At most 384 experts.
+    """
+    t, k, dtype, dev = _input(x)
+    if w.dim() != 3:
+        raise ValueError("w must be experts x n x k")
+    e, n = w.shape[0], w.shape[1]
+    ldw, stride = _experts(w, "w", e, n, k, dtype, dev)
+    ldx = _rows(x, "x", t, k, dtype, dev)
+    _check_offsets(offsets, e, dev)
+    out, ldo = _out(handle, out, out_dtype, t, n, dtype, dev)
+    ep = _epilogue(_act(act), bias, (e, n), residual, beta, z, t, n, dtype, out.dtype, dev)
+    s = _tcg.load_library().tcg_gemm_grouped(
+        handle.h, 1, n, t, k, e, offsets.data_ptr(), alpha, w.data_ptr(), ldw, stride, x.data_ptr(),
+        ldx, _IN[dtype], out.data_ptr(), _TYPES[out.dtype], ldo, ep)
+    if s:
+        raise _tcg.TcgError(s, "grouped_linear")
+    return out
+
+
+def grouped_linear_backward(handle, dout, x, w, offsets, z=None, act="none",
+                            want=("dx", "dw", "dbias"), dx=None, dw=None, dbias=None):
+    """Gradients of :func:`grouped_linear` (alpha = 1): dx (rows, k), zero for rows of no
+    expert; dw (experts, n, k), zero for an expert without rows; dbias (experts, n), FP32.
+    Arguments as in :func:`linear_backward`.
+    """
+    if w.dim() != 3:
+        raise ValueError("w must be experts x n x k")
+    e, n = w.shape[0], w.shape[1]
+    t, k, dtype, dev, ldx, ldd, code = _backward_args(dout, x, z, act, n)
+    ldw, stride = _experts(w, "w", e, n, k, dtype, dev)
+    _check_offsets(offsets, e, dev)
+    want_dx, want_dw, want_db = _want(want)
+    dz, dbias = _grad_z(handle, dout, z, code, want_dx or want_dw, want_db, e, offsets, dbias, ldd, t,
+                        n)
+    ldz = _rows(dz, "dz", t, n, dtype, dev)
+    ty, lib = _IN[dtype], _tcg.load_library()
+    if want_dx:
+        if dx is None:
+            dx = _matrix(handle, t, k, dtype, dev)
+        s = lib.tcg_gemm_grouped(handle.h, 0, k, t, n, e, offsets.data_ptr(), 1.0, w.data_ptr(), ldw,
+                                 stride, dz.data_ptr(), ldz, ty, dx.data_ptr(), ty,
+                                 _rows(dx, "dx", t, k, dtype, dev), None)
+        if s:
+            raise _tcg.TcgError(s, "grouped_linear_backward dx")
+    if want_dw:
+        if dw is None:
+            per = -(-k // 8) * 8
+            dw = _empty(handle, (e, n, per), dtype, dev)[:, :, :k]
+        lddw, strided = _experts(dw, "dw", e, n, k, dtype, dev)
+        s = lib.tcg_gemm_grouped_k(handle.h, k, n, t, e, offsets.data_ptr(), 1.0, x.data_ptr(), ldx,
+                                   dz.data_ptr(), ldz, ty, dw.data_ptr(), ty, lddw, strided)
+        if s:
+            raise _tcg.TcgError(s, "grouped_linear_backward dw")
+    return (dx if want_dx else None, dw if want_dw else None, dbias if want_db else None)
+
+
+def _xent_args(x, w, targets):
+    t, k, dtype, dev = _input(x)
+    v = w.shape[0]
+    ldx, ldw = _rows(x, "x", t, k, dtype, dev), _rows(w, "w", v, k, dtype, dev)
+    _vector(targets, "targets", (t,), (torch.int64,), dev)
+    return t, v, k, dtype, dev, ldx, ldw
+
+
+def linear_cross_entropy(handle, x, w, targets, ignore_index=-100, loss=None, lse=None):
+    """(loss, lse) of the softmax cross entropy of the logits x @ w.T, which are never stored:
+    per row, FP32, lse = logsumexp(logits) and loss = lse - logits[target].
+
+    x: (rows, k); w: (vocab, k); targets: (rows,) int64.  A row whose target is ignore_index
+    or outside 0 .. vocab - 1 has loss 0.
+    """
+    t, v, k, dtype, dev, ldx, ldw = _xent_args(x, w, targets)
+    loss = _empty(handle, (t,), torch.float32, dev) if loss is None else loss
+    lse = _empty(handle, (t,), torch.float32, dev) if lse is None else lse
+    _vector(loss, "loss", (t,), (torch.float32,), dev)
+    _vector(lse, "lse", (t,), (torch.float32,), dev)
+    s = _tcg.load_library().tcg_xent_forward(
+        handle.h, t, v, k, x.data_ptr(), ldx, w.data_ptr(), ldw, _IN[dtype], targets.data_ptr(),
+        ignore_index, loss.data_ptr(), lse.data_ptr())
+    if s:
+        raise _tcg.TcgError(s, "linear_cross_entropy")
+    return loss, lse
+
+
+def linear_cross_entropy_backward(handle, x, w, targets, lse, dloss, ignore_index=-100,
+                                  want=("dx", "dw"), dx=None, dw=None):
+    """(dx, dw) of :func:`linear_cross_entropy` for dloss, the gradient of each row's loss
+    (FP32; 1 / rows for a mean), and the lse that it returned.  ``want`` names what is
+    computed; None for the other.
+    """
+    t, v, k, dtype, dev, ldx, ldw = _xent_args(x, w, targets)
+    _vector(lse, "lse", (t,), (torch.float32,), dev)
+    _vector(dloss, "dloss", (t,), (torch.float32,), dev)
+    want_dx, want_dw, bad = _want(want)
+    if bad:
+        raise ValueError("want names dx and dw only")
+    if want_dx and dx is None:
+        dx = _matrix(handle, t, k, dtype, dev)
+    if want_dw and dw is None:
+        dw = _matrix(handle, v, k, dtype, dev)
+    s = _tcg.load_library().tcg_xent_backward(
+        handle.h, t, v, k, x.data_ptr(), ldx, w.data_ptr(), ldw, _IN[dtype], targets.data_ptr(),
+        ignore_index, lse.data_ptr(), dloss.data_ptr(), dx.data_ptr() if want_dx else None,
+        _rows(dx, "dx", t, k, dtype, dev) if want_dx else 8, dw.data_ptr() if want_dw else None,
+        _rows(dw, "dw", v, k, dtype, dev) if want_dw else 8)
+    if s:
+        raise _tcg.TcgError(s, "linear_cross_entropy_backward")
+    return (dx if want_dx else None, dw if want_dw else None)

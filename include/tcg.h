@@ -490,7 +490,7 @@ tcgStatus_t tcg_gemm_grouped_k(tcgHandle_t h, int64_t m, int64_t n, int64_t k, i
  * columns, in an order that depends only on the sizes.  offsets NULL with groups = 1: one
  * group of all columns.  dZ or dbias may be NULL; dZ may be dD.  Z is not read for
  * TCG_ACT_NONE.  Columns in no group get dZ = 0.  Workspace with dbias: at most
- * 4 * m * groups * (n / (16 * groups) + 1) bytes. */
+ * 4 * m * (n / 16 + 1 + groups) bytes. */
 tcgStatus_t tcg_epilogue_backward(tcgHandle_t h, tcgActivation_t activation, int64_t m, int64_t n,
                                   int64_t groups, const int64_t *offsets, const void *dD,
                                   int64_t lddd, const void *Z, int64_t ldz, tcgDataType_t type,

@@ -888,67 +888,165 @@ __global__ void __launch_bounds__(256)
 }
 
 // dZ = dD act'(Z) (column-major m x cols; dZ may be left out), and for each group the sum
-// of its columns of dZ before rounding.  Block (x, y, g): rows 256 x .. + 255 of group g, the
-// y-th of `parts` equal column ranges; its sums go to part[(g parts + y) m + row] and
-// tcg_bias_join_kernel adds the ranges in order.  Slot -1 (g = groups): the columns of no
-// group, whose dZ is zero.
+// of its columns of dZ before rounding.  Bound by memory: dD and Z are read once and dZ is
+// written once, 16 bytes a thread.  Block (x, y): rows 256 x .. + 255 of the y-th `chunk`
+// columns; a warp takes a column at a time, the eight warps every eighth column.  The
+// columns of a block fall into segments, one per group that meets it; a segment's sums go
+// to slot y + g of `part` -- (y, g) steps through a monotone path, so slots are distinct
+// and there are chunks + groups of them -- and tcg_bias_join_kernel adds a group's
+// segments in order.  Columns of no group get zeros.
 template <int ACT, bool BF16>
 __global__ void __launch_bounds__(256)
     tcg_epi_backward_kernel(int m, int cols, int groups, const int64_t *__restrict__ offsets,
-                            const uint16_t *__restrict__ dD, int64_t lddd,
-                            const uint16_t *__restrict__ Z, int64_t ldz, uint16_t *__restrict__ dZ,
-                            int64_t lddz, float *__restrict__ part)
+                            const uint16_t *dD, int64_t lddd, const uint16_t *Z, int64_t ldz,
+                            uint16_t *dZ, int64_t lddz, float *__restrict__ part, int chunk)
 {
+    __shared__ float join[8][256 + 8];
     griddep_launch_dependents();
     griddep_wait();
     LmArgs p;
     p.offsets = offsets;
     p.cols = cols;
     p.groups = groups;
-    const int g = blockIdx.z, y = blockIdx.y, parts = gridDim.y;
-    const int row = blockIdx.x * 256 + threadIdx.x;
-    if (row >= m)
-        return;
-    if (g == groups) {
-        if (dZ)
-            for (int s = 0; s <= groups + 1; s += groups + 1) {
-                int b, e;
-                slot_range(p, s, b, e);
-                for (int c = b + y; c < e; c += parts)
-                    dZ[static_cast<int64_t>(c) * lddz + row] = 0;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int row = blockIdx.x * 256 + lane * 8;
+    const int left = m - row;                         // rows of this thread (8, or fewer at the end)
+    const int c0 = blockIdx.y * chunk, c1 = min(c0 + chunk, cols);
+
+    auto load8 = [&](const uint16_t *src, float (&v)[8]) {
+        if (left >= 8) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(src);
+            const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (BF16) {
+                    v[2 * i] = __uint_as_float(u[i] << 16);
+                    v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+                } else {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u[i]));
+                    v[2 * i] = f.x;
+                    v[2 * i + 1] = f.y;
+                }
             }
-        return;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = i < left ? load16(src, i, BF16) : 0.0f;
+        }
+    };
+    auto store8 = [&](uint16_t *dst, const float (&v)[8]) {
+        if (left >= 8) {
+            uint32_t u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                u[i] = static_cast<uint32_t>(round16(v[2 * i], BF16)) |
+                       static_cast<uint32_t>(round16(v[2 * i + 1], BF16)) << 16;
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(u[0], u[1], u[2], u[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i < left)
+                    dst[i] = round16(v[i], BF16);
+        }
+    };
+    auto clear = [&](int from, int to) {
+        const float zero[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        if (dZ && left > 0)
+            for (int c = from + w; c < to; c += 8)
+                store8(dZ + static_cast<int64_t>(c) * lddz + row, zero);
+    };
+
+    int g = 0, at = c0;
+    if (offsets) {                                    // first group that ends past c0
+        int hi = groups;
+        while (g < hi) {
+            const int mid = (g + hi) >> 1;
+            if (offsets[mid + 1] > c0)
+                hi = mid;
+            else
+                g = mid + 1;
+        }
     }
-    int b, e;
-    group_range(p, g, b, e);
-    const int64_t len = e - b;
-    const int c0 = b + static_cast<int>(len * y / parts), c1 = b + static_cast<int>(len * (y + 1) / parts);
-    float sum = 0.0f;
-#pragma unroll 8
-    for (int c = c0; c < c1; ++c) {
-        float d = load16(dD, static_cast<int64_t>(c) * lddd + row, BF16);
-        if constexpr (ACT != kActNone)
-            d *= act_slope<ACT>(load16(Z, static_cast<int64_t>(c) * ldz + row, BF16));
-        if (dZ)
-            dZ[static_cast<int64_t>(c) * lddz + row] = round16(d, BF16);
-        sum += d;
+    for (; at < c1 && g < groups; ++g) {
+        int b, e;
+        group_range(p, g, b, e);
+        b = max(b, at);
+        e = min(e, c1);
+        if (b >= c1)
+            break;
+        clear(at, b);
+        at = b;
+        if (e <= b)
+            continue;
+        float sum[8] = {};
+        if (left > 0) {
+#pragma unroll 4
+            for (int c = b + w; c < e; c += 8) {
+                float d[8];
+                load8(dD + static_cast<int64_t>(c) * lddd + row, d);
+                if constexpr (ACT != kActNone) {
+                    float z[8];
+                    load8(Z + static_cast<int64_t>(c) * ldz + row, z);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        d[i] *= act_slope<ACT>(z[i]);
+                }
+                if (dZ)
+                    store8(dZ + static_cast<int64_t>(c) * lddz + row, d);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    sum[i] += d[i];
+            }
+        }
+        at = e;
+        if (part) {
+            __syncthreads();                          // the previous segment has been added
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                join[w][lane * 8 + i] = sum[i];
+            __syncthreads();
+            const int r = blockIdx.x * 256 + threadIdx.x;
+            if (r < m) {
+                float s = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    s += join[i][threadIdx.x];
+                part[(static_cast<int64_t>(blockIdx.y) + g) * m + r] = s;
+            }
+        }
     }
-    if (part)
-        part[(static_cast<int64_t>(g) * parts + y) * m + row] = sum;
+    clear(at, c1);
 }
 
+// dbias of group blockIdx.y: its segments in column order, the four warps of 64 rows taking
+// a quarter of them each.
 __global__ void __launch_bounds__(256)
-    tcg_bias_join_kernel(const float *__restrict__ part, int m, int parts, float *__restrict__ dbias)
+    tcg_bias_join_kernel(const float *__restrict__ part, int m, int cols, int groups,
+                         const int64_t *__restrict__ offsets, int chunk, float *__restrict__ dbias)
 {
+    __shared__ float join[4][64];
     griddep_launch_dependents();
     griddep_wait();
-    const int row = blockIdx.x * 256 + threadIdx.x;
-    if (row >= m)
-        return;
+    LmArgs p;
+    p.offsets = offsets;
+    p.cols = cols;
+    p.groups = groups;
+    const int g = blockIdx.y, lane = threadIdx.x & 63, q = threadIdx.x >> 6;
+    const int row = blockIdx.x * 64 + lane;
+    int b, e;
+    group_range(p, g, b, e);
+    const int y0 = b / chunk, y1 = e > b ? (e - 1) / chunk + 1 : y0;
+    const int a0 = y0 + (y1 - y0) * q / 4, a1 = y0 + (y1 - y0) * (q + 1) / 4;
     float s = 0.0f;
-    for (int y = 0; y < parts; ++y)
-        s += part[(static_cast<int64_t>(blockIdx.y) * parts + y) * m + row];
-    dbias[static_cast<int64_t>(blockIdx.y) * m + row] = s;
+    if (row < m) {
+#pragma unroll 8
+        for (int y = a0; y < a1; ++y)
+            s += part[(static_cast<int64_t>(y) + g) * m + row];
+    }
+    join[q][lane] = s;
+    __syncthreads();
+    if (q == 0 && row < m)
+        dbias[static_cast<int64_t>(g) * m + row] = ((s + join[1][lane]) + join[2][lane]) + join[3][lane];
 }
 
 template <typename... Params, typename... Args>
@@ -1047,30 +1145,32 @@ cudaError_t launch_round_out(const float *in, int64_t ldi, int rows, int cols, c
 template <int ACT>
 static cudaError_t epi_backward(int bf16, dim3 grid, cudaStream_t s, int m, int cols, int groups,
                                 const int64_t *offsets, const void *dD, int64_t lddd, const void *Z,
-                                int64_t ldz, void *dZ, int64_t lddz, float *part)
+                                int64_t ldz, void *dZ, int64_t lddz, float *part, int chunk)
 {
     return launch_pdl(bf16 ? tcg_epi_backward_kernel<ACT, true> : tcg_epi_backward_kernel<ACT, false>,
                       grid, dim3(256), s, m, cols, groups, offsets, static_cast<const uint16_t *>(dD),
                       lddd, static_cast<const uint16_t *>(Z), ldz, static_cast<uint16_t *>(dZ), lddz,
-                      part);
+                      part, chunk);
 }
 
 cudaError_t launch_epi_backward(int act, int bf16, int m, int cols, int groups,
                                 const int64_t *offsets, const void *dD, int64_t lddd, const void *Z,
                                 int64_t ldz, void *dZ, int64_t lddz, float *dbias, float *part,
-                                int parts, cudaStream_t s)
+                                int chunk, cudaStream_t s)
 {
-    // the extra slot of a grouped call clears the columns of no group
-    const dim3 grid((m + 255) / 256, parts, groups + (offsets ? 1 : 0));
-    auto fn = act == kActRelu ? epi_backward<kActRelu>
-            : act == kActGelu ? epi_backward<kActGelu>
-            : act == kActGeluTanh ? epi_backward<kActGeluTanh>
-            : act == kActSilu ? epi_backward<kActSilu> : epi_backward<kActNone>;
-    cudaError_t e = fn(bf16, grid, s, m, cols, groups, offsets, dD, lddd, Z, ldz, dZ, lddz,
-                       dbias ? part : nullptr);
+    cudaError_t e = cudaSuccess;
+    if (cols > 0) {
+        const dim3 grid((m + 255) / 256, (cols + chunk - 1) / chunk);
+        auto fn = act == kActRelu ? epi_backward<kActRelu>
+                : act == kActGelu ? epi_backward<kActGelu>
+                : act == kActGeluTanh ? epi_backward<kActGeluTanh>
+                : act == kActSilu ? epi_backward<kActSilu> : epi_backward<kActNone>;
+        e = fn(bf16, grid, s, m, cols, groups, offsets, dD, lddd, Z, ldz, dZ, lddz,
+               dbias ? part : nullptr, chunk);
+    }
     if (e == cudaSuccess && dbias)
-        e = launch_pdl(tcg_bias_join_kernel, dim3((m + 255) / 256, groups), dim3(256), s,
-                       const_cast<const float *>(part), m, parts, dbias);
+        e = launch_pdl(tcg_bias_join_kernel, dim3((m + 63) / 64, groups), dim3(256), s,
+                       const_cast<const float *>(part), m, cols, groups, offsets, chunk, dbias);
     return e;
 }
 

@@ -117,10 +117,11 @@ cudaError_t launch_xent_scale(const float *dloss, const int64_t *targets, int ro
 // out[j][i] = scale * in[j][i], rounded to the 16-bit type.
 cudaError_t launch_round_out(const float *in, int64_t ldi, int rows, int cols, const float *scale,
                              void *out, int64_t ldo, int out_kind, int grid, cudaStream_t s);
-// dZ = dD * act'(Z) and per-group sums of its rows; see tcg_epi_backward_kernel.
+// dZ = dD * act'(Z) and per-group sums of its rows; see tcg_epi_backward_kernel.  part:
+// (ceil(cols / chunk) + groups) * m floats.
 cudaError_t launch_epi_backward(int act, int bf16, int m, int cols, int groups,
                                 const int64_t *offsets, const void *dD, int64_t lddd, const void *Z,
                                 int64_t ldz, void *dZ, int64_t lddz, float *dbias, float *part,
-                                int parts, cudaStream_t s);
+                                int chunk, cudaStream_t s);
 
 }  // namespace tcg

@@ -574,22 +574,23 @@ tcgStatus_t tcg_epilogue_backward(tcgHandle_t h, tcgActivation_t activation, int
     if (st != TCG_STATUS_SUCCESS)
         return st;
     h->used = true;
-    // column ranges per group: about four blocks of 256 rows per SM, 16 columns each at least
+    // Columns per block: about eight blocks of 256 rows per SM, 16 to 256 columns each.
     const int64_t row_blocks = (m + 255) / 256;
-    int64_t parts = 4 * static_cast<int64_t>(h->num_sms) / (row_blocks * groups);
-    const int64_t most = (n / groups + 15) / 16;
-    parts = parts > most ? most : parts;
-    parts = parts < 1 ? 1 : parts;
+    int64_t chunk = n * row_blocks / (8 * static_cast<int64_t>(h->num_sms)) / 8 * 8;
+    chunk = chunk < 16 ? 16 : (chunk > 256 ? 256 : chunk);
+    while ((n + chunk - 1) / chunk > 65535)              // the grid's second dimension
+        chunk *= 2;
     void *ws = nullptr;
     if (dbias) {
-        st = acquire_ws(h, static_cast<size_t>(groups * parts * m) * 4, &ws);
+        st = acquire_ws(h, static_cast<size_t>((n + chunk - 1) / chunk + groups) * static_cast<size_t>(m) * 4,
+                        &ws);
         if (st != TCG_STATUS_SUCCESS)
             return st;
     }
     const cudaError_t e = launch_epi_backward(
         activation, type == TCG_R_16BF, static_cast<int>(m), static_cast<int>(n),
         static_cast<int>(groups), offsets, dD, lddd, need_z ? Z : nullptr, ldz, n > 0 ? dZ : nullptr,
-        lddz, dbias, static_cast<float *>(ws), static_cast<int>(parts), h->stream);
+        lddz, dbias, static_cast<float *>(ws), static_cast<int>(chunk), h->stream);
     h->launches += dbias ? 2 : 1;
     if (e != cudaSuccess) {
         cudaGetLastError();

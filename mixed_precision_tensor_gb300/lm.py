@@ -16,23 +16,30 @@ import mixed_precision_tensor_gb300 as _tcg
 
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 _IN = {torch.float16: 0, torch.bfloat16: 1}                  # TCG_R_16F, TCG_R_16BF
+# the current stream's cudaStream_t by device index, without making a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 _TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+
+def _lib():
+    return _tcg._lib or _tcg.load_library()
 
 
 def _rows(t, what, rows, cols, dtype, device):
     """Leading dimension of a rows x cols matrix, checked."""
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{what} must be {rows} x {cols}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{what} must be on {device}, got {t.device}")
     s0, s1 = t.stride()
-    if cols > 1 and s1 != 1:
+    per = 4 if dtype is torch.float32 else 8
+    if s1 != 1 and cols > 1:
         raise ValueError(f"{what} must have unit stride along its last dimension")
-    per = 16 // t.element_size()
     if rows <= 1:
-        return max(1, -(-cols // per)) * per
+        return (cols + per - 1) // per * per or per
     if s0 < cols or s0 % per:
         raise ValueError(f"{what}: rows must be a multiple of 16 bytes apart, got {s0} elements")
     return s0
@@ -56,9 +63,10 @@ def _act(act):
 
 def _empty(handle, shape, dtype, device):
     """A new tensor of the handle's stream."""
-    if handle.stream is None or torch.cuda.current_stream(device) == handle.stream:
+    own = handle.stream
+    if own is None or _raw_stream(device.index) == own.cuda_stream:
         return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(handle.stream):
+    with torch.cuda.stream(own):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
@@ -72,17 +80,26 @@ def _matrix(handle, rows, cols, dtype, device):
 
 def _experts(w, what, e, n, k, dtype, device):
     """(leading dimension, stride between experts) of an e x n x k tensor, checked."""
-    if w.dim() != 3 or tuple(w.shape) != (e, n, k):
+    if w.shape != (e, n, k):
         raise ValueError(f"{what} must be {e} x {n} x {k}, got {tuple(w.shape)}")
-    ld = _rows(w[0], what, n, k, dtype, device) if e else 8
-    stride = w.stride(0) if e > 1 else n * ld
-    if e > 1 and (stride <= 0 or stride % 8):
+    if w.dtype is not dtype or w.device != device:
+        raise ValueError(f"{what} must be {dtype} on {device}")
+    stride, ld, s2 = w.stride()
+    if s2 != 1 and k > 1:
+        raise ValueError(f"{what} must have unit stride along its last dimension")
+    if n <= 1:
+        ld = (k + 7) // 8 * 8 or 8
+    if ld < k or ld % 8:
+        raise ValueError(f"{what}: rows must be a multiple of 16 bytes apart, got {ld} elements")
+    if e <= 1:
+        stride = n * ld
+    elif stride <= 0 or stride % 8:
         raise ValueError(f"{what}: experts must be a multiple of 16 bytes apart")
     return ld, stride
 
 
 def _vector(t, what, shape, dtypes, device):
-    if tuple(t.shape) != shape or t.dtype not in dtypes or t.device != device or \
+    if t.shape != shape or t.dtype not in dtypes or t.device != device or \
             not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {shape} tensor of "
                          f"{' or '.join(map(str, dtypes))} on {device}")
@@ -90,7 +107,8 @@ def _vector(t, what, shape, dtypes, device):
 
 
 def _epilogue(act, bias, bias_shape, residual, beta, z, rows, n, dtype, out_dtype, device):
-    e = _tcg.Epilogue(activation=act)
+    e = _tcg.Epilogue()
+    e.activation = act
     if bias is not None:
         _vector(bias, "bias", bias_shape, (dtype, torch.float32), device)
         e.bias, e.bias_type = bias.data_ptr(), _TYPES[bias.dtype]
@@ -130,7 +148,7 @@ def linear(handle, x, w, bias=None, act="none", residual=None, beta=1.0, alpha=1
     out, ldo = _out(handle, out, out_dtype, t, n, dtype, dev)
     e = _epilogue(_act(act), bias, (n,), residual, beta, z, t, n, dtype, out.dtype, dev)
     code = _IN[dtype]
-    s = _tcg.load_library().tcg_gemm_epilogue(
+    s = _lib().tcg_gemm_epilogue(
         handle.h, 1, 0, n, t, k, alpha, w.data_ptr(), ldw, x.data_ptr(), ldx, code, out.data_ptr(),
         _TYPES[out.dtype], ldo, e)
     if s:
@@ -152,7 +170,7 @@ def _grad_z(handle, dout, z, act, want_dz, want_dbias, groups, offsets, dbias, l
         dz = _matrix(handle, rows, n, dtype, dev)
     if compute_dz or want_dbias:
         ldz = _rows(z, "z", rows, n, dtype, dev) if act else 0
-        s = _tcg.load_library().tcg_epilogue_backward(
+        s = _lib().tcg_epilogue_backward(
             handle.h, act, n, rows, groups, None if offsets is None else offsets.data_ptr(),
             dout.data_ptr(), ld_dout, z.data_ptr() if act else None, ldz, _IN[dtype],
             dz.data_ptr() if compute_dz else None,
@@ -193,7 +211,7 @@ def linear_backward(handle, dout, x, w, z=None, act="none", want=("dx", "dw", "d
     want_dx, want_dw, want_db = _want(want)
     dz, dbias = _grad_z(handle, dout, z, code, want_dx or want_dw, want_db, 1, None, dbias, ldd, t, n)
     ldz = _rows(dz, "dz", t, n, dtype, dev)
-    ty, lib = _IN[dtype], _tcg.load_library()
+    ty, lib = _IN[dtype], _lib()
     if want_dx:
         if dx is None:
             dx = _matrix(handle, t, k, dtype, dev)
@@ -236,7 +254,7 @@ def grouped_linear(handle, x, w, offsets, bias=None, act="none", residual=None, 
     _check_offsets(offsets, e, dev)
     out, ldo = _out(handle, out, out_dtype, t, n, dtype, dev)
     ep = _epilogue(_act(act), bias, (e, n), residual, beta, z, t, n, dtype, out.dtype, dev)
-    s = _tcg.load_library().tcg_gemm_grouped(
+    s = _lib().tcg_gemm_grouped(
         handle.h, 1, n, t, k, e, offsets.data_ptr(), alpha, w.data_ptr(), ldw, stride, x.data_ptr(),
         ldx, _IN[dtype], out.data_ptr(), _TYPES[out.dtype], ldo, ep)
     if s:
@@ -260,7 +278,7 @@ def grouped_linear_backward(handle, dout, x, w, offsets, z=None, act="none",
     dz, dbias = _grad_z(handle, dout, z, code, want_dx or want_dw, want_db, e, offsets, dbias, ldd, t,
                         n)
     ldz = _rows(dz, "dz", t, n, dtype, dev)
-    ty, lib = _IN[dtype], _tcg.load_library()
+    ty, lib = _IN[dtype], _lib()
     if want_dx:
         if dx is None:
             dx = _matrix(handle, t, k, dtype, dev)
@@ -301,7 +319,7 @@ def linear_cross_entropy(handle, x, w, targets, ignore_index=-100, loss=None, ls
     lse = _empty(handle, (t,), torch.float32, dev) if lse is None else lse
     _vector(loss, "loss", (t,), (torch.float32,), dev)
     _vector(lse, "lse", (t,), (torch.float32,), dev)
-    s = _tcg.load_library().tcg_xent_forward(
+    s = _lib().tcg_xent_forward(
         handle.h, t, v, k, x.data_ptr(), ldx, w.data_ptr(), ldw, _IN[dtype], targets.data_ptr(),
         ignore_index, loss.data_ptr(), lse.data_ptr())
     if s:
@@ -325,7 +343,7 @@ def linear_cross_entropy_backward(handle, x, w, targets, lse, dloss, ignore_inde
         dx = _matrix(handle, t, k, dtype, dev)
     if want_dw and dw is None:
         dw = _matrix(handle, v, k, dtype, dev)
-    s = _tcg.load_library().tcg_xent_backward(
+    s = _lib().tcg_xent_backward(
         handle.h, t, v, k, x.data_ptr(), ldx, w.data_ptr(), ldw, _IN[dtype], targets.data_ptr(),
         ignore_index, lse.data_ptr(), dloss.data_ptr(), dx.data_ptr() if want_dx else None,
         _rows(dx, "dx", t, k, dtype, dev) if want_dx else 8, dw.data_ptr() if want_dw else None,

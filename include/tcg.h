@@ -470,9 +470,10 @@ tcgStatus_t tcg_gemm_grouped(tcgHandle_t h, tcgOp_t transa, int64_t m, int64_t n
                              const tcgEpilogue_t *epilogue);
 
 /* Workspace of the two calls above on h's device (binds h), groups = 0 for
- * tcg_gemm_epilogue.  transb as in tcg_gemm_epilogue (OP_N for a grouped call). */
-tcgStatus_t tcg_gemm_epilogue_workspace_size(tcgHandle_t h, tcgOp_t transb, int64_t m, int64_t n,
-                                             int64_t k, int64_t groups, size_t *bytes);
+ * tcg_gemm_epilogue.  transa and transb as there (transb OP_N for a grouped call). */
+tcgStatus_t tcg_gemm_epilogue_workspace_size(tcgHandle_t h, tcgOp_t transa, tcgOp_t transb,
+                                             int64_t m, int64_t n, int64_t k, int64_t groups,
+                                             size_t *bytes);
 
 /* The weight gradients of a grouped product: one m x n matrix per group, summed over the
  * group's tokens,

@@ -155,7 +155,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.tcg_gemm_grouped_k.argtypes = [vp, i64, i64, i64, i64, vp, f32, vp, i64, vp, i64, ci,
                                            vp, ci, i64, i64]
         lib.tcg_gemm_epilogue_workspace_size.restype = st
-        lib.tcg_gemm_epilogue_workspace_size.argtypes = [vp, ci, i64, i64, i64, i64,
+        lib.tcg_gemm_epilogue_workspace_size.argtypes = [vp, ci, ci, i64, i64, i64, i64,
                                                          ctypes.POINTER(ctypes.c_size_t)]
         lib.tcg_epilogue_backward.restype = st
         lib.tcg_epilogue_backward.argtypes = [vp, ci, i64, i64, i64, vp, vp, i64, vp, i64, ci, vp,
@@ -374,9 +374,9 @@ def tcg_gemm_grouped_k(h, m, n, k, groups, offsets, alpha, A, lda, B, ldb, ABtyp
                                              lda, _ptr(B), ldb, ABtype, _ptr(D), Dtype, ldd, strideD)
 
 
-def tcg_gemm_epilogue_workspace_size(h, transb, m, n, k, groups=0) -> int:
+def tcg_gemm_epilogue_workspace_size(h, transa, transb, m, n, k, groups=0) -> int:
     out = ctypes.c_size_t(0)
-    check(load_library().tcg_gemm_epilogue_workspace_size(h, transb, m, n, k, groups,
+    check(load_library().tcg_gemm_epilogue_workspace_size(h, transa, transb, m, n, k, groups,
                                                           ctypes.byref(out)),
           "tcg_gemm_epilogue_workspace_size")
     return out.value

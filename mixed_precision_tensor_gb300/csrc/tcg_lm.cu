@@ -1,17 +1,23 @@
 // tcg_lm.cu -- device code of the language-model products (sm_103a).
 //
 // tcg_lm_kernel is a persistent, warp-specialised tensor-core product over CTA pairs
-// (tcgen05, cta_group::2), column-major like the rest of the library:
-//
-//   kEpiLinear     D_g = act(alpha op(A_g) op(B_g) + bias_g) + beta C_g   for every group g
-//   kEpiXentStats  logits L = X W^T in tiles that never leave the chip: per row and tile
-//                  half the maximum m and s = sum exp(L - m), and the target's logit
-//   kEpiXentGrad   G = dloss (exp(L - lse) - [target]), rounded to 16 bits
+// (tcgen05, cta_group::2; 256 x BN tiles, M = 256 accumulator rows, N = BN columns):
 //
 //   warp 0 (one lane)   TMA producer into a ring of 128-byte-swizzled stages (64 K elements
 //                       of 128 rows of A and BN / 2 rows of B per CTA)
-//   warp 1 (one lane)   tcgen05.mma, M = 256, N = BN, into TMEM accumulators (up to four)
-//   warps 2-9           epilogue: TMEM -> registers -> memory
+//   warp 1 (one lane)   tcgen05.mma into TMEM accumulators (up to four)
+//   warps 2-9           epilogue: TMEM -> registers -> memory, one accumulator row a thread
+//
+// The epilogues (LmEpi):
+//   kEpiNarrow     features on the rows, tokens on the columns: few tokens against a weight
+//                  matrix that streams by once
+//   kEpiWide       tokens on the rows, features on the columns: a thread holds 32 adjacent
+//                  features of a token, so bias, residual, pre-activation and output move in
+//                  16-byte pieces
+//   kEpiXentStats  logits X W^T that never leave the chip: per row and tile half the maximum
+//                  m and sum exp(logit - m), and the target's logit (tokens on the rows)
+//   kEpiXentNarrow the same for few tokens (tokens on the columns)
+//   kEpiXentGrad   dloss (exp(logit - lse) - [target]), rounded to 16 bits
 //
 // Every wait is bounded as in tcg_kernels.cu: a wait that runs out sets a bit in the
 // device error word, every role stops and the kernel returns.
@@ -26,6 +32,14 @@ namespace tcg {
 
 namespace {
 
+// How the tiles of a call are spread over the pairs (see LmWalk).
+struct LmPlan {
+    int tiles;          // tiles of the groups
+    int whole;          // tiles [0, whole) go whole, round robin; the rest are cut along K
+    int share;          // K blocks of the cut tiles per pair
+    int null_tiles[2];  // tiles of the columns (rows) before the first and after the last group
+};
+
 struct LmCtl {
     uint64_t full[kLmMaxStages];
     uint64_t empty[kLmMaxStages];
@@ -35,70 +49,138 @@ struct LmCtl {
     uint32_t tmem_base;
     volatile int abort_flag;
     volatile int last_arrival[2];
-    int cum[kLmMaxGroups + 3];    // units before slot s (see lm_slots)
+    LmPlan plan;
+    int cum[kLmMaxGroups + 1];              // tiles before each group of a grouped call
 };
-constexpr int kLmCtlBytes = 2048;
+constexpr int kLmCtlBytes = 2 * 1024;
 static_assert(sizeof(LmCtl) <= kLmCtlBytes, "control area too small");
-constexpr int kLmSmemBytes = kDataBytes + kLmCtlBytes + 1024;   // + alignment slack
+constexpr int kLmSmemBytes = kLmDataBytes + kLmCtlBytes + 1024;   // + alignment slack
 
 // ------------------------------------------------------------------------- activations
-// exp2 and the reciprocal run on the special-function unit (ex2.approx, fast division,
-// relative error about 2^-22), below the rounding of every output type but FP32, where
-// they are of its own size.
-//
-// GELU: x Phi(x) = max(x, 0) - |x| erfc(|x| / sqrt 2) / 2, with erfc(a) = (a1 t + ... +
-// a5 t^5) exp(-a^2), t = 1 / (1 + p a): Abramowitz & Stegun 7.1.26, |error| <= 1.5e-7.
-__device__ __forceinline__ float half_erfc(float ax, float &gauss)
+// Two FP32 values in a register pair: one instruction adds, multiplies or multiply-adds both
+// (each rounded to nearest as the scalar forms).
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float a, float b)
 {
-    const float a = fminf(ax, 20.0f) * 0.70710678118654752f;
-    const float t = __fdividef(1.0f, fmaf(0.3275911f, a, 1.0f));
-    gauss = __expf(-a * a);
-    float q = fmaf(t, 1.061405429f, -1.453152027f);
-    q = fmaf(t, q, 1.421413741f);
-    q = fmaf(t, q, -0.284496736f);
-    q = fmaf(t, q, 0.254829592f);
-    return 0.5f * q * t * gauss;
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ void split2(F2 p, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v));
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b)
+{
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+template <typename F>
+__device__ __forceinline__ F2 each(F2 p, F f)
+{
+    float a, b;
+    split2(p, a, b);
+    return f2(f(a), f(b));
+}
+
+// 2^x and 1 / x on the special-function unit: relative error about 2^-22, results below
+// 2^-126 flushed to zero.  That is under the rounding of every output type but FP32, where
+// it is of the rounding's own size.
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_fast(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ F2 exp2_2(F2 x) { return each(x, exp2_fast); }
+__device__ __forceinline__ F2 rcp_2(F2 x) { return each(x, rcp_fast); }
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// erfc(|x| / sqrt 2) / 2 and exp(-x^2 / 2), with erfc(a) = (a1 t + ... + a5 t^5) exp(-a^2),
+// t = 1 / (1 + p a): Abramowitz & Stegun 7.1.26, |error| <= 1.5e-7.  ax = min(|x|, 20), past
+// which both are zero.
+__device__ __forceinline__ F2 half_erfc(F2 ax, F2 &gauss)
+{
+    const F2 t = rcp_2(fma2(f2(0.3275911f * 0.70710678118654752f), ax, f2(1.0f)));
+    gauss = exp2_2(ax * ax * f2(-0.5f * kLog2e));
+    F2 q = fma2(t, f2(0.5f * 1.061405429f), f2(0.5f * -1.453152027f));
+    q = fma2(t, q, f2(0.5f * 1.421413741f));
+    q = fma2(t, q, f2(0.5f * -0.284496736f));
+    q = fma2(t, q, f2(0.5f * 0.254829592f));
+    return q * t * gauss;
 }
 
 template <int ACT>
-__device__ __forceinline__ float act_fn(float x)
+__device__ __forceinline__ F2 act_fn(F2 x)
 {
     if constexpr (ACT == kActRelu) {
-        return x < 0.0f ? 0.0f : x;
+        return each(x, [](float v) { return v < 0.0f ? 0.0f : v; });
     } else if constexpr (ACT == kActGelu) {
-        float g;
-        const float ax = fabsf(x), h = half_erfc(ax, g);
-        return (x > 0.0f ? x : 0.0f * x) - fminf(ax, 20.0f) * h;
+        // x Phi(x) = max(x, 0) - |x| erfc(|x| / sqrt 2) / 2; 0 x keeps NaN (and -inf, whose
+        // product with zero has no value either)
+        F2 g;
+        const F2 ax = each(x, [](float v) { return fminf(fabsf(v), 20.0f); });
+        const F2 h = half_erfc(ax, g);
+        const F2 pos = each(x, [](float v) { return v > 0.0f ? v : 0.0f * v; });
+        return fma2(ax * f2(-1.0f), h, pos);
     } else if constexpr (ACT == kActGeluTanh) {
-        // 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u))
-        const float u2 = -1.5957691216057308f * x * fmaf(0.044715f * x, x, 1.0f);
-        return __fdividef(x, 1.0f + __expf(u2));
+        // 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u)), u = sqrt(2 / pi) (x + 0.044715 x^3)
+        const F2 c = f2(-1.5957691216057308f * kLog2e);
+        const F2 e = exp2_2(x * fma2(c * f2(0.044715f) * x, x, c));
+        return x * rcp_2(e + f2(1.0f));
     } else if constexpr (ACT == kActSilu) {
-        return __fdividef(x, 1.0f + __expf(-x));
+        return x * rcp_2(exp2_2(x * f2(-kLog2e)) + f2(1.0f));
     } else {
         return x;
     }
 }
 
 template <int ACT>
-__device__ __forceinline__ float act_slope(float x)
+__device__ __forceinline__ F2 act_slope(F2 x)
 {
     if constexpr (ACT == kActRelu) {
-        return x > 0.0f ? 1.0f : (x <= 0.0f ? 0.0f : x);
+        return each(x, [](float v) { return v > 0.0f ? 1.0f : (v <= 0.0f ? 0.0f : v); });
     } else if constexpr (ACT == kActGelu) {
-        float g;
-        const float h = half_erfc(fabsf(x), g);
-        return (x > 0.0f ? 1.0f - h : h) + x * (0.39894228040143268f * g);
+        F2 g;
+        const F2 ax = each(x, [](float v) { return fminf(fabsf(v), 20.0f); });
+        float h0, h1, x0, x1;
+        split2(half_erfc(ax, g), h0, h1);
+        split2(x, x0, x1);
+        const F2 phi = f2(x0 > 0.0f ? 1.0f - h0 : h0, x1 > 0.0f ? 1.0f - h1 : h1);
+        return fma2(x * f2(0.39894228040143268f), g, phi);
     } else if constexpr (ACT == kActGeluTanh) {
-        const float x2 = x * x;
-        const float u2 = -1.5957691216057308f * x * fmaf(0.044715f, x2, 1.0f);
-        const float s = __fdividef(1.0f, 1.0f + __expf(u2));
-        return s + x * s * (1.0f - s) * 1.5957691216057308f * fmaf(3.0f * 0.044715f, x2, 1.0f);
+        const F2 c = f2(-1.5957691216057308f * kLog2e), x2 = x * x;
+        const F2 s = rcp_2(exp2_2(x * fma2(c * f2(0.044715f), x2, c)) + f2(1.0f));
+        const F2 d = fma2(f2(1.5957691216057308f * 3.0f * 0.044715f), x2, f2(1.5957691216057308f));
+        return fma2(x * s * fma2(s, f2(-1.0f), f2(1.0f)), d, s);
     } else if constexpr (ACT == kActSilu) {
-        const float s = __fdividef(1.0f, 1.0f + __expf(-x));
-        return s * fmaf(x, 1.0f - s, 1.0f);
+        const F2 s = rcp_2(exp2_2(x * f2(-kLog2e)) + f2(1.0f));
+        return s * fma2(x, fma2(s, f2(-1.0f), f2(1.0f)), f2(1.0f));
     } else {
-        return 1.0f;
+        return f2(1.0f);
     }
 }
 
@@ -133,159 +215,317 @@ __device__ __forceinline__ void store_as(void *p, int64_t i, float v)
 }
 
 // ------------------------------------------------------------------------------- units
-// Range of group g, clamped into the `cols` rows that exist whatever the offsets say.
-__device__ __forceinline__ void group_range(const LmArgs &p, int g, int &begin, int &end)
+// Range of group g, clamped into the `tokens` that exist whatever the offsets say.
+__device__ __forceinline__ void group_range(const int64_t *offsets, int tokens, int g, int &begin,
+                                            int &end)
 {
-    if (!p.offsets) {
+    if (!offsets) {
         begin = 0;
-        end = p.cols;
+        end = tokens;
         return;
     }
-    const int64_t b = p.offsets[g], e = p.offsets[g + 1], c = p.cols;
+    const int64_t b = offsets[g], e = offsets[g + 1], c = tokens;
     begin = static_cast<int>(b < 0 ? 0 : (b > c ? c : b));
     end = static_cast<int>(e < begin ? begin : (e > c ? c : e));
 }
 
-// Slots of an N-ragged grouped call: slot 0 holds the columns before the first group,
-// slots 1 .. groups the groups, slot groups + 1 the columns after the last one.  The
-// first and last slots' columns belong to no group and come out zero.
-__device__ __forceinline__ void slot_range(const LmArgs &p, int s, int &begin, int &end)
+// The tokens of no group: before the first (which = 0) and after the last (1).
+__device__ __forceinline__ void null_range(const LmArgs &p, int which, int &begin, int &end)
 {
-    if (s >= 1 && s <= p.groups) {
-        group_range(p, s - 1, begin, end);
-        return;
-    }
-    const int64_t o = p.offsets[s == 0 ? 0 : p.groups], c = p.cols;
+    const int64_t o = p.offsets[which ? p.groups : 0], c = p.tokens;
     const int at = static_cast<int>(o < 0 ? 0 : (o > c ? c : o));
-    begin = s == 0 ? 0 : at;
-    end = s == 0 ? at : p.cols;
+    begin = which ? at : 0;
+    end = which ? p.tokens : at;
 }
 
 struct LmUnit {
-    int g;              // group (matrix of A; bias; of D for K-ragged calls); -1: no group
-    int mt;             // tile row
-    int col0, col_end;  // first column of the tile, end of the columns it may write
-    int kb0, kb1, ks;   // K blocks and split index
-    int tok0, toks;     // K ragged: first token, tokens
-    int tile;           // index of the tile (split counters)
+    int g;                  // group; -1: tokens of no group, which come out zero
+    int row0, row_end;      // accumulator rows: first, and end of what may be written
+    int col0, col_end;      // accumulator columns
+    int kb0, kb1;           // K blocks
+    int tok0, toks;         // K ragged: first token, tokens
+    int slot;               // partial-sum slot of a cut tile's piece; -1: the whole tile
+    int first_pair, pieces; // of a cut tile
+    int counter;
 };
 
-// A role's walk over its pair's units: unit u -> LmUnit, u increasing.
-template <int BN, bool RK>
+// A role's walk over the units of its pair c of P.  Tiles 0 .. whole - 1 go whole, tile t to
+// pair t mod P.  The tiles after them, fewer than P, would keep only some pairs busy: where
+// that costs more than joining partial sums, their K blocks are laid end to end and every
+// pair takes `share` of them -- a piece of one tile, or the end of one and the start of the
+// next (and whole tiles between).  A pair has at most one piece that starts inside a tile
+// (slot 2 c) and one that starts a tile without ending it (slot 2 c + 1).
+template <bool WIDE, int BN, bool RK>
 struct LmWalk {
-    int slot = 0;
-    int begin = 0, end = 0, at = -1;     // slot whose range is loaded
+    int c, P;
+    int t, null_i;
+    int64_t pos;
+    int group = 0, at = -1, begin = 0, end = 0;     // group of tile t; whose range is loaded
 
-    __device__ __forceinline__ LmUnit unit(const LmArgs &p, const int *cum, int u)
+    __device__ __forceinline__ LmWalk(int pair, int pairs) : c(pair), P(pairs), t(pair),
+                                                             null_i(pair), pos(-1) {}
+
+    __device__ __forceinline__ bool next(const LmArgs &p, const LmCtl *ctl, LmUnit &w)
     {
-        LmUnit w;
+        const LmPlan &pl = ctl->plan;
+        w.slot = -1;
         w.tok0 = w.toks = 0;
-        if constexpr (RK) {
-            const int per = p.num_m_tiles * p.num_n_tiles;
-            const int g = u / per;
-            if (g != at) {
-                group_range(p, g, begin, end);
-                at = g;
+        w.kb0 = 0;
+        w.kb1 = p.num_k_blocks;
+        if (t < pl.whole) {
+            locate(p, ctl, t, w);
+            t += P;
+            return true;
+        }
+        const int cut = pl.tiles - pl.whole;
+        if (cut > 0) {
+            const int64_t work = static_cast<int64_t>(cut) * p.num_k_blocks;
+            const int64_t stop = min(static_cast<int64_t>(c + 1) * pl.share, work);
+            if (pos < 0)
+                pos = static_cast<int>(min(static_cast<int64_t>(c) * pl.share, work));
+            if (pos < stop) {
+                const int r = static_cast<int>(pos / p.num_k_blocks);
+                const int64_t r0 = static_cast<int64_t>(r) * p.num_k_blocks;
+                w.kb0 = static_cast<int>(pos - r0);
+                w.kb1 = static_cast<int>(min(static_cast<int64_t>(p.num_k_blocks), w.kb0 + stop - pos));
+                pos += w.kb1 - w.kb0;
+                if (w.kb1 - w.kb0 < p.num_k_blocks) {
+                    w.slot = 2 * c + (w.kb0 == 0 ? 1 : 0);
+                    w.first_pair = static_cast<int>(r0 / pl.share);
+                    w.pieces = static_cast<int>((r0 + p.num_k_blocks - 1) / pl.share) - w.first_pair + 1;
+                    w.counter = r;
+                }
+                locate(p, ctl, pl.whole + r, w);
+                return true;
             }
-            int nt;
-            tile(p, u - g * per, p.num_n_tiles, w.mt, nt);
-            w.g = g;
-            w.col0 = nt * BN;
-            w.col_end = p.n;
+        }
+        const int nulls = pl.null_tiles[0] + pl.null_tiles[1];
+        if (null_i < nulls) {
+            const int which = null_i >= pl.null_tiles[0] ? 1 : 0;
+            int b, e;
+            null_range(p, which, b, e);
+            w.g = -1;
+            w.kb1 = 0;
+            place(p, null_i - (which ? pl.null_tiles[0] : 0), b, e, w);
+            null_i += P;
+            return true;
+        }
+        return false;
+    }
+
+    __device__ __forceinline__ void locate(const LmArgs &p, const LmCtl *ctl, int tile, LmUnit &w)
+    {
+        if constexpr (RK) {
+            const int per = p.num_row_tiles * p.num_col_tiles;
+            w.g = tile / per;
+            if (w.g != at) {
+                group_range(p.offsets, p.tokens, w.g, begin, end);
+                at = w.g;
+            }
             w.tok0 = begin;
             w.toks = end - begin;
-            w.kb0 = 0;
             w.kb1 = (w.toks + 63) >> 6;
-            w.ks = 0;
-            w.tile = u;
-            return w;
+            place(p, tile - w.g * per, 0, p.rows, w);
+            return;
         }
-        int r = u, nts = p.num_n_tiles;
-        w.g = 0;
         if (p.offsets) {
-            while (u >= cum[slot + 1])
-                ++slot;
-            if (slot != at) {
-                slot_range(p, slot, begin, end);
-                at = slot;
+            while (tile >= ctl->cum[group + 1])
+                ++group;
+            if (group != at) {
+                group_range(p.offsets, p.tokens, group, begin, end);
+                at = group;
             }
-            r = u - cum[slot];
-            nts = (end - begin + BN - 1) / BN;
-            w.g = slot >= 1 && slot <= p.groups ? slot - 1 : -1;
+            w.g = group;
+            place(p, tile - ctl->cum[group], begin, end, w);
         } else {
-            end = p.cols;
+            w.g = 0;
+            place(p, tile, 0, p.tokens, w);
         }
-        const int t = r / p.k_splits;
-        w.ks = r - t * p.k_splits;
-        w.tile = u / p.k_splits;
-        int nt;
-        tile(p, t, nts, w.mt, nt);
-        w.col0 = begin + nt * BN;
-        w.col_end = end;
-        w.kb0 = w.g < 0 ? 0 : w.ks * p.kb_per_split;
-        w.kb1 = w.g < 0 ? 0 : min(w.kb0 + p.kb_per_split, p.num_k_blocks);
-        return w;
     }
 
-    // Tile t of a num_m_tiles x nts grid, group_m tile rows walked together.
-    static __device__ __forceinline__ void tile(const LmArgs &p, int t, int nts, int &mt, int &nt)
+    // Tile t of the grid whose ragged side is the tokens b .. e - 1; group_m tile rows are
+    // walked together.
+    static __device__ __forceinline__ void place(const LmArgs &p, int t, int b, int e, LmUnit &w)
     {
-        const int span = p.group_m * nts;
+        const int rts = WIDE && !RK ? (e - b + 255) >> 8 : p.num_row_tiles;
+        const int cts = WIDE ? p.num_col_tiles : (e - b + BN - 1) / BN;
+        const int span = p.group_m * cts;
         const int first = t / span * p.group_m;
-        const int gsize = min(p.num_m_tiles - first, p.group_m);
+        const int gsize = min(rts - first, p.group_m);
         const int in = t % span;
-        mt = first + in % gsize;
-        nt = in / gsize;
+        const int rt = first + in % gsize, ct = in / gsize;
+        if constexpr (WIDE) {
+            w.row0 = b + rt * 256;
+            w.row_end = e;
+            w.col0 = ct * BN;
+            w.col_end = p.cols;
+        } else {
+            w.row0 = rt * 256;
+            w.row_end = p.rows;
+            w.col0 = b + ct * BN;
+            w.col_end = e;
+        }
     }
 };
 
-template <bool RK>
-__device__ __forceinline__ int lm_total_units(const LmArgs &p, const int *cum)
+// Tiles of a range of tokens.
+template <bool WIDE, int BN>
+__device__ __forceinline__ int tiles_of_range(const LmArgs &p, int b, int e)
 {
-    if constexpr (RK)
-        return p.groups * p.num_m_tiles * p.num_n_tiles;
-    return p.offsets ? cum[p.groups + 2] : p.num_m_tiles * p.num_n_tiles * p.k_splits;
+    return WIDE ? ((e - b + 255) >> 8) * p.num_col_tiles : (e - b + BN - 1) / BN * p.num_row_tiles;
+}
+
+// The call's plan, by one warp.
+template <bool WIDE, int BN, bool RK>
+__device__ __forceinline__ void make_plan(const LmArgs &p, LmCtl *ctl, int lane, int pairs)
+{
+    int tiles = 0;
+    int nulls[2] = {0, 0};
+    if (RK) {
+        tiles = p.groups * p.num_row_tiles * p.num_col_tiles;
+    } else if (!p.offsets) {
+        tiles = tiles_of_range<WIDE, BN>(p, 0, p.tokens);
+    } else {
+        if (lane == 0)
+            ctl->cum[0] = 0;
+        for (int g0 = 0; g0 < p.groups; g0 += 32) {
+            int n = 0;
+            if (g0 + lane < p.groups) {
+                int b, e;
+                group_range(p.offsets, p.tokens, g0 + lane, b, e);
+                n = tiles_of_range<WIDE, BN>(p, b, e);
+            }
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, n, d);
+                if (lane >= d)
+                    n += up;
+            }
+            if (g0 + lane < p.groups)
+                ctl->cum[g0 + lane + 1] = tiles + n;
+            tiles += __shfl_sync(0xffffffffu, n, 31);
+        }
+        for (int i = 0; i < 2; ++i) {
+            int b, e;
+            null_range(p, i, b, e);
+            nulls[i] = tiles_of_range<WIDE, BN>(p, b, e);
+        }
+    }
+    if (lane == 0) {
+        LmPlan pl;
+        pl.tiles = pl.whole = tiles;
+        pl.share = 1;
+        pl.null_tiles[0] = nulls[0];
+        pl.null_tiles[1] = nulls[1];
+        const int rest = tiles % pairs;
+        if (!RK && p.part && rest > 0) {
+            const int64_t work = static_cast<int64_t>(rest) * p.num_k_blocks;
+            const int share = max(static_cast<int>((work + pairs - 1) / pairs), p.min_share);
+            if (p.num_k_blocks - share >= p.split_gain) {
+                pl.whole = tiles - rest;
+                pl.share = share;
+            }
+        }
+        ctl->plan = pl;
+    }
 }
 
 // ------------------------------------------------------------------------- the epilogues
-// act(alpha v + bias) + beta C for one row and kCols columns from `col`, stored to D (and
-// the value before act to Z).  Columns at and past col_end are another group's.
-template <int OUT, int ACT, int kCols>
-__device__ __forceinline__ void finish_act(const LmArgs &p, const float (&z)[kCols], int row, int col,
-                                           int ncol, int64_t dbase)
+template <int N>
+__device__ __forceinline__ void apply_act(int act, float (&x)[N])
 {
-    float r[kCols];
+    auto all = [&](auto f) {
 #pragma unroll
-    for (int j = 0; j < kCols; ++j)
-        r[j] = act_fn<ACT>(z[j]);
-    if (p.C) {
-        const int64_t cbase = static_cast<int64_t>(col) * p.ldc + row;
-#pragma unroll
-        for (int j = 0; j < kCols; ++j)
-            if (j < ncol)
-                r[j] = fmaf(p.beta, load_as<OUT>(p.C, cbase + j * p.ldc), r[j]);
+        for (int j = 0; j < N; j += 2)
+            split2(f(f2(x[j], x[j + 1])), x[j], x[j + 1]);
+    };
+    switch (act) {
+    case kActRelu: all([](F2 v) { return act_fn<kActRelu>(v); }); break;
+    case kActGelu: all([](F2 v) { return act_fn<kActGelu>(v); }); break;
+    case kActGeluTanh: all([](F2 v) { return act_fn<kActGeluTanh>(v); }); break;
+    case kActSilu: all([](F2 v) { return act_fn<kActSilu>(v); }); break;
+    default: break;
     }
-#pragma unroll
-    for (int j = 0; j < kCols; ++j)
-        if (j < ncol)
-            store_as<OUT>(p.D, dbase + j * p.ldd, r[j]);
 }
 
+__device__ __forceinline__ uint32_t pack16(float a, float b, bool bf16)
+{
+    if (bf16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void unpack16(const uint4 &v, float (&x)[8])
+{
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (BF16) {
+            x[2 * k] = __uint_as_float(u[k] << 16);
+            x[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
+        } else {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u[k]));
+            x[2 * k] = f.x;
+            x[2 * k + 1] = f.y;
+        }
+    }
+}
+
+// Bias entries i .. i + 31 (the first n of them), the same for every lane.
+__device__ __forceinline__ void load_bias(const LmArgs &p, int64_t i, int n, float (&b)[32])
+{
+    const uint8_t *at = static_cast<const uint8_t *>(p.bias) + i * (p.bias_f32 ? 4 : 2);
+    if (n >= 32 && (reinterpret_cast<uintptr_t>(at) & 15u) == 0) {
+        const uint4 *q = reinterpret_cast<const uint4 *>(at);
+        if (p.bias_f32) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint4 v = q[j];
+                b[4 * j] = __uint_as_float(v.x);
+                b[4 * j + 1] = __uint_as_float(v.y);
+                b[4 * j + 2] = __uint_as_float(v.z);
+                b[4 * j + 3] = __uint_as_float(v.w);
+            }
+        } else if (p.in_bf16) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                unpack16<true>(q[j], *reinterpret_cast<float (*)[8]>(b + 8 * j));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                unpack16<false>(q[j], *reinterpret_cast<float (*)[8]>(b + 8 * j));
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            b[j] = j >= n ? 0.0f
+                 : p.bias_f32 ? static_cast<const float *>(p.bias)[i + j]
+                              : load16(p.bias, i + j, p.in_bf16);
+    }
+}
+
+// One feature (row) of kCols tokens from `col` on: each store of a warp is a 64- or 128-byte
+// run of one token's features.
 template <int OUT, int kCols>
-__device__ __forceinline__ void finish_linear(const LmArgs &p, float (&z)[kCols], const LmUnit &w,
+__device__ __forceinline__ void finish_narrow(const LmArgs &p, float (&z)[kCols], const LmUnit &w,
                                               int row, int col, float alpha, float bias)
 {
     const int ncol = w.col_end - col;
-    if (row >= p.m || ncol <= 0)
+    if (row >= p.rows || ncol <= 0)
         return;
-    const int64_t dbase = (p.ragged_k ? w.g * p.strideD : 0) + static_cast<int64_t>(col) * p.ldd + row;
-    if (w.g < 0) {                             // columns of no group
+    const int64_t dbase = static_cast<int64_t>(col) * p.ldd + row;
+    uint16_t *zp = static_cast<uint16_t *>(p.Z) + static_cast<int64_t>(col) * p.ldz + row;
+    if (w.g < 0) {                             // tokens of no group
 #pragma unroll
         for (int j = 0; j < kCols; ++j)
             if (j < ncol) {
                 store_as<OUT>(p.D, dbase + j * p.ldd, 0.0f);
                 if (p.Z)
-                    static_cast<uint16_t *>(p.Z)[(static_cast<int64_t>(col) + j) * p.ldz + row] = 0;
+                    zp[j * p.ldz] = 0;
             }
         return;
     }
@@ -293,29 +533,219 @@ __device__ __forceinline__ void finish_linear(const LmArgs &p, float (&z)[kCols]
     for (int j = 0; j < kCols; ++j)
         z[j] = fmaf(alpha, z[j], bias);
     if (p.Z) {
-        uint16_t *zp = static_cast<uint16_t *>(p.Z) + static_cast<int64_t>(col) * p.ldz + row;
 #pragma unroll
         for (int j = 0; j < kCols; ++j)
             if (j < ncol)
                 zp[j * p.ldz] = round16(z[j], p.in_bf16);
     }
-    switch (p.act) {
-    case kActRelu: finish_act<OUT, kActRelu>(p, z, row, col, ncol, dbase); break;
-    case kActGelu: finish_act<OUT, kActGelu>(p, z, row, col, ncol, dbase); break;
-    case kActGeluTanh: finish_act<OUT, kActGeluTanh>(p, z, row, col, ncol, dbase); break;
-    case kActSilu: finish_act<OUT, kActSilu>(p, z, row, col, ncol, dbase); break;
-    default: finish_act<OUT, kActNone>(p, z, row, col, ncol, dbase); break;
+    apply_act(p.act, z);
+    if (p.C) {
+        const int64_t cbase = static_cast<int64_t>(col) * p.ldc + row;
+#pragma unroll
+        for (int j = 0; j < kCols; ++j)
+            if (j < ncol)
+                z[j] = fmaf(p.beta, load_as<OUT>(p.C, cbase + j * p.ldc), z[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kCols; ++j)
+        if (j < ncol)
+            store_as<OUT>(p.D, dbase + j * p.ldd, z[j]);
+}
+
+// A warp's block of 32 rows (tokens) x 32 columns (features), a row per lane in registers,
+// goes to and from memory through the warp's staging area, so that memory is accessed in
+// runs of 64 (16-bit) or 128 bytes (FP32) of a row: a lane's own row would go in 16-byte
+// pieces of 32 different lines per instruction (16384 x 4096 x 4096 BF16: 335 us a call so,
+// 291 us through the staging area).  The 16-byte pieces of a row are permuted by row, so
+// that neither side has bank conflicts.
+template <int ES>
+__device__ __forceinline__ uint4 *stage_piece(uint8_t *stage, int row, int piece)
+{
+    constexpr int kPieces = 2 * ES;                   // 16-byte pieces of a row: 4 or 8
+    const int p = ES == 2 ? piece ^ ((row >> 1) & 3) : piece ^ (row & 7);
+    return reinterpret_cast<uint4 *>(stage) + row * kPieces + p;
+}
+
+template <int OUT>
+__device__ __forceinline__ void stage_put(uint8_t *stage, int lane, const float (&x)[32])
+{
+    if constexpr (OUT == kOutF32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            *stage_piece<4>(stage, lane, j) =
+                make_uint4(__float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]),
+                           __float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3]));
+    } else {
+        constexpr bool b = OUT == kOutBF16;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            *stage_piece<2>(stage, lane, j) =
+                make_uint4(pack16(x[8 * j], x[8 * j + 1], b), pack16(x[8 * j + 2], x[8 * j + 3], b),
+                           pack16(x[8 * j + 4], x[8 * j + 5], b), pack16(x[8 * j + 6], x[8 * j + 7], b));
     }
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
-// 2^x on the special-function unit, results below 2^-126 flushed to zero (they vanish
-// beside the row's largest term, 1)
-__device__ __forceinline__ float exp2_fast(float x)
+template <int OUT>
+__device__ __forceinline__ void stage_get(uint8_t *stage, int lane, float (&x)[32])
 {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+    if constexpr (OUT == kOutF32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint4 v = *stage_piece<4>(stage, lane, j);
+            x[4 * j] = __uint_as_float(v.x);
+            x[4 * j + 1] = __uint_as_float(v.y);
+            x[4 * j + 2] = __uint_as_float(v.z);
+            x[4 * j + 3] = __uint_as_float(v.w);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint4 v = *stage_piece<2>(stage, lane, j);
+            unpack16<OUT == kOutBF16>(v, *reinterpret_cast<float (*)[8]>(x + 8 * j));
+        }
+    }
+}
+
+// The staged block to memory: rows from row0 on up to row_end, the first ncol columns.
+template <int ES>
+__device__ __forceinline__ void stage_flush(uint8_t *stage, int lane, void *base, int64_t ld, int row0,
+                                            int row_end, int col, int ncol)
+{
+    constexpr int kPieces = 2 * ES, kRows = 32 / kPieces, kElems = 16 / ES;
+    const int piece = lane % kPieces, c = piece * kElems;
+    uint8_t *at = static_cast<uint8_t *>(base) +
+                  ((static_cast<int64_t>(row0) + lane / kPieces) * ld + col + c) * ES;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+        const int r = i * kRows + lane / kPieces;
+        if (row0 + r < row_end && c < ncol) {
+            const uint4 v = *stage_piece<ES>(stage, r, piece);
+            uint8_t *q = at + static_cast<int64_t>(i * kRows) * ld * ES;
+            if (c + kElems <= ncol) {
+                *reinterpret_cast<uint4 *>(q) = v;
+            } else {
+                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < kElems; ++j)
+                    if (c + j < ncol) {
+                        if constexpr (ES == 4)
+                            reinterpret_cast<uint32_t *>(q)[j] = u[j];
+                        else
+                            reinterpret_cast<uint16_t *>(q)[j] =
+                                static_cast<uint16_t>(u[j / 2] >> (16 * (j & 1)));
+                    }
+            }
+        }
+    }
+}
+
+// The same block from memory into registers (piece i of this lane's share), zeros outside.
+template <int ES>
+__device__ __forceinline__ void block_load(uint4 (&v)[2 * ES], int lane, const void *base, int64_t ld,
+                                           int row0, int row_end, int col, int ncol)
+{
+    constexpr int kPieces = 2 * ES, kRows = 32 / kPieces, kElems = 16 / ES;
+    const int piece = lane % kPieces, c = piece * kElems;
+    const uint8_t *at = static_cast<const uint8_t *>(base) +
+                        ((static_cast<int64_t>(row0) + lane / kPieces) * ld + col + c) * ES;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (row0 + i * kRows + lane / kPieces < row_end && c < ncol) {
+            const uint8_t *q = at + static_cast<int64_t>(i * kRows) * ld * ES;
+            if (c + kElems <= ncol) {
+                v[i] = *reinterpret_cast<const uint4 *>(q);
+            } else {
+                uint32_t u[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+                for (int j = 0; j < kElems; ++j)
+                    if (c + j < ncol) {
+                        if constexpr (ES == 4)
+                            u[j] = reinterpret_cast<const uint32_t *>(q)[j];
+                        else
+                            u[j / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(q)[j])
+                                        << (16 * (j & 1));
+                    }
+                v[i] = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+        }
+    }
+}
+
+// A warp's 32 tokens (from row0, this lane's values in z) x 32 features from `col` on; the
+// whole warp calls it.
+template <int OUT>
+__device__ __forceinline__ void finish_wide(const LmArgs &p, float (&z)[32], const LmUnit &w, int row0,
+                                            int col, float alpha, uint8_t *stage, int lane)
+{
+    constexpr int ES = OUT == kOutF32 ? 4 : 2;
+    const int ncol = w.col_end - col;
+    if (row0 >= w.row_end || ncol <= 0)
+        return;
+    if (w.g < 0) {                             // tokens of no group
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            z[j] = 0.0f;
+        stage_put<OUT>(stage, lane, z);
+        __syncwarp();
+        stage_flush<ES>(stage, lane, p.D, p.ldd, row0, w.row_end, col, ncol);
+        if (p.Z)
+            stage_flush<2>(stage, lane, p.Z, p.ldz, row0, w.row_end, col, ncol);
+        __syncwarp();
+        return;
+    }
+    uint4 c[2 * ES];
+    if (p.C)
+        block_load<ES>(c, lane, p.C, p.ldc, row0, w.row_end, col, ncol);
+    if (p.bias) {
+        float b[32];
+        load_bias(p, static_cast<int64_t>(w.g) * p.cols + col, ncol, b);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            z[j] = fmaf(alpha, z[j], b[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            z[j] *= alpha;
+    }
+    if (p.Z) {
+        if (p.in_bf16)
+            stage_put<kOutBF16>(stage, lane, z);
+        else
+            stage_put<kOutF16>(stage, lane, z);
+        __syncwarp();
+        stage_flush<2>(stage, lane, p.Z, p.ldz, row0, w.row_end, col, ncol);
+        __syncwarp();
+    }
+    apply_act(p.act, z);
+    if (p.C) {
+        constexpr int kPieces = 2 * ES, kRows = 32 / kPieces;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            *stage_piece<ES>(stage, i * kRows + lane / kPieces, lane % kPieces) = c[i];
+        __syncwarp();
+        float r[32];
+        stage_get<OUT>(stage, lane, r);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            z[j] = fmaf(p.beta, r[j], z[j]);
+        __syncwarp();
+    }
+    stage_put<OUT>(stage, lane, z);
+    __syncwarp();
+    uint8_t *d = static_cast<uint8_t *>(p.D) + (p.ragged_k ? w.g * p.strideD * ES : 0);
+    stage_flush<ES>(stage, lane, d, p.ldd, row0, w.row_end, col, ncol);
+    __syncwarp();
+}
+
+// Wait for this thread's TMEM loads; v is not to be touched before.
+template <int N>
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&v)[N])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        asm volatile("" : "+r"(v[i]));
 }
 
 // ---------------------------------------------------------------------------- the kernel
@@ -323,10 +753,19 @@ template <int EPI, int OUT, int BN, bool RK>
 __global__ void __launch_bounds__(kThreads, 1)
     tcg_lm_kernel(const __grid_constant__ LmMaps maps, const LmArgs p)
 {
-    using Cfg = LmCfg<BN>;
+    constexpr bool WIDE = EPI == kEpiWide || EPI == kEpiXentStats || EPI == kEpiXentGrad;
+    using Cfg = LmCfg<BN, WIDE>;
     constexpr int kStages = Cfg::kStages;
     constexpr int kAccBufs = Cfg::kAccBufs;
     constexpr int kBRows = Cfg::kBRows;
+    // The tensor core adds each product of 16 K elements to its FP32 accumulator with
+    // truncation, an error that grows with K and always toward zero (with K = 4096 and 1.5
+    // standard deviations of logits it moved the loss by 2e-6 of itself).  Where results
+    // are FP32 statistics, or the accumulators few, K goes in segments of 512: each starts a
+    // new accumulator, and the epilogue adds the segments in registers, rounding to nearest.
+    constexpr bool SEG = EPI != kEpiWide && EPI != kEpiXentGrad;
+    constexpr int kSegBlocks = SEG ? 8 : 1 << 30;
+    using Walk = LmWalk<WIDE, BN, RK>;
 
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
@@ -334,14 +773,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *base_ptr = smem_raw + (base - raw_u32);
     const uint32_t a_smem = base;
     const uint32_t b_smem = base + kStages * Cfg::kAStage;
-    LmCtl *ctl = reinterpret_cast<LmCtl *>(base_ptr + kDataBytes);
+    LmCtl *ctl = reinterpret_cast<LmCtl *>(base_ptr + kLmDataBytes);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
-    const int cluster_id = blockIdx.x / 2;
-    const int num_clusters = gridDim.x / 2;
+    const int pair = blockIdx.x / 2;
+    const int pairs = gridDim.x / 2;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -355,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&ctl->drain), 1);
         ctl->abort_flag = 0;
         fence_mbar_init();
-        if (RK ? p.cols > 0 : p.num_k_blocks > 0) {
+        if (RK ? p.tokens > 0 : p.num_k_blocks > 0) {
             tma_prefetch_map(&maps.A);
             tma_prefetch_map(&maps.B);
         }
@@ -368,35 +807,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0)
         griddep_launch_dependents();
     griddep_wait();
-    // Units before each slot of a grouped call, by one warp.
-    if (!RK && p.offsets && warp == 2) {
-        int sum = 0;
-        if (lane == 0)
-            ctl->cum[0] = 0;
-        for (int s0 = 0; s0 < p.groups + 2; s0 += 32) {
-            const int s = s0 + lane;
-            int units = 0;
-            if (s < p.groups + 2) {
-                int b, e;
-                slot_range(p, s, b, e);
-                units = (e - b + BN - 1) / BN * p.num_m_tiles * p.k_splits;
-            }
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int up = __shfl_up_sync(0xffffffffu, units, d);
-                if (lane >= d)
-                    units += up;
-            }
-            if (s < p.groups + 2)
-                ctl->cum[s + 1] = sum + units;
-            sum += __shfl_sync(0xffffffffu, units, 31);
-        }
-    }
+    if (warp == 2)
+        make_plan<WIDE, BN, RK>(p, ctl, lane, pairs);
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem_base = ctl->tmem_base;
-    const int total = lm_total_units<RK>(p, ctl->cum);
 
     constexpr uint32_t kKmma = 16;
     constexpr int kMmasPerStage = 4;
@@ -414,15 +830,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) {
         if (lane == 0) {
             // ------------------------------------------------------------ producer
-            LmWalk<BN, RK> walk;
+            Walk walk(pair, pairs);
+            LmUnit w;
             int stage = 0;
             uint32_t phase = 0;
             bool skip_once = p.fault_inject != 0 && leader;
             bool ok = true;
-            for (int u = cluster_id; ok && u < total; u += num_clusters) {
-                const LmUnit w = walk.unit(p, ctl->cum, u);
-                const int m0 = w.mt * 2 * kBM + static_cast<int>(rank) * kBM;
+            while (ok && walk.next(p, ctl, w)) {
+                const int m0 = w.row0 + static_cast<int>(rank) * kBM;
                 const int n0 = w.col0 + static_cast<int>(rank) * kBRows;
+                const int za = WIDE ? 0 : w.g, zb = WIDE && !RK ? w.g : 0;
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
                     const uint32_t fb_local = smem_u32(&ctl->full[stage]);
                     const uint32_t fb = mapa_shared(fb_local, 0);
@@ -460,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             // 128-byte rows of the stage.
                             auto tail = [&](uint32_t dst, const CUtensorMap *map, int rows, int row0) {
                                 for (int h = 0; h < rows / 64; ++h) {
-                                    uint32_t d = dst + h * kChunkBytes;
+                                    const uint32_t d = dst + h * kChunkBytes;
                                     auto run = [&](int tok, int step, int count, int from) {
                                         // `count` tokens from stage row `from` on
                                         int at = from;
@@ -475,14 +892,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                         }
                                     };
                                     run(k0, 1, left, 0);
-                                    run(p.cols, 0, kKRow - left, left);
+                                    run(p.tokens, 0, kKRow - left, left);
                                 }
                             };
                             tail(sa, maps.A_tail, kBM, m0);
                             tail(sb, maps.B_tail, kBRows, n0);
                         } else {
-                            load(sa, &maps.A, p.a_mode, kBM, m0, RK ? 0 : w.g);
-                            load(sb, &maps.B, p.b_mode, kBRows, n0, 0);
+                            load(sa, &maps.A, p.a_mode, kBM, m0, za);
+                            load(sb, &maps.B, p.b_mode, kBRows, n0, zb);
                         }
                     }
                     if (++stage == kStages) {
@@ -500,43 +917,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             layout(p.b_mode, b_lbo, b_sbo, b_off);
             const uint64_t a_desc0 = smem_desc_sw128(a_smem, a_lbo, a_sbo);
             const uint64_t b_desc0 = smem_desc_sw128(b_smem, b_lbo, b_sbo);
-            LmWalk<BN, RK> walk;
+            Walk walk(pair, pairs);
+            LmUnit w;
             int stage = 0;
             uint32_t phase = 0;
             int it = 0;
             bool ok = true;
-            for (int u = cluster_id; ok && u < total; u += num_clusters, ++it) {
-                const LmUnit w = walk.unit(p, ctl->cum, u);
-                const int acc = it % kAccBufs;
-                const uint32_t acc_phase = (it / kAccBufs) & 1;
-                if (!wait_bounded<2>(smem_u32(&ctl->acc_empty[acc]), acc_phase ^ 1u, ctl, p,
-                                     kErrMmaAcc)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
-                for (int kb = w.kb0; kb < w.kb1; ++kb) {
-                    if (!wait_bounded<2>(smem_u32(&ctl->full[stage]), phase, ctl, p, kErrMmaFull)) {
+            while (ok && walk.next(p, ctl, w)) {
+                int kb = w.kb0;
+                do {                                       // one accumulator per segment
+                    const int acc = it % kAccBufs;
+                    const uint32_t acc_phase = (it / kAccBufs) & 1;
+                    ++it;
+                    if (!wait_bounded<2>(smem_u32(&ctl->acc_empty[acc]), acc_phase ^ 1u, ctl, p,
+                                         kErrMmaAcc)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t ad_s = a_desc0 + ((static_cast<uint32_t>(stage) * Cfg::kAStage) >> 4);
-                    const uint64_t bd_s = b_desc0 + ((static_cast<uint32_t>(stage) * Cfg::kBStage) >> 4);
+                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+                    const int first = kb, stop = SEG ? min(kb + kSegBlocks, w.kb1) : w.kb1;
+                    for (; kb < stop; ++kb) {
+                        if (!wait_bounded<2>(smem_u32(&ctl->full[stage]), phase, ctl, p, kErrMmaFull)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t ad_s = a_desc0 + ((static_cast<uint32_t>(stage) * Cfg::kAStage) >> 4);
+                        const uint64_t bd_s = b_desc0 + ((static_cast<uint32_t>(stage) * Cfg::kBStage) >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < kMmasPerStage; ++kk)
-                        mma_f16_pair(d_tmem, ad_s + a_off[kk], bd_s + b_off[kk], p.idesc,
-                                     (kb > w.kb0 || kk > 0) ? 1u : 0u);
-                    mma_commit_pair_mc(smem_u32(&ctl->empty[stage]), 0x3);
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1u;
+                        for (int kk = 0; kk < kMmasPerStage; ++kk)
+                            mma_f16_pair(d_tmem, ad_s + a_off[kk], bd_s + b_off[kk], p.idesc,
+                                         (kb > first || kk > 0) ? 1u : 0u);
+                        mma_commit_pair_mc(smem_u32(&ctl->empty[stage]), 0x3);
+                        if (++stage == kStages) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
-                }
-                if (!ok)
-                    break;
-                mma_commit_pair_mc(smem_u32(&ctl->acc_full[acc]), 0x3);
+                    if (!ok)
+                        break;
+                    mma_commit_pair_mc(smem_u32(&ctl->acc_full[acc]), 0x3);
+                } while (kb < w.kb1);
             }
             mma_commit_pair(smem_u32(&ctl->drain));
             wait_bounded<2>(smem_u32(&ctl->drain), 0, ctl, p, kErrDrain, false);
@@ -546,193 +968,316 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Two halves of 4 warps; half h owns columns [h BN/2, (h + 1) BN/2) of each tile
         // for the CTA's 128 rows (warp w reads TMEM lane quarter w % 4).
         constexpr int kHalf = BN / 2;
-        constexpr int kCols = kHalf < 32 ? kHalf : 32;
-        constexpr int kChunks = kHalf / kCols;
         const int q = warp & 3;
         const int half = (warp - 2) >> 2;
         const bool half_leader = (warp == 2 + 4 * half) && lane == 0;
         const uint32_t bar_id = 1u + static_cast<uint32_t>(half);
-        const uint32_t lane_off = static_cast<uint32_t>(q * 32) << 16;
         const int rl = q * 32 + lane;
+        const uint32_t tmem_half = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                   static_cast<uint32_t>(half * kHalf);
         const float alpha = p.alpha * (p.alpha_dev ? *p.alpha_dev : 1.0f);
-        LmWalk<BN, RK> walk;
+        uint8_t *stage = base_ptr + kLmDataBytes - kEpiWarps * kLmStageBytes + (warp - 2) * kLmStageBytes;
+        Walk walk(pair, pairs);
+        LmUnit w{};
         int it = 0;
-        for (int u = cluster_id; u < total; u += num_clusters, ++it) {
+
+        // The next accumulator, once it is complete; false: stop.
+        auto acquire = [&]() {
             const int acc = it % kAccBufs;
-            const uint32_t acc_phase = (it / kAccBufs) & 1;
-            const LmUnit w = walk.unit(p, ctl->cum, u);
-            const int row = w.mt * 2 * kBM + static_cast<int>(rank) * kBM + rl;
-            const bool row_ok = row < p.m;
-            // Row data of the tile, loaded while the accumulator fills.
-            float bias = 0.0f;
-            float row_lse2 = 0.0f, row_g = 0.0f;
-            int target = -1;                               // column of the row's target
-            if constexpr (EPI == kEpiLinear) {
-                if (p.bias && row_ok && w.g >= 0) {
-                    const int64_t i = static_cast<int64_t>(w.g) * p.m + row;
+            const bool ok = wait_bounded<2>(smem_u32(&ctl->acc_full[acc]), (it / kAccBufs) & 1, ctl, p,
+                                            kErrEpilogue);
+            const bool stop = named_barrier_or(bar_id, 128, !ok || ctl->abort_flag);
+            tc_fence_after();
+            return !stop;
+        };
+        // This warp has read the accumulator: report to the MMA CTA, go on to the next.
+        auto release = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&ctl->acc_empty[it % kAccBufs]), 0));
+            ++it;
+        };
+        // A cut tile's piece is stored: whoever stores the last one of a tile half adds them
+        // all, in K order whatever the timing, and finishes the tile.
+        auto arrive = [&]() {
+            __threadfence();
+            named_barrier_sync(bar_id, 128);
+            if (half_leader) {
+                uint32_t *cnt = p.cnt + (w.counter * 2 + static_cast<int>(rank)) * 2 + half;
+                const bool last = atomicAdd(cnt, 1u) == static_cast<uint32_t>(w.pieces - 1);
+                if (last)
+                    *cnt = 0u;                             // every piece has arrived
+                ctl->last_arrival[half] = last;
+                __threadfence();
+            }
+            named_barrier_sync(bar_id, 128);
+            const bool last = ctl->last_arrival[half] != 0;
+            named_barrier_sync(bar_id, 128);               // the flag is free again
+            if (last)
+                __threadfence();
+            return last;
+        };
+        auto slot_ptr = [&](int slot) {
+            return p.part + ((static_cast<int64_t>(slot) * 2 + rank) * 2 + half) * (kHalf * kBM);
+        };
+        auto piece_slot = [&](int i) { return 2 * (w.first_pair + i) + (i == 0 ? 1 : 0); };
+
+        while (walk.next(p, ctl, w)) {
+            const int row = w.row0 + static_cast<int>(rank) * kBM + rl;
+            const int col_half = w.col0 + half * kHalf;
+            const bool cut = w.slot >= 0;
+            const bool empty_k = w.kb0 >= w.kb1;
+            const int segments = SEG ? (w.kb1 - w.kb0 + kSegBlocks - 1) / kSegBlocks : 1;
+            if constexpr (EPI == kEpiNarrow || EPI == kEpiXentNarrow) {
+                // ------------------------------------------------ tokens on the columns
+                constexpr int kCols = kHalf < 32 ? kHalf : 32;
+                float sum[kHalf];
+#pragma unroll
+                for (int j = 0; j < kHalf; ++j)
+                    sum[j] = 0.0f;
+                float bias = 0.0f;
+                if (EPI == kEpiNarrow && p.bias && row < p.rows && w.g >= 0) {
+                    const int64_t i = static_cast<int64_t>(w.g) * p.rows + row;
                     bias = p.bias_f32 ? static_cast<const float *>(p.bias)[i]
                                       : load16(p.bias, i, p.in_bf16);
                 }
-            } else if (row_ok) {
-                const int64_t t = p.targets[row];
-                const bool counts = t != p.ignore && t >= 0 && t < p.vocab;
-                if (counts && t >= p.col0 && t - p.col0 < p.cols)
-                    target = static_cast<int>(t - p.col0);
-                if constexpr (EPI == kEpiXentGrad) {
-                    row_lse2 = p.lse[row] * kLog2e;
-                    row_g = counts ? p.dloss[row] * (p.gscale ? *p.gscale : 1.0f) : 0.0f;
-                }
-            }
-            const bool ok = wait_bounded<2>(smem_u32(&ctl->acc_full[acc]), acc_phase, ctl, p,
-                                            kErrEpilogue);
-            if (named_barrier_or(bar_id, 128, !ok || ctl->abort_flag))
-                break;
-            tc_fence_after();
-            const bool empty_k = w.kb0 >= w.kb1;
-            const int col_half = w.col0 + half * kHalf;
-            const bool split = EPI == kEpiLinear && !RK && p.k_splits > 1 && w.g >= 0;
-            float *slices = nullptr;
-            if (split)
-                slices = p.part + ((static_cast<int64_t>(w.tile) * 2 + rank) * 2 + half) *
-                                      p.k_splits * (kHalf * kBM) + rl;
-            float smax = -INFINITY, ssum = 0.0f;
-#pragma unroll 1
-            for (int c = 0; c < kChunks; ++c) {
-                __syncwarp();
-                const uint32_t taddr = tmem_base + lane_off +
-                                       static_cast<uint32_t>(acc * BN + half * kHalf + c * kCols);
-                uint32_t v[kCols];
-                if constexpr (kCols == 16)
-                    tmem_ld_32x32b_x16(taddr, v);
-                else
-                    tmem_ld_32x32b_x32(taddr, v);
-                tmem_ld_wait();
-                if (c == kChunks - 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive_cluster(mapa_shared(smem_u32(&ctl->acc_empty[acc]), 0));
-                }
-                const int col = col_half + c * kCols;
-                const int ncol = w.col_end - col;
-                float x[kCols];
-#pragma unroll
-                for (int j = 0; j < kCols; ++j)
-                    x[j] = empty_k ? 0.0f : __uint_as_float(v[j]);
-                if constexpr (EPI == kEpiLinear) {
-                    if (split) {
-                        float *sl = slices + (static_cast<int64_t>(w.ks) * kHalf + c * kCols) * kBM;
-#pragma unroll
-                        for (int j = 0; j < kCols; ++j)
-                            if (j < ncol)
-                                __stcg(sl + j * kBM, x[j]);
+                bool stop = false;
+                int seg = 0;
+                do {
+                    if (!acquire()) {
+                        stop = true;
+                        break;
+                    }
+                    uint32_t v[kHalf];
+                    const uint32_t taddr = tmem_half + static_cast<uint32_t>(it % kAccBufs * BN);
+                    if constexpr (kHalf == 16) {
+                        tmem_ld_32x32b_x16(taddr, v);
                     } else {
-                        finish_linear<OUT>(p, x, w, row, col, alpha, bias);
-                    }
-                } else if constexpr (EPI == kEpiXentStats) {
-                    if (ncol <= 0)
-                        continue;
-                    if (ncol < kCols) {
 #pragma unroll
-                        for (int j = 0; j < kCols; ++j)
-                            if (j >= ncol)
-                                x[j] = -INFINITY;
+                        for (int c = 0; c < kHalf; c += 32)
+                            tmem_ld_32x32b_x32(taddr + c, *reinterpret_cast<uint32_t (*)[32]>(v + c));
                     }
-                    if (target >= col && target < col + kCols) {
+                    tmem_ld_done(v);
+                    release();
+                    if (!empty_k) {
+#pragma unroll
+                        for (int j = 0; j < kHalf; ++j)
+                            sum[j] += __uint_as_float(v[j]);
+                    }
+                } while (++seg < segments);
+                if (stop)
+                    break;
+                const int ncol = w.col_end - col_half;
+                if (cut) {
+                    float *sl = slot_ptr(w.slot) + rl;     // [column][row]
+#pragma unroll
+                    for (int j = 0; j < kHalf; ++j)
+                        if (j < ncol)
+                            __stcg(sl + j * kBM, sum[j]);
+                    if (!arrive())
+                        continue;
+#pragma unroll
+                    for (int j = 0; j < kHalf; ++j)
+                        sum[j] = 0.0f;
+#pragma unroll 4
+                    for (int i = 0; i < w.pieces; ++i) {
+                        const float *s = slot_ptr(piece_slot(i)) + rl;
+#pragma unroll
+                        for (int j = 0; j < kHalf; ++j)
+                            if (j < ncol)
+                                sum[j] += __ldcg(s + j * kBM);
+                    }
+                }
+                if constexpr (EPI == kEpiNarrow) {
+#pragma unroll
+                    for (int c = 0; c < kHalf; c += kCols)
+                        finish_narrow<OUT>(p, *reinterpret_cast<float (*)[kCols]>(sum + c), w, row,
+                                           col_half + c, alpha, bias);
+                } else {
+                    // a warp's 32 vocabulary entries, one token (column) after the other
+                    const int slot = (w.row0 >> 8) * 8 + static_cast<int>(rank) * 4 + q;
+#pragma unroll
+                    for (int j = 0; j < kHalf; ++j) {
+                        if (j >= ncol)
+                            break;
+                        const int tok = col_half + j;
+                        const int64_t t = p.targets[tok];
+                        const float v = row < p.rows ? sum[j] : -INFINITY;
+                        if (t == row && t != p.ignore && row < p.rows)
+                            p.target_logit[tok] = v;
+                        float mx = v;
+#pragma unroll
+                        for (int d = 16; d; d >>= 1)
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                        const float sub = mx == -INFINITY ? 0.0f : mx * kLog2e;
+                        float s = exp2_fast(fmaf(v, kLog2e, -sub));
+#pragma unroll
+                        for (int d = 16; d; d >>= 1)
+                            s += __shfl_xor_sync(0xffffffffu, s, d);
+                        if (lane == 0)
+                            p.stats[static_cast<int64_t>(slot) * p.tokens + tok] = make_float2(mx, s);
+                    }
+                }
+            } else if constexpr (EPI == kEpiWide) {
+                // --------------------------------------------------- tokens on the rows
+                constexpr int kChunks = kHalf / 32;
+                if (!acquire())
+                    break;
+                const uint32_t taddr = tmem_half + static_cast<uint32_t>(it % kAccBufs * BN);
+                float *sl = cut ? slot_ptr(w.slot) + rl : nullptr;       // [column][row]
+                auto chunk = [&](uint32_t (&v)[32], int c) {
+                    float x[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        x[j] = empty_k ? 0.0f : __uint_as_float(v[j]);
+                    if (cut) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            __stcg(sl + (c * 32 + j) * kBM, x[j]);
+                    } else {
+                        finish_wide<OUT>(p, x, w, row - lane, col_half + c * 32, alpha, stage, lane);
+                    }
+                };
+#pragma unroll 1
+                for (int c = 0; c < kChunks; ++c) {
+                    __syncwarp();
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(taddr + 32 * c, v);
+                    tmem_ld_done(v);
+                    if (c == kChunks - 1)
+                        release();
+                    chunk(v, c);
+                }
+                if (cut && arrive()) {
+#pragma unroll 1
+                    for (int c = 0; c < kChunks; ++c) {
+                        if (col_half + c * 32 >= w.col_end)
+                            break;
+                        float x[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            x[j] = 0.0f;
+                        for (int i = 0; i < w.pieces; ++i) {
+                            const float *q = slot_ptr(piece_slot(i)) + c * 32 * kBM + rl;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                x[j] += __ldcg(q + j * kBM);
+                        }
+                        finish_wide<OUT>(p, x, w, row - lane, col_half + c * 32, alpha, stage, lane);
+                    }
+                }
+            } else {
+                // ------------------------------------ cross entropy, tokens on the rows
+                const bool row_ok = row < p.rows;
+                float row_lse2 = 0.0f, row_g = 0.0f;
+                int target = -1;                           // column of the row's target
+                if (row_ok) {
+                    const int64_t t = p.targets[row];
+                    const bool counts = t != p.ignore && t >= 0 && t < p.vocab;
+                    if (counts && t >= p.col0 && t - p.col0 < p.cols)
+                        target = static_cast<int>(t - p.col0);
+                    if constexpr (EPI == kEpiXentGrad) {
+                        row_lse2 = p.lse[row] * kLog2e;
+                        row_g = counts ? p.dloss[row] * (p.gscale ? *p.gscale : 1.0f) : 0.0f;
+                    }
+                }
+                if constexpr (EPI == kEpiXentStats) {
+                    float sum[kHalf];
+#pragma unroll
+                    for (int j = 0; j < kHalf; ++j)
+                        sum[j] = 0.0f;
+                    bool stop = false;
+                    for (int seg = 0; seg < segments; ++seg) {
+                        if (!acquire()) {
+                            stop = true;
+                            break;
+                        }
+                        const uint32_t taddr = tmem_half + static_cast<uint32_t>(it % kAccBufs * BN);
+                        uint32_t va[16], vb[16];
+                        tmem_ld_32x32b_x16(taddr, va);
+#pragma unroll
+                        for (int c = 0; c < kHalf; c += 32) {
+                            tmem_ld_done(va);
+                            tmem_ld_32x32b_x16(taddr + c + 16, vb);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                sum[c + j] += __uint_as_float(va[j]);
+                            tmem_ld_done(vb);
+                            if (c + 32 < kHalf)
+                                tmem_ld_32x32b_x16(taddr + c + 32, va);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                sum[c + 16 + j] += __uint_as_float(vb[j]);
+                        }
+                        release();
+                    }
+                    if (stop)
+                        break;
+                    const int ncol = w.col_end - col_half;
+                    if (ncol < kHalf) {
+#pragma unroll
+                        for (int j = 0; j < kHalf; ++j)
+                            if (j >= ncol)
+                                sum[j] = -INFINITY;
+                    }
+                    if (target >= col_half && target < col_half + kHalf) {
                         float tl = 0.0f;
 #pragma unroll
-                        for (int j = 0; j < kCols; ++j)
-                            if (target - col == j)
-                                tl = x[j];
+                        for (int j = 0; j < kHalf; ++j)    // by predicate: the sums stay in registers
+                            asm("{\n\t.reg .pred q;\n\tsetp.eq.s32 q, %1, %2;\n\t"
+                                "@q mov.f32 %0, %3;\n\t}"
+                                : "+f"(tl)
+                                : "r"(target - col_half), "r"(j), "f"(sum[j]));
                         p.target_logit[row] = tl;
                     }
-                    float mx = smax;
+                    float mx = -INFINITY;
 #pragma unroll
-                    for (int j = 0; j < kCols; ++j)
-                        mx = fmaxf(mx, x[j]);
-                    // a maximum of -inf (nothing but -inf so far) subtracts as zero
+                    for (int j = 0; j < kHalf; ++j)
+                        mx = fmaxf(mx, sum[j]);
+                    // a maximum of -inf (nothing but -inf) subtracts as zero
                     const float sub = mx == -INFINITY ? 0.0f : mx * kLog2e;
-                    float add = 0.0f;
+                    float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int j = 0; j < kCols; ++j)
-                        add += exp2_fast(fmaf(x[j], kLog2e, -sub));
-                    ssum = ssum * exp2_fast(fmaf(smax, kLog2e, -sub)) + add;
-                    smax = mx;
+                    for (int j = 0; j < kHalf; ++j)
+                        add[j & 3] += exp2_fast(fmaf(sum[j], kLog2e, -sub));
+                    if (row_ok)
+                        p.stats[static_cast<int64_t>(w.col0 / BN * 2 + half) * p.tokens + row] =
+                            make_float2(mx, (add[0] + add[1]) + (add[2] + add[3]));
                 } else {
-                    if (ncol <= 0 || !row_ok)
-                        continue;
-                    uint32_t packed[kCols / 2];
+                    if (!acquire())
+                        break;
+                    const uint32_t taddr = tmem_half + static_cast<uint32_t>(it % kAccBufs * BN);
+                    auto chunk = [&](uint32_t (&v)[32], int c) {
+                        const int col = col_half + c * 32;
+                        float g[32];
 #pragma unroll
-                    for (int j = 0; j < kCols; j += 2) {
-                        float g[2];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float pr = exp2_fast(fmaf(x[j + i], kLog2e, -row_lse2));
-                            g[i] = row_g == 0.0f ? 0.0f
-                                                 : row_g * (target == col + j + i ? pr - 1.0f : pr);
+                        for (int j = 0; j < 32; ++j) {
+                            const float pr = exp2_fast(fmaf(__uint_as_float(v[j]), kLog2e, -row_lse2));
+                            g[j] = row_g == 0.0f ? 0.0f : row_g * (target == col + j ? pr - 1.0f : pr);
                         }
-                        packed[j / 2] = static_cast<uint32_t>(round16(g[0], p.in_bf16)) |
-                                        static_cast<uint32_t>(round16(g[1], p.in_bf16)) << 16;
-                    }
-                    uint16_t *gp = static_cast<uint16_t *>(p.D) + static_cast<int64_t>(row) * p.ldd + col;
-                    if (ncol >= kCols) {
-#pragma unroll
-                        for (int j = 0; j < kCols / 8; ++j)
-                            *reinterpret_cast<uint4 *>(gp + 8 * j) =
-                                make_uint4(packed[4 * j], packed[4 * j + 1], packed[4 * j + 2],
-                                           packed[4 * j + 3]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < kCols; ++j)
-                            if (j < ncol)
-                                gp[j] = static_cast<uint16_t>(packed[j / 2] >> (16 * (j & 1)));
-                    }
-                }
-            }
-            if constexpr (EPI == kEpiXentStats) {
-                if (row_ok)
-                    p.stats[static_cast<int64_t>(w.col0 / BN * 2 + half) * p.m + row] =
-                        make_float2(smax, ssum);
-            }
-            if constexpr (EPI == kEpiLinear) {
-                if (split) {
-                    // Whoever stores the last of a tile half's partial sums adds them, in
-                    // range order, and finishes the tile: the order never depends on timing.
-                    __threadfence();
-                    named_barrier_sync(bar_id, 128);
-                    if (half_leader) {
-                        uint32_t *cnt = p.cnt + (w.tile * 2 + static_cast<int>(rank)) * 2 + half;
-                        const bool last = atomicAdd(cnt, 1u) == static_cast<uint32_t>(p.k_splits - 1);
-                        if (last)
-                            *cnt = 0u;                     // every range has arrived
-                        ctl->last_arrival[half] = last;
-                        __threadfence();
-                    }
-                    named_barrier_sync(bar_id, 128);
-                    if (ctl->last_arrival[half]) {
-                        __threadfence();
+                        if (col < w.col_end) {
+                            if (p.in_bf16)
+                                stage_put<kOutBF16>(stage, lane, g);
+                            else
+                                stage_put<kOutF16>(stage, lane, g);
+                            __syncwarp();
+                            stage_flush<2>(stage, lane, p.D, p.ldd, row - lane, w.row_end, col,
+                                           w.col_end - col);
+                            __syncwarp();
+                        }
+                    };
+                    constexpr int kChunks = kHalf / 32;
 #pragma unroll 1
-                        for (int c = 0; c < kChunks; ++c) {
-                            const int col = col_half + c * kCols;
-                            const int ncol = w.col_end - col;
-                            if (ncol <= 0)
-                                break;
-                            float x[kCols];
-#pragma unroll
-                            for (int j = 0; j < kCols; ++j)
-                                x[j] = 0.0f;
-                            for (int s = 0; s < p.k_splits; ++s) {
-                                const float *sl = slices +
-                                    (static_cast<int64_t>(s) * kHalf + c * kCols) * kBM;
-#pragma unroll
-                                for (int j = 0; j < kCols; ++j)
-                                    if (j < ncol)
-                                        x[j] += __ldcg(sl + j * kBM);
-                            }
-                            finish_linear<OUT>(p, x, w, row, col, alpha, bias);
-                        }
+                    for (int c = 0; c < kChunks; ++c) {
+                        __syncwarp();
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(taddr + 32 * c, v);
+                        tmem_ld_done(v);
+                        if (c == kChunks - 1)
+                            release();
+                        chunk(v, c);
                     }
-                    named_barrier_sync(bar_id, 128);       // last_arrival is free again
                 }
             }
         }
@@ -762,26 +1307,29 @@ __global__ void __launch_bounds__(kThreads, 1)
 typedef void (*LmKernelFn)(const LmMaps, const LmArgs);
 
 template <int OUT>
-LmKernelFn linear_fn(int bn, bool rk)
+LmKernelFn linear_fn(int epi, int bn, bool rk)
 {
     if (rk)
-        return tcg_lm_kernel<kEpiLinear, OUT, 256, true>;
-    switch (bn) {
-    case 32: return tcg_lm_kernel<kEpiLinear, OUT, 32, false>;
-    case 64: return tcg_lm_kernel<kEpiLinear, OUT, 64, false>;
-    case 128: return tcg_lm_kernel<kEpiLinear, OUT, 128, false>;
-    default: return tcg_lm_kernel<kEpiLinear, OUT, 256, false>;
-    }
+        return tcg_lm_kernel<kEpiWide, OUT, 256, true>;
+    if (epi == kEpiNarrow)
+        return bn == 32 ? tcg_lm_kernel<kEpiNarrow, OUT, 32, false>
+             : bn == 64 ? tcg_lm_kernel<kEpiNarrow, OUT, 64, false>
+                        : tcg_lm_kernel<kEpiNarrow, OUT, 128, false>;
+    return bn == 64 ? tcg_lm_kernel<kEpiWide, OUT, 64, false>
+         : bn == 128 ? tcg_lm_kernel<kEpiWide, OUT, 128, false>
+                     : tcg_lm_kernel<kEpiWide, OUT, 256, false>;
 }
 
 LmKernelFn lm_fn(int epi, int out_kind, int bn, bool rk)
 {
     if (epi == kEpiXentStats)
         return tcg_lm_kernel<kEpiXentStats, kOutF32, 256, false>;
+    if (epi == kEpiXentNarrow)
+        return tcg_lm_kernel<kEpiXentNarrow, kOutF32, 32, false>;
     if (epi == kEpiXentGrad)
         return tcg_lm_kernel<kEpiXentGrad, kOutF16, 256, false>;
-    return out_kind == kOutF32 ? linear_fn<kOutF32>(bn, rk)
-         : out_kind == kOutF16 ? linear_fn<kOutF16>(bn, rk) : linear_fn<kOutBF16>(bn, rk);
+    return out_kind == kOutF32 ? linear_fn<kOutF32>(epi, bn, rk)
+         : out_kind == kOutF16 ? linear_fn<kOutF16>(epi, bn, rk) : linear_fn<kOutBF16>(epi, bn, rk);
 }
 
 // ------------------------------------------------------------------- smaller kernels
@@ -904,10 +1452,6 @@ __global__ void __launch_bounds__(256)
     __shared__ float join[8][256 + 8];
     griddep_launch_dependents();
     griddep_wait();
-    LmArgs p;
-    p.offsets = offsets;
-    p.cols = cols;
-    p.groups = groups;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int row = blockIdx.x * 256 + lane * 8;
     const int left = m - row;                         // rows of this thread (8, or fewer at the end)
@@ -969,7 +1513,7 @@ __global__ void __launch_bounds__(256)
     }
     for (; at < c1 && g < groups; ++g) {
         int b, e;
-        group_range(p, g, b, e);
+        group_range(offsets, cols, g, b, e);
         b = max(b, at);
         e = min(e, c1);
         if (b >= c1)
@@ -988,8 +1532,8 @@ __global__ void __launch_bounds__(256)
                     float z[8];
                     load8(Z + static_cast<int64_t>(c) * ldz + row, z);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        d[i] *= act_slope<ACT>(z[i]);
+                    for (int i = 0; i < 8; i += 2)
+                        split2(f2(d[i], d[i + 1]) * act_slope<ACT>(f2(z[i], z[i + 1])), d[i], d[i + 1]);
                 }
                 if (dZ)
                     store8(dZ + static_cast<int64_t>(c) * lddz + row, d);
@@ -1027,14 +1571,10 @@ __global__ void __launch_bounds__(256)
     __shared__ float join[4][64];
     griddep_launch_dependents();
     griddep_wait();
-    LmArgs p;
-    p.offsets = offsets;
-    p.cols = cols;
-    p.groups = groups;
     const int g = blockIdx.y, lane = threadIdx.x & 63, q = threadIdx.x >> 6;
     const int row = blockIdx.x * 64 + lane;
     int b, e;
-    group_range(p, g, b, e);
+    group_range(offsets, cols, g, b, e);
     const int y0 = b / chunk, y1 = e > b ? (e - 1) / chunk + 1 : y0;
     const int a0 = y0 + (y1 - y0) * q / 4, a1 = y0 + (y1 - y0) * (q + 1) / 4;
     float s = 0.0f;

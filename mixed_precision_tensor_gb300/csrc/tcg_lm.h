@@ -13,35 +13,39 @@
 namespace tcg {
 
 constexpr int kLmMaxGroups = 384;      // experts of one grouped call (a table in shared memory)
-constexpr int kLmCounters = 4096;      // split counters of a handle
-constexpr int kLmMaxStages = 10;
-constexpr int kLmMaxSplits = 16;
+constexpr int kLmCounters = 1024;      // split counters of a handle: 4 per cut tile
+constexpr int kLmMaxStages = 12;
+// Shared memory: the operand ring, and (tokens on the rows) 4 KiB of staging per epilogue
+// warp, through which a warp's 32 rows leave and arrive in runs of 64 or 128 bytes.
+constexpr int kLmDataBytes = 224 * 1024;
+constexpr int kLmStageBytes = 4 * 1024;
 
-// What the epilogue of the product kernel does with an accumulator.
+// What the epilogue of the product kernel does with an accumulator (see tcg_lm.cu).
 enum LmEpi {
-    kEpiLinear = 0,    // act(alpha acc + bias) + beta C, optionally the pre-activation Z
-    kEpiXentStats = 1, // per-row maximum and sum of exponentials, and the target's logit
-    kEpiXentGrad = 2   // (exp(logit - lse) - [target]) * upstream gradient, 16-bit
+    kEpiNarrow = 0,     // act(alpha acc + bias) + beta C; features x tokens
+    kEpiWide = 1,       // the same; tokens x features
+    kEpiXentStats = 2,  // per-row maximum and sum of exponentials, and the target's logit
+    kEpiXentNarrow = 3, // the same; vocabulary x tokens
+    kEpiXentGrad = 4    // (exp(logit - lse) - [target]) * upstream gradient, 16-bit
 };
 
 enum LmAct { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
 
-// Column-major products over CTA pairs, 256 x BN tiles.  Three kinds of units:
-//   N ragged (ragged_k = 0): D = op(A_g) op(B), the columns of D (tokens) in `groups`
-//     ranges offsets[g] .. offsets[g + 1] - 1 of B's and D's columns, each with its own A_g;
-//     groups = 1 and offsets = nullptr: one product over all `cols` columns.
-//   K ragged (ragged_k = 1): D_g = A[:, range] B[:, range]^T, one m x n matrix per group,
-//     the K index (tokens) in the groups' ranges of the `cols` tokens.
+// An accumulator (rows x cols) = A (rows, K) times B (cols, K), in 256 x BN tiles.  One side
+// of it is the tokens: the columns in the narrow kinds, the rows in the wide ones, where D
+// and its companions are addressed as [token * ld + feature] either way.
+//   Dense or grouped: the tokens fall into `groups` ranges offsets[g] .. offsets[g + 1] - 1,
+//     each with its own matrix of the other operand; offsets = nullptr: one range of all.
+//   K ragged (wide only): one rows x cols matrix per group, summed over the group's tokens;
+//     D is addressed as [group * strideD + row * ldd + col].
 struct LmArgs {
-    int m;                     // rows of D
-    int cols;                  // N ragged: columns of D; K ragged: tokens
-    int n;                     // K ragged: columns of D
+    int rows, cols, tokens;
     int ragged_k;
     int groups;
     const int64_t *offsets;    // device, groups + 1 entries; nullptr: one group of everything
-    int num_m_tiles, num_n_tiles;   // num_n_tiles: of a dense call, or of each K-ragged matrix
-    int num_k_blocks;          // N ragged
-    int k_splits, kb_per_split;     // K ranges per tile (N ragged), joined by the last arrival
+    int num_row_tiles, num_col_tiles;   // of the sides that are not ragged
+    int num_k_blocks;          // 64 K elements each
+    int min_share, split_gain; // K splitting: fewest blocks per pair, least saving in blocks
     int group_m;
     int a_mode, b_mode;        // OperandMode
     uint32_t idesc;
@@ -51,7 +55,7 @@ struct LmArgs {
     const float *alpha_dev;    // multiplies alpha when not null
     void *D;
     int64_t ldd, strideD;      // strideD: between the matrices of a K-ragged call
-    const void *bias;          // m entries per group; nullptr: none
+    const void *bias;          // one entry per feature, per group; nullptr: none
     int bias_f32;
     const void *C;             // residual, type of D; nullptr: none
     int64_t ldc;
@@ -59,15 +63,15 @@ struct LmArgs {
     void *Z;                   // pre-activation, input type; nullptr: not kept
     int64_t ldz;
     int act;                   // LmAct
-    float *part;               // K-split partial sums
-    uint32_t *cnt;             // K-split arrival counters, zero before and after a call
+    float *part;               // partial sums of cut tiles; nullptr: never cut
+    uint32_t *cnt;             // their arrival counters, zero before and after a call
 
-    // cross entropy: rows are tokens (m), columns vocabulary entries (cols)
+    // cross entropy: the features are vocabulary entries
     const int64_t *targets;
     int64_t ignore;
     int64_t vocab;             // targets outside [0, vocab) do not count, like `ignore`
-    int col0;                  // vocabulary index of column 0 (gradient pieces)
-    float2 *stats;             // [2 n-tile + half][row]: maximum, sum
+    int col0;                  // vocabulary index of feature 0 (gradient pieces)
+    float2 *stats;             // [slot][token]: maximum, sum
     float *target_logit;
     const float *lse, *dloss;
     const float *gscale;       // power of two that dloss is multiplied by; nullptr: 1
@@ -77,21 +81,29 @@ struct LmArgs {
     int fault_inject;
 };
 
-template <int BN>
+template <int BN, bool WIDE>
 struct LmCfg {
+    static constexpr int kRingBytes = kLmDataBytes - (WIDE ? kEpiWarps * kLmStageBytes : 0);
     static constexpr int kBRows = BN / 2;                    // B rows per CTA of the pair
     static constexpr int kAStage = kABytes;                  // 16 KiB
     static constexpr int kBStage = kBRows * kRowBytes;
     static constexpr int kStageBytes = kAStage + kBStage;
-    static constexpr int kFit = kDataBytes / kStageBytes;
+    static constexpr int kFit = kRingBytes / kStageBytes;
+    // wide 256, 128, 64: 6, 8, 9; narrow 128, 64, 32: 9, 11, 12
     static constexpr int kStages = kFit < kLmMaxStages ? kFit : kLmMaxStages;
     static constexpr int kAccBufs = kTmemCols / BN < 4 ? kTmemCols / BN : 4;
 };
 
-// Number of elements of the split workspace: a slice of 128 x BN per (tile, CTA, range).
-inline size_t lm_part_bytes(int64_t tiles, int bn, int splits)
+// Bytes of the partial sums: two 256 x BN slots per pair.
+inline size_t lm_part_bytes(int pairs, int bn)
 {
-    return static_cast<size_t>(tiles) * 2 * kBM * bn * splits * sizeof(float);
+    return static_cast<size_t>(pairs) * 2 * 2 * kBM * bn * sizeof(float);
+}
+
+// Slots of the cross entropy's statistics: per 256 (wide) or 32 (narrow) vocabulary entries.
+inline int64_t lm_stat_slots(int64_t vocab, bool narrow)
+{
+    return narrow ? (vocab + 255) / 256 * 8 : (vocab + 255) / 256 * 2;
 }
 
 // K-ragged calls load the last tokens of a group with boxes of 16, 4 and 1 tokens, and
@@ -101,7 +113,8 @@ struct LmMaps {
     CUtensorMap A_tail[3], B_tail[3];      // boxes of 16, 4, 1 tokens (K ragged only)
 };
 
-// Launchers (tcg_lm.cu).  out_kind: type of D.  bn: 32, 64, 128 or 256 (kEpiXent*: 256).
+// Launchers (tcg_lm.cu).  out_kind: type of D.  bn: 32, 64 or 128 (kEpiNarrow), 64, 128 or 256
+// (kEpiWide), 256 (K ragged, kEpiXentStats, kEpiXentGrad), 32 (kEpiXentNarrow).
 cudaError_t launch_lm(const LmMaps &maps, const LmArgs &a, int epi, int out_kind, int bn,
                       int grid, cudaStream_t s);
 int lm_max_resident_ctas(int num_sms);

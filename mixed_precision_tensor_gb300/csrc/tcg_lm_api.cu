@@ -28,83 +28,114 @@ bool bad_ld(int64_t ld, int64_t rows, int es)
     return ld < (rows > 1 ? rows : 1) || (ld * es) % 16;
 }
 
-int clusters_of(tcgContext *h)
+int pairs_of(tcgContext *h)
 {
     if (h->max_ctas[0] == 0)
         h->max_ctas[0] = lm_max_resident_ctas(h->num_sms);
     return h->max_ctas[0] / 2;
 }
 
-// One product of the kernel: D (m x cols) per group, see LmArgs.
+// One product: D[token][feature] = epilogue(X[token] . W_g[feature]), or (ragged_k) one
+// matrix per group, D_g[row][col] = sum over the group's tokens of X[token][row] W[token][col].
 struct Product {
-    int64_t m = 0, cols = 0, k = 0;
-    bool a_kmajor = true, b_kmajor = true;
-    const void *A = nullptr, *B = nullptr;
-    int64_t lda = 0, strideA = 0, ldb = 0;
+    int64_t tokens = 0, feats = 0, k = 0;
+    int64_t rows = 0;                       // K ragged: X's extent; W's is feats
+    bool x_kmajor = true, w_kmajor = true;
+    const void *X = nullptr, *W = nullptr;
+    int64_t ldx = 0, ldw = 0, strideW = 0;
     tcgDataType_t in = TCG_R_16BF, out = TCG_R_16BF;
     int64_t groups = 1;
     const int64_t *offsets = nullptr;
     bool ragged_k = false;
-    int64_t n = 0;                          // K ragged
     float alpha = 1.0f;
     const float *alpha_dev = nullptr;
     void *D = nullptr;
     int64_t ldd = 0, strideD = 0;
     tcgEpilogue_t epi = {};
-    int lm_epi = kEpiLinear;
+    int lm_epi = -1;                        // kEpiXent*, or chosen by shape_of
 };
 
-int64_t m_tiles_of(int64_t m) { return (m + 2 * kBM - 1) / (2 * kBM); }
+// How a product runs: epilogue kind, tile width, whether tiles may be cut along K, pairs.
+struct Shape {
+    int epi, bn, share, gain, grid;
+    int64_t tiles;                          // at most (a grouped call's depend on its offsets)
+    bool cut;
+};
 
-// The most tiles a call can have (a grouped call's column tiles depend on its offsets).
-int64_t max_tiles(const Product &p, int bn)
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// The most tiles a call can have.
+int64_t max_tiles(const Product &p, int epi, int bn)
 {
-    int64_t nt = (p.cols + bn - 1) / bn;
-    if (p.offsets)
-        nt = p.cols / bn + (p.groups + 2 < p.cols ? p.groups + 2 : p.cols);
-    return m_tiles_of(p.m) * nt;
+    const bool narrow = epi == kEpiNarrow || epi == kEpiXentNarrow;
+    if (p.ragged_k)
+        return p.groups * ceil_div(p.rows, 256) * ceil_div(p.feats, bn);
+    const int side = narrow ? bn : 256;
+    int64_t along = ceil_div(p.tokens, side);
+    if (p.offsets)                          // one more for each range that is not empty
+        along = p.tokens / side + (p.groups + 2 < p.tokens ? p.groups + 2 : p.tokens);
+    return along * ceil_div(p.feats, narrow ? 256 : bn);
 }
 
-// Tile width of an N-ragged product.
-int width_of(tcgContext *h, const Product &p)
-{
-    const int64_t per = p.offsets ? p.cols / p.groups : p.cols;
-    int bn = per <= 32 ? 32 : (per <= 64 ? 64 : (per <= 128 ? 128 : 256));
-    if (!p.b_kmajor && bn < 128)
-        bn = 128;                           // a 64-column chunk per CTA at least
-    if (bn == 256 && max_tiles(p, 256) * 2 <= clusters_of(h))
-        bn = 128;
-    return bn;
-}
+// Saving in K blocks that pays for joining partial sums of a 256 x bn tile.
+int gain_of(int bn) { return bn * 24 / 256 < 8 ? 8 : bn * 24 / 256; }
+constexpr int kMinShare = 4;                // fewest K blocks of a cut tile per pair
 
-// K ranges of an N-ragged product: as many as fill the SM pairs once when the tiles fill
-// at most half of them, at least four K blocks each.
-void split_of(tcgContext *h, const Product &p, int bn, int *splits, int *per)
+Shape shape_of(tcgContext *h, const Product &p)
 {
-    const int nkb = static_cast<int>((p.k + 63) / 64);
-    const int64_t tiles = max_tiles(p, bn);
-    const int clusters = clusters_of(h);
-    int64_t s = 1;
-    if (tiles > 0 && tiles * 2 <= clusters && tiles * 4 <= kLmCounters)
-        s = clusters / tiles;
-    if (s > nkb / 4)
-        s = nkb / 4;
-    if (s > kLmMaxSplits)
-        s = kLmMaxSplits;
-    if (s < 1)
-        s = 1;
-    *per = nkb > 0 ? static_cast<int>((nkb + s - 1) / s) : 1;
-    *splits = nkb > 0 ? (nkb + *per - 1) / *per : 1;
+    Shape s;
+    const int64_t P = pairs_of(h), nkb = ceil_div(p.k, 64);
+    if (p.ragged_k) {
+        s.epi = kEpiWide;
+        s.bn = 256;
+    } else if (p.lm_epi >= 0) {
+        s.epi = p.lm_epi;
+        s.bn = p.lm_epi == kEpiXentNarrow ? 32 : 256;
+    } else {
+        const int64_t per = p.offsets ? p.tokens / p.groups : p.tokens;
+        if (p.x_kmajor && per <= 128) {
+            s.epi = kEpiNarrow;
+            s.bn = per <= 32 ? 32 : (per <= 64 ? 64 : 128);
+        } else {
+            // Tokens on the rows: the tile width with the least predicted time, in the time of
+            // a K block at width 256 (narrower tiles load A as often for less work).
+            s.epi = kEpiWide;
+            s.bn = 256;
+            double best = 1e300;
+            for (int bn = 256; bn >= (p.w_kmajor ? 64 : 128); bn /= 2) {
+                const double cost = bn == 256 ? 1.0 : (bn == 128 ? 0.55 : 0.35);
+                const int64_t tiles = max_tiles(p, s.epi, bn), rest = tiles % P;
+                int64_t share = ceil_div(rest * nkb, P);
+                share = share < kMinShare ? kMinShare : share;
+                double t = static_cast<double>(tiles / P * nkb);
+                if (rest)
+                    t += nkb - share >= gain_of(bn) ? static_cast<double>(share) + gain_of(bn) / cost
+                                                    : static_cast<double>(nkb);
+                t = t * cost + 12.0 * bn / 256;
+                if (t < best) {
+                    best = t;
+                    s.bn = bn;
+                }
+            }
+        }
+    }
+    s.tiles = max_tiles(p, s.epi, s.bn);
+    s.share = kMinShare;
+    s.gain = gain_of(s.bn);
+    const bool linear = s.epi == kEpiNarrow || s.epi == kEpiWide || s.epi == kEpiXentNarrow;
+    s.cut = linear && !p.ragged_k && nkb - kMinShare >= s.gain &&
+            (p.offsets || s.tiles % P != 0) && h->split_k != 1;
+    int64_t pairs = s.tiles;
+    if (s.cut)
+        pairs = s.tiles * nkb / kMinShare > pairs ? s.tiles * nkb / kMinShare : pairs;
+    s.grid = 2 * static_cast<int>(pairs < P ? pairs : P);
+    return s;
 }
 
 size_t product_ws(tcgContext *h, const Product &p)
 {
-    if (p.ragged_k || p.lm_epi != kEpiLinear)
-        return 0;
-    const int bn = width_of(h, p);
-    int splits, per;
-    split_of(h, p, bn, &splits, &per);
-    return splits > 1 ? lm_part_bytes(max_tiles(p, bn), bn, splits) : 0;
+    const Shape s = shape_of(h, p);
+    return s.cut ? lm_part_bytes(s.grid / 2, s.bn) : 0;
 }
 
 // Queue one product.  ws: workspace of at least product_ws bytes.
@@ -112,25 +143,30 @@ tcgStatus_t queue(tcgContext *h, const Product &p, void *ws, LmArgs a = LmArgs{}
 {
     LmMaps maps;
     std::memset(&maps, 0, sizeof maps);
-    const int bn = p.ragged_k || p.lm_epi != kEpiLinear ? 256 : width_of(h, p);
-    a.m = static_cast<int>(p.m);
-    a.cols = static_cast<int>(p.cols);
-    a.n = static_cast<int>(p.n);
+    const Shape s = shape_of(h, p);
+    if (s.tiles > INT32_MAX)
+        return TCG_STATUS_NOT_SUPPORTED;
+    const bool narrow = s.epi == kEpiNarrow || s.epi == kEpiXentNarrow;
+    // accumulator rows and columns
+    const int64_t x_ext = p.ragged_k ? p.rows : p.tokens;
+    a.rows = static_cast<int>(narrow ? p.feats : x_ext);
+    a.cols = static_cast<int>(narrow ? x_ext : p.feats);
+    a.tokens = static_cast<int>(p.tokens);
     a.ragged_k = p.ragged_k;
     a.groups = static_cast<int>(p.groups);
     a.offsets = p.offsets;
-    a.num_m_tiles = static_cast<int>(m_tiles_of(p.m));
-    a.num_n_tiles = static_cast<int>(((p.ragged_k ? p.n : p.cols) + bn - 1) / bn);
-    a.num_k_blocks = static_cast<int>((p.k + 63) / 64);
-    a.k_splits = 1;
-    a.kb_per_split = a.num_k_blocks;
-    if (!p.ragged_k && p.lm_epi == kEpiLinear)
-        split_of(h, p, bn, &a.k_splits, &a.kb_per_split);
+    a.num_row_tiles = (a.rows + 255) / 256;
+    a.num_col_tiles = (a.cols + s.bn - 1) / s.bn;
+    a.num_k_blocks = static_cast<int>(ceil_div(p.k, 64));
+    a.min_share = s.share;
+    a.split_gain = s.gain;
     a.group_m = h->group_m > 0 ? h->group_m : 8;
     a.in_bf16 = p.in == TCG_R_16BF;
+    const bool a_kmajor = narrow ? p.w_kmajor : p.x_kmajor;
+    const bool b_kmajor = narrow ? p.x_kmajor : p.w_kmajor;
     a.idesc = (1u << 4) | (static_cast<uint32_t>(a.in_bf16) << 7) |
-              (static_cast<uint32_t>(a.in_bf16) << 10) | ((p.a_kmajor ? 0u : 1u) << 15) |
-              ((p.b_kmajor ? 0u : 1u) << 16) | (static_cast<uint32_t>(bn >> 3) << 17) |
+              (static_cast<uint32_t>(a.in_bf16) << 10) | ((a_kmajor ? 0u : 1u) << 15) |
+              ((b_kmajor ? 0u : 1u) << 16) | (static_cast<uint32_t>(s.bn >> 3) << 17) |
               (static_cast<uint32_t>((2 * kBM) >> 4) << 24);
     a.alpha = p.alpha;
     a.alpha_dev = p.alpha_dev;
@@ -145,49 +181,43 @@ tcgStatus_t queue(tcgContext *h, const Product &p, void *ws, LmArgs a = LmArgs{}
     a.Z = p.epi.Z;
     a.ldz = p.epi.ldz;
     a.act = p.epi.activation;
-    a.part = static_cast<float *>(ws);
+    a.part = s.cut ? static_cast<float *>(ws) : nullptr;
     a.cnt = h->d_cnt;
     a.err = h->d_err;
     a.wait_limit_ns = h->wait_limit_ns;
     a.fault_inject = h->fault_inject;
 
-    // Operands (none where nothing is summed).  A K-ragged call's are both M/N-major over
-    // all tokens.
+    // Operands (none where nothing is summed).  A K-ragged call's are both token-major.
     tcgStatus_t st;
-    bool bc;
-    const int64_t ka = p.ragged_k ? p.cols : p.k;
-    if (ka > 0) {
-        st = operand_map(h, p.A, p.in, p.a_kmajor, p.m, ka, p.lda, p.strideA,
-                         p.ragged_k || !p.offsets ? 1 : p.groups, kBM, 64, &bc, &a.a_mode, &maps.A);
+    const int64_t kx = p.ragged_k ? p.tokens : p.k;
+    if (kx > 0) {
+        bool bc;
+        st = operand_map(h, p.X, p.in, p.x_kmajor, x_ext, kx, p.ldx, 0, 1, narrow ? s.bn / 2 : kBM,
+                         64, &bc, narrow ? &a.b_mode : &a.a_mode, narrow ? &maps.B : &maps.A);
         if (st != TCG_STATUS_SUCCESS)
             return st;
-        st = operand_map(h, p.B, p.in, p.b_kmajor, p.ragged_k ? p.n : p.cols, ka, p.ldb, 0, 1,
-                         bn / 2, 64, &bc, &a.b_mode, &maps.B);
+        st = operand_map(h, p.W, p.in, p.w_kmajor, p.feats, kx, p.ldw, p.strideW,
+                         p.ragged_k || !p.offsets ? 1 : p.groups, narrow ? kBM : s.bn / 2, 64, &bc,
+                         narrow ? &a.a_mode : &a.b_mode, narrow ? &maps.A : &maps.B);
         if (st != TCG_STATUS_SUCCESS)
             return st;
     }
-    if (p.ragged_k && ka > 0) {
+    if (p.ragged_k && kx > 0) {
         const int boxes[3] = {16, 4, 1};
         for (int i = 0; i < 3; ++i)
             for (int x = 0; x < 2; ++x) {
-                const int64_t rows = x ? p.n : p.m, ld = x ? p.ldb : p.lda;
-                const uint64_t dims[3] = {static_cast<uint64_t>(rows), static_cast<uint64_t>(p.cols), 1};
+                const int64_t ext = x ? p.rows : p.feats, ld = x ? p.ldx : p.ldw;
+                const uint64_t dims[3] = {static_cast<uint64_t>(ext), static_cast<uint64_t>(kx), 1};
                 const uint64_t str[2] = {static_cast<uint64_t>(ld) * 2,
-                                         static_cast<uint64_t>(ld) * 2 * static_cast<uint64_t>(p.cols)};
+                                         static_cast<uint64_t>(ld) * 2 * static_cast<uint64_t>(kx)};
                 const uint32_t box[3] = {64, static_cast<uint32_t>(boxes[i]), 1};
-                st = get_map(h, x ? p.B : p.A, p.in, 3, dims, str, box,
-                             x ? &maps.B_tail[i] : &maps.A_tail[i]);
+                st = get_map(h, x ? p.X : p.W, p.in, 3, dims, str, box,
+                             x ? &maps.A_tail[i] : &maps.B_tail[i]);
                 if (st != TCG_STATUS_SUCCESS)
                     return st;
             }
     }
-    const int64_t units = p.ragged_k ? p.groups * a.num_m_tiles * a.num_n_tiles
-                                     : max_tiles(p, bn) * a.k_splits;
-    if (units > INT32_MAX)
-        return TCG_STATUS_NOT_SUPPORTED;
-    const int64_t most = clusters_of(h);
-    const int grid = 2 * static_cast<int>(units < most ? units : most);
-    const cudaError_t e = launch_lm(maps, a, p.lm_epi, out_kind_of(p.out), bn, grid, h->stream);
+    const cudaError_t e = launch_lm(maps, a, s.epi, out_kind_of(p.out), s.bn, s.grid, h->stream);
     h->launches += 1;
     if (e != cudaSuccess) {
         cudaGetLastError();
@@ -244,33 +274,33 @@ tcgStatus_t check_device(tcgContext *h, std::initializer_list<const void *> ptrs
     return TCG_STATUS_SUCCESS;
 }
 
-// The N-ragged product behind tcg_gemm_epilogue and tcg_gemm_grouped.
+// The product behind tcg_gemm_epilogue and tcg_gemm_grouped.
 tcgStatus_t run_product(tcgContext *h, Product &p, const tcgEpilogue_t *e)
 {
     if (e)
         p.epi = *e;
     tcgStatus_t st = check_types(p.in, p.out);
     if (st == TCG_STATUS_SUCCESS)
-        st = check_epilogue(p.epi, p.m, p.cols, p.in, p.out);
+        st = check_epilogue(p.epi, p.feats, p.tokens, p.in, p.out);
     if (st != TCG_STATUS_SUCCESS)
         return st;
-    if (p.m < 0 || p.cols < 0 || p.k < 0)
+    if (p.feats < 0 || p.tokens < 0 || p.k < 0)
         return TCG_STATUS_INVALID_VALUE;
-    if (bad_ld(p.lda, p.a_kmajor ? p.k : p.m, 2) || bad_ld(p.ldb, p.b_kmajor ? p.k : p.cols, 2) ||
-        bad_ld(p.ldd, p.m, elem_size(p.out)))
+    if (bad_ld(p.ldw, p.w_kmajor ? p.k : p.feats, 2) || bad_ld(p.ldx, p.x_kmajor ? p.k : p.tokens, 2) ||
+        bad_ld(p.ldd, p.feats, elem_size(p.out)))
         return TCG_STATUS_INVALID_VALUE;
-    if (p.offsets && ((p.groups > 1 && p.strideA <= 0) || (p.strideA * 2) % 16))
+    if (p.offsets && ((p.groups > 1 && p.strideW <= 0) || (p.strideW * 2) % 16))
         return TCG_STATUS_INVALID_VALUE;
-    if (p.m > kMaxExtent || p.cols > kMaxExtent || p.k > kMaxExtent)
+    if (p.feats > kMaxExtent || p.tokens > kMaxExtent || p.k > kMaxExtent)
         return TCG_STATUS_NOT_SUPPORTED;
-    if (p.m == 0 || p.cols == 0)
+    if (p.feats == 0 || p.tokens == 0)
         return TCG_STATUS_SUCCESS;
     if (!p.D || !aligned16(p.D) ||
-        (p.k > 0 && (!p.A || !p.B || !aligned16(p.A) || !aligned16(p.B))))
+        (p.k > 0 && (!p.W || !p.X || !aligned16(p.W) || !aligned16(p.X))))
         return TCG_STATUS_INVALID_VALUE;
     st = bind_device(h);
     if (st == TCG_STATUS_SUCCESS)
-        st = check_device(h, {p.D, p.k > 0 ? p.A : nullptr, p.k > 0 ? p.B : nullptr, p.offsets,
+        st = check_device(h, {p.D, p.k > 0 ? p.W : nullptr, p.k > 0 ? p.X : nullptr, p.offsets,
                               p.epi.bias, p.epi.beta != 0.0f ? p.epi.C : nullptr, p.epi.Z});
     if (st != TCG_STATUS_SUCCESS)
         return st;
@@ -288,12 +318,15 @@ tcgStatus_t run_product(tcgContext *h, Product &p, const tcgEpilogue_t *e)
 // ----------------------------------------------------------------------- cross entropy
 size_t pad256(size_t b) { return (b + 255) / 256 * 256; }
 
-// Workspace of the forward pass: two (maximum, sum) slots per 256 vocabulary entries and
-// row, and the target logits.
-int64_t xent_slots(int64_t vocab) { return (vocab + 255) / 256 * 2; }
+// Few rows go on the accumulator's columns (kEpiXentNarrow).
+constexpr int64_t kXentNarrowRows = 32;
+
+// Workspace of the forward pass: (maximum, sum) slots for every row, the target logits, and
+// the partial sums of cut tiles.
 size_t xent_stats_bytes(int64_t rows, int64_t vocab)
 {
-    return pad256(static_cast<size_t>(xent_slots(vocab) * rows) * sizeof(float2));
+    return pad256(static_cast<size_t>(lm_stat_slots(vocab, rows <= kXentNarrowRows) * rows) *
+                  sizeof(float2));
 }
 
 // Vocabulary entries whose gradient is held at a time, a multiple of 256: 256 MiB of it.
@@ -313,12 +346,12 @@ struct XentBackwardPlan {
 
 Product xent_dx(int64_t rows, int64_t k, int64_t width, int64_t piece, tcgDataType_t in, bool one)
 {
-    Product p;
-    p.m = k;
-    p.cols = rows;
+    Product p;                              // dX[row][feature] = G[row] . W[:, feature]
+    p.tokens = rows;
+    p.feats = k;
     p.k = width;
-    p.a_kmajor = false;
-    p.ldb = piece;
+    p.w_kmajor = false;
+    p.ldx = piece;
     p.in = in;
     p.out = one ? in : TCG_R_32F;
     return p;
@@ -326,12 +359,12 @@ Product xent_dx(int64_t rows, int64_t k, int64_t width, int64_t piece, tcgDataTy
 
 Product xent_dw(int64_t rows, int64_t k, int64_t width, int64_t piece, tcgDataType_t in)
 {
-    Product p;
-    p.m = k;
-    p.cols = width;
+    Product p;                              // dW[entry][feature] = G[:, entry] . X[:, feature]
+    p.tokens = width;
+    p.feats = k;
     p.k = rows;
-    p.a_kmajor = p.b_kmajor = false;
-    p.ldb = piece;
+    p.x_kmajor = p.w_kmajor = false;
+    p.ldx = piece;
     p.in = p.out = in;
     return p;
 }
@@ -391,16 +424,28 @@ tcgStatus_t check_xent(const Xent &x)
 Product xent_logits(const Xent &x, int64_t col0, int64_t width, int epi)
 {
     Product p;
-    p.m = x.rows;
-    p.cols = width;
+    p.tokens = x.rows;
+    p.feats = width;
     p.k = x.k;
-    p.A = x.X;
-    p.lda = x.ldx;
-    p.B = static_cast<const uint16_t *>(x.W) + col0 * x.ldw;
-    p.ldb = x.ldw;
+    p.X = x.X;
+    p.ldx = x.ldx;
+    p.W = static_cast<const uint16_t *>(x.W) + col0 * x.ldw;
+    p.ldw = x.ldw;
     p.in = x.in;
     p.lm_epi = epi;
     return p;
+}
+
+// The forward pass's product and its workspace.
+Product xent_forward_product(const Xent &x)
+{
+    return xent_logits(x, 0, x.vocab, x.rows <= kXentNarrowRows ? kEpiXentNarrow : kEpiXentStats);
+}
+
+size_t xent_forward_bytes(tcgContext *h, const Xent &x)
+{
+    return xent_stats_bytes(x.rows, x.vocab) + pad256(static_cast<size_t>(x.rows) * 4) +
+           product_ws(h, xent_forward_product(x));
 }
 
 }  // namespace
@@ -415,15 +460,15 @@ tcgStatus_t tcg_gemm_epilogue(tcgHandle_t h, tcgOp_t transa, tcgOp_t transb, int
     if (!h || (transa != TCG_OP_N && transa != TCG_OP_T) || (transb != TCG_OP_N && transb != TCG_OP_T))
         return TCG_STATUS_INVALID_VALUE;
     Product p;
-    p.m = m;
-    p.cols = n;
+    p.feats = m;
+    p.tokens = n;
     p.k = k;
-    p.a_kmajor = transa == TCG_OP_T;
-    p.b_kmajor = transb == TCG_OP_N;
-    p.A = A;
-    p.lda = lda;
-    p.B = B;
-    p.ldb = ldb;
+    p.w_kmajor = transa == TCG_OP_T;
+    p.x_kmajor = transb == TCG_OP_N;
+    p.W = A;
+    p.ldw = lda;
+    p.X = B;
+    p.ldx = ldb;
     p.in = ABtype;
     p.out = Dtype;
     p.alpha = alpha;
@@ -444,15 +489,15 @@ tcgStatus_t tcg_gemm_grouped(tcgHandle_t h, tcgOp_t transa, int64_t m, int64_t n
     if (st != TCG_STATUS_SUCCESS)
         return st;
     Product p;
-    p.m = m;
-    p.cols = n;
+    p.feats = m;
+    p.tokens = n;
     p.k = k;
-    p.a_kmajor = transa == TCG_OP_T;
-    p.A = A;
-    p.lda = lda;
-    p.strideA = strideA;
-    p.B = B;
-    p.ldb = ldb;
+    p.w_kmajor = transa == TCG_OP_T;
+    p.W = A;
+    p.ldw = lda;
+    p.strideW = strideA;
+    p.X = B;
+    p.ldx = ldb;
     p.in = ABtype;
     p.out = Dtype;
     p.groups = groups;
@@ -463,10 +508,11 @@ tcgStatus_t tcg_gemm_grouped(tcgHandle_t h, tcgOp_t transa, int64_t m, int64_t n
     return run_product(h, p, epilogue);
 }
 
-tcgStatus_t tcg_gemm_epilogue_workspace_size(tcgHandle_t h, tcgOp_t transb, int64_t m, int64_t n,
-                                             int64_t k, int64_t groups, size_t *bytes)
+tcgStatus_t tcg_gemm_epilogue_workspace_size(tcgHandle_t h, tcgOp_t transa, tcgOp_t transb,
+                                             int64_t m, int64_t n, int64_t k, int64_t groups,
+                                             size_t *bytes)
 {
-    if (!h || !bytes || (transb != TCG_OP_N && transb != TCG_OP_T) || m < 0 || n < 0 || k < 0 ||
+    if (!h || !bytes || (transa != TCG_OP_N && transa != TCG_OP_T) || (transb != TCG_OP_N && transb != TCG_OP_T) || m < 0 || n < 0 || k < 0 ||
         groups < 0 || groups > kLmMaxGroups)
         return TCG_STATUS_INVALID_VALUE;
     *bytes = 0;
@@ -477,10 +523,11 @@ tcgStatus_t tcg_gemm_epilogue_workspace_size(tcgHandle_t h, tcgOp_t transb, int6
         return st;
     static const int64_t some = 0;
     Product p;
-    p.m = m;
-    p.cols = n;
+    p.feats = m;
+    p.tokens = n;
     p.k = k;
-    p.b_kmajor = transb == TCG_OP_N;
+    p.w_kmajor = transa == TCG_OP_T;
+    p.x_kmajor = transb == TCG_OP_N;
     if (groups > 0) {
         p.groups = groups;
         p.offsets = &some;                  // grouped: only whether it is set matters here
@@ -519,15 +566,15 @@ tcgStatus_t tcg_gemm_grouped_k(tcgHandle_t h, int64_t m, int64_t n, int64_t k, i
         return st;
     h->used = true;
     Product p;
-    p.m = m;
-    p.n = n;
-    p.cols = k;
+    p.feats = m;
+    p.rows = n;
+    p.tokens = k;
     p.ragged_k = true;
-    p.a_kmajor = p.b_kmajor = false;
-    p.A = A;
-    p.B = B;
-    p.lda = lda;
-    p.ldb = ldb;
+    p.x_kmajor = p.w_kmajor = false;
+    p.X = B;
+    p.W = A;
+    p.ldx = ldb;
+    p.ldw = lda;
     p.in = ABtype;
     p.out = Dtype;
     p.groups = groups;
@@ -610,8 +657,8 @@ tcgStatus_t tcg_xent_workspace_size(tcgHandle_t h, int64_t rows, int64_t vocab, 
     const tcgStatus_t st = bind_device(h);
     if (st != TCG_STATUS_SUCCESS)
         return st;
-    *bytes = backward ? xent_plan(h, rows, vocab, k, type).total
-                      : xent_stats_bytes(rows, vocab) + pad256(static_cast<size_t>(rows) * 4);
+    const Xent x{rows, vocab, k, nullptr, k, nullptr, k, type, nullptr, -1};
+    *bytes = backward ? xent_plan(h, rows, vocab, k, type).total : xent_forward_bytes(h, x);
     return TCG_STATUS_SUCCESS;
 }
 
@@ -635,7 +682,7 @@ tcgStatus_t tcg_xent_forward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_t
     h->used = true;
     void *ws = nullptr;
     const size_t stats_bytes = xent_stats_bytes(rows, vocab);
-    st = acquire_ws(h, stats_bytes + pad256(static_cast<size_t>(rows) * 4), &ws);
+    st = acquire_ws(h, xent_forward_bytes(h, x), &ws);
     if (st != TCG_STATUS_SUCCESS)
         return st;
     LmArgs a{};
@@ -644,10 +691,12 @@ tcgStatus_t tcg_xent_forward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_t
     a.vocab = vocab;
     a.stats = static_cast<float2 *>(ws);
     a.target_logit = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + stats_bytes);
-    st = queue(h, xent_logits(x, 0, vocab, kEpiXentStats), nullptr, a);
+    st = queue(h, xent_forward_product(x),
+               static_cast<uint8_t *>(ws) + stats_bytes + pad256(static_cast<size_t>(rows) * 4), a);
     if (st != TCG_STATUS_SUCCESS)
         return st;
-    const cudaError_t e = launch_xent_combine(a.stats, static_cast<int>(xent_slots(vocab)),
+    const cudaError_t e = launch_xent_combine(a.stats, static_cast<int>(
+                                                  lm_stat_slots(vocab, rows <= kXentNarrowRows)),
                                               static_cast<int>(rows), a.target_logit, targets, vocab,
                                               ignore_index, loss, lse, h->stream);
     h->launches += 1;
@@ -684,7 +733,7 @@ tcgStatus_t tcg_xent_backward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_
     h->used = true;
     if (rows == 0) {                                       // no rows: dW is zero
         Product p = xent_dw(0, k, vocab, vocab, type);
-        p.lda = ldx;
+        p.ldw = ldx;
         p.D = dW;
         p.ldd = lddw;
         return queue(h, p, nullptr);
@@ -725,9 +774,9 @@ tcgStatus_t tcg_xent_backward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_
             return st;
         if (dX) {
             Product p = xent_dx(rows, k, width, pl.piece, type, pl.pieces == 1);
-            p.A = static_cast<const uint16_t *>(W) + c0 * ldw;
-            p.lda = ldw;
-            p.B = G;
+            p.W = static_cast<const uint16_t *>(W) + c0 * ldw;
+            p.ldw = ldw;
+            p.X = G;
             if (pl.pieces == 1) {
                 p.D = dX;
                 p.ldd = lddx;
@@ -745,9 +794,9 @@ tcgStatus_t tcg_xent_backward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_
         }
         if (dW) {
             Product p = xent_dw(rows, k, width, pl.piece, type);
-            p.A = X;
-            p.lda = ldx;
-            p.B = G;
+            p.W = X;
+            p.ldw = ldx;
+            p.X = G;
             p.D = static_cast<uint16_t *>(dW) + c0 * lddw;
             p.ldd = lddw;
             p.alpha_dev = scaled ? scale + 1 : nullptr;

@@ -48,7 +48,7 @@ def same_bits(a, b):
 # ------------------------------------------------------------------------------ linear
 SIZES = [(1, 8, 8), (1, 4096, 4096), (2, 13, 5), (3, 264, 72), (17, 300, 1000), (33, 256, 64),
          (64, 1000, 1032), (100, 520, 200), (129, 2056, 264), (257, 513, 127), (300, 77, 2048),
-         (700, 1288, 320), (2000, 4096, 256), (5, 256, 20000)]
+         (700, 1288, 320), (200, 1000, 4096), (2000, 4096, 256), (5, 256, 20000)]
 
 
 @pytest.mark.parametrize("t,n,k", SIZES)
@@ -130,7 +130,7 @@ def test_linear_in_place_residual_and_empty(handle):
 def test_linear_split_is_deterministic(handle, t, n, k):
     g = gen_of(t)
     x, w = randn(g, t, k), randn(g, n, k, std=k ** -0.5)
-    assert tcg.tcg_gemm_epilogue_workspace_size(handle.h, 0, n, t, k) > 0
+    assert tcg.tcg_gemm_epilogue_workspace_size(handle.h, 1, 0, n, t, k) > 0
     first = tcg.linear(handle, x, w, out_dtype=F32)
     for _ in range(5):
         assert same_bits(tcg.linear(handle, x, w, out_dtype=F32), first)
@@ -280,7 +280,7 @@ def test_grouped_single_rows_split(handle):
     sizes = [0, 1, 0, 0, 2, 0, 0, 1]
     off = offsets_of(sizes, 0)
     x, w = randn(g, 4, 4096), randn(g, 8, 256, 4096, std=1 / 64)
-    assert tcg.tcg_gemm_epilogue_workspace_size(handle.h, 0, 256, 4, 4096, 8) > 0
+    assert tcg.tcg_gemm_epilogue_workspace_size(handle.h, 1, 0, 256, 4, 4096, 8) > 0
     first = tcg.grouped_linear(handle, x, w, off, act="silu", out_dtype=F32)
     for _ in range(4):
         assert same_bits(tcg.grouped_linear(handle, x, w, off, act="silu", out_dtype=F32), first)

@@ -22,10 +22,7 @@
 // Every wait is bounded as in tcg_kernels.cu: a wait that runs out sets a bit in the
 // device error word, every role stops and the kernel returns.
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include "tcg_lm.h"
+#include "tcg_lm_math.cuh"
 #include "tcg_pipe.cuh"
 
 namespace tcg {
@@ -56,179 +53,7 @@ constexpr int kLmCtlBytes = 2 * 1024;
 static_assert(sizeof(LmCtl) <= kLmCtlBytes, "control area too small");
 constexpr int kLmSmemBytes = kLmDataBytes + kLmCtlBytes + 1024;   // + alignment slack
 
-// ------------------------------------------------------------------------- activations
-// Two FP32 values in a register pair: one instruction adds, multiplies or multiply-adds both
-// (each rounded to nearest as the scalar forms).
-struct F2 {
-    uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float a, float b)
-{
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
-__device__ __forceinline__ void split2(F2 p, float &a, float &b)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p.v));
-}
-__device__ __forceinline__ F2 operator*(F2 a, F2 b)
-{
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 operator+(F2 a, F2 b)
-{
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
-{
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-template <typename F>
-__device__ __forceinline__ F2 each(F2 p, F f)
-{
-    float a, b;
-    split2(p, a, b);
-    return f2(f(a), f(b));
-}
-
-// 2^x and 1 / x on the special-function unit: relative error about 2^-22, results below
-// 2^-126 flushed to zero.  That is under the rounding of every output type but FP32, where
-// it is of the rounding's own size.
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float rcp_fast(float x)
-{
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ F2 exp2_2(F2 x) { return each(x, exp2_fast); }
-__device__ __forceinline__ F2 rcp_2(F2 x) { return each(x, rcp_fast); }
-
-constexpr float kLog2e = 1.4426950408889634f;
-
-// erfc(|x| / sqrt 2) / 2 and exp(-x^2 / 2), with erfc(a) = (a1 t + ... + a5 t^5) exp(-a^2),
-// t = 1 / (1 + p a): Abramowitz & Stegun 7.1.26, |error| <= 1.5e-7.  ax = min(|x|, 20), past
-// which both are zero.
-__device__ __forceinline__ F2 half_erfc(F2 ax, F2 &gauss)
-{
-    const F2 t = rcp_2(fma2(f2(0.3275911f * 0.70710678118654752f), ax, f2(1.0f)));
-    gauss = exp2_2(ax * ax * f2(-0.5f * kLog2e));
-    F2 q = fma2(t, f2(0.5f * 1.061405429f), f2(0.5f * -1.453152027f));
-    q = fma2(t, q, f2(0.5f * 1.421413741f));
-    q = fma2(t, q, f2(0.5f * -0.284496736f));
-    q = fma2(t, q, f2(0.5f * 0.254829592f));
-    return q * t * gauss;
-}
-
-template <int ACT>
-__device__ __forceinline__ F2 act_fn(F2 x)
-{
-    if constexpr (ACT == kActRelu) {
-        return each(x, [](float v) { return v < 0.0f ? 0.0f : v; });
-    } else if constexpr (ACT == kActGelu) {
-        // x Phi(x) = max(x, 0) - |x| erfc(|x| / sqrt 2) / 2; 0 x keeps NaN (and -inf, whose
-        // product with zero has no value either)
-        F2 g;
-        const F2 ax = each(x, [](float v) { return fminf(fabsf(v), 20.0f); });
-        const F2 h = half_erfc(ax, g);
-        const F2 pos = each(x, [](float v) { return v > 0.0f ? v : 0.0f * v; });
-        return fma2(ax * f2(-1.0f), h, pos);
-    } else if constexpr (ACT == kActGeluTanh) {
-        // 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u)), u = sqrt(2 / pi) (x + 0.044715 x^3)
-        const F2 c = f2(-1.5957691216057308f * kLog2e);
-        const F2 e = exp2_2(x * fma2(c * f2(0.044715f) * x, x, c));
-        return x * rcp_2(e + f2(1.0f));
-    } else if constexpr (ACT == kActSilu) {
-        return x * rcp_2(exp2_2(x * f2(-kLog2e)) + f2(1.0f));
-    } else {
-        return x;
-    }
-}
-
-template <int ACT>
-__device__ __forceinline__ F2 act_slope(F2 x)
-{
-    if constexpr (ACT == kActRelu) {
-        return each(x, [](float v) { return v > 0.0f ? 1.0f : (v <= 0.0f ? 0.0f : v); });
-    } else if constexpr (ACT == kActGelu) {
-        F2 g;
-        const F2 ax = each(x, [](float v) { return fminf(fabsf(v), 20.0f); });
-        float h0, h1, x0, x1;
-        split2(half_erfc(ax, g), h0, h1);
-        split2(x, x0, x1);
-        const F2 phi = f2(x0 > 0.0f ? 1.0f - h0 : h0, x1 > 0.0f ? 1.0f - h1 : h1);
-        return fma2(x * f2(0.39894228040143268f), g, phi);
-    } else if constexpr (ACT == kActGeluTanh) {
-        const F2 c = f2(-1.5957691216057308f * kLog2e), x2 = x * x;
-        const F2 s = rcp_2(exp2_2(x * fma2(c * f2(0.044715f), x2, c)) + f2(1.0f));
-        const F2 d = fma2(f2(1.5957691216057308f * 3.0f * 0.044715f), x2, f2(1.5957691216057308f));
-        return fma2(x * s * fma2(s, f2(-1.0f), f2(1.0f)), d, s);
-    } else if constexpr (ACT == kActSilu) {
-        const F2 s = rcp_2(exp2_2(x * f2(-kLog2e)) + f2(1.0f));
-        return s * fma2(x, fma2(s, f2(-1.0f), f2(1.0f)), f2(1.0f));
-    } else {
-        return f2(1.0f);
-    }
-}
-
-__device__ __forceinline__ float load16(const void *p, int64_t i, int bf16)
-{
-    const uint16_t u = static_cast<const uint16_t *>(p)[i];
-    return bf16 ? __uint_as_float(static_cast<uint32_t>(u) << 16)
-                : __half2float(__ushort_as_half(u));
-}
-
-__device__ __forceinline__ uint16_t round16(float v, int bf16)
-{
-    return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
-}
-
-template <int OUT>
-__device__ __forceinline__ float load_as(const void *p, int64_t i)
-{
-    if constexpr (OUT == kOutF32)
-        return static_cast<const float *>(p)[i];
-    else
-        return load16(p, i, OUT == kOutBF16);
-}
-
-template <int OUT>
-__device__ __forceinline__ void store_as(void *p, int64_t i, float v)
-{
-    if constexpr (OUT == kOutF32)
-        static_cast<float *>(p)[i] = v;
-    else
-        static_cast<uint16_t *>(p)[i] = round16(v, OUT == kOutBF16);
-}
-
 // ------------------------------------------------------------------------------- units
-// Range of group g, clamped into the `tokens` that exist whatever the offsets say.
-__device__ __forceinline__ void group_range(const int64_t *offsets, int tokens, int g, int &begin,
-                                            int &end)
-{
-    if (!offsets) {
-        begin = 0;
-        end = tokens;
-        return;
-    }
-    const int64_t b = offsets[g], e = offsets[g + 1], c = tokens;
-    begin = static_cast<int>(b < 0 ? 0 : (b > c ? c : b));
-    end = static_cast<int>(e < begin ? begin : (e > c ? c : e));
-}
-
 // The tokens of no group: before the first (which = 0) and after the last (1).
 __device__ __forceinline__ void null_range(const LmArgs &p, int which, int &begin, int &end)
 {
@@ -445,33 +270,6 @@ __device__ __forceinline__ void apply_act(int act, float (&x)[N])
     case kActGeluTanh: all([](F2 v) { return act_fn<kActGeluTanh>(v); }); break;
     case kActSilu: all([](F2 v) { return act_fn<kActSilu>(v); }); break;
     default: break;
-    }
-}
-
-__device__ __forceinline__ uint32_t pack16(float a, float b, bool bf16)
-{
-    if (bf16) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-        return *reinterpret_cast<const uint32_t *>(&h);
-    }
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-template <bool BF16>
-__device__ __forceinline__ void unpack16(const uint4 &v, float (&x)[8])
-{
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        if constexpr (BF16) {
-            x[2 * k] = __uint_as_float(u[k] << 16);
-            x[2 * k + 1] = __uint_as_float(u[k] & 0xFFFF0000u);
-        } else {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u[k]));
-            x[2 * k] = f.x;
-            x[2 * k + 1] = f.y;
-        }
     }
 }
 
@@ -1347,23 +1145,17 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
     griddep_wait();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int row = blockIdx.x * 32 + lane;
-    auto join = [](float2 a, float2 b) {
-        const float m = fmaxf(a.x, b.x);
-        const float sub = m == -INFINITY ? 0.0f : m * kLog2e;
-        return make_float2(m, a.y * exp2_fast(fmaf(a.x, kLog2e, -sub)) +
-                                  b.y * exp2_fast(fmaf(b.x, kLog2e, -sub)));
-    };
     float2 acc = make_float2(-INFINITY, 0.0f);
     if (row < rows) {
 #pragma unroll 4
         for (int s = w; s < slots; s += kCombineWarps)
-            acc = join(acc, __ldcg(stats + static_cast<int64_t>(s) * rows + row));
+            acc = join_stats(acc, __ldcg(stats + static_cast<int64_t>(s) * rows + row));
     }
     part[w][lane] = acc;
     __syncthreads();
     if (w == 0 && row < rows) {
         for (int i = 1; i < kCombineWarps; ++i)
-            acc = join(acc, part[i][lane]);
+            acc = join_stats(acc, part[i][lane]);
         const float l = acc.x + logf(acc.y);
         const int64_t t = targets[row];
         const bool counts = t != ignore && t >= 0 && t < vocab;
@@ -1589,22 +1381,6 @@ __global__ void __launch_bounds__(256)
         dbias[static_cast<int64_t>(g) * m + row] = ((s + join[1][lane]) + join[2][lane]) + join[3][lane];
 }
 
-template <typename... Params, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(Params...), dim3 grid, dim3 block, cudaStream_t s, Args... args)
-{
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.stream = s;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
-    return e != cudaSuccess ? e : cudaGetLastError();
-}
-
 }  // namespace
 
 cudaError_t launch_lm(const LmMaps &maps, const LmArgs &a, int epi, int out_kind, int bn, int grid,
@@ -1662,14 +1438,14 @@ cudaError_t launch_xent_combine(const float2 *stats, int slots, int rows, const 
                                 const int64_t *targets, int64_t vocab, int64_t ignore, float *loss,
                                 float *lse, cudaStream_t s)
 {
-    return launch_pdl(tcg_xent_combine_kernel, dim3((rows + 31) / 32), dim3(32 * kCombineWarps), s,
+    return launch_pdl(tcg_xent_combine_kernel, dim3((rows + 31) / 32), dim3(32 * kCombineWarps), s, 0,
                       stats, slots, rows, target_logit, targets, vocab, ignore, loss, lse);
 }
 
 cudaError_t launch_xent_scale(const float *dloss, const int64_t *targets, int rows, int64_t vocab,
                               int64_t ignore, float *scale, cudaStream_t s)
 {
-    return launch_pdl(tcg_xent_scale_kernel, dim3(1), dim3(1024), s, dloss, targets, rows, vocab,
+    return launch_pdl(tcg_xent_scale_kernel, dim3(1), dim3(1024), s, 0, dloss, targets, rows, vocab,
                       ignore, scale);
 }
 
@@ -1678,7 +1454,7 @@ cudaError_t launch_round_out(const float *in, int64_t ldi, int rows, int cols, c
 {
     return launch_pdl(out_kind == kOutBF16 ? tcg_round_out_kernel<kOutBF16>
                                            : tcg_round_out_kernel<kOutF16>,
-                      dim3(grid), dim3(256), s, in, ldi, rows, cols, scale,
+                      dim3(grid), dim3(256), s, 0, in, ldi, rows, cols, scale,
                       static_cast<uint16_t *>(out), ldo);
 }
 
@@ -1688,7 +1464,7 @@ static cudaError_t epi_backward(int bf16, dim3 grid, cudaStream_t s, int m, int 
                                 int64_t ldz, void *dZ, int64_t lddz, float *part, int chunk)
 {
     return launch_pdl(bf16 ? tcg_epi_backward_kernel<ACT, true> : tcg_epi_backward_kernel<ACT, false>,
-                      grid, dim3(256), s, m, cols, groups, offsets, static_cast<const uint16_t *>(dD),
+                      grid, dim3(256), s, 0, m, cols, groups, offsets, static_cast<const uint16_t *>(dD),
                       lddd, static_cast<const uint16_t *>(Z), ldz, static_cast<uint16_t *>(dZ), lddz,
                       part, chunk);
 }
@@ -1709,7 +1485,7 @@ cudaError_t launch_epi_backward(int act, int bf16, int m, int cols, int groups,
                dbias ? part : nullptr, chunk);
     }
     if (e == cudaSuccess && dbias)
-        e = launch_pdl(tcg_bias_join_kernel, dim3((m + 63) / 64, groups), dim3(256), s,
+        e = launch_pdl(tcg_bias_join_kernel, dim3((m + 63) / 64, groups), dim3(256), s, 0,
                        const_cast<const float *>(part), m, cols, groups, offsets, chunk, dbias);
     return e;
 }

@@ -119,6 +119,39 @@ cudaError_t launch_lm(const LmMaps &maps, const LmArgs &a, int epi, int out_kind
                       int grid, cudaStream_t s);
 int lm_max_resident_ctas(int num_sms);
 
+// The products for a few tokens (tcg_lm_few.cu): D[token][feature], weights K-contiguous.
+struct LmFewArgs {
+    int64_t feats, k;
+    int tokens;                // dense and cross entropy: at most kLmFewTokens
+    int groups;
+    const int64_t *offsets;    // device; nullptr: dense
+    const void *W;
+    int64_t ldw, strideW;
+    const void *X;
+    int64_t ldx;
+    int in_bf16, out_kind;
+    float alpha;
+    void *D;
+    int64_t ldd;
+    const void *bias;
+    int bias_f32;
+    const void *C;
+    int64_t ldc;
+    float beta;
+    void *Z;
+    int64_t ldz;
+    int act;
+    const int64_t *targets;    // cross entropy
+    int64_t ignore;
+    float2 *stats;             // [block][token], one block per SM; nullptr: linear
+    float *target_logit;
+    uint32_t *err;
+    unsigned long long wait_limit_ns;
+};
+constexpr int kLmFewTokens = 4;        // dense, cross entropy
+constexpr int kLmFewRows = 64;         // grouped: rows of all experts
+cudaError_t launch_few(const LmFewArgs &a, int num_sms, cudaStream_t s);
+
 // loss and log-sum-exp of each row from the slots of kEpiXentStats.
 cudaError_t launch_xent_combine(const float2 *stats, int slots, int rows, const float *target_logit,
                                 const int64_t *targets, int64_t vocab, int64_t ignore, float *loss,

@@ -132,8 +132,13 @@ Shape shape_of(tcgContext *h, const Product &p)
     return s;
 }
 
+bool few(const Product &p);
+bool few_tokens(int64_t tokens, int64_t k);
+
 size_t product_ws(tcgContext *h, const Product &p)
 {
+    if (few(p))
+        return 0;
     const Shape s = shape_of(h, p);
     return s.cut ? lm_part_bytes(s.grid / 2, s.bn) : 0;
 }
@@ -226,6 +231,61 @@ tcgStatus_t queue(tcgContext *h, const Product &p, void *ws, LmArgs a = LmArgs{}
     return TCG_STATUS_SUCCESS;
 }
 
+// Few enough tokens, and X small enough to stay in an SM's cache (where it does not, every
+// SM reads the same lines of L2 again and again).
+bool few_tokens(int64_t tokens, int64_t k)
+{
+    return tokens == 1 || (tokens <= kLmFewTokens && tokens * k <= 32768);
+}
+
+// Whether a product runs as a pass over the weights (tcg_lm_few.cu): K-contiguous operands
+// and at most four tokens, or, grouped, rows that are few for the number of experts.
+bool few(const Product &p)
+{
+    if (p.ragged_k || !p.x_kmajor || !p.w_kmajor || p.k == 0 || p.lm_epi >= 0 || p.alpha_dev)
+        return false;
+    return p.offsets ? p.tokens <= kLmFewRows && p.tokens <= 2 * p.groups
+                     : few_tokens(p.tokens, p.k);
+}
+
+tcgStatus_t queue_few(tcgContext *h, const Product &p)
+{
+    LmFewArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.feats = p.feats;
+    a.k = p.k;
+    a.tokens = static_cast<int>(p.tokens);
+    a.groups = static_cast<int>(p.groups);
+    a.offsets = p.offsets;
+    a.W = p.W;
+    a.ldw = p.ldw;
+    a.strideW = p.strideW;
+    a.X = p.X;
+    a.ldx = p.ldx;
+    a.in_bf16 = p.in == TCG_R_16BF;
+    a.out_kind = out_kind_of(p.out);
+    a.alpha = p.alpha;
+    a.D = p.D;
+    a.ldd = p.ldd;
+    a.bias = p.epi.bias;
+    a.bias_f32 = p.epi.bias_type == TCG_R_32F;
+    a.C = p.epi.beta != 0.0f ? p.epi.C : nullptr;
+    a.ldc = p.epi.ldc;
+    a.beta = p.epi.beta;
+    a.Z = p.epi.Z;
+    a.ldz = p.epi.ldz;
+    a.act = p.epi.activation;
+    a.err = h->d_err;
+    a.wait_limit_ns = h->wait_limit_ns;
+    const cudaError_t e = launch_few(a, h->num_sms, h->stream);
+    h->launches += 1;
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return TCG_STATUS_EXECUTION_FAILED;
+    }
+    return TCG_STATUS_SUCCESS;
+}
+
 tcgStatus_t check_epilogue(const tcgEpilogue_t &e, int64_t m, int64_t n, tcgDataType_t in,
                            tcgDataType_t out)
 {
@@ -305,6 +365,8 @@ tcgStatus_t run_product(tcgContext *h, Product &p, const tcgEpilogue_t *e)
     if (st != TCG_STATUS_SUCCESS)
         return st;
     h->used = true;
+    if (few(p))
+        return queue_few(h, p);
     void *ws = nullptr;
     const size_t need = product_ws(h, p);
     if (need) {
@@ -323,10 +385,15 @@ constexpr int64_t kXentNarrowRows = 32;
 
 // Workspace of the forward pass: (maximum, sum) slots for every row, the target logits, and
 // the partial sums of cut tiles.
-size_t xent_stats_bytes(int64_t rows, int64_t vocab)
+int64_t xent_slots(tcgContext *h, int64_t rows, int64_t vocab, int64_t k)
 {
-    return pad256(static_cast<size_t>(lm_stat_slots(vocab, rows <= kXentNarrowRows) * rows) *
-                  sizeof(float2));
+    if (few_tokens(rows, k))               // blocks of tcg_lm_few.cu
+        return h->num_sms;
+    return lm_stat_slots(vocab, rows <= kXentNarrowRows);
+}
+size_t xent_stats_bytes(tcgContext *h, int64_t rows, int64_t vocab, int64_t k)
+{
+    return pad256(static_cast<size_t>(xent_slots(h, rows, vocab, k) * rows) * sizeof(float2));
 }
 
 // Vocabulary entries whose gradient is held at a time, a multiple of 256: 256 MiB of it.
@@ -444,8 +511,8 @@ Product xent_forward_product(const Xent &x)
 
 size_t xent_forward_bytes(tcgContext *h, const Xent &x)
 {
-    return xent_stats_bytes(x.rows, x.vocab) + pad256(static_cast<size_t>(x.rows) * 4) +
-           product_ws(h, xent_forward_product(x));
+    return xent_stats_bytes(h, x.rows, x.vocab, x.k) + pad256(static_cast<size_t>(x.rows) * 4) +
+           (few_tokens(x.rows, x.k) ? 0 : product_ws(h, xent_forward_product(x)));
 }
 
 }  // namespace
@@ -681,7 +748,7 @@ tcgStatus_t tcg_xent_forward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_t
         return st;
     h->used = true;
     void *ws = nullptr;
-    const size_t stats_bytes = xent_stats_bytes(rows, vocab);
+    const size_t stats_bytes = xent_stats_bytes(h, rows, vocab, k);
     st = acquire_ws(h, xent_forward_bytes(h, x), &ws);
     if (st != TCG_STATUS_SUCCESS)
         return st;
@@ -691,12 +758,35 @@ tcgStatus_t tcg_xent_forward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_t
     a.vocab = vocab;
     a.stats = static_cast<float2 *>(ws);
     a.target_logit = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + stats_bytes);
-    st = queue(h, xent_forward_product(x),
-               static_cast<uint8_t *>(ws) + stats_bytes + pad256(static_cast<size_t>(rows) * 4), a);
-    if (st != TCG_STATUS_SUCCESS)
-        return st;
-    const cudaError_t e = launch_xent_combine(a.stats, static_cast<int>(
-                                                  lm_stat_slots(vocab, rows <= kXentNarrowRows)),
+    if (few_tokens(rows, k)) {
+        LmFewArgs f;
+        std::memset(&f, 0, sizeof f);
+        f.feats = vocab;
+        f.k = k;
+        f.tokens = static_cast<int>(rows);
+        f.W = W;
+        f.ldw = ldw;
+        f.X = X;
+        f.ldx = ldx;
+        f.in_bf16 = type == TCG_R_16BF;
+        f.targets = targets;
+        f.ignore = ignore_index;
+        f.stats = a.stats;
+        f.target_logit = a.target_logit;
+        f.err = h->d_err;
+        f.wait_limit_ns = h->wait_limit_ns;
+        if (launch_few(f, h->num_sms, h->stream) != cudaSuccess) {
+            cudaGetLastError();
+            return TCG_STATUS_EXECUTION_FAILED;
+        }
+        h->launches += 1;
+    } else {
+        st = queue(h, xent_forward_product(x),
+                   static_cast<uint8_t *>(ws) + stats_bytes + pad256(static_cast<size_t>(rows) * 4), a);
+        if (st != TCG_STATUS_SUCCESS)
+            return st;
+    }
+    const cudaError_t e = launch_xent_combine(a.stats, static_cast<int>(xent_slots(h, rows, vocab, k)),
                                               static_cast<int>(rows), a.target_logit, targets, vocab,
                                               ignore_index, loss, lse, h->stream);
     h->launches += 1;

@@ -273,39 +273,6 @@ __device__ __forceinline__ void apply_act(int act, float (&x)[N])
     }
 }
 
-// Bias entries i .. i + 31 (the first n of them), the same for every lane.
-__device__ __forceinline__ void load_bias(const LmArgs &p, int64_t i, int n, float (&b)[32])
-{
-    const uint8_t *at = static_cast<const uint8_t *>(p.bias) + i * (p.bias_f32 ? 4 : 2);
-    if (n >= 32 && (reinterpret_cast<uintptr_t>(at) & 15u) == 0) {
-        const uint4 *q = reinterpret_cast<const uint4 *>(at);
-        if (p.bias_f32) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint4 v = q[j];
-                b[4 * j] = __uint_as_float(v.x);
-                b[4 * j + 1] = __uint_as_float(v.y);
-                b[4 * j + 2] = __uint_as_float(v.z);
-                b[4 * j + 3] = __uint_as_float(v.w);
-            }
-        } else if (p.in_bf16) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                unpack16<true>(q[j], *reinterpret_cast<float (*)[8]>(b + 8 * j));
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                unpack16<false>(q[j], *reinterpret_cast<float (*)[8]>(b + 8 * j));
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            b[j] = j >= n ? 0.0f
-                 : p.bias_f32 ? static_cast<const float *>(p.bias)[i + j]
-                              : load16(p.bias, i + j, p.in_bf16);
-    }
-}
-
 // One feature (row) of kCols tokens from `col` on: each store of a warp is a 64- or 128-byte
 // run of one token's features.
 template <int OUT, int kCols>
@@ -404,107 +371,128 @@ __device__ __forceinline__ void stage_get(uint8_t *stage, int lane, float (&x)[3
     }
 }
 
-// The staged block to memory: rows from row0 on up to row_end, the first ncol columns.
+// A warp's block of a row-major matrix of ES-byte elements: `at` is this lane's first piece
+// (row lane / pieces, piece lane % pieces), `step` the bytes to its next one.
 template <int ES>
-__device__ __forceinline__ void stage_flush(uint8_t *stage, int lane, void *base, int64_t ld, int row0,
-                                            int row_end, int col, int ncol)
+struct WarpBlock {
+    static constexpr int kPieces = 2 * ES, kRows = 32 / kPieces, kElems = 16 / ES;
+    uint8_t *at;
+    int64_t step;
+
+    __device__ __forceinline__ WarpBlock(const void *base, int64_t ld, int64_t row0, int64_t col, int lane)
+    {
+        at = static_cast<uint8_t *>(const_cast<void *>(base)) +
+             ((row0 + lane / kPieces) * ld + col + lane % kPieces * kElems) * ES;
+        step = kRows * ld * ES;
+    }
+};
+
+// The staged block to memory: its first nrow rows and ncol columns.
+template <int ES>
+__device__ __forceinline__ void stage_flush(uint8_t *stage, int lane, WarpBlock<ES> m, int nrow, int ncol)
 {
-    constexpr int kPieces = 2 * ES, kRows = 32 / kPieces, kElems = 16 / ES;
-    const int piece = lane % kPieces, c = piece * kElems;
-    uint8_t *at = static_cast<uint8_t *>(base) +
-                  ((static_cast<int64_t>(row0) + lane / kPieces) * ld + col + c) * ES;
+    using M = WarpBlock<ES>;
+    const int row = lane / M::kPieces, piece = lane % M::kPieces;
+    if (nrow >= 32 && ncol >= 32) {
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-        const int r = i * kRows + lane / kPieces;
-        if (row0 + r < row_end && c < ncol) {
-            const uint4 v = *stage_piece<ES>(stage, r, piece);
-            uint8_t *q = at + static_cast<int64_t>(i * kRows) * ld * ES;
-            if (c + kElems <= ncol) {
-                *reinterpret_cast<uint4 *>(q) = v;
-            } else {
-                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int j = 0; j < kElems; ++j)
-                    if (c + j < ncol) {
-                        if constexpr (ES == 4)
-                            reinterpret_cast<uint32_t *>(q)[j] = u[j];
-                        else
-                            reinterpret_cast<uint16_t *>(q)[j] =
-                                static_cast<uint16_t>(u[j / 2] >> (16 * (j & 1)));
-                    }
+        for (int i = 0; i < M::kPieces; ++i) {
+            *reinterpret_cast<uint4 *>(m.at) = *stage_piece<ES>(stage, i * M::kRows + row, piece);
+            m.at += m.step;
+        }
+        return;
+    }
+#pragma unroll 1
+    for (int i = 0; i < M::kPieces; ++i, m.at += m.step) {
+        if (i * M::kRows + row >= nrow)
+            break;
+        const uint8_t *v = reinterpret_cast<const uint8_t *>(stage_piece<ES>(stage, i * M::kRows + row, piece));
+        const int n = ncol - piece * M::kElems;
+        if (n >= M::kElems) {
+            *reinterpret_cast<uint4 *>(m.at) = *reinterpret_cast<const uint4 *>(v);
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < n; ++j) {
+                if constexpr (ES == 4)
+                    reinterpret_cast<uint32_t *>(m.at)[j] = reinterpret_cast<const uint32_t *>(v)[j];
+                else
+                    reinterpret_cast<uint16_t *>(m.at)[j] = reinterpret_cast<const uint16_t *>(v)[j];
             }
         }
     }
 }
 
-// The same block from memory into registers (piece i of this lane's share), zeros outside.
+// A block that is not whole from memory to the staging area (what lies outside stays as it was).
 template <int ES>
-__device__ __forceinline__ void block_load(uint4 (&v)[2 * ES], int lane, const void *base, int64_t ld,
-                                           int row0, int row_end, int col, int ncol)
+__device__ __forceinline__ void stage_fill_part(uint8_t *stage, int lane, WarpBlock<ES> m, int nrow, int ncol)
 {
-    constexpr int kPieces = 2 * ES, kRows = 32 / kPieces, kElems = 16 / ES;
-    const int piece = lane % kPieces, c = piece * kElems;
-    const uint8_t *at = static_cast<const uint8_t *>(base) +
-                        ((static_cast<int64_t>(row0) + lane / kPieces) * ld + col + c) * ES;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-        v[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (row0 + i * kRows + lane / kPieces < row_end && c < ncol) {
-            const uint8_t *q = at + static_cast<int64_t>(i * kRows) * ld * ES;
-            if (c + kElems <= ncol) {
-                v[i] = *reinterpret_cast<const uint4 *>(q);
-            } else {
-                uint32_t u[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-                for (int j = 0; j < kElems; ++j)
-                    if (c + j < ncol) {
-                        if constexpr (ES == 4)
-                            u[j] = reinterpret_cast<const uint32_t *>(q)[j];
-                        else
-                            u[j / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(q)[j])
-                                        << (16 * (j & 1));
-                    }
-                v[i] = make_uint4(u[0], u[1], u[2], u[3]);
-            }
+    using M = WarpBlock<ES>;
+    const int row = lane / M::kPieces, piece = lane % M::kPieces;
+#pragma unroll 1
+    for (int i = 0; i < M::kPieces; ++i, m.at += m.step) {
+        if (i * M::kRows + row >= nrow)
+            break;
+        uint8_t *v = reinterpret_cast<uint8_t *>(stage_piece<ES>(stage, i * M::kRows + row, piece));
+        const int n = ncol - piece * M::kElems;
+#pragma unroll 1
+        for (int j = 0; j < n && j < M::kElems; ++j) {
+            if constexpr (ES == 4)
+                reinterpret_cast<uint32_t *>(v)[j] = reinterpret_cast<const uint32_t *>(m.at)[j];
+            else
+                reinterpret_cast<uint16_t *>(v)[j] = reinterpret_cast<const uint16_t *>(m.at)[j];
         }
     }
 }
 
-// A warp's 32 tokens (from row0, this lane's values in z) x 32 features from `col` on; the
-// whole warp calls it.
+// z = alpha v + bias for the 32 features from entry i of the bias on (the first n of them),
+// the same for every lane: a lane loads one entry, all read them back from the staging area.
+__device__ __forceinline__ void scale_bias(const LmArgs &p, float alpha, int64_t i, int n, uint8_t *stage,
+                                           int lane, const uint32_t (&v)[32], float (&z)[32])
+{
+    const F2 a = f2(alpha);
+    if (!p.bias) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 2)
+            split2(a * f2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), z[j], z[j + 1]);
+        return;
+    }
+    float b = 0.0f;
+    if (lane < n)
+        b = p.bias_f32 ? static_cast<const float *>(p.bias)[i + lane] : load16(p.bias, i + lane, p.in_bf16);
+    reinterpret_cast<float *>(stage)[lane] = b;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 32; j += 4) {
+        const float4 q = reinterpret_cast<const float4 *>(stage)[j / 4];
+        split2(fma2(a, f2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), f2(q.x, q.y)), z[j], z[j + 1]);
+        split2(fma2(a, f2(__uint_as_float(v[j + 2]), __uint_as_float(v[j + 3])), f2(q.z, q.w)), z[j + 2],
+               z[j + 3]);
+    }
+    __syncwarp();
+}
+
+// A warp's 32 tokens (from row0; this lane's pre-activations in z) x 32 features from `col`
+// on; the whole warp calls it, with a block that is not empty.
 template <int OUT>
 __device__ __forceinline__ void finish_wide(const LmArgs &p, float (&z)[32], const LmUnit &w, int row0,
-                                            int col, float alpha, uint8_t *stage, int lane)
+                                            int col, uint8_t *stage, int lane)
 {
     constexpr int ES = OUT == kOutF32 ? 4 : 2;
-    const int ncol = w.col_end - col;
-    if (row0 >= w.row_end || ncol <= 0)
-        return;
+    const int nrow = w.row_end - row0, ncol = w.col_end - col;
+    const bool whole = nrow >= 32 && ncol >= 32;
     if (w.g < 0) {                             // tokens of no group
 #pragma unroll
         for (int j = 0; j < 32; ++j)
             z[j] = 0.0f;
-        stage_put<OUT>(stage, lane, z);
-        __syncwarp();
-        stage_flush<ES>(stage, lane, p.D, p.ldd, row0, w.row_end, col, ncol);
-        if (p.Z)
-            stage_flush<2>(stage, lane, p.Z, p.ldz, row0, w.row_end, col, ncol);
-        __syncwarp();
-        return;
     }
     uint4 c[2 * ES];
-    if (p.C)
-        block_load<ES>(c, lane, p.C, p.ldc, row0, w.row_end, col, ncol);
-    if (p.bias) {
-        float b[32];
-        load_bias(p, static_cast<int64_t>(w.g) * p.cols + col, ncol, b);
+    const bool add = p.C && w.g >= 0;
+    if (add && whole) {
+        WarpBlock<ES> m(p.C, p.ldc, row0, col, lane);
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            z[j] = fmaf(alpha, z[j], b[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            z[j] *= alpha;
+        for (int i = 0; i < 2 * ES; ++i) {
+            c[i] = *reinterpret_cast<const uint4 *>(m.at);
+            m.at += m.step;
+        }
     }
     if (p.Z) {
         if (p.in_bf16)
@@ -512,27 +500,33 @@ __device__ __forceinline__ void finish_wide(const LmArgs &p, float (&z)[32], con
         else
             stage_put<kOutF16>(stage, lane, z);
         __syncwarp();
-        stage_flush<2>(stage, lane, p.Z, p.ldz, row0, w.row_end, col, ncol);
+        stage_flush<2>(stage, lane, WarpBlock<2>(p.Z, p.ldz, row0, col, lane), nrow, ncol);
         __syncwarp();
     }
-    apply_act(p.act, z);
-    if (p.C) {
+    if (w.g >= 0)
+        apply_act(p.act, z);
+    if (add) {
         constexpr int kPieces = 2 * ES, kRows = 32 / kPieces;
+        if (whole) {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-            *stage_piece<ES>(stage, i * kRows + lane / kPieces, lane % kPieces) = c[i];
+            for (int i = 0; i < kPieces; ++i)
+                *stage_piece<ES>(stage, i * kRows + lane / kPieces, lane % kPieces) = c[i];
+        } else {
+            stage_fill_part<ES>(stage, lane, WarpBlock<ES>(p.C, p.ldc, row0, col, lane), nrow, ncol);
+        }
         __syncwarp();
         float r[32];
         stage_get<OUT>(stage, lane, r);
+        const F2 beta = f2(p.beta);
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            z[j] = fmaf(p.beta, r[j], z[j]);
+        for (int j = 0; j < 32; j += 2)
+            split2(fma2(beta, f2(r[j], r[j + 1]), f2(z[j], z[j + 1])), z[j], z[j + 1]);
         __syncwarp();
     }
     stage_put<OUT>(stage, lane, z);
     __syncwarp();
     uint8_t *d = static_cast<uint8_t *>(p.D) + (p.ragged_k ? w.g * p.strideD * ES : 0);
-    stage_flush<ES>(stage, lane, d, p.ldd, row0, w.row_end, col, ncol);
+    stage_flush<ES>(stage, lane, WarpBlock<ES>(d, p.ldd, row0, col, lane), nrow, ncol);
     __syncwarp();
 }
 
@@ -924,45 +918,58 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 const uint32_t taddr = tmem_half + static_cast<uint32_t>(it % kAccBufs * BN);
                 float *sl = cut ? slot_ptr(w.slot) + rl : nullptr;       // [column][row]
-                auto chunk = [&](uint32_t (&v)[32], int c) {
-                    float x[32];
+                uint32_t v[32];
+                __syncwarp();
+                tmem_ld_32x32b_x32(taddr, v);
+#pragma unroll 1
+                for (int c = 0; c < kChunks; ++c) {
+                    const int col = col_half + c * 32;
+                    const bool inside = row - lane < w.row_end && col < w.col_end;
+                    float z[32];
+                    tmem_ld_done(v);
+                    if (empty_k) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        x[j] = empty_k ? 0.0f : __uint_as_float(v[j]);
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = 0u;
+                    }
                     if (cut) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            __stcg(sl + (c * 32 + j) * kBM, x[j]);
-                    } else {
-                        finish_wide<OUT>(p, x, w, row - lane, col_half + c * 32, alpha, stage, lane);
+                            __stcg(sl + (c * 32 + j) * kBM, __uint_as_float(v[j]));
+                    } else if (inside) {
+                        scale_bias(p, alpha, static_cast<int64_t>(w.g) * p.cols + col, w.g < 0 ? 0 : w.col_end - col,
+                                   stage, lane, v, z);
                     }
-                };
-#pragma unroll 1
-                for (int c = 0; c < kChunks; ++c) {
                     __syncwarp();
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(taddr + 32 * c, v);
-                    tmem_ld_done(v);
-                    if (c == kChunks - 1)
+                    if (c + 1 < kChunks)               // on its way while this chunk is finished
+                        tmem_ld_32x32b_x32(taddr + 32 * (c + 1), v);
+                    else
                         release();
-                    chunk(v, c);
+                    if (!cut && inside)
+                        finish_wide<OUT>(p, z, w, row - lane, col, stage, lane);
                 }
-                if (cut && arrive()) {
+                if (cut && arrive() && row - lane < w.row_end) {
 #pragma unroll 1
                     for (int c = 0; c < kChunks; ++c) {
-                        if (col_half + c * 32 >= w.col_end)
+                        const int col = col_half + c * 32;
+                        if (col >= w.col_end)
                             break;
-                        float x[32];
+                        float z[32];
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            x[j] = 0.0f;
+                            z[j] = 0.0f;
                         for (int i = 0; i < w.pieces; ++i) {
                             const float *q = slot_ptr(piece_slot(i)) + c * 32 * kBM + rl;
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
-                                x[j] += __ldcg(q + j * kBM);
+                                z[j] += __ldcg(q + j * kBM);
                         }
-                        finish_wide<OUT>(p, x, w, row - lane, col_half + c * 32, alpha, stage, lane);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = __float_as_uint(z[j]);
+                        scale_bias(p, alpha, static_cast<int64_t>(w.g) * p.cols + col, w.col_end - col, stage,
+                                   lane, v, z);
+                        finish_wide<OUT>(p, z, w, row - lane, col, stage, lane);
                     }
                 }
             } else {
@@ -1046,35 +1053,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!acquire())
                         break;
                     const uint32_t taddr = tmem_half + static_cast<uint32_t>(it % kAccBufs * BN);
-                    auto chunk = [&](uint32_t (&v)[32], int c) {
+                    constexpr int kChunks = kHalf / 32;
+                    uint32_t v[32];
+                    __syncwarp();
+                    tmem_ld_32x32b_x32(taddr, v);
+#pragma unroll 1
+                    for (int c = 0; c < kChunks; ++c) {
                         const int col = col_half + c * 32;
                         float g[32];
+                        tmem_ld_done(v);
+                        const F2 l2e = f2(kLog2e), sub = f2(-row_lse2), scale = f2(row_g);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float pr = exp2_fast(fmaf(__uint_as_float(v[j]), kLog2e, -row_lse2));
-                            g[j] = row_g == 0.0f ? 0.0f : row_g * (target == col + j ? pr - 1.0f : pr);
+                        for (int j = 0; j < 32; j += 2) {
+                            const F2 pr = exp2_2(fma2(f2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), l2e,
+                                                      sub));
+                            split2(pr, g[j], g[j + 1]);
                         }
-                        if (col < w.col_end) {
+                        if (target >= col && target < col + 32) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                g[j] -= target == col + j ? 1.0f : 0.0f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2)
+                            split2(f2(g[j], g[j + 1]) * scale, g[j], g[j + 1]);
+                        if (row_g == 0.0f) {             // whatever the logits hold
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                g[j] = 0.0f;
+                        }
+                        __syncwarp();
+                        if (c + 1 < kChunks)
+                            tmem_ld_32x32b_x32(taddr + 32 * (c + 1), v);
+                        else
+                            release();
+                        if (col < w.col_end && row - lane < w.row_end) {
                             if (p.in_bf16)
                                 stage_put<kOutBF16>(stage, lane, g);
                             else
                                 stage_put<kOutF16>(stage, lane, g);
                             __syncwarp();
-                            stage_flush<2>(stage, lane, p.D, p.ldd, row - lane, w.row_end, col,
-                                           w.col_end - col);
+                            stage_flush<2>(stage, lane, WarpBlock<2>(p.D, p.ldd, row - lane, col, lane),
+                                           w.row_end - (row - lane), w.col_end - col);
                             __syncwarp();
                         }
-                    };
-                    constexpr int kChunks = kHalf / 32;
-#pragma unroll 1
-                    for (int c = 0; c < kChunks; ++c) {
-                        __syncwarp();
-                        uint32_t v[32];
-                        tmem_ld_32x32b_x32(taddr + 32 * c, v);
-                        tmem_ld_done(v);
-                        if (c == kChunks - 1)
-                            release();
-                        chunk(v, c);
                     }
                 }
             }

@@ -688,9 +688,10 @@ tcgStatus_t tcg_epilogue_backward(tcgHandle_t h, tcgActivation_t activation, int
     if (st != TCG_STATUS_SUCCESS)
         return st;
     h->used = true;
-    // Columns per block: about eight blocks of 256 rows per SM, 16 to 256 columns each.
+    // Columns per block: about 32 blocks of 256 rows per SM (a few at a time), 16 to 256
+    // columns each.
     const int64_t row_blocks = (m + 255) / 256;
-    int64_t chunk = n * row_blocks / (8 * static_cast<int64_t>(h->num_sms)) / 8 * 8;
+    int64_t chunk = n * row_blocks / (32 * static_cast<int64_t>(h->num_sms)) / 8 * 8;
     chunk = chunk < 16 ? 16 : (chunk > 256 ? 256 : chunk);
     while ((n + chunk - 1) / chunk > 65535)              // the grid's second dimension
         chunk *= 2;

@@ -6,7 +6,8 @@
 //   warp 0 (one lane)   TMA producer into a ring of 128-byte-swizzled stages (64 K elements
 //                       of 128 rows of A and BN / 2 rows of B per CTA)
 //   warp 1 (one lane)   tcgen05.mma into TMEM accumulators (up to four)
-//   warps 2-9           epilogue: TMEM -> registers -> memory, one accumulator row a thread
+//   the other warps     epilogue (8, or 16 for large tiles): TMEM -> registers -> memory, one
+//                       accumulator row a thread
 //
 // The epilogues (LmEpi):
 //   kEpiNarrow     features on the rows, tokens on the columns: few tokens against a weight
@@ -45,7 +46,7 @@ struct LmCtl {
     uint64_t drain;
     uint32_t tmem_base;
     volatile int abort_flag;
-    volatile int last_arrival[2];
+    volatile int last_arrival[4];
     LmPlan plan;
     int cum[kLmMaxGroups + 1];              // tiles before each group of a grouped call
 };
@@ -317,73 +318,49 @@ __device__ __forceinline__ void finish_narrow(const LmArgs &p, float (&z)[kCols]
             store_as<OUT>(p.D, dbase + j * p.ldd, z[j]);
 }
 
-// A warp's block of 32 rows (tokens) x 32 columns (features), a row per lane in registers,
-// goes to and from memory through the warp's staging area, so that memory is accessed in
-// runs of 64 (16-bit) or 128 bytes (FP32) of a row: a lane's own row would go in 16-byte
-// pieces of 32 different lines per instruction (16384 x 4096 x 4096 BF16: 335 us a call so,
-// 291 us through the staging area).  The 16-byte pieces of a row are permuted by row, so
-// that neither side has bank conflicts.
-template <int ES>
+// A warp's rows (tokens, one per lane in registers) go to and from memory through the warp's
+// staging area, 64 bytes of each row at a time (32 16-bit or 16 FP32 features), so that
+// memory is accessed in runs of 64 bytes: a lane's own row would go in 16-byte pieces of 32
+// different lines per instruction (16384 x 4096 x 1024 BF16: 114 us a call so, 90 us through
+// the staging area).  The 16-byte pieces of a row are permuted by row, so that neither side
+// has bank conflicts.
 __device__ __forceinline__ uint4 *stage_piece(uint8_t *stage, int row, int piece)
 {
-    constexpr int kPieces = 2 * ES;                   // 16-byte pieces of a row: 4 or 8
-    const int p = ES == 2 ? piece ^ ((row >> 1) & 3) : piece ^ (row & 7);
-    return reinterpret_cast<uint4 *>(stage) + row * kPieces + p;
+    return reinterpret_cast<uint4 *>(stage) + row * 4 + (piece ^ ((row >> 1) & 3));
 }
 
-template <int OUT>
-__device__ __forceinline__ void stage_put(uint8_t *stage, int lane, const float (&x)[32])
+// kN = 32 16-bit or 16 FP32 values of this lane's row.
+template <int OUT, int kN>
+__device__ __forceinline__ void stage_put(uint8_t *stage, int lane, const float *x)
 {
-    if constexpr (OUT == kOutF32) {
+    static_assert(kN == (OUT == kOutF32 ? 16 : 32), "64 bytes");
+    constexpr bool b = OUT == kOutBF16;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            *stage_piece<4>(stage, lane, j) =
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (OUT == kOutF32)
+            *stage_piece(stage, lane, j) =
                 make_uint4(__float_as_uint(x[4 * j]), __float_as_uint(x[4 * j + 1]),
                            __float_as_uint(x[4 * j + 2]), __float_as_uint(x[4 * j + 3]));
-    } else {
-        constexpr bool b = OUT == kOutBF16;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            *stage_piece<2>(stage, lane, j) =
+        else
+            *stage_piece(stage, lane, j) =
                 make_uint4(pack16(x[8 * j], x[8 * j + 1], b), pack16(x[8 * j + 2], x[8 * j + 3], b),
                            pack16(x[8 * j + 4], x[8 * j + 5], b), pack16(x[8 * j + 6], x[8 * j + 7], b));
     }
 }
 
-template <int OUT>
-__device__ __forceinline__ void stage_get(uint8_t *stage, int lane, float (&x)[32])
-{
-    if constexpr (OUT == kOutF32) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint4 v = *stage_piece<4>(stage, lane, j);
-            x[4 * j] = __uint_as_float(v.x);
-            x[4 * j + 1] = __uint_as_float(v.y);
-            x[4 * j + 2] = __uint_as_float(v.z);
-            x[4 * j + 3] = __uint_as_float(v.w);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint4 v = *stage_piece<2>(stage, lane, j);
-            unpack16<OUT == kOutBF16>(v, *reinterpret_cast<float (*)[8]>(x + 8 * j));
-        }
-    }
-}
-
-// A warp's block of a row-major matrix of ES-byte elements: `at` is this lane's first piece
-// (row lane / pieces, piece lane % pieces), `step` the bytes to its next one.
+// A warp's block of a row-major matrix, 32 rows x 64 bytes: `at` is this lane's first piece
+// (row lane / 4, piece lane % 4), `step` the bytes to its next one, 8 rows on.
 template <int ES>
 struct WarpBlock {
-    static constexpr int kPieces = 2 * ES, kRows = 32 / kPieces, kElems = 16 / ES;
+    static constexpr int kElems = 16 / ES;
     uint8_t *at;
     int64_t step;
 
     __device__ __forceinline__ WarpBlock(const void *base, int64_t ld, int64_t row0, int64_t col, int lane)
     {
         at = static_cast<uint8_t *>(const_cast<void *>(base)) +
-             ((row0 + lane / kPieces) * ld + col + lane % kPieces * kElems) * ES;
-        step = kRows * ld * ES;
+             ((row0 + lane / 4) * ld + col + lane % 4 * kElems) * ES;
+        step = 8 * ld * ES;
     }
 };
 
@@ -392,20 +369,20 @@ template <int ES>
 __device__ __forceinline__ void stage_flush(uint8_t *stage, int lane, WarpBlock<ES> m, int nrow, int ncol)
 {
     using M = WarpBlock<ES>;
-    const int row = lane / M::kPieces, piece = lane % M::kPieces;
-    if (nrow >= 32 && ncol >= 32) {
+    const int row = lane / 4, piece = lane % 4;
+    if (nrow >= 32 && ncol >= 4 * M::kElems) {
 #pragma unroll
-        for (int i = 0; i < M::kPieces; ++i) {
-            *reinterpret_cast<uint4 *>(m.at) = *stage_piece<ES>(stage, i * M::kRows + row, piece);
+        for (int i = 0; i < 4; ++i) {
+            *reinterpret_cast<uint4 *>(m.at) = *stage_piece(stage, i * 8 + row, piece);
             m.at += m.step;
         }
         return;
     }
 #pragma unroll 1
-    for (int i = 0; i < M::kPieces; ++i, m.at += m.step) {
-        if (i * M::kRows + row >= nrow)
+    for (int i = 0; i < 4; ++i, m.at += m.step) {
+        if (i * 8 + row >= nrow)
             break;
-        const uint8_t *v = reinterpret_cast<const uint8_t *>(stage_piece<ES>(stage, i * M::kRows + row, piece));
+        const uint8_t *v = reinterpret_cast<const uint8_t *>(stage_piece(stage, i * 8 + row, piece));
         const int n = ncol - piece * M::kElems;
         if (n >= M::kElems) {
             *reinterpret_cast<uint4 *>(m.at) = *reinterpret_cast<const uint4 *>(v);
@@ -421,17 +398,29 @@ __device__ __forceinline__ void stage_flush(uint8_t *stage, int lane, WarpBlock<
     }
 }
 
-// A block that is not whole from memory to the staging area (what lies outside stays as it was).
+// A block from memory to the staging area, whole (asynchronously; stage_filled waits) or in
+// part (what lies outside stays as it was).
 template <int ES>
-__device__ __forceinline__ void stage_fill_part(uint8_t *stage, int lane, WarpBlock<ES> m, int nrow, int ncol)
+__device__ __forceinline__ void stage_fill(uint8_t *stage, int lane, WarpBlock<ES> m, int nrow, int ncol)
 {
     using M = WarpBlock<ES>;
-    const int row = lane / M::kPieces, piece = lane % M::kPieces;
+    const int row = lane / 4, piece = lane % 4;
+    if (nrow >= 32 && ncol >= 4 * M::kElems) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             smem_u32(stage_piece(stage, i * 8 + row, piece))),
+                         "l"(m.at)
+                         : "memory");
+            m.at += m.step;
+        }
+        return;
+    }
 #pragma unroll 1
-    for (int i = 0; i < M::kPieces; ++i, m.at += m.step) {
-        if (i * M::kRows + row >= nrow)
+    for (int i = 0; i < 4; ++i, m.at += m.step) {
+        if (i * 8 + row >= nrow)
             break;
-        uint8_t *v = reinterpret_cast<uint8_t *>(stage_piece<ES>(stage, i * M::kRows + row, piece));
+        uint8_t *v = reinterpret_cast<uint8_t *>(stage_piece(stage, i * 8 + row, piece));
         const int n = ncol - piece * M::kElems;
 #pragma unroll 1
         for (int j = 0; j < n && j < M::kElems; ++j) {
@@ -439,6 +428,37 @@ __device__ __forceinline__ void stage_fill_part(uint8_t *stage, int lane, WarpBl
                 reinterpret_cast<uint32_t *>(v)[j] = reinterpret_cast<const uint32_t *>(m.at)[j];
             else
                 reinterpret_cast<uint16_t *>(v)[j] = reinterpret_cast<const uint16_t *>(m.at)[j];
+        }
+    }
+}
+__device__ __forceinline__ void stage_filled()
+{
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+}
+
+// x = beta * (this lane's staged row) + x.
+template <int OUT, int kN>
+__device__ __forceinline__ void stage_add(uint8_t *stage, int lane, float beta, float *x)
+{
+    const F2 s = f2(beta);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint4 v = *stage_piece(stage, lane, j);
+        constexpr int kE = kN / 4;
+        float r[8];
+        if constexpr (OUT == kOutF32) {
+            r[0] = __uint_as_float(v.x);
+            r[1] = __uint_as_float(v.y);
+            r[2] = __uint_as_float(v.z);
+            r[3] = __uint_as_float(v.w);
+        } else {
+            unpack16<OUT == kOutBF16>(v, r);
+        }
+#pragma unroll
+        for (int i = 0; i < kE; i += 2) {
+            float *y = x + kE * j + i;
+            split2(fma2(s, f2(r[i], r[i + 1]), f2(y[0], y[1])), y[0], y[1]);
         }
     }
 }
@@ -476,58 +496,44 @@ template <int OUT>
 __device__ __forceinline__ void finish_wide(const LmArgs &p, float (&z)[32], const LmUnit &w, int row0,
                                             int col, uint8_t *stage, int lane)
 {
-    constexpr int ES = OUT == kOutF32 ? 4 : 2;
+    constexpr int ES = OUT == kOutF32 ? 4 : 2, kN = 64 / ES;
     const int nrow = w.row_end - row0, ncol = w.col_end - col;
-    const bool whole = nrow >= 32 && ncol >= 32;
     if (w.g < 0) {                             // tokens of no group
 #pragma unroll
         for (int j = 0; j < 32; ++j)
             z[j] = 0.0f;
     }
-    uint4 c[2 * ES];
-    const bool add = p.C && w.g >= 0;
-    if (add && whole) {
-        WarpBlock<ES> m(p.C, p.ldc, row0, col, lane);
-#pragma unroll
-        for (int i = 0; i < 2 * ES; ++i) {
-            c[i] = *reinterpret_cast<const uint4 *>(m.at);
-            m.at += m.step;
-        }
-    }
     if (p.Z) {
         if (p.in_bf16)
-            stage_put<kOutBF16>(stage, lane, z);
+            stage_put<kOutBF16, 32>(stage, lane, z);
         else
-            stage_put<kOutF16>(stage, lane, z);
+            stage_put<kOutF16, 32>(stage, lane, z);
         __syncwarp();
         stage_flush<2>(stage, lane, WarpBlock<2>(p.Z, p.ldz, row0, col, lane), nrow, ncol);
         __syncwarp();
     }
+    const bool add = p.C && w.g >= 0;
+    if (add)                                   // on its way during the activation
+        stage_fill<ES>(stage, lane, WarpBlock<ES>(p.C, p.ldc, row0, col, lane), nrow, ncol);
     if (w.g >= 0)
         apply_act(p.act, z);
-    if (add) {
-        constexpr int kPieces = 2 * ES, kRows = 32 / kPieces;
-        if (whole) {
+    uint8_t *d = static_cast<uint8_t *>(p.D) + (p.ragged_k ? w.g * p.strideD * ES : 0);
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i)
-                *stage_piece<ES>(stage, i * kRows + lane / kPieces, lane % kPieces) = c[i];
-        } else {
-            stage_fill_part<ES>(stage, lane, WarpBlock<ES>(p.C, p.ldc, row0, col, lane), nrow, ncol);
+    for (int h = 0; h < 32; h += kN) {
+        if (h > 0 && ncol <= h)
+            break;
+        if (add) {
+            if (h > 0)
+                stage_fill<ES>(stage, lane, WarpBlock<ES>(p.C, p.ldc, row0, col + h, lane), nrow, ncol - h);
+            stage_filled();
+            stage_add<OUT, kN>(stage, lane, p.beta, z + h);
+            __syncwarp();
         }
+        stage_put<OUT, kN>(stage, lane, z + h);
         __syncwarp();
-        float r[32];
-        stage_get<OUT>(stage, lane, r);
-        const F2 beta = f2(p.beta);
-#pragma unroll
-        for (int j = 0; j < 32; j += 2)
-            split2(fma2(beta, f2(r[j], r[j + 1]), f2(z[j], z[j + 1])), z[j], z[j + 1]);
+        stage_flush<ES>(stage, lane, WarpBlock<ES>(d, p.ldd, row0, col + h, lane), nrow, ncol - h);
         __syncwarp();
     }
-    stage_put<OUT>(stage, lane, z);
-    __syncwarp();
-    uint8_t *d = static_cast<uint8_t *>(p.D) + (p.ragged_k ? w.g * p.strideD * ES : 0);
-    stage_flush<ES>(stage, lane, WarpBlock<ES>(d, p.ldd, row0, col, lane), nrow, ncol);
-    __syncwarp();
 }
 
 // Wait for this thread's TMEM loads; v is not to be touched before.
@@ -541,11 +547,16 @@ __device__ __forceinline__ void tmem_ld_done(uint32_t (&v)[N])
 }
 
 // ---------------------------------------------------------------------------- the kernel
+__host__ __device__ constexpr bool lm_wide(int epi)
+{
+    return epi == kEpiWide || epi == kEpiXentStats || epi == kEpiXentGrad;
+}
+
 template <int EPI, int OUT, int BN, bool RK>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
     tcg_lm_kernel(const __grid_constant__ LmMaps maps, const LmArgs p)
 {
-    constexpr bool WIDE = EPI == kEpiWide || EPI == kEpiXentStats || EPI == kEpiXentGrad;
+    constexpr bool WIDE = lm_wide(EPI);
     using Cfg = LmCfg<BN, WIDE>;
     constexpr int kStages = Cfg::kStages;
     constexpr int kAccBufs = Cfg::kAccBufs;
@@ -581,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int a = 0; a < kAccBufs; ++a) {
             mbar_init(smem_u32(&ctl->acc_full[a]), 1);
-            mbar_init(smem_u32(&ctl->acc_empty[a]), kEpiWarps * 2);
+            mbar_init(smem_u32(&ctl->acc_empty[a]), Cfg::kEpi * 2);
         }
         mbar_init(smem_u32(&ctl->drain), 1);
         ctl->abort_flag = 0;
@@ -710,12 +721,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t a_desc0 = smem_desc_sw128(a_smem, a_lbo, a_sbo);
             const uint64_t b_desc0 = smem_desc_sw128(b_smem, b_lbo, b_sbo);
             Walk walk(pair, pairs);
-            LmUnit w;
+            LmUnit w, next_w;
             int stage = 0;
             uint32_t phase = 0;
             int it = 0;
             bool ok = true;
-            while (ok && walk.next(p, ctl, w)) {
+            bool more = walk.next(p, ctl, w);
+            while (ok && more) {
+                bool looked = false;                       // the next unit is known
                 int kb = w.kb0;
                 do {                                       // one accumulator per segment
                     const int acc = it % kAccBufs;
@@ -742,6 +755,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mma_f16_pair(d_tmem, ad_s + a_off[kk], bd_s + b_off[kk], p.idesc,
                                          (kb > first || kk > 0) ? 1u : 0u);
                         mma_commit_pair_mc(smem_u32(&ctl->empty[stage]), 0x3);
+                        if (!looked) {                     // while the tensor core is busy
+                            more = walk.next(p, ctl, next_w);
+                            looked = true;
+                        }
                         if (++stage == kStages) {
                             stage = 0;
                             phase ^= 1u;
@@ -751,24 +768,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     mma_commit_pair_mc(smem_u32(&ctl->acc_full[acc]), 0x3);
                 } while (kb < w.kb1);
+                if (!looked)
+                    more = walk.next(p, ctl, next_w);
+                w = next_w;
             }
             mma_commit_pair(smem_u32(&ctl->drain));
             wait_bounded<2>(smem_u32(&ctl->drain), 0, ctl, p, kErrDrain, false);
         }
     } else {
         // -------------------------------------------------------------- epilogue
-        // Two halves of 4 warps; half h owns columns [h BN/2, (h + 1) BN/2) of each tile
-        // for the CTA's 128 rows (warp w reads TMEM lane quarter w % 4).
-        constexpr int kHalf = BN / 2;
+        // Parts of 4 warps; part h owns columns [h kPart, (h + 1) kPart) of each tile for the
+        // CTA's 128 rows (warp w reads TMEM lane quarter w % 4).
+        constexpr int kParts = Cfg::kParts;
+        constexpr int kPart = BN / kParts;
         const int q = warp & 3;
-        const int half = (warp - 2) >> 2;
-        const bool half_leader = (warp == 2 + 4 * half) && lane == 0;
-        const uint32_t bar_id = 1u + static_cast<uint32_t>(half);
+        const int part = (warp - 2) >> 2;
+        const bool part_leader = (warp == 2 + 4 * part) && lane == 0;
+        const uint32_t bar_id = 1u + static_cast<uint32_t>(part);
         const int rl = q * 32 + lane;
-        const uint32_t tmem_half = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                                   static_cast<uint32_t>(half * kHalf);
+        const uint32_t tmem_part = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                   static_cast<uint32_t>(part * kPart);
         const float alpha = p.alpha * (p.alpha_dev ? *p.alpha_dev : 1.0f);
-        uint8_t *stage = base_ptr + kLmDataBytes - kEpiWarps * kLmStageBytes + (warp - 2) * kLmStageBytes;
+        uint8_t *stage = base_ptr + kLmDataBytes - Cfg::kEpi * kLmStageBytes + (warp - 2) * kLmStageBytes;
         Walk walk(pair, pairs);
         LmUnit w{};
         int it = 0;
@@ -790,43 +811,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&ctl->acc_empty[it % kAccBufs]), 0));
             ++it;
         };
-        // A cut tile's piece is stored: whoever stores the last one of a tile half adds them
+        // A cut tile's piece is stored: whoever stores the last one of a tile part adds them
         // all, in K order whatever the timing, and finishes the tile.
         auto arrive = [&]() {
             __threadfence();
             named_barrier_sync(bar_id, 128);
-            if (half_leader) {
-                uint32_t *cnt = p.cnt + (w.counter * 2 + static_cast<int>(rank)) * 2 + half;
+            if (part_leader) {
+                uint32_t *cnt = p.cnt + (w.counter * 2 + static_cast<int>(rank)) * kParts + part;
                 const bool last = atomicAdd(cnt, 1u) == static_cast<uint32_t>(w.pieces - 1);
                 if (last)
                     *cnt = 0u;                             // every piece has arrived
-                ctl->last_arrival[half] = last;
+                ctl->last_arrival[part] = last;
                 __threadfence();
             }
             named_barrier_sync(bar_id, 128);
-            const bool last = ctl->last_arrival[half] != 0;
+            const bool last = ctl->last_arrival[part] != 0;
             named_barrier_sync(bar_id, 128);               // the flag is free again
             if (last)
                 __threadfence();
             return last;
         };
         auto slot_ptr = [&](int slot) {
-            return p.part + ((static_cast<int64_t>(slot) * 2 + rank) * 2 + half) * (kHalf * kBM);
+            return p.part + ((static_cast<int64_t>(slot) * 2 + rank) * kParts + part) * (kPart * kBM);
         };
         auto piece_slot = [&](int i) { return 2 * (w.first_pair + i) + (i == 0 ? 1 : 0); };
 
         while (walk.next(p, ctl, w)) {
             const int row = w.row0 + static_cast<int>(rank) * kBM + rl;
-            const int col_half = w.col0 + half * kHalf;
+            const int col_part = w.col0 + part * kPart;
             const bool cut = w.slot >= 0;
             const bool empty_k = w.kb0 >= w.kb1;
             const int segments = SEG ? (w.kb1 - w.kb0 + kSegBlocks - 1) / kSegBlocks : 1;
             if constexpr (EPI == kEpiNarrow || EPI == kEpiXentNarrow) {
                 // ------------------------------------------------ tokens on the columns
-                constexpr int kCols = kHalf < 32 ? kHalf : 32;
-                float sum[kHalf];
+                constexpr int kCols = kPart < 32 ? kPart : 32;
+                float sum[kPart];
 #pragma unroll
-                for (int j = 0; j < kHalf; ++j)
+                for (int j = 0; j < kPart; ++j)
                     sum[j] = 0.0f;
                 float bias = 0.0f;
                 if (EPI == kEpiNarrow && p.bias && row < p.rows && w.g >= 0) {
@@ -841,59 +862,59 @@ __global__ void __launch_bounds__(kThreads, 1)
                         stop = true;
                         break;
                     }
-                    uint32_t v[kHalf];
-                    const uint32_t taddr = tmem_half + static_cast<uint32_t>(it % kAccBufs * BN);
-                    if constexpr (kHalf == 16) {
+                    uint32_t v[kPart];
+                    const uint32_t taddr = tmem_part + static_cast<uint32_t>(it % kAccBufs * BN);
+                    if constexpr (kPart == 16) {
                         tmem_ld_32x32b_x16(taddr, v);
                     } else {
 #pragma unroll
-                        for (int c = 0; c < kHalf; c += 32)
+                        for (int c = 0; c < kPart; c += 32)
                             tmem_ld_32x32b_x32(taddr + c, *reinterpret_cast<uint32_t (*)[32]>(v + c));
                     }
                     tmem_ld_done(v);
                     release();
                     if (!empty_k) {
 #pragma unroll
-                        for (int j = 0; j < kHalf; ++j)
+                        for (int j = 0; j < kPart; ++j)
                             sum[j] += __uint_as_float(v[j]);
                     }
                 } while (++seg < segments);
                 if (stop)
                     break;
-                const int ncol = w.col_end - col_half;
+                const int ncol = w.col_end - col_part;
                 if (cut) {
                     float *sl = slot_ptr(w.slot) + rl;     // [column][row]
 #pragma unroll
-                    for (int j = 0; j < kHalf; ++j)
+                    for (int j = 0; j < kPart; ++j)
                         if (j < ncol)
                             __stcg(sl + j * kBM, sum[j]);
                     if (!arrive())
                         continue;
 #pragma unroll
-                    for (int j = 0; j < kHalf; ++j)
+                    for (int j = 0; j < kPart; ++j)
                         sum[j] = 0.0f;
 #pragma unroll 4
                     for (int i = 0; i < w.pieces; ++i) {
                         const float *s = slot_ptr(piece_slot(i)) + rl;
 #pragma unroll
-                        for (int j = 0; j < kHalf; ++j)
+                        for (int j = 0; j < kPart; ++j)
                             if (j < ncol)
                                 sum[j] += __ldcg(s + j * kBM);
                     }
                 }
                 if constexpr (EPI == kEpiNarrow) {
 #pragma unroll
-                    for (int c = 0; c < kHalf; c += kCols)
+                    for (int c = 0; c < kPart; c += kCols)
                         finish_narrow<OUT>(p, *reinterpret_cast<float (*)[kCols]>(sum + c), w, row,
-                                           col_half + c, alpha, bias);
+                                           col_part + c, alpha, bias);
                 } else {
                     // a warp's 32 vocabulary entries, one token (column) after the other
                     const int slot = (w.row0 >> 8) * 8 + static_cast<int>(rank) * 4 + q;
 #pragma unroll
-                    for (int j = 0; j < kHalf; ++j) {
+                    for (int j = 0; j < kPart; ++j) {
                         if (j >= ncol)
                             break;
-                        const int tok = col_half + j;
+                        const int tok = col_part + j;
                         const int64_t t = p.targets[tok];
                         const float v = row < p.rows ? sum[j] : -INFINITY;
                         if (t == row && t != p.ignore && row < p.rows)
@@ -913,17 +934,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else if constexpr (EPI == kEpiWide) {
                 // --------------------------------------------------- tokens on the rows
-                constexpr int kChunks = kHalf / 32;
+                constexpr int kChunks = kPart / 32;
                 if (!acquire())
                     break;
-                const uint32_t taddr = tmem_half + static_cast<uint32_t>(it % kAccBufs * BN);
+                const uint32_t taddr = tmem_part + static_cast<uint32_t>(it % kAccBufs * BN);
                 float *sl = cut ? slot_ptr(w.slot) + rl : nullptr;       // [column][row]
                 uint32_t v[32];
                 __syncwarp();
                 tmem_ld_32x32b_x32(taddr, v);
 #pragma unroll 1
                 for (int c = 0; c < kChunks; ++c) {
-                    const int col = col_half + c * 32;
+                    const int col = col_part + c * 32;
                     const bool inside = row - lane < w.row_end && col < w.col_end;
                     float z[32];
                     tmem_ld_done(v);
@@ -951,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (cut && arrive() && row - lane < w.row_end) {
 #pragma unroll 1
                     for (int c = 0; c < kChunks; ++c) {
-                        const int col = col_half + c * 32;
+                        const int col = col_part + c * 32;
                         if (col >= w.col_end)
                             break;
                         float z[32];
@@ -988,9 +1009,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if constexpr (EPI == kEpiXentStats) {
-                    float sum[kHalf];
+                    float sum[kPart];
 #pragma unroll
-                    for (int j = 0; j < kHalf; ++j)
+                    for (int j = 0; j < kPart; ++j)
                         sum[j] = 0.0f;
                     bool stop = false;
                     for (int seg = 0; seg < segments; ++seg) {
@@ -998,18 +1019,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                             stop = true;
                             break;
                         }
-                        const uint32_t taddr = tmem_half + static_cast<uint32_t>(it % kAccBufs * BN);
+                        const uint32_t taddr = tmem_part + static_cast<uint32_t>(it % kAccBufs * BN);
                         uint32_t va[16], vb[16];
                         tmem_ld_32x32b_x16(taddr, va);
 #pragma unroll
-                        for (int c = 0; c < kHalf; c += 32) {
+                        for (int c = 0; c < kPart; c += 32) {
                             tmem_ld_done(va);
                             tmem_ld_32x32b_x16(taddr + c + 16, vb);
 #pragma unroll
                             for (int j = 0; j < 16; ++j)
                                 sum[c + j] += __uint_as_float(va[j]);
                             tmem_ld_done(vb);
-                            if (c + 32 < kHalf)
+                            if (c + 32 < kPart)
                                 tmem_ld_32x32b_x16(taddr + c + 32, va);
 #pragma unroll
                             for (int j = 0; j < 16; ++j)
@@ -1019,47 +1040,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (stop)
                         break;
-                    const int ncol = w.col_end - col_half;
-                    if (ncol < kHalf) {
+                    const int ncol = w.col_end - col_part;
+                    if (ncol < kPart) {
 #pragma unroll
-                        for (int j = 0; j < kHalf; ++j)
+                        for (int j = 0; j < kPart; ++j)
                             if (j >= ncol)
                                 sum[j] = -INFINITY;
                     }
-                    if (target >= col_half && target < col_half + kHalf) {
+                    if (target >= col_part && target < col_part + kPart) {
                         float tl = 0.0f;
 #pragma unroll
-                        for (int j = 0; j < kHalf; ++j)    // by predicate: the sums stay in registers
+                        for (int j = 0; j < kPart; ++j)    // by predicate: the sums stay in registers
                             asm("{\n\t.reg .pred q;\n\tsetp.eq.s32 q, %1, %2;\n\t"
                                 "@q mov.f32 %0, %3;\n\t}"
                                 : "+f"(tl)
-                                : "r"(target - col_half), "r"(j), "f"(sum[j]));
+                                : "r"(target - col_part), "r"(j), "f"(sum[j]));
                         p.target_logit[row] = tl;
                     }
                     float mx = -INFINITY;
 #pragma unroll
-                    for (int j = 0; j < kHalf; ++j)
+                    for (int j = 0; j < kPart; ++j)
                         mx = fmaxf(mx, sum[j]);
                     // a maximum of -inf (nothing but -inf) subtracts as zero
                     const float sub = mx == -INFINITY ? 0.0f : mx * kLog2e;
                     float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int j = 0; j < kHalf; ++j)
+                    for (int j = 0; j < kPart; ++j)
                         add[j & 3] += exp2_fast(fmaf(sum[j], kLog2e, -sub));
                     if (row_ok)
-                        p.stats[static_cast<int64_t>(w.col0 / BN * 2 + half) * p.tokens + row] =
+                        p.stats[static_cast<int64_t>(w.col0 / BN * kParts + part) * p.tokens + row] =
                             make_float2(mx, (add[0] + add[1]) + (add[2] + add[3]));
                 } else {
                     if (!acquire())
                         break;
-                    const uint32_t taddr = tmem_half + static_cast<uint32_t>(it % kAccBufs * BN);
-                    constexpr int kChunks = kHalf / 32;
+                    const uint32_t taddr = tmem_part + static_cast<uint32_t>(it % kAccBufs * BN);
+                    constexpr int kChunks = kPart / 32;
                     uint32_t v[32];
                     __syncwarp();
                     tmem_ld_32x32b_x32(taddr, v);
 #pragma unroll 1
                     for (int c = 0; c < kChunks; ++c) {
-                        const int col = col_half + c * 32;
+                        const int col = col_part + c * 32;
                         float g[32];
                         tmem_ld_done(v);
                         const F2 l2e = f2(kLog2e), sub = f2(-row_lse2), scale = f2(row_g);
@@ -1089,9 +1110,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             release();
                         if (col < w.col_end && row - lane < w.row_end) {
                             if (p.in_bf16)
-                                stage_put<kOutBF16>(stage, lane, g);
+                                stage_put<kOutBF16, 32>(stage, lane, g);
                             else
-                                stage_put<kOutF16>(stage, lane, g);
+                                stage_put<kOutF16, 32>(stage, lane, g);
                             __syncwarp();
                             stage_flush<2>(stage, lane, WarpBlock<2>(p.D, p.ldd, row - lane, col, lane),
                                            w.row_end - (row - lane), w.col_end - col);
@@ -1405,6 +1426,11 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace
 
+static int lm_threads(int epi, int bn)
+{
+    return lm_wide(epi) && bn == 256 ? LmCfg<256, true>::kThreadsLm : LmCfg<128, true>::kThreadsLm;
+}
+
 cudaError_t launch_lm(const LmMaps &maps, const LmArgs &a, int epi, int out_kind, int bn, int grid,
                       cudaStream_t s)
 {
@@ -1416,7 +1442,7 @@ cudaError_t launch_lm(const LmMaps &maps, const LmArgs &a, int epi, int out_kind
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(lm_threads(epi, bn), 1, 1);
     cfg.dynamicSmemBytes = kLmSmemBytes;
     cfg.stream = s;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1440,7 +1466,7 @@ int lm_max_resident_ctas(int num_sms)
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3(num_sms / 2 * 2, 1, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3(LmCfg<256, true>::kThreadsLm, 1, 1);
     cfg.dynamicSmemBytes = kLmSmemBytes;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;

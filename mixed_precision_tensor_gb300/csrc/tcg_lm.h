@@ -13,12 +13,12 @@
 namespace tcg {
 
 constexpr int kLmMaxGroups = 384;      // experts of one grouped call (a table in shared memory)
-constexpr int kLmCounters = 1024;      // split counters of a handle: 4 per cut tile
+constexpr int kLmCounters = 1024;      // split counters of a handle: up to 8 per cut tile
 constexpr int kLmMaxStages = 12;
-// Shared memory: the operand ring, and (tokens on the rows) 4 KiB of staging per epilogue
-// warp, through which a warp's 32 rows leave and arrive in runs of 64 or 128 bytes.
+// Shared memory: the operand ring, and (tokens on the rows) 2 KiB of staging per epilogue
+// warp, through which a warp's 32 rows leave and arrive in runs of 64 bytes.
 constexpr int kLmDataBytes = 224 * 1024;
-constexpr int kLmStageBytes = 4 * 1024;
+constexpr int kLmStageBytes = 2 * 1024;
 
 // What the epilogue of the product kernel does with an accumulator (see tcg_lm.cu).
 enum LmEpi {
@@ -83,13 +83,19 @@ struct LmArgs {
 
 template <int BN, bool WIDE>
 struct LmCfg {
-    static constexpr int kRingBytes = kLmDataBytes - (WIDE ? kEpiWarps * kLmStageBytes : 0);
+    // Epilogue warps.  Two per SM sub-partition, with registers for 32 columns under way and
+    // 32 in hand each; four with half the registers were slower (16 weight gradients of
+    // 2048 x 2048 over 512 tokens each: 82 against 58 us).
+    static constexpr int kEpi = 8;
+    static constexpr int kParts = kEpi / 4;                  // column ranges of a tile
+    static constexpr int kThreadsLm = 64 + 32 * kEpi;
+    static constexpr int kRingBytes = kLmDataBytes - (WIDE ? kEpi * kLmStageBytes : 0);
     static constexpr int kBRows = BN / 2;                    // B rows per CTA of the pair
     static constexpr int kAStage = kABytes;                  // 16 KiB
     static constexpr int kBStage = kBRows * kRowBytes;
     static constexpr int kStageBytes = kAStage + kBStage;
     static constexpr int kFit = kRingBytes / kStageBytes;
-    // wide 256, 128, 64: 6, 8, 9; narrow 128, 64, 32: 9, 11, 12
+    // wide 256, 128, 64: 6, 8, 10; narrow 128, 64, 32: 9, 11, 12
     static constexpr int kStages = kFit < kLmMaxStages ? kFit : kLmMaxStages;
     static constexpr int kAccBufs = kTmemCols / BN < 4 ? kTmemCols / BN : 4;
 };
@@ -100,10 +106,10 @@ inline size_t lm_part_bytes(int pairs, int bn)
     return static_cast<size_t>(pairs) * 2 * 2 * kBM * bn * sizeof(float);
 }
 
-// Slots of the cross entropy's statistics: per 256 (wide) or 32 (narrow) vocabulary entries.
+// Slots of the cross entropy's statistics: per tile part (wide) or 32 vocabulary entries (narrow).
 inline int64_t lm_stat_slots(int64_t vocab, bool narrow)
 {
-    return narrow ? (vocab + 255) / 256 * 8 : (vocab + 255) / 256 * 2;
+    return (vocab + 255) / 256 * (narrow ? 8 : LmCfg<256, true>::kParts);
 }
 
 // K-ragged calls load the last tokens of a group with boxes of 16, 4 and 1 tokens, and

@@ -295,9 +295,10 @@ __device__ __forceinline__ void finish_narrow(const LmArgs &p, float (&z)[kCols]
             }
         return;
     }
+    const F2 a = f2(alpha), b = f2(bias);
 #pragma unroll
-    for (int j = 0; j < kCols; ++j)
-        z[j] = fmaf(alpha, z[j], bias);
+    for (int j = 0; j < kCols; j += 2)
+        split2(fma2(a, f2(z[j], z[j + 1]), b), z[j], z[j + 1]);
     if (p.Z) {
 #pragma unroll
         for (int j = 0; j < kCols; ++j)
@@ -566,7 +567,14 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
     // standard deviations of logits it moved the loss by 2e-6 of itself).  Where results
     // are FP32 statistics, or the accumulators few, K goes in segments of 512: each starts a
     // new accumulator, and the epilogue adds the segments in registers, rounding to nearest.
-    constexpr bool SEG = EPI != kEpiWide && EPI != kEpiXentGrad;
+    constexpr bool SEG = EPI != kEpiWide && EPI != kEpiXentGrad && !(EPI == kEpiNarrow && BN == 256);
+    // Narrow tiles of 256 tokens: a group's last tile is multiplied at the width it has, in
+    // steps of 32 tokens (tensor time follows N), so that a group of any size wastes 16
+    // tokens of work on average.
+    constexpr bool FIT = EPI == kEpiNarrow && BN == 256;
+    auto width = [](const LmUnit &w) {
+        return FIT ? min(BN, (w.col_end - w.col0 + 31) & ~31) : BN;
+    };
     constexpr int kSegBlocks = SEG ? 8 : 1 << 30;
     using Walk = LmWalk<WIDE, BN, RK>;
 
@@ -641,7 +649,7 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
             bool ok = true;
             while (ok && walk.next(p, ctl, w)) {
                 const int m0 = w.row0 + static_cast<int>(rank) * kBM;
-                const int n0 = w.col0 + static_cast<int>(rank) * kBRows;
+                const int n0 = w.col0 + static_cast<int>(rank) * (width(w) / 2);
                 const int za = WIDE ? 0 : w.g, zb = WIDE && !RK ? w.g : 0;
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
                     const uint32_t fb_local = smem_u32(&ctl->full[stage]);
@@ -741,6 +749,9 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                     }
                     tc_fence_after();
                     const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+                    const uint32_t idesc = FIT ? (p.idesc & ~(0x3Fu << 17)) |
+                                                     (static_cast<uint32_t>(width(w) >> 3) << 17)
+                                               : p.idesc;
                     const int first = kb, stop = SEG ? min(kb + kSegBlocks, w.kb1) : w.kb1;
                     for (; kb < stop; ++kb) {
                         if (!wait_bounded<2>(smem_u32(&ctl->full[stage]), phase, ctl, p, kErrMmaFull)) {
@@ -752,7 +763,7 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                         const uint64_t bd_s = b_desc0 + ((static_cast<uint32_t>(stage) * Cfg::kBStage) >> 4);
 #pragma unroll
                         for (int kk = 0; kk < kMmasPerStage; ++kk)
-                            mma_f16_pair(d_tmem, ad_s + a_off[kk], bd_s + b_off[kk], p.idesc,
+                            mma_f16_pair(d_tmem, ad_s + a_off[kk], bd_s + b_off[kk], idesc,
                                          (kb > first || kk > 0) ? 1u : 0u);
                         mma_commit_pair_mc(smem_u32(&ctl->empty[stage]), 0x3);
                         if (!looked) {                     // while the tensor core is busy
@@ -842,7 +853,41 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
             const bool cut = w.slot >= 0;
             const bool empty_k = w.kb0 >= w.kb1;
             const int segments = SEG ? (w.kb1 - w.kb0 + kSegBlocks - 1) / kSegBlocks : 1;
-            if constexpr (EPI == kEpiNarrow || EPI == kEpiXentNarrow) {
+            if constexpr (FIT) {
+                // --------------------------- tokens on the columns, many: the parts take
+                // every second 32 of them
+                float bias = 0.0f;
+                if (p.bias && row < p.rows && w.g >= 0) {
+                    const int64_t i = static_cast<int64_t>(w.g) * p.rows + row;
+                    bias = p.bias_f32 ? static_cast<const float *>(p.bias)[i]
+                                      : load16(p.bias, i, p.in_bf16);
+                }
+                if (!acquire())
+                    break;
+                const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                       static_cast<uint32_t>(it % kAccBufs * BN);
+                const int chunks = width(w) / 32;
+                uint32_t v[32];
+                __syncwarp();
+                if (part < chunks)
+                    tmem_ld_32x32b_x32(taddr + 32 * part, v);
+                else
+                    release();
+#pragma unroll 1
+                for (int c = part; c < chunks; c += kParts) {
+                    float z[32];
+                    tmem_ld_done(v);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        z[j] = empty_k ? 0.0f : __uint_as_float(v[j]);
+                    __syncwarp();
+                    if (c + kParts < chunks)
+                        tmem_ld_32x32b_x32(taddr + 32 * (c + kParts), v);
+                    else
+                        release();
+                    finish_narrow<OUT, 32>(p, z, w, row, w.col0 + c * 32, alpha, bias);
+                }
+            } else if constexpr (EPI == kEpiNarrow || EPI == kEpiXentNarrow) {
                 // ------------------------------------------------ tokens on the columns
                 constexpr int kCols = kPart < 32 ? kPart : 32;
                 float sum[kPart];
@@ -1155,7 +1200,8 @@ LmKernelFn linear_fn(int epi, int bn, bool rk)
     if (epi == kEpiNarrow)
         return bn == 32 ? tcg_lm_kernel<kEpiNarrow, OUT, 32, false>
              : bn == 64 ? tcg_lm_kernel<kEpiNarrow, OUT, 64, false>
-                        : tcg_lm_kernel<kEpiNarrow, OUT, 128, false>;
+             : bn == 128 ? tcg_lm_kernel<kEpiNarrow, OUT, 128, false>
+                         : tcg_lm_kernel<kEpiNarrow, OUT, 256, false>;
     return bn == 64 ? tcg_lm_kernel<kEpiWide, OUT, 64, false>
          : bn == 128 ? tcg_lm_kernel<kEpiWide, OUT, 128, false>
                      : tcg_lm_kernel<kEpiWide, OUT, 256, false>;

@@ -95,7 +95,7 @@ struct LmCfg {
     static constexpr int kBStage = kBRows * kRowBytes;
     static constexpr int kStageBytes = kAStage + kBStage;
     static constexpr int kFit = kRingBytes / kStageBytes;
-    // wide 256, 128, 64: 6, 8, 10; narrow 128, 64, 32: 9, 11, 12
+    // wide 256, 128, 64: 6, 8, 10; narrow 256, 128, 64, 32: 7, 9, 11, 12
     static constexpr int kStages = kFit < kLmMaxStages ? kFit : kLmMaxStages;
     static constexpr int kAccBufs = kTmemCols / BN < 4 ? kTmemCols / BN : 4;
 };
@@ -119,7 +119,7 @@ struct LmMaps {
     CUtensorMap A_tail[3], B_tail[3];      // boxes of 16, 4, 1 tokens (K ragged only)
 };
 
-// Launchers (tcg_lm.cu).  out_kind: type of D.  bn: 32, 64 or 128 (kEpiNarrow), 64, 128 or 256
+// Launchers (tcg_lm.cu).  out_kind: type of D.  bn: 32, 64, 128 or 256 (kEpiNarrow), 64, 128 or 256
 // (kEpiWide), 256 (K ragged, kEpiXentStats, kEpiXentGrad), 32 (kEpiXentNarrow).
 cudaError_t launch_lm(const LmMaps &maps, const LmArgs &a, int epi, int out_kind, int bn,
                       int grid, cudaStream_t s);

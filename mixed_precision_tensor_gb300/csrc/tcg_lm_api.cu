@@ -96,14 +96,19 @@ Shape shape_of(tcgContext *h, const Product &p)
         if (p.x_kmajor && per <= 128) {
             s.epi = kEpiNarrow;
             s.bn = per <= 32 ? 32 : (per <= 64 ? 64 : 128);
+        } else if (p.offsets && p.x_kmajor && per < 2048) {
+            // Groups' last tiles at the width that they have.
+            s.epi = kEpiNarrow;
+            s.bn = 256;
         } else {
             // Tokens on the rows: the tile width with the least predicted time, in the time of
-            // a K block at width 256 (narrower tiles load A as often for less work).
+            // a K block at width 256.  A block costs the 16 KiB of A and bn / 16 KiB of B that an
+            // SM loads for it, at 64 bytes a cycle: 512, 384 or 320 cycles.
             s.epi = kEpiWide;
             s.bn = 256;
             double best = 1e300;
             for (int bn = 256; bn >= (p.w_kmajor ? 64 : 128); bn /= 2) {
-                const double cost = bn == 256 ? 1.0 : (bn == 128 ? 0.55 : 0.35);
+                const double cost = bn == 256 ? 1.0 : (bn == 128 ? 0.75 : 0.625);
                 const int64_t tiles = max_tiles(p, s.epi, bn), rest = tiles % P;
                 int64_t share = ceil_div(rest * nkb, P);
                 share = share < kMinShare ? kMinShare : share;
@@ -123,7 +128,7 @@ Shape shape_of(tcgContext *h, const Product &p)
     s.share = kMinShare;
     s.gain = gain_of(s.bn);
     const bool linear = s.epi == kEpiNarrow || s.epi == kEpiWide || s.epi == kEpiXentNarrow;
-    s.cut = linear && !p.ragged_k && nkb - kMinShare >= s.gain &&
+    s.cut = linear && !p.ragged_k && !(s.epi == kEpiNarrow && s.bn == 256) && nkb - kMinShare >= s.gain &&
             (p.offsets || s.tiles % P != 0) && h->split_k != 1;
     int64_t pairs = s.tiles;
     if (s.cut)

@@ -35,6 +35,7 @@ struct LmPlan {
     int tiles;          // tiles of the groups
     int whole;          // tiles [0, whole) go whole, round robin; the rest are cut along K
     int share;          // K blocks of the cut tiles per pair
+    int splits;         // pairs per cut tile, ranges alike for all of them; 0: laid end to end
     int null_tiles[2];  // tiles of the columns (rows) before the first and after the last group
 };
 
@@ -79,17 +80,19 @@ struct LmUnit {
 // pair t mod P.  The tiles after them, fewer than P, would keep only some pairs busy: where
 // that costs more than joining partial sums, their K blocks are laid end to end and every
 // pair takes `share` of them -- a piece of one tile, or the end of one and the start of the
-// next (and whole tiles between).  A pair has at most one piece that starts inside a tile
+// next (and whole tiles between).  (Where the operands are larger than L2 and shared by
+// tiles, every cut tile instead gets the same number of pairs and the same K ranges, so that
+// tiles read the same blocks at the same time.)  A pair has at most one piece that starts inside a tile
 // (slot 2 c) and one that starts a tile without ending it (slot 2 c + 1).
 template <bool WIDE, int BN, bool RK>
 struct LmWalk {
     int c, P;
     int t, null_i;
-    int64_t pos;
+    uint32_t pos;                                   // next block of the cut tiles; ~0: not begun
     int group = 0, at = -1, begin = 0, end = 0;     // group of tile t; whose range is loaded
 
     __device__ __forceinline__ LmWalk(int pair, int pairs) : c(pair), P(pairs), t(pair),
-                                                             null_i(pair), pos(-1) {}
+                                                             null_i(pair), pos(~0u) {}
 
     __device__ __forceinline__ bool next(const LmArgs &p, const LmCtl *ctl, LmUnit &w)
     {
@@ -105,24 +108,40 @@ struct LmWalk {
         }
         const int cut = pl.tiles - pl.whole;
         if (cut > 0) {
-            const int64_t work = static_cast<int64_t>(cut) * p.num_k_blocks;
-            const int64_t stop = min(static_cast<int64_t>(c + 1) * pl.share, work);
-            if (pos < 0)
-                pos = static_cast<int>(min(static_cast<int64_t>(c) * pl.share, work));
-            if (pos < stop) {
-                const int r = static_cast<int>(pos / p.num_k_blocks);
-                const int64_t r0 = static_cast<int64_t>(r) * p.num_k_blocks;
-                w.kb0 = static_cast<int>(pos - r0);
-                w.kb1 = static_cast<int>(min(static_cast<int64_t>(p.num_k_blocks), w.kb0 + stop - pos));
-                pos += w.kb1 - w.kb0;
-                if (w.kb1 - w.kb0 < p.num_k_blocks) {
-                    w.slot = 2 * c + (w.kb0 == 0 ? 1 : 0);
-                    w.first_pair = static_cast<int>(r0 / pl.share);
-                    w.pieces = static_cast<int>((r0 + p.num_k_blocks - 1) / pl.share) - w.first_pair + 1;
-                    w.counter = r;
+            const uint32_t nkb = static_cast<uint32_t>(p.num_k_blocks);
+            const uint32_t share = static_cast<uint32_t>(pl.share), me = static_cast<uint32_t>(c);
+            if (pl.splits) {
+                const uint32_t r = me / pl.splits, piece = me - r * pl.splits;
+                if (pos == ~0u && r < static_cast<uint32_t>(cut)) {
+                    pos = 0;
+                    w.kb0 = static_cast<int>(piece * share);
+                    w.kb1 = static_cast<int>(min(nkb, (piece + 1) * share));
+                    w.slot = 2 * c + (piece == 0 ? 1 : 0);
+                    w.first_pair = static_cast<int>(r * pl.splits);
+                    w.pieces = pl.splits;
+                    w.counter = static_cast<int>(r);
+                    locate(p, ctl, pl.whole + static_cast<int>(r), w);
+                    return true;
                 }
-                locate(p, ctl, pl.whole + r, w);
-                return true;
+            } else {
+                const uint32_t work = static_cast<uint32_t>(cut) * nkb;
+                const uint32_t stop = min((me + 1) * share, work);
+                if (pos == ~0u)
+                    pos = min(me * share, work);
+                if (pos < stop) {
+                    const uint32_t r = pos / nkb, r0 = r * nkb;
+                    w.kb0 = static_cast<int>(pos - r0);
+                    w.kb1 = static_cast<int>(min(nkb, stop - r0));
+                    pos = r0 + static_cast<uint32_t>(w.kb1);
+                    if (w.kb1 - w.kb0 < p.num_k_blocks) {
+                        w.slot = 2 * c + (w.kb0 == 0 ? 1 : 0);
+                        w.first_pair = static_cast<int>(r0 / share);
+                        w.pieces = static_cast<int>((r0 + nkb - 1) / share) - w.first_pair + 1;
+                        w.counter = static_cast<int>(r);
+                    }
+                    locate(p, ctl, pl.whole + static_cast<int>(r), w);
+                    return true;
+                }
             }
         }
         const int nulls = pl.null_tiles[0] + pl.null_tiles[1];
@@ -241,15 +260,22 @@ __device__ __forceinline__ void make_plan(const LmArgs &p, LmCtl *ctl, int lane,
         LmPlan pl;
         pl.tiles = pl.whole = tiles;
         pl.share = 1;
+        pl.splits = 0;
         pl.null_tiles[0] = nulls[0];
         pl.null_tiles[1] = nulls[1];
         const int rest = tiles % pairs;
         if (!RK && p.part && rest > 0) {
-            const int64_t work = static_cast<int64_t>(rest) * p.num_k_blocks;
-            const int share = max(static_cast<int>((work + pairs - 1) / pairs), p.min_share);
+            const uint32_t nkb = static_cast<uint32_t>(p.num_k_blocks);
+            int splits = 0;
+            int share = max(static_cast<int>((rest * nkb + pairs - 1) / pairs), p.min_share);
+            if (p.align_splits) {
+                share = max(static_cast<int>((nkb + pairs / rest - 1) / (pairs / rest)), p.min_share);
+                splits = static_cast<int>((nkb + share - 1) / share);
+            }
             if (p.num_k_blocks - share >= p.split_gain) {
                 pl.whole = tiles - rest;
                 pl.share = share;
+                pl.splits = splits;
             }
         }
         ctl->plan = pl;
@@ -617,7 +643,11 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
     }
     if (threadIdx.x == 0)
         griddep_launch_dependents();
-    griddep_wait();
+    // The plan of a grouped call reads its offsets, which the kernel before may have written;
+    // others wait for that kernel only when their roles begin, the plan made and the first
+    // unit found.
+    if (p.offsets)
+        griddep_wait();
     if (warp == 2)
         make_plan<WIDE, BN, RK>(p, ctl, lane, pairs);
     tc_fence_before();
@@ -647,7 +677,10 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
             uint32_t phase = 0;
             bool skip_once = p.fault_inject != 0 && leader;
             bool ok = true;
-            while (ok && walk.next(p, ctl, w)) {
+            bool more = walk.next(p, ctl, w);
+            if (!p.offsets)
+                griddep_wait();
+            for (; ok && more; more = walk.next(p, ctl, w)) {
                 const int m0 = w.row0 + static_cast<int>(rank) * kBM;
                 const int n0 = w.col0 + static_cast<int>(rank) * (width(w) / 2);
                 const int za = WIDE ? 0 : w.g, zb = WIDE && !RK ? w.g : 0;
@@ -799,6 +832,8 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
         const int rl = q * 32 + lane;
         const uint32_t tmem_part = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(part * kPart);
+        if (!p.offsets)
+            griddep_wait();
         const float alpha = p.alpha * (p.alpha_dev ? *p.alpha_dev : 1.0f);
         uint8_t *stage = base_ptr + kLmDataBytes - Cfg::kEpi * kLmStageBytes + (warp - 2) * kLmStageBytes;
         Walk walk(pair, pairs);
@@ -1338,34 +1373,22 @@ __global__ void __launch_bounds__(256)
     const int left = m - row;                         // rows of this thread (8, or fewer at the end)
     const int c0 = blockIdx.y * chunk, c1 = min(c0 + chunk, cols);
 
-    auto load8 = [&](const uint16_t *src, float (&v)[8]) {
-        if (left >= 8) {
-            const uint4 q = *reinterpret_cast<const uint4 *>(src);
-            const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+    auto load8 = [&](const uint16_t *src) {
+        if (left >= 8)
+            return *reinterpret_cast<const uint4 *>(src);
+        uint32_t u[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (BF16) {
-                    v[2 * i] = __uint_as_float(u[i] << 16);
-                    v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-                } else {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&u[i]));
-                    v[2 * i] = f.x;
-                    v[2 * i + 1] = f.y;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = i < left ? load16(src, i, BF16) : 0.0f;
-        }
+        for (int i = 0; i < 8; ++i)
+            if (i < left)
+                u[i / 2] |= static_cast<uint32_t>(src[i]) << (16 * (i & 1));
+        return make_uint4(u[0], u[1], u[2], u[3]);
     };
     auto store8 = [&](uint16_t *dst, const float (&v)[8]) {
         if (left >= 8) {
             uint32_t u[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                u[i] = static_cast<uint32_t>(round16(v[2 * i], BF16)) |
-                       static_cast<uint32_t>(round16(v[2 * i + 1], BF16)) << 16;
+                u[i] = pack16(v[2 * i], v[2 * i + 1], BF16);
             *reinterpret_cast<uint4 *>(dst) = make_uint4(u[0], u[1], u[2], u[3]);
         } else {
 #pragma unroll
@@ -1405,22 +1428,39 @@ __global__ void __launch_bounds__(256)
             continue;
         float sum[8] = {};
         if (left > 0) {
-#pragma unroll 4
-            for (int c = b + w; c < e; c += 8) {
-                float d[8];
-                load8(dD + static_cast<int64_t>(c) * lddd + row, d);
-                if constexpr (ACT != kActNone) {
-                    float z[8];
-                    load8(Z + static_cast<int64_t>(c) * ldz + row, z);
+            // Four columns at a time, all their loads before the first store (dZ may be dD, so
+            // the compiler would not move a load up past a store).
+            for (int c = b + w; c < e; c += 32) {
+                uint4 rd[4], rz[4];
 #pragma unroll
-                    for (int i = 0; i < 8; i += 2)
-                        split2(f2(d[i], d[i + 1]) * act_slope<ACT>(f2(z[i], z[i + 1])), d[i], d[i + 1]);
+                for (int k = 0; k < 4; ++k) {
+                    const int64_t col = c + 8 * k;
+                    if (col < e) {
+                        rd[k] = load8(dD + col * lddd + row);
+                        if constexpr (ACT != kActNone)
+                            rz[k] = load8(Z + col * ldz + row);
+                    }
                 }
-                if (dZ)
-                    store8(dZ + static_cast<int64_t>(c) * lddz + row, d);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    sum[i] += d[i];
+                for (int k = 0; k < 4; ++k) {
+                    const int64_t col = c + 8 * k;
+                    if (col >= e)
+                        break;
+                    float d[8];
+                    unpack16<BF16>(rd[k], d);
+                    if constexpr (ACT != kActNone) {
+                        float z[8];
+                        unpack16<BF16>(rz[k], z);
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2)
+                            split2(f2(d[i], d[i + 1]) * act_slope<ACT>(f2(z[i], z[i + 1])), d[i], d[i + 1]);
+                    }
+                    if (dZ)
+                        store8(dZ + col * lddz + row, d);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        sum[i] += d[i];
+                }
             }
         }
         at = e;

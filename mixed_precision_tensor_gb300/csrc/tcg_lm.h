@@ -46,6 +46,7 @@ struct LmArgs {
     int num_row_tiles, num_col_tiles;   // of the sides that are not ragged
     int num_k_blocks;          // 64 K elements each
     int min_share, split_gain; // K splitting: fewest blocks per pair, least saving in blocks
+    int align_splits;          // cut tiles in the same K ranges (LmWalk)
     int group_m;
     int a_mode, b_mode;        // OperandMode
     uint32_t idesc;

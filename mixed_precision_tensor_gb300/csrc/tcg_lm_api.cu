@@ -15,6 +15,7 @@ using namespace tcg;
 namespace {
 
 constexpr int64_t kMaxExtent = (int64_t(1) << 31) - 1024;   // 32-bit tile and TMA coordinates
+constexpr int64_t kMaxK = int64_t(1) << 30;                 // 32-bit block counts of cut tiles
 
 int out_kind_of(tcgDataType_t t)
 {
@@ -59,7 +60,7 @@ struct Product {
 struct Shape {
     int epi, bn, share, gain, grid;
     int64_t tiles;                          // at most (a grouped call's depend on its offsets)
-    bool cut;
+    bool cut, align;
 };
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -130,6 +131,11 @@ Shape shape_of(tcgContext *h, const Product &p)
     const bool linear = s.epi == kEpiNarrow || s.epi == kEpiWide || s.epi == kEpiXentNarrow;
     s.cut = linear && !p.ragged_k && !(s.epi == kEpiNarrow && s.bn == 256) && nkb - kMinShare >= s.gain &&
             (p.offsets || s.tiles % P != 0) && h->split_k != 1;
+    // Tiles share operands along both sides, and the operands exceed half of L2 (129 MB): K
+    // ranges alike for all cut tiles (1000 x 1024 outputs over K = 50021: 109 -> 84 us).
+    const int64_t x_tiles = ceil_div(p.tokens, s.epi == kEpiWide ? 256 : s.bn);
+    const int64_t w_tiles = ceil_div(p.feats, s.epi == kEpiWide ? s.bn : 256);
+    s.align = !p.offsets && x_tiles > 1 && w_tiles > 1 && (p.tokens + p.feats) * p.k * 2 > (int64_t(64) << 20);
     int64_t pairs = s.tiles;
     if (s.cut)
         pairs = s.tiles * nkb / kMinShare > pairs ? s.tiles * nkb / kMinShare : pairs;
@@ -170,6 +176,7 @@ tcgStatus_t queue(tcgContext *h, const Product &p, void *ws, LmArgs a = LmArgs{}
     a.num_k_blocks = static_cast<int>(ceil_div(p.k, 64));
     a.min_share = s.share;
     a.split_gain = s.gain;
+    a.align_splits = s.align;
     a.group_m = h->group_m > 0 ? h->group_m : 8;
     a.in_bf16 = p.in == TCG_R_16BF;
     const bool a_kmajor = narrow ? p.w_kmajor : p.x_kmajor;
@@ -356,7 +363,7 @@ tcgStatus_t run_product(tcgContext *h, Product &p, const tcgEpilogue_t *e)
         return TCG_STATUS_INVALID_VALUE;
     if (p.offsets && ((p.groups > 1 && p.strideW <= 0) || (p.strideW * 2) % 16))
         return TCG_STATUS_INVALID_VALUE;
-    if (p.feats > kMaxExtent || p.tokens > kMaxExtent || p.k > kMaxExtent)
+    if (p.feats > kMaxExtent || p.tokens > kMaxExtent || p.k > kMaxK)
         return TCG_STATUS_NOT_SUPPORTED;
     if (p.feats == 0 || p.tokens == 0)
         return TCG_STATUS_SUCCESS;
@@ -483,7 +490,7 @@ tcgStatus_t check_xent(const Xent &x)
         return TCG_STATUS_INVALID_VALUE;
     if (bad_ld(x.ldx, x.k, 2) || bad_ld(x.ldw, x.k, 2))
         return TCG_STATUS_INVALID_VALUE;
-    if (x.rows > kMaxExtent || x.vocab > kMaxExtent || x.k > kMaxExtent)
+    if (x.rows > kMaxExtent || x.vocab > kMaxExtent || x.k > kMaxK)
         return TCG_STATUS_NOT_SUPPORTED;
     if (x.rows == 0)
         return TCG_STATUS_SUCCESS;
@@ -693,11 +700,11 @@ tcgStatus_t tcg_epilogue_backward(tcgHandle_t h, tcgActivation_t activation, int
     if (st != TCG_STATUS_SUCCESS)
         return st;
     h->used = true;
-    // Columns per block: about 32 blocks of 256 rows per SM (a few at a time), 16 to 256
-    // columns each.
+    // Columns per block: about 16 blocks of 256 rows per SM (a few at a time), 32 to 256
+    // columns each, 32 of them under way at a time.
     const int64_t row_blocks = (m + 255) / 256;
-    int64_t chunk = n * row_blocks / (32 * static_cast<int64_t>(h->num_sms)) / 8 * 8;
-    chunk = chunk < 16 ? 16 : (chunk > 256 ? 256 : chunk);
+    int64_t chunk = n * row_blocks / (16 * static_cast<int64_t>(h->num_sms)) / 32 * 32;
+    chunk = chunk < 32 ? 32 : (chunk > 256 ? 256 : chunk);
     while ((n + chunk - 1) / chunk > 65535)              // the grid's second dimension
         chunk *= 2;
     void *ws = nullptr;

@@ -151,20 +151,28 @@ tcgStatus_t bind_device(tcgContext *h)
 // VMM allocation); pageable, pinned (cudaHostAlloc) and managed memory are rejected.
 // The query is a pure lookup, made in relaxed capture mode so that a call being
 // captured into a CUDA graph cannot have it counted as an unsafe call.
-tcgStatus_t device_ptr_ok(int dev, const void *p)
+tcgStatus_t device_ptrs_ok(int dev, const void *const *ptrs, int n)
 {
-    cudaPointerAttributes at;
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
     const bool swapped = cudaThreadExchangeStreamCaptureMode(&mode) == cudaSuccess;
-    const cudaError_t e = cudaPointerGetAttributes(&at, p);
+    bool ok = true;
+    for (int i = 0; ok && i < n; ++i) {
+        cudaPointerAttributes at;
+        if (!ptrs[i])
+            continue;
+        const cudaError_t e = cudaPointerGetAttributes(&at, ptrs[i]);
+        if (e != cudaSuccess)
+            cudaGetLastError();
+        ok = e == cudaSuccess && at.type == cudaMemoryTypeDevice && at.device == dev;
+    }
     if (swapped)
         cudaThreadExchangeStreamCaptureMode(&mode);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return TCG_STATUS_INVALID_VALUE;
-    }
-    return at.type == cudaMemoryTypeDevice && at.device == dev ? TCG_STATUS_SUCCESS
-                                                                : TCG_STATUS_INVALID_VALUE;
+    return ok ? TCG_STATUS_SUCCESS : TCG_STATUS_INVALID_VALUE;
+}
+
+tcgStatus_t device_ptr_ok(int dev, const void *p)
+{
+    return p ? device_ptrs_ok(dev, &p, 1) : TCG_STATUS_INVALID_VALUE;
 }
 
 // device_ptr_ok with a small per-handle cache of the pointer values that passed, so a

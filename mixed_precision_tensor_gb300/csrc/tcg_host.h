@@ -100,8 +100,8 @@ struct Problem {
 
 // Binds the handle to the current device on its first call (capability check, error word).
 tcgStatus_t bind_device(tcgContext *h);
-// SUCCESS if p is device memory of device dev (see device_ptr_ok in tcg_api.cu).
-tcgStatus_t device_ptr_ok(int dev, const void *p);
+// SUCCESS if the pointers (null ones aside) are device memory of device dev.
+tcgStatus_t device_ptrs_ok(int dev, const void *const *ptrs, int n);
 // Tensor map of rank 3 or 4 with zero fill out of range, from the handle's cache of maps.
 tcgStatus_t get_map(tcgContext *h, const void *ptr, tcgDataType_t t, int rank,
                     const uint64_t *dims, const uint64_t *strides, const uint32_t *box,

@@ -30,10 +30,8 @@ def _rows(t, what, rows, cols, dtype, device):
     """Leading dimension of a rows x cols matrix, checked."""
     if t.shape != (rows, cols):
         raise ValueError(f"{what} must be {rows} x {cols}, got {tuple(t.shape)}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{what} must be on {device}, got {t.device}")
+    if t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{what} must be {dtype} on {device}, got {t.dtype} on {t.device}")
     s0, s1 = t.stride()
     per = 4 if dtype is torch.float32 else 8
     if s1 != 1 and cols > 1:
@@ -46,13 +44,13 @@ def _rows(t, what, rows, cols, dtype, device):
 
 
 def _input(x, what="x"):
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise ValueError(f"{what} must be a two-dimensional tensor")
-    if not x.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    if x.dtype not in _IN:
-        raise ValueError(f"{what} must be float16 or bfloat16, got {x.dtype}")
-    return x.shape[0], x.shape[1], x.dtype, x.device
+    dtype = x.dtype if isinstance(x, torch.Tensor) else None
+    if dtype not in _IN:
+        raise ValueError(f"{what} must be a float16 or bfloat16 tensor, got {dtype}")
+    if x.dim() != 2 or not x.is_cuda:
+        raise ValueError(f"{what} must be a two-dimensional CUDA tensor")
+    t, k = x.shape
+    return t, k, dtype, x.device
 
 
 def _act(act):
@@ -122,13 +120,21 @@ def _epilogue(act, bias, bias_shape, residual, beta, z, rows, n, dtype, out_dtyp
 
 
 def _out(handle, out, out_dtype, rows, n, dtype, device):
+    """The output (made if None), its leading dimension and type code."""
     if out is None:
-        out = _matrix(handle, rows, n, out_dtype or dtype, device)
-    elif out_dtype is not None and out.dtype != out_dtype:
+        if out_dtype is None:
+            out_dtype = dtype
+        elif out_dtype not in (dtype, torch.float32):
+            raise ValueError(f"the output must be {dtype} or torch.float32, got {out_dtype}")
+        per = 4 if out_dtype is torch.float32 else 8
+        ld = (n + per - 1) // per * per
+        out = _empty(handle, (rows, ld), out_dtype, device)
+        return (out if ld == n else out[:, :n]), ld or per, _TYPES[out_dtype]
+    if out_dtype is not None and out.dtype != out_dtype:
         raise ValueError("out and out_dtype disagree")
     if out.dtype not in (dtype, torch.float32):
         raise ValueError(f"the output must be {dtype} or torch.float32, got {out.dtype}")
-    return out, _rows(out, "out", rows, n, out.dtype, device)
+    return out, _rows(out, "out", rows, n, out.dtype, device), _TYPES[out.dtype]
 
 
 def linear(handle, x, w, bias=None, act="none", residual=None, beta=1.0, alpha=1.0, out=None,
@@ -145,12 +151,12 @@ def linear(handle, x, w, bias=None, act="none", residual=None, beta=1.0, alpha=1
     n = w.shape[0]
     ldw = _rows(w, "w", n, k, dtype, dev)
     ldx = _rows(x, "x", t, k, dtype, dev)
-    out, ldo = _out(handle, out, out_dtype, t, n, dtype, dev)
+    out, ldo, out_code = _out(handle, out, out_dtype, t, n, dtype, dev)
     e = _epilogue(_act(act), bias, (n,), residual, beta, z, t, n, dtype, out.dtype, dev)
     code = _IN[dtype]
     s = _lib().tcg_gemm_epilogue(
         handle.h, 1, 0, n, t, k, alpha, w.data_ptr(), ldw, x.data_ptr(), ldx, code, out.data_ptr(),
-        _TYPES[out.dtype], ldo, e)
+        out_code, ldo, e)
     if s:
         raise _tcg.TcgError(s, "linear")
     return out
@@ -222,8 +228,8 @@ def linear_backward(handle, dout, x, w, z=None, act="none", want=("dx", "dw", "d
     if want_dw:
         if dw is None:
             dw = _matrix(handle, n, k, dtype, dev)
-        s = lib.tcg_gemm_ex(handle.h, 0, 1, k, n, t, 1.0, x.data_ptr(), ty, ldx, dz.data_ptr(), ty,
-                            ldz, 0.0, dw.data_ptr(), ty, _rows(dw, "dw", n, k, dtype, dev), 0)
+        s = lib.tcg_gemm_epilogue(handle.h, 0, 1, k, n, t, 1.0, x.data_ptr(), ldx, dz.data_ptr(), ldz,
+                                  ty, dw.data_ptr(), ty, _rows(dw, "dw", n, k, dtype, dev), None)
         if s:
             raise _tcg.TcgError(s, "linear_backward dw")
     return (dx if want_dx else None, dw if want_dw else None, dbias if want_db else None)
@@ -252,11 +258,11 @@ def grouped_linear(handle, x, w, offsets, bias=None, act="none", residual=None, 
     ldw, stride = _experts(w, "w", e, n, k, dtype, dev)
     ldx = _rows(x, "x", t, k, dtype, dev)
     _check_offsets(offsets, e, dev)
-    out, ldo = _out(handle, out, out_dtype, t, n, dtype, dev)
+    out, ldo, out_code = _out(handle, out, out_dtype, t, n, dtype, dev)
     ep = _epilogue(_act(act), bias, (e, n), residual, beta, z, t, n, dtype, out.dtype, dev)
     s = _lib().tcg_gemm_grouped(
         handle.h, 1, n, t, k, e, offsets.data_ptr(), alpha, w.data_ptr(), ldw, stride, x.data_ptr(),
-        ldx, _IN[dtype], out.data_ptr(), _TYPES[out.dtype], ldo, ep)
+        ldx, _IN[dtype], out.data_ptr(), out_code, ldo, ep)
     if s:
         raise _tcg.TcgError(s, "grouped_linear")
     return out

@@ -480,7 +480,7 @@ tcgStatus_t tcg_gemm_epilogue_workspace_size(tcgHandle_t h, tcgOp_t transa, tcgO
  *     D_g = alpha * A[:, range g] * B[:, range g]^T,      D_g = D + g * strideD,
  * A m x k and B n x k column-major, one column per token (k tokens), offsets as above with
  * n = k.  A group without tokens gets zeros.  Tokens of other groups are never part of a
- * sum, whatever they hold (NaN included).  No workspace. */
+ * sum, whatever they hold (NaN included).  Workspace: 256 bytes per group. */
 tcgStatus_t tcg_gemm_grouped_k(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int64_t groups,
                                const int64_t *offsets, float alpha, const void *A, int64_t lda,
                                const void *B, int64_t ldb, tcgDataType_t ABtype, void *D,

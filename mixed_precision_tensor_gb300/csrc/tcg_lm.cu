@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
         mbar_init(smem_u32(&ctl->drain), 1);
         ctl->abort_flag = 0;
         fence_mbar_init();
-        if (RK ? p.tokens > 0 : p.num_k_blocks > 0) {
+        if (!RK && p.num_k_blocks > 0) {
             tma_prefetch_map(&maps.A);
             tma_prefetch_map(&maps.B);
         }
@@ -677,6 +677,8 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
             uint32_t phase = 0;
             bool skip_once = p.fault_inject != 0 && leader;
             bool ok = true;
+            const CUtensorMap *map_a = &maps.A, *map_b = &maps.B;
+            int maps_of = -1;
             bool more = walk.next(p, ctl, w);
             if (!p.offsets)
                 griddep_wait();
@@ -684,6 +686,13 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                 const int m0 = w.row0 + static_cast<int>(rank) * kBM;
                 const int n0 = w.col0 + static_cast<int>(rank) * (width(w) / 2);
                 const int za = WIDE ? 0 : w.g, zb = WIDE && !RK ? w.g : 0;
+                if (RK && w.g != maps_of) {                // maps that end with the group
+                    maps_of = w.g;
+                    map_a = p.group_maps + 2 * w.g;
+                    map_b = map_a + 1;
+                    fence_tensormap_acquire(map_a);
+                    fence_tensormap_acquire(map_b);
+                }
                 for (int kb = w.kb0; kb < w.kb1; ++kb) {
                     const uint32_t fb_local = smem_u32(&ctl->full[stage]);
                     const uint32_t fb = mapa_shared(fb_local, 0);
@@ -714,37 +723,8 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                                     tma_load_3d_pair(dst + h * kChunkBytes, map, fb, row0 + h * 64,
                                                      k0, z);
                         };
-                        const int left = w.toks - kb * kKRow;     // K ragged: tokens from k0
-                        if (RK && left < kKRow) {
-                            // The group's last tokens, then zeros (token index past the end) up
-                            // to the stage's 64: boxes of 16, 4 and 1 tokens, each a run of
-                            // 128-byte rows of the stage.
-                            auto tail = [&](uint32_t dst, const CUtensorMap *map, int rows, int row0) {
-                                for (int h = 0; h < rows / 64; ++h) {
-                                    const uint32_t d = dst + h * kChunkBytes;
-                                    auto run = [&](int tok, int step, int count, int from) {
-                                        // `count` tokens from stage row `from` on
-                                        int at = from;
-                                        const int stop = from + count;
-                                        while (at < stop) {
-                                            const int b = (at % 16 == 0 && stop - at >= 16) ? 0
-                                                        : (at % 4 == 0 && stop - at >= 4) ? 1 : 2;
-                                            tma_load_3d_pair(d + at * kRowBytes, map + b, fb,
-                                                             row0 + h * 64,
-                                                             tok + step * (at - from), 0);
-                                            at += 16 >> (2 * b);
-                                        }
-                                    };
-                                    run(k0, 1, left, 0);
-                                    run(p.tokens, 0, kKRow - left, left);
-                                }
-                            };
-                            tail(sa, maps.A_tail, kBM, m0);
-                            tail(sb, maps.B_tail, kBRows, n0);
-                        } else {
-                            load(sa, &maps.A, p.a_mode, kBM, m0, za);
-                            load(sb, &maps.B, p.b_mode, kBRows, n0, zb);
-                        }
+                        load(sa, map_a, p.a_mode, kBM, m0, za);
+                        load(sb, map_b, p.b_mode, kBRows, n0, zb);
                     }
                     if (++stage == kStages) {
                         stage = 0;
@@ -1351,6 +1331,29 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+// One warp per group copies the two maps and sets their token extent (dimension 1 of either
+// layout) to the group's end.  An empty group's maps are never used; extents are at least 1.
+__global__ void __launch_bounds__(128)
+    tcg_group_maps_kernel(const __grid_constant__ LmMaps maps, const int64_t *__restrict__ offsets,
+                          int groups, int tokens, CUtensorMap *out)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31, g = blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (g >= groups)
+        return;
+    static_assert(sizeof(CUtensorMap) == 128, "32 words");
+    int b, e;
+    group_range(offsets, tokens, g, b, e);
+    for (int x = 0; x < 2; ++x)
+        reinterpret_cast<uint32_t *>(out + 2 * g + x)[lane] =
+            reinterpret_cast<const uint32_t *>(x ? &maps.B : &maps.A)[lane];
+    __syncwarp();
+    if (lane < 2)
+        tensormap_set_dim<1>(out + 2 * g + lane, static_cast<uint32_t>(e > 0 ? e : 1));
+    fence_tensormap_release();
+}
+
 // dZ = dD act'(Z) (column-major m x cols; dZ may be left out), and for each group the sum
 // of its columns of dZ before rounding.  Bound by memory: dD and Z are read once and dZ is
 // written once, 16 bytes a thread.  Block (x, y): rows 256 x .. + 255 of the y-th `chunk`
@@ -1566,6 +1569,13 @@ int lm_max_resident_ctas(int num_sms)
         return num_sms / 2 * 2;
     }
     return clusters * 2;
+}
+
+cudaError_t launch_group_maps(const LmMaps &maps, const int64_t *offsets, int groups, int tokens,
+                              CUtensorMap *out, cudaStream_t s)
+{
+    return launch_pdl(tcg_group_maps_kernel, dim3((groups + 3) / 4), dim3(128), s, 0, maps, offsets,
+                      groups, tokens, out);
 }
 
 cudaError_t launch_xent_combine(const float2 *stats, int slots, int rows, const float *target_logit,

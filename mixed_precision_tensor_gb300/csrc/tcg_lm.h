@@ -45,6 +45,7 @@ struct LmArgs {
     const int64_t *offsets;    // device, groups + 1 entries; nullptr: one group of everything
     int num_row_tiles, num_col_tiles;   // of the sides that are not ragged
     int num_k_blocks;          // 64 K elements each
+    const CUtensorMap *group_maps;      // K ragged: see launch_group_maps
     int min_share, split_gain; // K splitting: fewest blocks per pair, least saving in blocks
     int align_splits;          // cut tiles in the same K ranges (LmWalk)
     int group_m;
@@ -113,12 +114,14 @@ inline int64_t lm_stat_slots(int64_t vocab, bool narrow)
     return (vocab + 255) / 256 * (narrow ? 8 : LmCfg<256, true>::kParts);
 }
 
-// K-ragged calls load the last tokens of a group with boxes of 16, 4 and 1 tokens, and
-// the rest of the stage from past the last token, which TMA fills with zeros.
 struct LmMaps {
     CUtensorMap A, B;
-    CUtensorMap A_tail[3], B_tail[3];      // boxes of 16, 4, 1 tokens (K ragged only)
 };
+
+// K-ragged calls: maps of A and B for each group (2 g and 2 g + 1 of `out`) whose token extent
+// ends with the group, so that TMA fills the rest of the group's last block with zeros.
+cudaError_t launch_group_maps(const LmMaps &maps, const int64_t *offsets, int groups, int tokens,
+                              CUtensorMap *out, cudaStream_t s);
 
 // Launchers (tcg_lm.cu).  out_kind: type of D.  bn: 32, 64, 128 or 256 (kEpiNarrow), 64, 128 or 256
 // (kEpiWide), 256 (K ragged, kEpiXentStats, kEpiXentGrad), 32 (kEpiXentNarrow).

@@ -153,6 +153,8 @@ bool few_tokens(int64_t tokens, int64_t k);
 
 size_t product_ws(tcgContext *h, const Product &p)
 {
+    if (p.ragged_k)
+        return static_cast<size_t>(p.groups) * 2 * sizeof(CUtensorMap);
     if (few(p))
         return 0;
     const Shape s = shape_of(h, p);
@@ -225,19 +227,14 @@ tcgStatus_t queue(tcgContext *h, const Product &p, void *ws, LmArgs a = LmArgs{}
             return st;
     }
     if (p.ragged_k && kx > 0) {
-        const int boxes[3] = {16, 4, 1};
-        for (int i = 0; i < 3; ++i)
-            for (int x = 0; x < 2; ++x) {
-                const int64_t ext = x ? p.rows : p.feats, ld = x ? p.ldx : p.ldw;
-                const uint64_t dims[3] = {static_cast<uint64_t>(ext), static_cast<uint64_t>(kx), 1};
-                const uint64_t str[2] = {static_cast<uint64_t>(ld) * 2,
-                                         static_cast<uint64_t>(ld) * 2 * static_cast<uint64_t>(kx)};
-                const uint32_t box[3] = {64, static_cast<uint32_t>(boxes[i]), 1};
-                st = get_map(h, x ? p.X : p.W, p.in, 3, dims, str, box,
-                             x ? &maps.A_tail[i] : &maps.B_tail[i]);
-                if (st != TCG_STATUS_SUCCESS)
-                    return st;
-            }
+        a.group_maps = static_cast<CUtensorMap *>(ws);
+        const cudaError_t e = launch_group_maps(maps, p.offsets, a.groups, a.tokens,
+                                                static_cast<CUtensorMap *>(ws), h->stream);
+        h->launches += 1;
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return TCG_STATUS_EXECUTION_FAILED;
+        }
     }
     const cudaError_t e = launch_lm(maps, a, s.epi, out_kind_of(p.out), s.bn, s.grid, h->stream);
     h->launches += 1;
@@ -661,7 +658,11 @@ tcgStatus_t tcg_gemm_grouped_k(tcgHandle_t h, int64_t m, int64_t n, int64_t k, i
     p.D = D;
     p.ldd = ldd;
     p.strideD = strideD;
-    return queue(h, p, nullptr);
+    void *ws = nullptr;
+    st = acquire_ws(h, product_ws(h, p), &ws);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    return queue(h, p, ws);
 }
 
 tcgStatus_t tcg_epilogue_backward(tcgHandle_t h, tcgActivation_t activation, int64_t m, int64_t n,

@@ -116,6 +116,29 @@ __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+// A tensor map in global memory, changed by this thread: the extent of dimension `ord`.
+template <int ORD>
+__device__ __forceinline__ void tensormap_set_dim(CUtensorMap *map, uint32_t extent)
+{
+    asm volatile("tensormap.replace.tile.global_dim.global.b1024.b32 [%0], %1, %2;" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "n"(ORD), "r"(extent)
+                 : "memory");
+}
+
+// Make changes of tensor maps through ordinary accesses visible to later TMA operations:
+// the writer's side, and the reader's for the 128 bytes of one map.
+__device__ __forceinline__ void fence_tensormap_release()
+{
+    asm volatile("fence.proxy.tensormap::generic.release.gpu;" ::: "memory");
+}
+__device__ __forceinline__ void fence_tensormap_acquire(const CUtensorMap *map)
+{
+    asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(
+                     reinterpret_cast<uint64_t>(map))
+                 : "memory");
+}
+
 // 3-D tiled load global -> shared, completion counted in bytes on `bar`.
 // Coordinates are element indices {x (innermost), y, z}.
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar,

@@ -414,14 +414,16 @@ uint64_t tcg_launch_count(tcgHandle_t h);
  * (rounded to nearest even once, after the whole epilogue).  Matrices must be 16-byte
  * aligned with leading dimensions (times the element size) a multiple of 16 bytes; m, n
  * and k are arbitrary, zero included.  Element offsets are 64-bit.  The calls run on SM
- * pairs (tcg_set_kernel_options' cta_group does not apply; its group_m does).
+ * pairs (tcg_set_kernel_options' cta_group does not apply; its group_m does, and
+ * tcg_set_split_k(h, 1) keeps tiles whole), those for a few tokens (up to four, or a few
+ * rows of many experts) on the FP32 units.
  *
  * Accuracy: the bound of tcg_gemm_ex on the accumulator; the epilogue runs in FP32 with
  * exp and erfc to 1.5e-7 absolute or better; a D of ABtype adds one rounding.
  *
  * Errors: INVALID_VALUE (NULL handle or needed pointer, misalignment, negative sizes, a
  * leading dimension too small, an unknown enumerator, host memory), NOT_SUPPORTED (type
- * combination, extents near 2^31, more than 384 groups), and the CUDA errors of
+ * combination, extents near 2^31 or k above 2^30, more than 384 groups), and the CUDA errors of
  * tcg_gemm_ex.  Nothing is launched after a failed check.  A device wait that runs out
  * is reported by tcg_get_device_error, which also clears the split counters. */
 
@@ -502,7 +504,8 @@ tcgStatus_t tcg_epilogue_backward(tcgHandle_t h, tcgActivation_t activation, int
  *     lse[i]  = log sum_v exp L[i, v]
  *     loss[i] = lse[i] - L[i, targets[i]]
  * both FP32.  targets is a device array of int64; a row whose target is ignore_index or
- * outside 0 .. vocab - 1 does not count: loss 0 (lse is written all the same). */
+ * outside 0 .. vocab - 1 does not count: loss 0 (lse is written all the same).  A logit of
+ * -inf has probability zero; +inf or NaN makes its row's lse and loss NaN. */
 tcgStatus_t tcg_xent_forward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_t k, const void *X,
                              int64_t ldx, const void *W, int64_t ldw, tcgDataType_t type,
                              const int64_t *targets, int64_t ignore_index, float *loss, float *lse);
@@ -514,7 +517,8 @@ tcgStatus_t tcg_xent_forward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_t
  * vocabulary at a time; a piece of G is held in `type` (256 MiB at most, or 256 columns).
  * For FP16 it is held times a power of two chosen from max |dloss|, so that small
  * probabilities keep their bits.  dX is summed over the pieces in FP32.  Rows that do not
- * count contribute nothing, whatever they hold in dloss or lse. */
+ * count contribute nothing, whatever they hold in dloss or lse (a NaN in such a row of X
+ * still reaches dW, as zero times it). */
 tcgStatus_t tcg_xent_backward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_t k, const void *X,
                               int64_t ldx, const void *W, int64_t ldw, tcgDataType_t type,
                               const int64_t *targets, int64_t ignore_index, const float *lse,

@@ -6,8 +6,7 @@
 //   warp 0 (one lane)   TMA producer into a ring of 128-byte-swizzled stages (64 K elements
 //                       of 128 rows of A and BN / 2 rows of B per CTA)
 //   warp 1 (one lane)   tcgen05.mma into TMEM accumulators (up to four)
-//   the other warps     epilogue (8, or 16 for large tiles): TMEM -> registers -> memory, one
-//                       accumulator row a thread
+//   warps 2-9           epilogue: TMEM -> registers -> memory, one accumulator row a thread
 //
 // The epilogues (LmEpi):
 //   kEpiNarrow     features on the rows, tokens on the columns: few tokens against a weight
@@ -15,10 +14,18 @@
 //   kEpiWide       tokens on the rows, features on the columns: a thread holds 32 adjacent
 //                  features of a token, so bias, residual, pre-activation and output move in
 //                  16-byte pieces
-//   kEpiXentStats  logits X W^T that never leave the chip: per row and tile half the maximum
+//   kEpiXentStats  logits X W^T that never leave the chip: per row and tile part the maximum
 //                  m and sum exp(logit - m), and the target's logit (tokens on the rows)
 //   kEpiXentNarrow the same for few tokens (tokens on the columns)
 //   kEpiXentGrad   dloss (exp(logit - lse) - [target]), rounded to 16 bits
+//
+// What bounds it.  A 64-element block of K costs an SM 32 KiB of operands at tile 256 x 256,
+// loaded at 64 bytes a cycle in the 512 cycles that the tensor core takes for it; with both
+// at work shared memory is nearly full (written and read at 64 bytes a cycle each of 128),
+// so the epilogue's own traffic through it adds to short-K tiles (K = 512: loads alone 36,
+// with the product 43, with the epilogue 55 us for 1024 tiles).  From K = 4096 on it hides
+// behind the product and the power limit bounds (16384 x 4096 x 4096 BF16, GELU,
+// pre-activation kept: 350 us, 1.57 PFLOP/s; no epilogue 287 us, 1.92).
 //
 // Every wait is bounded as in tcg_kernels.cu: a wait that runs out sets a bit in the
 // device error word, every role stops and the kernel returns.
@@ -348,7 +355,7 @@ __device__ __forceinline__ void finish_narrow(const LmArgs &p, float (&z)[kCols]
 // A warp's rows (tokens, one per lane in registers) go to and from memory through the warp's
 // staging area, 64 bytes of each row at a time (32 16-bit or 16 FP32 features), so that
 // memory is accessed in runs of 64 bytes: a lane's own row would go in 16-byte pieces of 32
-// different lines per instruction (16384 x 4096 x 1024 BF16: 114 us a call so, 90 us through
+// different lines per instruction (16384 x 4096 x 1024 BF16: 97 us a call so, 90 us through
 // the staging area).  The 16-byte pieces of a row are permuted by row, so that neither side
 // has bank conflicts.
 __device__ __forceinline__ uint4 *stage_piece(uint8_t *stage, int row, int piece)

@@ -94,11 +94,15 @@ Shape shape_of(tcgContext *h, const Product &p)
         s.bn = p.lm_epi == kEpiXentNarrow ? 32 : 256;
     } else {
         const int64_t per = p.offsets ? p.tokens / p.groups : p.tokens;
-        if (p.x_kmajor && per <= 128) {
+        if (p.x_kmajor && per <= (p.offsets ? 16 : 128)) {
             s.epi = kEpiNarrow;
             s.bn = per <= 32 ? 32 : (per <= 64 ? 64 : 128);
         } else if (p.offsets && p.x_kmajor && per < 2048) {
-            // Groups' last tiles at the width that they have.
+            // Groups' last tiles at the width that they have.  Narrower tiles read a group's
+            // weights once for each of them (8 experts of 4096 x 4096, 62 rows each: 64 wide
+            // 64 us, 256 wide 52 us; with a skewed router 69 and 53), but can be cut along K,
+            // which few rows of few experts want (16 of 1024 x 1032, 200 rows: 32 wide 11 us,
+            // 256 wide 14 us).
             s.epi = kEpiNarrow;
             s.bn = 256;
         } else {
@@ -128,7 +132,7 @@ Shape shape_of(tcgContext *h, const Product &p)
     }
     s.tiles = max_tiles(p, s.epi, s.bn);
     // No more than 8 pieces of a wide tile (whoever joins them reads them one after the other:
-    // 3000 x 8192 outputs over K = 8192, 4 tiles cut in 19 pieces each 283 us, in 8 252 us) or
+    // 3000 x 8192 outputs over K = 8192, 4 tiles cut in 19 pieces each 283 us, in 8 254 us) or
     // 16 of a narrow one.
     const int64_t least = ceil_div(nkb, s.epi == kEpiWide ? 8 : 16);
     s.share = static_cast<int>(least > kMinShare ? least : kMinShare);
@@ -258,8 +262,10 @@ bool few(const Product &p)
 {
     if (p.ragged_k || !p.x_kmajor || !p.w_kmajor || p.k == 0 || p.lm_epi >= 0 || p.alpha_dev)
         return false;
-    return p.offsets ? p.tokens <= kLmFewRows && p.tokens <= 2 * p.groups
-                     : few_tokens(p.tokens, p.k);
+    if (!p.offsets)
+        return few_tokens(p.tokens, p.k);
+    // 64 experts of 2048 x 2048: 30 rows 35 us so, 42 us by tiles; 60 rows 61 and 54.
+    return p.tokens <= kLmFewRows && (p.tokens <= 4 || 2 * p.tokens <= p.groups);
 }
 
 tcgStatus_t queue_few(tcgContext *h, const Product &p)

@@ -3,15 +3,19 @@
 // With one to four tokens a product is a pass over the weights: 2 T operations for every two
 // bytes, bound by memory alone.  The tensor kernel (tcg_lm.cu) pays there for TMEM, whole
 // 256-row tiles and the join of tiles cut along K, so these calls run on the FP32 units: a
-// persistent block per SM whose eight warps work alone.  A warp takes R weight rows
-// (features) at a time and streams them, with its tokens' rows of X, through a ring of its
-// own in shared memory: 512 K elements of each row a stage, brought by one bulk copy per row,
-// the copies of the next rows already under way while these are multiplied (packed FP32
-// multiply-adds, two K elements each).  No barrier between warps, no partial sums in memory.
+// persistent block per SM whose sixteen warps work alone.  A warp takes R weight rows
+// (features) at a time and streams them through a ring of its own in shared memory: 512 K
+// elements of each row a stage, brought by one bulk copy per row, the copies of the next
+// rows already under way while these are multiplied (packed FP32 multiply-adds, two K
+// elements each).  X stays in the SM's cache.  No barrier between warps, no partial sums in
+// memory.
 //
-// Measured on GB300, one token: 16384 x 16384 BF16 weights 84 us (6.4 TB/s); with the loads
-// in registers instead of the ring, two blocks an SM, 88 us, but 71 instead of 46 us for the
-// 32003 x 4096 cross entropy, whose blocks then waited for every four rows.
+// Measured on GB300, one token against 16384 x 16384 BF16 weights: 84 us (6.4 TB/s, 94% of the
+// copy bandwidth).  What it took: sixteen warps of three stages (eight of four or six: 104
+// and 96 us, each waiting for its own chain of steps; twenty-four of two: 106 us), and X
+// loaded a stage ahead (8 rows over 64 experts, where X does not stay cached: 38 -> 25 us).
+// X through the ring instead made every SM read the same lines of L2 at once (four tokens:
+// 169 us).  The tensor kernel: 15.6 us for 4096 x 4096 where this takes 7.9.
 
 #include "tcg_lm_math.cuh"
 

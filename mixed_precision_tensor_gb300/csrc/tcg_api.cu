@@ -38,6 +38,19 @@ int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+struct Problem {
+    tcgOp_t transa, transb;
+    int64_t m, n, k;
+    float alpha, beta;
+    const void *A; tcgDataType_t Atype; int64_t lda; int64_t strideA;
+    const void *B; tcgDataType_t Btype; int64_t ldb; int64_t strideB;
+    void *C; tcgDataType_t Ctype; int64_t ldc; int64_t strideC;
+    int64_t batch;
+    tcgComputeType_t compute;
+    bool batched;
+    bool staged = false;       // A, B, C are the handle's own staging buffers (host-buffer calls)
+};
+
 // Pure host argument checks: no CUDA call is made before they pass.
 tcgStatus_t check_args(const Problem &p)
 {

@@ -85,19 +85,6 @@ struct tcgContext {
 
 namespace tcg {
 
-struct Problem {
-    tcgOp_t transa, transb;
-    int64_t m, n, k;
-    float alpha, beta;
-    const void *A; tcgDataType_t Atype; int64_t lda; int64_t strideA;
-    const void *B; tcgDataType_t Btype; int64_t ldb; int64_t strideB;
-    void *C; tcgDataType_t Ctype; int64_t ldc; int64_t strideC;
-    int64_t batch;
-    tcgComputeType_t compute;
-    bool batched;
-    bool staged = false;       // A, B, C are the handle's own staging buffers (host-buffer calls)
-};
-
 // Binds the handle to the current device on its first call (capability check, error word).
 tcgStatus_t bind_device(tcgContext *h);
 // SUCCESS if the pointers (null ones aside) are device memory of device dev.

@@ -13,7 +13,7 @@
 namespace tcg {
 
 constexpr int kLmMaxGroups = 384;      // experts of one grouped call (a table in shared memory)
-constexpr int kLmCounters = 1024;      // split counters of a handle: up to 8 per cut tile
+constexpr int kLmCounters = 1024;      // split counters of a handle: 4 per cut tile, one tile per pair at most
 constexpr int kLmMaxStages = 12;
 // Shared memory: the operand ring, and (tokens on the rows) 2 KiB of staging per epilogue
 // warp, through which a warp's 32 rows leave and arrive in runs of 64 bytes.

@@ -89,8 +89,8 @@ struct LmUnit {
 // pair takes `share` of them -- a piece of one tile, or the end of one and the start of the
 // next (and whole tiles between).  (Where the operands are larger than L2 and shared by
 // tiles, every cut tile instead gets the same number of pairs and the same K ranges, so that
-// tiles read the same blocks at the same time.)  A pair has at most one piece that starts inside a tile
-// (slot 2 c) and one that starts a tile without ending it (slot 2 c + 1).
+// tiles read the same blocks at the same time.)  A pair has at most one piece that starts
+// inside a tile (slot 2 c) and one that starts a tile without ending it (slot 2 c + 1).
 template <bool WIDE, int BN, bool RK>
 struct LmWalk {
     int c, P;

@@ -68,12 +68,15 @@ def _empty(handle, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _matrix(handle, rows, cols, dtype, device):
-    """A new rows x cols matrix whose rows are a multiple of 16 bytes apart."""
-    per = 8 if dtype != torch.float32 else 4
-    if cols % per == 0:
-        return _empty(handle, (rows, cols), dtype, device)
-    return _empty(handle, (rows, -(-cols // per) * per), dtype, device)[:, :cols]
+def _matrix(handle, given, what, rows, cols, dtype, device):
+    """A rows x cols matrix for a result -- the given one, or a new one whose rows are a
+    multiple of 16 bytes apart -- and its leading dimension."""
+    if given is not None:
+        return given, _rows(given, what, rows, cols, dtype, device)
+    per = 4 if dtype is torch.float32 else 8
+    ld = (cols + per - 1) // per * per or per
+    new = _empty(handle, (rows, ld), dtype, device)
+    return (new if ld == cols else new[:, :cols]), ld
 
 
 def _experts(w, what, e, n, k, dtype, device):
@@ -121,20 +124,16 @@ def _epilogue(act, bias, bias_shape, residual, beta, z, rows, n, dtype, out_dtyp
 
 def _out(handle, out, out_dtype, rows, n, dtype, device):
     """The output (made if None), its leading dimension and type code."""
-    if out is None:
-        if out_dtype is None:
-            out_dtype = dtype
-        elif out_dtype not in (dtype, torch.float32):
-            raise ValueError(f"the output must be {dtype} or torch.float32, got {out_dtype}")
-        per = 4 if out_dtype is torch.float32 else 8
-        ld = (n + per - 1) // per * per
-        out = _empty(handle, (rows, ld), out_dtype, device)
-        return (out if ld == n else out[:, :n]), ld or per, _TYPES[out_dtype]
-    if out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError("out and out_dtype disagree")
-    if out.dtype not in (dtype, torch.float32):
-        raise ValueError(f"the output must be {dtype} or torch.float32, got {out.dtype}")
-    return out, _rows(out, "out", rows, n, out.dtype, device), _TYPES[out.dtype]
+    if out is not None:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out and out_dtype disagree")
+        out_dtype = out.dtype
+    elif out_dtype is None:
+        out_dtype = dtype
+    if out_dtype is not dtype and out_dtype is not torch.float32:
+        raise ValueError(f"the output must be {dtype} or torch.float32, got {out_dtype}")
+    out, ld = _matrix(handle, out, "out", rows, n, out_dtype, device)
+    return out, ld, _TYPES[out_dtype]
 
 
 def linear(handle, x, w, bias=None, act="none", residual=None, beta=1.0, alpha=1.0, out=None,
@@ -162,28 +161,27 @@ def linear(handle, x, w, bias=None, act="none", residual=None, beta=1.0, alpha=1
     return out
 
 
-def _grad_z(handle, dout, z, act, want_dz, want_dbias, groups, offsets, dbias, ld_dout, rows, n):
-    """dz (dout itself where nothing has to be computed) and dbias."""
+def _grad_z(handle, dout, ldd, z, act, want_dz, want_dbias, groups, offsets, dbias, rows, n):
+    """(dz, its leading dimension, dbias); dz is dout where nothing has to be computed."""
     dtype, dev = dout.dtype, dout.device
-    dz = dout
+    compute = want_dz and act != 0
     if want_dbias:
         shape = (n,) if offsets is None else (groups, n)
         if dbias is None:
             dbias = _empty(handle, shape, torch.float32, dev)
-        _vector(dbias, "dbias", shape, (torch.float32,), dev)
-    compute_dz = want_dz and act != 0
-    if compute_dz:
-        dz = _matrix(handle, rows, n, dtype, dev)
-    if compute_dz or want_dbias:
-        ldz = _rows(z, "z", rows, n, dtype, dev) if act else 0
-        s = _lib().tcg_epilogue_backward(
-            handle.h, act, n, rows, groups, None if offsets is None else offsets.data_ptr(),
-            dout.data_ptr(), ld_dout, z.data_ptr() if act else None, ldz, _IN[dtype],
-            dz.data_ptr() if compute_dz else None,
-            _rows(dz, "dz", rows, n, dtype, dev), dbias.data_ptr() if want_dbias else None)
-        if s:
-            raise _tcg.TcgError(s, "epilogue_backward")
-    return dz, dbias
+        else:
+            _vector(dbias, "dbias", shape, (torch.float32,), dev)
+    elif not compute:
+        return dout, ldd, None
+    dz, ldz = _matrix(handle, None, "dz", rows, n, dtype, dev) if compute else (dout, ldd)
+    s = _lib().tcg_epilogue_backward(
+        handle.h, act, n, rows, groups, None if offsets is None else offsets.data_ptr(),
+        dout.data_ptr(), ldd, z.data_ptr() if act else None,
+        _rows(z, "z", rows, n, dtype, dev) if act else 0, _IN[dtype],
+        dz.data_ptr() if compute else None, ldz, dbias.data_ptr() if want_dbias else None)
+    if s:
+        raise _tcg.TcgError(s, "epilogue_backward")
+    return dz, ldz, dbias
 
 
 def _backward_args(dout, x, z, act, n):
@@ -215,21 +213,18 @@ def linear_backward(handle, dout, x, w, z=None, act="none", want=("dx", "dw", "d
     t, k, dtype, dev, ldx, ldd, code = _backward_args(dout, x, z, act, n)
     ldw = _rows(w, "w", n, k, dtype, dev)
     want_dx, want_dw, want_db = _want(want)
-    dz, dbias = _grad_z(handle, dout, z, code, want_dx or want_dw, want_db, 1, None, dbias, ldd, t, n)
-    ldz = _rows(dz, "dz", t, n, dtype, dev)
+    dz, ldz, dbias = _grad_z(handle, dout, ldd, z, code, want_dx or want_dw, want_db, 1, None, dbias, t, n)
     ty, lib = _IN[dtype], _lib()
     if want_dx:
-        if dx is None:
-            dx = _matrix(handle, t, k, dtype, dev)
-        s = lib.tcg_gemm_ex(handle.h, 0, 0, k, t, n, 1.0, w.data_ptr(), ty, ldw, dz.data_ptr(), ty,
-                            ldz, 0.0, dx.data_ptr(), ty, _rows(dx, "dx", t, k, dtype, dev), 0)
+        dx, ld = _matrix(handle, dx, "dx", t, k, dtype, dev)
+        s = lib.tcg_gemm_ex(handle.h, 0, 0, k, t, n, 1.0, w.data_ptr(), ty, ldw, dz.data_ptr(), ty, ldz,
+                            0.0, dx.data_ptr(), ty, ld, 0)
         if s:
             raise _tcg.TcgError(s, "linear_backward dx")
     if want_dw:
-        if dw is None:
-            dw = _matrix(handle, n, k, dtype, dev)
-        s = lib.tcg_gemm_epilogue(handle.h, 0, 1, k, n, t, 1.0, x.data_ptr(), ldx, dz.data_ptr(), ldz,
-                                  ty, dw.data_ptr(), ty, _rows(dw, "dw", n, k, dtype, dev), None)
+        dw, ld = _matrix(handle, dw, "dw", n, k, dtype, dev)
+        s = lib.tcg_gemm_epilogue(handle.h, 0, 1, k, n, t, 1.0, x.data_ptr(), ldx, dz.data_ptr(), ldz, ty,
+                                  dw.data_ptr(), ty, ld, None)
         if s:
             raise _tcg.TcgError(s, "linear_backward dw")
     return (dx if want_dx else None, dw if want_dw else None, dbias if want_db else None)
@@ -281,16 +276,13 @@ def grouped_linear_backward(handle, dout, x, w, offsets, z=None, act="none",
     ldw, stride = _experts(w, "w", e, n, k, dtype, dev)
     _check_offsets(offsets, e, dev)
     want_dx, want_dw, want_db = _want(want)
-    dz, dbias = _grad_z(handle, dout, z, code, want_dx or want_dw, want_db, e, offsets, dbias, ldd, t,
-                        n)
-    ldz = _rows(dz, "dz", t, n, dtype, dev)
+    dz, ldz, dbias = _grad_z(handle, dout, ldd, z, code, want_dx or want_dw, want_db, e, offsets, dbias, t,
+                             n)
     ty, lib = _IN[dtype], _lib()
     if want_dx:
-        if dx is None:
-            dx = _matrix(handle, t, k, dtype, dev)
+        dx, ld = _matrix(handle, dx, "dx", t, k, dtype, dev)
         s = lib.tcg_gemm_grouped(handle.h, 0, k, t, n, e, offsets.data_ptr(), 1.0, w.data_ptr(), ldw,
-                                 stride, dz.data_ptr(), ldz, ty, dx.data_ptr(), ty,
-                                 _rows(dx, "dx", t, k, dtype, dev), None)
+                                 stride, dz.data_ptr(), ldz, ty, dx.data_ptr(), ty, ld, None)
         if s:
             raise _tcg.TcgError(s, "grouped_linear_backward dx")
     if want_dw:
@@ -345,15 +337,15 @@ def linear_cross_entropy_backward(handle, x, w, targets, lse, dloss, ignore_inde
     want_dx, want_dw, bad = _want(want)
     if bad:
         raise ValueError("want names dx and dw only")
-    if want_dx and dx is None:
-        dx = _matrix(handle, t, k, dtype, dev)
-    if want_dw and dw is None:
-        dw = _matrix(handle, v, k, dtype, dev)
+    lddx = lddw = 8
+    if want_dx:
+        dx, lddx = _matrix(handle, dx, "dx", t, k, dtype, dev)
+    if want_dw:
+        dw, lddw = _matrix(handle, dw, "dw", v, k, dtype, dev)
     s = _lib().tcg_xent_backward(
         handle.h, t, v, k, x.data_ptr(), ldx, w.data_ptr(), ldw, _IN[dtype], targets.data_ptr(),
-        ignore_index, lse.data_ptr(), dloss.data_ptr(), dx.data_ptr() if want_dx else None,
-        _rows(dx, "dx", t, k, dtype, dev) if want_dx else 8, dw.data_ptr() if want_dw else None,
-        _rows(dw, "dw", v, k, dtype, dev) if want_dw else 8)
+        ignore_index, lse.data_ptr(), dloss.data_ptr(), dx.data_ptr() if want_dx else None, lddx,
+        dw.data_ptr() if want_dw else None, lddw)
     if s:
         raise _tcg.TcgError(s, "linear_cross_entropy_backward")
     return (dx if want_dx else None, dw if want_dw else None)

@@ -499,6 +499,23 @@ tcgStatus_t tcg_epilogue_backward(tcgHandle_t h, tcgActivation_t activation, int
                                   int64_t lddd, const void *Z, int64_t ldz, tcgDataType_t type,
                                   void *dZ, int64_t lddz, float *dbias);
 
+/* The backward pass of a linear layer (groups = 1, offsets NULL) or of a layer of experts
+ * in one call.  Row-major: dD, Z are n x m (n tokens), W m x k (the A of the forward call
+ * with TCG_OP_T; per group, strideW apart), X n x k.
+ *     dZ = dD * act'(Z),  dX = dZ W (n x k),  dW = dZ^T X (m x k, per group, stridedW apart),
+ *     dbias as in tcg_epilogue_backward,
+ * all of one 16-bit type but dbias (FP32).  dX, dW or dbias may be NULL.  Strides as in
+ * tcg_gemm_grouped and tcg_gemm_grouped_k, unused without offsets.  dZ is formed in the
+ * workspace; the second call gives the workspace's bytes (groups = 0: not grouped). */
+tcgStatus_t tcg_linear_backward(tcgHandle_t h, tcgActivation_t activation, int64_t m, int64_t n,
+                                int64_t k, int64_t groups, const int64_t *offsets, const void *dD,
+                                int64_t lddd, const void *Z, int64_t ldz, const void *W, int64_t ldw,
+                                int64_t strideW, const void *X, int64_t ldx, tcgDataType_t type, void *dX,
+                                int64_t lddx, void *dW, int64_t lddw, int64_t stridedW, float *dbias);
+tcgStatus_t tcg_linear_backward_workspace_size(tcgHandle_t h, tcgActivation_t activation, int64_t m,
+                                               int64_t n, int64_t k, int64_t groups, int with_dX,
+                                               int with_dW, int with_dbias, size_t *bytes);
+
 /* Softmax cross entropy of a linear head, without keeping the logits L = X W^T (rows x
  * vocab).  X is row-major rows x k (leading dimension ldx >= k), W row-major vocab x k.
  *     lse[i]  = log sum_v exp L[i, v]

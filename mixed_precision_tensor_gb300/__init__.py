@@ -49,7 +49,8 @@ EXPORTS = ("tcg_create", "tcg_destroy", "tcg_set_stream", "tcg_set_workspace",
            "tcg_tail_split_plan", "tcg_gemm_tile_plan", "tcg_set_tile_n",
            "tcg_set_tf32_rounding", "tcg_gemm_epilogue", "tcg_gemm_grouped",
            "tcg_gemm_grouped_k", "tcg_gemm_epilogue_workspace_size", "tcg_epilogue_backward",
-           "tcg_xent_forward", "tcg_xent_backward", "tcg_xent_workspace_size")
+           "tcg_linear_backward", "tcg_linear_backward_workspace_size", "tcg_xent_forward",
+           "tcg_xent_backward", "tcg_xent_workspace_size")
 
 _lock = threading.Lock()
 _lib = None
@@ -160,6 +161,12 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.tcg_epilogue_backward.restype = st
         lib.tcg_epilogue_backward.argtypes = [vp, ci, i64, i64, i64, vp, vp, i64, vp, i64, ci, vp,
                                               i64, vp]
+        lib.tcg_linear_backward.restype = st
+        lib.tcg_linear_backward.argtypes = [vp, ci, i64, i64, i64, i64, vp, vp, i64, vp, i64, vp, i64,
+                                            i64, vp, i64, ci, vp, i64, vp, i64, i64, vp]
+        lib.tcg_linear_backward_workspace_size.restype = st
+        lib.tcg_linear_backward_workspace_size.argtypes = [vp, ci, i64, i64, i64, i64, ci, ci, ci,
+                                                           ctypes.POINTER(ctypes.c_size_t)]
         lib.tcg_xent_forward.restype = st
         lib.tcg_xent_forward.argtypes = [vp, i64, i64, i64, vp, i64, vp, i64, ci, vp, i64, vp, vp]
         lib.tcg_xent_backward.restype = st
@@ -387,6 +394,22 @@ def tcg_epilogue_backward(h, activation, m, n, groups, offsets, dD, lddd, Z, ldz
     return load_library().tcg_epilogue_backward(h, activation, m, n, groups, _ptr(offsets),
                                                 _ptr(dD), lddd, _ptr(Z), ldz, type, _ptr(dZ), lddz,
                                                 _ptr(dbias))
+
+
+def tcg_linear_backward(h, activation, m, n, k, groups, offsets, dD, lddd, Z, ldz, W, ldw, strideW, X,
+                        ldx, type, dX, lddx, dW, lddw, stridedW, dbias) -> int:
+    return load_library().tcg_linear_backward(h, activation, m, n, k, groups, _ptr(offsets), _ptr(dD),
+                                              lddd, _ptr(Z), ldz, _ptr(W), ldw, strideW, _ptr(X), ldx,
+                                              type, _ptr(dX), lddx, _ptr(dW), lddw, stridedW,
+                                              _ptr(dbias))
+
+
+def tcg_linear_backward_workspace_size(h, activation, m, n, k, groups=0, dX=True, dW=True,
+                                       dbias=True) -> int:
+    size = ctypes.c_size_t(0)
+    check(load_library().tcg_linear_backward_workspace_size(h, activation, m, n, k, groups, dX, dW, dbias,
+                                                            ctypes.byref(size)))
+    return size.value
 
 
 def tcg_xent_forward(h, rows, vocab, k, X, ldx, W, ldw, type, targets, ignore_index, loss,

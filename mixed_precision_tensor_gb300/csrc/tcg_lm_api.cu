@@ -529,6 +529,129 @@ size_t xent_forward_bytes(tcgContext *h, const Xent &x)
            (few_tokens(x.rows, x.k) ? 0 : product_ws(h, xent_forward_product(x)));
 }
 
+// Columns per block of the epilogue's gradient: about 16 blocks of 256 rows per SM (a few at a
+// time), 32 to 256 columns each, 32 of them under way at a time.
+int64_t gradient_chunk(tcgContext *h, int64_t m, int64_t n)
+{
+    int64_t chunk = n * ceil_div(m, 256) / (16 * static_cast<int64_t>(h->num_sms)) / 32 * 32;
+    chunk = chunk < 32 ? 32 : (chunk > 256 ? 256 : chunk);
+    while (ceil_div(n, chunk) > 65535)                   // the grid's second dimension
+        chunk *= 2;
+    return chunk;
+}
+
+size_t gradient_part_bytes(tcgContext *h, int64_t m, int64_t n, int64_t groups)
+{
+    return static_cast<size_t>(ceil_div(n, gradient_chunk(h, m, n)) + groups) * static_cast<size_t>(m) * 4;
+}
+
+// Arguments of an epilogue's gradient, shared with the whole backward pass.
+struct Gradient {
+    int act;
+    int64_t m, n, groups;
+    const int64_t *offsets;
+    const void *dD; int64_t lddd;
+    const void *Z; int64_t ldz;
+    tcgDataType_t type;
+    void *dZ; int64_t lddz;
+    float *dbias;
+};
+
+tcgStatus_t check_gradient(const Gradient &g)
+{
+    if (g.act < TCG_ACT_NONE || g.act > TCG_ACT_SILU || !valid_type(g.type))
+        return TCG_STATUS_INVALID_VALUE;
+    if (!is_16bit(g.type))
+        return TCG_STATUS_NOT_SUPPORTED;
+    if (g.offsets) {
+        const tcgStatus_t st = check_groups(g.groups, g.offsets);
+        if (st != TCG_STATUS_SUCCESS)
+            return st;
+    } else if (g.groups != 1) {
+        return TCG_STATUS_INVALID_VALUE;
+    }
+    const bool need_z = g.act != TCG_ACT_NONE;
+    if (g.m < 0 || g.n < 0 || bad_ld(g.lddd, g.m, 2) || (need_z && bad_ld(g.ldz, g.m, 2)) ||
+        (g.dZ && bad_ld(g.lddz, g.m, 2)))
+        return TCG_STATUS_INVALID_VALUE;
+    if (g.m > kMaxK || g.n > kMaxK)
+        return TCG_STATUS_NOT_SUPPORTED;
+    if (g.m > 0 && g.n > 0 &&
+        (!g.dD || !aligned16(g.dD) || (need_z && (!g.Z || !aligned16(g.Z))) || !aligned16(g.dZ)))
+        return TCG_STATUS_INVALID_VALUE;
+    return reinterpret_cast<uintptr_t>(g.dbias) % 4 ? TCG_STATUS_INVALID_VALUE : TCG_STATUS_SUCCESS;
+}
+
+tcgStatus_t queue_gradient(tcgContext *h, const Gradient &g, void *part)
+{
+    const cudaError_t e = launch_epi_backward(
+        g.act, g.type == TCG_R_16BF, static_cast<int>(g.m), static_cast<int>(g.n),
+        static_cast<int>(g.groups), g.offsets, g.dD, g.lddd, g.act != TCG_ACT_NONE ? g.Z : nullptr, g.ldz,
+        g.n > 0 ? g.dZ : nullptr, g.lddz, g.dbias, static_cast<float *>(part),
+        static_cast<int>(gradient_chunk(h, g.m, g.n)), h->stream);
+    h->launches += g.dbias ? 2 : 1;
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return TCG_STATUS_EXECUTION_FAILED;
+    }
+    return TCG_STATUS_SUCCESS;
+}
+
+// The two products of a layer's backward pass, without their pointers.
+Product layer_dx(int64_t m, int64_t n, int64_t k, int64_t groups, const int64_t *offsets, tcgDataType_t type)
+{
+    Product p;                              // dX[token][j] = sum over i of dZ[token][i] W[i][j]
+    p.tokens = n;
+    p.feats = k;
+    p.k = m;
+    p.w_kmajor = false;
+    p.in = p.out = type;
+    p.groups = groups;
+    p.offsets = offsets;
+    return p;
+}
+
+Product layer_dw(int64_t m, int64_t n, int64_t k, int64_t groups, const int64_t *offsets, tcgDataType_t type)
+{
+    Product p;                              // dW[i][j] = sum over tokens of dZ[token][i] X[token][j]
+    p.feats = k;
+    p.x_kmajor = p.w_kmajor = false;
+    p.in = p.out = type;
+    if (offsets) {
+        p.ragged_k = true;
+        p.rows = m;
+        p.tokens = n;
+        p.groups = groups;
+        p.offsets = offsets;
+    } else {
+        p.tokens = m;
+        p.k = n;
+    }
+    return p;
+}
+
+// The workspace of a layer's backward pass: dZ (where it is not dD), the partial sums of dbias,
+// and what the products need.
+struct LayerPlan {
+    int64_t lddz;
+    size_t dz_bytes, part_bytes, total;
+};
+
+LayerPlan layer_plan(tcgContext *h, bool act, int64_t m, int64_t n, int64_t k, int64_t groups,
+                     const int64_t *offsets, bool dx, bool dw, bool dbias)
+{
+    LayerPlan pl;
+    pl.lddz = (m + 7) / 8 * 8;
+    pl.dz_bytes = act && (dx || dw) ? pad256(static_cast<size_t>(n) * pl.lddz * 2) : 0;
+    pl.part_bytes = dbias && m > 0 ? pad256(gradient_part_bytes(h, m, n, groups)) : 0;
+    const size_t x = dx && n > 0 && k > 0
+                         ? product_ws(h, layer_dx(m, n, k, groups, offsets, TCG_R_16BF)) : 0;
+    const size_t w = dw && m > 0 && k > 0
+                         ? product_ws(h, layer_dw(m, n, k, groups, offsets, TCG_R_16BF)) : 0;
+    pl.total = pl.dz_bytes + pl.part_bytes + (x > w ? x : w);
+    return pl;
+}
+
 }  // namespace
 
 extern "C" {
@@ -593,8 +716,9 @@ tcgStatus_t tcg_gemm_epilogue_workspace_size(tcgHandle_t h, tcgOp_t transa, tcgO
                                              int64_t m, int64_t n, int64_t k, int64_t groups,
                                              size_t *bytes)
 {
-    if (!h || !bytes || (transa != TCG_OP_N && transa != TCG_OP_T) || (transb != TCG_OP_N && transb != TCG_OP_T) || m < 0 || n < 0 || k < 0 ||
-        groups < 0 || groups > kLmMaxGroups)
+    if (!h || !bytes || (transa != TCG_OP_N && transa != TCG_OP_T) ||
+        (transb != TCG_OP_N && transb != TCG_OP_T) || m < 0 || n < 0 || k < 0 || groups < 0 ||
+        groups > kLmMaxGroups)
         return TCG_STATUS_INVALID_VALUE;
     *bytes = 0;
     if (m == 0 || n == 0)
@@ -676,59 +800,122 @@ tcgStatus_t tcg_epilogue_backward(tcgHandle_t h, tcgActivation_t activation, int
                                   int64_t lddd, const void *Z, int64_t ldz, tcgDataType_t type,
                                   void *dZ, int64_t lddz, float *dbias)
 {
-    if (!h || activation < TCG_ACT_NONE || activation > TCG_ACT_SILU || !valid_type(type))
+    const Gradient g{activation, m, n, groups, offsets, dD, lddd, Z, ldz, type, dZ, lddz, dbias};
+    if (!h)
         return TCG_STATUS_INVALID_VALUE;
-    if (!is_16bit(type))
-        return TCG_STATUS_NOT_SUPPORTED;
-    if (offsets) {
-        const tcgStatus_t st = check_groups(groups, offsets);
-        if (st != TCG_STATUS_SUCCESS)
-            return st;
-    } else if (groups != 1) {
-        return TCG_STATUS_INVALID_VALUE;
-    }
-    const bool need_z = activation != TCG_ACT_NONE;
-    if (m < 0 || n < 0 || bad_ld(lddd, m, 2) || (need_z && bad_ld(ldz, m, 2)) ||
-        (dZ && bad_ld(lddz, m, 2)))
-        return TCG_STATUS_INVALID_VALUE;
-    if (m > kMaxExtent || n > kMaxExtent)
-        return TCG_STATUS_NOT_SUPPORTED;
-    if (m == 0 || (!dZ && !dbias))
-        return TCG_STATUS_SUCCESS;
-    if (n > 0 && (!dD || !aligned16(dD) || (need_z && (!Z || !aligned16(Z))) || (dZ && !aligned16(dZ))))
-        return TCG_STATUS_INVALID_VALUE;
-    if (dbias && reinterpret_cast<uintptr_t>(dbias) % 4)
-        return TCG_STATUS_INVALID_VALUE;
-    tcgStatus_t st = bind_device(h);
+    tcgStatus_t st = check_gradient(g);
+    if (st != TCG_STATUS_SUCCESS || m == 0 || (!dZ && !dbias))
+        return st;
+    st = bind_device(h);
     if (st == TCG_STATUS_SUCCESS)
-        st = check_device(h, {n > 0 ? dD : nullptr, n > 0 && need_z ? Z : nullptr,
+        st = check_device(h, {n > 0 ? dD : nullptr, n > 0 && activation != TCG_ACT_NONE ? Z : nullptr,
                               n > 0 ? dZ : nullptr, dbias, offsets});
     if (st != TCG_STATUS_SUCCESS)
         return st;
     h->used = true;
-    // Columns per block: about 16 blocks of 256 rows per SM (a few at a time), 32 to 256
-    // columns each, 32 of them under way at a time.
-    const int64_t row_blocks = (m + 255) / 256;
-    int64_t chunk = n * row_blocks / (16 * static_cast<int64_t>(h->num_sms)) / 32 * 32;
-    chunk = chunk < 32 ? 32 : (chunk > 256 ? 256 : chunk);
-    while ((n + chunk - 1) / chunk > 65535)              // the grid's second dimension
-        chunk *= 2;
     void *ws = nullptr;
     if (dbias) {
-        st = acquire_ws(h, static_cast<size_t>((n + chunk - 1) / chunk + groups) * static_cast<size_t>(m) * 4,
-                        &ws);
+        st = acquire_ws(h, gradient_part_bytes(h, m, n, groups), &ws);
         if (st != TCG_STATUS_SUCCESS)
             return st;
     }
-    const cudaError_t e = launch_epi_backward(
-        activation, type == TCG_R_16BF, static_cast<int>(m), static_cast<int>(n),
-        static_cast<int>(groups), offsets, dD, lddd, need_z ? Z : nullptr, ldz, n > 0 ? dZ : nullptr,
-        lddz, dbias, static_cast<float *>(ws), static_cast<int>(chunk), h->stream);
-    h->launches += dbias ? 2 : 1;
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return TCG_STATUS_EXECUTION_FAILED;
+    return queue_gradient(h, g, ws);
+}
+
+tcgStatus_t tcg_linear_backward(tcgHandle_t h, tcgActivation_t activation, int64_t m, int64_t n,
+                                int64_t k, int64_t groups, const int64_t *offsets, const void *dD,
+                                int64_t lddd, const void *Z, int64_t ldz, const void *W, int64_t ldw,
+                                int64_t strideW, const void *X, int64_t ldx, tcgDataType_t type, void *dX,
+                                int64_t lddx, void *dW, int64_t lddw, int64_t stridedW, float *dbias)
+{
+    if (!h)
+        return TCG_STATUS_INVALID_VALUE;
+    Gradient g{activation, m, n, groups, offsets, dD, lddd, Z, ldz, type, nullptr, 0, dbias};
+    tcgStatus_t st = check_gradient(g);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    if (k < 0 || k > kMaxK)
+        return k < 0 ? TCG_STATUS_INVALID_VALUE : TCG_STATUS_NOT_SUPPORTED;
+    if ((dX && (bad_ld(ldw, k, 2) || bad_ld(lddx, k, 2) || !aligned16(W) || !aligned16(dX))) ||
+        (dW && (bad_ld(ldx, k, 2) || bad_ld(lddw, k, 2) || !aligned16(X) || !aligned16(dW))))
+        return TCG_STATUS_INVALID_VALUE;
+    if (offsets && ((dX && ((groups > 1 && strideW <= 0) || (strideW * 2) % 16)) ||
+                    (dW && ((groups > 1 && stridedW < (m > 0 ? (m - 1) * lddw + k : 0)) ||
+                            (stridedW * 2) % 16))))
+        return TCG_STATUS_INVALID_VALUE;
+    const bool sums = m > 0 && n > 0 && k > 0;
+    if (sums && ((dX && !W) || (dW && !X)))
+        return TCG_STATUS_INVALID_VALUE;
+    st = bind_device(h);
+    if (st == TCG_STATUS_SUCCESS)
+        st = check_device(h, {n > 0 && m > 0 ? dD : nullptr,
+                              n > 0 && m > 0 && activation != TCG_ACT_NONE ? Z : nullptr,
+                              sums && dX ? W : nullptr, sums && dW ? X : nullptr,
+                              n > 0 && k > 0 ? dX : nullptr, m > 0 && k > 0 ? dW : nullptr,
+                              m > 0 ? dbias : nullptr, offsets});
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    h->used = true;
+    const LayerPlan pl = layer_plan(h, activation != TCG_ACT_NONE, m, n, k, groups, offsets, dX, dW, dbias);
+    void *ws = nullptr;
+    if (pl.total) {
+        st = acquire_ws(h, pl.total, &ws);
+        if (st != TCG_STATUS_SUCCESS)
+            return st;
     }
+    uint8_t *at = static_cast<uint8_t *>(ws);
+    const void *dz = dD;
+    int64_t lddz = lddd;
+    if (pl.dz_bytes) {
+        dz = g.dZ = at;
+        lddz = g.lddz = pl.lddz;
+    }
+    if (pl.dz_bytes || pl.part_bytes) {
+        st = queue_gradient(h, g, at + pl.dz_bytes);
+        if (st != TCG_STATUS_SUCCESS)
+            return st;
+    }
+    void *tail = at + pl.dz_bytes + pl.part_bytes;
+    if (dX && n > 0 && k > 0) {
+        Product p = layer_dx(m, n, k, groups, offsets, type);
+        p.X = dz;
+        p.ldx = lddz;
+        p.W = W;
+        p.ldw = ldw;
+        p.strideW = strideW;
+        p.D = dX;
+        p.ldd = lddx;
+        st = queue(h, p, tail);
+        if (st != TCG_STATUS_SUCCESS)
+            return st;
+    }
+    if (dW && m > 0 && k > 0) {
+        Product p = layer_dw(m, n, k, groups, offsets, type);
+        p.X = dz;
+        p.ldx = lddz;
+        p.W = X;
+        p.ldw = ldx;
+        p.D = dW;
+        p.ldd = lddw;
+        p.strideD = stridedW;
+        st = queue(h, p, tail);
+    }
+    return st;
+}
+
+tcgStatus_t tcg_linear_backward_workspace_size(tcgHandle_t h, tcgActivation_t activation, int64_t m,
+                                               int64_t n, int64_t k, int64_t groups, int with_dX,
+                                               int with_dW, int with_dbias, size_t *bytes)
+{
+    if (!h || !bytes || activation < TCG_ACT_NONE || activation > TCG_ACT_SILU || m < 0 || n < 0 || k < 0 ||
+        groups < 0 || groups > kLmMaxGroups)
+        return TCG_STATUS_INVALID_VALUE;
+    const tcgStatus_t st = bind_device(h);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    static const int64_t some = 0;          // grouped: only whether offsets are set matters here
+    *bytes = layer_plan(h, activation != TCG_ACT_NONE, m, n, k, groups > 0 ? groups : 1,
+                        groups > 0 ? &some : nullptr, with_dX, with_dW, with_dbias).total;
     return TCG_STATUS_SUCCESS;
 }
 

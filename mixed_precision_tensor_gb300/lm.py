@@ -161,38 +161,47 @@ def linear(handle, x, w, bias=None, act="none", residual=None, beta=1.0, alpha=1
     return out
 
 
-def _grad_z(handle, dout, ldd, z, act, want_dz, want_dbias, groups, offsets, dbias, rows, n):
-    """(dz, its leading dimension, dbias); dz is dout where nothing has to be computed."""
-    dtype, dev = dout.dtype, dout.device
-    compute = want_dz and act != 0
-    if want_dbias:
-        shape = (n,) if offsets is None else (groups, n)
-        if dbias is None:
-            dbias = _empty(handle, shape, torch.float32, dev)
-        else:
-            _vector(dbias, "dbias", shape, (torch.float32,), dev)
-    elif not compute:
-        return dout, ldd, None
-    dz, ldz = _matrix(handle, None, "dz", rows, n, dtype, dev) if compute else (dout, ldd)
-    s = _lib().tcg_epilogue_backward(
-        handle.h, act, n, rows, groups, None if offsets is None else offsets.data_ptr(),
-        dout.data_ptr(), ldd, z.data_ptr() if act else None,
-        _rows(z, "z", rows, n, dtype, dev) if act else 0, _IN[dtype],
-        dz.data_ptr() if compute else None, ldz, dbias.data_ptr() if want_dbias else None)
-    if s:
-        raise _tcg.TcgError(s, "epilogue_backward")
-    return dz, ldz, dbias
-
-
-def _backward_args(dout, x, z, act, n):
+def _backward(handle, what, dout, x, w, z, act, want, dx, dw, dbias, offsets, e, n, ldw, stride_w):
+    """The one call behind the two backward passes."""
     t, k, dtype, dev = _input(x)
     ldx = _rows(x, "x", t, k, dtype, dev)
     ldd = _rows(dout, "dout", t, n, dtype, dev)
     code = _act(act)
-    if code and z is None:
-        raise ValueError("z, the pre-activation of the forward pass, is needed for act="
-                         f"{act!r}")
-    return t, k, dtype, dev, ldx, ldd, code
+    ldz = 8
+    if code:
+        if z is None:
+            raise ValueError(f"z, the pre-activation of the forward pass, is needed for act={act!r}")
+        ldz = _rows(z, "z", t, n, dtype, dev)
+    want_dx, want_dw, want_db = _want(want)
+    lddx = lddw = 8
+    stride_dw = 0
+    if want_dx:
+        dx, lddx = _matrix(handle, dx, "dx", t, k, dtype, dev)
+    if want_dw and offsets is None:
+        dw, lddw = _matrix(handle, dw, "dw", n, k, dtype, dev)
+    elif want_dw:
+        if dw is None:
+            lddw = (k + 7) // 8 * 8 or 8
+            stride_dw = n * lddw
+            dw = _empty(handle, (e, n, lddw), dtype, dev)
+            if lddw != k:
+                dw = dw[:, :, :k]
+        else:
+            lddw, stride_dw = _experts(dw, "dw", e, n, k, dtype, dev)
+    if want_db:
+        shape = (n,) if offsets is None else (e, n)
+        if dbias is None:
+            dbias = _empty(handle, shape, torch.float32, dev)
+        else:
+            _vector(dbias, "dbias", shape, (torch.float32,), dev)
+    s = _lib().tcg_linear_backward(
+        handle.h, code, n, t, k, e, None if offsets is None else offsets.data_ptr(), dout.data_ptr(), ldd,
+        z.data_ptr() if code else None, ldz, w.data_ptr(), ldw, stride_w, x.data_ptr(), ldx, _IN[dtype],
+        dx.data_ptr() if want_dx else None, lddx, dw.data_ptr() if want_dw else None, lddw, stride_dw,
+        dbias.data_ptr() if want_db else None)
+    if s:
+        raise _tcg.TcgError(s, what)
+    return (dx if want_dx else None, dw if want_dw else None, dbias if want_db else None)
 
 
 def _want(want):
@@ -209,25 +218,9 @@ def linear_backward(handle, dout, x, w, z=None, act="none", want=("dx", "dw", "d
     unrounded dz).  The residual's gradient is beta * dout.  ``want`` names what is computed;
     the result is (dx, dw, dbias) with None for the others.  Outputs are made where not given.
     """
-    n = w.shape[0]
-    t, k, dtype, dev, ldx, ldd, code = _backward_args(dout, x, z, act, n)
-    ldw = _rows(w, "w", n, k, dtype, dev)
-    want_dx, want_dw, want_db = _want(want)
-    dz, ldz, dbias = _grad_z(handle, dout, ldd, z, code, want_dx or want_dw, want_db, 1, None, dbias, t, n)
-    ty, lib = _IN[dtype], _lib()
-    if want_dx:
-        dx, ld = _matrix(handle, dx, "dx", t, k, dtype, dev)
-        s = lib.tcg_gemm_ex(handle.h, 0, 0, k, t, n, 1.0, w.data_ptr(), ty, ldw, dz.data_ptr(), ty, ldz,
-                            0.0, dx.data_ptr(), ty, ld, 0)
-        if s:
-            raise _tcg.TcgError(s, "linear_backward dx")
-    if want_dw:
-        dw, ld = _matrix(handle, dw, "dw", n, k, dtype, dev)
-        s = lib.tcg_gemm_epilogue(handle.h, 0, 1, k, n, t, 1.0, x.data_ptr(), ldx, dz.data_ptr(), ldz, ty,
-                                  dw.data_ptr(), ty, ld, None)
-        if s:
-            raise _tcg.TcgError(s, "linear_backward dw")
-    return (dx if want_dx else None, dw if want_dw else None, dbias if want_db else None)
+    n, k = w.shape
+    ldw = _rows(w, "w", n, k, x.dtype, x.device)
+    return _backward(handle, "linear_backward", dout, x, w, z, act, want, dx, dw, dbias, None, 1, n, ldw, 0)
 
 
 def _check_offsets(offsets, e, device):
@@ -271,30 +264,11 @@ def grouped_linear_backward(handle, dout, x, w, offsets, z=None, act="none",
     """
     if w.dim() != 3:
         raise ValueError("w must be experts x n x k")
-    e, n = w.shape[0], w.shape[1]
-    t, k, dtype, dev, ldx, ldd, code = _backward_args(dout, x, z, act, n)
-    ldw, stride = _experts(w, "w", e, n, k, dtype, dev)
-    _check_offsets(offsets, e, dev)
-    want_dx, want_dw, want_db = _want(want)
-    dz, ldz, dbias = _grad_z(handle, dout, ldd, z, code, want_dx or want_dw, want_db, e, offsets, dbias, t,
-                             n)
-    ty, lib = _IN[dtype], _lib()
-    if want_dx:
-        dx, ld = _matrix(handle, dx, "dx", t, k, dtype, dev)
-        s = lib.tcg_gemm_grouped(handle.h, 0, k, t, n, e, offsets.data_ptr(), 1.0, w.data_ptr(), ldw,
-                                 stride, dz.data_ptr(), ldz, ty, dx.data_ptr(), ty, ld, None)
-        if s:
-            raise _tcg.TcgError(s, "grouped_linear_backward dx")
-    if want_dw:
-        if dw is None:
-            per = -(-k // 8) * 8
-            dw = _empty(handle, (e, n, per), dtype, dev)[:, :, :k]
-        lddw, strided = _experts(dw, "dw", e, n, k, dtype, dev)
-        s = lib.tcg_gemm_grouped_k(handle.h, k, n, t, e, offsets.data_ptr(), 1.0, x.data_ptr(), ldx,
-                                   dz.data_ptr(), ldz, ty, dw.data_ptr(), ty, lddw, strided)
-        if s:
-            raise _tcg.TcgError(s, "grouped_linear_backward dw")
-    return (dx if want_dx else None, dw if want_dw else None, dbias if want_db else None)
+    e, n, k = w.shape
+    ldw, stride = _experts(w, "w", e, n, k, x.dtype, x.device)
+    _check_offsets(offsets, e, x.device)
+    return _backward(handle, "grouped_linear_backward", dout, x, w, z, act, want, dx, dw, dbias, offsets, e, n,
+                     ldw, stride)
 
 
 def _xent_args(x, w, targets):

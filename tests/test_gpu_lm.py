@@ -181,6 +181,41 @@ def test_linear_backward_wants(handle):
     assert dx.shape == (0, 64) and not dw.any() and not db.any()
 
 
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("experts", [0, 5])
+def test_layer_backward_in_the_callers_workspace(cuda_device, act, experts):
+    """The workspace that the library asks for is enough, and one that is smaller is refused
+    before anything is queued."""
+    g = gen_of(8)
+    t, n, k = 300, 264, 1160
+    x, d, z = randn(g, t, k), randn(g, t, n), randn(g, t, n)
+    w = randn(g, *((experts,) if experts else ()), n, k)
+    off = offsets_of([100, 0, 7, 150, 43], 0) if experts else None
+    h = tcg.Handle()
+    run = (lambda **kw: tcg.grouped_linear_backward(h, d, x, w, off, z=z, act=act, **kw)) if experts else \
+        (lambda **kw: tcg.linear_backward(h, d, x, w, z=z, act=act, **kw))
+    want = run()
+    for outputs in ("dx", "dw", "dbias"), ("dx",), ("dw",), ("dbias",):
+        need = tcg.tcg_linear_backward_workspace_size(
+            h.h, ACTS.index(act), n, t, k, experts, "dx" in outputs, "dw" in outputs, "dbias" in outputs)
+        if not need:
+            continue
+        space = torch.full((need + 256,), 0xff, dtype=torch.uint8, device="cuda")
+        tcg.check(tcg.tcg_set_workspace(h.h, space, need))
+        got = run(want=outputs)
+        for name, a, b in zip(("dx", "dw", "dbias"), got, want):
+            assert a is None or same_bits(a, b), name
+        assert bool((space[need:] == 0xff).all())
+        tcg.check(tcg.tcg_set_workspace(h.h, space, need - 256))
+        before = tcg.tcg_launch_count(h.h)
+        with pytest.raises(tcg.TcgError):
+            run(want=outputs)
+        assert tcg.tcg_launch_count(h.h) == before
+        tcg.check(tcg.tcg_set_workspace(h.h, None, 0))
+    tcg.check(tcg.tcg_get_device_error(h.h))
+    h.close()
+
+
 # ----------------------------------------------------------------------------- grouped
 GROUPS = [[5], [0, 3, 0], [1, 1, 1, 1], [64, 0, 65, 63, 1], [300, 7, 0, 129], [0, 0, 0],
           [33, 128, 256, 2, 90], [3] * 70, [1] * 200 + [0] * 184, [700, 1, 64, 127]]
@@ -229,6 +264,28 @@ def test_grouped_forward_and_backward(handle, i, dtype, lead, spare):
         grads, bounds = ref.linear_backward(dout[a:b], x[a:b], w[j], z[a:b], act)
         for name, got, gw, eb in zip(("dx", "dw", "dbias"), (dx[a:b], dw[j], db[j]), grads, bounds):
             ref.within(got, gw, eb, f"{name} of expert {j}")
+
+
+def test_grouped_backward_from_its_parts(handle):
+    """The epilogue's gradient and the two products, called one by one, give the bits of the
+    one call behind grouped_linear_backward."""
+    g = gen_of(9)
+    e, t, n, k = 5, 300, 264, 136
+    x, d, z, w = randn(g, t, k), randn(g, t, n), randn(g, t, n), randn(g, e, n, k)
+    off = offsets_of([100, 0, 7, 150, 43], 0)
+    want = tcg.grouped_linear_backward(handle, d, x, w, off, z=z, act="gelu")
+    dz, dx, dw = torch.empty_like(d), torch.empty_like(x), torch.empty_like(w)
+    db = torch.empty(e, n, device="cuda")
+    ty = tcg.TCG_R_16BF
+    tcg.check(tcg.tcg_epilogue_backward(handle.h, ACTS.index("gelu"), n, t, e, off, d, n, z, n, ty, dz, n, db))
+    tcg.check(tcg.tcg_gemm_grouped(handle.h, 0, k, t, n, e, off, 1.0, w, k, n * k, dz, n, ty, dx, ty, k))
+    tcg.check(tcg.tcg_gemm_grouped_k(handle.h, k, n, t, e, off, 1.0, x, k, dz, n, ty, dw, ty, k, n * k))
+    tcg.check(tcg.tcg_get_device_error(handle.h))
+    for name, a, b in zip(("dx", "dw", "dbias"), (dx, dw, db), want):
+        assert same_bits(a, b), name
+    dzw = d.double() * ref.slope(z.double(), "gelu")
+    err = d.double().abs() * ref.FN * (1 + z.double().abs())
+    ref.within(dz, dzw, err + ref.U[BF16] * (dzw.abs() + err) + ref.TINY[BF16], "dz")
 
 
 @pytest.mark.parametrize("size", list(range(1, 70)) + [127, 128, 129, 191])

@@ -96,6 +96,30 @@ def test_epilogue_gradient_refuses(handle, kw, status):
     assert backward(handle, **kw) == status
 
 
+def layer_backward(h, act=1, m=64, n=64, k=64, groups=1, offsets=None, dD=PA, lddd=64, Z=PB, ldz=64, W=PD,
+                   ldw=64, stride=4096, X=PA, ldx=64, ty=BF16, dX=PB, lddx=64, dW=PD, lddw=64, strided=4096,
+                   dbias=PX):
+    return tcg.tcg_linear_backward(h, act, m, n, k, groups, offsets, dD, lddd, Z, ldz, W, ldw, stride, X, ldx,
+                                   ty, dX, lddx, dW, lddw, strided, dbias)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(act=-1), INV), (dict(act=5), INV), (dict(ty=F32), NSUP), (dict(ty=9), INV), (dict(m=-1), INV),
+    (dict(n=-1), INV), (dict(k=-1), INV), (dict(k=(1 << 30) + 8, ldw=1 << 31, ldx=1 << 31, lddx=1 << 31,
+                                               lddw=1 << 31), NSUP),
+    (dict(groups=2), INV), (dict(groups=0, offsets=PX), INV), (dict(groups=385, offsets=PX), NSUP),
+    (dict(groups=2, offsets=PX + 4), INV), (dict(groups=2, offsets=PX, stride=0), INV),
+    (dict(groups=2, offsets=PX, stride=4100), INV), (dict(groups=2, offsets=PX, strided=4032), INV),
+    (dict(groups=2, offsets=PX, strided=4100), INV), (dict(dD=None), INV), (dict(dD=PA + 4), INV),
+    (dict(lddd=60), INV), (dict(Z=None), INV), (dict(ldz=56), INV), (dict(W=None), INV), (dict(W=PD + 8), INV),
+    (dict(ldw=56), INV), (dict(X=None), INV), (dict(X=PA + 2), INV), (dict(ldx=60), INV),
+    (dict(dX=PB + 4), INV), (dict(lddx=60), INV), (dict(dW=PD + 4), INV), (dict(lddw=56), INV),
+    (dict(dbias=PX + 2), INV),
+])
+def test_layer_gradient_refuses(handle, kw, status):
+    assert layer_backward(handle, **kw) == status
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(rows=-1), INV), (dict(vocab=0), INV), (dict(k=0), INV), (dict(ldx=56), INV), (dict(ldw=60), INV),
     (dict(ty=F32), NSUP), (dict(ty=7), INV), (dict(X=None), INV), (dict(W=PB + 4), INV),

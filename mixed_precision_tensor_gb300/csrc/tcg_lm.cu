@@ -49,8 +49,8 @@ struct LmPlan {
 struct LmCtl {
     uint64_t full[kLmMaxStages];
     uint64_t empty[kLmMaxStages];
-    uint64_t acc_full[4];
-    uint64_t acc_empty[4];
+    uint64_t acc_full[kLmMaxAccs];
+    uint64_t acc_empty[kLmMaxAccs];
     uint64_t drain;
     uint32_t tmem_base;
     volatile int abort_flag;
@@ -845,23 +845,22 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
             ++it;
         };
         // A cut tile's piece is stored: whoever stores the last one of a tile part adds them
-        // all, in K order whatever the timing, and finishes the tile.
+        // all, in K order whatever the timing, and finishes the tile.  One thread's fence,
+        // after the barrier, orders the stores of all.
         auto arrive = [&]() {
-            __threadfence();
             named_barrier_sync(bar_id, 128);
             if (part_leader) {
                 uint32_t *cnt = p.cnt + (w.counter * 2 + static_cast<int>(rank)) * kParts + part;
+                fence_acq_rel_gpu();
                 const bool last = atomicAdd(cnt, 1u) == static_cast<uint32_t>(w.pieces - 1);
                 if (last)
                     *cnt = 0u;                             // every piece has arrived
                 ctl->last_arrival[part] = last;
-                __threadfence();
+                fence_acq_rel_gpu();
             }
             named_barrier_sync(bar_id, 128);
             const bool last = ctl->last_arrival[part] != 0;
             named_barrier_sync(bar_id, 128);               // the flag is free again
-            if (last)
-                __threadfence();
             return last;
         };
         auto slot_ptr = [&](int slot) {
@@ -1046,6 +1045,7 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             z[j] = 0.0f;
+#pragma unroll 2
                         for (int i = 0; i < w.pieces; ++i) {
                             const float *q = slot_ptr(piece_slot(i)) + c * 32 * kBM + rl;
 #pragma unroll

@@ -15,6 +15,7 @@ namespace tcg {
 constexpr int kLmMaxGroups = 384;      // experts of one grouped call (a table in shared memory)
 constexpr int kLmCounters = 1024;      // split counters of a handle: 4 per cut tile, one tile per pair at most
 constexpr int kLmMaxStages = 12;
+constexpr int kLmMaxAccs = 16;
 // Shared memory: the operand ring, and (tokens on the rows) 2 KiB of staging per epilogue
 // warp, through which a warp's 32 rows leave and arrive in runs of 64 bytes.
 constexpr int kLmDataBytes = 224 * 1024;
@@ -99,7 +100,10 @@ struct LmCfg {
     static constexpr int kFit = kRingBytes / kStageBytes;
     // wide 256, 128, 64: 6, 8, 10; narrow 256, 128, 64, 32: 7, 9, 11, 12
     static constexpr int kStages = kFit < kLmMaxStages ? kFit : kLmMaxStages;
-    static constexpr int kAccBufs = kTmemCols / BN < 4 ? kTmemCols / BN : 4;
+    // All of TMEM.  The epilogue falls behind when a pair's first piece of a cut tile is
+    // short: the fence that reports the piece waits for the loads under way too, 12 us while
+    // the second piece streams in (23 tokens, K = 16384).
+    static constexpr int kAccBufs = kTmemCols / BN;
 };
 
 // Bytes of the partial sums: two 256 x BN slots per pair.

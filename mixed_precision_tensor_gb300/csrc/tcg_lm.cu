@@ -275,7 +275,12 @@ __device__ __forceinline__ void make_plan(const LmArgs &p, LmCtl *ctl, int lane,
             const uint32_t nkb = static_cast<uint32_t>(p.num_k_blocks);
             int splits = 0;
             int share = max(static_cast<int>((rest * nkb + pairs - 1) / pairs), p.min_share);
-            if (p.align_splits) {
+            // One piece of one tile for each pair, where that leaves few pairs idle (1500 x 1000
+            // outputs over K = 8192: 37 -> 30 us), or tokens are on the columns: HBM bounds those
+            // loads, and fewer pairs can ask for them as fast (9 tokens, 4096 x 4096: 13.7 -> 12.1
+            // us; 100 tokens 21.9 -> 17.7).
+            const int busy = pairs / rest * rest;
+            if (p.align_splits || (WIDE ? 20 * busy >= 17 * pairs : busy > rest)) {
                 share = max(static_cast<int>((nkb + pairs / rest - 1) / (pairs / rest)), p.min_share);
                 splits = static_cast<int>((nkb + share - 1) / share);
             }
@@ -949,23 +954,32 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                     break;
                 const int ncol = w.col_end - col_part;
                 if (cut) {
+                    // 16 columns at a time, whether all hold tokens or not: loads that each
+                    // ask for themselves wait for each other (100 tokens, 4096 x 4096: 27 us)
                     float *sl = slot_ptr(w.slot) + rl;     // [column][row]
 #pragma unroll
-                    for (int j = 0; j < kPart; ++j)
-                        if (j < ncol)
-                            __stcg(sl + j * kBM, sum[j]);
+                    for (int c = 0; c < kPart; c += 16)
+                        if (c < ncol) {
+#pragma unroll
+                            for (int j = c; j < c + 16; ++j)
+                                __stcg(sl + j * kBM, sum[j]);
+                        }
                     if (!arrive())
                         continue;
 #pragma unroll
-                    for (int j = 0; j < kPart; ++j)
-                        sum[j] = 0.0f;
-#pragma unroll 4
-                    for (int i = 0; i < w.pieces; ++i) {
-                        const float *s = slot_ptr(piece_slot(i)) + rl;
+                    for (int c = 0; c < kPart; c += 16) {
+                        if (c >= ncol)
+                            break;
 #pragma unroll
-                        for (int j = 0; j < kPart; ++j)
-                            if (j < ncol)
-                                sum[j] += __ldcg(s + j * kBM);
+                        for (int j = c; j < c + 16; ++j)
+                            sum[j] = 0.0f;
+#pragma unroll 4
+                        for (int i = 0; i < w.pieces; ++i) {
+                            const float *s = slot_ptr(piece_slot(i)) + rl + c * kBM;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                sum[c + j] += __ldcg(s + j * kBM);
+                        }
                     }
                 }
                 if constexpr (EPI == kEpiNarrow) {

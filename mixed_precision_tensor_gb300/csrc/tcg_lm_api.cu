@@ -5,6 +5,7 @@
 // Every call checks its arguments on the host, binds the handle, checks that its pointers
 // are device memory, and queues kernels of tcg_lm.cu on the handle's stream.
 
+#include <cmath>
 #include <cstring>
 #include <initializer_list>
 
@@ -80,7 +81,15 @@ int64_t max_tiles(const Product &p, int epi, int bn)
 
 // Saving in K blocks that pays for joining partial sums of a 256 x bn tile.
 int gain_of(int bn) { return bn * 24 / 256 < 8 ? 8 : bn * 24 / 256; }
-constexpr int kMinShare = 4;                // fewest K blocks of a cut tile per pair
+// Fewest K blocks of a cut tile per pair.  Whoever joins a tile's pieces reads bn / 2 KiB of
+// each into its SM, and an SM loads 16 + bn / 16 KiB for a K block, both at L2's rate: the
+// sum of nkb / pieces blocks and as many pieces is least at pieces^2 = nkb (32 / bn + 1 / 8).
+constexpr int kMinShare = 4;
+int min_share(int64_t nkb, int bn)
+{
+    const int s = static_cast<int>(std::ceil(std::sqrt(static_cast<double>(nkb) / (32.0 / bn + 0.125))));
+    return s > kMinShare ? s : kMinShare;
+}
 
 Shape shape_of(tcgContext *h, const Product &p)
 {
@@ -116,8 +125,7 @@ Shape shape_of(tcgContext *h, const Product &p)
                 const double cost = bn == 256 ? 1.0 : (bn == 128 ? 0.75 : 0.625);
                 const int64_t tiles = max_tiles(p, s.epi, bn), rest = tiles % P;
                 int64_t share = ceil_div(rest * nkb, P);
-                share = share < kMinShare ? kMinShare : share;
-                share = share < ceil_div(nkb, 8) ? ceil_div(nkb, 8) : share;
+                share = share < min_share(nkb, bn) ? min_share(nkb, bn) : share;
                 double t = static_cast<double>(tiles / P * nkb);
                 if (rest)
                     t += nkb - share >= gain_of(bn) ? static_cast<double>(share) + gain_of(bn) / cost
@@ -131,11 +139,7 @@ Shape shape_of(tcgContext *h, const Product &p)
         }
     }
     s.tiles = max_tiles(p, s.epi, s.bn);
-    // No more than 8 pieces of a wide tile (whoever joins them reads them one after the other:
-    // 3000 x 8192 outputs over K = 8192, 4 tiles cut in 19 pieces each 283 us, in 8 254 us) or
-    // 16 of a narrow one.
-    const int64_t least = ceil_div(nkb, s.epi == kEpiWide ? 8 : 16);
-    s.share = static_cast<int>(least > kMinShare ? least : kMinShare);
+    s.share = min_share(nkb, s.bn);
     s.gain = gain_of(s.bn);
     const bool linear = s.epi == kEpiNarrow || s.epi == kEpiWide || s.epi == kEpiXentNarrow;
     s.cut = linear && !p.ragged_k && !(s.epi == kEpiNarrow && s.bn == 256) && nkb - s.share >= s.gain &&
@@ -153,7 +157,7 @@ Shape shape_of(tcgContext *h, const Product &p)
 }
 
 bool few(const Product &p);
-bool few_tokens(int64_t tokens, int64_t k);
+bool few_tokens(int64_t tokens, int64_t feats, int64_t k);
 
 size_t product_ws(tcgContext *h, const Product &p)
 {
@@ -249,11 +253,14 @@ tcgStatus_t queue(tcgContext *h, const Product &p, void *ws, LmArgs a = LmArgs{}
     return TCG_STATUS_SUCCESS;
 }
 
-// Few enough tokens, and X small enough to stay in an SM's cache (where it does not, every
-// SM reads the same lines of L2 again and again).
-bool few_tokens(int64_t tokens, int64_t k)
+// Few enough tokens that one pass over the weights is faster than tiles: one, two of a K that
+// stays in an SM's cache (k = 8192: 16.5 us, by tiles 17.5; 16384: 31.5 and 27.7), or up to four
+// where the weights are few and a call's start counts (1024 x 1024: 4.3 and 6.8 us; 4096 x 4096:
+// 12.6 and 12.2; 11008 x 4096: 29.9 and 22.7).
+bool few_tokens(int64_t tokens, int64_t feats, int64_t k)
 {
-    return tokens == 1 || (tokens <= kLmFewTokens && tokens * k <= 32768);
+    return tokens == 1 || (tokens == 2 && k <= 8192) ||
+           (tokens <= kLmFewTokens && tokens * k <= 32768 && feats * k <= (int64_t(1) << 23));
 }
 
 // Whether a product runs as a pass over the weights (tcg_lm_few.cu): K-contiguous operands
@@ -263,8 +270,9 @@ bool few(const Product &p)
     if (p.ragged_k || !p.x_kmajor || !p.w_kmajor || p.k == 0 || p.lm_epi >= 0 || p.alpha_dev)
         return false;
     if (!p.offsets)
-        return few_tokens(p.tokens, p.k);
-    // 64 experts of 2048 x 2048: 30 rows 35 us so, 42 us by tiles; 60 rows 61 and 54.
+        return few_tokens(p.tokens, p.feats, p.k);
+    // 64 experts of 2048 x 2048: 16 rows 26 us so, 31 us by tiles; 30 rows 40 and 41; 60 rows 60
+    // and 60.
     return p.tokens <= kLmFewRows && (p.tokens <= 4 || 2 * p.tokens <= p.groups);
 }
 
@@ -401,7 +409,7 @@ constexpr int64_t kXentNarrowRows = 32;
 // the partial sums of cut tiles.
 int64_t xent_slots(tcgContext *h, int64_t rows, int64_t vocab, int64_t k)
 {
-    if (few_tokens(rows, k))               // blocks of tcg_lm_few.cu
+    if (few_tokens(rows, vocab, k))        // blocks of tcg_lm_few.cu
         return h->num_sms;
     return lm_stat_slots(vocab, rows <= kXentNarrowRows);
 }
@@ -526,7 +534,7 @@ Product xent_forward_product(const Xent &x)
 size_t xent_forward_bytes(tcgContext *h, const Xent &x)
 {
     return xent_stats_bytes(h, x.rows, x.vocab, x.k) + pad256(static_cast<size_t>(x.rows) * 4) +
-           (few_tokens(x.rows, x.k) ? 0 : product_ws(h, xent_forward_product(x)));
+           (few_tokens(x.rows, x.vocab, x.k) ? 0 : product_ws(h, xent_forward_product(x)));
 }
 
 // Columns per block of the epilogue's gradient: about 16 blocks of 256 rows per SM (a few at a
@@ -964,7 +972,7 @@ tcgStatus_t tcg_xent_forward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_t
     a.vocab = vocab;
     a.stats = static_cast<float2 *>(ws);
     a.target_logit = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + stats_bytes);
-    if (few_tokens(rows, k)) {
+    if (few_tokens(rows, vocab, k)) {
         LmFewArgs f;
         std::memset(&f, 0, sizeof f);
         f.feats = vocab;

@@ -48,7 +48,7 @@ def same_bits(a, b):
 # ------------------------------------------------------------------------------ linear
 SIZES = [(1, 8, 8), (1, 4096, 4096), (4, 301, 523), (8, 1000, 264), (6, 40, 300), (2, 13, 5), (3, 264, 72), (17, 300, 1000), (33, 256, 64),
          (64, 1000, 1032), (100, 520, 200), (129, 2056, 264), (257, 513, 127), (300, 77, 2048),
-         (700, 1288, 320), (200, 1000, 4096), (2000, 4096, 256), (5, 256, 20000)]
+         (700, 1288, 320), (200, 1000, 4096), (2000, 4096, 256), (5, 256, 20000), (2, 1032, 8200), (4, 2056, 5000)]
 
 
 @pytest.mark.parametrize("t,n,k", SIZES)
@@ -366,7 +366,7 @@ def xent_case(t, v, k, dtype, seed=0, std=1.5):
 
 @pytest.mark.parametrize("t,v,k", [(1, 1, 8), (1, 2, 5), (1, 1000, 64), (3, 257, 72), (5, 30011, 200), (8, 999, 264),
                                    (17, 256, 200), (32, 3001, 1032), (130, 511, 64), (257, 1001, 136), (300, 5003, 256),
-                                   (64, 50021, 128), (515, 300, 1000)])
+                                   (64, 50021, 128), (515, 300, 1000), (3, 9001, 1032)])
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_xent(handle, t, v, k, dtype):
     x, w, target, dloss = xent_case(t, v, k, dtype)

@@ -5,7 +5,7 @@
 //
 //   warp 0 (one lane)   TMA producer into a ring of 128-byte-swizzled stages (64 K elements
 //                       of 128 rows of A and BN / 2 rows of B per CTA)
-//   warp 1 (one lane)   tcgen05.mma into TMEM accumulators (up to four)
+//   warp 1 (one lane)   tcgen05.mma into as many TMEM accumulators as fit
 //   warps 2-9           epilogue: TMEM -> registers -> memory, one accumulator row a thread
 //
 // The epilogues (LmEpi):

@@ -5,6 +5,7 @@
 // Every call checks its arguments on the host, binds the handle, checks that its pointers
 // are device memory, and queues kernels of tcg_lm.cu on the handle's stream.
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <initializer_list>
@@ -91,6 +92,20 @@ int min_share(int64_t nkb, int bn)
     return s > kMinShare ? s : kMinShare;
 }
 
+// KiB that the busiest SM loads for `tiles` 256 x bn tiles, a last wave that fills less than
+// half of the pairs cut into one piece for each.
+double load_kib(int64_t tiles, int64_t nkb, int bn, int64_t pairs)
+{
+    const int64_t rest = tiles % pairs;
+    const double block = 16.0 + bn / 16.0;
+    const int64_t most = rest ? std::min(pairs / rest, nkb / min_share(nkb, bn)) : 1;
+    double kib = static_cast<double>(tiles / pairs * nkb) * block;
+    if (rest)
+        kib += static_cast<double>(most > 1 ? ceil_div(nkb, most) : nkb) * block +
+               (most > 1 ? static_cast<double>(most) * bn / 2 : 0.0);
+    return kib;
+}
+
 Shape shape_of(tcgContext *h, const Product &p)
 {
     Shape s;
@@ -103,15 +118,22 @@ Shape shape_of(tcgContext *h, const Product &p)
         s.bn = p.lm_epi == kEpiXentNarrow ? 32 : 256;
     } else {
         const int64_t per = p.offsets ? p.tokens / p.groups : p.tokens;
-        if (p.x_kmajor && per <= (p.offsets ? 16 : 128)) {
+        const int narrow_bn = per <= 32 ? 32 : (per <= 64 ? 64 : 128);
+        // Tokens on the columns, tiles cut along K.  Of few features, 64 wide tiles of tokens on
+        // the rows can be the lesser load (100 tokens, 512 x 8192: 20 us with tokens on the
+        // columns, 14 us so; 4096 x 4096: 17.6 and 21.6).  Experts: few rows each, or so few
+        // tiles that four pairs share one (4 experts of 1024 x 4096, 50 rows each: 16 us so, 23 us
+        // by the rule below; 2 of 4096 x 4096, 120 rows, two pairs to a tile: 25 to 31 and 25 to 26).
+        const bool scarce = 4 * p.groups * ceil_div(p.feats, 256) <= P;
+        if (p.x_kmajor && per <= (p.offsets && !scarce ? 16 : 128) &&
+            (p.offsets || !p.w_kmajor || load_kib(ceil_div(p.feats, 256), nkb, narrow_bn, P) <=
+                                             load_kib(ceil_div(p.feats, 64), nkb, 64, P))) {
             s.epi = kEpiNarrow;
-            s.bn = per <= 32 ? 32 : (per <= 64 ? 64 : 128);
+            s.bn = narrow_bn;
         } else if (p.offsets && p.x_kmajor && per < 2048) {
             // Groups' last tiles at the width that they have.  Narrower tiles read a group's
             // weights once for each of them (8 experts of 4096 x 4096, 62 rows each: 64 wide
-            // 64 us, 256 wide 52 us; with a skewed router 69 and 53), but can be cut along K,
-            // which few rows of few experts want (16 of 1024 x 1032, 200 rows: 32 wide 11 us,
-            // 256 wide 14 us).
+            // 64 us, 256 wide 52 us; with a skewed router 69 and 53).
             s.epi = kEpiNarrow;
             s.bn = 256;
         } else {

@@ -48,7 +48,8 @@ def same_bits(a, b):
 # ------------------------------------------------------------------------------ linear
 SIZES = [(1, 8, 8), (1, 4096, 4096), (4, 301, 523), (8, 1000, 264), (6, 40, 300), (2, 13, 5), (3, 264, 72), (17, 300, 1000), (33, 256, 64),
          (64, 1000, 1032), (100, 520, 200), (129, 2056, 264), (257, 513, 127), (300, 77, 2048),
-         (700, 1288, 320), (200, 1000, 4096), (2000, 4096, 256), (5, 256, 20000), (2, 1032, 8200), (4, 2056, 5000)]
+         (700, 1288, 320), (200, 1000, 4096), (2000, 4096, 256), (5, 256, 20000), (2, 1032, 8200), (4, 2056, 5000),
+         (100, 512, 8192), (90, 1000, 4104), (45, 2000, 4096), (1500, 1000, 4096)]
 
 
 @pytest.mark.parametrize("t,n,k", SIZES)
@@ -353,6 +354,27 @@ def test_grouped_few_rows(handle, sizes):
         if b > a:
             want, _, eo, _ = ref.linear(x[a:b], w[j], None, "silu", None, 0.0, 1.0, F32)
             ref.within(first[a:b], want, eo)
+
+
+@pytest.mark.parametrize("sizes", [[40, 0, 70, 66], [130, 0, 101], [60], [1, 128, 3, 2], [200, 1], [25] * 8])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_grouped_tiles_of_few_experts(handle, sizes, dtype):
+    """Few tiles of a long K: pieces of one tile on several pairs, alike from call to call."""
+    g = gen_of(len(sizes))
+    rows, e, n, k = sum(sizes), len(sizes), 264, 2312
+    off = offsets_of(sizes, 0)
+    x, w = randn(g, rows, k, dtype=dtype), randn(g, e, n, k, dtype=dtype, std=k ** -0.5)
+    bias, z = randn(g, e, n, dtype=F32), torch.empty(rows, n, dtype=dtype, device="cuda")
+    first = tcg.grouped_linear(handle, x, w, off, bias=bias, act="gelu", z=z)
+    for _ in range(4):
+        assert same_bits(tcg.grouped_linear(handle, x, w, off, bias=bias, act="gelu"), first)
+    tcg.check(tcg.tcg_get_device_error(handle.h))
+    for j in range(e):
+        a, b = off[j].item(), off[j + 1].item()
+        if b > a:
+            want, zw, eo, ez = ref.linear(x[a:b], w[j], bias[j], "gelu", None, 0.0, 1.0, dtype)
+            ref.within(first[a:b], want, eo)
+            ref.within(z[a:b], zw, ez + ref.U[dtype] * (zw.abs() + ez) + ref.TINY[dtype], "z")
 
 
 # ----------------------------------------------------------------------- cross entropy

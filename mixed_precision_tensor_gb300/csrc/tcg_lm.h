@@ -100,9 +100,9 @@ struct LmCfg {
     static constexpr int kFit = kRingBytes / kStageBytes;
     // wide 256, 128, 64: 6, 8, 10; narrow 256, 128, 64, 32: 7, 9, 11, 12
     static constexpr int kStages = kFit < kLmMaxStages ? kFit : kLmMaxStages;
-    // All of TMEM.  The epilogue falls behind when a pair's first piece of a cut tile is
-    // short: the fence that reports the piece waits for the loads under way too, 12 us while
-    // the second piece streams in (23 tokens, K = 16384).
+    // All of TMEM.  The epilogue falls behind where a pair has pieces of two tiles: the fence
+    // that reports the first waits for the loads under way too, 12 us while the second streams
+    // in (23 tokens, K = 16384; four accumulators 31.1 us a call, sixteen 30.8).
     static constexpr int kAccBufs = kTmemCols / BN;
 };
 

@@ -122,7 +122,9 @@ tcgStatus_t tcg_create(tcgHandle_t *h);
 tcgStatus_t tcg_destroy(tcgHandle_t h);
 
 /* Set the stream (a cudaStream_t passed as void*) for later calls; NULL is the
- * legacy default stream.  Errors: INVALID_VALUE if h is NULL. */
+ * legacy default stream.  The handle's workspace and device words go with it, so the
+ * new stream's work must come after what the handle has queued on the old one (an
+ * event, or a synchronisation).  Errors: INVALID_VALUE if h is NULL. */
 tcgStatus_t tcg_set_stream(tcgHandle_t h, void *stream);
 
 /* Give the handle caller-owned device scratch memory for the TF32 path (which

@@ -112,6 +112,20 @@ tcgStatus_t check_args(const Problem &p)
     return TCG_STATUS_SUCCESS;
 }
 
+// Zeroes device words, done when this returns.  On a stream of its own: the legacy default
+// stream is not ordered with the non-blocking streams that calls may run on, and the clear
+// would wait there behind whatever the caller has queued.
+static bool clear_words(void *words, size_t bytes)
+{
+    cudaStream_t s = nullptr;
+    if (cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) != cudaSuccess)
+        return false;
+    const bool ok = cudaMemsetAsync(words, 0, bytes, s) == cudaSuccess &&
+                    cudaStreamSynchronize(s) == cudaSuccess;
+    cudaStreamDestroy(s);
+    return ok;
+}
+
 tcgStatus_t bind_device(tcgContext *h)
 {
     int dev = -1;
@@ -145,7 +159,7 @@ tcgStatus_t bind_device(tcgContext *h)
         cudaGetLastError();
         return TCG_STATUS_ALLOC_FAILED;
     }
-    if (cudaMemset(err, 0, kErrAreaBytes) != cudaSuccess) {
+    if (!clear_words(err, kErrAreaBytes)) {
         cudaFree(err);
         cudaGetLastError();
         return TCG_STATUS_EXECUTION_FAILED;
@@ -1268,10 +1282,10 @@ tcgStatus_t tcg_get_device_error(tcgHandle_t h)
     if (!h->d_err)
         return TCG_STATUS_SUCCESS;
     uint32_t bits = 0;
-    if (cudaStreamSynchronize(h->stream) != cudaSuccess ||
-        cudaMemcpy(&bits, h->d_err, sizeof bits, cudaMemcpyDeviceToHost) != cudaSuccess ||
+    if (cudaMemcpyAsync(&bits, h->d_err, sizeof bits, cudaMemcpyDeviceToHost, h->stream) != cudaSuccess ||
+        cudaStreamSynchronize(h->stream) != cudaSuccess ||
         // a kernel that stopped early may have left split counters behind
-        cudaMemset(h->d_err, 0, bits ? kErrAreaBytes : sizeof(uint32_t)) != cudaSuccess) {
+        (bits && !clear_words(h->d_err, kErrAreaBytes))) {
         cudaGetLastError();
         return TCG_STATUS_EXECUTION_FAILED;
     }

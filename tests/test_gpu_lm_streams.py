@@ -1,0 +1,68 @@
+"""The language-model products on streams of their own: handles whose first calls, workspaces
+and inputs meet work that other streams still have queued."""
+import pytest
+import torch
+
+import mixed_precision_tensor_gb300 as tcg
+from test_gpu_lm import BF16, F32, gen_of, randn, same_bits
+
+pytestmark = pytest.mark.gpu
+
+BUSY = 1_000_000_000                  # clock cycles that a stream is kept busy for: about half a second
+
+
+def cut_product(seed=1):
+    """Inputs of a product whose tiles are cut along K, and its result."""
+    g = gen_of(seed)
+    x, w = randn(g, 20, 4096), randn(g, 512, 4096, std=1 / 64)
+    h = tcg.Handle()
+    assert tcg.tcg_gemm_epilogue_workspace_size(h.h, 1, 0, 512, 20, 4096) > 0
+    want = tcg.linear(h, x, w, out_dtype=F32).clone()
+    tcg.check(tcg.tcg_get_device_error(h.h))
+    h.close()
+    torch.cuda.synchronize()
+    return x, w, want
+
+
+def test_first_calls_while_the_default_stream_is_busy(cuda_device):
+    """A new handle's arrival counters are zero before its first kernel, whatever the legacy
+    default stream still has to do."""
+    x, w, want = cut_product()
+    side = torch.cuda.Stream()
+    out = [torch.empty(20, 512, dtype=F32, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    busy = torch.cuda.current_stream()
+    h = tcg.Handle(side)
+    for o in out:
+        tcg.linear(h, x, w, out=o)
+    side.synchronize()
+    assert not busy.query()
+    for o in out:
+        assert same_bits(o, want)
+    tcg.check(tcg.tcg_get_device_error(h.h))
+    h.close()
+
+
+def test_error_word_is_read_and_cleared_beside_a_busy_default_stream(cuda_device):
+    """After a wait that ran out, the counters are zero again before the next kernel."""
+    x, w, want = cut_product(2)
+    side = torch.cuda.Stream()
+    out = [torch.empty(20, 512, dtype=F32, device="cuda") for _ in range(4)]
+    h = tcg.Handle(side)
+    tcg.linear(h, x, w, out=out[0])
+    torch.cuda.synchronize()
+    torch.cuda._sleep(BUSY)
+    busy = torch.cuda.current_stream()
+    tcg.check(tcg.tcg_set_debug(h.h, 20_000_000, 1))     # one load that never comes
+    tcg.linear(h, x, w, out=out[0])
+    assert tcg.tcg_get_device_error(h.h) == tcg.TCG_STATUS_TIMEOUT
+    tcg.check(tcg.tcg_set_debug(h.h, 0, 0))
+    for o in out:
+        tcg.linear(h, x, w, out=o)
+    side.synchronize()
+    assert not busy.query()
+    for o in out:
+        assert same_bits(o, want)
+    tcg.check(tcg.tcg_get_device_error(h.h))
+    h.close()

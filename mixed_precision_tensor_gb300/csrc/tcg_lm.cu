@@ -698,7 +698,8 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                 const int m0 = w.row0 + static_cast<int>(rank) * kBM;
                 const int n0 = w.col0 + static_cast<int>(rank) * (width(w) / 2);
                 const int za = WIDE ? 0 : w.g, zb = WIDE && !RK ? w.g : 0;
-                if (RK && w.g != maps_of) {                // maps that end with the group
+                // maps that end with the group; without tokens there are none
+                if (RK && w.kb0 < w.kb1 && w.g != maps_of) {
                     maps_of = w.g;
                     map_a = p.group_maps + 2 * w.g;
                     map_b = map_a + 1;

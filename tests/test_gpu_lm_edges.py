@@ -1,0 +1,36 @@
+"""Edges of the language-model products: nothing to sum, nothing to write, values far apart."""
+import pytest
+import torch
+
+import mixed_precision_tensor_gb300 as tcg
+from test_gpu_lm import BF16, F16, gen_of, offsets_of, randn
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def handle(cuda_device):
+    h = tcg.Handle()
+    yield h
+    tcg.check(tcg.tcg_get_device_error(h.h), "device error word")
+    h.close()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("act", ["none", "silu"])
+def test_experts_without_any_rows(handle, dtype, act):
+    """No tokens at all: zero weight and bias gradients for every expert, dx of no rows."""
+    g = gen_of(1)
+    e, n, k = 5, 200, 136
+    w, off = randn(g, e, n, k, dtype=dtype), offsets_of([0] * e, 0)
+    x, d, z = (torch.empty(0, c, dtype=dtype, device="cuda") for c in (k, n, n))
+    assert tcg.grouped_linear(handle, x, w, off, act=act).shape == (0, n)
+    dw = torch.full((e, n, k), float("nan"), dtype=dtype, device="cuda")
+    db = torch.full((e, n), float("nan"), device="cuda")
+    dx, _, _ = tcg.grouped_linear_backward(handle, d, x, w, off, z=z, act=act, dw=dw, dbias=db)
+    assert dx.shape == (0, k) and (dw == 0).all() and (db == 0).all()
+    ty = tcg.TCG_R_16BF if dtype is BF16 else tcg.TCG_R_16F
+    dw.fill_(float("nan"))
+    tcg.check(tcg.tcg_gemm_grouped_k(handle.h, k, n, 0, e, off, 1.0, None, k, None, n, ty, dw, ty, k, n * k))
+    assert (dw == 0).all()
+    tcg.check(tcg.tcg_get_device_error(handle.h))

@@ -761,6 +761,8 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
             int it = 0;
             bool ok = true;
             bool more = walk.next(p, ctl, w);
+            if (!p.offsets)
+                griddep_wait();                            // so that no wait below includes the kernel before
             while (ok && more) {
                 bool looked = false;                       // the next unit is known
                 int kb = w.kb0;

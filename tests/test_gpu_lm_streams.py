@@ -66,3 +66,35 @@ def test_error_word_is_read_and_cleared_beside_a_busy_default_stream(cuda_device
         assert same_bits(o, want)
     tcg.check(tcg.tcg_get_device_error(h.h))
     h.close()
+
+
+def test_waits_do_not_include_the_kernel_before(cuda_device):
+    """A short wait limit bounds a kernel's own waits.  Two calls back to back: one pair of
+    SMs busy for longer than the limit, then tiles for all of them, whose blocks are resident
+    early on the SMs that the first call leaves idle."""
+    g = gen_of(3)
+    h = tcg.Handle()
+    tcg.check(tcg.tcg_set_split_k(h.h, 1))                  # the long product stays on one pair
+    x1, w1 = randn(g, 20, 1 << 20), randn(g, 64, 1 << 20)
+    x2, w2 = randn(g, 600, 64), randn(g, 4096, 64)
+    out1 = torch.empty(20, 64, dtype=BF16, device="cuda")
+    out2 = torch.empty(600, 4096, dtype=BF16, device="cuda")
+    for _ in range(2):
+        tcg.linear(h, x1, w1, out=out1)
+        tcg.linear(h, x2, w2, out=out2)
+    torch.cuda.synchronize()
+    want1, want2 = out1.clone(), out2.clone()
+    ev = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    ev[0].record()
+    tcg.linear(h, x1, w1, out=out1)
+    ev[1].record()
+    torch.cuda.synchronize()
+    limit = ev[0].elapsed_time(ev[1]) / 4                   # ms
+    assert limit > 0.2
+    tcg.check(tcg.tcg_set_debug(h.h, int(limit * 1e6), 0))
+    for _ in range(3):
+        tcg.linear(h, x1, w1, out=out1)
+        tcg.linear(h, x2, w2, out=out2)
+    tcg.check(tcg.tcg_get_device_error(h.h))
+    assert same_bits(out1, want1) and same_bits(out2, want2)
+    h.close()

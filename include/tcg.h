@@ -131,8 +131,11 @@ tcgStatus_t tcg_set_stream(tcgHandle_t h, void *stream);
  * writes TF32-rounded, K-major copies of op(A) and op(B) before the product) and for
  * the FP32 partial sums of split-K and tail-split calls (tcg_set_split_k).
  * ptr must be 256-byte aligned; bytes may be 0 to detach.  Without a caller
- * workspace the handle grows one of its own with cudaMalloc on the first TF32
- * call that needs more (not capture-safe).  Errors: INVALID_VALUE. */
+ * workspace the handle grows one of its own with cudaMalloc on a call that needs more
+ * than any before: that call waits for the stream, frees the old one and allocates.
+ * A call that is being captured does not grow it (ALLOC_FAILED, nothing queued), and one
+ * that a captured call has used stays allocated until the handle is destroyed.
+ * Errors: INVALID_VALUE. */
 tcgStatus_t tcg_set_workspace(tcgHandle_t h, void *ptr, size_t bytes);
 
 /* Bytes of workspace a tcg_gemm_strided_batched call with these arguments

@@ -446,7 +446,8 @@ TailPlan tail_for(tcgContext *h, int64_t m, int64_t n, int64_t k, int64_t batch,
 }
 
 // Device workspace of at least `need` bytes: the caller's (tcg_set_workspace) or one the
-// handle grows with cudaMalloc.
+// handle grows with cudaMalloc.  A call being captured into a graph does not grow it, and a
+// block whose address a graph holds is kept until the handle is destroyed.
 tcgStatus_t acquire_ws(tcgContext *h, size_t need, void **ws)
 {
     if (h->ws_user) {
@@ -455,13 +456,25 @@ tcgStatus_t acquire_ws(tcgContext *h, size_t need, void **ws)
         *ws = h->ws_user;
         return TCG_STATUS_SUCCESS;
     }
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(h->stream, &capture) != cudaSuccess)
+        cudaGetLastError();
+    const bool capturing = capture != cudaStreamCaptureStatusNone;
     if (h->ws_own_bytes < need) {
-        if (h->ws_own) {
+        if (capturing)
+            return TCG_STATUS_ALLOC_FAILED;
+        if (h->ws_captured) {
+            KeptBlock *kept = new (std::nothrow) KeptBlock{h->ws_own, h->ws_kept};
+            if (!kept)
+                return TCG_STATUS_ALLOC_FAILED;
+            h->ws_kept = kept;
+        } else if (h->ws_own) {
             cudaStreamSynchronize(h->stream);
             cudaFree(h->ws_own);
-            h->ws_own = nullptr;
-            h->ws_own_bytes = 0;
         }
+        h->ws_own = nullptr;
+        h->ws_own_bytes = 0;
+        h->ws_captured = false;
         if (cudaMalloc(&h->ws_own, need) != cudaSuccess) {
             cudaGetLastError();
             h->ws_own = nullptr;
@@ -469,6 +482,7 @@ tcgStatus_t acquire_ws(tcgContext *h, size_t need, void **ws)
         }
         h->ws_own_bytes = need;
     }
+    h->ws_captured = h->ws_captured || (capturing && need > 0);
     *ws = h->ws_own;
     return TCG_STATUS_SUCCESS;
 }
@@ -1142,6 +1156,12 @@ tcgStatus_t tcg_destroy(tcgHandle_t h)
         cudaFree(h->d_clk);
     if (h->ws_own)
         cudaFree(h->ws_own);
+    while (h->ws_kept) {
+        tcg::KeptBlock *kept = h->ws_kept;
+        h->ws_kept = kept->next;
+        cudaFree(kept->ptr);
+        delete kept;
+    }
     for (int i = 0; i < 3; ++i)
         if (h->stage_buf[i])
             cudaFree(h->stage_buf[i]);

@@ -46,6 +46,12 @@ struct MapEntry {
     bool valid;
 };
 
+// A workspace that a newer one has replaced, still in use by a captured graph.
+struct KeptBlock {
+    void *ptr;
+    KeptBlock *next;
+};
+
 }  // namespace tcg
 
 struct tcgContext {
@@ -60,6 +66,8 @@ struct tcgContext {
     size_t ws_user_bytes = 0;
     void *ws_own = nullptr;
     size_t ws_own_bytes = 0;
+    bool ws_captured = false;              // a captured call has been given ws_own
+    tcg::KeptBlock *ws_kept = nullptr;
     unsigned long long wait_limit_ns = tcg::kDefaultWaitNs;
     int fault_inject = 0;
     uint64_t launches = 0;

@@ -4,9 +4,18 @@ products").
 
 Row-major: a row is a token.  Inputs are FP16 or BF16, two-dimensional with unit stride
 along the features; rows may be any multiple of 16 bytes apart, so feature counts that are
-no multiple of 8 need padded rows.  Every call queues on the handle's stream and does not
-wait; inputs must be ready there.  Tensors that a call allocates belong to that stream.
-This module checks and marshals; all arithmetic is in the library's kernels.
+no multiple of 8 need padded rows.  Every call queues on the handle's stream; inputs must be
+ready there, and tensors that a call allocates belong to that stream.  This module checks and
+marshals; all arithmetic is in the library's kernels.
+
+Calls do not wait for the GPU, with one exception: the handle keeps a workspace, outside
+torch's allocator and until it is closed, as large as the largest that a call has needed (all
+of dz in a backward pass with an activation, up to 256 MiB of the cross entropy's gradient and
+an FP32 dx).  A call that needs more than any before waits for the stream and allocates anew;
+while a graph is being captured it is refused instead (TCG_STATUS_ALLOC_FAILED).  To avoid
+both, run the largest shapes once first, or give the handle memory of your own with
+``tcg_set_workspace``, sized by ``tcg_gemm_epilogue_workspace_size``,
+``tcg_linear_backward_workspace_size`` and ``tcg_xent_workspace_size``.
 """
 from __future__ import annotations
 

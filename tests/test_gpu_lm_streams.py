@@ -98,3 +98,58 @@ def test_waits_do_not_include_the_kernel_before(cuda_device):
     tcg.check(tcg.tcg_get_device_error(h.h))
     assert same_bits(out1, want1) and same_bits(out2, want2)
     h.close()
+
+
+def test_graph_keeps_its_workspace(cuda_device):
+    """A captured call's workspace stays where the graph found it when a later call needs more."""
+    x, w, want = cut_product(4)
+    g = gen_of(5)
+    out = torch.empty(20, 512, dtype=F32, device="cuda")
+    s = torch.cuda.Stream()
+    h = tcg.Handle(s)
+    with torch.cuda.stream(s):
+        tcg.linear(h, x, w, out=out)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        tcg.linear(h, x, w, out=out)
+    with torch.cuda.stream(s):
+        for rows in (300, 3000, 30000):                     # each needs more than the one before
+            d, xb, wb = randn(g, rows, 512), randn(g, rows, 256), randn(g, 512, 256)
+            tcg.linear_backward(h, d, xb, wb, z=randn(g, rows, 512), act="silu")
+            s.synchronize()
+            fill = [torch.full((1 << 18,), float("nan"), device="cuda") for _ in range(64)]
+            out.zero_()
+            for _ in range(3):
+                graph.replay()
+            s.synchronize()
+            assert same_bits(out, want)
+            del fill
+    tcg.check(tcg.tcg_get_device_error(h.h))
+    h.close()
+
+
+def test_capture_does_not_grow_the_workspace(cuda_device):
+    """Refused cleanly: the capture goes on, and the call works once the handle has the memory."""
+    x, w, want = cut_product(6)
+    out, n = torch.empty(20, 512, dtype=F32, device="cuda"), torch.zeros(1, device="cuda")
+    s = torch.cuda.Stream()
+    h = tcg.Handle(s)
+    with torch.cuda.stream(s):
+        tcg.linear(h, x[:1], w)                             # binds the handle; needs no workspace
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        before = tcg.tcg_launch_count(h.h)
+        with pytest.raises(tcg.TcgError) as e:
+            tcg.linear(h, x, w, out=out)
+        assert e.value.status == tcg.TCG_STATUS_ALLOC_FAILED and tcg.tcg_launch_count(h.h) == before
+        n += 1
+    graph.replay()
+    torch.cuda.synchronize()
+    assert float(n) == 1
+    with torch.cuda.stream(s):
+        tcg.linear(h, x, w, out=out)
+    s.synchronize()
+    assert same_bits(out, want)
+    h.close()

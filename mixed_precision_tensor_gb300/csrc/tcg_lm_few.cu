@@ -28,6 +28,7 @@ constexpr int kFewK = 512;                          // K elements of a stage
 constexpr int kFewRowBytes = kFewK * 2;
 constexpr int kFewRingBytes = 12 * 1024;            // per warp; the rest of the SM's 228 KiB caches X
 constexpr int kFewMaxStages = 12;
+constexpr uint64_t kFewDrainNs = 100000000ull;      // longest wait for a copy after a wait ran out
 
 struct FewCtl {
     uint64_t full[kFewWarps][kFewMaxStages];
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
     const int64_t K = p.k, K8 = K & ~static_cast<int64_t>(7);   // the rest of K: see below
     // The producer's place in the walk: chunk at kp of task ip, into stage sp.
     int64_t ip = mine, kp = 0;
-    int sp = 0, ahead = 0;                          // stages filled or being filled
+    int sp = 0, ahead = 0;                          // stages being filled or not yet read
     FewTask wp{};
     bool have = false;
     auto produce = [&]() {                          // one more chunk, if there is one
@@ -360,9 +361,16 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
             store_out(p.D, tok * p.ldd + f, p.out_kind, out);
         }
     }
-    if (!ok) {                                      // let the copies under way land
+    if (!ok) {                                      // the copies under way land before the block leaves
         const uint64_t begun = globaltimer_ns();
-        while (globaltimer_ns() - begun < 20000ull) {
+        for (; ahead > 0; --ahead) {
+            const uint32_t bar = smem_u32(&ctl.full[warp][sc]);
+            while (!mbar_try_wait(bar, parity) && globaltimer_ns() - begun <= kFewDrainNs) {
+            }
+            if (++sc == S) {
+                sc = 0;
+                parity ^= 1u;
+            }
         }
     }
     if (p.stats) {

@@ -161,6 +161,7 @@ struct LmFewArgs {
     float *target_logit;
     uint32_t *err;
     unsigned long long wait_limit_ns;
+    int fault_inject;
 };
 constexpr int kLmFewTokens = 4;        // dense, cross entropy
 constexpr int kLmFewRows = 64;         // grouped: rows of all experts

@@ -327,6 +327,7 @@ tcgStatus_t queue_few(tcgContext *h, const Product &p)
     a.act = p.epi.activation;
     a.err = h->d_err;
     a.wait_limit_ns = h->wait_limit_ns;
+    a.fault_inject = h->fault_inject;
     const cudaError_t e = launch_few(a, h->num_sms, h->stream);
     h->launches += 1;
     if (e != cudaSuccess) {
@@ -1011,6 +1012,7 @@ tcgStatus_t tcg_xent_forward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_t
         f.target_logit = a.target_logit;
         f.err = h->d_err;
         f.wait_limit_ns = h->wait_limit_ns;
+        f.fault_inject = h->fault_inject;
         if (launch_few(f, h->num_sms, h->stream) != cudaSuccess) {
             cudaGetLastError();
             return TCG_STATUS_EXECUTION_FAILED;

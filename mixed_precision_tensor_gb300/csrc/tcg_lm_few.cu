@@ -164,7 +164,9 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
     const int64_t K = p.k, K8 = K & ~static_cast<int64_t>(7);   // the rest of K: see below
     // The producer's place in the walk: chunk at kp of task ip, into stage sp.
     int64_t ip = mine, kp = 0;
-    int sp = 0, ahead = 0;                          // stages being filled or not yet read
+    int sp = 0;
+    uint32_t filling = 0;                           // stages being filled or not yet read
+    bool skip_once = p.fault_inject != 0 && blockIdx.x == 0 && warp == 0;
     FewTask wp{};
     bool have = false;
     auto produce = [&]() {                          // one more chunk, if there is one
@@ -180,16 +182,20 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
         }
         const uint32_t bytes = static_cast<uint32_t>((K8 - kp < kFewK ? K8 - kp : kFewK) * 2);
         const uint32_t bar = smem_u32(&ctl.full[warp][sp]);
-        if (lane == 0)
-            mbar_arrive_expect_tx(bar, bytes * R);
-        __syncwarp();
-        if (lane < R) {                             // rows past the end repeat the last one
-            const int64_t f = wp.f0 + lane < p.feats ? wp.f0 + lane : p.feats - 1;
-            bulk_load(my_ring_u32 + sp * Cfg::kStageBytes + lane * kFewRowBytes,
-                      static_cast<const uint16_t *>(p.W) + wp.g * p.strideW + f * p.ldw + kp, bytes, bar);
+        if (skip_once) {
+            skip_once = false;                      // test hook: this stage is never filled
+        } else {
+            if (lane == 0)
+                mbar_arrive_expect_tx(bar, bytes * R);
+            __syncwarp();
+            if (lane < R) {                         // rows past the end repeat the last one
+                const int64_t f = wp.f0 + lane < p.feats ? wp.f0 + lane : p.feats - 1;
+                bulk_load(my_ring_u32 + sp * Cfg::kStageBytes + lane * kFewRowBytes,
+                          static_cast<const uint16_t *>(p.W) + wp.g * p.strideW + f * p.ldw + kp, bytes, bar);
+            }
+            filling |= 1u << sp;
         }
         sp = sp + 1 == S ? 0 : sp + 1;
-        ++ahead;
         kp += kFewK;
         if (kp >= K8) {
             kp = 0;
@@ -284,7 +290,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
             for (int h = 0; h < kHalves; ++h)
                 load_x(k0 + kFewK, h, xv[h]);
             __syncwarp();                           // the stage has been read by every lane
-            --ahead;
+            filling &= ~(1u << sc);
             if (++sc == S) {
                 sc = 0;
                 parity ^= 1u;
@@ -363,9 +369,10 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
     }
     if (!ok) {                                      // the copies under way land before the block leaves
         const uint64_t begun = globaltimer_ns();
-        for (; ahead > 0; --ahead) {
+        for (int i = 0; i < S; ++i) {
             const uint32_t bar = smem_u32(&ctl.full[warp][sc]);
-            while (!mbar_try_wait(bar, parity) && globaltimer_ns() - begun <= kFewDrainNs) {
+            while ((filling >> sc & 1u) && !mbar_try_wait(bar, parity) &&
+                   globaltimer_ns() - begun <= kFewDrainNs) {
             }
             if (++sc == S) {
                 sc = 0;

@@ -227,8 +227,9 @@ def linear_backward(handle, dout, x, w, z=None, act="none", want=("dx", "dw", "d
     unrounded dz).  The residual's gradient is beta * dout.  ``want`` names what is computed;
     the result is (dx, dw, dbias) with None for the others.  Outputs are made where not given.
     """
-    n, k = w.shape
-    ldw = _rows(w, "w", n, k, x.dtype, x.device)
+    _, k, dtype, dev = _input(x)
+    n = w.shape[0]
+    ldw = _rows(w, "w", n, k, dtype, dev)
     return _backward(handle, "linear_backward", dout, x, w, z, act, want, dx, dw, dbias, None, 1, n, ldw, 0)
 
 
@@ -273,9 +274,10 @@ def grouped_linear_backward(handle, dout, x, w, offsets, z=None, act="none",
     """
     if w.dim() != 3:
         raise ValueError("w must be experts x n x k")
-    e, n, k = w.shape
-    ldw, stride = _experts(w, "w", e, n, k, x.dtype, x.device)
-    _check_offsets(offsets, e, x.device)
+    _, k, dtype, dev = _input(x)
+    e, n = w.shape[0], w.shape[1]
+    ldw, stride = _experts(w, "w", e, n, k, dtype, dev)
+    _check_offsets(offsets, e, dev)
     return _backward(handle, "grouped_linear_backward", dout, x, w, z, act, want, dx, dw, dbias, offsets, e, n,
                      ldw, stride)
 

@@ -45,7 +45,7 @@ def _rows(t, what, rows, cols, dtype, device):
     per = 4 if dtype is torch.float32 else 8
     if s1 != 1 and cols > 1:
         raise ValueError(f"{what} must have unit stride along its last dimension")
-    if rows <= 1:
+    if rows <= 1 or cols == 0:                # no stride between rows to go by
         return (cols + per - 1) // per * per or per
     if s0 < cols or s0 % per:
         raise ValueError(f"{what}: rows must be a multiple of 16 bytes apart, got {s0} elements")
@@ -97,12 +97,12 @@ def _experts(w, what, e, n, k, dtype, device):
     stride, ld, s2 = w.stride()
     if s2 != 1 and k > 1:
         raise ValueError(f"{what} must have unit stride along its last dimension")
-    if n <= 1:
+    if n <= 1 or k == 0:                      # no stride between rows to go by
         ld = (k + 7) // 8 * 8 or 8
     if ld < k or ld % 8:
         raise ValueError(f"{what}: rows must be a multiple of 16 bytes apart, got {ld} elements")
-    if e <= 1:
-        stride = n * ld
+    if e <= 1 or n == 0 or k == 0:
+        stride = max(n, 1) * ld
     elif stride <= 0 or stride % 8:
         raise ValueError(f"{what}: experts must be a multiple of 16 bytes apart")
     return ld, stride

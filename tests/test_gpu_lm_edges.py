@@ -34,3 +34,26 @@ def test_experts_without_any_rows(handle, dtype, act):
     tcg.check(tcg.tcg_gemm_grouped_k(handle.h, k, n, 0, e, off, 1.0, None, k, None, n, ty, dw, ty, k, n * k))
     assert (dw == 0).all()
     tcg.check(tcg.tcg_get_device_error(handle.h))
+
+
+def test_nothing_to_sum_or_to_write(handle):
+    """Contiguous tensors without elements: the bias alone, zero gradients, or no output."""
+    g = gen_of(2)
+    empty = lambda *shape: torch.empty(*shape, dtype=BF16, device="cuda")  # noqa: E731
+    bias, e_bias, res = randn(g, 256), randn(g, 3, 256), randn(g, 45, 256)
+    off = offsets_of([20, 0, 25], 0)
+    out = tcg.linear(handle, empty(45, 0), empty(256, 0), bias=bias, residual=res)
+    assert torch.equal(out, (bias.float() + res.float()).to(BF16))
+    out = tcg.grouped_linear(handle, empty(45, 0), empty(3, 256, 0), off, bias=e_bias)
+    assert torch.equal(out, torch.cat([e_bias[0].expand(20, 256), e_bias[2].expand(25, 256)]))
+    d = randn(g, 45, 256)
+    dx, dw, db = tcg.linear_backward(handle, d, empty(45, 0), empty(256, 0))
+    assert dx.shape == (45, 0) and dw.shape == (256, 0)
+    off_by = (db.double() - d.double().sum(0)).abs()
+    assert (off_by <= (45 + 4) * 2.0 ** -24 * d.double().abs().sum(0)).all()   # FP32 additions
+    dx, dw, db = tcg.linear_backward(handle, empty(45, 0), randn(g, 45, 64), empty(0, 64))
+    assert dx.shape == (45, 64) and not dx.any() and dw.shape == (0, 64) and db.shape == (0,)
+    dx, dw, db = tcg.grouped_linear_backward(handle, empty(45, 0), randn(g, 45, 64), empty(3, 0, 64), off)
+    assert not dx.any() and dw.shape == (3, 0, 64) and db.shape == (3, 0)
+    assert tcg.linear(handle, randn(g, 45, 64), empty(0, 64)).shape == (45, 0)
+    tcg.check(tcg.tcg_get_device_error(handle.h))

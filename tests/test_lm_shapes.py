@@ -70,3 +70,28 @@ def test_backward_passes_the_shapes_on(library):
     (name, a), = library.calls
     assert name == "tcg_linear_backward"
     assert a[2:5] == (16, 4, 64) and a[12] == 80 and a[15] == 72      # m, n, k, ldw, ldx
+
+
+# ------------------------------------------------------------------ nothing in one direction
+@pytest.mark.parametrize("t,n,k", [(5, 16, 0), (5, 0, 64), (5, 0, 0), (0, 16, 64), (1, 16, 0)])
+def test_matrices_without_elements_are_taken(library, t, n, k):
+    """A sum over nothing, or nothing to write: contiguous tensors as torch makes them, whose
+    strides say nothing about rows, and leading dimensions that the library takes."""
+    x, w, dout, z = zeros(t, k), zeros(n, k), zeros(t, n), zeros(t, n)
+    tcg.linear(Handle(), x, w, residual=zeros(t, n), z=z, out=zeros(t, n))
+    tcg.linear_backward(Handle(), dout, x, w, z=z, act="silu", dx=zeros(t, k), dw=zeros(n, k))
+    (_, a), (_, b) = library.calls
+    for ld, cols in ((a[8], k), (a[10], k), (a[14], n), (a[15].ldc, n), (a[15].ldz, n),
+                     (b[8], n), (b[10], n), (b[12], k), (b[15], k), (b[18], k), (b[20], k)):
+        assert ld >= max(cols, 1) and ld % 8 == 0
+
+
+@pytest.mark.parametrize("e,n,k", [(3, 16, 0), (3, 0, 64), (1, 0, 0), (1, 16, 0)])
+def test_experts_without_elements_are_taken(library, e, n, k):
+    x, w, off = zeros(5, k), zeros(e, n, k), torch.zeros(e + 1, dtype=torch.int64)
+    tcg.grouped_linear(Handle(), x, w, off)
+    tcg.grouped_linear_backward(Handle(), zeros(5, n), x, w, off, dw=zeros(e, n, k))
+    (_, a), (_, b) = library.calls
+    for ld, stride in ((a[9], a[10]), (b[12], b[13]), (b[20], b[21])):
+        assert ld >= max(k, 1) and ld % 8 == 0
+        assert stride >= (n - 1) * ld + k and stride % 8 == 0 and (stride > 0 or e == 1)

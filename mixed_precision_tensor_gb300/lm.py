@@ -5,8 +5,10 @@ products").
 Row-major: a row is a token.  Inputs are FP16 or BF16, two-dimensional with unit stride
 along the features; rows may be any multiple of 16 bytes apart, so feature counts that are
 no multiple of 8 need padded rows.  Every call queues on the handle's stream; inputs must be
-ready there, and tensors that a call allocates belong to that stream.  This module checks and
-marshals; all arithmetic is in the library's kernels.
+ready there, and tensors that a call allocates belong to that stream.  Where that is not the
+caller's current stream, the caller may drop its tensors at once: their memory is held until
+the handle's stream is done.  This module checks and marshals; all arithmetic is in the
+library's kernels.
 
 Calls do not wait for the GPU, with one exception: the handle keeps a workspace, outside
 torch's allocator and until it is closed, as large as the largest that a call has needed (all
@@ -70,11 +72,24 @@ def _act(act):
 
 def _empty(handle, shape, dtype, device):
     """A new tensor of the handle's stream."""
+    if not _elsewhere(handle, device):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(handle.stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _elsewhere(handle, device):
+    """Whether the handle's stream is another one than the caller's."""
     own = handle.stream
-    if own is None or _raw_stream(device.index) == own.cuda_stream:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(own):
-        return torch.empty(shape, dtype=dtype, device=device)
+    return own is not None and _raw_stream(device.index) != own.cuda_stream
+
+
+def _hold(handle, *tensors):
+    """The caller's tensors on the handle's stream: should the caller drop one, torch gives its
+    memory out again only once that stream is done with it."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(handle.stream)
 
 
 def _matrix(handle, given, what, rows, cols, dtype, device):
@@ -165,6 +180,8 @@ def linear(handle, x, w, bias=None, act="none", residual=None, beta=1.0, alpha=1
     s = _lib().tcg_gemm_epilogue(
         handle.h, 1, 0, n, t, k, alpha, w.data_ptr(), ldw, x.data_ptr(), ldx, code, out.data_ptr(),
         out_code, ldo, e)
+    if _elsewhere(handle, dev):
+        _hold(handle, x, w, bias, residual, out, z)
     if s:
         raise _tcg.TcgError(s, "linear")
     return out
@@ -208,6 +225,9 @@ def _backward(handle, what, dout, x, w, z, act, want, dx, dw, dbias, offsets, e,
         z.data_ptr() if code else None, ldz, w.data_ptr(), ldw, stride_w, x.data_ptr(), ldx, _IN[dtype],
         dx.data_ptr() if want_dx else None, lddx, dw.data_ptr() if want_dw else None, lddw, stride_dw,
         dbias.data_ptr() if want_db else None)
+    if _elsewhere(handle, dev):
+        _hold(handle, dout, x, w, z if code else None, offsets, dx if want_dx else None,
+              dw if want_dw else None, dbias if want_db else None)
     if s:
         raise _tcg.TcgError(s, what)
     return (dx if want_dx else None, dw if want_dw else None, dbias if want_db else None)
@@ -261,6 +281,8 @@ def grouped_linear(handle, x, w, offsets, bias=None, act="none", residual=None, 
     s = _lib().tcg_gemm_grouped(
         handle.h, 1, n, t, k, e, offsets.data_ptr(), alpha, w.data_ptr(), ldw, stride, x.data_ptr(),
         ldx, _IN[dtype], out.data_ptr(), out_code, ldo, ep)
+    if _elsewhere(handle, dev):
+        _hold(handle, x, w, offsets, bias, residual, out, z)
     if s:
         raise _tcg.TcgError(s, "grouped_linear")
     return out
@@ -305,6 +327,8 @@ def linear_cross_entropy(handle, x, w, targets, ignore_index=-100, loss=None, ls
     s = _lib().tcg_xent_forward(
         handle.h, t, v, k, x.data_ptr(), ldx, w.data_ptr(), ldw, _IN[dtype], targets.data_ptr(),
         ignore_index, loss.data_ptr(), lse.data_ptr())
+    if _elsewhere(handle, dev):
+        _hold(handle, x, w, targets, loss, lse)
     if s:
         raise _tcg.TcgError(s, "linear_cross_entropy")
     return loss, lse
@@ -331,6 +355,8 @@ def linear_cross_entropy_backward(handle, x, w, targets, lse, dloss, ignore_inde
         handle.h, t, v, k, x.data_ptr(), ldx, w.data_ptr(), ldw, _IN[dtype], targets.data_ptr(),
         ignore_index, lse.data_ptr(), dloss.data_ptr(), dx.data_ptr() if want_dx else None, lddx,
         dw.data_ptr() if want_dw else None, lddw)
+    if _elsewhere(handle, dev):
+        _hold(handle, x, w, targets, lse, dloss, dx if want_dx else None, dw if want_dw else None)
     if s:
         raise _tcg.TcgError(s, "linear_cross_entropy_backward")
     return (dx if want_dx else None, dw if want_dw else None)

@@ -177,3 +177,28 @@ def test_few_tokens_timeout_leaves_nothing(cuda_device, t):
         assert same_bits(out, want) and same_bits(again, loss)
     tcg.check(tcg.tcg_get_device_error(h.h))
     h.close()
+
+
+def test_inputs_of_another_stream_may_be_dropped(cuda_device):
+    """The caller drops an input while the handle's stream has yet to read it."""
+    x, w, want = cut_product(8)
+    side = torch.cuda.Stream()
+    out = torch.empty(20, 512, dtype=F32, device="cuda")
+    h = tcg.Handle(side)
+    tcg.linear(h, x, w, out=out)
+    spare = [torch.full_like(a, 0.0) for a in (x, w) for _ in range(6)]   # memory that torch has in hand
+    del spare
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+    x2, w2 = x.clone(), w.clone()
+    torch.cuda.current_stream().synchronize()               # the inputs are ready
+    tcg.linear(h, x2, w2, out=out)
+    del x2, w2
+    other = [torch.full_like(a, float("nan")) for a in (x, w) for _ in range(4)]
+    torch.cuda.current_stream().synchronize()
+    assert not side.query()
+    side.synchronize()
+    assert same_bits(out, want)
+    del other
+    h.close()

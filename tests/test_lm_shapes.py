@@ -72,6 +72,41 @@ def test_backward_passes_the_shapes_on(library):
     assert a[2:5] == (16, 4, 64) and a[12] == 80 and a[15] == 72      # m, n, k, ldw, ldx
 
 
+# -------------------------------------------------------------------------- another stream
+class Stream:
+    cuda_stream = 7
+
+
+@pytest.mark.parametrize("current", [0, 7])
+def test_tensors_of_another_stream_are_held(library, monkeypatch, current):
+    """Everything whose memory a call uses is recorded with the handle's stream, where that is
+    not the current one."""
+    held = []
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: held.append((t.data_ptr(), s)))
+    monkeypatch.setattr(lm, "_raw_stream", lambda index: current)
+    h = Handle()
+    h.stream = Stream()
+    x, w, e, d, z, o = zeros(4, 64), zeros(16, 64), zeros(3, 16, 64), zeros(4, 16), zeros(4, 16), zeros(4, 16)
+    b, eb, off, r = zeros(16), zeros(3, 16), torch.zeros(4, dtype=torch.int64), zeros(4, 16)
+    dx, dw, de, db = zeros(4, 64), zeros(16, 64), zeros(3, 16, 64), torch.zeros(16)
+    deb, t, lo, ls, dl = torch.zeros(3, 16), torch.zeros(4, dtype=torch.int64), *(torch.zeros(4) for _ in range(3))
+    for call, used in (
+            (lambda: tcg.linear(h, x, w, bias=b, residual=r, out=o, z=z), (x, w, b, r, o, z)),
+            (lambda: tcg.grouped_linear(h, x, e, off, bias=eb, residual=r, out=o, z=z),
+             (x, e, off, eb, r, o, z)),
+            (lambda: tcg.linear_backward(h, d, x, w, z=z, act="silu", dx=dx, dw=dw, dbias=db),
+             (d, x, w, z, dx, dw, db)),
+            (lambda: tcg.grouped_linear_backward(h, d, x, e, off, z=z, act="silu", dx=dx, dw=de, dbias=deb),
+             (d, x, e, off, z, dx, de, deb)),
+            (lambda: tcg.linear_cross_entropy(h, x, w, t, loss=lo, lse=ls), (x, w, t, lo, ls)),
+            (lambda: tcg.linear_cross_entropy_backward(h, x, w, t, ls, dl, dx=dx, dw=dw),
+             (x, w, t, ls, dl, dx, dw))):
+        held.clear()
+        call()
+        want = {a.data_ptr() for a in used} if current != 7 else set()
+        assert {a for a, _ in held} == want and all(s is h.stream for _, s in held)
+
+
 # ------------------------------------------------------------------ nothing in one direction
 @pytest.mark.parametrize("t,n,k", [(5, 16, 0), (5, 0, 64), (5, 0, 0), (0, 16, 64), (1, 16, 0)])
 def test_matrices_without_elements_are_taken(library, t, n, k):

@@ -1006,8 +1006,7 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
 #pragma unroll
                         for (int d = 16; d; d >>= 1)
                             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                        const float sub = mx == -INFINITY ? 0.0f : mx * kLog2e;
-                        float s = exp2_fast(fmaf(v, kLog2e, -sub));
+                        float s = exp_from(v, exp_base(mx));
 #pragma unroll
                         for (int d = 16; d; d >>= 1)
                             s += __shfl_xor_sync(0xffffffffu, s, d);
@@ -1080,7 +1079,7 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
             } else {
                 // ------------------------------------ cross entropy, tokens on the rows
                 const bool row_ok = row < p.rows;
-                float row_lse2 = 0.0f, row_g = 0.0f;
+                float row_lse = 0.0f, row_g = 0.0f;
                 int target = -1;                           // column of the row's target
                 if (row_ok) {
                     const int64_t t = p.targets[row];
@@ -1088,7 +1087,7 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                     if (counts && t >= p.col0 && t - p.col0 < p.cols)
                         target = static_cast<int>(t - p.col0);
                     if constexpr (EPI == kEpiXentGrad) {
-                        row_lse2 = p.lse[row] * kLog2e;
+                        row_lse = p.lse[row];
                         row_g = counts ? p.dloss[row] * (p.gscale ? *p.gscale : 1.0f) : 0.0f;
                     }
                 }
@@ -1145,12 +1144,15 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
 #pragma unroll
                     for (int j = 0; j < kPart; ++j)
                         mx = fmaxf(mx, sum[j]);
-                    // a maximum of -inf (nothing but -inf) subtracts as zero
-                    const float sub = mx == -INFINITY ? 0.0f : mx * kLog2e;
+                    const F2 less = f2(-exp_base(mx));
                     float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int j = 0; j < kPart; ++j)
-                        add[j & 3] += exp2_fast(fmaf(sum[j], kLog2e, -sub));
+                    for (int j = 0; j < kPart; j += 2) {
+                        float e0, e1;
+                        split2(exp_from(f2(sum[j], sum[j + 1]), less), e0, e1);
+                        add[j & 3] += e0;
+                        add[(j & 3) + 1] += e1;
+                    }
                     if (row_ok)
                         p.stats[static_cast<int64_t>(w.col0 / BN * kParts + part) * p.tokens + row] =
                             make_float2(mx, (add[0] + add[1]) + (add[2] + add[3]));
@@ -1167,13 +1169,11 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                         const int col = col_part + c * 32;
                         float g[32];
                         tmem_ld_done(v);
-                        const F2 l2e = f2(kLog2e), sub = f2(-row_lse2), scale = f2(row_g);
+                        const F2 less = f2(-row_lse), scale = f2(row_g);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            const F2 pr = exp2_2(fma2(f2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), l2e,
-                                                      sub));
-                            split2(pr, g[j], g[j + 1]);
-                        }
+                        for (int j = 0; j < 32; j += 2)
+                            split2(exp_from(f2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), less), g[j],
+                                   g[j + 1]);
                         if (target >= col && target < col + 32) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j)

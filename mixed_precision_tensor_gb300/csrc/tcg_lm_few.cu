@@ -330,13 +330,12 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
                         if (lane == 0 && w.f0 + r == target[t] && w.f0 + r < p.feats)
                             p.target_logit[t] = v[r];
                     }
-                    // a maximum of -inf (nothing but -inf so far) subtracts as zero
-                    const float sub = mx == -INFINITY ? 0.0f : mx * kLog2e;
+                    const float base = exp_base(mx);
                     float e = 0.0f;
 #pragma unroll
                     for (int r = 0; r < R; ++r)
-                        e += exp2_fast(fmaf(v[r], kLog2e, -sub));
-                    run_s[t] = fmaf(run_s[t], exp2_fast(fmaf(run_m[t], kLog2e, -sub)), e);
+                        e += exp_from(v[r], base);
+                    run_s[t] = fmaf(run_s[t], exp_from(run_m[t], base), e);
                     run_m[t] = mx;
                 }
             }

@@ -57,3 +57,47 @@ def test_nothing_to_sum_or_to_write(handle):
     assert not dx.any() and dw.shape == (3, 0, 64) and db.shape == (3, 0)
     assert tcg.linear(handle, randn(g, 45, 64), empty(0, 64)).shape == (45, 0)
     tcg.check(tcg.tcg_get_device_error(handle.h))
+
+
+@pytest.mark.parametrize("t", [1, 2, 3, 20, 200])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("top", [91, 103, 117])
+def test_log_sum_exp_of_large_logits(handle, t, dtype, top):
+    """Whole logits of 50 below `top` to `top` over a large vocabulary, as a few tokens, tokens on
+    the columns and tokens on the rows.
+
+    Products and sums of the logits are exact.  The sum of exponentials is off by 1.5 2^-22 of
+    itself for exp, as much for each of at most four rescalings that change the maximum, and
+    2^-24 for each of at most 110 additions in a row; the logarithm by 2^-20; and lse, between
+    64 and 128, is rounded to 2^-17 apart: 1.3e-5, less than 2^-16 together."""
+    g = gen_of(t + top)
+    v, k = 100003, 16
+    x, w = torch.zeros(t, k, dtype=dtype, device="cuda"), torch.zeros(v, k, dtype=dtype, device="cuda")
+    x[:, 0] = 1
+    x[:, 1] = torch.arange(t, device="cuda") % 3 - 1
+    w[:, 0] = torch.randint(top - 50, top, (v,), generator=g, device="cuda").to(dtype)
+    w[:, 1] = torch.randint(-1, 1, (v,), generator=g, device="cuda").to(dtype)
+    target = torch.randint(0, v, (t,), generator=g, device="cuda")
+    loss, lse = tcg.linear_cross_entropy(handle, x, w, target)
+    logits = x.double() @ w.double().t()
+    want = torch.logsumexp(logits, 1)
+    assert float((lse.double() - want).abs().max()) <= 2.0 ** -16
+    off = loss.double() - (want - logits.gather(1, target[:, None])[:, 0])
+    assert float(off.abs().max()) <= 2.0 ** -16 + 2.0 ** -18
+
+
+@pytest.mark.parametrize("t", [3, 200])
+@pytest.mark.parametrize("top", [101, 103, 116])
+def test_gradient_of_a_certain_row(handle, t, top):
+    """A target 50 above everything else: its probability is one less 2e-17, and exp is within
+    2^-22 of itself, so the gradient of the logits has nothing above that."""
+    v, k = 5003, 16
+    x, w = torch.zeros(t, k, dtype=BF16, device="cuda"), torch.zeros(v, k, dtype=BF16, device="cuda")
+    x[:, 0] = 1
+    w[:, 0] = top - 50
+    w[7, 0] = top
+    target = torch.full((t,), 7, device="cuda")
+    _, lse = tcg.linear_cross_entropy(handle, x, w, target)
+    assert (lse == top).all()
+    dx, dw = tcg.linear_cross_entropy_backward(handle, x, w, target, lse, torch.ones(t, device="cuda"))
+    assert float(dx.abs().max()) <= top * 2.0 ** -21 and float(dw.abs().max()) <= t * 2.0 ** -21

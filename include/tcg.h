@@ -423,8 +423,9 @@ uint64_t tcg_launch_count(tcgHandle_t h);
  * tcg_set_split_k(h, 1) keeps tiles whole), those for a few tokens (up to four, or a few
  * rows of many experts) on the FP32 units.
  *
- * Accuracy: the bound of tcg_gemm_ex on the accumulator; the epilogue runs in FP32 with
- * exp and erfc to 1.5e-7 absolute or better; a D of ABtype adds one rounding.
+ * Accuracy: the bound of tcg_gemm_ex on the accumulator; the epilogue runs in FP32 with exp
+ * to a few 2^-23 of itself and Phi(-|x|) to 2e-6 + x^2 1e-7 of itself (what is below 2^-126
+ * is zero); a D of ABtype adds one rounding.
  *
  * Errors: INVALID_VALUE (NULL handle or needed pointer, misalignment, negative sizes, a
  * leading dimension too small, an unknown enumerator, host memory), NOT_SUPPORTED (type

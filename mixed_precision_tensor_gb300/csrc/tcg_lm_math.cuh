@@ -73,17 +73,22 @@ __device__ __forceinline__ F2 rcp_2(F2 x) { return each(x, rcp_fast); }
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// erfc(|x| / sqrt 2) / 2 and exp(-x^2 / 2), with erfc(a) = (a1 t + ... + a5 t^5) exp(-a^2),
-// t = 1 / (1 + p a): Abramowitz & Stegun 7.1.26, |error| <= 1.5e-7.  ax = min(|x|, 20), past
-// which both are zero.
+// erfc(|x| / sqrt 2) / 2 and gauss = exp(-x^2 / 2), ax = min(|x|, 20), past which both are
+// zero.  The quotient of the two is smooth in t = 1 / (1 + 0.361 |x|): t times a polynomial of
+// degree 6, fitted over |x| <= 13.5 for the least maximum of its error relative to the quotient
+// (7.3e-7).  So the tail is right to its own size where FP32 holds it: within 1.3e-6 of itself,
+// and x^2 7.5e-8 for the rounded argument of gauss.  (A fit of the absolute error has two terms
+// fewer, but is off by 5e-5 of itself at -3 and by 1% at -8.)
 __device__ __forceinline__ F2 half_erfc(F2 ax, F2 &gauss)
 {
-    const F2 t = rcp_2(fma2(f2(0.3275911f * 0.70710678118654752f), ax, f2(1.0f)));
+    const F2 t = rcp_2(fma2(f2(0.361f), ax, f2(1.0f)));
     gauss = exp2_2(ax * ax * f2(-0.5f * kLog2e));
-    F2 q = fma2(t, f2(0.5f * 1.061405429f), f2(0.5f * -1.453152027f));
-    q = fma2(t, q, f2(0.5f * 1.421413741f));
-    q = fma2(t, q, f2(0.5f * -0.284496736f));
-    q = fma2(t, q, f2(0.5f * 0.254829592f));
+    F2 q = fma2(t, f2(0.0477842689f), f2(-0.180867106f));
+    q = fma2(t, q, f2(0.180101722f));
+    q = fma2(t, q, f2(0.026798008f));
+    q = fma2(t, q, f2(0.139898449f));
+    q = fma2(t, q, f2(0.142172173f));
+    q = fma2(t, q, f2(0.144112632f));
     return q * t * gauss;
 }
 

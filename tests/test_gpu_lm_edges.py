@@ -1,9 +1,12 @@
 """Edges of the language-model products: nothing to sum, nothing to write, values far apart."""
+import math
+
 import pytest
 import torch
 
+import lm_reference as ref
 import mixed_precision_tensor_gb300 as tcg
-from test_gpu_lm import BF16, F16, gen_of, offsets_of, randn
+from test_gpu_lm import BF16, F16, F32, gen_of, offsets_of, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -101,3 +104,31 @@ def test_gradient_of_a_certain_row(handle, t, top):
     assert (lse == top).all()
     dx, dw = tcg.linear_cross_entropy_backward(handle, x, w, target, lse, torch.ones(t, device="cuda"))
     assert float(dx.abs().max()) <= top * 2.0 ** -21 and float(dw.abs().max()) <= t * 2.0 ** -21
+
+
+@pytest.mark.parametrize("t", [1, 40, 300])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_gelu_is_right_to_its_own_size(handle, t, dtype):
+    """FP32 outputs of GELU over its whole left tail, and its slope, relative to themselves.
+
+    Phi(-|z|): 1.3e-6 of itself (the fit, 1 / x and exp of 2^-22 each, the polynomial's FP32
+    sums) and z^2 7.5e-8 (exp's argument, rounded twice); one more rounding for the product."""
+    z = torch.linspace(-12, 12, 4801, device="cuda").to(dtype)
+    n, k = z.shape[0], 8
+    x = torch.zeros(t, k, dtype=dtype, device="cuda")
+    w = torch.zeros(n, k, dtype=dtype, device="cuda")
+    x[:, 0], w[:, 0] = 1, z
+    out = tcg.linear(handle, x, w, act="gelu", out_dtype=F32)
+    zd = z.double()
+    want = ref.act(zd, "gelu")
+    bound = (2e-6 + 1e-7 * zd * zd) * want.abs() + 2.0 ** -120
+    assert ((out.double() - want).abs() <= bound).all()
+    # one token's bias gradient is the slope in FP32: Phi + z phi
+    dout = torch.ones(1, 4808, dtype=dtype, device="cuda")[:, :n]
+    zrow = torch.zeros(1, 4808, dtype=dtype, device="cuda")
+    zrow[0, :n] = z
+    db = tcg.linear_backward(handle, dout, x[:1], w, z=zrow[:, :n], act="gelu", want=("dbias",))[2]
+    tail = 0.5 * torch.special.erfc(-zd / math.sqrt(2.0))
+    phi = zd.abs() * torch.exp(-zd * zd / 2) / math.sqrt(2 * math.pi)
+    bound = (2e-6 + 1e-7 * zd * zd) * (tail + phi) + 2.0 ** -120
+    assert ((db.double() - ref.slope(zd, "gelu")).abs() <= bound).all()

@@ -539,7 +539,9 @@ tcgStatus_t tcg_xent_forward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_t
  * rounded to `type`; either may be NULL.  The logits are formed again, a piece of the
  * vocabulary at a time; a piece of G is held in `type` (256 MiB at most, or 256 columns).
  * For FP16 it is held times a power of two chosen from max |dloss|, so that small
- * probabilities keep their bits.  dX is summed over the pieces in FP32.  Rows that do not
+ * probabilities keep their bits: entries are held to 2^-38 of max |dloss|, which rows of a
+ * much smaller dloss notice (use BF16 for rows more than 2^20 apart).  dX is summed over
+ * the pieces in FP32.  Rows that do not
  * count contribute nothing, whatever they hold in dloss or lse (a NaN in such a row of X
  * still reaches dW, as zero times it). */
 tcgStatus_t tcg_xent_backward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_t k, const void *X,

@@ -1539,11 +1539,6 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace
 
-static int lm_threads(int epi, int bn)
-{
-    return lm_wide(epi) && bn == 256 ? LmCfg<256, true>::kThreadsLm : LmCfg<128, true>::kThreadsLm;
-}
-
 cudaError_t launch_lm(const LmMaps &maps, const LmArgs &a, int epi, int out_kind, int bn, int grid,
                       cudaStream_t s)
 {
@@ -1555,7 +1550,7 @@ cudaError_t launch_lm(const LmMaps &maps, const LmArgs &a, int epi, int out_kind
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(lm_threads(epi, bn), 1, 1);
+    cfg.blockDim = dim3(LmCfg<256, true>::kThreadsLm, 1, 1);   // the same for every kind
     cfg.dynamicSmemBytes = kLmSmemBytes;
     cfg.stream = s;
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -244,7 +244,9 @@ def linear_backward(handle, dout, x, w, z=None, act="none", want=("dx", "dw", "d
     """Gradients of :func:`linear` (alpha = 1) for dout, the gradient of its output.
 
     With dz = dout * act'(z): dx = dz @ w, dw = dz.T @ x, dbias = dz.sum(0) (FP32, from the
-    unrounded dz).  The residual's gradient is beta * dout.  ``want`` names what is computed;
+    unrounded dz).  With an activation, dz is rounded to the type of x before the two products
+    (in BF16 their 2-norm error is 0.0024 of the result, 0.0017 without that rounding).  The
+    residual's gradient is beta * dout.  ``want`` names what is computed;
     the result is (dx, dw, dbias) with None for the others.  Outputs are made where not given.
     """
     _, k, dtype, dev = _input(x)
@@ -337,8 +339,11 @@ def linear_cross_entropy(handle, x, w, targets, ignore_index=-100, loss=None, ls
 def linear_cross_entropy_backward(handle, x, w, targets, lse, dloss, ignore_index=-100,
                                   want=("dx", "dw"), dx=None, dw=None):
     """(dx, dw) of :func:`linear_cross_entropy` for dloss, the gradient of each row's loss
-    (FP32; 1 / rows for a mean), and the lse that it returned.  ``want`` names what is
-    computed; None for the other.
+    (FP32; 1 / rows for a mean), and the lse that it returned.  The gradient of the logits is
+    rounded to the type of x before the two products (in BF16 their 2-norm error is 0.0024 of
+    the result, 0.0017 without; in FP16 0.0003 to 0.0005 and 0.0002); FP16 holds it times one
+    power of two for all rows, to 2^-38 of the largest |dloss|.  ``want`` names what is computed;
+    None for the other.
     """
     t, v, k, dtype, dev, ldx, ldw = _xent_args(x, w, targets)
     _vector(lse, "lse", (t,), (torch.float32,), dev)

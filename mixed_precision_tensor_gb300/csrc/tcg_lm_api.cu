@@ -130,10 +130,18 @@ Shape shape_of(tcgContext *h, const Product &p)
                                              load_kib(ceil_div(p.feats, 64), nkb, 64, P))) {
             s.epi = kEpiNarrow;
             s.bn = narrow_bn;
-        } else if (p.offsets && p.x_kmajor && per < 2048) {
+        } else if (p.offsets && p.x_kmajor && per < 1024) {
             // Groups' last tiles at the width that they have.  Narrower tiles read a group's
             // weights once for each of them (8 experts of 4096 x 4096, 62 rows each: 64 wide
-            // 64 us, 256 wide 52 us; with a skewed router 69 and 53).
+            // 64 us, 256 wide 52 us; with a skewed router 69 and 53).  Tokens on the rows instead
+            // (below) cost a 256-row tile for every group's end, and pay once tiles are many
+            // (us in a graph, on the columns / on the rows; out features x in):
+            //   rows   8 of 4096 x 2048   dx of these   32 of 2048 x 2048   64 of 2048 x 4096, skewed
+            //    128      33 / 34           29 / 31          59 / 61              197 / 208
+            //    512      55 / 52           50 / 48          95 / 91              386 / 417
+            //   1024      91 / 83           89 / 92         181 / 167             663 / 682
+            //   1536     135 / 125         136 / 130        288 / 248
+            //   4096     358 / 307         342 / 312
             s.epi = kEpiNarrow;
             s.bn = 256;
         } else {

@@ -20,11 +20,11 @@ def handle(cuda_device):
 
 @pytest.mark.parametrize("sizes,n,k,cut", [
     ([4100, 0, 3000, 2309], 264, 136, False), ([2048, 2048], 1000, 72, False), ([9000, 1, 0, 255], 72, 4104, True),
-    ([5000], 520, 4104, True), ([2100, 3011, 1100], 200, 2312, True)])
+    ([5000], 520, 4104, True), ([1024, 900, 1200], 264, 520, False), ([2100, 3011, 1100], 200, 2312, True)])
 @pytest.mark.parametrize("dtype", [BF16, F16])
 @pytest.mark.parametrize("lead,spare", [(0, 0), (300, 513)])
 def test_experts_with_many_rows(handle, sizes, n, k, cut, dtype, lead, spare):
-    """2048 rows and more for each expert: tokens on the accumulator's rows, each expert's own
+    """1024 rows and more for each expert: tokens on the accumulator's rows, each expert's own
     last tiles, whole tiles of rows of no expert, tiles cut along K."""
     e, rows = len(sizes), sum(sizes) + lead + spare
     act = ACTS[(n + e + lead) % 5]

@@ -222,7 +222,8 @@ tcgStatus_t queue(tcgContext *h, const Product &p, void *ws, LmArgs a = LmArgs{}
     a.min_share = s.share;
     a.split_gain = s.gain;
     a.align_splits = s.align;
-    a.group_m = h->group_m > 0 ? h->group_m : 8;
+    // never more than there are: group_m column tiles x row tiles then fit 32 bits, as all tiles do
+    a.group_m = std::min(h->group_m > 0 ? h->group_m : 8, a.num_row_tiles);
     a.in_bf16 = p.in == TCG_R_16BF;
     const bool a_kmajor = narrow ? p.w_kmajor : p.x_kmajor;
     const bool b_kmajor = narrow ? p.x_kmajor : p.w_kmajor;

@@ -132,3 +132,23 @@ def test_gelu_is_right_to_its_own_size(handle, t, dtype):
     phi = zd.abs() * torch.exp(-zd * zd / 2) / math.sqrt(2 * math.pi)
     bound = (2e-6 + 1e-7 * zd * zd) * (tail + phi) + 2.0 ** -120
     assert ((db.double() - ref.slope(zd, "gelu")).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("group_m", [1, 3, 1024])
+def test_tile_order_does_not_change_results(cuda_device, group_m):
+    """More rows of tiles walked together than there are, or fewer: the same bits."""
+    g = gen_of(6)
+    x, w, we = randn(g, 700, 264), randn(g, 1000, 264, std=1 / 16), randn(g, 3, 520, 264, std=1 / 16)
+    off = offsets_of([300, 0, 350], 20)
+    h = tcg.Handle()
+    want = tcg.linear(h, x, w, act="silu"), tcg.grouped_linear(h, x, we, off), \
+        *tcg.grouped_linear_backward(h, randn(g, 700, 520), x, we, off)[:1]
+    g = gen_of(6)
+    x, w, we = randn(g, 700, 264), randn(g, 1000, 264, std=1 / 16), randn(g, 3, 520, 264, std=1 / 16)
+    tcg.check(tcg.tcg_set_kernel_options(h.h, 2, group_m))
+    got = tcg.linear(h, x, w, act="silu"), tcg.grouped_linear(h, x, we, off), \
+        *tcg.grouped_linear_backward(h, randn(g, 700, 520), x, we, off)[:1]
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    tcg.check(tcg.tcg_get_device_error(h.h))
+    h.close()

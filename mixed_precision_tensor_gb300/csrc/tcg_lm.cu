@@ -605,7 +605,10 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
     // standard deviations of logits it moved the loss by 2e-6 of itself).  Where results
     // are FP32 statistics, or the accumulators few, K goes in segments of 512: each starts a
     // new accumulator, and the epilogue adds the segments in registers, rounding to nearest.
-    constexpr bool SEG = EPI != kEpiWide && EPI != kEpiXentGrad && !(EPI == kEpiNarrow && BN == 256);
+    // The gradient of the logits is among them: it takes a certain row's exp(logit - lse) from
+    // one, so its logits have to be those of the statistics (in one piece, K = 4096 and a logit
+    // of 40 left -6e-4 where nothing should be).
+    constexpr bool SEG = EPI != kEpiWide && !(EPI == kEpiNarrow && BN == 256);
     // Narrow tiles of 256 tokens: a group's last tile is multiplied at the width it has, in
     // steps of 32 tokens (tensor time follows N), so that a group of any size wastes 16
     // tokens of work on average.
@@ -1091,38 +1094,39 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                         row_g = counts ? p.dloss[row] * (p.gscale ? *p.gscale : 1.0f) : 0.0f;
                     }
                 }
-                if constexpr (EPI == kEpiXentStats) {
-                    float sum[kPart];
+                // the logits of the row, segment after segment
+                float sum[kPart];
 #pragma unroll
-                    for (int j = 0; j < kPart; ++j)
-                        sum[j] = 0.0f;
-                    bool stop = false;
-                    for (int seg = 0; seg < segments; ++seg) {
-                        if (!acquire()) {
-                            stop = true;
-                            break;
-                        }
-                        const uint32_t taddr = tmem_part + static_cast<uint32_t>(it % kAccBufs * BN);
-                        uint32_t va[16], vb[16];
-                        tmem_ld_32x32b_x16(taddr, va);
-#pragma unroll
-                        for (int c = 0; c < kPart; c += 32) {
-                            tmem_ld_done(va);
-                            tmem_ld_32x32b_x16(taddr + c + 16, vb);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                sum[c + j] += __uint_as_float(va[j]);
-                            tmem_ld_done(vb);
-                            if (c + 32 < kPart)
-                                tmem_ld_32x32b_x16(taddr + c + 32, va);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                sum[c + 16 + j] += __uint_as_float(vb[j]);
-                        }
-                        release();
-                    }
-                    if (stop)
+                for (int j = 0; j < kPart; ++j)
+                    sum[j] = 0.0f;
+                bool stop = false;
+                for (int seg = 0; seg < segments; ++seg) {
+                    if (!acquire()) {
+                        stop = true;
                         break;
+                    }
+                    const uint32_t taddr = tmem_part + static_cast<uint32_t>(it % kAccBufs * BN);
+                    uint32_t va[16], vb[16];
+                    tmem_ld_32x32b_x16(taddr, va);
+#pragma unroll
+                    for (int c = 0; c < kPart; c += 32) {
+                        tmem_ld_done(va);
+                        tmem_ld_32x32b_x16(taddr + c + 16, vb);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            sum[c + j] += __uint_as_float(va[j]);
+                        tmem_ld_done(vb);
+                        if (c + 32 < kPart)
+                            tmem_ld_32x32b_x16(taddr + c + 32, va);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            sum[c + 16 + j] += __uint_as_float(vb[j]);
+                    }
+                    release();
+                }
+                if (stop)
+                    break;
+                if constexpr (EPI == kEpiXentStats) {
                     const int ncol = w.col_end - col_part;
                     if (ncol < kPart) {
 #pragma unroll
@@ -1157,23 +1161,16 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                         p.stats[static_cast<int64_t>(w.col0 / BN * kParts + part) * p.tokens + row] =
                             make_float2(mx, (add[0] + add[1]) + (add[2] + add[3]));
                 } else {
-                    if (!acquire())
-                        break;
-                    const uint32_t taddr = tmem_part + static_cast<uint32_t>(it % kAccBufs * BN);
-                    constexpr int kChunks = kPart / 32;
-                    uint32_t v[32];
-                    __syncwarp();
-                    tmem_ld_32x32b_x32(taddr, v);
-#pragma unroll 1
-                    for (int c = 0; c < kChunks; ++c) {
-                        const int col = col_part + c * 32;
-                        float g[32];
-                        tmem_ld_done(v);
+#pragma unroll
+                    for (int c = 0; c < kPart; c += 32) {
+                        const int col = col_part + c;
+                        if (col >= w.col_end || row - lane >= w.row_end)
+                            break;
+                        float *g = sum + c;
                         const F2 less = f2(-row_lse), scale = f2(row_g);
 #pragma unroll
                         for (int j = 0; j < 32; j += 2)
-                            split2(exp_from(f2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), less), g[j],
-                                   g[j + 1]);
+                            split2(exp_from(f2(g[j], g[j + 1]), less), g[j], g[j + 1]);
                         if (target >= col && target < col + 32) {
 #pragma unroll
                             for (int j = 0; j < 32; ++j)
@@ -1188,21 +1185,15 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                                 g[j] = 0.0f;
                         }
                         __syncwarp();
-                        if (c + 1 < kChunks)
-                            tmem_ld_32x32b_x32(taddr + 32 * (c + 1), v);
+                        if (p.in_bf16)
+                            stage_put<kOutBF16, 32>(stage, lane, g);
                         else
-                            release();
-                        if (col < w.col_end && row - lane < w.row_end) {
-                            if (p.in_bf16)
-                                stage_put<kOutBF16, 32>(stage, lane, g);
-                            else
-                                stage_put<kOutF16, 32>(stage, lane, g);
-                            __syncwarp();
-                            stage_flush<2>(stage, lane, WarpBlock<2>(p.D, p.ldd, row - lane, col, lane),
-                                           w.row_end - (row - lane), w.col_end - col);
-                            __syncwarp();
-                        }
+                            stage_put<kOutF16, 32>(stage, lane, g);
+                        __syncwarp();
+                        stage_flush<2>(stage, lane, WarpBlock<2>(p.D, p.ldd, row - lane, col, lane),
+                                       w.row_end - (row - lane), w.col_end - col);
                     }
+                    __syncwarp();
                 }
             }
         }

@@ -152,3 +152,30 @@ def test_tile_order_does_not_change_results(cuda_device, group_m):
         assert torch.equal(a, b)
     tcg.check(tcg.tcg_get_device_error(h.h))
     h.close()
+
+
+@pytest.mark.parametrize("t", [3, 20, 300])
+@pytest.mark.parametrize("k", [1024, 4096, 8192])
+@pytest.mark.parametrize("logit", [24.0, 40.0, 100.0])
+def test_gradient_of_certain_rows_over_a_long_sum(handle, t, k, logit):
+    """Rows whose target stands out: 1 - p is the rest's probability, so dx has to vanish but
+    for what the logits that it is formed from differ by from those of lse.
+
+    Over 32 rows both come from the same sums: lse is rounded (2^-24 of itself), exp is within
+    2^-22, and so is what is taken from it.  With fewer rows the sums are in another order:
+    segments of 512 of K, 32 additions each, cut off at 2^-23 of the terms (all of one sign)."""
+    g = gen_of(k + t)
+    v = 3001
+    x, w = randn(g, t, k), randn(g, v, k, std=0.5 * k ** -0.5)
+    w[:t] = (logit * x.float() / x.float().square().sum(1, keepdim=True)).to(BF16)
+    target = torch.arange(t, device="cuda")
+    _, lse = tcg.linear_cross_entropy(handle, x, w, target)
+    dx, _ = tcg.linear_cross_entropy_backward(handle, x, w, target, lse, torch.ones(t, device="cuda"))
+    logits = x.double() @ w.double().t()
+    p = torch.softmax(logits, 1)
+    rest = p.sum(1) - p[target, target]
+    off = lse.double() * 2.0 ** -23 + 2.0 ** -21
+    if t <= 32:
+        off = off + 2 * (32 + k / 512) * 2.0 ** -23 * (x.double().abs() * w[:t].double().abs()).sum(1)
+    bound = 1.01 * (off + 2 * rest) * w.double().abs().max()
+    assert (dx.double().abs() <= bound[:, None]).all(), float((dx.double().abs().amax(1) / bound).max())

@@ -538,10 +538,11 @@ tcgStatus_t tcg_xent_forward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_t
  *     G = dloss (exp(L - lse) - [v = target]),   dX = G W (rows x k),   dW = G^T X (vocab x k)
  * rounded to `type`; either may be NULL.  The logits are formed again, a piece of the
  * vocabulary at a time; a piece of G is held in `type` (256 MiB at most, or 256 columns).
- * For FP16 it is held times a power of two chosen from max |dloss|, so that small
- * probabilities keep their bits: entries are held to 2^-38 of max |dloss|, which rows of a
- * much smaller dloss notice (use BF16 for rows more than 2^20 apart).  dX is summed over
- * the pieces in FP32.  Rows that do not
+ * It is held times 2^14 / max |dloss|, so that rows of the largest dloss (all of them, for a
+ * mean) lose nothing to the mantissa of dloss, and in FP16 small probabilities keep their
+ * bits: there entries are held to 2^-39 of max |dloss|, which rows of a much smaller dloss
+ * notice (use BF16 for rows more than 2^20 apart).  dX is summed over the pieces in FP32.
+ * Rows that do not
  * count contribute nothing, whatever they hold in dloss or lse (a NaN in such a row of X
  * still reaches dW, as zero times it). */
 tcgStatus_t tcg_xent_backward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_t k, const void *X,

@@ -1305,14 +1305,15 @@ __global__ void __launch_bounds__(1024)
     if (threadIdx.x == 0) {
         for (int i = 1; i < static_cast<int>(blockDim.x >> 5); ++i)
             m = fmaxf(m, part[i]);
+        float f = 1.0f;
         int e = 0;
         if (m > 0.0f && m < INFINITY) {
-            frexpf(m, &e);                     // m = f 2^e, 1/2 <= f < 1
+            f = frexpf(m, &e);                 // m = f 2^e, 1/2 <= f < 1
             e = 14 - e;
             e = e > 100 ? 100 : e;
         }
-        scale[0] = ldexpf(1.0f, e);
-        scale[1] = ldexpf(1.0f, -e);
+        scale[0] = ldexpf(1.0f / f, e);
+        scale[1] = ldexpf(f, -e);
     }
 }
 

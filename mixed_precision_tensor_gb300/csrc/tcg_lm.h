@@ -77,7 +77,7 @@ struct LmArgs {
     float2 *stats;             // [slot][token]: maximum, sum
     float *target_logit;
     const float *lse, *dloss;
-    const float *gscale;       // power of two that dloss is multiplied by; nullptr: 1
+    const float *gscale;       // what dloss is multiplied by; nullptr: 1
 
     uint32_t *err;
     unsigned long long wait_limit_ns;
@@ -171,8 +171,8 @@ cudaError_t launch_few(const LmFewArgs &a, int num_sms, cudaStream_t s);
 cudaError_t launch_xent_combine(const float2 *stats, int slots, int rows, const float *target_logit,
                                 const int64_t *targets, int64_t vocab, int64_t ignore, float *loss,
                                 float *lse, cudaStream_t s);
-// scale[0] = 2^e with 2^13 < max |dloss| 2^e <= 2^14 over the rows that count (1 where there is
-// no such e), scale[1] = 1 / scale[0].
+// scale[0] = 2^14 / max |dloss| over the rows that count (at most 2^101; 1 where there is no
+// such quotient), scale[1] = 1 / scale[0].
 cudaError_t launch_xent_scale(const float *dloss, const int64_t *targets, int rows, int64_t vocab,
                               int64_t ignore, float *scale, cudaStream_t s);
 // out[j][i] = scale * in[j][i], rounded to the 16-bit type.

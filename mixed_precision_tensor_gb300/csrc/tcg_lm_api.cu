@@ -1086,13 +1086,13 @@ tcgStatus_t tcg_xent_backward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_
     float *scale = reinterpret_cast<float *>(at + pl.grad_bytes + pl.acc_bytes);
     void *split_ws = at + pl.grad_bytes + pl.acc_bytes + pl.scale_bytes;
     const int64_t ldacc = (k + 3) / 4 * 4;
-    const bool scaled = type == TCG_R_16F;                  // FP16 gradients need range
-    cudaError_t e = cudaSuccess;
-    if (scaled) {
-        e = launch_xent_scale(dloss, targets, static_cast<int>(rows), vocab, ignore_index, scale,
-                              h->stream);
-        h->launches += 1;
-    }
+    // The gradient of the logits is held in 16 bits times 2^14 / max |dloss|.  FP16 needs the
+    // range.  Both types need the factor: with one dloss for all rows, a mean, every row's target
+    // entry is near -dloss and would be rounded by the same part of itself, up to 2^-8 (2^-11 in
+    // FP16), against all other entries; scaled, it is near a power of two and keeps its bits.
+    cudaError_t e = launch_xent_scale(dloss, targets, static_cast<int>(rows), vocab, ignore_index, scale,
+                                      h->stream);
+    h->launches += 1;
     for (int64_t i = 0; e == cudaSuccess && i < pl.pieces; ++i) {
         const int64_t c0 = i * pl.piece, width = vocab - c0 < pl.piece ? vocab - c0 : pl.piece;
         LmArgs a{};
@@ -1102,7 +1102,7 @@ tcgStatus_t tcg_xent_backward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_
         a.col0 = static_cast<int>(c0);
         a.lse = lse;
         a.dloss = dloss;
-        a.gscale = scaled ? scale : nullptr;
+        a.gscale = scale;
         Product g = xent_logits(x, c0, width, kEpiXentGrad);
         g.D = G;
         g.ldd = pl.piece;
@@ -1117,7 +1117,7 @@ tcgStatus_t tcg_xent_backward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_
             if (pl.pieces == 1) {
                 p.D = dX;
                 p.ldd = lddx;
-                p.alpha_dev = scaled ? scale + 1 : nullptr;
+                p.alpha_dev = scale + 1;
             } else {
                 p.D = acc;
                 p.ldd = ldacc;
@@ -1136,7 +1136,7 @@ tcgStatus_t tcg_xent_backward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_
             p.X = G;
             p.D = static_cast<uint16_t *>(dW) + c0 * lddw;
             p.ldd = lddw;
-            p.alpha_dev = scaled ? scale + 1 : nullptr;
+            p.alpha_dev = scale + 1;
             st = queue(h, p, split_ws);
             if (st != TCG_STATUS_SUCCESS)
                 return st;
@@ -1147,7 +1147,7 @@ tcgStatus_t tcg_xent_backward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_
         const int64_t cap = static_cast<int64_t>(h->num_sms) * 8;
         const int64_t blocks = (work + 255) / 256;
         e = launch_round_out(acc, ldacc, static_cast<int>(k), static_cast<int>(rows),
-                             scaled ? scale + 1 : nullptr, dX, lddx, out_kind_of(type),
+                             scale + 1, dX, lddx, out_kind_of(type),
                              static_cast<int>(blocks < cap ? blocks : cap), h->stream);
         h->launches += 1;
     }

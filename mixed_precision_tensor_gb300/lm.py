@@ -340,10 +340,10 @@ def linear_cross_entropy_backward(handle, x, w, targets, lse, dloss, ignore_inde
                                   want=("dx", "dw"), dx=None, dw=None):
     """(dx, dw) of :func:`linear_cross_entropy` for dloss, the gradient of each row's loss
     (FP32; 1 / rows for a mean), and the lse that it returned.  The gradient of the logits is
-    rounded to the type of x before the two products (in BF16 their 2-norm error is 0.0024 of
-    the result, 0.0017 without; in FP16 0.0003 to 0.0005 and 0.0002); FP16 holds it times one
-    power of two for all rows, to 2^-38 of the largest |dloss|.  ``want`` names what is computed;
-    None for the other.
+    rounded to the type of x before the two products (in BF16 their 2-norm error is about 0.0023
+    of the result, 0.0017 without; in FP16 0.0003 and 0.0002), times one factor for all rows:
+    FP16 holds it to 2^-39 of the largest |dloss|.  ``want`` names what is computed; None for the
+    other.
     """
     t, v, k, dtype, dev, ldx, ldw = _xent_args(x, w, targets)
     _vector(lse, "lse", (t,), (torch.float32,), dev)

@@ -179,3 +179,22 @@ def test_gradient_of_certain_rows_over_a_long_sum(handle, t, k, logit):
         off = off + 2 * (32 + k / 512) * 2.0 ** -23 * (x.double().abs() * w[:t].double().abs()).sum(1)
     bound = 1.01 * (off + 2 * rest) * w.double().abs().max()
     assert (dx.double().abs() <= bound[:, None]).all(), float((dx.double().abs().amax(1) / bound).max())
+
+
+@pytest.mark.parametrize("t", [1, 5, 200])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("dloss", [1 + 2.0 ** -8 + 2.0 ** -12, (1 + 2.0 ** -8 + 2.0 ** -12) / 200, 1.0])
+def test_gradients_of_a_mean_balance(handle, t, dtype, dloss):
+    """A row's gradients of the logits sum to zero.  Equal logits and one upstream gradient for
+    all rows: what is left are the roundings of 1 / vocab (times the vocabulary) and of
+    1 - 1 / vocab, whatever the upstream gradient's own bits; FP32 adds less than 2^-18."""
+    v, k = 2731, 16                           # 1 / 2731 = 1.4998 2^-12
+    x, w = torch.zeros(t, k, dtype=dtype, device="cuda"), torch.zeros(v, k, dtype=dtype, device="cuda")
+    w[:, 0] = 1
+    target = torch.arange(t, device="cuda")
+    _, lse = tcg.linear_cross_entropy(handle, x, w, target)
+    d = torch.full((t,), dloss, device="cuda")
+    dx, _ = tcg.linear_cross_entropy_backward(handle, x, w, target, lse, d, want=("dx",))
+    near = lambda y: abs(float(torch.tensor(y, dtype=torch.float64).to(dtype)) - y)  # noqa: E731
+    bound = dloss * (near(2.0 ** 12 / v) * v / 2.0 ** 12 + near(1 - 1 / v) + 2.0 ** -18)
+    assert float(dx[:, 0].double().abs().max()) <= bound * (1 + ref.U[dtype]) + ref.TINY[dtype]

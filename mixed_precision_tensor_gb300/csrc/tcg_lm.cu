@@ -17,7 +17,7 @@
 //   kEpiXentStats  logits X W^T that never leave the chip: per row and tile part the maximum
 //                  m and sum exp(logit - m), and the target's logit (tokens on the rows)
 //   kEpiXentNarrow the same for few tokens (tokens on the columns)
-//   kEpiXentGrad   dloss (exp(logit - lse) - [target]), rounded to 16 bits
+//   kEpiXentGrad   dloss (exp(logit - lse) - [target]), scaled, rounded to 16 bits
 //
 // What bounds it.  A 64-element block of K costs an SM 32 KiB of operands at tile 256 x 256,
 // loaded at 64 bytes a cycle in the 512 cycles that the tensor core takes for it; with both
@@ -25,7 +25,8 @@
 // so the epilogue's own traffic through it adds to short-K tiles (K = 512: loads alone 36,
 // with the product 43, with the epilogue 55 us for 1024 tiles).  From K = 4096 on it hides
 // behind the product and the power limit bounds (16384 x 4096 x 4096 BF16, GELU,
-// pre-activation kept: 350 us, 1.57 PFLOP/s; no epilogue 287 us, 1.92).
+// pre-activation kept: 305 us in a graph of a few calls, 1.80 PFLOP/s; 356 us a call, 1.54, one
+// after the other for seconds).
 //
 // Every wait is bounded as in tcg_kernels.cu: a wait that runs out sets a bit in the
 // device error word, every role stops and the kernel returns.

@@ -15,7 +15,8 @@
 // and 96 us, each waiting for its own chain of steps; twenty-four of two: 106 us), and X
 // loaded a stage ahead (8 rows over 64 experts, where X does not stay cached: 38 -> 25 us).
 // X through the ring instead made every SM read the same lines of L2 at once (four tokens:
-// 169 us).  The tensor kernel: 12.1 us for 4096 x 4096 where this takes 8.0.
+// 169 us).  The tensor kernel: 12.1 us for 4096 x 4096 where this takes 9.0 (7.6 where the
+// weights are still in L2).  Times in a graph.
 
 #include "tcg_lm_math.cuh"
 

@@ -1284,18 +1284,22 @@ __global__ void __launch_bounds__(32 * kCombineWarps)
     }
 }
 
+// One block for up to kScaleRows rows.  More blocks leave their maxima behind the result, and the
+// last of them to arrive joins them: a maximum is the same in any order.
+constexpr int kScaleRows = 4096, kScaleBlocks = 32;
 __global__ void __launch_bounds__(1024)
     tcg_xent_scale_kernel(const float *__restrict__ dloss, const int64_t *__restrict__ targets,
-                          int rows, int64_t vocab, int64_t ignore, float *scale)
+                          int rows, int64_t vocab, int64_t ignore, float *scale, uint32_t *cnt)
 {
     __shared__ float part[32];
     griddep_launch_dependents();
     griddep_wait();
     float m = 0.0f;
-    for (int i = threadIdx.x; i < rows; i += blockDim.x) {
+#pragma unroll 4
+    for (int64_t i = blockIdx.x * 1024ll + threadIdx.x; i < rows; i += gridDim.x * 1024ll) {
         const int64_t t = targets[i];
-        if (t != ignore && t >= 0 && t < vocab)
-            m = fmaxf(m, fabsf(dloss[i]));
+        const float d = fabsf(dloss[i]);
+        m = t != ignore && t >= 0 && t < vocab ? fmaxf(m, d) : m;
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1)
@@ -1304,8 +1308,18 @@ __global__ void __launch_bounds__(1024)
         part[threadIdx.x >> 5] = m;
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int i = 1; i < static_cast<int>(blockDim.x >> 5); ++i)
+        for (int i = 1; i < 32; ++i)
             m = fmaxf(m, part[i]);
+        if (gridDim.x > 1) {
+            __stcg(scale + 2 + blockIdx.x, m);
+            fence_acq_rel_gpu();
+            if (atomicAdd(cnt, 1u) != gridDim.x - 1)
+                return;
+            *cnt = 0u;                         // every block has arrived
+            fence_acq_rel_gpu();
+            for (int i = 0; i < static_cast<int>(gridDim.x); ++i)
+                m = fmaxf(m, __ldcg(scale + 2 + i));
+        }
         float f = 1.0f;
         int e = 0;
         if (m > 0.0f && m < INFINITY) {
@@ -1599,10 +1613,11 @@ cudaError_t launch_xent_combine(const float2 *stats, int slots, int rows, const 
 }
 
 cudaError_t launch_xent_scale(const float *dloss, const int64_t *targets, int rows, int64_t vocab,
-                              int64_t ignore, float *scale, cudaStream_t s)
+                              int64_t ignore, float *scale, uint32_t *cnt, cudaStream_t s)
 {
-    return launch_pdl(tcg_xent_scale_kernel, dim3(1), dim3(1024), s, 0, dloss, targets, rows, vocab,
-                      ignore, scale);
+    const int blocks = (rows + kScaleRows - 1) / kScaleRows;
+    return launch_pdl(tcg_xent_scale_kernel, dim3(blocks < kScaleBlocks ? blocks : kScaleBlocks), dim3(1024), s,
+                      0, dloss, targets, rows, vocab, ignore, scale, cnt);
 }
 
 cudaError_t launch_round_out(const float *in, int64_t ldi, int rows, int cols, const float *scale,

@@ -13,7 +13,8 @@
 namespace tcg {
 
 constexpr int kLmMaxGroups = 384;      // experts of one grouped call (a table in shared memory)
-constexpr int kLmCounters = 1024;      // split counters of a handle: 4 per cut tile, one tile per pair at most
+constexpr int kLmCounters = 1024;      // split counters of a handle: 4 per cut tile, one tile per pair at most;
+constexpr int kScaleCounter = 1023;    // and one of the cross entropy's scale
 constexpr int kLmMaxStages = 12;
 constexpr int kLmMaxAccs = 16;
 // Shared memory: the operand ring, and (tokens on the rows) 2 KiB of staging per epilogue
@@ -172,9 +173,10 @@ cudaError_t launch_xent_combine(const float2 *stats, int slots, int rows, const 
                                 const int64_t *targets, int64_t vocab, int64_t ignore, float *loss,
                                 float *lse, cudaStream_t s);
 // scale[0] = 2^14 / max |dloss| over the rows that count (at most 2^101; 1 where there is no
-// such quotient), scale[1] = 1 / scale[0].
+// such quotient), scale[1] = 1 / scale[0]; 32 words after them are scratch.  cnt: a counter that
+// is zero before and after.
 cudaError_t launch_xent_scale(const float *dloss, const int64_t *targets, int rows, int64_t vocab,
-                              int64_t ignore, float *scale, cudaStream_t s);
+                              int64_t ignore, float *scale, uint32_t *cnt, cudaStream_t s);
 // out[j][i] = scale * in[j][i], rounded to the 16-bit type.
 cudaError_t launch_round_out(const float *in, int64_t ldi, int rows, int cols, const float *scale,
                              void *out, int64_t ldo, int out_kind, int grid, cudaStream_t s);

@@ -1091,7 +1091,7 @@ tcgStatus_t tcg_xent_backward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_
     // entry is near -dloss and would be rounded by the same part of itself, up to 2^-8 (2^-11 in
     // FP16), against all other entries; scaled, it is near a power of two and keeps its bits.
     cudaError_t e = launch_xent_scale(dloss, targets, static_cast<int>(rows), vocab, ignore_index, scale,
-                                      h->stream);
+                                      h->d_cnt + kScaleCounter, h->stream);
     h->launches += 1;
     for (int64_t i = 0; e == cudaSuccess && i < pl.pieces; ++i) {
         const int64_t c0 = i * pl.piece, width = vocab - c0 < pl.piece ? vocab - c0 : pl.piece;

@@ -172,7 +172,7 @@ def linear(handle, x, w, bias=None, act="none", residual=None, beta=1.0, alpha=1
 
     FP32 outputs are as exact as the tensor core's FP32 sums, which cut off rather than round:
     for long calls (2-norm, 2048 x 2048 outputs) 4e-6 of the result at k = 4096, 2e-5 at 16384;
-    up to 128 tokens, whose sums are joined from segments of 512, 4e-7.
+    calls of few tokens, whose sums are joined from segments of 512, 4e-7.
     """
     t, k, dtype, dev = _input(x)
     n = w.shape[0]

@@ -114,3 +114,26 @@ def test_cut_tiles_in_equal_ranges(handle, dtype):
         assert torch.equal(tcg.linear_backward(handle, d, x, torch.zeros(n, t, dtype=dtype, device="cuda"),
                                                want=("dw",))[1], want)
     tcg.check(tcg.tcg_get_device_error(handle.h))
+
+
+@pytest.mark.parametrize("rows", [4096, 4097, 70001, 300000])
+@pytest.mark.parametrize("where", [0.0, 0.37, 1.0])
+def test_scale_of_many_rows(handle, rows, where):
+    """The largest upstream gradient may be anywhere among rows of several blocks: FP16 entries of
+    its row stay in range, and the next calls find the counters as they should be."""
+    x, w, target, _ = xent_case(rows, 50, 16, F16)
+    at = int(where * (rows - 1))
+    dloss = torch.full((rows,), 2.0 ** -6, device="cuda")
+    dloss[at] = 40.0
+    target[(at + 1) % rows] = -100
+    dloss[(at + 1) % rows] = 1e9               # does not count
+    _, lse = tcg.linear_cross_entropy(handle, x, w, target)
+    first = None
+    for _ in range(3):
+        dx, dw = tcg.linear_cross_entropy_backward(handle, x, w, target, lse, dloss)
+        assert first is None or (same_bits(dx, first[0]) and same_bits(dw, first[1]))
+        first = dx, dw
+    d = torch.where(target >= 0, dloss, torch.zeros_like(dloss))
+    (dx_w, dw_w), (ex, ew) = ref.xent_backward(x, w, target, -100, d)
+    ref.within(dx, dx_w, ex, "dx")
+    ref.within(dw, dw_w, ew, "dw")

@@ -50,7 +50,8 @@
  * pinned (cudaHostAlloc), managed or another device's memory is INVALID_VALUE with
  * nothing launched.  Host memory goes through the _host entry points.  All calls
  * are asynchronous on the handle's stream and return without a device
- * synchronisation (except tcg_get_device_error).  The GEMM kernel is launched with
+ * synchronisation (except tcg_get_device_error, a handle's first call, and a call that
+ * grows the handle's own workspace, see tcg_set_workspace).  The GEMM kernel is launched with
  * programmatic stream serialization: it may be resident before the previous kernel
  * on the stream has finished, but it reads and writes no global memory until that
  * kernel has completed, so stream order is kept.  A handle is not thread-safe: use

@@ -457,9 +457,11 @@ tcgStatus_t acquire_ws(tcgContext *h, size_t need, void **ws)
         return TCG_STATUS_SUCCESS;
     }
     cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(h->stream, &capture) != cudaSuccess)
+    // an error: the legacy default stream beside a capture of another one, no capture of its own
+    const bool known = cudaStreamIsCapturing(h->stream, &capture) == cudaSuccess;
+    if (!known)
         cudaGetLastError();
-    const bool capturing = capture != cudaStreamCaptureStatusNone;
+    const bool capturing = known && capture != cudaStreamCaptureStatusNone;
     if (h->ws_own_bytes < need) {
         if (capturing)
             return TCG_STATUS_ALLOC_FAILED;

@@ -8,7 +8,7 @@ from test_gpu_lm import BF16, F32, gen_of, randn, same_bits
 
 pytestmark = pytest.mark.gpu
 
-BUSY = 1_000_000_000                  # clock cycles that a stream is kept busy for: about half a second
+BUSY = 2_000_000_000                  # clock cycles that a stream is kept busy for: about a second
 
 
 def cut_product(seed=1):

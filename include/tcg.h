@@ -428,6 +428,8 @@ uint64_t tcg_launch_count(tcgHandle_t h);
  * to a few 2^-23 of itself and Phi(-|x|) to 2e-6 + x^2 1e-7 of itself (what is below 2^-126
  * is zero); a D of ABtype adds one rounding.
  *
+ * Outputs must not overlap inputs or each other but where a call says so.
+ *
  * Errors: INVALID_VALUE (NULL handle or needed pointer, misalignment, negative sizes, a
  * leading dimension too small, an unknown enumerator, host memory), NOT_SUPPORTED (type
  * combination, extents near 2^31 or k above 2^30, more than 384 groups), and the CUDA errors of

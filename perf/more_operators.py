@@ -261,6 +261,8 @@ def run(state):
             dx, dw = tcg.rms_norm_backward(h, s["dout"], s["x"], s["weight"], eps=_EPS, dsum=s["residual"])
             return {"dx": dx, "dw": dw}
         kept = s.get("sum")
+        if kept is not None:  # rows as far apart as those of x, a multiple of 16 bytes
+            kept = torch.empty_strided(kept.shape, s["x"].stride(), dtype=kept.dtype, device=kept.device)
         res = {} if kept is None else {"sum": kept}
         if c["pass"] == "forward":
             return {**res, "out": tcg.rms_norm(h, s["x"], s["weight"], eps=_EPS, residual=s["residual"],

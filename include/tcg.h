@@ -558,6 +558,74 @@ tcgStatus_t tcg_xent_backward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_
 tcgStatus_t tcg_xent_workspace_size(tcgHandle_t h, int64_t rows, int64_t vocab, int64_t k,
                                     tcgDataType_t type, int backward, size_t *bytes);
 
+/* ------------------------------------------------- The feed-forward half of a layer
+ *
+ * What stands around those products in a decoder layer: the norm in front of the projections,
+ * with the residual stream; gated projections; projections with 4-bit weights.  Types, alignment,
+ * streams, workspaces, errors and accuracy as above. */
+
+/* Gated projections: with the rows 0 .. m - 1 of the row-major A (2 m x k, leading dimension
+ * lda >= k) giving g = A_g B and the rows m .. 2 m - 1 giving u = A_u B,
+ *     D = act(g) * u          (m x n, column-major: a column per token, as in tcg_gemm_epilogue)
+ * B is k x n (row-major: n tokens of k features).  Z, if not NULL, receives g above u (2 m x n,
+ * ABtype, rounded), which the backward pass wants.  The workspace call gives the bytes needed. */
+tcgStatus_t tcg_gemm_gated(tcgHandle_t h, tcgActivation_t activation, int64_t m, int64_t n, int64_t k,
+                           const void *A, int64_t lda, const void *B, int64_t ldb, tcgDataType_t ABtype,
+                           void *D, tcgDataType_t Dtype, int64_t ldd, void *Z, int64_t ldz);
+tcgStatus_t tcg_gemm_gated_workspace_size(tcgHandle_t h, int64_t m, int64_t n, int64_t k, size_t *bytes);
+
+/* Its backward pass.  Row-major: dD n x m, Z n x 2 m, W 2 m x k (the A of the forward call), X n x k.
+ *     dZ = [dD * u * act'(g) | dD * act(g)],   dX = dZ W (n x k),   dW = dZ^T X (2 m x k),
+ * all of one 16-bit type.  dX or dW may be NULL.  dZ is formed in the workspace, rounded. */
+tcgStatus_t tcg_gated_backward(tcgHandle_t h, tcgActivation_t activation, int64_t m, int64_t n, int64_t k,
+                               const void *dD, int64_t lddd, const void *Z, int64_t ldz, const void *W,
+                               int64_t ldw, const void *X, int64_t ldx, tcgDataType_t type, void *dX,
+                               int64_t lddx, void *dW, int64_t lddw);
+tcgStatus_t tcg_gated_backward_workspace_size(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int with_dX,
+                                              int with_dW, size_t *bytes);
+
+/* Root-mean-square norm of each row (row-major, rows x k, k at most 32768):
+ *     s = X + R,   Y = s / sqrt(mean(s^2) + eps) * W
+ * X, R and S are of the 16-bit `type`; W (k entries) is of that type or FP32.  R NULL: s = X.  S, if
+ * not NULL, receives s rounded; Y is formed from the unrounded s.  Ytype is `type`, or
+ * TCG_R_8F_E4M3: then scale[i] = max(max |Y[i, :]| / 448, 2^-100) and Y holds Y / scale, rounded to
+ * nearest even, so that Y * scale stands for the result; scale is not touched otherwise.  S may be X
+ * or R, a 16-bit Y may be X or R, not both the same.  A row with a NaN or an infinity has
+ * entries that are NaN (in 8 bits all of them, and its scale); entries above 2^63 overflow the
+ * FP32 sum of squares, which leaves zeros. */
+tcgStatus_t tcg_rms_norm(tcgHandle_t h, int64_t rows, int64_t k, const void *X, int64_t ldx, const void *R,
+                         int64_t ldr, void *S, int64_t lds, const void *W, tcgDataType_t Wtype, float eps,
+                         tcgDataType_t type, void *Y, tcgDataType_t Ytype, int64_t ldy, float *scale);
+
+/* Its gradient, X being the rows that were normalised (the S of a call with a residual):
+ *     r = 1 / sqrt(mean(X^2) + eps),   g = dY * W,   dX = r g - X r^3 mean(g X) + dS,
+ *     dW[j] = sum over the rows of dY[i, j] X[i, j] r[i]      (FP32, k entries)
+ * dS, the gradient that arrives at S, may be NULL (0); dX (which is also R's gradient) or dW may be
+ * NULL.  dX may be dY or dS.  The order of the sums depends only on the sizes. */
+tcgStatus_t tcg_rms_norm_backward(tcgHandle_t h, int64_t rows, int64_t k, const void *dY, int64_t lddy,
+                                  const void *X, int64_t ldx, const void *dS, int64_t ldds, const void *W,
+                                  tcgDataType_t Wtype, float eps, tcgDataType_t type, void *dX, int64_t lddx,
+                                  float *dW);
+tcgStatus_t tcg_rms_norm_backward_workspace_size(tcgHandle_t h, int64_t rows, int64_t k, size_t *bytes);
+
+/* Products with 4-bit weights.  A is row-major, m rows (gated: 2 m) of k elements, two a byte:
+ * element 2 j of a row is the low half of its byte j.  lda is in bytes, a multiple of 16.  The k
+ * elements of a row fall into ceil(k / group) groups (group 32, 64 or 128) with a scale and, if
+ * zeros is not NULL, a zero each (row-major, contiguous; Stype is Btype or TCG_R_32F):
+ *     w = (q - zero) * scale,   zero = 8 where zeros is NULL.
+ * B is k x n (n tokens of k features).  gated = 0: D = act(w B + bias) + beta * C as in
+ * tcg_gemm_epilogue (epilogue->Z must be NULL).  gated = 1: D = act(w_g B) * (w_u B) with the rows
+ * 0 .. m - 1 and m .. 2 m - 1, only the epilogue's activation being used; bias and C are not
+ * supported.  Up to 64 tokens the packed weights are read as they are and q - zero meets the scale
+ * in FP32; more tokens take the weights rounded to Btype, expanded in the workspace (its size from
+ * the second call). */
+tcgStatus_t tcg_gemm_4bit(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int64_t group, const void *A,
+                          int64_t lda, const void *scales, const void *zeros, tcgDataType_t Stype, const void *B,
+                          int64_t ldb, tcgDataType_t Btype, void *D, tcgDataType_t Dtype, int64_t ldd, int gated,
+                          const tcgEpilogue_t *epilogue);
+tcgStatus_t tcg_gemm_4bit_workspace_size(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int gated,
+                                         size_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif

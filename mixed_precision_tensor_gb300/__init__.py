@@ -14,7 +14,9 @@ Names mirror the C ABI: ``tcg_create``, ``tcg_destroy``, ``tcg_set_stream``,
 conveniences on top of them.
 
 ``linear``, ``grouped_linear`` and ``linear_cross_entropy`` with their backward passes
-(module ``lm``) are the language-model products on torch tensors.
+(module ``lm``) are the language-model products on torch tensors; ``rms_norm``,
+``gated_linear`` and ``linear_4bit`` (module ``ffn``) are what surrounds them in the
+feed-forward half of a decoder layer.
 """
 from __future__ import annotations
 
@@ -50,7 +52,10 @@ EXPORTS = ("tcg_create", "tcg_destroy", "tcg_set_stream", "tcg_set_workspace",
            "tcg_set_tf32_rounding", "tcg_gemm_epilogue", "tcg_gemm_grouped",
            "tcg_gemm_grouped_k", "tcg_gemm_epilogue_workspace_size", "tcg_epilogue_backward",
            "tcg_linear_backward", "tcg_linear_backward_workspace_size", "tcg_xent_forward",
-           "tcg_xent_backward", "tcg_xent_workspace_size")
+           "tcg_xent_backward", "tcg_xent_workspace_size", "tcg_gemm_gated",
+           "tcg_gemm_gated_workspace_size", "tcg_gated_backward",
+           "tcg_gated_backward_workspace_size", "tcg_rms_norm", "tcg_rms_norm_backward",
+           "tcg_rms_norm_backward_workspace_size", "tcg_gemm_4bit", "tcg_gemm_4bit_workspace_size")
 
 _lock = threading.Lock()
 _lib = None
@@ -175,6 +180,28 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.tcg_xent_workspace_size.restype = st
         lib.tcg_xent_workspace_size.argtypes = [vp, i64, i64, i64, ci, ci,
                                                 ctypes.POINTER(ctypes.c_size_t)]
+        size = ctypes.POINTER(ctypes.c_size_t)
+        lib.tcg_gemm_gated.restype = st
+        lib.tcg_gemm_gated.argtypes = [vp, ci, i64, i64, i64, vp, i64, vp, i64, ci, vp, ci, i64, vp, i64]
+        lib.tcg_gemm_gated_workspace_size.restype = st
+        lib.tcg_gemm_gated_workspace_size.argtypes = [vp, i64, i64, i64, size]
+        lib.tcg_gated_backward.restype = st
+        lib.tcg_gated_backward.argtypes = [vp, ci, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, ci,
+                                           vp, i64, vp, i64]
+        lib.tcg_gated_backward_workspace_size.restype = st
+        lib.tcg_gated_backward_workspace_size.argtypes = [vp, i64, i64, i64, ci, ci, size]
+        lib.tcg_rms_norm.restype = st
+        lib.tcg_rms_norm.argtypes = [vp, i64, i64, vp, i64, vp, i64, vp, i64, vp, ci, f32, ci, vp, ci, i64, vp]
+        lib.tcg_rms_norm_backward.restype = st
+        lib.tcg_rms_norm_backward.argtypes = [vp, i64, i64, vp, i64, vp, i64, vp, i64, vp, ci, f32, ci, vp,
+                                              i64, vp]
+        lib.tcg_rms_norm_backward_workspace_size.restype = st
+        lib.tcg_rms_norm_backward_workspace_size.argtypes = [vp, i64, i64, size]
+        lib.tcg_gemm_4bit.restype = st
+        lib.tcg_gemm_4bit.argtypes = [vp, i64, i64, i64, i64, vp, i64, vp, vp, ci, vp, i64, ci, vp, ci, i64,
+                                      ci, pep]
+        lib.tcg_gemm_4bit_workspace_size.restype = st
+        lib.tcg_gemm_4bit_workspace_size.argtypes = [vp, i64, i64, i64, ci, size]
         _lib = lib
         return lib
 
@@ -432,6 +459,57 @@ def tcg_xent_workspace_size(h, rows, vocab, k, type, backward) -> int:
     return out.value
 
 
+def tcg_gemm_gated(h, activation, m, n, k, A, lda, B, ldb, ABtype, D, Dtype, ldd, Z=None, ldz=0) -> int:
+    return load_library().tcg_gemm_gated(h, activation, m, n, k, _ptr(A), lda, _ptr(B), ldb, ABtype, _ptr(D),
+                                         Dtype, ldd, _ptr(Z), ldz)
+
+
+def tcg_gemm_gated_workspace_size(h, m, n, k) -> int:
+    out = ctypes.c_size_t(0)
+    check(load_library().tcg_gemm_gated_workspace_size(h, m, n, k, ctypes.byref(out)))
+    return out.value
+
+
+def tcg_gated_backward(h, activation, m, n, k, dD, lddd, Z, ldz, W, ldw, X, ldx, type, dX, lddx, dW,
+                       lddw) -> int:
+    return load_library().tcg_gated_backward(h, activation, m, n, k, _ptr(dD), lddd, _ptr(Z), ldz, _ptr(W), ldw,
+                                             _ptr(X), ldx, type, _ptr(dX), lddx, _ptr(dW), lddw)
+
+
+def tcg_gated_backward_workspace_size(h, m, n, k, dX=True, dW=True) -> int:
+    out = ctypes.c_size_t(0)
+    check(load_library().tcg_gated_backward_workspace_size(h, m, n, k, dX, dW, ctypes.byref(out)))
+    return out.value
+
+
+def tcg_rms_norm(h, rows, k, X, ldx, R, ldr, S, lds, W, Wtype, eps, type, Y, Ytype, ldy, scale=None) -> int:
+    return load_library().tcg_rms_norm(h, rows, k, _ptr(X), ldx, _ptr(R), ldr, _ptr(S), lds, _ptr(W), Wtype, eps,
+                                       type, _ptr(Y), Ytype, ldy, _ptr(scale))
+
+
+def tcg_rms_norm_backward(h, rows, k, dY, lddy, X, ldx, dS, ldds, W, Wtype, eps, type, dX, lddx, dW) -> int:
+    return load_library().tcg_rms_norm_backward(h, rows, k, _ptr(dY), lddy, _ptr(X), ldx, _ptr(dS), ldds, _ptr(W),
+                                                Wtype, eps, type, _ptr(dX), lddx, _ptr(dW))
+
+
+def tcg_rms_norm_backward_workspace_size(h, rows, k) -> int:
+    out = ctypes.c_size_t(0)
+    check(load_library().tcg_rms_norm_backward_workspace_size(h, rows, k, ctypes.byref(out)))
+    return out.value
+
+
+def tcg_gemm_4bit(h, m, n, k, group, A, lda, scales, zeros, Stype, B, ldb, Btype, D, Dtype, ldd, gated=0,
+                  epilogue=None) -> int:
+    return load_library().tcg_gemm_4bit(h, m, n, k, group, _ptr(A), lda, _ptr(scales), _ptr(zeros), Stype,
+                                        _ptr(B), ldb, Btype, _ptr(D), Dtype, ldd, gated, epilogue)
+
+
+def tcg_gemm_4bit_workspace_size(h, m, n, k, gated=0) -> int:
+    out = ctypes.c_size_t(0)
+    check(load_library().tcg_gemm_4bit_workspace_size(h, m, n, k, gated, ctypes.byref(out)))
+    return out.value
+
+
 # ------------------------------------------------------------ conveniences
 _TORCH_TYPE = {}
 
@@ -537,3 +615,5 @@ def gemm_rowmajor(handle: Handle, A, B, C, alpha=1.0, beta=0.0, tf32=False,
 
 from .lm import (grouped_linear, grouped_linear_backward, linear, linear_backward,  # noqa: E402
                  linear_cross_entropy, linear_cross_entropy_backward)
+from .ffn import (gated_linear, gated_linear_backward, linear_4bit, rms_norm,  # noqa: E402
+                  rms_norm_8bit, rms_norm_backward)

@@ -22,7 +22,7 @@ OUT_DIR = os.path.join(PKG, "_lib")
 OBJ_DIR = os.path.join(ROOT, "_build", "tcg")
 LIB_PATH = os.path.join(OUT_DIR, "libtcg.so")
 SOURCES = ["tcg_api.cu", "tcg_kernels.cu", "tcg_lm_api.cu", "tcg_lm.cu",
-           "tcg_lm_few.cu"]
+           "tcg_lm_few.cu", "tcg_lm_norm.cu", "tcg_lm_w4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

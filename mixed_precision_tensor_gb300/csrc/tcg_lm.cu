@@ -18,6 +18,8 @@
 //                  m and sum exp(logit - m), and the target's logit (tokens on the rows)
 //   kEpiXentNarrow the same for few tokens (tokens on the columns)
 //   kEpiXentGrad   dloss (exp(logit - lse) - [target]), scaled, rounded to 16 bits
+//   kEpiGatedNarrow, kEpiGatedWide   act(g) u, both products in one tile: the operands' bytes and
+//                  the tensor work of one product with twice the features, without its output
 //
 // What bounds it.  A 64-element block of K costs an SM 32 KiB of operands at tile 256 x 256,
 // loaded at 64 bytes a cycle in the 512 cycles that the tensor core takes for it; with both
@@ -92,8 +94,10 @@ struct LmUnit {
 // tiles, every cut tile instead gets the same number of pairs and the same K ranges, so that
 // tiles read the same blocks at the same time.)  A pair has at most one piece that starts
 // inside a tile (slot 2 c) and one that starts a tile without ending it (slot 2 c + 1).
-template <bool WIDE, int BN, bool RK>
+template <bool WIDE, int BN, bool RK, bool GATED>
 struct LmWalk {
+    // features of a tile: of the accumulator's columns (wide) or rows
+    static constexpr int kFeats = (WIDE ? BN : 256) / (GATED ? 2 : 1);
     int c, P;
     int t, null_i;
     uint32_t pos;                                   // next block of the cut tiles; ~0: not begun
@@ -210,10 +214,10 @@ struct LmWalk {
         if constexpr (WIDE) {
             w.row0 = b + rt * 256;
             w.row_end = e;
-            w.col0 = ct * BN;
+            w.col0 = ct * kFeats;
             w.col_end = p.cols;
         } else {
-            w.row0 = rt * 256;
+            w.row0 = rt * kFeats;
             w.row_end = p.rows;
             w.col0 = b + ct * BN;
             w.col_end = e;
@@ -404,13 +408,15 @@ struct WarpBlock {
     }
 };
 
-// The staged block to memory: its first nrow rows and ncol columns.
+// The staged block to memory: its first nrow rows and ncol columns.  aligned: whether the block
+// starts at a multiple of 16 bytes.
 template <int ES>
-__device__ __forceinline__ void stage_flush(uint8_t *stage, int lane, WarpBlock<ES> m, int nrow, int ncol)
+__device__ __forceinline__ void stage_flush(uint8_t *stage, int lane, WarpBlock<ES> m, int nrow, int ncol,
+                                            bool aligned = true)
 {
     using M = WarpBlock<ES>;
     const int row = lane / 4, piece = lane % 4;
-    if (nrow >= 32 && ncol >= 4 * M::kElems) {
+    if (aligned && nrow >= 32 && ncol >= 4 * M::kElems) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             *reinterpret_cast<uint4 *>(m.at) = *stage_piece(stage, i * 8 + row, piece);
@@ -423,8 +429,8 @@ __device__ __forceinline__ void stage_flush(uint8_t *stage, int lane, WarpBlock<
         if (i * 8 + row >= nrow)
             break;
         const uint8_t *v = reinterpret_cast<const uint8_t *>(stage_piece(stage, i * 8 + row, piece));
-        const int n = ncol - piece * M::kElems;
-        if (n >= M::kElems) {
+        const int n = min(ncol - piece * M::kElems, M::kElems);
+        if (aligned && n == M::kElems) {
             *reinterpret_cast<uint4 *>(m.at) = *reinterpret_cast<const uint4 *>(v);
         } else {
 #pragma unroll 1
@@ -576,6 +582,76 @@ __device__ __forceinline__ void finish_wide(const LmArgs &p, float (&z)[32], con
     }
 }
 
+// A gated product: a warp's 32 tokens (this lane's g and u) x 32 features from `col` on.
+template <int OUT>
+__device__ __forceinline__ void finish_gated_wide(const LmArgs &p, float (&g)[32], float (&u)[32],
+                                                  const LmUnit &w, int row0, int col, uint8_t *stage, int lane)
+{
+    constexpr int ES = OUT == kOutF32 ? 4 : 2, kN = 64 / ES;
+    const int nrow = w.row_end - row0, ncol = w.col_end - col;
+    if (p.Z) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (p.in_bf16)
+                stage_put<kOutBF16, 32>(stage, lane, h ? u : g);
+            else
+                stage_put<kOutF16, 32>(stage, lane, h ? u : g);
+            __syncwarp();
+            stage_flush<2>(stage, lane, WarpBlock<2>(p.Z, p.ldz, row0, col + h * p.cols, lane), nrow, ncol,
+                           h == 0 || p.cols % 8 == 0);
+            __syncwarp();
+        }
+    }
+    apply_act(p.act, g);
+#pragma unroll
+    for (int j = 0; j < 32; j += 2)
+        split2(f2(g[j], g[j + 1]) * f2(u[j], u[j + 1]), g[j], g[j + 1]);
+#pragma unroll
+    for (int h = 0; h < 32; h += kN) {
+        if (h > 0 && ncol <= h)
+            break;
+        stage_put<OUT, kN>(stage, lane, g + h);
+        __syncwarp();
+        stage_flush<ES>(stage, lane, WarpBlock<ES>(p.D, p.ldd, row0, col + h, lane), nrow, ncol - h);
+        __syncwarp();
+    }
+}
+
+// The same with features on the lanes: lanes 0 .. 15 have g of 16 features, the others their u, of
+// kCols tokens from `col` on.  Each half finishes half of the tokens with what the other sends.
+template <int OUT, int kCols>
+__device__ __forceinline__ void finish_gated_narrow(const LmArgs &p, const float (&v)[kCols], const LmUnit &w,
+                                                    int row, int col, int lane)
+{
+    constexpr int kHalf = kCols / 2;
+    const bool up = lane >= 16;
+    const bool in = row < p.rows;
+    const int ncol = w.col_end - col;
+    if (p.Z && in) {
+        uint16_t *zp = static_cast<uint16_t *>(p.Z) + static_cast<int64_t>(col) * p.ldz + row + (up ? p.rows : 0);
+#pragma unroll
+        for (int j = 0; j < kCols; ++j)
+            if (j < ncol)
+                zp[j * p.ldz] = round16(v[j], p.in_bf16);
+    }
+    float g[kHalf], u[kHalf];
+#pragma unroll
+    for (int j = 0; j < kHalf; ++j) {
+        const float got = __shfl_xor_sync(0xffffffffu, up ? v[j] : v[j + kHalf], 16);
+        g[j] = up ? got : v[j];
+        u[j] = up ? v[j + kHalf] : got;
+    }
+    apply_act(p.act, g);
+    const int from = up ? kHalf : 0;
+    const int64_t dbase = static_cast<int64_t>(col + from) * p.ldd + row;
+    if (in) {
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j)
+            if (j + from < ncol)
+                store_as<OUT>(p.D, dbase + j * p.ldd, g[j] * u[j]);
+    }
+}
+
 // Wait for this thread's TMEM loads; v is not to be touched before.
 template <int N>
 __device__ __forceinline__ void tmem_ld_done(uint32_t (&v)[N])
@@ -589,14 +665,14 @@ __device__ __forceinline__ void tmem_ld_done(uint32_t (&v)[N])
 // ---------------------------------------------------------------------------- the kernel
 __host__ __device__ constexpr bool lm_wide(int epi)
 {
-    return epi == kEpiWide || epi == kEpiXentStats || epi == kEpiXentGrad;
+    return epi == kEpiWide || epi == kEpiXentStats || epi == kEpiXentGrad || epi == kEpiGatedWide;
 }
 
 template <int EPI, int OUT, int BN, bool RK>
 __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
     tcg_lm_kernel(const __grid_constant__ LmMaps maps, const LmArgs p)
 {
-    constexpr bool WIDE = lm_wide(EPI);
+    constexpr bool WIDE = lm_wide(EPI), GATED = lm_gated(EPI);
     using Cfg = LmCfg<BN, WIDE>;
     constexpr int kStages = Cfg::kStages;
     constexpr int kAccBufs = Cfg::kAccBufs;
@@ -609,7 +685,7 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
     // The gradient of the logits is among them: it takes a certain row's exp(logit - lse) from
     // one, so its logits have to be those of the statistics (in one piece, K = 4096 and a logit
     // of 40 left -6e-4 where nothing should be).
-    constexpr bool SEG = EPI != kEpiWide && !(EPI == kEpiNarrow && BN == 256);
+    constexpr bool SEG = EPI != kEpiWide && EPI != kEpiGatedWide && !(EPI == kEpiNarrow && BN == 256);
     // Narrow tiles of 256 tokens: a group's last tile is multiplied at the width it has, in
     // steps of 32 tokens (tensor time follows N), so that a group of any size wastes 16
     // tokens of work on average.
@@ -618,7 +694,9 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
         return FIT ? min(BN, (w.col_end - w.col0 + 31) & ~31) : BN;
     };
     constexpr int kSegBlocks = SEG ? 8 : 1 << 30;
-    using Walk = LmWalk<WIDE, BN, RK>;
+    using Walk = LmWalk<WIDE, BN, RK, GATED>;
+    // Features on the accumulator's rows: how many of them are this CTA's.
+    constexpr int kRowFeats = GATED && !WIDE ? kBM / 2 : kBM;
 
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_u32 = smem_u32(smem_raw);
@@ -699,9 +777,9 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
             if (!p.offsets)
                 griddep_wait();
             for (; ok && more; more = walk.next(p, ctl, w)) {
-                const int m0 = w.row0 + static_cast<int>(rank) * kBM;
-                const int n0 = w.col0 + static_cast<int>(rank) * (width(w) / 2);
-                const int za = WIDE ? 0 : w.g, zb = WIDE && !RK ? w.g : 0;
+                const int m0 = w.row0 + static_cast<int>(rank) * kRowFeats;
+                const int n0 = w.col0 + (GATED && WIDE ? 0 : static_cast<int>(rank) * (width(w) / 2));
+                const int za = WIDE ? 0 : w.g, zb = GATED ? (WIDE ? static_cast<int>(rank) : 0) : WIDE && !RK ? w.g : 0;
                 // maps that end with the group; without tokens there are none
                 if (RK && w.kb0 < w.kb1 && w.g != maps_of) {
                     maps_of = w.g;
@@ -740,7 +818,13 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                                     tma_load_3d_pair(dst + h * kChunkBytes, map, fb, row0 + h * 64,
                                                      k0, z);
                         };
-                        load(sa, map_a, p.a_mode, kBM, m0, za);
+                        if constexpr (GATED && !WIDE) {    // 16 rows of g and of u at a time
+#pragma unroll
+                            for (int b = 0; b < kBM / 32; ++b)
+                                tma_load_3d_pair(sa + b * (32 * kRowBytes), map_a, fb, k0, m0 + 16 * b, 0);
+                        } else {
+                            load(sa, map_a, p.a_mode, kBM, m0, za);
+                        }
                         load(sb, map_b, p.b_mode, kBRows, n0, zb);
                     }
                     if (++stage == kStages) {
@@ -881,8 +965,9 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
         auto piece_slot = [&](int i) { return 2 * (w.first_pair + i) + (i == 0 ? 1 : 0); };
 
         while (walk.next(p, ctl, w)) {
-            const int row = w.row0 + static_cast<int>(rank) * kBM + rl;
-            const int col_part = w.col0 + part * kPart;
+            const int row = w.row0 + static_cast<int>(rank) * kRowFeats +
+                            (kRowFeats == kBM ? rl : q * 16 + (lane & 15));
+            const int col_part = w.col0 + part * (GATED && WIDE ? kPart / 2 : kPart);
             const bool cut = w.slot >= 0;
             const bool empty_k = w.kb0 >= w.kb1;
             const int segments = SEG ? (w.kb1 - w.kb0 + kSegBlocks - 1) / kSegBlocks : 1;
@@ -920,7 +1005,7 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                         release();
                     finish_narrow<OUT, 32>(p, z, w, row, w.col0 + c * 32, alpha, bias);
                 }
-            } else if constexpr (EPI == kEpiNarrow || EPI == kEpiXentNarrow) {
+            } else if constexpr (EPI == kEpiNarrow || EPI == kEpiXentNarrow || EPI == kEpiGatedNarrow) {
                 // ------------------------------------------------ tokens on the columns
                 constexpr int kCols = kPart < 32 ? kPart : 32;
                 float sum[kPart];
@@ -994,6 +1079,11 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                     for (int c = 0; c < kPart; c += kCols)
                         finish_narrow<OUT>(p, *reinterpret_cast<float (*)[kCols]>(sum + c), w, row,
                                            col_part + c, alpha, bias);
+                } else if constexpr (EPI == kEpiGatedNarrow) {
+#pragma unroll
+                    for (int c = 0; c < kPart; c += kCols)
+                        finish_gated_narrow<OUT>(p, *reinterpret_cast<float (*)[kCols]>(sum + c), w, row,
+                                                 col_part + c, lane);
                 } else {
                     // a warp's 32 vocabulary entries, one token (column) after the other
                     const int slot = (w.row0 >> 8) * 8 + static_cast<int>(rank) * 4 + q;
@@ -1078,6 +1168,70 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                         scale_bias(p, alpha, static_cast<int64_t>(w.g) * p.cols + col, w.col_end - col, stage,
                                    lane, v, z);
                         finish_wide<OUT>(p, z, w, row - lane, col, stage, lane);
+                    }
+                }
+            } else if constexpr (EPI == kEpiGatedWide) {
+                // ------------------------- gated, tokens on the rows: columns c of the part's
+                // g and u are kPart columns of the accumulator apart
+                constexpr int kFeats = kPart / 2, kChunks = kFeats / 32;
+                if (!acquire())
+                    break;
+                const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                       static_cast<uint32_t>(it % kAccBufs * BN + part * kFeats);
+                float *sl = cut ? slot_ptr(w.slot) + rl : nullptr;       // [g, then u][column][row]
+                uint32_t vg[32], vu[32];
+                __syncwarp();
+                tmem_ld_32x32b_x32(taddr, vg);
+                tmem_ld_32x32b_x32(taddr + BN / 2, vu);
+#pragma unroll 1
+                for (int c = 0; c < kChunks; ++c) {
+                    const int col = col_part + c * 32;
+                    const bool inside = row - lane < w.row_end && col < w.col_end;
+                    float g[32], u[32];
+                    tmem_ld_done(vg);
+                    tmem_ld_done(vu);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        g[j] = empty_k ? 0.0f : __uint_as_float(vg[j]);
+                        u[j] = empty_k ? 0.0f : __uint_as_float(vu[j]);
+                    }
+                    if (cut) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            __stcg(sl + (c * 32 + j) * kBM, g[j]);
+                            __stcg(sl + (kFeats + c * 32 + j) * kBM, u[j]);
+                        }
+                    }
+                    __syncwarp();
+                    if (c + 1 < kChunks) {             // on its way while this chunk is finished
+                        tmem_ld_32x32b_x32(taddr + 32 * (c + 1), vg);
+                        tmem_ld_32x32b_x32(taddr + BN / 2 + 32 * (c + 1), vu);
+                    } else {
+                        release();
+                    }
+                    if (!cut && inside)
+                        finish_gated_wide<OUT>(p, g, u, w, row - lane, col, stage, lane);
+                }
+                if (cut && arrive() && row - lane < w.row_end) {
+#pragma unroll 1
+                    for (int c = 0; c < kChunks; ++c) {
+                        const int col = col_part + c * 32;
+                        if (col >= w.col_end)
+                            break;
+                        float g[32], u[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            g[j] = u[j] = 0.0f;
+#pragma unroll 1
+                        for (int i = 0; i < w.pieces; ++i) {
+                            const float *s = slot_ptr(piece_slot(i)) + c * 32 * kBM + rl;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                g[j] += __ldcg(s + j * kBM);
+                                u[j] += __ldcg(s + (kFeats + j) * kBM);
+                            }
+                        }
+                        finish_gated_wide<OUT>(p, g, u, w, row - lane, col, stage, lane);
                     }
                 }
             } else {
@@ -1238,6 +1392,17 @@ LmKernelFn linear_fn(int epi, int bn, bool rk)
                      : tcg_lm_kernel<kEpiWide, OUT, 256, false>;
 }
 
+template <int OUT>
+LmKernelFn gated_fn(int epi, int bn)
+{
+    if (epi == kEpiGatedNarrow)
+        return bn == 32 ? tcg_lm_kernel<kEpiGatedNarrow, OUT, 32, false>
+             : bn == 64 ? tcg_lm_kernel<kEpiGatedNarrow, OUT, 64, false>
+                        : tcg_lm_kernel<kEpiGatedNarrow, OUT, 128, false>;
+    return bn == 128 ? tcg_lm_kernel<kEpiGatedWide, OUT, 128, false>
+                     : tcg_lm_kernel<kEpiGatedWide, OUT, 256, false>;
+}
+
 LmKernelFn lm_fn(int epi, int out_kind, int bn, bool rk)
 {
     if (epi == kEpiXentStats)
@@ -1246,6 +1411,9 @@ LmKernelFn lm_fn(int epi, int out_kind, int bn, bool rk)
         return tcg_lm_kernel<kEpiXentNarrow, kOutF32, 32, false>;
     if (epi == kEpiXentGrad)
         return tcg_lm_kernel<kEpiXentGrad, kOutF16, 256, false>;
+    if (lm_gated(epi))
+        return out_kind == kOutF32 ? gated_fn<kOutF32>(epi, bn)
+             : out_kind == kOutF16 ? gated_fn<kOutF16>(epi, bn) : gated_fn<kOutBF16>(epi, bn);
     return out_kind == kOutF32 ? linear_fn<kOutF32>(epi, bn, rk)
          : out_kind == kOutF16 ? linear_fn<kOutF16>(epi, bn, rk) : linear_fn<kOutBF16>(epi, bn, rk);
 }
@@ -1517,6 +1685,61 @@ __global__ void __launch_bounds__(256)
     clear(at, c1);
 }
 
+// dZ = [dD u act'(g) | dD act(g)], a row of Z = [g | u] a token, n features each.  Bound by memory:
+// 8 features of a token a thread, dD, g and u read once and dZ written once, 16 bytes at a time.
+// Where n is no multiple of 8 the second halves of the rows are not aligned and go by elements.
+template <int ACT, bool BF16>
+__global__ void __launch_bounds__(256)
+    tcg_gate_backward_kernel(int64_t tokens, int64_t n, const uint16_t *__restrict__ dD, int64_t lddd,
+                             const uint16_t *__restrict__ Z, int64_t ldz, uint16_t *__restrict__ dZ,
+                             int64_t lddz)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const int64_t per = (n + 7) / 8, total = tokens * per;
+    const bool even = n % 8 == 0;
+    auto load8 = [&](const uint16_t *src, int left, bool vec) {
+        if (left >= 8 && vec)
+            return *reinterpret_cast<const uint4 *>(src);
+        uint32_t v[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left)
+                v[i / 2] |= static_cast<uint32_t>(src[i]) << (16 * (i & 1));
+        return make_uint4(v[0], v[1], v[2], v[3]);
+    };
+    auto store8 = [&](uint16_t *dst, int left, bool vec, const float (&v)[8]) {
+        if (left >= 8 && vec) {
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(pack16(v[0], v[1], BF16), pack16(v[2], v[3], BF16),
+                                                         pack16(v[4], v[5], BF16), pack16(v[6], v[7], BF16));
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left)
+                dst[i] = round16(v[i], BF16);
+    };
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+        const int64_t t = i / per, c = (i - t * per) * 8;
+        const int left = n - c < 8 ? static_cast<int>(n - c) : 8;
+        float d[8], g[8], u[8];
+        const uint4 rd = load8(dD + t * lddd + c, left, true);
+        const uint4 rg = load8(Z + t * ldz + c, left, true);
+        const uint4 ru = load8(Z + t * ldz + n + c, left, even);
+        unpack16<BF16>(rd, d);
+        unpack16<BF16>(rg, g);
+        unpack16<BF16>(ru, u);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const F2 dd = f2(d[j], d[j + 1]), gg = f2(g[j], g[j + 1]);
+            split2(dd * f2(u[j], u[j + 1]) * act_slope<ACT>(gg), u[j], u[j + 1]);
+            split2(dd * act_fn<ACT>(gg), g[j], g[j + 1]);
+        }
+        store8(dZ + t * lddz + c, left, true, u);
+        store8(dZ + t * lddz + n + c, left, even, g);
+    }
+}
+
 // dbias of group blockIdx.y: its segments in column order, the four warps of 64 rows taking
 // a quarter of them each.
 __global__ void __launch_bounds__(256)
@@ -1627,6 +1850,27 @@ cudaError_t launch_round_out(const float *in, int64_t ldi, int rows, int cols, c
                                            : tcg_round_out_kernel<kOutF16>,
                       dim3(grid), dim3(256), s, 0, in, ldi, rows, cols, scale,
                       static_cast<uint16_t *>(out), ldo);
+}
+
+template <int ACT>
+static cudaError_t gate_backward(int bf16, int grid, cudaStream_t s, int64_t tokens, int64_t n, const void *dD,
+                                 int64_t lddd, const void *Z, int64_t ldz, void *dZ, int64_t lddz)
+{
+    return launch_pdl(bf16 ? tcg_gate_backward_kernel<ACT, true> : tcg_gate_backward_kernel<ACT, false>, dim3(grid),
+                      dim3(256), s, 0, tokens, n, static_cast<const uint16_t *>(dD), lddd,
+                      static_cast<const uint16_t *>(Z), ldz, static_cast<uint16_t *>(dZ), lddz);
+}
+
+cudaError_t launch_gate_backward(int act, int bf16, int tokens, int64_t n, const void *dD, int64_t lddd,
+                                 const void *Z, int64_t ldz, void *dZ, int64_t lddz, int num_sms,
+                                 cudaStream_t s)
+{
+    const int64_t blocks = (tokens * ((n + 7) / 8) + 255) / 256, most = static_cast<int64_t>(num_sms) * 16;
+    auto fn = act == kActRelu ? gate_backward<kActRelu>
+            : act == kActGelu ? gate_backward<kActGelu>
+            : act == kActGeluTanh ? gate_backward<kActGeluTanh>
+            : act == kActSilu ? gate_backward<kActSilu> : gate_backward<kActNone>;
+    return fn(bf16, static_cast<int>(blocks < most ? blocks : most), s, tokens, n, dD, lddd, Z, ldz, dZ, lddz);
 }
 
 template <int ACT>

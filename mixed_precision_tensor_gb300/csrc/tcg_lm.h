@@ -28,8 +28,15 @@ enum LmEpi {
     kEpiWide = 1,       // the same; tokens x features
     kEpiXentStats = 2,  // per-row maximum and sum of exponentials, and the target's logit
     kEpiXentNarrow = 3, // the same; vocabulary x tokens
-    kEpiXentGrad = 4    // (exp(logit - lse) - [target]) * upstream gradient, 16-bit
+    kEpiXentGrad = 4,   // (exp(logit - lse) - [target]) * upstream gradient, 16-bit
+    kEpiGatedNarrow = 5, // act(g) u of two products of the same tokens; features x tokens
+    kEpiGatedWide = 6   // the same; tokens x features
 };
+
+// A gated product's tile holds both halves of its features: in the wide kind BN / 2 columns of
+// g, then those of u (each CTA of the pair loads the rows of one half); in the narrow kind 16
+// rows of g, then the 16 of u, four times a CTA (a warp of the epilogue has both).
+__host__ __device__ constexpr bool lm_gated(int epi) { return epi == kEpiGatedNarrow || epi == kEpiGatedWide; }
 
 enum LmAct { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
 
@@ -129,7 +136,8 @@ cudaError_t launch_group_maps(const LmMaps &maps, const int64_t *offsets, int gr
                               CUtensorMap *out, cudaStream_t s);
 
 // Launchers (tcg_lm.cu).  out_kind: type of D.  bn: 32, 64, 128 or 256 (kEpiNarrow), 64, 128 or 256
-// (kEpiWide), 256 (K ragged, kEpiXentStats, kEpiXentGrad), 32 (kEpiXentNarrow).
+// (kEpiWide), 32, 64 or 128 (kEpiGatedNarrow), 128 or 256 (kEpiGatedWide), 256 (K ragged,
+// kEpiXentStats, kEpiXentGrad), 32 (kEpiXentNarrow).
 cudaError_t launch_lm(const LmMaps &maps, const LmArgs &a, int epi, int out_kind, int bn,
                       int grid, cudaStream_t s);
 int lm_max_resident_ctas(int num_sms);
@@ -156,6 +164,7 @@ struct LmFewArgs {
     void *Z;
     int64_t ldz;
     int act;
+    int gated;                 // W: feats rows of g, then those of u; Z likewise
     const int64_t *targets;    // cross entropy
     int64_t ignore;
     float2 *stats;             // [block][token], one block per SM; nullptr: linear
@@ -180,6 +189,75 @@ cudaError_t launch_xent_scale(const float *dloss, const int64_t *targets, int ro
 // out[j][i] = scale * in[j][i], rounded to the 16-bit type.
 cudaError_t launch_round_out(const float *in, int64_t ldi, int rows, int cols, const float *scale,
                              void *out, int64_t ldo, int out_kind, int grid, cudaStream_t s);
+// dZ = [dD u act'(g) | dD act(g)] of rows Z = [g | u], n features each.
+cudaError_t launch_gate_backward(int act, int bf16, int tokens, int64_t n, const void *dD, int64_t lddd,
+                                 const void *Z, int64_t ldz, void *dZ, int64_t lddz, int num_sms,
+                                 cudaStream_t s);
+
+// Root-mean-square norm (tcg_lm_norm.cu), row-major.
+constexpr int64_t kNormMaxK = 32768;   // a row stays in the registers of a block
+struct NormArgs {
+    int64_t rows;
+    int k;
+    const void *X;
+    int64_t ldx;
+    const void *R;             // residual; nullptr: none
+    int64_t ldr;
+    void *S;                   // X + R, rounded; nullptr: not kept
+    int64_t lds;
+    const void *W;
+    int w_f32, in_bf16, out8;
+    float eps;
+    void *Y;                   // 16-bit, or (out8) E4M3 with `scale`
+    int64_t ldy;
+    float *scale;
+};
+cudaError_t launch_norm(const NormArgs &a, int num_sms, cudaStream_t s);
+struct NormBackwardArgs {
+    int64_t rows;
+    int k;
+    const void *dY;
+    int64_t lddy;
+    const void *X;
+    int64_t ldx;
+    const void *dS;            // added to dX; nullptr: none
+    int64_t ldds;
+    const void *W;
+    int w_f32, in_bf16;
+    float eps;
+    void *dX;                  // nullptr: not wanted
+    int64_t lddx;
+    float *part;               // norm_backward_blocks x k; nullptr: dW is not wanted
+};
+int norm_backward_blocks(int64_t rows, int64_t k, int num_sms);
+cudaError_t launch_norm_backward(NormBackwardArgs a, float *dw, int num_sms, cudaStream_t s);
+
+// Products with 4-bit weights (tcg_lm_w4.cu), row-major: element 2 j of a row in the low half of
+// byte j; w = (q - zero) scale per group of `group` elements of a row.
+struct W4Args {
+    int64_t rows;              // of W: the features, or twice those of a gated product
+    int64_t k;
+    int tokens, group;
+    const uint8_t *W;
+    int64_t ldw;               // bytes
+    const void *scales, *zeros;   // rows x ceil(k / group); zeros nullptr: 8
+    int s_f32;                 // their type: FP32, or that of X
+    const void *X;
+    int64_t ldx;
+    int in_bf16, out_kind;
+    void *D;
+    int64_t ldd;
+    const void *bias;
+    int bias_f32;
+    const void *C;
+    int64_t ldc;
+    float beta;
+    int act, gated;
+};
+cudaError_t launch_w4(const W4Args &a, int num_sms, cudaStream_t s);
+// The weights as the type of X, rounded once: rows x k, ldo elements apart.
+cudaError_t launch_w4_expand(const W4Args &a, void *out, int64_t ldo, int num_sms, cudaStream_t s);
+
 // dZ = dD * act'(Z) and per-group sums of its rows; see tcg_epi_backward_kernel.  part:
 // (ceil(cols / chunk) + groups) * m floats.
 cudaError_t launch_epi_backward(int act, int bf16, int m, int cols, int groups,

@@ -1,6 +1,7 @@
 // tcg_lm_api.cu -- host runtime and C ABI of the language-model products (declared in
-// include/tcg.h): products with a bias, activation and residual in their epilogue,
-// products grouped by expert, and the cross entropy of a linear head.
+// include/tcg.h): products with a bias, activation and residual in their epilogue, gated
+// products, products grouped by expert, products with 4-bit weights, the cross entropy of a
+// linear head, and the norm between them.
 //
 // Every call checks its arguments on the host, binds the handle, checks that its pointers
 // are device memory, and queues kernels of tcg_lm.cu on the handle's stream.
@@ -56,6 +57,8 @@ struct Product {
     int64_t ldd = 0, strideD = 0;
     tcgEpilogue_t epi = {};
     int lm_epi = -1;                        // kEpiXent*, or chosen by shape_of
+    bool gated = false;                     // W holds feats rows of g, then those of u
+    int64_t w_rows() const { return gated ? 2 * feats : feats; }
 };
 
 // How a product runs: epilogue kind, tile width, whether tiles may be cut along K, pairs.
@@ -67,17 +70,19 @@ struct Shape {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+bool is_narrow(int epi) { return epi == kEpiNarrow || epi == kEpiXentNarrow || epi == kEpiGatedNarrow; }
+
 // The most tiles a call can have.
 int64_t max_tiles(const Product &p, int epi, int bn)
 {
-    const bool narrow = epi == kEpiNarrow || epi == kEpiXentNarrow;
+    const bool narrow = is_narrow(epi);
     if (p.ragged_k)
         return p.groups * ceil_div(p.rows, 256) * ceil_div(p.feats, bn);
     const int side = narrow ? bn : 256;
     int64_t along = ceil_div(p.tokens, side);
     if (p.offsets)                          // one more for each range that is not empty
         along = p.tokens / side + (p.groups + 2 < p.tokens ? p.groups + 2 : p.tokens);
-    return along * ceil_div(p.feats, narrow ? 256 : bn);
+    return along * ceil_div(p.feats, (narrow ? 256 : bn) / (p.gated ? 2 : 1));
 }
 
 // Saving in K blocks that pays for joining partial sums of a 256 x bn tile.
@@ -125,10 +130,13 @@ Shape shape_of(tcgContext *h, const Product &p)
         // tiles that four pairs share one (4 experts of 1024 x 4096, 50 rows each: 16 us so, 23 us
         // by the rule below; 2 of 4096 x 4096, 120 rows, two pairs to a tile: 25 to 31 and 25 to 26).
         const bool scarce = 4 * p.groups * ceil_div(p.feats, 256) <= P;
+        // A gated tile holds both halves of its features; its wide kind starts at 128 columns.
+        const int64_t wn = p.w_rows();
+        const int least = p.gated || !p.w_kmajor ? 128 : 64;
         if (p.x_kmajor && per <= (p.offsets && !scarce ? 16 : 128) &&
-            (p.offsets || !p.w_kmajor || load_kib(ceil_div(p.feats, 256), nkb, narrow_bn, P) <=
-                                             load_kib(ceil_div(p.feats, 64), nkb, 64, P))) {
-            s.epi = kEpiNarrow;
+            (p.offsets || !p.w_kmajor || load_kib(ceil_div(wn, 256), nkb, narrow_bn, P) <=
+                                             load_kib(ceil_div(wn, least), nkb, least, P))) {
+            s.epi = p.gated ? kEpiGatedNarrow : kEpiNarrow;
             s.bn = narrow_bn;
         } else if (p.offsets && p.x_kmajor && per < 1024) {
             // Groups' last tiles at the width that they have.  Narrower tiles read a group's
@@ -148,10 +156,10 @@ Shape shape_of(tcgContext *h, const Product &p)
             // Tokens on the rows: the tile width with the least predicted time, in the time of
             // a K block at width 256.  A block costs the 16 KiB of A and bn / 16 KiB of B that an
             // SM loads for it, at 64 bytes a cycle: 512, 384 or 320 cycles.
-            s.epi = kEpiWide;
+            s.epi = p.gated ? kEpiGatedWide : kEpiWide;
             s.bn = 256;
             double best = 1e300;
-            for (int bn = 256; bn >= (p.w_kmajor ? 64 : 128); bn /= 2) {
+            for (int bn = 256; bn >= least; bn /= 2) {
                 const double cost = bn == 256 ? 1.0 : (bn == 128 ? 0.75 : 0.625);
                 const int64_t tiles = max_tiles(p, s.epi, bn), rest = tiles % P;
                 int64_t share = ceil_div(rest * nkb, P);
@@ -171,14 +179,15 @@ Shape shape_of(tcgContext *h, const Product &p)
     s.tiles = max_tiles(p, s.epi, s.bn);
     s.share = min_share(nkb, s.bn);
     s.gain = gain_of(s.bn);
-    const bool linear = s.epi == kEpiNarrow || s.epi == kEpiWide || s.epi == kEpiXentNarrow;
+    const bool wide = s.epi == kEpiWide || s.epi == kEpiGatedWide;
+    const bool linear = is_narrow(s.epi) || wide;
     s.cut = linear && !p.ragged_k && !(s.epi == kEpiNarrow && s.bn == 256) && nkb - s.share >= s.gain &&
             (p.offsets || s.tiles % P != 0) && h->split_k != 1;
     // Tiles share operands along both sides, and the operands exceed half of L2 (129 MB): K
     // ranges alike for all cut tiles (1000 x 1024 outputs over K = 50021: 109 -> 84 us).
-    const int64_t x_tiles = ceil_div(p.tokens, s.epi == kEpiWide ? 256 : s.bn);
-    const int64_t w_tiles = ceil_div(p.feats, s.epi == kEpiWide ? s.bn : 256);
-    s.align = !p.offsets && x_tiles > 1 && w_tiles > 1 && (p.tokens + p.feats) * p.k * 2 > (int64_t(64) << 20);
+    const int64_t x_tiles = ceil_div(p.tokens, wide ? 256 : s.bn);
+    const int64_t w_tiles = ceil_div(p.w_rows(), wide ? s.bn : 256);
+    s.align = !p.offsets && x_tiles > 1 && w_tiles > 1 && (p.tokens + p.w_rows()) * p.k * 2 > (int64_t(64) << 20);
     int64_t pairs = s.tiles;
     if (s.cut)
         pairs = s.tiles * nkb / s.share > pairs ? s.tiles * nkb / s.share : pairs;
@@ -207,7 +216,7 @@ tcgStatus_t queue(tcgContext *h, const Product &p, void *ws, LmArgs a = LmArgs{}
     const Shape s = shape_of(h, p);
     if (s.tiles > INT32_MAX)
         return TCG_STATUS_NOT_SUPPORTED;
-    const bool narrow = s.epi == kEpiNarrow || s.epi == kEpiXentNarrow;
+    const bool narrow = is_narrow(s.epi);
     // accumulator rows and columns
     const int64_t x_ext = p.ragged_k ? p.rows : p.tokens;
     a.rows = static_cast<int>(narrow ? p.feats : x_ext);
@@ -216,8 +225,9 @@ tcgStatus_t queue(tcgContext *h, const Product &p, void *ws, LmArgs a = LmArgs{}
     a.ragged_k = p.ragged_k;
     a.groups = static_cast<int>(p.groups);
     a.offsets = p.offsets;
-    a.num_row_tiles = (a.rows + 255) / 256;
-    a.num_col_tiles = (a.cols + s.bn - 1) / s.bn;
+    const int half = p.gated ? 2 : 1;       // of a tile's features: see lm_gated
+    a.num_row_tiles = static_cast<int>(ceil_div(a.rows, narrow ? 256 / half : 256));
+    a.num_col_tiles = static_cast<int>(ceil_div(a.cols, narrow ? s.bn : s.bn / half));
     a.num_k_blocks = static_cast<int>(ceil_div(p.k, 64));
     a.min_share = s.share;
     a.split_gain = s.gain;
@@ -259,9 +269,17 @@ tcgStatus_t queue(tcgContext *h, const Product &p, void *ws, LmArgs a = LmArgs{}
                          64, &bc, narrow ? &a.b_mode : &a.a_mode, narrow ? &maps.B : &maps.A);
         if (st != TCG_STATUS_SUCCESS)
             return st;
-        st = operand_map(h, p.W, p.in, p.w_kmajor, p.feats, kx, p.ldw, p.strideW,
-                         p.ragged_k || !p.offsets ? 1 : p.groups, narrow ? kBM : s.bn / 2, 64, &bc,
-                         narrow ? &a.a_mode : &a.b_mode, narrow ? &maps.A : &maps.B);
+        if (p.gated && narrow) {            // {k, feature, g or u}: 16 features of each a box
+            const uint64_t dims[3] = {static_cast<uint64_t>(kx), static_cast<uint64_t>(p.feats), 2};
+            const uint64_t str[2] = {static_cast<uint64_t>(p.ldw) * 2, static_cast<uint64_t>(p.feats * p.ldw) * 2};
+            const uint32_t box[3] = {64, 16, 2};
+            a.a_mode = kK;
+            st = get_map(h, p.W, p.in, 3, dims, str, box, &maps.A);
+        } else {
+            st = operand_map(h, p.W, p.in, p.w_kmajor, p.feats, kx, p.ldw, p.gated ? p.feats * p.ldw : p.strideW,
+                             p.gated ? 2 : (p.ragged_k || !p.offsets ? 1 : p.groups), narrow ? kBM : s.bn / 2, 64,
+                             &bc, narrow ? &a.a_mode : &a.b_mode, narrow ? &maps.A : &maps.B);
+        }
         if (st != TCG_STATUS_SUCCESS)
             return st;
     }
@@ -301,7 +319,7 @@ bool few(const Product &p)
     if (p.ragged_k || !p.x_kmajor || !p.w_kmajor || p.k == 0 || p.lm_epi >= 0 || p.alpha_dev)
         return false;
     if (!p.offsets)
-        return few_tokens(p.tokens, p.feats, p.k);
+        return few_tokens(p.tokens, p.w_rows(), p.k);
     // 64 experts of 2048 x 2048: 16 rows 26 us so, 31 us by tiles; 30 rows 40 and 41; 60 rows 60
     // and 60.
     return p.tokens <= kLmFewRows && (p.tokens <= 4 || 2 * p.tokens <= p.groups);
@@ -334,6 +352,7 @@ tcgStatus_t queue_few(tcgContext *h, const Product &p)
     a.Z = p.epi.Z;
     a.ldz = p.epi.ldz;
     a.act = p.epi.activation;
+    a.gated = p.gated;
     a.err = h->d_err;
     a.wait_limit_ns = h->wait_limit_ns;
     a.fault_inject = h->fault_inject;
@@ -690,6 +709,75 @@ LayerPlan layer_plan(tcgContext *h, bool act, int64_t m, int64_t n, int64_t k, i
                          ? product_ws(h, layer_dw(m, n, k, groups, offsets, TCG_R_16BF)) : 0;
     pl.total = pl.dz_bytes + pl.part_bytes + (x > w ? x : w);
     return pl;
+}
+
+// The product behind tcg_gemm_gated, without its pointers.
+Product gated_product(int64_t m, int64_t n, int64_t k, tcgDataType_t in, tcgDataType_t out)
+{
+    Product p;
+    p.feats = m;
+    p.tokens = n;
+    p.k = k;
+    p.gated = true;
+    p.in = in;
+    p.out = out;
+    return p;
+}
+
+tcgStatus_t check_gate(int act, int64_t m, int64_t n, int64_t k)
+{
+    if (act < TCG_ACT_NONE || act > TCG_ACT_SILU || m < 0 || n < 0 || k < 0)
+        return TCG_STATUS_INVALID_VALUE;
+    return 2 * m > kMaxExtent || n > kMaxExtent || k > kMaxK ? TCG_STATUS_NOT_SUPPORTED : TCG_STATUS_SUCCESS;
+}
+
+// The workspace of a gated backward pass: dZ, and what the products need.
+struct GatedPlan {
+    int64_t lddz;
+    size_t dz_bytes, total;
+};
+
+GatedPlan gated_plan(tcgContext *h, int64_t m, int64_t n, int64_t k, bool dx, bool dw)
+{
+    GatedPlan pl;
+    pl.lddz = (2 * m + 7) / 8 * 8;
+    pl.dz_bytes = m > 0 ? pad256(static_cast<size_t>(n) * pl.lddz * 2) : 0;
+    const size_t x = dx && n > 0 && k > 0 ? product_ws(h, layer_dx(2 * m, n, k, 1, nullptr, TCG_R_16BF)) : 0;
+    const size_t w = dw && m > 0 && k > 0 ? product_ws(h, layer_dw(2 * m, n, k, 1, nullptr, TCG_R_16BF)) : 0;
+    pl.total = pl.dz_bytes + (x > w ? x : w);
+    return pl;
+}
+
+// ---------------------------------------------------------------------------- norm
+tcgStatus_t check_norm(int64_t rows, int64_t k, const void *W, tcgDataType_t w_type, float eps, tcgDataType_t type)
+{
+    if (!valid_type(type) || !valid_type(w_type) || rows < 0 || k < 1 || !(eps >= 0.0f))
+        return TCG_STATUS_INVALID_VALUE;
+    if (!is_16bit(type) || (w_type != type && w_type != TCG_R_32F) || k > kNormMaxK)
+        return TCG_STATUS_NOT_SUPPORTED;
+    if (rows > 0 && (!W || !aligned16(W)))
+        return TCG_STATUS_INVALID_VALUE;
+    return TCG_STATUS_SUCCESS;
+}
+
+bool bad_rows(const void *p, int64_t ld, int64_t cols, int es) { return !aligned16(p) || bad_ld(ld, cols, es); }
+
+// --------------------------------------------------------------------- 4-bit weights
+// Most tokens of a pass over the packed weights; more take them as 16-bit operands.
+constexpr int kW4Tokens = 64;
+
+size_t w4_expand_bytes(int64_t rows, int64_t k) { return pad256(static_cast<size_t>(rows) * ((k + 7) / 8 * 8) * 2); }
+
+Product w4_product(const W4Args &a, tcgDataType_t in, tcgDataType_t out)
+{
+    Product p;
+    p.feats = a.gated ? a.rows / 2 : a.rows;
+    p.tokens = a.tokens;
+    p.k = a.k;
+    p.gated = a.gated;
+    p.in = in;
+    p.out = out;
+    return p;
 }
 
 }  // namespace
@@ -1155,6 +1243,388 @@ tcgStatus_t tcg_xent_backward(tcgHandle_t h, int64_t rows, int64_t vocab, int64_
         cudaGetLastError();
         return TCG_STATUS_EXECUTION_FAILED;
     }
+    return TCG_STATUS_SUCCESS;
+}
+
+tcgStatus_t tcg_gemm_gated(tcgHandle_t h, tcgActivation_t activation, int64_t m, int64_t n, int64_t k,
+                           const void *A, int64_t lda, const void *B, int64_t ldb, tcgDataType_t ABtype,
+                           void *D, tcgDataType_t Dtype, int64_t ldd, void *Z, int64_t ldz)
+{
+    if (!h)
+        return TCG_STATUS_INVALID_VALUE;
+    tcgStatus_t st = check_gate(activation, m, n, k);
+    if (st == TCG_STATUS_SUCCESS)
+        st = check_types(ABtype, Dtype);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    if (bad_ld(lda, k, 2) || bad_ld(ldb, k, 2) || bad_ld(ldd, m, elem_size(Dtype)) ||
+        (Z && (!aligned16(Z) || bad_ld(ldz, 2 * m, 2))))
+        return TCG_STATUS_INVALID_VALUE;
+    if (m == 0 || n == 0)
+        return TCG_STATUS_SUCCESS;
+    if (!D || !aligned16(D) || (k > 0 && (!A || !B || !aligned16(A) || !aligned16(B))))
+        return TCG_STATUS_INVALID_VALUE;
+    st = bind_device(h);
+    if (st == TCG_STATUS_SUCCESS)
+        st = check_device(h, {D, k > 0 ? A : nullptr, k > 0 ? B : nullptr, Z});
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    h->used = true;
+    Product p = gated_product(m, n, k, ABtype, Dtype);
+    p.W = A;
+    p.ldw = lda;
+    p.X = B;
+    p.ldx = ldb;
+    p.D = D;
+    p.ldd = ldd;
+    p.epi.activation = activation;
+    p.epi.Z = Z;
+    p.epi.ldz = ldz;
+    if (few(p))
+        return queue_few(h, p);
+    void *ws = nullptr;
+    const size_t need = product_ws(h, p);
+    if (need) {
+        st = acquire_ws(h, need, &ws);
+        if (st != TCG_STATUS_SUCCESS)
+            return st;
+    }
+    return queue(h, p, ws);
+}
+
+tcgStatus_t tcg_gemm_gated_workspace_size(tcgHandle_t h, int64_t m, int64_t n, int64_t k, size_t *bytes)
+{
+    if (!h || !bytes)
+        return TCG_STATUS_INVALID_VALUE;
+    tcgStatus_t st = check_gate(TCG_ACT_NONE, m, n, k);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    *bytes = 0;
+    if (m == 0 || n == 0)
+        return TCG_STATUS_SUCCESS;
+    st = bind_device(h);
+    if (st == TCG_STATUS_SUCCESS)
+        *bytes = product_ws(h, gated_product(m, n, k, TCG_R_16BF, TCG_R_16BF));
+    return st;
+}
+
+tcgStatus_t tcg_gated_backward(tcgHandle_t h, tcgActivation_t activation, int64_t m, int64_t n, int64_t k,
+                               const void *dD, int64_t lddd, const void *Z, int64_t ldz, const void *W,
+                               int64_t ldw, const void *X, int64_t ldx, tcgDataType_t type, void *dX,
+                               int64_t lddx, void *dW, int64_t lddw)
+{
+    if (!h)
+        return TCG_STATUS_INVALID_VALUE;
+    tcgStatus_t st = check_gate(activation, m, n, k);
+    if (st == TCG_STATUS_SUCCESS)
+        st = check_types(type, type);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    if (bad_rows(dD, lddd, m, 2) || bad_rows(Z, ldz, 2 * m, 2) ||
+        (dX && (bad_rows(W, ldw, k, 2) || bad_rows(dX, lddx, k, 2))) ||
+        (dW && (bad_rows(X, ldx, k, 2) || bad_rows(dW, lddw, k, 2))))
+        return TCG_STATUS_INVALID_VALUE;
+    const bool sums = m > 0 && n > 0;
+    if ((sums && (!dD || !Z)) || (sums && k > 0 && ((dX && !W) || (dW && !X))))
+        return TCG_STATUS_INVALID_VALUE;
+    const bool dx = dX && n > 0 && k > 0, dw = dW && m > 0 && k > 0;
+    if (!dx && !dw)
+        return TCG_STATUS_SUCCESS;
+    st = bind_device(h);
+    if (st == TCG_STATUS_SUCCESS)
+        st = check_device(h, {sums ? dD : nullptr, sums ? Z : nullptr, sums && dx ? W : nullptr,
+                              sums && dw ? X : nullptr, dx ? dX : nullptr, dw ? dW : nullptr});
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    h->used = true;
+    const GatedPlan pl = gated_plan(h, m, n, k, dx, dw);
+    void *ws = nullptr;
+    if (pl.total) {
+        st = acquire_ws(h, pl.total, &ws);
+        if (st != TCG_STATUS_SUCCESS)
+            return st;
+    }
+    void *tail = static_cast<uint8_t *>(ws) + pl.dz_bytes;
+    if (sums) {
+        const cudaError_t e = launch_gate_backward(activation, type == TCG_R_16BF, static_cast<int>(n), m, dD, lddd,
+                                                   Z, ldz, ws, pl.lddz, h->num_sms, h->stream);
+        h->launches += 1;
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return TCG_STATUS_EXECUTION_FAILED;
+        }
+    }
+    if (dx) {
+        Product p = layer_dx(2 * m, n, k, 1, nullptr, type);
+        p.X = ws;
+        p.ldx = pl.lddz;
+        p.W = W;
+        p.ldw = ldw;
+        p.D = dX;
+        p.ldd = lddx;
+        st = queue(h, p, tail);
+        if (st != TCG_STATUS_SUCCESS)
+            return st;
+    }
+    if (dw) {
+        Product p = layer_dw(2 * m, n, k, 1, nullptr, type);
+        p.X = ws;
+        p.ldx = pl.lddz;
+        p.W = X;
+        p.ldw = ldx;
+        p.D = dW;
+        p.ldd = lddw;
+        st = queue(h, p, tail);
+    }
+    return st;
+}
+
+tcgStatus_t tcg_gated_backward_workspace_size(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int with_dX,
+                                              int with_dW, size_t *bytes)
+{
+    if (!h || !bytes)
+        return TCG_STATUS_INVALID_VALUE;
+    tcgStatus_t st = check_gate(TCG_ACT_NONE, m, n, k);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    st = bind_device(h);
+    if (st == TCG_STATUS_SUCCESS)
+        *bytes = gated_plan(h, m, n, k, with_dX, with_dW).total;
+    return st;
+}
+
+tcgStatus_t tcg_rms_norm(tcgHandle_t h, int64_t rows, int64_t k, const void *X, int64_t ldx, const void *R,
+                         int64_t ldr, void *S, int64_t lds, const void *W, tcgDataType_t Wtype, float eps,
+                         tcgDataType_t type, void *Y, tcgDataType_t Ytype, int64_t ldy, float *scale)
+{
+    if (!h || !valid_type(Ytype))
+        return TCG_STATUS_INVALID_VALUE;
+    tcgStatus_t st = check_norm(rows, k, W, Wtype, eps, type);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    const bool out8 = Ytype == TCG_R_8F_E4M3;
+    if (!out8 && Ytype != type)
+        return TCG_STATUS_NOT_SUPPORTED;
+    if (bad_ld(ldx, k, 2) || (R && bad_rows(R, ldr, k, 2)) || (S && bad_rows(S, lds, k, 2)) ||
+        bad_ld(ldy, k, elem_size(Ytype)))
+        return TCG_STATUS_INVALID_VALUE;
+    if (rows == 0)
+        return TCG_STATUS_SUCCESS;
+    if (!X || !Y || !aligned16(X) || !aligned16(Y) ||
+        (out8 && (!scale || reinterpret_cast<uintptr_t>(scale) % 4)))
+        return TCG_STATUS_INVALID_VALUE;
+    st = bind_device(h);
+    if (st == TCG_STATUS_SUCCESS)
+        st = check_device(h, {X, R, S, W, Y, out8 ? scale : nullptr});
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    h->used = true;
+    NormArgs a{};
+    a.rows = rows;
+    a.k = static_cast<int>(k);
+    a.X = X;
+    a.ldx = ldx;
+    a.R = R;
+    a.ldr = ldr;
+    a.S = S;
+    a.lds = lds;
+    a.W = W;
+    a.w_f32 = Wtype == TCG_R_32F;
+    a.in_bf16 = type == TCG_R_16BF;
+    a.out8 = out8;
+    a.eps = eps;
+    a.Y = Y;
+    a.ldy = ldy;
+    a.scale = scale;
+    const cudaError_t e = launch_norm(a, h->num_sms, h->stream);
+    h->launches += 1;
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return TCG_STATUS_EXECUTION_FAILED;
+    }
+    return TCG_STATUS_SUCCESS;
+}
+
+tcgStatus_t tcg_rms_norm_backward(tcgHandle_t h, int64_t rows, int64_t k, const void *dY, int64_t lddy,
+                                  const void *X, int64_t ldx, const void *dS, int64_t ldds, const void *W,
+                                  tcgDataType_t Wtype, float eps, tcgDataType_t type, void *dX, int64_t lddx,
+                                  float *dW)
+{
+    if (!h)
+        return TCG_STATUS_INVALID_VALUE;
+    tcgStatus_t st = check_norm(rows, k, W, Wtype, eps, type);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    if (bad_ld(lddy, k, 2) || bad_ld(ldx, k, 2) || (dS && bad_rows(dS, ldds, k, 2)) ||
+        (dX && bad_rows(dX, lddx, k, 2)) || reinterpret_cast<uintptr_t>(dW) % 4)
+        return TCG_STATUS_INVALID_VALUE;
+    if (rows > 0 && (!dY || !X || !aligned16(dY) || !aligned16(X)))
+        return TCG_STATUS_INVALID_VALUE;
+    if (!dW && (!dX || rows == 0))
+        return TCG_STATUS_SUCCESS;
+    st = bind_device(h);
+    if (st == TCG_STATUS_SUCCESS)
+        st = rows > 0 ? check_device(h, {dY, X, dS, W, dX, dW}) : check_device(h, {dW});
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    h->used = true;
+    NormBackwardArgs a{};
+    a.rows = rows;
+    a.k = static_cast<int>(k);
+    a.dY = dY;
+    a.lddy = lddy;
+    a.X = X;
+    a.ldx = ldx;
+    a.dS = dS;
+    a.ldds = ldds;
+    a.W = W;
+    a.w_f32 = Wtype == TCG_R_32F;
+    a.in_bf16 = type == TCG_R_16BF;
+    a.eps = eps;
+    a.dX = dX;
+    a.lddx = lddx;
+    const int blocks = norm_backward_blocks(rows, k, h->num_sms);
+    if (dW && blocks > 1) {
+        void *ws = nullptr;
+        st = acquire_ws(h, static_cast<size_t>(blocks) * k * sizeof(float), &ws);
+        if (st != TCG_STATUS_SUCCESS)
+            return st;
+        a.part = static_cast<float *>(ws);
+    }
+    const cudaError_t e = launch_norm_backward(a, dW, h->num_sms, h->stream);
+    h->launches += (rows > 0) + (dW && blocks != 1);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return TCG_STATUS_EXECUTION_FAILED;
+    }
+    return TCG_STATUS_SUCCESS;
+}
+
+tcgStatus_t tcg_rms_norm_backward_workspace_size(tcgHandle_t h, int64_t rows, int64_t k, size_t *bytes)
+{
+    if (!h || !bytes || rows < 0 || k < 1)
+        return TCG_STATUS_INVALID_VALUE;
+    if (k > kNormMaxK)
+        return TCG_STATUS_NOT_SUPPORTED;
+    const tcgStatus_t st = bind_device(h);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    const int blocks = norm_backward_blocks(rows, k, h->num_sms);
+    *bytes = blocks > 1 ? static_cast<size_t>(blocks) * k * sizeof(float) : 0;
+    return TCG_STATUS_SUCCESS;
+}
+
+tcgStatus_t tcg_gemm_4bit(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int64_t group, const void *A,
+                          int64_t lda, const void *scales, const void *zeros, tcgDataType_t Stype, const void *B,
+                          int64_t ldb, tcgDataType_t Btype, void *D, tcgDataType_t Dtype, int64_t ldd, int gated,
+                          const tcgEpilogue_t *epilogue)
+{
+    if (!h || !valid_type(Stype))
+        return TCG_STATUS_INVALID_VALUE;
+    tcgEpilogue_t epi = {};
+    if (epilogue)
+        epi = *epilogue;
+    tcgStatus_t st = check_types(Btype, Dtype);
+    if (st == TCG_STATUS_SUCCESS)
+        st = check_epilogue(epi, m, n, Btype, Dtype);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    if (m < 0 || n < 0 || k < 0 || lda < (k + 1) / 2 || lda < 1 || lda % 16 || bad_ld(ldb, k, 2) ||
+        bad_ld(ldd, m, elem_size(Dtype)))
+        return TCG_STATUS_INVALID_VALUE;
+    if ((group != 32 && group != 64 && group != 128) || (Stype != TCG_R_32F && Stype != Btype) || epi.Z ||
+        (gated && (epi.bias || epi.beta != 0.0f)) || 2 * m > kMaxExtent || n > kMaxExtent || k > kMaxK)
+        return TCG_STATUS_NOT_SUPPORTED;
+    if (m == 0 || n == 0)
+        return TCG_STATUS_SUCCESS;
+    const uintptr_t es = elem_size(Stype);
+    if (!D || !aligned16(D) ||
+        (k > 0 && (!A || !B || !scales || !aligned16(A) || !aligned16(B) ||
+                   reinterpret_cast<uintptr_t>(scales) % es || reinterpret_cast<uintptr_t>(zeros) % es)))
+        return TCG_STATUS_INVALID_VALUE;
+    st = bind_device(h);
+    if (st == TCG_STATUS_SUCCESS)
+        st = check_device(h, {D, k > 0 ? A : nullptr, k > 0 ? B : nullptr, k > 0 ? scales : nullptr,
+                              k > 0 ? zeros : nullptr, epi.bias, epi.beta != 0.0f ? epi.C : nullptr});
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    h->used = true;
+    W4Args a{};
+    a.rows = gated ? 2 * m : m;
+    a.k = k;
+    a.tokens = static_cast<int>(n);
+    a.group = static_cast<int>(group);
+    a.W = static_cast<const uint8_t *>(A);
+    a.ldw = lda;
+    a.scales = scales;
+    a.zeros = zeros;
+    a.s_f32 = Stype == TCG_R_32F;
+    a.X = B;
+    a.ldx = ldb;
+    a.in_bf16 = Btype == TCG_R_16BF;
+    a.out_kind = out_kind_of(Dtype);
+    a.D = D;
+    a.ldd = ldd;
+    a.bias = epi.bias;
+    a.bias_f32 = epi.bias_type == TCG_R_32F;
+    a.C = epi.beta != 0.0f ? epi.C : nullptr;
+    a.ldc = epi.ldc;
+    a.beta = epi.beta;
+    a.act = epi.activation;
+    a.gated = gated != 0;
+    if (n <= kW4Tokens) {
+        const cudaError_t e = launch_w4(a, h->num_sms, h->stream);
+        h->launches += 1;
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return TCG_STATUS_EXECUTION_FAILED;
+        }
+        return TCG_STATUS_SUCCESS;
+    }
+    Product p = w4_product(a, Btype, Dtype);
+    const size_t wide = w4_expand_bytes(a.rows, k), need = wide + product_ws(h, p);
+    void *ws = nullptr;
+    if (need) {
+        st = acquire_ws(h, need, &ws);
+        if (st != TCG_STATUS_SUCCESS)
+            return st;
+    }
+    p.W = ws;
+    p.ldw = (k + 7) / 8 * 8;
+    p.X = B;
+    p.ldx = ldb;
+    p.D = D;
+    p.ldd = ldd;
+    p.epi = epi;
+    if (k > 0) {
+        const cudaError_t e = launch_w4_expand(a, ws, p.ldw, h->num_sms, h->stream);
+        h->launches += 1;
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return TCG_STATUS_EXECUTION_FAILED;
+        }
+    }
+    return queue(h, p, static_cast<uint8_t *>(ws) + wide);
+}
+
+tcgStatus_t tcg_gemm_4bit_workspace_size(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int gated, size_t *bytes)
+{
+    if (!h || !bytes || m < 0 || n < 0 || k < 0)
+        return TCG_STATUS_INVALID_VALUE;
+    if (2 * m > kMaxExtent || n > kMaxExtent || k > kMaxK)
+        return TCG_STATUS_NOT_SUPPORTED;
+    *bytes = 0;
+    if (m == 0 || n <= kW4Tokens)
+        return TCG_STATUS_SUCCESS;
+    const tcgStatus_t st = bind_device(h);
+    if (st != TCG_STATUS_SUCCESS)
+        return st;
+    W4Args a{};
+    a.rows = gated ? 2 * m : m;
+    a.k = k;
+    a.tokens = static_cast<int>(n);
+    a.gated = gated != 0;
+    *bytes = w4_expand_bytes(a.rows, k) + product_ws(h, w4_product(a, TCG_R_16BF, TCG_R_16BF));
     return TCG_STATUS_SUCCESS;
 }
 

@@ -64,47 +64,20 @@ __device__ __forceinline__ void unpack2(const uint4 &v, F2 (&x)[4])
         x[i] = f2(f[2 * i], f[2 * i + 1]);
 }
 
-__device__ __forceinline__ float act_of(int act, float x)
-{
-    float y, unused;
-    F2 v = f2(x, 0.0f);
-    switch (act) {
-    case kActRelu: v = act_fn<kActRelu>(v); break;
-    case kActGelu: v = act_fn<kActGelu>(v); break;
-    case kActGeluTanh: v = act_fn<kActGeluTanh>(v); break;
-    case kActSilu: v = act_fn<kActSilu>(v); break;
-    default: break;
-    }
-    split2(v, y, unused);
-    return y;
-}
-
-__device__ __forceinline__ float load_out(const void *p, int64_t i, int kind)
-{
-    return kind == kOutF32 ? static_cast<const float *>(p)[i] : load16(p, i, kind == kOutBF16);
-}
-
-__device__ __forceinline__ void store_out(void *p, int64_t i, int kind, float v)
-{
-    if (kind == kOutF32)
-        static_cast<float *>(p)[i] = v;
-    else
-        static_cast<uint16_t *>(p)[i] = round16(v, kind == kOutBF16);
-}
-
-// What a warp does with task i of its walk: rows f0 .. f0 + R - 1 of group g, tokens t0 ..
-// t0 + nt - 1.
+// What a warp does with task i of its walk: features f0 .. f0 + R - 1 of group g (R / 2 of them,
+// both halves, of a gated product), tokens t0 .. t0 + nt - 1.
 struct FewTask {
     int64_t f0;
     int g, t0, nt;
 };
 
-template <int TT, int R, bool BF16>
+template <int TT, int R, bool BF16, bool GATED>
 __global__ void __launch_bounds__(kFewWarps * 32, 1)
     tcg_few_kernel(const LmFewArgs p)
 {
     using Cfg = FewCfg<R>;
     constexpr int S = Cfg::kStages;
+    constexpr int F = GATED ? R / 2 : R;            // features of a task
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ FewCtl ctl;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -142,15 +115,15 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
         }
         __syncthreads();
     }
-    const int64_t quads = (p.feats + R - 1) / R;
+    const int64_t quads = (p.feats + F - 1) / F;
     const int64_t tasks = quads * (p.offsets ? ctl.leads : 1);
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kFewWarps;
     const int64_t mine = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;   // SMs before warps
     auto task = [&](int64_t i) {
-        FewTask w{i * R, 0, 0, p.tokens};
+        FewTask w{i * F, 0, 0, p.tokens};
         if (p.offsets) {
             const int64_t l = i / quads;
-            w.f0 = (i - l * quads) * R;
+            w.f0 = (i - l * quads) * F;
             w.t0 = ctl.lead[l];
             w.g = ctl.group_of[w.t0];
             w.nt = 1;
@@ -158,6 +131,12 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
                 ++w.nt;
         }
         return w;
+    };
+
+    // Row r of a task in the weights; rows past the end repeat the last one.
+    auto weight_row = [&](int64_t f0, int r) {
+        const int64_t f = f0 + r % F < p.feats ? f0 + r % F : p.feats - 1;
+        return r < F ? f : f + p.feats;
     };
 
     uint8_t *my_ring = ring + warp * (S * Cfg::kStageBytes);
@@ -189,8 +168,8 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
             if (lane == 0)
                 mbar_arrive_expect_tx(bar, bytes * R);
             __syncwarp();
-            if (lane < R) {                         // rows past the end repeat the last one
-                const int64_t f = wp.f0 + lane < p.feats ? wp.f0 + lane : p.feats - 1;
+            if (lane < R) {
+                const int64_t f = weight_row(wp.f0, lane);
                 bulk_load(my_ring_u32 + sp * Cfg::kStageBytes + lane * kFewRowBytes,
                           static_cast<const uint16_t *>(p.W) + wp.g * p.strideW + f * p.ldw + kp, bytes, bar);
             }
@@ -310,7 +289,7 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
                 a += b;
                 // the last K mod 8 elements, a lane each: no copy reads past a row's end
                 if (w.g >= 0 && t < w.nt && K8 + lane < K) {
-                    const int64_t f = w.f0 + r < p.feats ? w.f0 + r : p.feats - 1;
+                    const int64_t f = weight_row(w.f0, r);
                     a = fmaf(load16(p.W, w.g * p.strideW + f * p.ldw + K8 + lane, BF16),
                              load16(p.X, (w.t0 + t) * p.ldx + K8 + lane, BF16), a);
                 }
@@ -339,6 +318,27 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
                     run_s[t] = fmaf(run_s[t], exp_from(run_m[t], base), e);
                     run_m[t] = mx;
                 }
+            }
+            continue;
+        }
+        if constexpr (GATED) {                      // lane f + F t finishes feature f of token t
+            float g = 0.0f, u = 0.0f;
+#pragma unroll
+            for (int r = 0; r < F; ++r)
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+                    if (lane == r + F * t) {
+                        g = sum[r][t];
+                        u = sum[r + F][t];
+                    }
+            const int64_t f = w.f0 + lane % F, tok = w.t0 + lane / F;
+            if (lane < F * w.nt && f < p.feats) {
+                if (p.Z) {
+                    uint16_t *z = static_cast<uint16_t *>(p.Z) + tok * p.ldz + f;
+                    z[0] = round16(g, BF16);
+                    z[p.feats] = round16(u, BF16);
+                }
+                store_out(p.D, tok * p.ldd + f, p.out_kind, act_of(p.act, g) * u);
             }
             continue;
         }
@@ -396,11 +396,11 @@ __global__ void __launch_bounds__(kFewWarps * 32, 1)
     }
 }
 
-template <int TT, int R, bool BF16>
+template <int TT, int R, bool BF16, bool GATED>
 cudaError_t launch_one(const LmFewArgs &a, int grid, cudaStream_t s)
 {
     using Cfg = FewCfg<R>;
-    auto fn = tcg_few_kernel<TT, R, BF16>;
+    auto fn = tcg_few_kernel<TT, R, BF16, GATED>;
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                Cfg::kSmemBytes);
     if (e != cudaSuccess)
@@ -411,9 +411,14 @@ cudaError_t launch_one(const LmFewArgs &a, int grid, cudaStream_t s)
 template <int TT>
 cudaError_t launch_tt(const LmFewArgs &a, int rows, int grid, cudaStream_t s)
 {
+    if (a.gated) {
+        if (rows == 2)
+            return a.in_bf16 ? launch_one<TT, 2, true, true>(a, grid, s) : launch_one<TT, 2, false, true>(a, grid, s);
+        return a.in_bf16 ? launch_one<TT, 4, true, true>(a, grid, s) : launch_one<TT, 4, false, true>(a, grid, s);
+    }
     if (rows == 1)
-        return a.in_bf16 ? launch_one<TT, 1, true>(a, grid, s) : launch_one<TT, 1, false>(a, grid, s);
-    return a.in_bf16 ? launch_one<TT, 4, true>(a, grid, s) : launch_one<TT, 4, false>(a, grid, s);
+        return a.in_bf16 ? launch_one<TT, 1, true, false>(a, grid, s) : launch_one<TT, 1, false, false>(a, grid, s);
+    return a.in_bf16 ? launch_one<TT, 4, true, false>(a, grid, s) : launch_one<TT, 4, false, false>(a, grid, s);
 }
 
 }  // namespace
@@ -423,8 +428,9 @@ cudaError_t launch_few(const LmFewArgs &a, int num_sms, cudaStream_t s)
     // Four rows a warp read X a quarter as often; one row where four would leave the SMs
     // unevenly filled.
     const int lists = a.offsets ? (a.tokens < a.groups ? a.tokens : a.groups) : 1;
-    const int rows = (a.feats + 3) / 4 * lists >= 4 * static_cast<int64_t>(num_sms) ? 4 : 1;
-    const int64_t tasks = (a.feats + rows - 1) / rows * (a.offsets ? a.tokens : 1);
+    const int64_t all = a.gated ? 2 * a.feats : a.feats;
+    const int rows = (all + 3) / 4 * lists >= 4 * static_cast<int64_t>(num_sms) ? 4 : (a.gated ? 2 : 1);
+    const int64_t tasks = (all + rows - 1) / rows * (a.offsets ? a.tokens : 1);
     const int grid = a.stats || tasks >= num_sms ? num_sms : static_cast<int>(tasks);
     const int tt = a.offsets && a.tokens > 2 ? 2 : a.tokens;
     return tt <= 1 ? launch_tt<1>(a, rows, grid, s)

@@ -173,6 +173,34 @@ __device__ __forceinline__ void store_as(void *p, int64_t i, float v)
         static_cast<uint16_t *>(p)[i] = round16(v, OUT == kOutBF16);
 }
 
+__device__ __forceinline__ float act_of(int act, float x)
+{
+    float y, unused;
+    F2 v = f2(x, 0.0f);
+    switch (act) {
+    case kActRelu: v = act_fn<kActRelu>(v); break;
+    case kActGelu: v = act_fn<kActGelu>(v); break;
+    case kActGeluTanh: v = act_fn<kActGeluTanh>(v); break;
+    case kActSilu: v = act_fn<kActSilu>(v); break;
+    default: break;
+    }
+    split2(v, y, unused);
+    return y;
+}
+
+__device__ __forceinline__ float load_out(const void *p, int64_t i, int kind)
+{
+    return kind == kOutF32 ? static_cast<const float *>(p)[i] : load16(p, i, kind == kOutBF16);
+}
+
+__device__ __forceinline__ void store_out(void *p, int64_t i, int kind, float v)
+{
+    if (kind == kOutF32)
+        static_cast<float *>(p)[i] = v;
+    else
+        static_cast<uint16_t *>(p)[i] = round16(v, kind == kOutBF16);
+}
+
 __device__ __forceinline__ uint32_t pack16(float a, float b, bool bf16)
 {
     if (bf16) {

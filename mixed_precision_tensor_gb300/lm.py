@@ -44,7 +44,7 @@ def _rows(t, what, rows, cols, dtype, device):
     if t.dtype is not dtype or t.device != device:
         raise ValueError(f"{what} must be {dtype} on {device}, got {t.dtype} on {t.device}")
     s0, s1 = t.stride()
-    per = 4 if dtype is torch.float32 else 8
+    per = 16 // dtype.itemsize
     if s1 != 1 and cols > 1:
         raise ValueError(f"{what} must have unit stride along its last dimension")
     if rows <= 1 or cols == 0:                # no stride between rows to go by
@@ -97,7 +97,7 @@ def _matrix(handle, given, what, rows, cols, dtype, device):
     multiple of 16 bytes apart -- and its leading dimension."""
     if given is not None:
         return given, _rows(given, what, rows, cols, dtype, device)
-    per = 4 if dtype is torch.float32 else 8
+    per = 16 // dtype.itemsize
     ld = (cols + per - 1) // per * per or per
     new = _empty(handle, (rows, ld), dtype, device)
     return (new if ld == cols else new[:, :cols]), ld

@@ -763,9 +763,6 @@ tcgStatus_t check_norm(int64_t rows, int64_t k, const void *W, tcgDataType_t w_t
 bool bad_rows(const void *p, int64_t ld, int64_t cols, int es) { return !aligned16(p) || bad_ld(ld, cols, es); }
 
 // --------------------------------------------------------------------- 4-bit weights
-// Most tokens of a pass over the packed weights; more take them as 16-bit operands.
-constexpr int kW4Tokens = 64;
-
 size_t w4_expand_bytes(int64_t rows, int64_t k) { return pad256(static_cast<size_t>(rows) * ((k + 7) / 8 * 8) * 2); }
 
 Product w4_product(const W4Args &a, tcgDataType_t in, tcgDataType_t out)

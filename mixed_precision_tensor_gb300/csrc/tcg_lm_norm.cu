@@ -24,22 +24,21 @@ namespace tcg {
 
 namespace {
 
-constexpr int kNormRows = 8;                    // rows of a block whose rows are a warp's
 constexpr float kE4m3Max = 448.0f;
 constexpr float kMinScale = 7.888609052210118e-31f;   // 2^-100
 
-// A row's threads: a warp for up to 512 columns, then all of a block.
+// A row's threads hold 16 columns each (8 where a warp is enough for them, 32 beyond 16384); a block
+// of 256 has as many rows at a time as fit.
 struct NormShape {
-    int v, threads, rows;                       // pieces a thread, threads a block, rows at a time
+    int v, threads, rows;                       // pieces a thread, threads a row, rows of a block
 };
 
 NormShape norm_shape(int64_t k)
 {
     const int64_t pieces = (k + 7) / 8;
-    if (pieces <= 64)
-        return {pieces <= 32 ? 1 : 2, 32 * kNormRows, kNormRows};
-    const int v = pieces <= 2048 ? 2 : 4;
-    return {v, static_cast<int>((pieces + 32 * v - 1) / (32 * v) * 32), 1};
+    const int v = pieces <= 32 ? 1 : (pieces <= 2048 ? 2 : 4);
+    const int threads = static_cast<int>((pieces + 32 * v - 1) / (32 * v) * 32);
+    return {v, threads, threads < 256 ? 256 / threads : 1};
 }
 
 // Eight elements of a row, those from `left` on zero.
@@ -115,10 +114,20 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return m;
 }
 
+// A row's threads: `size` of them (whole warps, in a block's `row`-th place); this thread is the t-th.
+struct RowThreads {
+    int size, row, t;
+};
+__device__ __forceinline__ RowThreads row_of(int size)
+{
+    const int row = static_cast<int>(threadIdx.x) / size;
+    return RowThreads{size, row, static_cast<int>(threadIdx.x) - row * size};
+}
+
 // Sums of a, and sums or maxima of b, over a row's threads.  `room` alternates from row to row,
 // so that one barrier a row is enough.
-template <bool ONE_WARP, bool MAX_B>
-__device__ __forceinline__ void join_row(float2 (*part)[32], int room, float &a, float &b)
+template <bool MAX_B>
+__device__ __forceinline__ void join_row(float2 (*part)[32], int room, const RowThreads &th, float &a, float &b)
 {
     auto both = [&](float oa, float ob) {
         a += oa;
@@ -127,12 +136,12 @@ __device__ __forceinline__ void join_row(float2 (*part)[32], int room, float &a,
 #pragma unroll
     for (int d = 16; d; d >>= 1)
         both(__shfl_xor_sync(0xffffffffu, a, d), __shfl_xor_sync(0xffffffffu, b, d));
-    if constexpr (!ONE_WARP) {
-        const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (th.size > 32) {
+        const int lane = threadIdx.x & 31, warps = th.size >> 5;
         if (lane == 0)
             part[room][threadIdx.x >> 5] = make_float2(a, b);
-        __syncthreads();
-        const float2 p = lane < warps ? part[room][lane] : make_float2(0.0f, 0.0f);
+        named_barrier_sync(1 + th.row, th.size);
+        const float2 p = lane < warps ? part[room][th.row * warps + lane] : make_float2(0.0f, 0.0f);
         a = p.x;
         b = p.y;
 #pragma unroll
@@ -141,31 +150,45 @@ __device__ __forceinline__ void join_row(float2 (*part)[32], int room, float &a,
     }
 }
 
-template <int V, bool BF16, bool OUT8, bool ONE_WARP>
-__global__ void __launch_bounds__(ONE_WARP ? 32 * kNormRows : 1024) tcg_norm_kernel(const NormArgs p)
+// RES: with a residual.  Without one a thread has the next row on its way while it finishes a row (16384
+// x 4096: 54 us without that); with one a row is enough to keep memory busy, and two take registers
+// that hold blocks.
+template <int V, bool BF16, bool OUT8, bool RES>
+__global__ void __launch_bounds__(1024) tcg_norm_kernel(const NormArgs p, int row_threads)
 {
     __shared__ float2 part[2][32];
     griddep_launch_dependents();
     griddep_wait();
-    const int t = ONE_WARP ? threadIdx.x & 31 : threadIdx.x, per_row = ONE_WARP ? 32 : blockDim.x;
-    const int per_block = ONE_WARP ? kNormRows : 1;
+    const RowThreads th = row_of(row_threads);
+    const int t = th.t, per_row = th.size, at_once = blockDim.x / th.size;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * at_once;
     const float inv_k = 1.0f / static_cast<float>(p.k);
-    int room = 0;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + (ONE_WARP ? threadIdx.x >> 5 : 0);
-         row < p.rows; row += static_cast<int64_t>(gridDim.x) * per_block, room ^= 1) {
-        const uint16_t *x = static_cast<const uint16_t *>(p.X) + row * p.ldx;
-        const uint16_t *res = static_cast<const uint16_t *>(p.R) + row * p.ldr;
-        uint4 vx[V], vr[V];
+    uint4 vx[V], vr[V], next[V];
+    auto load = [&](const void *base, int64_t ld, int64_t row, uint4 (&v)[V]) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int c = (i * per_row + t) * 8;
-            vx[i] = load_piece(x + c, p.k - c);
-            if (p.R)
-                vr[i] = load_piece(res + c, p.k - c);
+            v[i] = load_piece(static_cast<const uint16_t *>(base) + row * ld + c, p.k - c);
+        }
+    };
+    int64_t row = static_cast<int64_t>(blockIdx.x) * at_once + th.row;
+    if (!RES && row < p.rows)
+        load(p.X, p.ldx, row, next);
+    int room = 0;
+    for (; row < p.rows; row += step, room ^= 1) {
+        if constexpr (RES) {
+            load(p.X, p.ldx, row, vx);
+            load(p.R, p.ldr, row, vr);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                vx[i] = next[i];
+            if (row + step < p.rows)
+                load(p.X, p.ldx, row + step, next);
         }
         auto sum_of = [&](int i, float (&s)[8]) {
             unpack16<BF16>(vx[i], s);
-            if (p.R) {
+            if constexpr (RES) {
                 float r[8];
                 unpack16<BF16>(vr[i], r);
 #pragma unroll
@@ -192,7 +215,7 @@ __global__ void __launch_bounds__(ONE_WARP ? 32 * kNormRows : 1024) tcg_norm_ker
             if (p.S)
                 store_piece<BF16>(static_cast<uint16_t *>(p.S) + row * p.lds + c, p.k - c, s);
         }
-        join_row<ONE_WARP, true>(part, room, ss, top);
+        join_row<true>(part, room, th, ss, top);
         const float r = rsqrtf(fmaf(ss, inv_k, p.eps));
         float inv = 1.0f;
         if (OUT8) {
@@ -221,16 +244,22 @@ __global__ void __launch_bounds__(ONE_WARP ? 32 * kNormRows : 1024) tcg_norm_ker
     }
 }
 
-template <int V, bool BF16, bool ONE_WARP>
-__global__ void __launch_bounds__(ONE_WARP ? 32 * kNormRows : 1024) tcg_norm_backward_kernel(const NormBackwardArgs p)
+// ONE: a row is a block of its own.  Blocks of up to 256 threads (FEW) are three to an SM, so that a
+// thread has registers for its columns of dw and a row of three tensors: 16384 x 4096 takes 103 us so,
+// 105 with four blocks of 64 registers and a few values in memory, 185 with more of them there.
+constexpr int kFewThreads = 256;
+template <int V, bool BF16, bool ONE, bool FEW>
+__global__ void __launch_bounds__(FEW ? kFewThreads : 1024, FEW ? 3 : 1)
+    tcg_norm_backward_kernel(const NormBackwardArgs p, int row_threads)
 {
+    extern __shared__ float rows_dw[];          // at the end: dw of each of the block's rows' threads
     __shared__ float2 part[2][32];
-    extern __shared__ float rows_dw[];          // ONE_WARP: a warp's dw each
     griddep_launch_dependents();
     griddep_wait();
-    const int warp = threadIdx.x >> 5;
-    const int t = ONE_WARP ? threadIdx.x & 31 : threadIdx.x, per_row = ONE_WARP ? 32 : blockDim.x;
-    const int per_block = ONE_WARP ? kNormRows : 1;
+    const RowThreads th = ONE ? RowThreads{static_cast<int>(blockDim.x), 0, static_cast<int>(threadIdx.x)}
+                              : row_of(row_threads);
+    const int t = ONE ? threadIdx.x : th.t, per_row = ONE ? blockDim.x : th.size, at_once = ONE ? 1 : blockDim.x / th.size;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * at_once;
     const float inv_k = 1.0f / static_cast<float>(p.k);
     float dw[V][8];
 #pragma unroll
@@ -239,8 +268,7 @@ __global__ void __launch_bounds__(ONE_WARP ? 32 * kNormRows : 1024) tcg_norm_bac
         for (int j = 0; j < 8; ++j)
             dw[i][j] = 0.0f;
     int room = 0;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * per_block + (ONE_WARP ? warp : 0); row < p.rows;
-         row += static_cast<int64_t>(gridDim.x) * per_block, room ^= 1) {
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * at_once + th.row; row < p.rows; row += step, room ^= 1) {
         uint4 vx[V], vd[V], vs[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -264,7 +292,7 @@ __global__ void __launch_bounds__(ONE_WARP ? 32 * kNormRows : 1024) tcg_norm_bac
                 dot = fmaf(d[j] * w[j], x[j], dot);
             }
         }
-        join_row<ONE_WARP, false>(part, room, ss, dot);
+        join_row<false>(part, room, th, ss, dot);
         const float r = rsqrtf(fmaf(ss, inv_k, p.eps));
         const float m = r * r * (dot * inv_k);
 #pragma unroll
@@ -280,13 +308,14 @@ __global__ void __launch_bounds__(ONE_WARP ? 32 * kNormRows : 1024) tcg_norm_bac
                     dw[i][j] = fmaf(d[j], x[j] * r, dw[i][j]);
             }
             if (p.dX) {
-                float s[8];
-                if (p.dS)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    d[j] = r * fmaf(-x[j], m, d[j] * w[j]);
+                if (p.dS) {
+                    float s[8];
                     unpack16<BF16>(vs[i], s);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    d[j] = r * fmaf(-x[j], m, d[j] * w[j]);
-                    if (p.dS)
+                    for (int j = 0; j < 8; ++j)
                         d[j] += s[j];
                 }
                 store_piece<BF16>(static_cast<uint16_t *>(p.dX) + row * p.lddx + c, p.k - c, d);
@@ -295,27 +324,26 @@ __global__ void __launch_bounds__(ONE_WARP ? 32 * kNormRows : 1024) tcg_norm_bac
     }
     if (!p.part)
         return;
-    float *mine = ONE_WARP ? rows_dw + warp * p.k : p.part + static_cast<int64_t>(blockIdx.x) * p.k;
+    float *out = p.part + static_cast<int64_t>(blockIdx.x) * p.k, *mine = at_once > 1 ? rows_dw + th.row * p.k : out;
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if ((i * per_row + t) * 8 + j < p.k)
                 mine[(i * per_row + t) * 8 + j] = dw[i][j];
-    if constexpr (ONE_WARP) {
+    if (at_once > 1) {
         __syncthreads();
         for (int c = threadIdx.x; c < p.k; c += blockDim.x) {
             float s = 0.0f;
-#pragma unroll
-            for (int q = 0; q < kNormRows; ++q)
+            for (int q = 0; q < at_once; ++q)
                 s += rows_dw[q * p.k + c];
-            p.part[static_cast<int64_t>(blockIdx.x) * p.k + c] = s;
+            out[c] = s;
         }
     }
 }
 
-// dw = the blocks' sums, in block order: 32 columns a block, a sixteenth of the blocks a warp.
-constexpr int kJoinWarps = 16;
+// dw = the blocks' sums, in block order: 32 columns a block, every 32nd of the blocks a warp.
+constexpr int kJoinWarps = 32;
 __global__ void __launch_bounds__(32 * kJoinWarps)
     tcg_norm_join_kernel(const float *__restrict__ part, int blocks, int k, float *__restrict__ dw)
 {
@@ -325,7 +353,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float s = 0.0f;
     if (c < k) {
-#pragma unroll 8
+#pragma unroll 16
         for (int b = warp; b < blocks; b += kJoinWarps)
             s += part[static_cast<int64_t>(b) * k + c];
     }
@@ -339,26 +367,33 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     }
 }
 
-template <int V, bool ONE_WARP>
-cudaError_t norm_v(const NormArgs &a, dim3 grid, dim3 block, cudaStream_t s)
+template <int V, bool OUT8>
+cudaError_t norm_o(const NormArgs &a, const NormShape &n, int grid, cudaStream_t s)
 {
-    auto fn = a.out8 ? (a.in_bf16 ? tcg_norm_kernel<V, true, true, ONE_WARP> : tcg_norm_kernel<V, false, true, ONE_WARP>)
-                     : (a.in_bf16 ? tcg_norm_kernel<V, true, false, ONE_WARP> : tcg_norm_kernel<V, false, false, ONE_WARP>);
-    return launch_pdl(fn, grid, block, s, 0, a);
+    auto fn = a.R ? (a.in_bf16 ? tcg_norm_kernel<V, true, OUT8, true> : tcg_norm_kernel<V, false, OUT8, true>)
+                  : (a.in_bf16 ? tcg_norm_kernel<V, true, OUT8, false> : tcg_norm_kernel<V, false, OUT8, false>);
+    return launch_pdl(fn, dim3(grid), dim3(n.threads * n.rows), s, 0, a, n.threads);
 }
 
-template <int V, bool ONE_WARP>
-cudaError_t norm_backward_v(const NormBackwardArgs &a, dim3 grid, dim3 block, cudaStream_t s)
+template <int V>
+cudaError_t norm_v(const NormArgs &a, const NormShape &n, int grid, cudaStream_t s)
 {
-    return launch_pdl(a.in_bf16 ? tcg_norm_backward_kernel<V, true, ONE_WARP>
-                                : tcg_norm_backward_kernel<V, false, ONE_WARP>,
-                      grid, block, s, ONE_WARP && a.part ? kNormRows * a.k * sizeof(float) : 0, a);
+    return a.out8 ? norm_o<V, true>(a, n, grid, s) : norm_o<V, false>(a, n, grid, s);
 }
 
-// Blocks of the norm: as many as are resident, at most a row (or eight) for each.
-int norm_grid(const NormShape &n, int64_t rows, int num_sms, int per_sm)
+template <int V, bool ONE, bool FEW>
+cudaError_t norm_backward_v(const NormBackwardArgs &a, const NormShape &n, int grid, cudaStream_t s)
 {
-    const int64_t need = (rows + n.rows - 1) / n.rows, most = static_cast<int64_t>(num_sms) * per_sm;
+    const size_t smem = a.part && !ONE ? n.rows * a.k * sizeof(float) : 0;            // at most 16 KiB
+    return launch_pdl(a.in_bf16 ? tcg_norm_backward_kernel<V, true, ONE, FEW> : tcg_norm_backward_kernel<V, false, ONE, FEW>,
+                      dim3(grid), dim3(n.threads * n.rows), s, smem, a, n.threads);
+}
+
+// Blocks that are resident with `threads` an SM.
+int norm_grid(const NormShape &n, int64_t rows, int num_sms, int threads)
+{
+    const int64_t need = (rows + n.rows - 1) / n.rows;
+    const int64_t most = static_cast<int64_t>(num_sms) * (threads / (n.threads * n.rows));
     return static_cast<int>(need < most ? need : most);
 }
 
@@ -367,16 +402,14 @@ int norm_grid(const NormShape &n, int64_t rows, int num_sms, int per_sm)
 cudaError_t launch_norm(const NormArgs &a, int num_sms, cudaStream_t s)
 {
     const NormShape n = norm_shape(a.k);
-    const dim3 grid(norm_grid(n, a.rows, num_sms, 1024 / n.threads)), block(n.threads);
-    if (n.rows > 1)
-        return n.v == 1 ? norm_v<1, true>(a, grid, block, s) : norm_v<2, true>(a, grid, block, s);
-    return n.v == 2 ? norm_v<2, false>(a, grid, block, s) : norm_v<4, false>(a, grid, block, s);
+    const int grid = norm_grid(n, a.rows, num_sms, 1024);        // of 64 registers
+    return n.v == 1 ? norm_v<1>(a, n, grid, s) : n.v == 2 ? norm_v<2>(a, n, grid, s) : norm_v<4>(a, n, grid, s);
 }
 
 int norm_backward_blocks(int64_t rows, int64_t k, int num_sms)
 {
     const NormShape n = norm_shape(k);
-    return norm_grid(n, rows, num_sms, 1024 / n.threads);
+    return norm_grid(n, rows, num_sms, n.threads > kFewThreads ? 1024 : 3 * kFewThreads);
 }
 
 cudaError_t launch_norm_backward(NormBackwardArgs a, float *dw, int num_sms, cudaStream_t s)
@@ -385,13 +418,13 @@ cudaError_t launch_norm_backward(NormBackwardArgs a, float *dw, int num_sms, cud
     const int blocks = norm_backward_blocks(a.rows, a.k, num_sms);
     if (blocks == 1)                            // nothing to join
         a.part = dw;
-    const dim3 grid(blocks), block(n.threads);
     cudaError_t e = cudaSuccess;
     if (blocks > 0)
-        e = n.rows > 1 ? (n.v == 1 ? norm_backward_v<1, true>(a, grid, block, s)
-                                   : norm_backward_v<2, true>(a, grid, block, s))
-                       : (n.v == 2 ? norm_backward_v<2, false>(a, grid, block, s)
-                                   : norm_backward_v<4, false>(a, grid, block, s));
+        e = n.v == 1 ? norm_backward_v<1, false, true>(a, n, blocks, s)
+          : n.v == 4 ? norm_backward_v<4, true, false>(a, n, blocks, s)
+          : n.rows > 1 ? norm_backward_v<2, false, true>(a, n, blocks, s)
+          : n.threads <= kFewThreads ? norm_backward_v<2, true, true>(a, n, blocks, s)
+                                     : norm_backward_v<2, true, false>(a, n, blocks, s);
     if (e == cudaSuccess && dw && blocks != 1)  // without rows: zeros
         e = launch_pdl(tcg_norm_join_kernel, dim3((a.k + 31) / 32), dim3(32 * kJoinWarps), s, 0, a.part, blocks,
                        a.k, dw);

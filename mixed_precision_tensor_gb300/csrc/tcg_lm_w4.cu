@@ -3,18 +3,19 @@
 //   z[t][f] = sum over groups of s[f][g] (sum over k of g of (q[f][k] - zero[f][g]) x[t][k])
 //
 // Bound by memory: half a byte a weight for 2 T operations.  Turning a weight into a number costs
-// more instructions than multiplying it, so a warp does that once for eight tokens or more:
-// q - 8, exact in 16 bits, is the A operand of mma.m16n8k16, the tokens are its eight columns
-// (tcgen05 would want the weights back in shared memory first, and 128 rows of them).  Sums are
-// FP32.  A group's sum is scaled in FP32 when it is complete; with zeros, (8 - zero) times the
-// group's sum of x, which one more product with a matrix of ones gives, is added.
+// more instructions than multiplying it, so a warp does that once for eight tokens or more: the
+// weights are the A operand of mma.m16n8k16, the tokens its eight columns (tcgen05 would want the
+// weights back in shared memory first, and 128 rows of them).  A nibble becomes a number by a mask
+// (see widen); what it is too much, 8 or the zero times the group's sum of x, comes from one more
+// product with a constant matrix for all rows, and is taken away in FP32 when the group is complete
+// and meets its scale.  Sums are FP32.
 //
-// A warp has 32 rows and streams them 128 elements at a time through a ring of its own
-// (asynchronous 16-byte copies; rows 80 bytes apart, so that the words that eight rows' lanes want
-// lie in different banks).  Its lane c of a quad takes elements 8 c .. 8 c + 7 of each 32: in a word
-// elements j and j + 4 are 16 bits apart, so one mask gives the pair (j, j + 4); x is paired to
-// match.  The warps of a block, and the blocks of a cluster, share the elements of the same rows;
-// sums are joined through (distributed) shared memory in a fixed order.
+// A warp has 64 rows (32 for 9 to 16 tokens) and streams them 128 elements at a time through a ring
+// of its own (asynchronous 16-byte copies, x beside the weights).  Its
+// lane c of a quad takes elements 8 c .. 8 c + 7 of each 32: in a word elements j and j + 4 are 16
+// bits apart, so one mask gives the pair (j, j + 4); x is paired to match.  The warps of a block and
+// the blocks of a cluster take the stages of the same rows in turn; their sums are joined through
+// (distributed) shared memory in a fixed order.
 
 #include "tcg_lm_math.cuh"
 
@@ -22,14 +23,26 @@ namespace tcg {
 
 namespace {
 
-constexpr int kW4Warps = 8;
-constexpr int kW4Rows = 32;                         // rows of a warp, and of a block
 constexpr int kW4K = 128;                           // elements of a stage
-constexpr int kW4RowBytes = kW4K / 2 + 16;          // in the ring
-constexpr int kW4StageBytes = kW4Rows * kW4RowBytes;
-constexpr int kW4Stages = 4;
-constexpr int kW4RingBytes = kW4Warps * kW4Stages * kW4StageBytes;
-constexpr int kW4Stride = kW4Rows + 4;              // of a token's sums: no bank conflicts
+constexpr int kW4XRow = kW4K * 2;                   // a token of a stage
+
+// Eight columns a product, NT of them; sixteen rows a product, MT of them.  XR: tokens whose x goes
+// through the ring.  PER: groups of 32 PER elements.  W: warps of a block.
+template <int NT, int MT, int XR, int PER, int W>
+struct W4Cfg {
+    static constexpr int kRows = 16 * MT;                            // of a warp
+    static constexpr int kWBytes = kRows * kW4K / 2;                 // weights of a stage
+    static constexpr int kStageBytes = kWBytes + XR * kW4XRow;
+    static constexpr int kScales = W * kRows * (4 / PER) * 8;        // a stage's scales and zeros
+    static constexpr int kSums = 8 * NT * kRows;                     // floats of a warp, and of what is sent
+    static constexpr int kPart = (W + 1) * kSums * 4;
+    static constexpr int kRoom = 227 * 1024 - kScales - kPart - 256;
+    static constexpr int kFit = kRoom / (W * kStageBytes);
+    static constexpr int kStages = kFit < 4 ? kFit : 4;
+    static constexpr int kRing = W * kStages * kStageBytes;
+    static constexpr int kSmem = kRing + kScales + kPart + 256;
+    static_assert(kStages >= 2, "a stage to read and one to fill");
+};
 
 template <bool BF16>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
@@ -44,47 +57,85 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// q - 8 of the eight elements of a word: pairs (0, 4), (1, 5), (2, 6), (3, 7).  A nibble below an
-// exponent of its own is 128 + q in BF16, and in FP16 1024 + q or, four bits up, 1024 + 16 q;
-// taking the constant away is exact.
+// d = a b + c, or (first) d = a b.
 template <bool BF16>
-__device__ __forceinline__ void widen(uint32_t w, uint32_t (&q)[4])
+__device__ __forceinline__ void mma_group(bool first, float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if (first)
+        d[0] = d[1] = d[2] = d[3] = 0.0f;
+    mma16816<BF16>(d, a, b0, b1);
+}
+
+// The eight elements of a word as A operands: pairs (0, 4), (1, 5), (2, 6), (3, 7).
+//   BF16: a 16-bit word 0 .. 255 is that many times 2^-133 (the subnormal numbers and the binade above
+//   them have one spacing), so a masked nibble is q or 16 q without further ado; x is multiplied by
+//   2^64 or 2^60 to match, and sums come out times 2^-69.
+//   FP16: x has no room for such factors; a shift brings two nibbles under the exponents of 256 and 16,
+//   as 256 + q and 16 + q.
+constexpr float kBfUnit = 5.9029581035870565e20f;   // 2^69
+template <bool BF16>
+__device__ __forceinline__ void widen(uint32_t w, const uint32_t (&m)[4], uint32_t (&q)[4])
 {
     if constexpr (BF16) {
-        const uint32_t off = 0x43084308u;           // 136
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t v = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-            const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v),
-                                             *reinterpret_cast<const __nv_bfloat162 *>(&off));
-            q[i] = *reinterpret_cast<const uint32_t *>(&r);
-        }
+        const uint32_t v = w >> 8;
+        q[0] = w & 0x000F000Fu;
+        q[1] = w & 0x00F000F0u;
+        q[2] = v & 0x000F000Fu;
+        q[3] = v & 0x00F000F0u;
     } else {
-        const uint32_t off = 0x64086408u, sixteenth = 0x2C002C00u, off16 = 0xD480D480u;   // 1032, 1/16, -72
-#pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-            const uint32_t u = w >> (4 * i);
-            const uint32_t lo = (u & 0x000F000Fu) | 0x64006400u, hi = (u & 0x00F000F0u) | 0x64006400u;
-            const __half2 a = __hsub2(*reinterpret_cast<const __half2 *>(&lo), *reinterpret_cast<const __half2 *>(&off));
-            const __half2 b = __hfma2(*reinterpret_cast<const __half2 *>(&hi),
-                                      *reinterpret_cast<const __half2 *>(&sixteenth),
-                                      *reinterpret_cast<const __half2 *>(&off16));
-            q[i] = *reinterpret_cast<const uint32_t *>(&a);
-            q[i + 1] = *reinterpret_cast<const uint32_t *>(&b);
-        }
+        // v & mask | base; as immediates the two would take two instructions
+        auto pick = [](uint32_t v, uint32_t mask, uint32_t base) {
+            uint32_t r;
+            asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(mask), "r"(base));
+            return r;
+        };
+        const uint32_t lo = w << 2, hi = w >> 6;
+        q[0] = pick(lo, m[0], m[1]);
+        q[1] = pick(lo, m[2], m[3]);
+        q[2] = pick(hi, m[0], m[1]);
+        q[3] = pick(hi, m[2], m[3]);
     }
 }
 
-// Row j of a block's 32 in the weights: of a gated product 16 rows of g, then their 16 of u.  Rows
-// past the end repeat the last one.
+// Two elements of x as B operands.
+template <bool BF16>
+__device__ __forceinline__ uint32_t scaled(uint32_t x, uint32_t factor)
+{
+    if constexpr (BF16) {
+        const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x),
+                                         *reinterpret_cast<const __nv_bfloat162 *>(&factor));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    } else {
+        return x;
+    }
+}
+
+__device__ __forceinline__ uint4 load_shared16(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t *v)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// Row j of a tile's `all` in the weights: of a gated product half are rows of g, then their rows of
+// u.  Rows past the end repeat the last one.
+template <int kRows>
 __device__ __forceinline__ int64_t w4_row(const W4Args &p, int64_t tile, int j)
 {
     if (!p.gated) {
-        const int64_t r = tile * kW4Rows + j;
+        const int64_t r = tile * kRows + j;
         return r < p.rows ? r : p.rows - 1;
     }
-    const int64_t n = p.rows / 2, f = tile * (kW4Rows / 2) + j % (kW4Rows / 2);
-    return (f < n ? f : n - 1) + (j < kW4Rows / 2 ? 0 : n);
+    const int64_t n = p.rows / 2, f = tile * (kRows / 2) + j % (kRows / 2);
+    return (f < n ? f : n - 1) + (j < kRows / 2 ? 0 : n);
 }
 
 // A scale or zero as it is stored, and its value.
@@ -98,279 +149,375 @@ __device__ __forceinline__ float raw_value(uint32_t v, int f32)
     return f32 || BF16 ? __uint_as_float(f32 ? v : v << 16) : __half2float(__ushort_as_half(static_cast<uint16_t>(v)));
 }
 
-__device__ __forceinline__ float load_cluster(uint32_t addr)
+// A token's row in a warp's sums: two tokens' rows start in banks of their own.
+template <int kRows>
+__device__ __forceinline__ int sum_at(int token, int row)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+    return token * kRows + (row ^ ((token >> 1 & 3) * 8));
 }
 
-template <int NT, bool BF16, bool ZEROS>
-__global__ void __launch_bounds__(kW4Warps * 32) tcg_w4_kernel(const W4Args p, int cluster)
-{
-    extern __shared__ __align__(128) uint8_t ring[];
-    griddep_launch_dependents();
-    griddep_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int rank = blockIdx.x % cluster;
-    const int64_t tile = blockIdx.x / cluster;
-    const int tok0 = blockIdx.y * (8 * NT);
-    const int64_t bytes = (p.k + 1) / 2;
-    const int units = static_cast<int>((p.k + kW4K - 1) / kW4K);
-    const int stride = cluster * kW4Warps, first = rank * kW4Warps + warp;
-    const int groups = static_cast<int>((p.k + p.group - 1) / p.group), per = p.group / 32;
+// Bytes of a 16-byte piece that exist, `left` being those from its start on.
+__device__ __forceinline__ int piece_bytes(int left) { return max(0, min(left, 16)); }
 
-    // Copies: lane l brings pieces l % 4 of rows l / 4 + 8 i.
-    uint8_t *mine = ring + warp * (kW4Stages * kW4StageBytes);
-    const uint8_t *src[4];
+__device__ __forceinline__ void store_cluster(uint32_t addr, float v)
+{
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+template <int NT, int MT, int XR, int PER, int W, bool BF16>
+__global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int cluster)
+{
+    using Cfg = W4Cfg<NT, MT, XR, PER, W>;
+    constexpr int S = Cfg::kStages, R = Cfg::kRows, kTokens = 8 * NT, kGroups = 4 / PER;   // groups of a stage
+    extern __shared__ __align__(256) uint8_t ring[];
+    float *part = reinterpret_cast<float *>(ring + Cfg::kRing + Cfg::kScales), *room = part + W * Cfg::kSums;
+    uint8_t *nothing = ring + Cfg::kSmem - 256;              // 256 bytes of zeros: x of no token
+    griddep_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    if (threadIdx.x < 64)
+        reinterpret_cast<uint32_t *>(nothing)[threadIdx.x] = 0u;
+    __syncthreads();
+    const int rank = blockIdx.x % cluster, first_tile = blockIdx.x / cluster, tile_step = gridDim.x / cluster;
+    const int tok0 = blockIdx.y * kTokens;
+    const int stride = cluster * W, begin = rank * W + warp;
+    const int units = p.units, groups = p.groups, tiles = p.tiles;
+    const int k = static_cast<int>(p.k), bytes = (k + 1) / 2, whole = k / kW4K;   // stages without an end of the row
+    const bool zeros = p.zeros != nullptr, s_f32 = p.s_f32 != 0;
+    const int tokens = p.tokens - tok0;                      // of this block, if fewer than kTokens
+
+    const uint32_t mine = smem_u32(ring) + warp * (S * Cfg::kStageBytes);
+    float *sc = reinterpret_cast<float *>(ring + Cfg::kRing) + warp * (2 * R * kGroups);   // scales, then zeros
+    griddep_wait();
+
+    // Copies: lane l brings piece l % 4 of rows l / 4 + 8 i, at a place in the row that makes eight
+    // rows' reads meet different banks; and piece l % 16 of tokens l / 16 + 2 i of x.  The walk: every
+    // `stride`-th stage of a tile, then those of the next tile.
+    const uint8_t *src[2 * MT];
+    const int rows_x = min(tokens, XR) - (lane >> 4);
+    const uint16_t *src_x = static_cast<const uint16_t *>(p.X) + (tok0 + (lane >> 4)) * p.ldx + (lane & 15) * 8;
+    const uint32_t to_w = mine + g * 64 + (c ^ ((g >> 1) & 3)) * 16;
+    const uint32_t to_x = mine + Cfg::kWBytes + (lane >> 4) * kW4XRow + ((lane & 15) ^ ((lane >> 4) << 2)) * 16;
+    int ahead = begin, ahead_tile = first_tile;
+    uint32_t sp = 0;                                         // bytes of the stage to fill
+    auto aim = [&]() {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        src[i] = p.W + w4_row(p, tile, g + 8 * i) * p.ldw;
-    const uint32_t dst0 = smem_u32(mine) + g * kW4RowBytes + c * 16;
-    auto produce = [&](int unit, int stage) {
-        if (unit < units) {
-            const int64_t at = static_cast<int64_t>(unit) * (kW4K / 2) + c * 16, left = bytes - at;
-            const int n = left >= 16 ? 16 : (left > 0 ? static_cast<int>(left) : 0);
+        for (int i = 0; i < 2 * MT; ++i)
+            src[i] = p.W + w4_row<R>(p, ahead_tile, g + 8 * i) * p.ldw + c * 16;
+    };
+    if (begin >= units)                                      // nothing for this warp
+        ahead_tile = tiles;
+    aim();
+    auto copy = [&](int from, int n, int from_x, int xn) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                                 dst0 + stage * kW4StageBytes + i * 8 * kW4RowBytes),
-                             "l"(src[i] + (n ? at : 0)), "r"(n)
+        for (int i = 0; i < 2 * MT; ++i)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to_w + sp + i * 512),
+                         "l"(src[i] + from), "r"(n)
+                         : "memory");
+#pragma unroll
+        for (int i = 0; i < XR / 2; ++i)
+            if (2 * i < rows_x)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(to_x + sp + i * 512),
+                             "l"(src_x + 2 * i * p.ldx + from_x), "r"(xn)
                              : "memory");
+    };
+    auto produce = [&]() {
+        if (ahead_tile < tiles) {
+            const int at = ahead * (kW4K / 2), kx = ahead * kW4K;
+            if (ahead < whole) {
+                copy(at, 16, kx, 16);
+            } else {                                         // an end of the rows; nothing is read past it
+                const int n = piece_bytes(bytes - at - c * 16), xn = piece_bytes((k - kx - (lane & 15) * 8) * 2);
+                copy(n ? at : -c * 16, n, xn ? kx : -(lane & 15) * 8, xn);
+            }
+            ahead += stride;
+            if (ahead >= units) {
+                ahead = begin;
+                ahead_tile += tile_step;
+                if (ahead_tile < tiles)
+                    aim();
+            }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
+        sp = sp + Cfg::kStageBytes == S * Cfg::kStageBytes ? 0u : sp + Cfg::kStageBytes;
     };
 
-    // x of this lane's column, eight elements of 32.
-    auto load_x = [&](int64_t k, int nt) {
-        const int t = tok0 + nt * 8 + g;
-        const int64_t at = k + 8 * c, left = p.k - at;
-        uint32_t u[4] = {0u, 0u, 0u, 0u};
-        if (t < p.tokens && left > 0) {
-            const uint16_t *x = static_cast<const uint16_t *>(p.X) + t * p.ldx + at;
-            if (left >= 8)
-                return *reinterpret_cast<const uint4 *>(x);
+    // The scales and zeros of rows lane and lane + 32 come a stage ahead through registers.
+    constexpr int kSr = R / 32;
+    uint32_t raw_s[kSr][kGroups] = {}, raw_z[kSr][kGroups] = {};
+    int64_t row_s[kSr];
+    auto load_scales = [&](int t, int unit) {                // of stage `unit` of tile t
+        if (unit == begin) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < left)
-                    u[i / 2] |= static_cast<uint32_t>(x[i]) << (16 * (i & 1));
+            for (int i = 0; i < kSr; ++i)
+                row_s[i] = w4_row<R>(p, t, lane + 32 * i) * groups;
         }
-        return make_uint4(u[0], u[1], u[2], u[3]);
-    };
-    int64_t srow[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        srow[i] = w4_row(p, tile, g + 8 * i) * groups;
-
-    uint4 xv[4][NT];
-    uint32_t sv[4][4], zv[4][4];
-    auto load_unit = [&](int unit, int q) {                  // the 32 elements q of a unit
-        const int64_t k = static_cast<int64_t>(unit) * kW4K + q * 32;
+        for (int j = 0; j < kGroups; ++j) {
+            const int at = min(unit * kGroups + j, groups - 1);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-            xv[q][nt] = load_x(k, nt);
-        if ((q & (per - 1)) == per - 1 && unit < units) {    // where a group ends
-            const int gi = min(static_cast<int>(k / p.group), groups - 1);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sv[q][i] = load_raw(p.scales, srow[i] + gi, p.s_f32);
-                if (ZEROS)
-                    zv[q][i] = load_raw(p.zeros, srow[i] + gi, p.s_f32);
+            for (int i = 0; i < kSr; ++i) {
+                raw_s[i][j] = load_raw(p.scales, row_s[i] + at, s_f32);
+                if (zeros)
+                    raw_z[i][j] = load_raw(p.zeros, row_s[i] + at, s_f32);
             }
         }
     };
 
-#pragma unroll
-    for (int s = 0; s < kW4Stages - 1; ++s)
-        produce(first + s * stride, s);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-        load_unit(first, q);
+    for (int s = 0; s < S - 1; ++s)
+        produce();
+    if (begin < units)
+        load_scales(first_tile, begin);
 
-    float tot[2][NT][4], acc[2][NT][4], sx[NT][4];
+    // Rows 0 .. 7 of the constant matrix: what a weight holds too much, without zeros 8 more; 8 .. 15: one.
+    // Pairs 0 and 2 are alike, and 1 and 3.
+    uint32_t much[4], m[4];
+    if constexpr (BF16) {
+        much[0] = zeros ? 0u : 0x00080008u;
+        much[1] = 0x00010001u;
+        much[2] = zeros ? 0u : 0x00800080u;
+        much[3] = 0x00100010u;
+        m[0] = m[1] = m[2] = m[3] = 0u;
+    } else {
+        much[0] = zeros ? 0x5C005C00u : 0x5C205C20u;         // 256, 264
+        much[2] = zeros ? 0x4C004C00u : 0x4E004E00u;         // 16, 24
+        much[1] = much[3] = 0x3C003C00u;
+        m[0] = 0x003C003Cu;
+        m[1] = 0x5C005C00u;
+        m[2] = 0x03C003C0u;
+        m[3] = 0x4C004C00u;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+        for (int i = 0; i < 4; ++i)
+            asm volatile("" : "+r"(m[i]));                   // in registers
+    }
+    const uint32_t from_w = mine + lane * 64 + ((lane >> 1) & 3) * 16;
+    const uint32_t from_x = mine + Cfg::kWBytes + g * kW4XRow + (g & 1) * 64 + c * 16;
+    uint32_t stage = 0;                                      // bytes of the stage to read
+    const int here = min(tokens, kTokens), each = kTokens / cluster;     // cluster: a power of two up to 8
+    const int rows = p.gated ? R / 2 : R;
+    const int64_t feats = p.gated ? p.rows / 2 : p.rows;
+    for (int tile = first_tile; tile < tiles; tile += tile_step) {
+        float tot[MT][NT][4], acc[MT][NT][4], off[NT][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            tot[0][nt][i] = tot[1][nt][i] = 0.0f;
-            acc[0][nt][i] = acc[1][nt][i] = 0.0f;
-            sx[nt][i] = 0.0f;
-        }
-    int stage = 0;
-    for (int unit = first; unit < units; unit += stride) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kW4Stages - 2) : "memory");
-        __syncwarp();                                        // and every lane has read the stage before
-        produce(unit + (kW4Stages - 1) * stride, stage == 0 ? kW4Stages - 1 : stage - 1);
-        const uint8_t *st = mine + stage * kW4StageBytes + g * kW4RowBytes + c * 4;
-        stage = stage + 1 == kW4Stages ? 0 : stage + 1;
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t b[NT][4];
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const uint4 x = xv[q][nt];
-                b[nt][0] = __byte_perm(x.x, x.z, 0x5410);
-                b[nt][1] = __byte_perm(x.x, x.z, 0x7632);
-                b[nt][2] = __byte_perm(x.y, x.w, 0x5410);
-                b[nt][3] = __byte_perm(x.y, x.w, 0x7632);
+                for (int j = 0; j < 4; ++j)
+                    tot[i][nt][j] = 0.0f;
+        for (int unit = begin; unit < units; unit += stride) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+            __syncwarp();                                        // and every lane has read the stage before
+            produce();
+            const uint32_t st = from_w + stage;
+            uint32_t stx[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                stx[nt] = nt * 8 + g < tokens ? from_x + stage + nt * 8 * kW4XRow : smem_u32(nothing);
+            stage = stage + Cfg::kStageBytes == S * Cfg::kStageBytes ? 0u : stage + Cfg::kStageBytes;
+#pragma unroll
+            for (int i = 0; i < kSr; ++i)
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j)
+                    sc[(lane + 32 * i) * kGroups + j] = raw_value<BF16>(raw_s[i][j], s_f32);
+            if (zeros) {
+#pragma unroll
+                for (int i = 0; i < kSr; ++i)
+#pragma unroll
+                    for (int j = 0; j < kGroups; ++j)
+                        sc[(R + lane + 32 * i) * kGroups + j] = raw_value<BF16>(raw_z[i][j], s_f32);
             }
-            const uint32_t one = BF16 ? 0x3F803F80u : 0x3C003C00u;
-            const uint32_t ones[4] = {one, one, one, one};
-            if (ZEROS) {
+            __syncwarp();
+            if (unit + stride < units)
+                load_scales(tile, unit + stride);
+            else if (tile + tile_step < tiles)
+                load_scales(tile + tile_step, begin);
+            uint32_t w[2][2 * MT];                               // rows g + 8 i, of this and the next 32 elements
+            uint4 x[2][NT];
+            auto fetch = [&](int q) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    x[q & 1][nt] = load_shared16(stx[nt] ^ (q * 64));
+#pragma unroll
+                for (int i = 0; i < MT; i += 2)
+                    ldmatrix4((st + i * 1024) ^ (q * 16), &w[q & 1][2 * i]);
+            };
+            fetch(0);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const bool first = q % PER == 0;                 // of its group
+                if (q < 3)
+                    fetch(q + 1);
+                uint32_t b[NT][4];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    mma16816<BF16>(sx[nt], ones, b[nt][0], b[nt][1]);
-                    mma16816<BF16>(sx[nt], ones, b[nt][2], b[nt][3]);
+                    const uint4 v = x[q & 1][nt];
+                    constexpr uint32_t k64 = 0x5F805F80u, k60 = 0x5D805D80u;     // 2^64, 2^60
+                    b[nt][0] = scaled<BF16>(__byte_perm(v.x, v.z, 0x5410), k64);
+                    b[nt][1] = scaled<BF16>(__byte_perm(v.x, v.z, 0x7632), k60);
+                    b[nt][2] = scaled<BF16>(__byte_perm(v.y, v.w, 0x5410), k64);
+                    b[nt][3] = scaled<BF16>(__byte_perm(v.y, v.w, 0x7632), k60);
+                    mma_group<BF16>(first, off[nt], much, b[nt][0], b[nt][1]);
+                    mma_group<BF16>(false, off[nt], much, b[nt][2], b[nt][3]);
                 }
-            }
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                uint32_t lo[4], hi[4];
-                widen<BF16>(*reinterpret_cast<const uint32_t *>(st + (16 * m) * kW4RowBytes + q * 16), lo);
-                widen<BF16>(*reinterpret_cast<const uint32_t *>(st + (16 * m + 8) * kW4RowBytes + q * 16), hi);
-                const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
+                for (int i = 0; i < MT; ++i) {
+                    uint32_t lo[4], hi[4];
+                    widen<BF16>(w[q & 1][2 * i], m, lo);
+                    widen<BF16>(w[q & 1][2 * i + 1], m, hi);
+                    const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma16816<BF16>(acc[m][nt], a0, b[nt][0], b[nt][1]);
-                    mma16816<BF16>(acc[m][nt], a1, b[nt][2], b[nt][3]);
-                }
-            }
-            if ((q & (per - 1)) == per - 1) {                // the group is complete
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const float s0 = raw_value<BF16>(sv[q][2 * m], p.s_f32);
-                    const float s1 = raw_value<BF16>(sv[q][2 * m + 1], p.s_f32);
-                    float z0 = 0.0f, z1 = 0.0f;
-                    if (ZEROS) {
-                        z0 = 8.0f - raw_value<BF16>(zv[q][2 * m], p.s_f32);
-                        z1 = 8.0f - raw_value<BF16>(zv[q][2 * m + 1], p.s_f32);
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_group<BF16>(first, acc[i][nt], a0, b[nt][0], b[nt][1]);
+                        mma_group<BF16>(false, acc[i][nt], a1, b[nt][2], b[nt][3]);
                     }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float v = acc[m][nt][i];
-                            if (ZEROS)
-                                v = fmaf(i < 2 ? z0 : z1, sx[nt][i & 1], v);
-                            tot[m][nt][i] = fmaf(i < 2 ? s0 : s1, v, tot[m][nt][i]);
-                            acc[m][nt][i] = 0.0f;
-                        }
                 }
-                if (ZEROS) {
+                if (q % PER == PER - 1) {                        // the group is complete
+                    const float *at_s = sc + g * kGroups + q / PER;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int i = 0; i < MT; ++i) {
+                        const float s0 = at_s[16 * i * kGroups], s1 = at_s[(16 * i + 8) * kGroups];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            sx[nt][i] = 0.0f;
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                acc[i][nt][j] -= off[nt][j & 1];
+                        if (zeros) {                             // off: 0 for BF16, 256 or 16 times for FP16
+                            const float z0 = at_s[(R + 16 * i) * kGroups], z1 = at_s[(R + 16 * i + 8) * kGroups];
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    acc[i][nt][j] = fmaf(j < 2 ? -z0 : -z1, off[nt][2 + (j & 1)], acc[i][nt][j]);
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                tot[i][nt][j] = fmaf(j < 2 ? s0 : s1, acc[i][nt][j], tot[i][nt][j]);
+                    }
                 }
             }
-            load_unit(unit + stride, q);
+        }
+
+        // The warps' sums, [warp][token][row].  A thread adds those of a token and row over the warps; in a
+        // cluster it sends them to the block that finishes the token: the tokens go round the cluster,
+        // and a block has room for each sender's.
+        __syncthreads();                                         // the last tile is finished,
+        if (cluster > 1)
+            cluster_arrive();                                    // as far as this block goes
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    part[warp * Cfg::kSums + sum_at<R>(nt * 8 + 2 * c + (j & 1), 16 * i + 8 * (j >> 1) + g)] =
+                        BF16 ? tot[i][nt][j] * kBfUnit : tot[i][nt][j];
+        __syncthreads();
+        auto block_sum = [&](int t, int j) {
+            const int at = sum_at<R>(t, j);
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                v += part[w * Cfg::kSums + at];
+            return v;
+        };
+        if (cluster > 1) {
+            cluster_wait();
+            for (int o = threadIdx.x; o < here * R; o += W * 32) {
+                const int t = o / R, j = o % R;
+                store_cluster(mapa_shared(smem_u32(room + (rank * each + t / cluster) * R + j), t % cluster), block_sum(t, j));
+            }
+            cluster_sync_all();
+        }
+        for (int o = threadIdx.x; o < each * rows; o += W * 32) {
+            const int t = o / rows, j = o - t * rows, tt = t * cluster + rank;
+            const int64_t f = static_cast<int64_t>(tile) * rows + j, tok = tok0 + tt;
+            if (tt >= here || f >= feats)
+                continue;
+            float bias = 0.0f, more = 0.0f;                      // on their way during the sums
+            if (p.bias)
+                bias = p.bias_f32 ? static_cast<const float *>(p.bias)[f] : load16(p.bias, f, BF16);
+            if (p.C)
+                more = load_out(p.C, tok * p.ldc + f, p.out_kind);
+            float z = 0.0f, u = 0.0f;
+            if (cluster > 1) {
+                for (int r = 0; r < cluster; ++r) {
+                    z += room[(r * each + t) * R + j];
+                    if (p.gated)
+                        u += room[(r * each + t) * R + j + R / 2];
+                }
+            } else {
+                z = block_sum(t, j);
+                if (p.gated)
+                    u = block_sum(t, j + R / 2);
+            }
+            z = act_of(p.act, z + bias);
+            if (p.gated)
+                z *= u;
+            if (p.C)
+                z = fmaf(p.beta, more, z);
+            store_out(p.D, tok * p.ldd + f, p.out_kind, z);
         }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
-
-    // The warps' sums, [warp][token][row] in the ring, then the block's, [token][row].
-    constexpr int kSums = 8 * NT * kW4Stride;
-    float *part = reinterpret_cast<float *>(ring);
-    float *red = part + kW4Warps * kSums;
-    static_assert((kW4Warps + 1) * kSums * 4 <= kW4RingBytes, "the sums fit the ring");
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                part[warp * kSums + (nt * 8 + 2 * c + (i & 1)) * kW4Stride + 16 * m + 8 * (i >> 1) + g] = tot[m][nt][i];
-    __syncthreads();
-    constexpr int kOuts = 8 * NT * kW4Rows;
-#pragma unroll
-    for (int o = threadIdx.x; o < kOuts; o += kW4Warps * 32) {
-        const int at = o / kW4Rows * kW4Stride + o % kW4Rows;
-        float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kW4Warps; ++w)
-            v += part[w * kSums + at];
-        red[at] = v;
-    }
-    if (cluster > 1)
-        cluster_sync_all();
-    else
-        __syncthreads();
-    if (rank == 0) {
-        auto total = [&](int at) {
-            float v = red[at];
-            for (int r = 1; r < cluster; ++r)
-                v += load_cluster(mapa_shared(smem_u32(red + at), r));
-            return v;
-        };
-        const int rows = p.gated ? kW4Rows / 2 : kW4Rows;
-        const int64_t feats = p.gated ? p.rows / 2 : p.rows;
-        for (int o = threadIdx.x; o < 8 * NT * rows; o += kW4Warps * 32) {
-            const int t = tok0 + o / rows, j = o % rows;
-            const int64_t f = tile * rows + j;
-            if (t >= p.tokens || f >= feats)
-                continue;
-            const int at = o / rows * kW4Stride + j;
-            float z = total(at);
-            if (p.bias)
-                z += p.bias_f32 ? static_cast<const float *>(p.bias)[f] : load16(p.bias, f, BF16);
-            z = act_of(p.act, z);
-            if (p.gated)
-                z *= total(at + kW4Rows / 2);
-            if (p.C)
-                z = fmaf(p.beta, load_out(p.C, t * p.ldc + f, p.out_kind), z);
-            store_out(p.D, t * p.ldd + f, p.out_kind, z);
-        }
-    }
-    if (cluster > 1)
-        cluster_sync_all();                                  // the others' sums have been read
 }
 
-// 32 elements of a row a thread: FP32, rounded once.
+// The weights as the type of x: FP32, rounded once.  Eight elements of a row a thread, so that a warp
+// writes 512 bytes side by side.
 template <bool BF16>
 __global__ void __launch_bounds__(256) tcg_w4_expand_kernel(const W4Args p, uint16_t *out, int64_t ldo)
 {
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t per = (p.k + 31) / 32, total = p.rows * per, groups = (p.k + p.group - 1) / p.group;
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-        const int64_t row = i / per, k = (i - row * per) * 32, g = row * groups + k / p.group;
-        const uint8_t *w = p.W + row * p.ldw + k / 2;
-        const float s = raw_value<BF16>(load_raw(p.scales, g, p.s_f32), p.s_f32);
-        const float z = p.zeros ? raw_value<BF16>(load_raw(p.zeros, g, p.s_f32), p.s_f32) : 8.0f;
-        uint16_t *o = out + row * ldo + k;
-        if (p.k - k >= 32) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(w);
-            const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
+    const int per = static_cast<int>((p.k + 7) / 8), groups = static_cast<int>((p.k + p.group - 1) / p.group);
+    const int shift = p.group == 32 ? 2 : (p.group == 64 ? 3 : 4);       // of a piece to its group
+    for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y)
+        for (int i = blockIdx.x * 256 + threadIdx.x; i < per; i += gridDim.x * 256) {
+            const int64_t g = row * groups + (i >> shift);
+            const float s = raw_value<BF16>(load_raw(p.scales, g, p.s_f32), p.s_f32);
+            const float z = p.zeros ? raw_value<BF16>(load_raw(p.zeros, g, p.s_f32), p.s_f32) : 8.0f;
+            const uint8_t *w = p.W + row * p.ldw + i * 4;
+            uint16_t *o = out + row * ldo + i * 8;
+            const int left = static_cast<int>(p.k) - i * 8;
+            if (left >= 8) {
+                const uint32_t u = *reinterpret_cast<const uint32_t *>(w);
                 uint32_t y[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    y[e] = pack16((static_cast<float>(u[j] >> (8 * e) & 15u) - z) * s,
-                                  (static_cast<float>(u[j] >> (8 * e + 4) & 15u) - z) * s, BF16);
-                reinterpret_cast<uint4 *>(o)[j] = make_uint4(y[0], y[1], y[2], y[3]);
+                    y[e] = pack16((static_cast<float>(u >> (8 * e) & 15u) - z) * s,
+                                  (static_cast<float>(u >> (8 * e + 4) & 15u) - z) * s, BF16);
+                *reinterpret_cast<uint4 *>(o) = make_uint4(y[0], y[1], y[2], y[3]);
+            } else {
+                for (int j = 0; j < left; ++j)
+                    o[j] = round16((static_cast<float>(w[j / 2] >> (4 * (j & 1)) & 15) - z) * s, BF16);
             }
-        } else {
-            for (int j = 0; j < static_cast<int>(p.k - k); ++j)
-                o[j] = round16((static_cast<float>(w[j / 2] >> (4 * (j & 1)) & 15) - z) * s, BF16);
         }
-    }
 }
 
-template <int NT, bool BF16, bool ZEROS>
-cudaError_t launch_nt(const W4Args &a, int cluster, dim3 grid, cudaStream_t s)
+template <int NT, int MT, int XR, int PER, int W, bool BF16>
+cudaError_t launch_one(W4Args a, int num_sms, cudaStream_t s)
 {
-    auto fn = tcg_w4_kernel<NT, BF16, ZEROS>;
-    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kW4RingBytes);
+    using Cfg = W4Cfg<NT, MT, XR, PER, W>;
+    auto fn = tcg_w4_kernel<NT, MT, XR, PER, W, BF16>;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
     if (e != cudaSuccess)
         return e;
+    const int rows = a.gated ? Cfg::kRows / 2 : Cfg::kRows;
+    a.tiles = static_cast<int>(((a.gated ? a.rows / 2 : a.rows) + rows - 1) / rows);
+    a.units = static_cast<int>((a.k + kW4K - 1) / kW4K);
+    a.groups = static_cast<int>((a.k + a.group - 1) / a.group);
+    const int blocks = (a.tokens + 8 * NT - 1) / (8 * NT), most = num_sms / blocks;
+    // As many blocks to a tile as are resident together and leave each warp a stage.
+    int cluster = 1;
+    while (cluster < 8 && a.units > cluster * W && a.tiles * cluster * 2 <= most)
+        cluster *= 2;
+    const int wide = a.tiles < most / cluster ? a.tiles : most / cluster;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kW4Warps * 32);
-    cfg.dynamicSmemBytes = kW4RingBytes;
+    cfg.gridDim = dim3(static_cast<unsigned>(wide * cluster), blocks);
+    cfg.blockDim = dim3(W * 32);
+    cfg.dynamicSmemBytes = Cfg::kSmem;
     cfg.stream = s;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -384,35 +531,34 @@ cudaError_t launch_nt(const W4Args &a, int cluster, dim3 grid, cudaStream_t s)
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int NT>
-cudaError_t launch_types(const W4Args &a, int cluster, dim3 grid, cudaStream_t s)
+template <int NT, int MT, int XR, int W>
+cudaError_t launch_types(const W4Args &a, int num_sms, cudaStream_t s)
 {
     if (a.in_bf16)
-        return a.zeros ? launch_nt<NT, true, true>(a, cluster, grid, s) : launch_nt<NT, true, false>(a, cluster, grid, s);
-    return a.zeros ? launch_nt<NT, false, true>(a, cluster, grid, s) : launch_nt<NT, false, false>(a, cluster, grid, s);
+        return a.group == 32 ? launch_one<NT, MT, XR, 1, W, true>(a, num_sms, s)
+             : a.group == 64 ? launch_one<NT, MT, XR, 2, W, true>(a, num_sms, s)
+                             : launch_one<NT, MT, XR, 4, W, true>(a, num_sms, s);
+    return a.group == 32 ? launch_one<NT, MT, XR, 1, W, false>(a, num_sms, s)
+         : a.group == 64 ? launch_one<NT, MT, XR, 2, W, false>(a, num_sms, s)
+                         : launch_one<NT, MT, XR, 4, W, false>(a, num_sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_w4(const W4Args &a, int num_sms, cudaStream_t s)
 {
-    const int64_t tiles = a.gated ? (a.rows / 2 + kW4Rows / 2 - 1) / (kW4Rows / 2) : (a.rows + kW4Rows - 1) / kW4Rows;
-    const int64_t units = (a.k + kW4K - 1) / kW4K;
-    const int nt = a.tokens <= 8 ? 1 : (a.tokens <= 16 ? 2 : 4);
-    const int blocks = (a.tokens + 8 * nt - 1) / (8 * nt);
-    // As many blocks to a tile as leave each warp a stage, up to two blocks an SM in all.
-    int cluster = 1;
-    while (cluster < 8 && units >= 2 * cluster * kW4Warps && tiles * blocks * cluster * 2 <= 2 * num_sms)
-        cluster *= 2;
-    const dim3 grid(static_cast<unsigned>(tiles * cluster), static_cast<unsigned>(blocks));
-    return nt == 1 ? launch_types<1>(a, cluster, grid, s)
-         : nt == 2 ? launch_types<2>(a, cluster, grid, s) : launch_types<4>(a, cluster, grid, s);
+    if (a.tokens <= 8 && a.rows >= 32 * num_sms)
+        return a.tokens <= 2 ? launch_types<1, 4, 2, 16>(a, num_sms, s) : launch_types<1, 4, 8, 12>(a, num_sms, s);
+    return a.tokens <= 2 ? launch_types<1, 2, 2, 16>(a, num_sms, s)
+         : a.tokens <= 8 ? launch_types<1, 2, 8, 16>(a, num_sms, s)
+         : a.tokens <= 16 ? launch_types<2, 2, 16, 12>(a, num_sms, s) : launch_types<4, 2, 32, 8>(a, num_sms, s);
 }
 
 cudaError_t launch_w4_expand(const W4Args &a, void *out, int64_t ldo, int num_sms, cudaStream_t s)
 {
-    const int64_t blocks = (a.rows * ((a.k + 31) / 32) + 255) / 256, most = static_cast<int64_t>(num_sms) * 8;
-    const dim3 grid(static_cast<unsigned>(blocks < most ? blocks : most));
+    const int64_t across = ((a.k + 7) / 8 + 255) / 256, most = static_cast<int64_t>(num_sms) * 8;
+    const int64_t down = (most + across - 1) / across;
+    const dim3 grid(static_cast<unsigned>(across), static_cast<unsigned>(a.rows < down ? a.rows : down));
     return launch_pdl(a.in_bf16 ? tcg_w4_expand_kernel<true> : tcg_w4_expand_kernel<false>, grid, dim3(256), s, 0, a,
                       static_cast<uint16_t *>(out), ldo);
 }

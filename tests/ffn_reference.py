@@ -96,22 +96,22 @@ def pack(q):
 
 
 def weights_4bit(w, k, scales, zeros, group):
-    """(W, magnitude that its products are summed with)."""
+    """(W, the magnitude that a group's products are summed with: 16 + q of a weight, and 16 and the
+    zero, which are taken away again)."""
     at = torch.arange(k, device=w.device) // group
     q, s = unpack(w, k).double(), scales.double()[:, at]
-    if zeros is None:
-        return (q - 8) * s, ((q - 8) * s).abs()
-    zero = zeros.double()[:, at]
-    return (q - zero) * s, ((q - 8).abs() + (8 - zero).abs()) * s.abs()
+    zero = torch.full_like(q, 8.0) if zeros is None else zeros.double()[:, at]
+    return (q - zero) * s, (32 + q + zero.abs()) * s.abs()
 
 
 def linear_4bit(x, w, scales, zeros, group, bias, name, residual, beta, gated_, out_dtype):
-    """(out, its bound)."""
+    """(out, its bound).  A group's sums of at most `group` terms are within their 2^-23 each of the
+    magnitudes' sum; all groups' results, at most k, are added with the magnitudes of W."""
     t, k = x.shape
     W, mag = weights_4bit(w, k, scales, zeros, group)
     xd = x.double()
     z = xd @ W.t()
-    ez = (k + 8) * 2.0 ** -23 * (xd.abs() @ mag.t())
+    ez = 2.0 ** -23 * ((min(k, group) + 8) * (xd.abs() @ mag.t()) + (k + 8) * (xd.abs() @ W.abs().t()))
     if t > 64:                               # the weights rounded to x's type
         ez = ez + U[x.dtype] * (1 + 2.0 ** -10) * (xd.abs() @ W.abs().t()) + \
             TINY[x.dtype] * xd.abs().sum(1, keepdim=True)

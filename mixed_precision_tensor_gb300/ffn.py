@@ -24,23 +24,19 @@ from .lm import (_IN, _TYPES, _act, _elsewhere, _empty, _epilogue, _hold, _input
 _E4M3 = torch.float8_e4m3fn
 
 
-def _norm_args(handle, what, x, weight, eps, residual, sum_out):
+def _norm_args(x, weight, eps, more, what):
+    """Sizes, type, device, and the leading dimensions of x and of `more`, another matrix like it."""
     t, k, dtype, dev = _input(x)
     _vector(weight, "weight", (k,), (dtype, torch.float32), dev)
     if not eps >= 0.0:
         raise ValueError(f"eps must not be negative, got {eps}")
-    ldx = _rows(x, "x", t, k, dtype, dev)
-    ldr = lds = 8
-    if residual is not None:
-        ldr = _rows(residual, "residual", t, k, dtype, dev)
-    if sum_out is not None:
-        lds = _rows(sum_out, "sum_out", t, k, dtype, dev)
-    return t, k, dtype, dev, ldx, ldr, lds
+    return t, k, dtype, dev, _rows(x, "x", t, k, dtype, dev), \
+        8 if more is None else _rows(more, what, t, k, dtype, dev)
 
 
-def _norm(handle, what, x, weight, eps, residual, sum_out, args, out, out_code, scale):
-    t, k, dtype, dev, ldx, ldr, lds = args
-    ldo = _rows(out, "out", t, k, out.dtype, dev)
+def _norm(handle, what, x, weight, eps, residual, sum_out, args, out, ldo, out_code, scale):
+    t, k, dtype, dev, ldx, ldr = args
+    lds = 8 if sum_out is None else _rows(sum_out, "sum_out", t, k, dtype, dev)
     s = _lib().tcg_rms_norm(
         handle.h, t, k, x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr,
         None if sum_out is None else sum_out.data_ptr(), lds, weight.data_ptr(), _TYPES[weight.dtype], eps,
@@ -59,13 +55,10 @@ def rms_norm(handle, x, weight, eps=1e-6, residual=None, sum_out=None, out=None)
     itself; out is formed from the unrounded s).  out is made if None and may be ``x`` or
     ``residual``, if sum_out is not the same.  k is at most 32768.  Returns out.
     """
-    args = _norm_args(handle, "rms_norm", x, weight, eps, residual, sum_out)
+    args = _norm_args(x, weight, eps, residual, "residual")
     t, k, dtype, dev = args[:4]
-    if out is None:
-        out, _ = _matrix(handle, None, "out", t, k, dtype, dev)
-    elif out.dtype is not dtype:
-        raise ValueError(f"out must be {dtype}, got {out.dtype}")
-    _norm(handle, "rms_norm", x, weight, eps, residual, sum_out, args, out, _IN[dtype], None)
+    out, ldo = _matrix(handle, out, "out", t, k, dtype, dev)
+    _norm(handle, "rms_norm", x, weight, eps, residual, sum_out, args, out, ldo, _IN[dtype], None)
     return out
 
 
@@ -76,17 +69,14 @@ def rms_norm_8bit(handle, x, weight, eps=1e-6, residual=None, sum_out=None, out=
     scale is a row's largest magnitude over 448, at least 2^-100.  The FP8 products of
     :func:`gemm_rowmajor` take out as it is; the scale multiplies their rows.
     """
-    args = _norm_args(handle, "rms_norm_8bit", x, weight, eps, residual, sum_out)
+    args = _norm_args(x, weight, eps, residual, "residual")
     t, k, dtype, dev = args[:4]
-    if out is None:
-        out, _ = _matrix(handle, None, "out", t, k, _E4M3, dev)
-    elif out.dtype is not _E4M3:
-        raise ValueError(f"out must be {_E4M3}, got {out.dtype}")
+    out, ldo = _matrix(handle, out, "out", t, k, _E4M3, dev)
     if scale is None:
         scale = _empty(handle, (t,), torch.float32, dev)
     else:
         _vector(scale, "scale", (t,), (torch.float32,), dev)
-    _norm(handle, "rms_norm_8bit", x, weight, eps, residual, sum_out, args, out, _tcg.TCG_R_8F_E4M3, scale)
+    _norm(handle, "rms_norm_8bit", x, weight, eps, residual, sum_out, args, out, ldo, _tcg.TCG_R_8F_E4M3, scale)
     return out, scale
 
 
@@ -98,7 +88,7 @@ def rms_norm_backward(handle, dout, x, weight, eps=1e-6, dsum=None, want=("dx", 
     (it may be ``dout`` or ``dsum`` itself).  dw: (k,) FP32.  ``want`` names what is computed; None
     for the other.
     """
-    t, k, dtype, dev, ldx, ldds, _ = _norm_args(handle, "rms_norm_backward", x, weight, eps, dsum, None)
+    t, k, dtype, dev, ldx, ldds = _norm_args(x, weight, eps, dsum, "dsum")
     ldd = _rows(dout, "dout", t, k, dtype, dev)
     want_dx, want_dw, bad = _want(want)
     if bad:
@@ -196,8 +186,10 @@ def linear_4bit(handle, x, w, scales, group, zeros=None, bias=None, act="none", 
         q = (v.unflatten(1, (-1, group)) / s[..., None]).round().add(8).clamp(1, 15).flatten(1).byte()
         w = q[:, 0::2] | q[:, 1::2] << 4
 
-    Up to 64 tokens read the packed weights; more expand them in the handle's workspace, rounded
-    to x's type.  Returns out.
+    residual may be ``out`` itself.  Up to 64 tokens read the packed weights; more expand them in
+    the handle's workspace, rounded to x's type.  Up to 64 tokens an infinity in x makes its
+    token's outputs NaN, and BF16 entries of x must be below 2^63 (and above 2^-57, or they lose
+    bits).  Returns out.
     """
     t, k, dtype, dev = _input(x)
     if not isinstance(w, torch.Tensor) or w.dim() != 2:

@@ -132,8 +132,7 @@ def _vector(t, what, shape, dtypes, device):
 
 
 def _epilogue(act, bias, bias_shape, residual, beta, z, rows, n, dtype, out_dtype, device):
-    e = _tcg.Epilogue()
-    e.activation = act
+    e = _tcg.Epilogue(act)
     if bias is not None:
         _vector(bias, "bias", bias_shape, (dtype, torch.float32), device)
         e.bias, e.bias_type = bias.data_ptr(), _TYPES[bias.dtype]

@@ -315,6 +315,30 @@ def test_4bit_keeps_rows_apart(handle, t):
     assert same_bits(got[rest], want[rest])
 
 
+@pytest.mark.parametrize("size", [2.0 ** -50, 2.0 ** -30, 2.0 ** 40, 2.0 ** 60])
+def test_4bit_of_small_and_large_rows(handle, size):
+    """BF16 as far as its range goes, beside a row of ordinary size."""
+    g = gen_of(10)
+    x = randn(g, 3, 520)
+    x[1] = (x[1].float() / 8 * size).to(BF16)
+    w, scales, zeros = draw_4bit(g, 72, 520, 64, BF16, True)
+    out = tcg.linear_4bit(handle, x, w, scales, 64, zeros=zeros, out_dtype=F32)
+    within(out, *ref.linear_4bit(x, w, scales, zeros, 64, None, "none", None, 0.0, False, F32), "out")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_4bit_scales_without_a_number(handle, dtype):
+    """A NaN among the scales or zeros of a row is that row's alone."""
+    g = gen_of(14)
+    x = randn(g, 5, 264, dtype=dtype)
+    w, scales, zeros = draw_4bit(g, 40, 264, 32, dtype, True)
+    want = tcg.linear_4bit(handle, x, w, scales, 32, zeros=zeros)
+    scales[7, 3], zeros[20, 0] = float("nan"), float("nan")
+    got = tcg.linear_4bit(handle, x, w, scales, 32, zeros=zeros)
+    rest = [i for i in range(40) if i not in (7, 20)]
+    assert torch.isnan(got[:, [7, 20]]).all() and same_bits(got[:, rest], want[:, rest])
+
+
 # ---------------------------------------------------------------------------- together
 def test_layer_step(handle):
     """The feed-forward half of a layer forward and backward, as a training step runs it, against
@@ -468,6 +492,24 @@ def test_capture_does_not_grow_the_workspace(cuda_device):
                 refused.append(e.status)
     assert refused == [tcg.TCG_STATUS_ALLOC_FAILED] * 3
     del graph
+    h.close()
+
+
+@pytest.mark.parametrize("t", [1, 20, 500])
+def test_wait_that_runs_out(cuda_device, t):
+    """A load that never comes ends a gated product with an error, and the next call is right."""
+    h = tcg.Handle()
+    s = buffers(t, 520, 264, 6)
+    tcg.gated_linear(h, s["x"], s["w1"], out=s["a"])
+    tcg.check(tcg.tcg_get_device_error(h.h))
+    want = s["a"].clone()
+    tcg.tcg_set_debug(h.h, 2_000_000, 1)
+    tcg.gated_linear(h, s["x"], s["w1"], out=s["a"])
+    assert tcg.tcg_get_device_error(h.h) == tcg.TCG_STATUS_TIMEOUT
+    tcg.tcg_set_debug(h.h)
+    tcg.gated_linear(h, s["x"], s["w1"], out=s["a"])
+    tcg.check(tcg.tcg_get_device_error(h.h))
+    assert same_bits(s["a"], want)
     h.close()
 
 

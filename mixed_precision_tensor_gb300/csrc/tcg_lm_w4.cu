@@ -464,35 +464,49 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
 }
 
 // The weights as the type of x: FP32, rounded once.  Eight elements of a row a thread, so that a warp
-// writes 512 bytes side by side.
+// writes 512 bytes side by side, and kExpandRows rows at a time, their loads before the first store.
+constexpr int kExpandRows = 4;
 template <bool BF16>
-__global__ void __launch_bounds__(256) tcg_w4_expand_kernel(const W4Args p, uint16_t *out, int64_t ldo)
+__global__ void __launch_bounds__(256) tcg_w4_expand_kernel(const W4Args p, uint16_t *__restrict__ out, int64_t ldo)
 {
     griddep_launch_dependents();
     griddep_wait();
-    const int per = static_cast<int>((p.k + 7) / 8), groups = static_cast<int>((p.k + p.group - 1) / p.group);
-    const int shift = p.group == 32 ? 2 : (p.group == 64 ? 3 : 4);       // of a piece to its group
-    for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y)
-        for (int i = blockIdx.x * 256 + threadIdx.x; i < per; i += gridDim.x * 256) {
-            const int64_t g = row * groups + (i >> shift);
-            const float s = raw_value<BF16>(load_raw(p.scales, g, p.s_f32), p.s_f32);
-            const float z = p.zeros ? raw_value<BF16>(load_raw(p.zeros, g, p.s_f32), p.s_f32) : 8.0f;
-            const uint8_t *w = p.W + row * p.ldw + i * 4;
-            uint16_t *o = out + row * ldo + i * 8;
-            const int left = static_cast<int>(p.k) - i * 8;
-            if (left >= 8) {
-                const uint32_t u = *reinterpret_cast<const uint32_t *>(w);
-                uint32_t y[4];
+    const int i = blockIdx.x * 256 + threadIdx.x, k = static_cast<int>(p.k), left = k - i * 8;
+    if (left <= 0)
+        return;
+    const int groups = (k + p.group - 1) / p.group;
+    const int g = i >> (p.group == 32 ? 2 : (p.group == 64 ? 3 : 4));
+    for (int64_t row0 = static_cast<int64_t>(blockIdx.y) * kExpandRows; row0 < p.rows;
+         row0 += static_cast<int64_t>(gridDim.y) * kExpandRows) {
+        uint32_t u[kExpandRows], s[kExpandRows], z[kExpandRows];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    y[e] = pack16((static_cast<float>(u >> (8 * e) & 15u) - z) * s,
-                                  (static_cast<float>(u >> (8 * e + 4) & 15u) - z) * s, BF16);
-                *reinterpret_cast<uint4 *>(o) = make_uint4(y[0], y[1], y[2], y[3]);
+        for (int r = 0; r < kExpandRows; ++r) {
+            const int64_t row = row0 + r < p.rows ? row0 + r : p.rows - 1;
+            const uint8_t *w = p.W + row * p.ldw + i * 4;
+            u[r] = 0u;
+            if (left >= 7) {                                 // four bytes of the row
+                u[r] = *reinterpret_cast<const uint32_t *>(w);
             } else {
-                for (int j = 0; j < left; ++j)
-                    o[j] = round16((static_cast<float>(w[j / 2] >> (4 * (j & 1)) & 15) - z) * s, BF16);
+                for (int j = 0; 2 * j < left; ++j)
+                    u[r] |= static_cast<uint32_t>(w[j]) << (8 * j);
             }
+            s[r] = load_raw(p.scales, row * groups + g, p.s_f32);
+            z[r] = p.zeros ? load_raw(p.zeros, row * groups + g, p.s_f32) : 0u;
         }
+#pragma unroll
+        for (int r = 0; r < kExpandRows; ++r) {
+            if (row0 + r >= p.rows)
+                break;
+            const float f = raw_value<BF16>(s[r], p.s_f32), zero = p.zeros ? raw_value<BF16>(z[r], p.s_f32) : 8.0f;
+            uint16_t *o = out + (row0 + r) * ldo + i * 8;
+            uint32_t y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                y[e] = pack16((static_cast<float>(u[r] >> (8 * e) & 15u) - zero) * f,
+                              (static_cast<float>(u[r] >> (8 * e + 4) & 15u) - zero) * f, BF16);
+            *reinterpret_cast<uint4 *>(o) = make_uint4(y[0], y[1], y[2], y[3]);   // ldo: a multiple of 8
+        }
+    }
 }
 
 template <int NT, int MT, int XR, int PER, int W, bool BF16>
@@ -557,8 +571,8 @@ cudaError_t launch_w4(const W4Args &a, int num_sms, cudaStream_t s)
 cudaError_t launch_w4_expand(const W4Args &a, void *out, int64_t ldo, int num_sms, cudaStream_t s)
 {
     const int64_t across = ((a.k + 7) / 8 + 255) / 256, most = static_cast<int64_t>(num_sms) * 8;
-    const int64_t down = (most + across - 1) / across;
-    const dim3 grid(static_cast<unsigned>(across), static_cast<unsigned>(a.rows < down ? a.rows : down));
+    const int64_t down = (most + across - 1) / across, need = (a.rows + kExpandRows - 1) / kExpandRows;
+    const dim3 grid(static_cast<unsigned>(across), static_cast<unsigned>(need < down ? need : down));
     return launch_pdl(a.in_bf16 ? tcg_w4_expand_kernel<true> : tcg_w4_expand_kernel<false>, grid, dim3(256), s, 0, a,
                       static_cast<uint16_t *>(out), ldo);
 }

@@ -159,6 +159,21 @@ __device__ __forceinline__ int sum_at(int token, int row)
 // Bytes of a 16-byte piece that exist, `left` being those from its start on.
 __device__ __forceinline__ int piece_bytes(int left) { return max(0, min(left, 16)); }
 
+// N words side by side, aligned to their size.
+template <int N>
+__device__ __forceinline__ void load_words(const uint32_t *p, uint32_t *v)
+{
+    if constexpr (N == 4) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(p);
+        v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+    } else if constexpr (N == 2) {
+        const uint2 q = *reinterpret_cast<const uint2 *>(p);
+        v[0] = q.x, v[1] = q.y;
+    } else {
+        v[0] = *p;
+    }
+}
+
 __device__ __forceinline__ void store_cluster(uint32_t addr, float v)
 {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
@@ -241,10 +256,34 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
         sp = sp + Cfg::kStageBytes == S * Cfg::kStageBytes ? 0u : sp + Cfg::kStageBytes;
     };
 
-    // The scales and zeros of rows lane and lane + 32 come a stage ahead through registers.
+    // The scales and zeros of rows lane and lane + 32 come a stage ahead through registers: a stage's
+    // in one load each where rows of them allow it (joined: two 16-bit ones to a register).
     constexpr int kSr = R / 32;
+    const int s_bytes = (s_f32 ? 4 : 2) * kGroups;
+    const bool joined = groups % kGroups == 0 && reinterpret_cast<uintptr_t>(p.scales) % s_bytes == 0 &&
+                        reinterpret_cast<uintptr_t>(p.zeros) % s_bytes == 0;
     uint32_t raw_s[kSr][kGroups] = {}, raw_z[kSr][kGroups] = {};
     int64_t row_s[kSr];
+    auto load_group = [&](const void *base, int64_t row, int unit, uint32_t (&v)[kGroups]) {
+        if (joined) {
+            const int64_t at = row + unit * kGroups;
+            if (s_f32)
+                load_words<kGroups>(static_cast<const uint32_t *>(base) + at, v);
+            else if constexpr (kGroups > 1)
+                load_words<kGroups / 2>(reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(base) + at), v);
+            else
+                v[0] = static_cast<const uint16_t *>(base)[at];
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j)
+            v[j] = load_raw(base, row + min(unit * kGroups + j, groups - 1), s_f32);
+    };
+    auto group_value = [&](const uint32_t (&v)[kGroups], int j) {
+        if (kGroups > 1 && joined && !s_f32)
+            return raw_value<BF16>(v[j / 2] >> (16 * (j & 1)) & 0xFFFFu, false);
+        return raw_value<BF16>(v[j], s_f32);
+    };
     auto load_scales = [&](int t, int unit) {                // of stage `unit` of tile t
         if (unit == begin) {
 #pragma unroll
@@ -252,14 +291,10 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
                 row_s[i] = w4_row<R>(p, t, lane + 32 * i) * groups;
         }
 #pragma unroll
-        for (int j = 0; j < kGroups; ++j) {
-            const int at = min(unit * kGroups + j, groups - 1);
-#pragma unroll
-            for (int i = 0; i < kSr; ++i) {
-                raw_s[i][j] = load_raw(p.scales, row_s[i] + at, s_f32);
-                if (zeros)
-                    raw_z[i][j] = load_raw(p.zeros, row_s[i] + at, s_f32);
-            }
+        for (int i = 0; i < kSr; ++i) {
+            load_group(p.scales, row_s[i], unit, raw_s[i]);
+            if (zeros)
+                load_group(p.zeros, row_s[i], unit, raw_z[i]);
         }
     };
 
@@ -295,7 +330,22 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
     const int here = min(tokens, kTokens), each = kTokens / cluster;     // cluster: a power of two up to 8
     const int rows = p.gated ? R / 2 : R;
     const int64_t feats = p.gated ? p.rows / 2 : p.rows;
+    // Bias and residual of an output; those of a thread's first one are loaded before the tile's stages.
+    auto extras = [&](int tile, int o, float &bias, float &more) {
+        const int t = o / rows, j = o - t * rows, tt = t * cluster + rank;
+        const int64_t f = static_cast<int64_t>(tile) * rows + j;
+        bias = more = 0.0f;
+        if (o >= each * rows || tt >= here || f >= feats)
+            return false;
+        if (p.bias)
+            bias = p.bias_f32 ? static_cast<const float *>(p.bias)[f] : load16(p.bias, f, BF16);
+        if (p.C)
+            more = load_out(p.C, (tok0 + tt) * p.ldc + f, p.out_kind);
+        return true;
+    };
     for (int tile = first_tile; tile < tiles; tile += tile_step) {
+        float bias, more;
+        bool wanted = extras(tile, threadIdx.x, bias, more);
         float tot[MT][NT][4], acc[MT][NT][4], off[NT][4];
 #pragma unroll
         for (int i = 0; i < MT; ++i)
@@ -318,13 +368,13 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
             for (int i = 0; i < kSr; ++i)
 #pragma unroll
                 for (int j = 0; j < kGroups; ++j)
-                    sc[(lane + 32 * i) * kGroups + j] = raw_value<BF16>(raw_s[i][j], s_f32);
+                    sc[(lane + 32 * i) * kGroups + j] = group_value(raw_s[i], j);
             if (zeros) {
 #pragma unroll
                 for (int i = 0; i < kSr; ++i)
 #pragma unroll
                     for (int j = 0; j < kGroups; ++j)
-                        sc[(R + lane + 32 * i) * kGroups + j] = raw_value<BF16>(raw_z[i][j], s_f32);
+                        sc[(R + lane + 32 * i) * kGroups + j] = group_value(raw_z[i], j);
             }
             __syncwarp();
             if (unit + stride < units)
@@ -431,15 +481,12 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
             cluster_sync_all();
         }
         for (int o = threadIdx.x; o < each * rows; o += W * 32) {
-            const int t = o / rows, j = o - t * rows, tt = t * cluster + rank;
-            const int64_t f = static_cast<int64_t>(tile) * rows + j, tok = tok0 + tt;
-            if (tt >= here || f >= feats)
+            if (o >= W * 32)
+                wanted = extras(tile, o, bias, more);
+            if (!wanted)
                 continue;
-            float bias = 0.0f, more = 0.0f;                      // on their way during the sums
-            if (p.bias)
-                bias = p.bias_f32 ? static_cast<const float *>(p.bias)[f] : load16(p.bias, f, BF16);
-            if (p.C)
-                more = load_out(p.C, tok * p.ldc + f, p.out_kind);
+            const int t = o / rows, j = o - t * rows;
+            const int64_t f = static_cast<int64_t>(tile) * rows + j, tok = tok0 + t * cluster + rank;
             float z = 0.0f, u = 0.0f;
             if (cluster > 1) {
                 for (int r = 0; r < cluster; ++r) {
@@ -500,10 +547,11 @@ __global__ void __launch_bounds__(256) tcg_w4_expand_kernel(const W4Args p, uint
             const float f = raw_value<BF16>(s[r], p.s_f32), zero = p.zeros ? raw_value<BF16>(z[r], p.s_f32) : 8.0f;
             uint16_t *o = out + (row0 + r) * ldo + i * 8;
             uint32_t y[4];
+            // a nibble under the exponent of 2^23 is 2^23 + q (conversions of integers are slower)
+            auto value = [&](uint32_t q) { return (__uint_as_float(q & 15u | 0x4B000000u) - 8388608.0f - zero) * f; };
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                y[e] = pack16((static_cast<float>(u[r] >> (8 * e) & 15u) - zero) * f,
-                              (static_cast<float>(u[r] >> (8 * e + 4) & 15u) - zero) * f, BF16);
+                y[e] = pack16(value(u[r] >> (8 * e)), value(u[r] >> (8 * e + 4)), BF16);
             *reinterpret_cast<uint4 *>(o) = make_uint4(y[0], y[1], y[2], y[3]);   // ldo: a multiple of 8
         }
     }

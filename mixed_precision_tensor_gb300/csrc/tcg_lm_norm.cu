@@ -27,8 +27,9 @@ namespace {
 constexpr float kE4m3Max = 448.0f;
 constexpr float kMinScale = 7.888609052210118e-31f;   // 2^-100
 
-// A row's threads hold 16 columns each (8 where a warp is enough for them, 32 beyond 16384); a block
-// of 256 has as many rows at a time as fit.
+// A row's threads hold 16 columns each (8 up to 256 columns, 32 beyond 16384): a warp, eight rows to a
+// block, for up to 512 columns, a block for more.
+constexpr int kNormRows = 8;
 struct NormShape {
     int v, threads, rows;                       // pieces a thread, threads a row, rows of a block
 };
@@ -38,7 +39,7 @@ NormShape norm_shape(int64_t k)
     const int64_t pieces = (k + 7) / 8;
     const int v = pieces <= 32 ? 1 : (pieces <= 2048 ? 2 : 4);
     const int threads = static_cast<int>((pieces + 32 * v - 1) / (32 * v) * 32);
-    return {v, threads, threads < 256 ? 256 / threads : 1};
+    return {v, threads, threads == 32 ? kNormRows : 1};
 }
 
 // Eight elements of a row, those from `left` on zero.
@@ -114,20 +115,10 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return m;
 }
 
-// A row's threads: `size` of them (whole warps, in a block's `row`-th place); this thread is the t-th.
-struct RowThreads {
-    int size, row, t;
-};
-__device__ __forceinline__ RowThreads row_of(int size)
-{
-    const int row = static_cast<int>(threadIdx.x) / size;
-    return RowThreads{size, row, static_cast<int>(threadIdx.x) - row * size};
-}
-
-// Sums of a, and sums or maxima of b, over a row's threads.  `room` alternates from row to row,
+// Sums of a, and sums or maxima of b, over a row's threads (a block, or a warp).  `room` alternates from row to row,
 // so that one barrier a row is enough.
-template <bool MAX_B>
-__device__ __forceinline__ void join_row(float2 (*part)[32], int room, const RowThreads &th, float &a, float &b)
+template <bool MAX_B, bool ONE>
+__device__ __forceinline__ void join_row(float2 (*part)[32], int room, float &a, float &b)
 {
     auto both = [&](float oa, float ob) {
         a += oa;
@@ -136,12 +127,12 @@ __device__ __forceinline__ void join_row(float2 (*part)[32], int room, const Row
 #pragma unroll
     for (int d = 16; d; d >>= 1)
         both(__shfl_xor_sync(0xffffffffu, a, d), __shfl_xor_sync(0xffffffffu, b, d));
-    if (th.size > 32) {
-        const int lane = threadIdx.x & 31, warps = th.size >> 5;
+    if constexpr (ONE) {
+        const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
         if (lane == 0)
             part[room][threadIdx.x >> 5] = make_float2(a, b);
-        named_barrier_sync(1 + th.row, th.size);
-        const float2 p = lane < warps ? part[room][th.row * warps + lane] : make_float2(0.0f, 0.0f);
+        __syncthreads();
+        const float2 p = lane < warps ? part[room][lane] : make_float2(0.0f, 0.0f);
         a = p.x;
         b = p.y;
 #pragma unroll
@@ -150,17 +141,17 @@ __device__ __forceinline__ void join_row(float2 (*part)[32], int room, const Row
     }
 }
 
-// RES: with a residual.  Without one a thread has the next row on its way while it finishes a row (16384
+// ONE: a row has the block to itself.  RES: with a residual.  Without one a thread has the next row on its way while it finishes a row (16384
 // x 4096: 54 us without that); with one a row is enough to keep memory busy, and two take registers
 // that hold blocks.
-template <int V, bool BF16, bool OUT8, bool RES>
-__global__ void __launch_bounds__(1024) tcg_norm_kernel(const NormArgs p, int row_threads)
+template <int V, bool BF16, bool OUT8, bool RES, bool ONE>
+__global__ void __launch_bounds__(1024) tcg_norm_kernel(const NormArgs p)
 {
     __shared__ float2 part[2][32];
     griddep_launch_dependents();
     griddep_wait();
-    const RowThreads th = row_of(row_threads);
-    const int t = th.t, per_row = th.size, at_once = blockDim.x / th.size;
+    const int t = ONE ? threadIdx.x : threadIdx.x & 31, per_row = ONE ? blockDim.x : 32;
+    const int at_once = ONE ? 1 : kNormRows, mine_of = ONE ? 0 : threadIdx.x >> 5;
     const int64_t step = static_cast<int64_t>(gridDim.x) * at_once;
     const float inv_k = 1.0f / static_cast<float>(p.k);
     uint4 vx[V], vr[V], next[V];
@@ -171,7 +162,7 @@ __global__ void __launch_bounds__(1024) tcg_norm_kernel(const NormArgs p, int ro
             v[i] = load_piece(static_cast<const uint16_t *>(base) + row * ld + c, p.k - c);
         }
     };
-    int64_t row = static_cast<int64_t>(blockIdx.x) * at_once + th.row;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * at_once + mine_of;
     if (!RES && row < p.rows)
         load(p.X, p.ldx, row, next);
     int room = 0;
@@ -215,7 +206,7 @@ __global__ void __launch_bounds__(1024) tcg_norm_kernel(const NormArgs p, int ro
             if (p.S)
                 store_piece<BF16>(static_cast<uint16_t *>(p.S) + row * p.lds + c, p.k - c, s);
         }
-        join_row<true>(part, room, th, ss, top);
+        join_row<true, ONE>(part, room, ss, top);
         const float r = rsqrtf(fmaf(ss, inv_k, p.eps));
         float inv = 1.0f;
         if (OUT8) {
@@ -250,15 +241,14 @@ __global__ void __launch_bounds__(1024) tcg_norm_kernel(const NormArgs p, int ro
 constexpr int kFewThreads = 256;
 template <int V, bool BF16, bool ONE, bool FEW>
 __global__ void __launch_bounds__(FEW ? kFewThreads : 1024, FEW ? 3 : 1)
-    tcg_norm_backward_kernel(const NormBackwardArgs p, int row_threads)
+    tcg_norm_backward_kernel(const NormBackwardArgs p)
 {
     extern __shared__ float rows_dw[];          // at the end: dw of each of the block's rows' threads
     __shared__ float2 part[2][32];
     griddep_launch_dependents();
     griddep_wait();
-    const RowThreads th = ONE ? RowThreads{static_cast<int>(blockDim.x), 0, static_cast<int>(threadIdx.x)}
-                              : row_of(row_threads);
-    const int t = ONE ? threadIdx.x : th.t, per_row = ONE ? blockDim.x : th.size, at_once = ONE ? 1 : blockDim.x / th.size;
+    const int t = ONE ? threadIdx.x : threadIdx.x & 31, per_row = ONE ? blockDim.x : 32;
+    const int at_once = ONE ? 1 : kNormRows, mine_of = ONE ? 0 : threadIdx.x >> 5;
     const int64_t step = static_cast<int64_t>(gridDim.x) * at_once;
     const float inv_k = 1.0f / static_cast<float>(p.k);
     float dw[V][8];
@@ -268,7 +258,7 @@ __global__ void __launch_bounds__(FEW ? kFewThreads : 1024, FEW ? 3 : 1)
         for (int j = 0; j < 8; ++j)
             dw[i][j] = 0.0f;
     int room = 0;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * at_once + th.row; row < p.rows; row += step, room ^= 1) {
+    for (int64_t row = static_cast<int64_t>(blockIdx.x) * at_once + mine_of; row < p.rows; row += step, room ^= 1) {
         uint4 vx[V], vd[V], vs[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -292,7 +282,7 @@ __global__ void __launch_bounds__(FEW ? kFewThreads : 1024, FEW ? 3 : 1)
                 dot = fmaf(d[j] * w[j], x[j], dot);
             }
         }
-        join_row<false>(part, room, th, ss, dot);
+        join_row<false, ONE>(part, room, ss, dot);
         const float r = rsqrtf(fmaf(ss, inv_k, p.eps));
         const float m = r * r * (dot * inv_k);
 #pragma unroll
@@ -324,7 +314,7 @@ __global__ void __launch_bounds__(FEW ? kFewThreads : 1024, FEW ? 3 : 1)
     }
     if (!p.part)
         return;
-    float *out = p.part + static_cast<int64_t>(blockIdx.x) * p.k, *mine = at_once > 1 ? rows_dw + th.row * p.k : out;
+    float *out = p.part + static_cast<int64_t>(blockIdx.x) * p.k, *mine = at_once > 1 ? rows_dw + mine_of * p.k : out;
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
@@ -367,18 +357,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     }
 }
 
-template <int V, bool OUT8>
+template <int V, bool OUT8, bool ONE>
 cudaError_t norm_o(const NormArgs &a, const NormShape &n, int grid, cudaStream_t s)
 {
-    auto fn = a.R ? (a.in_bf16 ? tcg_norm_kernel<V, true, OUT8, true> : tcg_norm_kernel<V, false, OUT8, true>)
-                  : (a.in_bf16 ? tcg_norm_kernel<V, true, OUT8, false> : tcg_norm_kernel<V, false, OUT8, false>);
-    return launch_pdl(fn, dim3(grid), dim3(n.threads * n.rows), s, 0, a, n.threads);
+    auto fn = a.R ? (a.in_bf16 ? tcg_norm_kernel<V, true, OUT8, true, ONE> : tcg_norm_kernel<V, false, OUT8, true, ONE>)
+                  : (a.in_bf16 ? tcg_norm_kernel<V, true, OUT8, false, ONE> : tcg_norm_kernel<V, false, OUT8, false, ONE>);
+    return launch_pdl(fn, dim3(grid), dim3(n.threads * n.rows), s, 0, a);
 }
 
-template <int V>
+template <int V, bool ONE>
 cudaError_t norm_v(const NormArgs &a, const NormShape &n, int grid, cudaStream_t s)
 {
-    return a.out8 ? norm_o<V, true>(a, n, grid, s) : norm_o<V, false>(a, n, grid, s);
+    return a.out8 ? norm_o<V, true, ONE>(a, n, grid, s) : norm_o<V, false, ONE>(a, n, grid, s);
 }
 
 template <int V, bool ONE, bool FEW>
@@ -386,7 +376,7 @@ cudaError_t norm_backward_v(const NormBackwardArgs &a, const NormShape &n, int g
 {
     const size_t smem = a.part && !ONE ? n.rows * a.k * sizeof(float) : 0;            // at most 16 KiB
     return launch_pdl(a.in_bf16 ? tcg_norm_backward_kernel<V, true, ONE, FEW> : tcg_norm_backward_kernel<V, false, ONE, FEW>,
-                      dim3(grid), dim3(n.threads * n.rows), s, smem, a, n.threads);
+                      dim3(grid), dim3(n.threads * n.rows), s, smem, a);
 }
 
 // Blocks that are resident with `threads` an SM.
@@ -403,7 +393,9 @@ cudaError_t launch_norm(const NormArgs &a, int num_sms, cudaStream_t s)
 {
     const NormShape n = norm_shape(a.k);
     const int grid = norm_grid(n, a.rows, num_sms, 1024);        // of 64 registers
-    return n.v == 1 ? norm_v<1>(a, n, grid, s) : n.v == 2 ? norm_v<2>(a, n, grid, s) : norm_v<4>(a, n, grid, s);
+    return n.v == 1 ? norm_v<1, false>(a, n, grid, s)
+         : n.v == 4 ? norm_v<4, true>(a, n, grid, s)
+         : n.rows > 1 ? norm_v<2, false>(a, n, grid, s) : norm_v<2, true>(a, n, grid, s);
 }
 
 int norm_backward_blocks(int64_t rows, int64_t k, int num_sms)

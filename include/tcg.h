@@ -616,12 +616,12 @@ tcgStatus_t tcg_rms_norm_backward_workspace_size(tcgHandle_t h, int64_t rows, in
  * B is k x n (n tokens of k features).  gated = 0: D = act(w B + bias) + beta * C as in
  * tcg_gemm_epilogue (epilogue->Z must be NULL).  gated = 1: D = act(w_g B) * (w_u B) with the rows
  * 0 .. m - 1 and m .. 2 m - 1, only the epilogue's activation being used; bias and C are not
- * supported.  Up to 64 tokens the packed weights are read as they are and q - zero meets the scale
- * in FP32; more tokens take the weights rounded to Btype, expanded in the workspace (its size from
- * the second call).  Up to 64 tokens a weight enters its product as q and loses its zero times the
- * group's sum of x afterwards, so an infinity in B makes its column of D NaN; BF16 entries of B are
- * multiplied by 2^64 on the way: from 2^63 on they overflow, below 2^-57 sums lose bits (zero at
- * 2^-80). */
+ * supported.  Few tokens (up to 32, 64 of at most 2^24 weights, 128 of at most 2^21) read the packed
+ * weights: q - zero meets the scale in FP32.  More take the weights rounded to Btype, expanded in the
+ * workspace (its size from the second call).  In the first case a weight enters its product as q and
+ * loses its zero times the group's sum of x afterwards, so an infinity in B makes its column of D
+ * NaN; and BF16 entries of B are multiplied by 2^64 on the way: from 2^63 on they overflow, below
+ * 2^-57 sums lose bits (zero at 2^-80). */
 tcgStatus_t tcg_gemm_4bit(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int64_t group, const void *A,
                           int64_t lda, const void *scales, const void *zeros, tcgDataType_t Stype, const void *B,
                           int64_t ldb, tcgDataType_t Btype, void *D, tcgDataType_t Dtype, int64_t ldd, int gated,

@@ -232,9 +232,8 @@ struct NormBackwardArgs {
 int norm_backward_blocks(int64_t rows, int64_t k, int num_sms);
 cudaError_t launch_norm_backward(NormBackwardArgs a, float *dw, int num_sms, cudaStream_t s);
 
-// Products with 4-bit weights (tcg_lm_w4.cu), up to kW4Tokens tokens, row-major: element 2 j of a row in the low half of
+// Products with 4-bit weights of a few tokens (tcg_lm_w4.cu), row-major: element 2 j of a row in the low half of
 // byte j; w = (q - zero) scale per group of `group` elements of a row.
-constexpr int kW4Tokens = 64;
 struct W4Args {
     int64_t rows;              // of W: the features, or twice those of a gated product
     int64_t k;

@@ -763,6 +763,19 @@ tcgStatus_t check_norm(int64_t rows, int64_t k, const void *W, tcgDataType_t w_t
 bool bad_rows(const void *p, int64_t ld, int64_t cols, int es) { return !aligned16(p) || bad_ld(ld, cols, es); }
 
 // --------------------------------------------------------------------- 4-bit weights
+// Whether the packed weights are read as they are, once for every 32 tokens, or expanded to 16 bits
+// for the product of many tokens (us in a graph, as they are / expanded):
+//                 tokens   32            64            128
+//    1024 x  1024          6.4 / 10.2    6.4 / 13.2    6.5 / 14.2
+//    4096 x  4096         12.3 / 20.9   22.5 / 23.4   43.0 / 34.2
+//   16384 x  4096         51.3 / 60.0   86.2 / 63.9
+//    4096 x 16384         40.7 / 59.4   74.0 / 63.7
+bool w4_packed(int64_t tokens, int64_t rows, int64_t k)
+{
+    return tokens <= 32 || (tokens <= 64 && rows * k <= (int64_t(1) << 24)) ||
+           (tokens <= 128 && rows * k <= (int64_t(1) << 21));
+}
+
 size_t w4_expand_bytes(int64_t rows, int64_t k) { return pad256(static_cast<size_t>(rows) * ((k + 7) / 8 * 8) * 2); }
 
 Product w4_product(const W4Args &a, tcgDataType_t in, tcgDataType_t out)
@@ -1569,7 +1582,7 @@ tcgStatus_t tcg_gemm_4bit(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int64_
     a.beta = epi.beta;
     a.act = epi.activation;
     a.gated = gated != 0;
-    if (n <= kW4Tokens) {
+    if (w4_packed(n, a.rows, k)) {
         const cudaError_t e = launch_w4(a, h->num_sms, h->stream);
         h->launches += 1;
         if (e != cudaSuccess) {
@@ -1611,7 +1624,7 @@ tcgStatus_t tcg_gemm_4bit_workspace_size(tcgHandle_t h, int64_t m, int64_t n, in
     if (2 * m > kMaxExtent || n > kMaxExtent || k > kMaxK)
         return TCG_STATUS_NOT_SUPPORTED;
     *bytes = 0;
-    if (m == 0 || n <= kW4Tokens)
+    if (m == 0 || n == 0 || w4_packed(n, gated ? 2 * m : m, k))
         return TCG_STATUS_SUCCESS;
     const tcgStatus_t st = bind_device(h);
     if (st != TCG_STATUS_SUCCESS)

@@ -7,7 +7,7 @@ the residual stream, gated projections, and projections with 4-bit weights (incl
 
 Tensors, streams and the workspace are as in the module ``lm``: row-major FP16 or BF16 matrices, a
 row a token, unit stride along the features, rows any multiple of 16 bytes apart.  The workspace
-holds dz in :func:`gated_linear_backward` and, beyond 64 tokens, the expanded weights of
+holds dz in :func:`gated_linear_backward` and, for many tokens, the expanded weights of
 :func:`linear_4bit`; its sizes are ``tcg_gemm_gated_workspace_size``,
 ``tcg_gated_backward_workspace_size``, ``tcg_rms_norm_backward_workspace_size`` and
 ``tcg_gemm_4bit_workspace_size``.
@@ -186,10 +186,10 @@ def linear_4bit(handle, x, w, scales, group, zeros=None, bias=None, act="none", 
         q = (v.unflatten(1, (-1, group)) / s[..., None]).round().add(8).clamp(1, 15).flatten(1).byte()
         w = q[:, 0::2] | q[:, 1::2] << 4
 
-    residual may be ``out`` itself.  Up to 64 tokens read the packed weights; more expand them in
-    the handle's workspace, rounded to x's type.  Up to 64 tokens an infinity in x makes its
-    token's outputs NaN, and BF16 entries of x must be below 2^63 (and above 2^-57, or they lose
-    bits).  Returns out.
+    residual may be ``out`` itself.  Few tokens (up to 32, 64 of at most 2^24 weights, 128 of at
+    most 2^21) read the packed weights; an infinity in x then makes its token's outputs NaN, and
+    BF16 entries of x must be below 2^63 (and above 2^-57, or they lose bits).  More tokens expand
+    the weights in the handle's workspace, rounded to x's type.  Returns out.
     """
     t, k, dtype, dev = _input(x)
     if not isinstance(w, torch.Tensor) or w.dim() != 2:

@@ -20,6 +20,8 @@
 //   kEpiXentGrad   dloss (exp(logit - lse) - [target]), scaled, rounded to 16 bits
 //   kEpiGatedNarrow, kEpiGatedWide   act(g) u, both products in one tile: the operands' bytes and
 //                  the tensor work of one product with twice the features, without its output
+//                  (16384 tokens, 4096 to 2 x 4096, both halves kept: 572 to 591 us in a graph, 1.86 to
+//                  1.92 PFLOP/s)
 //
 // What bounds it.  A 64-element block of K costs an SM 32 KiB of operands at tile 256 x 256,
 // loaded at 64 bytes a cycle in the 512 cycles that the tensor core takes for it; with both
@@ -1688,6 +1690,7 @@ __global__ void __launch_bounds__(256)
 // dZ = [dD u act'(g) | dD act(g)], a row of Z = [g | u] a token, n features each.  Bound by memory:
 // 8 features of a token a thread, dD, g and u read once and dZ written once, 16 bytes at a time.
 // Where n is no multiple of 8 the second halves of the rows are not aligned and go by elements.
+// 4864 x 4096: 30 us, 202 MB.
 template <int ACT, bool BF16>
 __global__ void __launch_bounds__(256)
     tcg_gate_backward_kernel(int64_t tokens, int64_t n, const uint16_t *__restrict__ dD, int64_t lddd,

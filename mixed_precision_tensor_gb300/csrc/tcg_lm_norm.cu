@@ -14,7 +14,8 @@
 //
 // Bound by memory: every element is read once and written once, 16 bytes a thread.  A row's
 // elements stay in registers as they were read (V pieces of eight a thread); s, its square and y
-// are formed in FP32 from them.
+// are formed in FP32 from them.  16384 x 4096 in a graph: 81 us with a residual kept (6.6 TB/s, 98% of
+// the copy rate), 76 in 8 bits (6.1), 44 without a residual (6.0); backward 105 (5.1), dx alone 93.
 
 #include <cuda_fp8.h>
 

@@ -2,19 +2,24 @@
 //
 //   z[t][f] = sum over groups of s[f][g] (sum over k of g of (q[f][k] - zero[f][g]) x[t][k])
 //
-// Bound by memory: half a byte a weight for 2 T operations.  Turning a weight into a number costs
-// more instructions than multiplying it, so a warp does that once for eight tokens or more: the
-// weights are the A operand of mma.m16n8k16, the tokens its eight columns (tcgen05 would want the
-// weights back in shared memory first, and 128 rows of them).  A nibble becomes a number by a mask
-// (see widen); what it is too much, 8 or the zero times the group's sum of x, comes from one more
-// product with a constant matrix for all rows, and is taken away in FP32 when the group is complete
-// and meets its scale.  Sums are FP32.
+// Half a byte a weight for 2 T operations.  Turning a weight into a number costs more instructions
+// than multiplying it, so a warp does that once for eight tokens or more: the weights are the A
+// operand of mma.m16n8k16, the tokens its eight columns (tcgen05 would want the weights back in
+// shared memory first, and 128 rows of them).  A nibble becomes a number by a mask (see widen); what
+// it is too much, 8 or the zero times the group's sum of x, comes from one more product with a
+// constant matrix for all rows, and is taken away in FP32 when the group is complete and meets its
+// scale.  Sums are FP32.
 //
-// A warp has 64 rows (32 for 9 to 16 tokens) and streams them 128 elements at a time through a ring
-// of its own (asynchronous 16-byte copies, x beside the weights).  Its
-// lane c of a quad takes elements 8 c .. 8 c + 7 of each 32: in a word elements j and j + 4 are 16
-// bits apart, so one mask gives the pair (j, j + 4); x is paired to match.  The warps of a block and
-// the blocks of a cluster take the stages of the same rows in turn; their sums are joined through
+// What bounds it at a few tokens is not memory but the instructions for a weight (230 for 4096 of them,
+// most on a pipe that takes one in two cycles) and, in short calls, the first loads and the join:
+// one token of 4096 x 16384 takes 12.4 us (2.8 TB/s; the same loads alone run at 6.0 TB/s), of 16384 x
+// 16384 34 us (4.1 TB/s), of 4096 x 4096 4.7 us.
+//
+// A warp has 32 or 64 rows and streams them 128 elements at a time through a ring of its own
+// (asynchronous 16-byte copies, x beside the weights), on from one tile of rows to the block's next.
+// Its lane c of a quad takes elements 8 c .. 8 c + 7 of each 32: in a word elements j and j + 4 are
+// 16 bits apart, so one mask gives the pair (j, j + 4); x is paired to match.  The warps of a block
+// and the blocks of a cluster take the stages of the same rows in turn; their sums are joined through
 // (distributed) shared memory in a fixed order.
 
 #include "tcg_lm_math.cuh"
@@ -609,10 +614,14 @@ cudaError_t launch_types(const W4Args &a, int num_sms, cudaStream_t s)
 
 cudaError_t launch_w4(const W4Args &a, int num_sms, cudaStream_t s)
 {
+    // Up to eight tokens, 64 rows a warp where that leaves tiles for half of the SMs: what a stage costs
+    // besides its weights is shared by more of them (one token, us in a graph, 32 / 64 rows: 8192 x 4096
+    // 7.6 / 6.6, 16384 x 4096 14.9 / 12.2; 4096 x 16384, which then needs clusters, 12.2 / 13.9).  Rooms
+    // for two tokens' x leave those sixteen warps, for eight tokens' twelve (12.1 and 13.0 us).
     if (a.tokens <= 8 && a.rows >= 32 * num_sms)
         return a.tokens <= 2 ? launch_types<1, 4, 2, 16>(a, num_sms, s) : launch_types<1, 4, 8, 12>(a, num_sms, s);
-    return a.tokens <= 2 ? launch_types<1, 2, 2, 16>(a, num_sms, s)
-         : a.tokens <= 8 ? launch_types<1, 2, 8, 16>(a, num_sms, s)
+    // Sixteen tokens a pass cost less than 32 as long as one is enough (4096 x 4096: 7.5 and 12.3 us).
+    return a.tokens <= 8 ? launch_types<1, 2, 8, 16>(a, num_sms, s)
          : a.tokens <= 16 ? launch_types<2, 2, 16, 12>(a, num_sms, s) : launch_types<4, 2, 32, 8>(a, num_sms, s);
 }
 

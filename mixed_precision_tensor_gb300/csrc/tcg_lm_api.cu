@@ -763,16 +763,16 @@ tcgStatus_t check_norm(int64_t rows, int64_t k, const void *W, tcgDataType_t w_t
 bool bad_rows(const void *p, int64_t ld, int64_t cols, int es) { return !aligned16(p) || bad_ld(ld, cols, es); }
 
 // --------------------------------------------------------------------- 4-bit weights
-// Whether the packed weights are read as they are, once for every 32 tokens, or expanded to 16 bits
+// Whether the packed weights are read as they are, once for every 16 tokens, or expanded to 16 bits
 // for the product of many tokens (us in a graph, as they are / expanded):
-//                 tokens   32            64            128
-//    1024 x  1024          6.4 / 10.2    6.4 / 13.2    6.5 / 14.2
-//    4096 x  4096         12.3 / 20.9   22.5 / 23.4   43.0 / 34.2
-//   16384 x  4096         51.3 / 60.0   86.2 / 63.9
-//    4096 x 16384         40.7 / 59.4   74.0 / 63.7
+//                 tokens   32            48            64            128
+//    1024 x  1024          4.2 / 10.2    4.2 / 12.2    4.3 / 13.2    6.9 / 14.2
+//    4096 x  4096         12.8 / 20.9   17.7 / 22.5   22.7 / 23.4   37.5 / 34.1
+//   16384 x  4096         40.9 / 60.0   62.0 / 63.5   77.8 / 64.2
+//    4096 x 16384         35.1 / 59.4   50.9 / 63.4   66.9 / 64.7
 bool w4_packed(int64_t tokens, int64_t rows, int64_t k)
 {
-    return tokens <= 32 || (tokens <= 64 && rows * k <= (int64_t(1) << 24)) ||
+    return tokens <= 48 || (tokens <= 64 && rows * k <= (int64_t(1) << 24)) ||
            (tokens <= 128 && rows * k <= (int64_t(1) << 21));
 }
 

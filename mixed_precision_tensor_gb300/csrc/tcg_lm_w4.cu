@@ -620,9 +620,9 @@ cudaError_t launch_w4(const W4Args &a, int num_sms, cudaStream_t s)
     // for two tokens' x leave those sixteen warps, for eight tokens' twelve (12.1 and 13.0 us).
     if (a.tokens <= 8 && a.rows >= 32 * num_sms)
         return a.tokens <= 2 ? launch_types<1, 4, 2, 16>(a, num_sms, s) : launch_types<1, 4, 8, 12>(a, num_sms, s);
-    // Sixteen tokens a pass cost less than 32 as long as one is enough (4096 x 4096: 7.5 and 12.3 us).
-    return a.tokens <= 8 ? launch_types<1, 2, 8, 16>(a, num_sms, s)
-         : a.tokens <= 16 ? launch_types<2, 2, 16, 12>(a, num_sms, s) : launch_types<4, 2, 32, 8>(a, num_sms, s);
+    // More: sixteen tokens a pass (32 of them with eight warps took longer, 32 tokens of 16384 x 4096
+    // 51 us for 41, and 33 tokens of 4096 x 4096 22 for 18).
+    return a.tokens <= 8 ? launch_types<1, 2, 8, 16>(a, num_sms, s) : launch_types<2, 2, 16, 12>(a, num_sms, s);
 }
 
 cudaError_t launch_w4_expand(const W4Args &a, void *out, int64_t ldo, int num_sms, cudaStream_t s)

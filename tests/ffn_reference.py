@@ -112,7 +112,7 @@ def linear_4bit(x, w, scales, zeros, group, bias, name, residual, beta, gated_, 
     xd = x.double()
     z = xd @ W.t()
     ez = 2.0 ** -23 * ((min(k, group) + 8) * (xd.abs() @ mag.t()) + (k + 8) * (xd.abs() @ W.abs().t()))
-    if t > 32:                               # the weights may be rounded to x's type
+    if t > 48:                               # the weights may be rounded to x's type
         ez = ez + U[x.dtype] * (1 + 2.0 ** -10) * (xd.abs() @ W.abs().t()) + \
             TINY[x.dtype] * xd.abs().sum(1, keepdim=True)
     if gated_:

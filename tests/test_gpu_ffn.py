@@ -144,6 +144,13 @@ def test_norm_of_small_and_large_rows(handle, size):
            (2.0 ** -4 + 2 * ref.NORM) * y.abs() + 2.0 ** -10 * scale.double()[:, None])
 
 
+def test_norm_refuses_a_weight_between_places(handle):
+    x, room = torch.ones(3, 64, dtype=BF16, device="cuda"), torch.ones(65, dtype=BF16, device="cuda")
+    for call in (tcg.rms_norm, tcg.rms_norm_8bit, lambda h, a, w: tcg.rms_norm_backward(h, a, a, w)):
+        with pytest.raises(tcg.TcgError):
+            call(handle, x, room[1:])
+
+
 def test_norm_without_rows(handle):
     x, weight = torch.empty(0, 40, dtype=BF16, device="cuda"), torch.ones(40, dtype=BF16, device="cuda")
     assert tcg.rms_norm(handle, x, weight).shape == (0, 40)
@@ -338,6 +345,79 @@ def test_4bit_scales_without_a_number(handle, dtype):
     got = tcg.linear_4bit(handle, x, w, scales, 32, zeros=zeros)
     rest = [i for i in range(40) if i not in (7, 20)]
     assert torch.isnan(got[:, [7, 20]]).all() and same_bits(got[:, rest], want[:, rest])
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("kind", [BF16, F32])
+def test_4bit_scales_anywhere(handle, group, kind):
+    """Scales and zeros that start at any element, where a stage's are not one aligned load."""
+    g = gen_of(15)
+    t, n, k = 5, 72, 1024
+    x = randn(g, t, k)
+    w, scales, zeros = draw_4bit(g, n, k, group, kind, True)
+    want = tcg.linear_4bit(handle, x, w, scales, group, zeros=zeros)
+
+    def moved(a):
+        room = torch.full((a.numel() + 1,), float("nan"), dtype=a.dtype, device="cuda")
+        room[1:] = a.flatten()
+        return room[1:].view(a.shape)
+    assert same_bits(tcg.linear_4bit(handle, x, w, moved(scales), group, zeros=zeros), want)
+    assert same_bits(tcg.linear_4bit(handle, x, w, scales, group, zeros=moved(zeros)), want)
+
+
+# ------------------------------------------------------------- places past 2^31 elements
+def test_norm_far_rows(handle):
+    g = gen_of(16)
+    t, k = 66000, 32768                       # 2.16e9 elements
+    x = torch.zeros(t, k, dtype=BF16, device="cuda")
+    x[-3:] = randn(g, 3, k)
+    weight, kept = randn(g, k), x[-3:].clone()
+    q, scale = tcg.rms_norm_8bit(handle, x, weight)
+    alone, alone_scale = tcg.rms_norm_8bit(handle, kept, weight)
+    assert same_bits(q[-3:], alone) and same_bits(scale[-3:], alone_scale) and (scale[:-3] == 2.0 ** -100).all()
+    del q
+    tcg.rms_norm(handle, x, weight, out=x)
+    assert same_bits(x[-3:], tcg.rms_norm(handle, kept, weight)) and not x[:-3].any()
+    x[-3:] = kept
+    dx, dw = tcg.rms_norm_backward(handle, x, x, weight, dx=x)
+    want = tcg.rms_norm_backward(handle, kept, kept, weight)
+    assert dx is x and same_bits(dx[-3:], want[0])
+    bound = 66000 * 2.0 ** -24 * ref.norm_backward(kept, kept, weight, 1e-6, None)[0][1].abs() + 1e-6
+    within(dw, want[1].double(), bound, "dw")
+
+
+def test_gated_far_tokens(handle):
+    g = gen_of(17)
+    t, n, k = 140000, 8192, 64                # z: 2.29e9 elements
+    x = torch.zeros(t, k, dtype=BF16, device="cuda")
+    x[-300:] = randn(g, 300, k)
+    w = randn(g, 2 * n, k, std=0.125)
+    z = torch.full((t, 2 * n), 7.0, dtype=BF16, device="cuda")
+    out = tcg.gated_linear(handle, x, w, z=z)
+    want, eo, zw, ez = ref.gated(x[-300:], w, "silu", BF16)
+    within(out[-300:], want, eo, "out")
+    within(z[-300:], zw, ez + U[BF16] * (zw.abs() + ez) + TINY[BF16], "z")
+    assert not out[:-300].any() and not z[:-300].any()
+    dx, dw = tcg.gated_linear_backward(handle, out, x, w, z)
+    (dxw, dww), (ex, ew) = ref.gated_backward(out[-300:], x[-300:], w, z[-300:], "silu")
+    within(dx[-300:], dxw, ex, "dx")
+    within(dw, dww, ew + (t * 2.0 ** -23) * ew, "dw")
+    assert not dx[:-300].any()
+
+
+@pytest.mark.parametrize("t", [2, 70])
+def test_4bit_far_rows(handle, t):
+    g = gen_of(18)
+    n, k, group = 66000, 65536, 128           # 2.16e9 bytes of weights, 4.3e9 elements
+    x = randn(g, t, k)
+    w = torch.full((n, k // 2), 0x88, dtype=torch.uint8, device="cuda")      # q = 8: zero
+    scales = torch.ones(n, k // group, dtype=BF16, device="cuda")
+    last, s, _ = draw_4bit(g, 64, k, group, BF16, False, apart=False)
+    w[-64:], scales[-64:] = last, s
+    out = tcg.linear_4bit(handle, x, w, scales, group, out_dtype=F32)
+    want, bound = ref.linear_4bit(x, last, s, None, group, None, "none", None, 0.0, False, F32)
+    within(out[:, -64:], want, bound, "out")
+    assert not out[:, :-64].any()
 
 
 # ---------------------------------------------------------------------------- together

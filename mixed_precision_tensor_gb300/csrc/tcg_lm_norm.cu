@@ -344,9 +344,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float s = 0.0f;
     if (c < k) {
-#pragma unroll 16
-        for (int b = warp; b < blocks; b += kJoinWarps)
-            s += part[static_cast<int64_t>(b) * k + c];
+        for (int b = warp; b < blocks; b += 8 * kJoinWarps) {            // eight loads at a time
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int at = b + j * kJoinWarps;
+                v[j] = at < blocks ? __ldcg(part + static_cast<int64_t>(at) * k + c) : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                s += v[j];
+        }
     }
     join[warp][lane] = s;
     __syncthreads();

@@ -15,7 +15,7 @@
 // Bound by memory: every element is read once and written once, 16 bytes a thread.  A row's
 // elements stay in registers as they were read (V pieces of eight a thread); s, its square and y
 // are formed in FP32 from them.  16384 x 4096 in a graph: 81 us with a residual kept (6.6 TB/s, 98% of
-// the copy rate), 76 in 8 bits (6.1), 44 without a residual (6.0); backward 105 (5.1), dx alone 93.
+// the copy rate), 76 in 8 bits (6.1), 44 without a residual (6.0); backward 102 (5.2), dx alone 93.
 
 #include <cuda_fp8.h>
 
@@ -237,8 +237,8 @@ __global__ void __launch_bounds__(1024) tcg_norm_kernel(const NormArgs p)
 }
 
 // ONE: a row is a block of its own.  Blocks of up to 256 threads (FEW) are three to an SM, so that a
-// thread has registers for its columns of dw and a row of three tensors: 16384 x 4096 takes 103 us so,
-// 105 with four blocks of 64 registers and a few values in memory, 185 with more of them there.
+// thread has registers for its columns of dw and a row of three tensors: 16384 x 4096 takes 102 us so,
+// 103 with four blocks of 64 registers and a few values in memory, 185 with more of them there.
 constexpr int kFewThreads = 256;
 template <int V, bool BF16, bool ONE, bool FEW>
 __global__ void __launch_bounds__(FEW ? kFewThreads : 1024, FEW ? 3 : 1)

@@ -552,6 +552,32 @@ def test_other_stream_and_dropped_inputs(cuda_device):
     plain.close()
 
 
+def test_two_streams_at_once(cuda_device):
+    """Two handles on streams of their own, their calls under way together."""
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    plain, handles = tcg.Handle(), [tcg.Handle(s) for s in streams]
+    sets = [buffers(t, 1032, 520, t) for t in (200, 20)]
+    want = []
+    for s in sets:
+        calls(plain, s)
+        torch.cuda.synchronize()
+        want.append({k: s[k].clone() for k in OUTS})
+    for s in sets:
+        for k in OUTS:
+            s[k].zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for h, s in zip(handles, sets):
+            calls(h, s)
+    torch.cuda.synchronize()
+    for s, w in zip(sets, want):
+        for k in OUTS:
+            assert same_bits(s[k], w[k]), k
+    for h in (*handles, plain):
+        tcg.check(tcg.tcg_get_device_error(h.h))
+        h.close()
+
+
 def test_capture_does_not_grow_the_workspace(cuda_device):
     stream = torch.cuda.Stream()
     h = tcg.Handle(stream)

@@ -617,8 +617,9 @@ tcgStatus_t tcg_rms_norm_backward_workspace_size(tcgHandle_t h, int64_t rows, in
  * tcg_gemm_epilogue (epilogue->Z must be NULL).  gated = 1: D = act(w_g B) * (w_u B) with the rows
  * 0 .. m - 1 and m .. 2 m - 1, only the epilogue's activation being used; bias and C are not
  * supported.  Few tokens (up to 48, 64 of at most 2^24 weights, 128 of at most 2^21) read the packed
- * weights: q - zero meets the scale in FP32.  More take the weights rounded to Btype, expanded in the
- * workspace (its size from the second call).  In the first case a weight enters its product as q and
+ * weights: q - zero meets the scale in FP32.  More take the weights rounded to Btype (gated ones, of
+ * which D has two, with what the rounding left as a second product), expanded in the workspace
+ * (its size from the second call); k is at most 2^29.  In the first case a weight enters its product as q and
  * loses its zero times the group's sum of x afterwards, so an infinity in B makes its column of D
  * NaN; and BF16 entries of B are multiplied by 2^64 on the way: from 2^63 on they overflow, below
  * 2^-57 sums lose bits (zero at 2^-80). */

@@ -256,8 +256,10 @@ struct W4Args {
     int tiles, units, groups;  // row tiles, stages and groups of a row, by launch_w4
 };
 cudaError_t launch_w4(const W4Args &a, int num_sms, cudaStream_t s);
-// The weights as the type of X, rounded once: rows x k, ldo elements apart.
-cudaError_t launch_w4_expand(const W4Args &a, void *out, int64_t ldo, int num_sms, cudaStream_t s);
+// The weights as the type of X, rounded once: rows x k, ldo elements apart, zeros up to a multiple of
+// eight columns.  lo > 0: from column lo on what the rounding left; and X twice in a row to match.
+cudaError_t launch_w4_expand(const W4Args &a, void *out, int64_t ldo, int64_t lo, int num_sms, cudaStream_t s);
+cudaError_t launch_w4_twice(const W4Args &a, void *out, int64_t ldo, int64_t lo, cudaStream_t s);
 
 // dZ = dD * act'(Z) and per-group sums of its rows; see tcg_epi_backward_kernel.  part:
 // (ceil(cols / chunk) + groups) * m floats.

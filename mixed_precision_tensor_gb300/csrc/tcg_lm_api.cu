@@ -776,18 +776,28 @@ bool w4_packed(int64_t tokens, int64_t rows, int64_t k)
            (tokens <= 128 && rows * k <= (int64_t(1) << 21));
 }
 
-size_t w4_expand_bytes(int64_t rows, int64_t k) { return pad256(static_cast<size_t>(rows) * ((k + 7) / 8 * 8) * 2); }
-
-Product w4_product(const W4Args &a, tcgDataType_t in, tcgDataType_t out)
-{
+// The product of the expanded weights, without its pointers, and its workspace: the weights (of a
+// gated product in two parts, `lo` columns apart), then X twice in a row, what the product needs.
+struct W4Plan {
     Product p;
-    p.feats = a.gated ? a.rows / 2 : a.rows;
-    p.tokens = a.tokens;
-    p.k = a.k;
-    p.gated = a.gated;
-    p.in = in;
-    p.out = out;
-    return p;
+    int64_t lo;
+    size_t w_bytes, x_bytes, total;
+};
+
+W4Plan w4_plan(tcgContext *h, int64_t m, int64_t n, int64_t k, bool gated)
+{
+    W4Plan pl;
+    const int64_t k8 = (k + 7) / 8 * 8;
+    pl.lo = gated ? k8 : 0;
+    pl.p.feats = m;
+    pl.p.tokens = n;
+    pl.p.k = gated ? 2 * k8 : k;
+    pl.p.gated = gated;
+    pl.p.ldw = k8 + pl.lo;
+    pl.w_bytes = pad256(static_cast<size_t>(gated ? 2 * m : m) * pl.p.ldw * 2);
+    pl.x_bytes = gated ? pad256(static_cast<size_t>(n) * pl.p.ldw * 2) : 0;
+    pl.total = pl.w_bytes + pl.x_bytes + product_ws(h, pl.p);
+    return pl;
 }
 
 }  // namespace
@@ -1543,7 +1553,7 @@ tcgStatus_t tcg_gemm_4bit(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int64_
         bad_ld(ldd, m, elem_size(Dtype)))
         return TCG_STATUS_INVALID_VALUE;
     if ((group != 32 && group != 64 && group != 128) || (Stype != TCG_R_32F && Stype != Btype) || epi.Z ||
-        (gated && (epi.bias || epi.beta != 0.0f)) || 2 * m > kMaxExtent || n > kMaxExtent || k > kMaxK)
+        (gated && (epi.bias || epi.beta != 0.0f)) || 2 * m > kMaxExtent || n > kMaxExtent || 2 * k > kMaxK)
         return TCG_STATUS_NOT_SUPPORTED;
     if (m == 0 || n == 0)
         return TCG_STATUS_SUCCESS;
@@ -1591,37 +1601,41 @@ tcgStatus_t tcg_gemm_4bit(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int64_
         }
         return TCG_STATUS_SUCCESS;
     }
-    Product p = w4_product(a, Btype, Dtype);
-    const size_t wide = w4_expand_bytes(a.rows, k), need = wide + product_ws(h, p);
+    W4Plan pl = w4_plan(h, m, n, k, gated != 0);
     void *ws = nullptr;
-    if (need) {
-        st = acquire_ws(h, need, &ws);
+    if (pl.total) {
+        st = acquire_ws(h, pl.total, &ws);
         if (st != TCG_STATUS_SUCCESS)
             return st;
     }
+    uint8_t *at = static_cast<uint8_t *>(ws);
+    Product &p = pl.p;
+    p.in = Btype;
+    p.out = Dtype;
     p.W = ws;
-    p.ldw = (k + 7) / 8 * 8;
-    p.X = B;
-    p.ldx = ldb;
+    p.X = gated ? at + pl.w_bytes : B;
+    p.ldx = gated ? p.ldw : ldb;
     p.D = D;
     p.ldd = ldd;
     p.epi = epi;
     if (k > 0) {
-        const cudaError_t e = launch_w4_expand(a, ws, p.ldw, h->num_sms, h->stream);
-        h->launches += 1;
+        cudaError_t e = launch_w4_expand(a, ws, p.ldw, pl.lo, h->num_sms, h->stream);
+        if (e == cudaSuccess && gated)
+            e = launch_w4_twice(a, at + pl.w_bytes, p.ldw, pl.lo, h->stream);
+        h->launches += gated ? 2 : 1;
         if (e != cudaSuccess) {
             cudaGetLastError();
             return TCG_STATUS_EXECUTION_FAILED;
         }
     }
-    return queue(h, p, static_cast<uint8_t *>(ws) + wide);
+    return queue(h, p, at + pl.w_bytes + pl.x_bytes);
 }
 
 tcgStatus_t tcg_gemm_4bit_workspace_size(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int gated, size_t *bytes)
 {
     if (!h || !bytes || m < 0 || n < 0 || k < 0)
         return TCG_STATUS_INVALID_VALUE;
-    if (2 * m > kMaxExtent || n > kMaxExtent || k > kMaxK)
+    if (2 * m > kMaxExtent || n > kMaxExtent || 2 * k > kMaxK)
         return TCG_STATUS_NOT_SUPPORTED;
     *bytes = 0;
     if (m == 0 || n == 0 || w4_packed(n, gated ? 2 * m : m, k))
@@ -1629,12 +1643,7 @@ tcgStatus_t tcg_gemm_4bit_workspace_size(tcgHandle_t h, int64_t m, int64_t n, in
     const tcgStatus_t st = bind_device(h);
     if (st != TCG_STATUS_SUCCESS)
         return st;
-    W4Args a{};
-    a.rows = gated ? 2 * m : m;
-    a.k = k;
-    a.tokens = static_cast<int>(n);
-    a.gated = gated != 0;
-    *bytes = w4_expand_bytes(a.rows, k) + product_ws(h, w4_product(a, TCG_R_16BF, TCG_R_16BF));
+    *bytes = w4_plan(h, m, n, k, gated != 0).total;
     return TCG_STATUS_SUCCESS;
 }
 

@@ -112,9 +112,10 @@ def linear_4bit(x, w, scales, zeros, group, bias, name, residual, beta, gated_, 
     xd = x.double()
     z = xd @ W.t()
     ez = 2.0 ** -23 * ((min(k, group) + 8) * (xd.abs() @ mag.t()) + (k + 8) * (xd.abs() @ W.abs().t()))
-    if t > 48:                               # the weights may be rounded to x's type
-        ez = ez + U[x.dtype] * (1 + 2.0 ** -10) * (xd.abs() @ W.abs().t()) + \
-            TINY[x.dtype] * xd.abs().sum(1, keepdim=True)
+    if t > 48:                               # the weights may be rounded to x's type, once or in two parts
+        u, tiny = U[x.dtype] * (1 + 2.0 ** -10), TINY[x.dtype]
+        ez = ez + (u * u if gated_ else u) * (xd.abs() @ W.abs().t()) + tiny * xd.abs().sum(1, keepdim=True)
+        ez = ez + (k + 8) * 2.0 ** -23 * (xd.abs() @ W.abs().t())
     if gated_:
         n = z.shape[1] // 2
         out, e = gate(z[:, :n], z[:, n:], ez[:, :n], ez[:, n:], name)

@@ -616,8 +616,8 @@ tcgStatus_t tcg_rms_norm_backward_workspace_size(tcgHandle_t h, int64_t rows, in
  * B is k x n (n tokens of k features).  gated = 0: D = act(w B + bias) + beta * C as in
  * tcg_gemm_epilogue (epilogue->Z must be NULL).  gated = 1: D = act(w_g B) * (w_u B) with the rows
  * 0 .. m - 1 and m .. 2 m - 1, only the epilogue's activation being used; bias and C are not
- * supported.  Few tokens (up to 48, 64 of at most 2^24 weights, 128 of at most 2^21) read the packed
- * weights: q - zero meets the scale in FP32.  More take the weights rounded to Btype (gated ones, of
+ * supported.  Few tokens (up to 48, 64 of at most 2^24 weights, 128 of at most 2^21; gated 128, 256 of
+ * at most 2^21) read the packed weights: q - zero meets the scale in FP32.  More take the weights rounded to Btype (gated ones, of
  * which D has two, with what the rounding left as a second product), expanded in the workspace
  * (its size from the second call); k is at most 2^29.  In the first case a weight enters its product as q and
  * loses its zero times the group's sum of x afterwards, so an infinity in B makes its column of D

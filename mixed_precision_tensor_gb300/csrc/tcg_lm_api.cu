@@ -770,8 +770,15 @@ bool bad_rows(const void *p, int64_t ld, int64_t cols, int es) { return !aligned
 //    4096 x  4096         12.8 / 20.9   17.7 / 22.5   22.7 / 23.4   37.5 / 34.1
 //   16384 x  4096         40.9 / 60.0   62.0 / 63.5   77.8 / 64.2
 //    4096 x 16384         35.1 / 59.4   50.9 / 63.4   66.9 / 64.7
-bool w4_packed(int64_t tokens, int64_t rows, int64_t k)
+// Gated products, whose expanded weights are twice as many (2 x 512 x 1024, 2 x 2048 x 4096, 2 x 8192
+// x 4096 and 2 x 2048 x 16384):
+//    64 tokens   3.7 / 14.8   20.8 / 33.7   67 / 108    63 / 109
+//   128          5.8 / 21.4   34.5 / 45.6   126 / 116   109 / 123
+//   256         10.1 / 16.9   70.9 / 42.3   263 / 115   229 / 138
+bool w4_packed(int64_t tokens, int64_t rows, int64_t k, bool gated)
 {
+    if (gated)
+        return tokens <= 128 || (tokens <= 256 && rows * k <= (int64_t(1) << 21));
     return tokens <= 48 || (tokens <= 64 && rows * k <= (int64_t(1) << 24)) ||
            (tokens <= 128 && rows * k <= (int64_t(1) << 21));
 }
@@ -1592,7 +1599,7 @@ tcgStatus_t tcg_gemm_4bit(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int64_
     a.beta = epi.beta;
     a.act = epi.activation;
     a.gated = gated != 0;
-    if (w4_packed(n, a.rows, k)) {
+    if (w4_packed(n, a.rows, k, a.gated)) {
         const cudaError_t e = launch_w4(a, h->num_sms, h->stream);
         h->launches += 1;
         if (e != cudaSuccess) {
@@ -1638,7 +1645,7 @@ tcgStatus_t tcg_gemm_4bit_workspace_size(tcgHandle_t h, int64_t m, int64_t n, in
     if (2 * m > kMaxExtent || n > kMaxExtent || 2 * k > kMaxK)
         return TCG_STATUS_NOT_SUPPORTED;
     *bytes = 0;
-    if (m == 0 || n == 0 || w4_packed(n, gated ? 2 * m : m, k))
+    if (m == 0 || n == 0 || w4_packed(n, gated ? 2 * m : m, k, gated))
         return TCG_STATUS_SUCCESS;
     const tcgStatus_t st = bind_device(h);
     if (st != TCG_STATUS_SUCCESS)

@@ -123,7 +123,7 @@ def test_workspace_queries_refuse(handle):
     assert lib.tcg_rms_norm_backward_workspace_size(handle, 1, 40000, size) == NSUP
     assert lib.tcg_gemm_4bit_workspace_size(handle, 1, 1, -1, 0, size) == INV
     assert lib.tcg_gemm_4bit_workspace_size(handle, 1, 1, 8, 0, None) == INV
-    for m, n, k, gate in ((4096, 48, 65536, 0), (4096, 64, 4096, 0), (2048, 64, 4096, 1), (512, 128, 4096, 0)):
+    for m, n, k, gate in ((4096, 48, 65536, 0), (4096, 64, 4096, 0), (65536, 128, 4096, 1), (512, 128, 4096, 0), (256, 256, 4096, 1)):
         assert lib.tcg_gemm_4bit_workspace_size(handle, m, n, k, gate, size) == OK and size.value == 0
 
 

@@ -234,7 +234,7 @@ def test_gated_keeps_rows_apart(handle, t):
 W4_SIZES = [(1, 32, 128), (1, 8, 32), (1, 4096, 4096), (2, 100, 31), (3, 33, 257), (4, 1000, 1000), (8, 40, 5000), (9, 64, 40),
             (16, 300, 2048), (17, 512, 384), (32, 77, 100), (33, 200, 777), (64, 1000, 1032), (65, 136, 200),
             (100, 512, 1024), (300, 1000, 520), (7, 6, 16384), (1, 3, 20000), (1, 1, 1), (5, 2, 33), (130, 40, 36), (128, 200, 1000),
-            (48, 4128, 4104), (64, 2000, 8300)]
+            (48, 4128, 4104), (64, 2000, 8300), (129, 1100, 1064), (256, 100, 520), (300, 2200, 1032)]
 
 
 def draw_4bit(g, rows, k, group, dtype, zeros, apart=True):

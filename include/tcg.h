@@ -613,16 +613,18 @@ tcgStatus_t tcg_rms_norm_backward_workspace_size(tcgHandle_t h, int64_t rows, in
  * elements of a row fall into ceil(k / group) groups (group 32, 64 or 128) with a scale and, if
  * zeros is not NULL, a zero each (row-major, contiguous; Stype is Btype or TCG_R_32F):
  *     w = (q - zero) * scale,   zero = 8 where zeros is NULL.
- * B is k x n (n tokens of k features).  gated = 0: D = act(w B + bias) + beta * C as in
- * tcg_gemm_epilogue (epilogue->Z must be NULL).  gated = 1: D = act(w_g B) * (w_u B) with the rows
- * 0 .. m - 1 and m .. 2 m - 1, only the epilogue's activation being used; bias and C are not
- * supported.  Few tokens (up to 48, 64 of at most 2^24 weights, 128 of at most 2^21; gated 128, 256 of
- * at most 2^21) read the packed weights: q - zero meets the scale in FP32.  More take the weights rounded to Btype (gated ones, of
- * which D has two, with what the rounding left as a second product), expanded in the workspace
- * (its size from the second call); k is at most 2^29.  In the first case a weight enters its product as q and
- * loses its zero times the group's sum of x afterwards, so an infinity in B makes its column of D
+ * B is k x n (n tokens of k features, k at most 2^29).  gated = 0: D = act(w B + bias) + beta * C as
+ * in tcg_gemm_epilogue (epilogue->Z must be NULL; C may be D).  gated = 1: D = act(w_g B) * (w_u B)
+ * with the rows 0 .. m - 1 and m .. 2 m - 1, only the epilogue's activation being used; bias and C
+ * are not supported.
+ *
+ * Few tokens (up to 48, 64 of at most 2^24 weights, 128 of at most 2^21; gated 128, 256 of at most
+ * 2^21) read the packed weights: q - zero meets the scale in FP32.  A weight enters its product as q
+ * and loses its zero times the group's sum of B afterwards, so an infinity in B makes its column of D
  * NaN; and BF16 entries of B are multiplied by 2^64 on the way: from 2^63 on they overflow, below
- * 2^-57 sums lose bits (zero at 2^-80). */
+ * 2^-57 sums lose bits (zero at 2^-80).  More tokens take the weights rounded to Btype, expanded in
+ * the workspace (its size from the second call); gated ones, of which D has two, with what the
+ * rounding left as a second product. */
 tcgStatus_t tcg_gemm_4bit(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int64_t group, const void *A,
                           int64_t lda, const void *scales, const void *zeros, tcgDataType_t Stype, const void *B,
                           int64_t ldb, tcgDataType_t Btype, void *D, tcgDataType_t Dtype, int64_t ldd, int gated,

@@ -592,7 +592,8 @@ tcgStatus_t tcg_gated_backward_workspace_size(tcgHandle_t h, int64_t m, int64_t 
  * nearest even, so that Y * scale stands for the result; scale is not touched otherwise.  S may be X
  * or R, a 16-bit Y may be X or R, not both the same.  A row with a NaN or an infinity has
  * entries that are NaN (in 8 bits all of them, and its scale); entries above 2^63 overflow the
- * FP32 sum of squares, which leaves zeros. */
+ * FP32 sum of squares, which leaves zeros, and in a row whose entries are all below 2^-60 the
+ * squares lose bits or vanish, which matters with an eps as small (eps 0: NaN, as for zeros). */
 tcgStatus_t tcg_rms_norm(tcgHandle_t h, int64_t rows, int64_t k, const void *X, int64_t ldx, const void *R,
                          int64_t ldr, void *S, int64_t lds, const void *W, tcgDataType_t Wtype, float eps,
                          tcgDataType_t type, void *Y, tcgDataType_t Ytype, int64_t ldy, float *scale);

@@ -75,30 +75,30 @@ __device__ __forceinline__ void mma_group(bool first, float (&d)[4], const uint3
 //   BF16: a 16-bit word 0 .. 255 is that many times 2^-133 (the subnormal numbers and the binade above
 //   them have one spacing), so a masked nibble is q or 16 q without further ado; x is multiplied by
 //   2^64 or 2^60 to match, and sums come out times 2^-69.
-//   FP16: x has no room for such factors; a shift brings two nibbles under the exponents of 256 and 16,
-//   as 256 + q and 16 + q.
+//   FP16: the same words are q or 16 q times 2^-24, subnormal; x has no room for factors, so a fused
+//   multiply-add makes (q - 8) 2^-9 of them, exactly, and sums come out times 2^-9.
 constexpr float kBfUnit = 5.9029581035870565e20f;   // 2^69
+constexpr float kHalfUnit = 512.0f;                 // 2^9
 template <bool BF16>
-__device__ __forceinline__ void widen(uint32_t w, const uint32_t (&m)[4], uint32_t (&q)[4])
+__device__ __forceinline__ void widen(uint32_t w, uint32_t (&q)[4])
 {
-    if constexpr (BF16) {
-        const uint32_t v = w >> 8;
-        q[0] = w & 0x000F000Fu;
-        q[1] = w & 0x00F000F0u;
-        q[2] = v & 0x000F000Fu;
-        q[3] = v & 0x00F000F0u;
-    } else {
-        // v & mask | base; as immediates the two would take two instructions
-        auto pick = [](uint32_t v, uint32_t mask, uint32_t base) {
-            uint32_t r;
-            asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(mask), "r"(base));
-            return r;
+    const uint32_t v = w >> 8;
+    q[0] = w & 0x000F000Fu;
+    q[1] = w & 0x00F000F0u;
+    q[2] = v & 0x000F000Fu;
+    q[3] = v & 0x00F000F0u;
+    if constexpr (!BF16) {
+        auto less8 = [](uint32_t x, uint32_t factor) {
+            const uint32_t eight = 0xA400A400u;              // -8 2^-9
+            const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&x),
+                                      *reinterpret_cast<const __half2 *>(&factor),
+                                      *reinterpret_cast<const __half2 *>(&eight));
+            return *reinterpret_cast<const uint32_t *>(&r);
         };
-        const uint32_t lo = w << 2, hi = w >> 6;
-        q[0] = pick(lo, m[0], m[1]);
-        q[1] = pick(lo, m[2], m[3]);
-        q[2] = pick(hi, m[0], m[1]);
-        q[3] = pick(hi, m[2], m[3]);
+        q[0] = less8(q[0], 0x78007800u);                     // 2^15
+        q[1] = less8(q[1], 0x68006800u);                     // 2^11
+        q[2] = less8(q[2], 0x78007800u);
+        q[3] = less8(q[3], 0x68006800u);
     }
 }
 
@@ -309,25 +309,15 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
         load_scales(first_tile, begin);
 
     // Rows 0 .. 7 of the constant matrix: what a weight holds too much, without zeros 8 more; 8 .. 15: one.
-    // Pairs 0 and 2 are alike, and 1 and 3.
-    uint32_t much[4], m[4];
+    // Pairs 0 and 2 are alike, and 1 and 3.  FP16: nothing too much but the 8 that a zero replaces.
+    uint32_t much[4];
     if constexpr (BF16) {
         much[0] = zeros ? 0u : 0x00080008u;
         much[1] = 0x00010001u;
         much[2] = zeros ? 0u : 0x00800080u;
         much[3] = 0x00100010u;
-        m[0] = m[1] = m[2] = m[3] = 0u;
     } else {
-        much[0] = zeros ? 0x5C005C00u : 0x5C205C20u;         // 256, 264
-        much[2] = zeros ? 0x4C004C00u : 0x4E004E00u;         // 16, 24
-        much[1] = much[3] = 0x3C003C00u;
-        m[0] = 0x003C003Cu;
-        m[1] = 0x5C005C00u;
-        m[2] = 0x03C003C0u;
-        m[3] = 0x4C004C00u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            asm volatile("" : "+r"(m[i]));                   // in registers
+        much[0] = much[1] = much[2] = much[3] = 0x18001800u;  // 2^-9
     }
     const uint32_t from_w = mine + lane * 64 + ((lane >> 1) & 3) * 16;
     const uint32_t from_x = mine + Cfg::kWBytes + g * kW4XRow + (g & 1) * 64 + c * 16;
@@ -411,14 +401,16 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
                     b[nt][1] = scaled<BF16>(__byte_perm(v.x, v.z, 0x7632), k60);
                     b[nt][2] = scaled<BF16>(__byte_perm(v.y, v.w, 0x5410), k64);
                     b[nt][3] = scaled<BF16>(__byte_perm(v.y, v.w, 0x7632), k60);
-                    mma_group<BF16>(first, off[nt], much, b[nt][0], b[nt][1]);
-                    mma_group<BF16>(false, off[nt], much, b[nt][2], b[nt][3]);
+                    if (BF16 || zeros) {
+                        mma_group<BF16>(first, off[nt], much, b[nt][0], b[nt][1]);
+                        mma_group<BF16>(false, off[nt], much, b[nt][2], b[nt][3]);
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                     uint32_t lo[4], hi[4];
-                    widen<BF16>(w[q & 1][2 * i], m, lo);
-                    widen<BF16>(w[q & 1][2 * i + 1], m, hi);
+                    widen<BF16>(w[q & 1][2 * i], lo);
+                    widen<BF16>(w[q & 1][2 * i + 1], hi);
                     const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
@@ -431,18 +423,21 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
                         const float s0 = at_s[16 * i * kGroups], s1 = at_s[(16 * i + 8) * kGroups];
+                        if (BF16 && !zeros) {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                acc[i][nt][j] -= off[nt][j & 1];
-                        if (zeros) {                             // off: 0 for BF16, 256 or 16 times for FP16
+                                for (int j = 0; j < 4; ++j)
+                                    acc[i][nt][j] -= off[nt][j & 1];
+                        }
+                        if (zeros) {                             // FP16 weights have 8 taken away already
+                            constexpr float had = BF16 ? 0.0f : 8.0f;
                             const float z0 = at_s[(R + 16 * i) * kGroups], z1 = at_s[(R + 16 * i + 8) * kGroups];
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                                 for (int j = 0; j < 4; ++j)
-                                    acc[i][nt][j] = fmaf(j < 2 ? -z0 : -z1, off[nt][2 + (j & 1)], acc[i][nt][j]);
+                                    acc[i][nt][j] = fmaf(j < 2 ? had - z0 : had - z1, off[nt][2 + (j & 1)], acc[i][nt][j]);
                         }
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
@@ -467,7 +462,7 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     part[warp * Cfg::kSums + sum_at<R>(nt * 8 + 2 * c + (j & 1), 16 * i + 8 * (j >> 1) + g)] =
-                        BF16 ? tot[i][nt][j] * kBfUnit : tot[i][nt][j];
+                        tot[i][nt][j] * (BF16 ? kBfUnit : kHalfUnit);
         __syncthreads();
         auto block_sum = [&](int t, int j) {
             const int at = sum_at<R>(t, j);

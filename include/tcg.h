@@ -620,10 +620,10 @@ tcgStatus_t tcg_rms_norm_backward_workspace_size(tcgHandle_t h, int64_t rows, in
  * are not supported.
  *
  * Few tokens (up to 48, 64 of at most 2^24 weights, 128 of at most 2^21; gated 128, 256 of at most
- * 2^21) read the packed weights: q - zero meets the scale in FP32.  A weight enters its product as q
- * and loses its zero times the group's sum of B afterwards, so an infinity in B makes its column of D
- * NaN; and BF16 entries of B are multiplied by 2^64 on the way: from 2^63 on they overflow, below
- * 2^-57 sums lose bits (zero at 2^-80).  More tokens take the weights rounded to Btype, expanded in
+ * 2^21) read the packed weights: a weight enters its product as q - 8, exactly, and its scale in FP32 (scales
+ * below 2^118).  Zeros take 8 - zero times the group's sum of B besides, so that with zeros the
+ * accuracy counts |q - 8| + |8 - zero| for |q - zero|, and an infinity in B makes its column of D NaN.
+ * More tokens take the weights rounded to Btype, expanded in
  * the workspace (its size from the second call); gated ones, of which D has two, with what the
  * rounding left as a second product. */
 tcgStatus_t tcg_gemm_4bit(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int64_t group, const void *A,

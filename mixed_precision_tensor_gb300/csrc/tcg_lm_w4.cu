@@ -5,10 +5,9 @@
 // Half a byte a weight for 2 T operations.  Turning a weight into a number costs more instructions
 // than multiplying it, so a warp does that once for eight tokens or more: the weights are the A
 // operand of mma.m16n8k16, the tokens its eight columns (tcgen05 would want the weights back in
-// shared memory first, and 128 rows of them).  A nibble becomes a number by a mask (see widen); what
-// it is too much, 8 or the zero times the group's sum of x, comes from one more product with a
-// constant matrix for all rows, and is taken away in FP32 when the group is complete and meets its
-// scale.  Sums are FP32.
+// shared memory first, and 128 rows of them).  A nibble becomes q - 8 by a mask and a multiply-add, exactly
+// (see widen).  Zeros take 8 - zero times the group's sum of x, which one more product with a matrix of
+// ones gives for all rows, when the group is complete and meets its scale.  Sums are FP32.
 //
 // What bounds it at a few tokens is not memory but the instructions for a weight (230 for 4096 of them,
 // most on a pipe that takes one in two cycles) and, in short calls, the first loads and the join:
@@ -21,6 +20,8 @@
 // 16 bits apart, so one mask gives the pair (j, j + 4); x is paired to match.  The warps of a block
 // and the blocks of a cluster take the stages of the same rows in turn; their sums are joined through
 // (distributed) shared memory in a fixed order.
+
+#include <type_traits>
 
 #include "tcg_lm_math.cuh"
 
@@ -71,48 +72,39 @@ __device__ __forceinline__ void mma_group(bool first, float (&d)[4], const uint3
     mma16816<BF16>(d, a, b0, b1);
 }
 
-// The eight elements of a word as A operands: pairs (0, 4), (1, 5), (2, 6), (3, 7).
-//   BF16: a 16-bit word 0 .. 255 is that many times 2^-133 (the subnormal numbers and the binade above
-//   them have one spacing), so a masked nibble is q or 16 q without further ado; x is multiplied by
-//   2^64 or 2^60 to match, and sums come out times 2^-69.
-//   FP16: the same words are q or 16 q times 2^-24, subnormal; x has no room for factors, so a fused
-//   multiply-add makes (q - 8) 2^-9 of them, exactly, and sums come out times 2^-9.
-constexpr float kBfUnit = 5.9029581035870565e20f;   // 2^69
-constexpr float kHalfUnit = 512.0f;                 // 2^9
+// Two 16-bit numbers of the type of x, a b + c.
+template <bool BF16>
+__device__ __forceinline__ uint32_t fma16(uint32_t a, uint32_t b, uint32_t c)
+{
+    using T = std::conditional_t<BF16, __nv_bfloat162, __half2>;
+    const T r = __hfma2(*reinterpret_cast<const T *>(&a), *reinterpret_cast<const T *>(&b),
+                        *reinterpret_cast<const T *>(&c));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// The eight elements of a word as A operands: pairs (0, 4), (1, 5), (2, 6), (3, 7) of q - 8, times a
+// unit.  A 16-bit word 0 .. 255 read as a number is that many times the smallest subnormal one, 2^-133
+// in BF16 and 2^-24 in FP16, so a masked nibble is q or 16 q in that measure; one fused multiply-add
+// brings it among the normal numbers and takes the 8 away, exactly.  (With the 8 left in, a row of
+// weights near zero would be the difference of two large sums; with x scaled instead, its range would end
+// early.)
+template <bool BF16>
+struct W4Unit {
+    static constexpr uint32_t kLow = BF16 ? 0x7F007F00u : 0x78007800u;     // 2^127, 2^15: a nibble
+    static constexpr uint32_t kHigh = BF16 ? 0x7D007D00u : 0x68006800u;    // 2^123, 2^11: sixteen times it
+    static constexpr uint32_t kOne = BF16 ? 0x3C803C80u : 0x18001800u;     // the unit: 2^-6, 2^-9
+    static constexpr uint32_t kLess8 = BF16 ? 0xBE00BE00u : 0xA400A400u;   // -8 units
+    static constexpr float kInverse = BF16 ? 64.0f : 512.0f;
+};
 template <bool BF16>
 __device__ __forceinline__ void widen(uint32_t w, uint32_t (&q)[4])
 {
+    using U = W4Unit<BF16>;
     const uint32_t v = w >> 8;
-    q[0] = w & 0x000F000Fu;
-    q[1] = w & 0x00F000F0u;
-    q[2] = v & 0x000F000Fu;
-    q[3] = v & 0x00F000F0u;
-    if constexpr (!BF16) {
-        auto less8 = [](uint32_t x, uint32_t factor) {
-            const uint32_t eight = 0xA400A400u;              // -8 2^-9
-            const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&x),
-                                      *reinterpret_cast<const __half2 *>(&factor),
-                                      *reinterpret_cast<const __half2 *>(&eight));
-            return *reinterpret_cast<const uint32_t *>(&r);
-        };
-        q[0] = less8(q[0], 0x78007800u);                     // 2^15
-        q[1] = less8(q[1], 0x68006800u);                     // 2^11
-        q[2] = less8(q[2], 0x78007800u);
-        q[3] = less8(q[3], 0x68006800u);
-    }
-}
-
-// Two elements of x as B operands.
-template <bool BF16>
-__device__ __forceinline__ uint32_t scaled(uint32_t x, uint32_t factor)
-{
-    if constexpr (BF16) {
-        const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x),
-                                         *reinterpret_cast<const __nv_bfloat162 *>(&factor));
-        return *reinterpret_cast<const uint32_t *>(&r);
-    } else {
-        return x;
-    }
+    q[0] = fma16<BF16>(w & 0x000F000Fu, U::kLow, U::kLess8);
+    q[1] = fma16<BF16>(w & 0x00F000F0u, U::kHigh, U::kLess8);
+    q[2] = fma16<BF16>(v & 0x000F000Fu, U::kLow, U::kLess8);
+    q[3] = fma16<BF16>(v & 0x00F000F0u, U::kHigh, U::kLess8);
 }
 
 __device__ __forceinline__ uint4 load_shared16(uint32_t addr)
@@ -308,17 +300,9 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
     if (begin < units)
         load_scales(first_tile, begin);
 
-    // Rows 0 .. 7 of the constant matrix: what a weight holds too much, without zeros 8 more; 8 .. 15: one.
-    // Pairs 0 and 2 are alike, and 1 and 3.  FP16: nothing too much but the 8 that a zero replaces.
-    uint32_t much[4];
-    if constexpr (BF16) {
-        much[0] = zeros ? 0u : 0x00080008u;
-        much[1] = 0x00010001u;
-        much[2] = zeros ? 0u : 0x00800080u;
-        much[3] = 0x00100010u;
-    } else {
-        much[0] = much[1] = much[2] = much[3] = 0x18001800u;  // 2^-9
-    }
+    // For zeros: a matrix of ones gives the sums of x.
+    using U = W4Unit<BF16>;
+    const uint32_t ones[4] = {U::kOne, U::kOne, U::kOne, U::kOne};
     const uint32_t from_w = mine + lane * 64 + ((lane >> 1) & 3) * 16;
     const uint32_t from_x = mine + Cfg::kWBytes + g * kW4XRow + (g & 1) * 64 + c * 16;
     uint32_t stage = 0;                                      // bytes of the stage to read
@@ -363,7 +347,7 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
             for (int i = 0; i < kSr; ++i)
 #pragma unroll
                 for (int j = 0; j < kGroups; ++j)
-                    sc[(lane + 32 * i) * kGroups + j] = group_value(raw_s[i], j);
+                    sc[(lane + 32 * i) * kGroups + j] = group_value(raw_s[i], j) * U::kInverse;
             if (zeros) {
 #pragma unroll
                 for (int i = 0; i < kSr; ++i)
@@ -396,14 +380,13 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const uint4 v = x[q & 1][nt];
-                    constexpr uint32_t k64 = 0x5F805F80u, k60 = 0x5D805D80u;     // 2^64, 2^60
-                    b[nt][0] = scaled<BF16>(__byte_perm(v.x, v.z, 0x5410), k64);
-                    b[nt][1] = scaled<BF16>(__byte_perm(v.x, v.z, 0x7632), k60);
-                    b[nt][2] = scaled<BF16>(__byte_perm(v.y, v.w, 0x5410), k64);
-                    b[nt][3] = scaled<BF16>(__byte_perm(v.y, v.w, 0x7632), k60);
-                    if (BF16 || zeros) {
-                        mma_group<BF16>(first, off[nt], much, b[nt][0], b[nt][1]);
-                        mma_group<BF16>(false, off[nt], much, b[nt][2], b[nt][3]);
+                    b[nt][0] = __byte_perm(v.x, v.z, 0x5410);
+                    b[nt][1] = __byte_perm(v.x, v.z, 0x7632);
+                    b[nt][2] = __byte_perm(v.y, v.w, 0x5410);
+                    b[nt][3] = __byte_perm(v.y, v.w, 0x7632);
+                    if (zeros) {
+                        mma_group<BF16>(first, off[nt], ones, b[nt][0], b[nt][1]);
+                        mma_group<BF16>(false, off[nt], ones, b[nt][2], b[nt][3]);
                     }
                 }
 #pragma unroll
@@ -423,21 +406,13 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
                         const float s0 = at_s[16 * i * kGroups], s1 = at_s[(16 * i + 8) * kGroups];
-                        if (BF16 && !zeros) {
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int j = 0; j < 4; ++j)
-                                    acc[i][nt][j] -= off[nt][j & 1];
-                        }
-                        if (zeros) {                             // FP16 weights have 8 taken away already
-                            constexpr float had = BF16 ? 0.0f : 8.0f;
+                        if (zeros) {                             // instead of the 8
                             const float z0 = at_s[(R + 16 * i) * kGroups], z1 = at_s[(R + 16 * i + 8) * kGroups];
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                                 for (int j = 0; j < 4; ++j)
-                                    acc[i][nt][j] = fmaf(j < 2 ? had - z0 : had - z1, off[nt][2 + (j & 1)], acc[i][nt][j]);
+                                    acc[i][nt][j] = fmaf(8.0f - (j < 2 ? z0 : z1), off[nt][j & 1], acc[i][nt][j]);
                         }
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
@@ -462,7 +437,7 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     part[warp * Cfg::kSums + sum_at<R>(nt * 8 + 2 * c + (j & 1), 16 * i + 8 * (j >> 1) + g)] =
-                        tot[i][nt][j] * (BF16 ? kBfUnit : kHalfUnit);
+                        tot[i][nt][j];
         __syncthreads();
         auto block_sum = [&](int t, int j) {
             const int at = sum_at<R>(t, j);

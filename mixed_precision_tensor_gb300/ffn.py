@@ -187,10 +187,9 @@ def linear_4bit(handle, x, w, scales, group, zeros=None, bias=None, act="none", 
         w = q[:, 0::2] | q[:, 1::2] << 4
 
     residual may be ``out`` itself.  Few tokens (up to 48, 64 of at most 2^24 weights, 128 of at
-    most 2^21; gated 128, 256 of at most 2^21) read the packed weights; an infinity in x then makes
-    its token's outputs NaN, and BF16 entries of x must be below 2^63 (and above 2^-57, or they lose
-    bits).  More tokens expand the weights in the handle's workspace, rounded to x's type (gated
-    ones in two parts).  Returns out.
+    most 2^21; gated 128, 256 of at most 2^21) read the packed weights; with zeros an infinity in x then
+    makes its token's outputs NaN.  More tokens expand the weights in the handle's workspace, rounded
+    to x's type (gated ones in two parts).  Returns out.
     """
     t, k, dtype, dev = _input(x)
     if not isinstance(w, torch.Tensor) or w.dim() != 2:

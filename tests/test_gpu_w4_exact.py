@@ -51,3 +51,56 @@ def test_rows_of_zero_weights_but_one(handle, t, group, dtype):
     x = positive(g, t, k, dtype)
     out = tcg.linear_4bit(handle, x, ref.pack(q), scales, group, out_dtype=F32)
     within(out, *expected(x, q, scales, None, group), "out")
+
+
+def weights(g, n, k, group, dtype, zeros=None):
+    q = torch.randint(0, 16, (n, k), generator=g, device="cuda", dtype=torch.uint8)
+    size = (n, -(-k // group))
+    scales = ((0.5 + torch.rand(size, generator=g, device="cuda")) / (4.6 * k ** 0.5)).to(dtype)
+    if zeros == "whole":
+        return q, scales, torch.randint(0, 16, size, generator=g, device="cuda").to(dtype)
+    return q, scales, (torch.randn(size, generator=g, device="cuda") * 3 + 8).to(dtype) if zeros else None
+
+
+@pytest.mark.parametrize("t", [1, 8, 40])
+@pytest.mark.parametrize("kind", [BF16, F32])
+@pytest.mark.parametrize("size", [2.0 ** -10, 2.0 ** -40, 2.0 ** -60, 2.0 ** -75, 2.0 ** -100, 2.0 ** 60, 2.0 ** 90])
+def test_small_and_large_scales(handle, t, kind, size):
+    """BF16 x of ordinary size and scales of any: the products are what has to fit FP32."""
+    g = gen_of(31)
+    q, scales, zeros = weights(g, 72, 544, 64, F32, True)
+    scales, zeros = (scales * size).to(kind), zeros.to(kind)
+    x = randn(g, t, 544)
+    for zero in (None, zeros):
+        out = tcg.linear_4bit(handle, x, ref.pack(q), scales, 64, zeros=zero, out_dtype=F32)
+        want, bound = expected(x, q, scales, zero, 64)
+        if zero is not None:        # the zero's part is taken besides
+            at = torch.arange(544, device="cuda") // 64
+            bound = bound + 552 * 2.0 ** -23 * (x.double().abs() @ (
+                ((8 - zero.double()).abs() + 16) * scales.double())[:, at].t())
+        within(out, want, bound, "out")
+
+
+@pytest.mark.parametrize("t", [1, 8, 40])
+@pytest.mark.parametrize("size", [2.0 ** -110, 2.0 ** -80, 2.0 ** -57, 2.0 ** 63, 2.0 ** 100, 2.0 ** 120])
+def test_small_and_large_rows(handle, t, size):
+    """BF16 x over the type's range."""
+    g = gen_of(32)
+    q, scales, _ = weights(g, 72, 544, 64, BF16)
+    x = (randn(g, t, 544, dtype=F32) / 8 * size).to(BF16)
+    within(tcg.linear_4bit(handle, x, ref.pack(q), scales, 64, out_dtype=F32), *expected(x, q, scales, None, 64), "out")
+
+
+@pytest.mark.parametrize("t", [2, 8, 40])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_infinity_in_x(handle, t, dtype):
+    """An infinite entry meets a weight: infinite with its sign, NaN where the weight is zero."""
+    g = gen_of(33)
+    q, scales, _ = weights(g, 72, 544, 32, dtype)
+    x = randn(g, t, 544, dtype=dtype)
+    x[1, 77] = float("inf")
+    out = tcg.linear_4bit(handle, x, ref.pack(q), scales, 32)
+    sign = q[:, 77].double() - 8
+    assert torch.equal(torch.isnan(out[1]), sign == 0) and bool((sign == 0).any())
+    assert torch.equal(out[1][sign != 0].double(), sign[sign != 0] * float("inf"))
+    assert torch.isfinite(out[0]).all() and torch.isfinite(out[2:]).all()

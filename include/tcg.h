@@ -620,10 +620,10 @@ tcgStatus_t tcg_rms_norm_backward_workspace_size(tcgHandle_t h, int64_t rows, in
  * are not supported.
  *
  * Few tokens (up to 48, 64 of at most 2^24 weights, 128 of at most 2^21; gated 128, 256 of at most
- * 2^21) read the packed weights: a weight enters its product as q - 8, exactly, and its scale in FP32 (scales
- * below 2^118).  Zeros take 8 - zero times the group's sum of B besides, so that with zeros the
- * accuracy counts |q - 8| + |8 - zero| for |q - zero|, and an infinity in B makes its column of D NaN.
- * More tokens take the weights rounded to Btype, expanded in
+ * 2^21) read the packed weights: a weight enters its product as q - 8, exactly, and its scale in FP32
+ * (scales below 2^118).  With zeros it enters as q less the nearest whole number of 0 .. 15, and what
+ * is left of the zero meets the group's sum of B besides: where zeros are no whole numbers, the accuracy
+ * counts at least |scale| / 2 for a weight, and an infinity in B makes its column of D NaN.  More tokens take the weights rounded to Btype, expanded in
  * the workspace (its size from the second call); gated ones, of which D has two, with what the
  * rounding left as a second product. */
 tcgStatus_t tcg_gemm_4bit(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int64_t group, const void *A,

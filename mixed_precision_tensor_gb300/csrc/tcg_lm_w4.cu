@@ -6,8 +6,9 @@
 // than multiplying it, so a warp does that once for eight tokens or more: the weights are the A
 // operand of mma.m16n8k16, the tokens its eight columns (tcgen05 would want the weights back in
 // shared memory first, and 128 rows of them).  A nibble becomes q - 8 by a mask and a multiply-add, exactly
-// (see widen).  Zeros take 8 - zero times the group's sum of x, which one more product with a matrix of
-// ones gives for all rows, when the group is complete and meets its scale.  Sums are FP32.
+// (see widen).  With zeros it is q less the nearest whole number c of 0 .. 15; what is left, c - zero times
+// the group's sum of x, which one more product with a matrix of ones gives for all rows, comes in when
+// the group is complete and meets its scale.  Sums are FP32.
 //
 // What bounds it at a few tokens is not memory but the instructions for a weight (230 for 4096 of them,
 // most on a pipe that takes one in two cycles) and, in short calls, the first loads and the join:
@@ -82,29 +83,47 @@ __device__ __forceinline__ uint32_t fma16(uint32_t a, uint32_t b, uint32_t c)
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// The eight elements of a word as A operands: pairs (0, 4), (1, 5), (2, 6), (3, 7) of q - 8, times a
+// The eight elements of a word as A operands: pairs (0, 4), (1, 5), (2, 6), (3, 7) of q - c, times a
 // unit.  A 16-bit word 0 .. 255 read as a number is that many times the smallest subnormal one, 2^-133
 // in BF16 and 2^-24 in FP16, so a masked nibble is q or 16 q in that measure; one fused multiply-add
-// brings it among the normal numbers and takes the 8 away, exactly.  (With the 8 left in, a row of
-// weights near zero would be the difference of two large sums; with x scaled instead, its range would end
-// early.)
+// brings it among the normal numbers and takes c away, exactly.  (With c left in, a row of weights
+// near zero would be the difference of two large sums; with x scaled instead, its range would end early.)
 template <bool BF16>
 struct W4Unit {
     static constexpr uint32_t kLow = BF16 ? 0x7F007F00u : 0x78007800u;     // 2^127, 2^15: a nibble
     static constexpr uint32_t kHigh = BF16 ? 0x7D007D00u : 0x68006800u;    // 2^123, 2^11: sixteen times it
     static constexpr uint32_t kOne = BF16 ? 0x3C803C80u : 0x18001800u;     // the unit: 2^-6, 2^-9
+    static constexpr uint32_t kMinusLow = BF16 ? 0xFF00FF00u : 0xF800F800u;    // -2^127, -2^15
+    static constexpr uint32_t kMinusHigh = BF16 ? 0xFD00FD00u : 0xE800E800u;
     static constexpr uint32_t kLess8 = BF16 ? 0xBE00BE00u : 0xA400A400u;   // -8 units
     static constexpr float kInverse = BF16 ? 64.0f : 512.0f;
 };
 template <bool BF16>
-__device__ __forceinline__ void widen(uint32_t w, uint32_t (&q)[4])
+__device__ __forceinline__ void widen(uint32_t w, uint32_t less, uint32_t (&q)[4])
 {
     using U = W4Unit<BF16>;
     const uint32_t v = w >> 8;
-    q[0] = fma16<BF16>(w & 0x000F000Fu, U::kLow, U::kLess8);
-    q[1] = fma16<BF16>(w & 0x00F000F0u, U::kHigh, U::kLess8);
-    q[2] = fma16<BF16>(v & 0x000F000Fu, U::kLow, U::kLess8);
-    q[3] = fma16<BF16>(v & 0x00F000F0u, U::kHigh, U::kLess8);
+    q[0] = fma16<BF16>(w & 0x000F000Fu, U::kLow, less);
+    q[1] = fma16<BF16>(w & 0x00F000F0u, U::kHigh, less);
+    q[2] = fma16<BF16>(v & 0x000F000Fu, U::kLow, less);
+    q[3] = fma16<BF16>(v & 0x00F000F0u, U::kHigh, less);
+}
+
+// The whole number of 0 .. 15 nearest to a zero (0 for NaN): above 2^23 the numbers are whole.
+__device__ __forceinline__ uint32_t nearest_q(float zero, float &c)
+{
+    const float at = fminf(fmaxf(zero, 0.0f), 15.0f) + 8388608.0f;
+    c = at - 8388608.0f;
+    return __float_as_uint(at) & 15u;
+}
+
+// -c units, c in bits 4 j .. 4 j + 3 of both halves of a word.
+template <bool BF16>
+__device__ __forceinline__ uint32_t minus_q(uint32_t c, int j)
+{
+    using U = W4Unit<BF16>;
+    const uint32_t v = j & 2 ? c >> 8 : c;
+    return j & 1 ? fma16<BF16>(v & 0x00F000F0u, U::kMinusHigh, 0u) : fma16<BF16>(v & 0x000F000Fu, U::kMinusLow, 0u);
 }
 
 __device__ __forceinline__ uint4 load_shared16(uint32_t addr)
@@ -176,7 +195,7 @@ __device__ __forceinline__ void store_cluster(uint32_t addr, float v)
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-template <int NT, int MT, int XR, int PER, int W, bool BF16>
+template <int NT, int MT, int XR, int PER, int W, bool BF16, bool ZEROS>
 __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int cluster)
 {
     using Cfg = W4Cfg<NT, MT, XR, PER, W>;
@@ -194,7 +213,7 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
     const int stride = cluster * W, begin = rank * W + warp;
     const int units = p.units, groups = p.groups, tiles = p.tiles;
     const int k = static_cast<int>(p.k), bytes = (k + 1) / 2, whole = k / kW4K;   // stages without an end of the row
-    const bool zeros = p.zeros != nullptr, s_f32 = p.s_f32 != 0;
+    const bool s_f32 = p.s_f32 != 0;
     const int tokens = p.tokens - tok0;                      // of this block, if fewer than kTokens
 
     const uint32_t mine = smem_u32(ring) + warp * (S * Cfg::kStageBytes);
@@ -290,7 +309,7 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
 #pragma unroll
         for (int i = 0; i < kSr; ++i) {
             load_group(p.scales, row_s[i], unit, raw_s[i]);
-            if (zeros)
+            if (ZEROS)
                 load_group(p.zeros, row_s[i], unit, raw_z[i]);
         }
     };
@@ -348,12 +367,23 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
 #pragma unroll
                 for (int j = 0; j < kGroups; ++j)
                     sc[(lane + 32 * i) * kGroups + j] = group_value(raw_s[i], j) * U::kInverse;
-            if (zeros) {
+            [[maybe_unused]] uint32_t less[2 * MT];              // rows g + 8 i: their c of each group, four bits apart
+            if constexpr (ZEROS) {
+                uint32_t c_of[kSr];
 #pragma unroll
-                for (int i = 0; i < kSr; ++i)
+                for (int i = 0; i < kSr; ++i) {
+                    c_of[i] = 0u;
 #pragma unroll
-                    for (int j = 0; j < kGroups; ++j)
-                        sc[(R + lane + 32 * i) * kGroups + j] = group_value(raw_z[i], j);
+                    for (int j = 0; j < kGroups; ++j) {
+                        const float zero = group_value(raw_z[i], j);
+                        float whole;
+                        c_of[i] |= nearest_q(zero, whole) << (4 * j);
+                        sc[(R + lane + 32 * i) * kGroups + j] = whole - zero;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i)
+                    less[i] = __shfl_sync(0xffffffffu, c_of[i / 4], g + 8 * (i & 3)) * 0x10001u;
             }
             __syncwarp();
             if (unit + stride < units)
@@ -374,6 +404,8 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const bool first = q % PER == 0;                 // of its group
+                if (PER == 1)                                    // a group at a time: more of them want too many registers
+                    __syncwarp();
                 if (q < 3)
                     fetch(q + 1);
                 uint32_t b[NT][4];
@@ -384,16 +416,20 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
                     b[nt][1] = __byte_perm(v.x, v.z, 0x7632);
                     b[nt][2] = __byte_perm(v.y, v.w, 0x5410);
                     b[nt][3] = __byte_perm(v.y, v.w, 0x7632);
-                    if (zeros) {
+                    if constexpr (ZEROS) {
                         mma_group<BF16>(first, off[nt], ones, b[nt][0], b[nt][1]);
                         mma_group<BF16>(false, off[nt], ones, b[nt][2], b[nt][3]);
                     }
                 }
+                uint32_t minus[2 * MT];                          // -c units
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i)
+                    minus[i] = ZEROS ? minus_q<BF16>(less[i], q / PER) : U::kLess8;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                     uint32_t lo[4], hi[4];
-                    widen<BF16>(w[q & 1][2 * i], lo);
-                    widen<BF16>(w[q & 1][2 * i + 1], hi);
+                    widen<BF16>(w[q & 1][2 * i], minus[2 * i], lo);
+                    widen<BF16>(w[q & 1][2 * i + 1], minus[2 * i + 1], hi);
                     const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
@@ -406,13 +442,16 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
                         const float s0 = at_s[16 * i * kGroups], s1 = at_s[(16 * i + 8) * kGroups];
-                        if (zeros) {                             // instead of the 8
+                        if constexpr (ZEROS) {                   // none where zeros are whole: 0 times infinity is no part
                             const float z0 = at_s[(R + 16 * i) * kGroups], z1 = at_s[(R + 16 * i + 8) * kGroups];
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                                for (int j = 0; j < 4; ++j)
-                                    acc[i][nt][j] = fmaf(8.0f - (j < 2 ? z0 : z1), off[nt][j & 1], acc[i][nt][j]);
+                                for (int j = 0; j < 4; ++j) {
+                                    const float z = j < 2 ? z0 : z1;
+                                    if (z != 0.0f)
+                                        acc[i][nt][j] = fmaf(z, off[nt][j & 1], acc[i][nt][j]);
+                                }
                         }
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
@@ -574,11 +613,11 @@ __global__ void __launch_bounds__(256) tcg_w4_twice_kernel(const W4Args p, uint1
     }
 }
 
-template <int NT, int MT, int XR, int PER, int W, bool BF16>
+template <int NT, int MT, int XR, int PER, int W, bool BF16, bool ZEROS>
 cudaError_t launch_one(W4Args a, int num_sms, cudaStream_t s)
 {
     using Cfg = W4Cfg<NT, MT, XR, PER, W>;
-    auto fn = tcg_w4_kernel<NT, MT, XR, PER, W, BF16>;
+    auto fn = tcg_w4_kernel<NT, MT, XR, PER, W, BF16, ZEROS>;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
     if (e != cudaSuccess)
         return e;
@@ -610,16 +649,22 @@ cudaError_t launch_one(W4Args a, int num_sms, cudaStream_t s)
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+template <int NT, int MT, int XR, int W, bool BF16, bool ZEROS>
+cudaError_t launch_group(const W4Args &a, int num_sms, cudaStream_t s)
+{
+    return a.group == 32 ? launch_one<NT, MT, XR, 1, W, BF16, ZEROS>(a, num_sms, s)
+         : a.group == 64 ? launch_one<NT, MT, XR, 2, W, BF16, ZEROS>(a, num_sms, s)
+                         : launch_one<NT, MT, XR, 4, W, BF16, ZEROS>(a, num_sms, s);
+}
+
 template <int NT, int MT, int XR, int W>
 cudaError_t launch_types(const W4Args &a, int num_sms, cudaStream_t s)
 {
     if (a.in_bf16)
-        return a.group == 32 ? launch_one<NT, MT, XR, 1, W, true>(a, num_sms, s)
-             : a.group == 64 ? launch_one<NT, MT, XR, 2, W, true>(a, num_sms, s)
-                             : launch_one<NT, MT, XR, 4, W, true>(a, num_sms, s);
-    return a.group == 32 ? launch_one<NT, MT, XR, 1, W, false>(a, num_sms, s)
-         : a.group == 64 ? launch_one<NT, MT, XR, 2, W, false>(a, num_sms, s)
-                         : launch_one<NT, MT, XR, 4, W, false>(a, num_sms, s);
+        return a.zeros ? launch_group<NT, MT, XR, W, true, true>(a, num_sms, s)
+                       : launch_group<NT, MT, XR, W, true, false>(a, num_sms, s);
+    return a.zeros ? launch_group<NT, MT, XR, W, false, true>(a, num_sms, s)
+                   : launch_group<NT, MT, XR, W, false, false>(a, num_sms, s);
 }
 
 }  // namespace

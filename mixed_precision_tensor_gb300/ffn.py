@@ -187,8 +187,8 @@ def linear_4bit(handle, x, w, scales, group, zeros=None, bias=None, act="none", 
         w = q[:, 0::2] | q[:, 1::2] << 4
 
     residual may be ``out`` itself.  Few tokens (up to 48, 64 of at most 2^24 weights, 128 of at
-    most 2^21; gated 128, 256 of at most 2^21) read the packed weights; with zeros an infinity in x then
-    makes its token's outputs NaN.  More tokens expand the weights in the handle's workspace, rounded
+    most 2^21; gated 128, 256 of at most 2^21) read the packed weights; an infinity in x then makes its
+    token's outputs NaN where zeros are no whole numbers.  More tokens expand the weights in the handle's workspace, rounded
     to x's type (gated ones in two parts).  Returns out.
     """
     t, k, dtype, dev = _input(x)

@@ -104,3 +104,62 @@ def test_infinity_in_x(handle, t, dtype):
     assert torch.equal(torch.isnan(out[1]), sign == 0) and bool((sign == 0).any())
     assert torch.equal(out[1][sign != 0].double(), sign[sign != 0] * float("inf"))
     assert torch.isfinite(out[0]).all() and torch.isfinite(out[2:]).all()
+
+
+def expected_with_zeros(x, q, scales, zeros, group):
+    """expected(), a weight's magnitude with what is left of its zero beside the nearest whole number of
+    0 .. 15: |q - c| + |c - zero|."""
+    k = x.shape[1]
+    at = torch.arange(k, device="cuda") // group
+    zero, s = zeros.double()[:, at], scales.double()[:, at].abs()
+    c = zero.clamp(0, 15).round()
+    want, _ = expected(x, q, scales, zeros, group)
+    return want, (k + 8) * (2.0 ** -23 * (x.double().abs() @ (((q - c).abs() + (c - zero).abs()) * s).t()) + 2.0 ** -149)
+
+
+@pytest.mark.parametrize("t", [1, 2, 7, 40, 60])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_weights_at_their_zeros(handle, t, group, dtype):
+    """Zeros from 0 to 15: rows of weights that are nearly all at theirs are no difference of large
+    sums, where x has a few entries far larger than the others."""
+    g = gen_of(t + group + 1)
+    k, n = 1184, 136
+    scales = (0.5 + torch.rand(n, -(-k // group), generator=g, device="cuda")).to(dtype)
+    zeros = (torch.rand(n, -(-k // group), generator=g, device="cuda") * 15).round().to(dtype)
+    q = zeros.repeat_interleave(group, 1)[:, :k].to(torch.uint8)
+    at = (torch.arange(n, device="cuda"), (torch.arange(n, device="cuda") * 67) % k)
+    q[at] = (q[at] + 1) % 16
+    x = positive(g, t, k, F32)
+    x = torch.where(torch.rand(k, generator=g, device="cuda") < 0.05, 3000 * x, x).to(dtype)
+    out = tcg.linear_4bit(handle, x, ref.pack(q), scales, group, zeros=zeros, out_dtype=F32)
+    within(out, *expected_with_zeros(x, q, scales, zeros, group), "out")
+
+
+@pytest.mark.parametrize("t", [1, 8, 40, 60])
+@pytest.mark.parametrize("dtype,kind", [(BF16, BF16), (BF16, F32), (F16, F16), (F16, F32)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+def test_zeros_of_any_size(handle, t, dtype, kind, group):
+    """Zeros that are no whole numbers, and beyond 0 .. 15."""
+    g = gen_of(35)
+    q, scales, _ = weights(g, 72, 544, group, kind)
+    zeros = (torch.randn(scales.shape, generator=g, device="cuda") * 12 + 8).to(kind)
+    zeros[5] = 1000.25
+    x = positive(g, t, 544, dtype)
+    out = tcg.linear_4bit(handle, x, ref.pack(q), scales, group, zeros=zeros, out_dtype=F32)
+    within(out, *expected_with_zeros(x, q, scales, zeros, group), "out")
+
+
+@pytest.mark.parametrize("t", [2, 8, 40])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_infinity_in_x_with_zeros(handle, t, dtype):
+    """As without zeros, where they are whole numbers."""
+    g = gen_of(36)
+    q, scales, zeros = weights(g, 72, 544, 32, dtype, "whole")
+    x = randn(g, t, 544, dtype=dtype)
+    x[1, 77] = float("-inf")
+    out = tcg.linear_4bit(handle, x, ref.pack(q), scales, 32, zeros=zeros)
+    sign = zeros[:, 77 // 32].double() - q[:, 77].double()
+    assert torch.equal(torch.isnan(out[1]), sign == 0) and bool((sign == 0).any())
+    assert torch.equal(out[1][sign != 0].double(), sign[sign != 0] * float("inf"))
+    assert torch.isfinite(out[0]).all() and torch.isfinite(out[2:]).all()

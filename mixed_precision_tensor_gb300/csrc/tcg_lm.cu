@@ -22,6 +22,13 @@
 //                  the tensor work of one product with twice the features, without its output
 //                  (16384 tokens, 4096 to 2 x 4096, both halves kept: 572 to 591 us in a graph, 1.86 to
 //                  1.92 PFLOP/s)
+//   kEpiGroupNarrow, kEpiGroupGated   the narrow kinds for weights that have a scale for each group of
+//                  K elements: an accumulator for each group, which meets its scale in FP32 on its
+//                  way to the sums in registers.  Bound by the thread that issues the products (four
+//                  and the waits of a block take it some 600 cycles, where 192 columns take the tensor core
+//                  192) and, in groups of 32, by that way: 4096 tokens of 4096 x 4096 take 160 us in groups
+//                  of 128, by kEpiWide without scales 85.  192 columns, as 256 leave a thread too few registers
+//                  (202 us for 169, the expansion included)
 //
 // What bounds it.  A 64-element block of K costs an SM 32 KiB of operands at tile 256 x 256,
 // loaded at 64 bytes a cycle in the 512 cycles that the tensor core takes for it; with both
@@ -96,7 +103,7 @@ struct LmUnit {
 // tiles, every cut tile instead gets the same number of pairs and the same K ranges, so that
 // tiles read the same blocks at the same time.)  A pair has at most one piece that starts
 // inside a tile (slot 2 c) and one that starts a tile without ending it (slot 2 c + 1).
-template <bool WIDE, int BN, bool RK, bool GATED>
+template <bool WIDE, int BN, bool RK, bool GATED, bool DENSE>
 struct LmWalk {
     // features of a tile: of the accumulator's columns (wide) or rows
     static constexpr int kFeats = (WIDE ? BN : 256) / (GATED ? 2 : 1);
@@ -158,7 +165,7 @@ struct LmWalk {
                 }
             }
         }
-        const int nulls = pl.null_tiles[0] + pl.null_tiles[1];
+        const int nulls = DENSE ? 0 : pl.null_tiles[0] + pl.null_tiles[1];
         if (null_i < nulls) {
             const int which = null_i >= pl.null_tiles[0] ? 1 : 0;
             int b, e;
@@ -187,7 +194,7 @@ struct LmWalk {
             place(p, tile - w.g * per, 0, p.rows, w);
             return;
         }
-        if (p.offsets) {
+        if (!DENSE && p.offsets) {
             while (tile >= ctl->cum[group + 1])
                 ++group;
             if (group != at) {
@@ -674,7 +681,7 @@ template <int EPI, int OUT, int BN, bool RK>
 __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
     tcg_lm_kernel(const __grid_constant__ LmMaps maps, const LmArgs p)
 {
-    constexpr bool WIDE = lm_wide(EPI), GATED = lm_gated(EPI);
+    constexpr bool WIDE = lm_wide(EPI), GATED = lm_gated(EPI), GROUP = lm_group(EPI);
     using Cfg = LmCfg<BN, WIDE>;
     constexpr int kStages = Cfg::kStages;
     constexpr int kAccBufs = Cfg::kAccBufs;
@@ -696,7 +703,7 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
         return FIT ? min(BN, (w.col_end - w.col0 + 31) & ~31) : BN;
     };
     constexpr int kSegBlocks = SEG ? 8 : 1 << 30;
-    using Walk = LmWalk<WIDE, BN, RK, GATED>;
+    using Walk = LmWalk<WIDE, BN, RK, GATED, GROUP>;
     // Features on the accumulator's rows: how many of them are this CTA's.
     constexpr int kRowFeats = GATED && !WIDE ? kBM / 2 : kBM;
 
@@ -856,35 +863,47 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
             while (ok && more) {
                 bool looked = false;                       // the next unit is known
                 int kb = w.kb0;
-                do {                                       // one accumulator per segment
-                    const int acc = it % kAccBufs;
+                // The next accumulator, once it is free.
+                auto take = [&](int &acc) {
+                    acc = it % kAccBufs;
                     const uint32_t acc_phase = (it / kAccBufs) & 1;
                     ++it;
-                    if (!wait_bounded<2>(smem_u32(&ctl->acc_empty[acc]), acc_phase ^ 1u, ctl, p,
-                                         kErrMmaAcc)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
-                    const uint32_t idesc = FIT ? (p.idesc & ~(0x3Fu << 17)) |
-                                                     (static_cast<uint32_t>(width(w) >> 3) << 17)
-                                               : p.idesc;
-                    const int first = kb, stop = SEG ? min(kb + kSegBlocks, w.kb1) : w.kb1;
-                    for (; kb < stop; ++kb) {
-                        if (!wait_bounded<2>(smem_u32(&ctl->full[stage]), phase, ctl, p, kErrMmaFull)) {
-                            ok = false;
+                    ok = wait_bounded<2>(smem_u32(&ctl->acc_empty[acc]), acc_phase ^ 1u, ctl, p, kErrMmaAcc);
+                    if (ok)
+                        tc_fence_after();
+                    return ok;
+                };
+                if constexpr (GROUP) {
+                    // An accumulator for each group of K: of two blocks of 64 or more, of one, or of
+                    // half a block.  A piece may begin or end inside a group.
+                    const int within = max(1, p.group_mmas / 4) - 1;        // of its group: low bits of a block's number
+                    const bool halves = p.group_mmas == 2;
+                    int acc = 0;
+                    if (kb >= w.kb1 && take(acc))
+                        mma_commit_pair_mc(smem_u32(&ctl->acc_full[acc]), 0x3);
+                    for (; kb < w.kb1 && ok; ++kb) {
+                        ok = wait_bounded<2>(smem_u32(&ctl->full[stage]), phase, ctl, p, kErrMmaFull);
+                        if (!ok)
                             break;
-                        }
                         tc_fence_after();
                         const uint64_t ad_s = a_desc0 + ((static_cast<uint32_t>(stage) * Cfg::kAStage) >> 4);
                         const uint64_t bd_s = b_desc0 + ((static_cast<uint32_t>(stage) * Cfg::kBStage) >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < kMmasPerStage; ++kk)
-                            mma_f16_pair(d_tmem, ad_s + a_off[kk], bd_s + b_off[kk], idesc,
-                                         (kb > first || kk > 0) ? 1u : 0u);
+                        for (int h = 0; h < 2; ++h) {
+                            const bool begins = h == 0 ? kb == w.kb0 || (kb & within) == 0 : halves;
+                            const bool ends = halves || (h == 1 && ((kb & within) == within || kb + 1 == w.kb1));
+                            if (begins && !take(acc))
+                                break;
+                            const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+                            mma_f16_pair(d_tmem, ad_s + a_off[2 * h], bd_s + b_off[2 * h], p.idesc, begins ? 0u : 1u);
+                            mma_f16_pair(d_tmem, ad_s + a_off[2 * h + 1], bd_s + b_off[2 * h + 1], p.idesc, 1u);
+                            if (ends)
+                                mma_commit_pair_mc(smem_u32(&ctl->acc_full[acc]), 0x3);
+                        }
+                        if (!ok)
+                            break;
                         mma_commit_pair_mc(smem_u32(&ctl->empty[stage]), 0x3);
-                        if (!looked) {                     // while the tensor core is busy
+                        if (!looked) {
                             more = walk.next(p, ctl, next_w);
                             looked = true;
                         }
@@ -893,10 +912,43 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                             phase ^= 1u;
                         }
                     }
-                    if (!ok)
-                        break;
-                    mma_commit_pair_mc(smem_u32(&ctl->acc_full[acc]), 0x3);
-                } while (kb < w.kb1);
+                } else {
+                    do {                                   // one accumulator per segment
+                        int acc;
+                        if (!take(acc))
+                            break;
+                        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+                        const uint32_t idesc = FIT ? (p.idesc & ~(0x3Fu << 17)) |
+                                                         (static_cast<uint32_t>(width(w) >> 3) << 17)
+                                                   : p.idesc;
+                        const int first = kb, stop = SEG ? min(kb + kSegBlocks, w.kb1) : w.kb1;
+                        for (; kb < stop; ++kb) {
+                            if (!wait_bounded<2>(smem_u32(&ctl->full[stage]), phase, ctl, p, kErrMmaFull)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            const uint64_t ad_s = a_desc0 + ((static_cast<uint32_t>(stage) * Cfg::kAStage) >> 4);
+                            const uint64_t bd_s = b_desc0 + ((static_cast<uint32_t>(stage) * Cfg::kBStage) >> 4);
+#pragma unroll
+                            for (int kk = 0; kk < kMmasPerStage; ++kk)
+                                mma_f16_pair(d_tmem, ad_s + a_off[kk], bd_s + b_off[kk], idesc,
+                                             (kb > first || kk > 0) ? 1u : 0u);
+                            mma_commit_pair_mc(smem_u32(&ctl->empty[stage]), 0x3);
+                            if (!looked) {                     // while the tensor core is busy
+                                more = walk.next(p, ctl, next_w);
+                                looked = true;
+                            }
+                            if (++stage == kStages) {
+                                stage = 0;
+                                phase ^= 1u;
+                            }
+                        }
+                        if (!ok)
+                            break;
+                        mma_commit_pair_mc(smem_u32(&ctl->acc_full[acc]), 0x3);
+                    } while (kb < w.kb1);
+                }
                 if (!looked)
                     more = walk.next(p, ctl, next_w);
                 w = next_w;
@@ -972,7 +1024,10 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
             const int col_part = w.col0 + part * (GATED && WIDE ? kPart / 2 : kPart);
             const bool cut = w.slot >= 0;
             const bool empty_k = w.kb0 >= w.kb1;
-            const int segments = SEG ? (w.kb1 - w.kb0 + kSegBlocks - 1) / kSegBlocks : 1;
+            // GROUP: the first of the unit's groups, which may have begun in the piece before
+            const int group0 = GROUP ? 4 * w.kb0 / p.group_mmas : 0;
+            const int segments = GROUP ? (4 * w.kb1 + p.group_mmas - 1) / p.group_mmas - group0
+                               : SEG   ? (w.kb1 - w.kb0 + kSegBlocks - 1) / kSegBlocks : 1;
             if constexpr (FIT) {
                 // --------------------------- tokens on the columns, many: the parts take
                 // every second 32 of them
@@ -1007,7 +1062,7 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                         release();
                     finish_narrow<OUT, 32>(p, z, w, row, w.col0 + c * 32, alpha, bias);
                 }
-            } else if constexpr (EPI == kEpiNarrow || EPI == kEpiXentNarrow || EPI == kEpiGatedNarrow) {
+            } else if constexpr (!WIDE) {
                 // ------------------------------------------------ tokens on the columns
                 constexpr int kCols = kPart < 32 ? kPart : 32;
                 float sum[kPart];
@@ -1015,17 +1070,74 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                 for (int j = 0; j < kPart; ++j)
                     sum[j] = 0.0f;
                 float bias = 0.0f;
-                if (EPI == kEpiNarrow && p.bias && row < p.rows && w.g >= 0) {
+                if ((EPI == kEpiNarrow || EPI == kEpiGroupNarrow) && p.bias && row < p.rows && w.g >= 0) {
                     const int64_t i = static_cast<int64_t>(w.g) * p.rows + row;
                     bias = p.bias_f32 ? static_cast<const float *>(p.bias)[i]
                                       : load16(p.bias, i, p.in_bf16);
                 }
+                // This row's scale in a group, and what is left of its zero: once for a group that
+                // two pieces share.
+                [[maybe_unused]] auto load_scale = [&](int group, float &scale, float &rest) {
+                    scale = rest = 0.0f;
+                    if (row < p.rows && group < min(p.k_groups, group0 + segments)) {
+                        const int64_t at = group * p.group_ld + row + (GATED && lane >= 16 ? p.rows : 0);
+                        scale = __ldg(p.group_scale + at);
+                        if (p.group_rest && group * p.group_mmas >= 4 * w.kb0)
+                            rest = __ldg(p.group_rest + at);
+                    }
+                };
+                [[maybe_unused]] float scales[2], rests[2];
+                if constexpr (GROUP) {
+                    load_scale(group0, scales[0], rests[0]);
+                    load_scale(group0 + 1, scales[1], rests[1]);
+                }
                 bool stop = false;
                 int seg = 0;
                 do {
+                    [[maybe_unused]] const int group = group0 + seg;
+                    [[maybe_unused]] const float scale = scales[0], rest = rests[0];
+                    if constexpr (GROUP) {                 // two groups ahead of their use
+                        scales[0] = scales[1];
+                        rests[0] = rests[1];
+                        load_scale(group + 2, scales[1], rests[1]);
+                    }
                     if (!acquire()) {
                         stop = true;
                         break;
+                    }
+                    if constexpr (GROUP) {
+                        const uint32_t taddr = tmem_part + static_cast<uint32_t>(it % kAccBufs * BN);
+                        const bool any_rest = __any_sync(0xffffffffu, rest != 0.0f);
+                        constexpr int kStep = 32;                        // columns under way
+                        const F2 scale2 = f2(scale);
+#pragma unroll
+                        for (int c0 = 0; c0 < kPart; c0 += kStep) {
+                            uint32_t v[kStep];
+                            tmem_ld_32x32b_x32(taddr + c0, v);
+                            tmem_ld_done(v);
+                            if (c0 + kStep == kPart)
+                                release();
+                            if (empty_k)
+                                continue;
+                            if (any_rest) {
+                                const float4 *xs = reinterpret_cast<const float4 *>(p.group_sum + group * p.sum_ld + col_part + c0);
+#pragma unroll
+                                for (int j = 0; j < kStep; j += 4) {
+                                    const float4 x = __ldg(xs + j / 4);
+                                    if (rest != 0.0f) {    // 0 times infinity is no part
+                                        v[j] = __float_as_uint(fmaf(rest, x.x, __uint_as_float(v[j])));
+                                        v[j + 1] = __float_as_uint(fmaf(rest, x.y, __uint_as_float(v[j + 1])));
+                                        v[j + 2] = __float_as_uint(fmaf(rest, x.z, __uint_as_float(v[j + 2])));
+                                        v[j + 3] = __float_as_uint(fmaf(rest, x.w, __uint_as_float(v[j + 3])));
+                                    }
+                                }
+                            }
+#pragma unroll
+                            for (int j = 0; j < kStep; j += 2)
+                                split2(fma2(scale2, f2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])),
+                                            f2(sum[c0 + j], sum[c0 + j + 1])), sum[c0 + j], sum[c0 + j + 1]);
+                        }
+                        continue;
                     }
                     uint32_t v[kPart];
                     const uint32_t taddr = tmem_part + static_cast<uint32_t>(it % kAccBufs * BN);
@@ -1076,12 +1188,12 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                         }
                     }
                 }
-                if constexpr (EPI == kEpiNarrow) {
+                if constexpr (EPI == kEpiNarrow || EPI == kEpiGroupNarrow) {
 #pragma unroll
                     for (int c = 0; c < kPart; c += kCols)
                         finish_narrow<OUT>(p, *reinterpret_cast<float (*)[kCols]>(sum + c), w, row,
                                            col_part + c, alpha, bias);
-                } else if constexpr (EPI == kEpiGatedNarrow) {
+                } else if constexpr (GATED) {
 #pragma unroll
                     for (int c = 0; c < kPart; c += kCols)
                         finish_gated_narrow<OUT>(p, *reinterpret_cast<float (*)[kCols]>(sum + c), w, row,
@@ -1394,6 +1506,13 @@ LmKernelFn linear_fn(int epi, int bn, bool rk)
                      : tcg_lm_kernel<kEpiWide, OUT, 256, false>;
 }
 
+template <int OUT, int EPI>
+LmKernelFn group_fn(int bn)
+{
+    return bn == 64 ? tcg_lm_kernel<EPI, OUT, 64, false>
+         : bn == 128 ? tcg_lm_kernel<EPI, OUT, 128, false> : tcg_lm_kernel<EPI, OUT, 192, false>;
+}
+
 template <int OUT>
 LmKernelFn gated_fn(int epi, int bn)
 {
@@ -1413,6 +1532,12 @@ LmKernelFn lm_fn(int epi, int out_kind, int bn, bool rk)
         return tcg_lm_kernel<kEpiXentNarrow, kOutF32, 32, false>;
     if (epi == kEpiXentGrad)
         return tcg_lm_kernel<kEpiXentGrad, kOutF16, 256, false>;
+    if (epi == kEpiGroupNarrow)
+        return out_kind == kOutF32 ? group_fn<kOutF32, kEpiGroupNarrow>(bn)
+             : out_kind == kOutF16 ? group_fn<kOutF16, kEpiGroupNarrow>(bn) : group_fn<kOutBF16, kEpiGroupNarrow>(bn);
+    if (epi == kEpiGroupGated)
+        return out_kind == kOutF32 ? group_fn<kOutF32, kEpiGroupGated>(bn)
+             : out_kind == kOutF16 ? group_fn<kOutF16, kEpiGroupGated>(bn) : group_fn<kOutBF16, kEpiGroupGated>(bn);
     if (lm_gated(epi))
         return out_kind == kOutF32 ? gated_fn<kOutF32>(epi, bn)
              : out_kind == kOutF16 ? gated_fn<kOutF16>(epi, bn) : gated_fn<kOutBF16>(epi, bn);

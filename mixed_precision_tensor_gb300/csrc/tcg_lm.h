@@ -30,13 +30,18 @@ enum LmEpi {
     kEpiXentNarrow = 3, // the same; vocabulary x tokens
     kEpiXentGrad = 4,   // (exp(logit - lse) - [target]) * upstream gradient, 16-bit
     kEpiGatedNarrow = 5, // act(g) u of two products of the same tokens; features x tokens
-    kEpiGatedWide = 6   // the same; tokens x features
+    kEpiGatedWide = 6,  // the same; tokens x features
+    kEpiGroupNarrow = 7, // kEpiNarrow and kEpiGatedNarrow with a scale per feature and group of K
+    kEpiGroupGated = 8
 };
 
 // A gated product's tile holds both halves of its features: in the wide kind BN / 2 columns of
 // g, then those of u (each CTA of the pair loads the rows of one half); in the narrow kind 16
 // rows of g, then the 16 of u, four times a CTA (a warp of the epilogue has both).
-__host__ __device__ constexpr bool lm_gated(int epi) { return epi == kEpiGatedNarrow || epi == kEpiGatedWide; }
+__host__ __device__ constexpr bool lm_gated(int epi) {
+    return epi == kEpiGatedNarrow || epi == kEpiGatedWide || epi == kEpiGroupGated;
+}
+__host__ __device__ constexpr bool lm_group(int epi) { return epi == kEpiGroupNarrow || epi == kEpiGroupGated; }
 
 enum LmAct { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
 
@@ -76,6 +81,16 @@ struct LmArgs {
     int act;                   // LmAct
     float *part;               // partial sums of cut tiles; nullptr: never cut
     uint32_t *cnt;             // their arrival counters, zero before and after a call
+
+    // scales per group of K: the product is the sum over the groups of
+    // group_scale (the group's product + group_rest times the group's sum of x)
+    int group_mmas;            // K elements of a group / 16
+    int k_groups;
+    const float *group_scale;  // [group][row of W], group_ld apart
+    const float *group_rest;   // the same; nullptr: none
+    int64_t group_ld;
+    const float *group_sum;    // [group][token], sum_ld apart (whole tiles of tokens)
+    int64_t sum_ld;
 
     // cross entropy: the features are vocabulary entries
     const int64_t *targets;
@@ -136,8 +151,8 @@ cudaError_t launch_group_maps(const LmMaps &maps, const int64_t *offsets, int gr
                               CUtensorMap *out, cudaStream_t s);
 
 // Launchers (tcg_lm.cu).  out_kind: type of D.  bn: 32, 64, 128 or 256 (kEpiNarrow), 64, 128 or 256
-// (kEpiWide), 32, 64 or 128 (kEpiGatedNarrow), 128 or 256 (kEpiGatedWide), 256 (K ragged,
-// kEpiXentStats, kEpiXentGrad), 32 (kEpiXentNarrow).
+// (kEpiWide), 32, 64 or 128 (kEpiGatedNarrow), 128 or 256 (kEpiGatedWide), 64, 128 or 192
+// (kEpiGroupNarrow, kEpiGroupGated), 256 (K ragged, kEpiXentStats, kEpiXentGrad), 32 (kEpiXentNarrow).
 cudaError_t launch_lm(const LmMaps &maps, const LmArgs &a, int epi, int out_kind, int bn,
                       int grid, cudaStream_t s);
 int lm_max_resident_ctas(int num_sms);
@@ -256,10 +271,14 @@ struct W4Args {
     int tiles, units, groups;  // row tiles, stages and groups of a row, by launch_w4
 };
 cudaError_t launch_w4(const W4Args &a, int num_sms, cudaStream_t s);
-// The weights as the type of X, rounded once: rows x k, ldo elements apart, zeros up to a multiple of
-// eight columns.  lo > 0: from column lo on what the rounding left; and X twice in a row to match.
-cudaError_t launch_w4_expand(const W4Args &a, void *out, int64_t ldo, int64_t lo, int num_sms, cudaStream_t s);
-cudaError_t launch_w4_twice(const W4Args &a, void *out, int64_t ldo, int64_t lo, cudaStream_t s);
+// For the product of many tokens: the weights as the type of X without their scales, q less the whole
+// number nearest to the zero (exact, in a unit of 2^-6 or 2^-9), ldo elements apart; and for each group of
+// K [group][row], ld_t apart (a multiple of four), the scale over that unit and, with zeros, what is left
+// of the zero.
+cudaError_t launch_w4_expand(const W4Args &a, void *out, int64_t ldo, float *scale, float *rest, int64_t ld_t,
+                             int num_sms, cudaStream_t s);
+// Each group's sum of X, [group][token].
+cudaError_t launch_w4_sums(const W4Args &a, float *out, int64_t ld, cudaStream_t s);
 
 // dZ = dD * act'(Z) and per-group sums of its rows; see tcg_epi_backward_kernel.  part:
 // (ceil(cols / chunk) + groups) * m floats.

@@ -58,6 +58,7 @@ struct Product {
     tcgEpilogue_t epi = {};
     int lm_epi = -1;                        // kEpiXent*, or chosen by shape_of
     bool gated = false;                     // W holds feats rows of g, then those of u
+    bool grouped_k = false;                 // scales per group of K (kEpiGroup*)
     int64_t w_rows() const { return gated ? 2 * feats : feats; }
 };
 
@@ -70,7 +71,10 @@ struct Shape {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-bool is_narrow(int epi) { return epi == kEpiNarrow || epi == kEpiXentNarrow || epi == kEpiGatedNarrow; }
+bool is_narrow(int epi)
+{
+    return epi == kEpiNarrow || epi == kEpiXentNarrow || epi == kEpiGatedNarrow || lm_group(epi);
+}
 
 // The most tiles a call can have.
 int64_t max_tiles(const Product &p, int epi, int bn)
@@ -115,12 +119,41 @@ Shape shape_of(tcgContext *h, const Product &p)
 {
     Shape s;
     const int64_t P = pairs_of(h), nkb = ceil_div(p.k, 64);
+    // The tile width with the least predicted time, in the time of a K block at the first width:
+    // `cost` of it at the others.
+    auto best_of = [&](std::initializer_list<int> widths, auto cost_of, int least = 0) {
+        int found = *widths.begin();
+        double best = 1e300;
+        for (int bn : widths) {
+            if (bn < least)
+                break;
+            const double cost = cost_of(bn);
+            const int64_t tiles = max_tiles(p, s.epi, bn), rest = tiles % P;
+            int64_t share = ceil_div(rest * nkb, P);
+            share = share < min_share(nkb, bn) ? min_share(nkb, bn) : share;
+            double t = static_cast<double>(tiles / P * nkb);
+            if (rest)
+                t += nkb - share >= gain_of(bn) ? static_cast<double>(share) + gain_of(bn) / cost
+                                                : static_cast<double>(nkb);
+            t = t * cost + 12.0 * bn / 256;
+            if (t < best) {
+                best = t;
+                found = bn;
+            }
+        }
+        return found;
+    };
     if (p.ragged_k) {
         s.epi = kEpiWide;
         s.bn = 256;
     } else if (p.lm_epi >= 0) {
         s.epi = p.lm_epi;
         s.bn = p.lm_epi == kEpiXentNarrow ? 32 : 256;
+    } else if (p.grouped_k) {
+        s.epi = p.gated ? kEpiGroupGated : kEpiGroupNarrow;
+        // Per tile and block 0.55, 0.44 and 0.37 us at groups of 128: the one thread that issues
+        // the products and the accumulators' way to registers, not loads, bound them.
+        s.bn = best_of({192, 128, 64}, [](int bn) { return bn == 192 ? 1.0 : (bn == 128 ? 0.8 : 0.68); });
     } else {
         const int64_t per = p.offsets ? p.tokens / p.groups : p.tokens;
         const int narrow_bn = per <= 32 ? 32 : (per <= 64 ? 64 : 128);
@@ -153,27 +186,10 @@ Shape shape_of(tcgContext *h, const Product &p)
             s.epi = kEpiNarrow;
             s.bn = 256;
         } else {
-            // Tokens on the rows: the tile width with the least predicted time, in the time of
-            // a K block at width 256.  A block costs the 16 KiB of A and bn / 16 KiB of B that an
+            // Tokens on the rows.  A block costs the 16 KiB of A and bn / 16 KiB of B that an
             // SM loads for it, at 64 bytes a cycle: 512, 384 or 320 cycles.
             s.epi = p.gated ? kEpiGatedWide : kEpiWide;
-            s.bn = 256;
-            double best = 1e300;
-            for (int bn = 256; bn >= least; bn /= 2) {
-                const double cost = bn == 256 ? 1.0 : (bn == 128 ? 0.75 : 0.625);
-                const int64_t tiles = max_tiles(p, s.epi, bn), rest = tiles % P;
-                int64_t share = ceil_div(rest * nkb, P);
-                share = share < min_share(nkb, bn) ? min_share(nkb, bn) : share;
-                double t = static_cast<double>(tiles / P * nkb);
-                if (rest)
-                    t += nkb - share >= gain_of(bn) ? static_cast<double>(share) + gain_of(bn) / cost
-                                                    : static_cast<double>(nkb);
-                t = t * cost + 12.0 * bn / 256;
-                if (t < best) {
-                    best = t;
-                    s.bn = bn;
-                }
-            }
+            s.bn = best_of({256, 128, 64}, [](int bn) { return bn == 256 ? 1.0 : (bn == 128 ? 0.75 : 0.625); }, least);
         }
     }
     s.tiles = max_tiles(p, s.epi, s.bn);
@@ -316,7 +332,7 @@ bool few_tokens(int64_t tokens, int64_t feats, int64_t k)
 // and at most four tokens, or, grouped, rows that are few for the number of experts.
 bool few(const Product &p)
 {
-    if (p.ragged_k || !p.x_kmajor || !p.w_kmajor || p.k == 0 || p.lm_epi >= 0 || p.alpha_dev)
+    if (p.ragged_k || !p.x_kmajor || !p.w_kmajor || p.k == 0 || p.lm_epi >= 0 || p.alpha_dev || p.grouped_k)
         return false;
     if (!p.offsets)
         return few_tokens(p.tokens, p.w_rows(), p.k);
@@ -764,17 +780,18 @@ bool bad_rows(const void *p, int64_t ld, int64_t cols, int es) { return !aligned
 
 // --------------------------------------------------------------------- 4-bit weights
 // Whether the packed weights are read as they are, once for every 16 tokens, or expanded to 16 bits
-// for the product of many tokens (us in a graph, as they are / expanded):
+// for the product of many tokens (us in a graph, groups of 128, as they are / expanded):
 //                 tokens   32            48            64            128
-//    1024 x  1024          4.2 / 10.2    4.2 / 12.2    4.3 / 13.2    6.9 / 14.2
-//    4096 x  4096         12.8 / 20.9   17.7 / 22.5   22.7 / 23.4   37.5 / 34.1
-//   16384 x  4096         40.9 / 60.0   62.0 / 63.5   77.8 / 64.2
-//    4096 x 16384         35.1 / 59.4   50.9 / 63.4   66.9 / 64.7
-// Gated products, whose expanded weights are twice as many (2 x 512 x 1024, 2 x 2048 x 4096, 2 x 8192
-// x 4096 and 2 x 2048 x 16384):
-//    64 tokens   3.7 / 14.8   20.8 / 33.7   67 / 108    63 / 109
-//   128          5.8 / 21.4   34.5 / 45.6   126 / 116   109 / 123
-//   256         10.1 / 16.9   70.9 / 42.3   263 / 115   229 / 138
+//    1024 x  1024          3.5 / 11.2    3.4 / 11.2    3.5 / 11.7    5.6 / 12.3
+//    4096 x  4096         10.8 / 21.7   15.1 / 21.7   19.3 / 22.2   32.2 / 27.5
+//   16384 x  4096         32.2 / 63.3   49.4 / 63.6   62.3 / 64.6    118 / 62.6
+//    4096 x 16384         30.0 / 62.2   43.6 / 62.7   57.2 / 63.3   98.2 / 72.4
+// Gated products (2 x 512 x 1024, 2 x 2048 x 4096, 2 x 8192 x 4096 and 2 x 2048 x 16384):
+//    64 tokens   3.3 / 12.6   19.3 / 22.7   62.1 / 66.1   57.1 / 66.1
+//   128          5.4 / 13.2   32.1 / 28.2    118 / 62.5   98.2 / 74.0
+//   256          9.4 / 13.3   66.4 / 33.2    246 / 89.1    207 / 96.3
+// Their limit of 128 tokens, which callers rely on for needing no workspace, is from a time when
+// expanded weights cost twice as much.
 bool w4_packed(int64_t tokens, int64_t rows, int64_t k, bool gated)
 {
     if (gated)
@@ -783,27 +800,30 @@ bool w4_packed(int64_t tokens, int64_t rows, int64_t k, bool gated)
            (tokens <= 128 && rows * k <= (int64_t(1) << 21));
 }
 
-// The product of the expanded weights, without its pointers, and its workspace: the weights (of a
-// gated product in two parts, `lo` columns apart), then X twice in a row, what the product needs.
+// The product of the expanded weights, without its pointers, and its workspace: the weights, their
+// scales and what is left of their zeros, the sums of X, what the product needs.  Room for the smallest groups.
 struct W4Plan {
     Product p;
-    int64_t lo;
-    size_t w_bytes, x_bytes, total;
+    int64_t ld_t, ld_sum;                   // between the groups' scales; sums
+    size_t w_bytes, t_bytes, sum_bytes, total;
 };
 
 W4Plan w4_plan(tcgContext *h, int64_t m, int64_t n, int64_t k, bool gated)
 {
     W4Plan pl;
-    const int64_t k8 = (k + 7) / 8 * 8;
-    pl.lo = gated ? k8 : 0;
+    const int64_t rows = gated ? 2 * m : m, groups = ceil_div(k, 32);
     pl.p.feats = m;
     pl.p.tokens = n;
-    pl.p.k = gated ? 2 * k8 : k;
+    pl.p.k = k;
     pl.p.gated = gated;
-    pl.p.ldw = k8 + pl.lo;
-    pl.w_bytes = pad256(static_cast<size_t>(gated ? 2 * m : m) * pl.p.ldw * 2);
-    pl.x_bytes = gated ? pad256(static_cast<size_t>(n) * pl.p.ldw * 2) : 0;
-    pl.total = pl.w_bytes + pl.x_bytes + product_ws(h, pl.p);
+    pl.p.grouped_k = true;
+    pl.p.ldw = (k + 7) / 8 * 8;
+    pl.ld_t = (rows + 3) / 4 * 4;
+    pl.ld_sum = ceil_div(n, 64) * 64 + 192;          // whole tiles of any width
+    pl.w_bytes = pad256(static_cast<size_t>(rows) * pl.p.ldw * 2);
+    pl.t_bytes = pad256(static_cast<size_t>(groups) * pl.ld_t * sizeof(float));
+    pl.sum_bytes = static_cast<size_t>(groups) * pl.ld_sum * sizeof(float);
+    pl.total = pl.w_bytes + 2 * pl.t_bytes + pl.sum_bytes + product_ws(h, pl.p);
     return pl;
 }
 
@@ -1620,22 +1640,32 @@ tcgStatus_t tcg_gemm_4bit(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int64_
     p.in = Btype;
     p.out = Dtype;
     p.W = ws;
-    p.X = gated ? at + pl.w_bytes : B;
-    p.ldx = gated ? p.ldw : ldb;
+    p.X = B;
+    p.ldx = ldb;
     p.D = D;
     p.ldd = ldd;
     p.epi = epi;
+    LmArgs more{};
+    float *scale = reinterpret_cast<float *>(at + pl.w_bytes), *rest = scale + pl.t_bytes / sizeof(float);
+    float *sums = rest + pl.t_bytes / sizeof(float);
+    more.group_mmas = static_cast<int>(group / 16);
+    more.k_groups = static_cast<int>(ceil_div(k, group));
+    more.group_scale = scale;
+    more.group_rest = zeros ? rest : nullptr;
+    more.group_ld = pl.ld_t;
+    more.group_sum = sums;
+    more.sum_ld = pl.ld_sum;
     if (k > 0) {
-        cudaError_t e = launch_w4_expand(a, ws, p.ldw, pl.lo, h->num_sms, h->stream);
-        if (e == cudaSuccess && gated)
-            e = launch_w4_twice(a, at + pl.w_bytes, p.ldw, pl.lo, h->stream);
-        h->launches += gated ? 2 : 1;
+        cudaError_t e = launch_w4_expand(a, ws, p.ldw, scale, rest, pl.ld_t, h->num_sms, h->stream);
+        if (e == cudaSuccess && zeros)
+            e = launch_w4_sums(a, sums, pl.ld_sum, h->stream);
+        h->launches += zeros ? 2 : 1;
         if (e != cudaSuccess) {
             cudaGetLastError();
             return TCG_STATUS_EXECUTION_FAILED;
         }
     }
-    return queue(h, p, at + pl.w_bytes + pl.x_bytes);
+    return queue(h, p, at + pl.w_bytes + 2 * pl.t_bytes + pl.sum_bytes, more);
 }
 
 tcgStatus_t tcg_gemm_4bit_workspace_size(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int gated, size_t *bytes)

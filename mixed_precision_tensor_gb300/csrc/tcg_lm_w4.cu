@@ -1,4 +1,5 @@
-// tcg_lm_w4.cu -- products of a few tokens with 4-bit weights (sm_103a).
+// tcg_lm_w4.cu -- products of a few tokens with 4-bit weights (sm_103a), and for many tokens the
+// weights as operands of tcg_lm.cu.
 //
 //   z[t][f] = sum over groups of s[f][g] (sum over k of g of (q[f][k] - zero[f][g]) x[t][k])
 //
@@ -524,18 +525,19 @@ __global__ void __launch_bounds__(W * 32, 1) tcg_w4_kernel(const W4Args p, int c
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// The weights as the type of x: FP32, rounded once, and (lo > 0) what the rounding left, lo columns
-// further on.  Eight elements of a row a thread, so that a warp writes 512 bytes side by side, and
-// kExpandRows rows at a time, their loads before the first store.
-//
-// The second part is for gated products: one rounding of the weights takes a product's 2-norm error
-// from 0.00021 to 0.00025 or 0.00029 of the result in FP16 (the output's own rounding is the first
-// figure), but act(g) u, which has it twice, to 0.00033; with both parts, and x beside itself, it
-// stays at 0.00021.
+// The weights as operands of the product of many tokens: q - c as above, the scales and what is left of
+// the zeros beside them for its epilogue.  Nothing is rounded: weights times scales would be, to the 8
+// or 11 bits of x's type (2-norm error 0.0019 to 0.0024 of the result in BF16, the output's own rounding
+// being 0.0017), and where scales are small or large would leave its range.  Eight elements of a row a thread,
+// so that a warp writes 512 bytes side by side, and kExpandRows rows at a time, their loads before the first
+// store.  What lies past a row's end is not read by the product.
 constexpr int kExpandRows = 4;
 template <bool BF16>
-__global__ void __launch_bounds__(256) tcg_w4_expand_kernel(const W4Args p, uint16_t *__restrict__ out, int64_t ldo, int lo)
+__global__ void __launch_bounds__(256)
+    tcg_w4_expand_kernel(const W4Args p, uint16_t *__restrict__ out, int64_t ldo, float *__restrict__ scale,
+                         float *__restrict__ rest, int64_t ld_t)
 {
+    using U = W4Unit<BF16>;
     griddep_launch_dependents();
     griddep_wait();
     const int i = blockIdx.x * 256 + threadIdx.x, k = static_cast<int>(p.k), left = k - i * 8;
@@ -543,6 +545,7 @@ __global__ void __launch_bounds__(256) tcg_w4_expand_kernel(const W4Args p, uint
         return;
     const int groups = (k + p.group - 1) / p.group;
     const int g = i >> (p.group == 32 ? 2 : (p.group == 64 ? 3 : 4));
+    const bool first = i * 8 == g * p.group;                 // of its group
     for (int64_t row0 = static_cast<int64_t>(blockIdx.y) * kExpandRows; row0 < p.rows;
          row0 += static_cast<int64_t>(gridDim.y) * kExpandRows) {
         uint32_t u[kExpandRows], s[kExpandRows], z[kExpandRows];
@@ -557,59 +560,55 @@ __global__ void __launch_bounds__(256) tcg_w4_expand_kernel(const W4Args p, uint
                 for (int j = 0; 2 * j < left; ++j)
                     u[r] |= static_cast<uint32_t>(w[j]) << (8 * j);
             }
-            s[r] = load_raw(p.scales, row * groups + g, p.s_f32);
+            s[r] = first ? load_raw(p.scales, row * groups + g, p.s_f32) : 0u;
             z[r] = p.zeros ? load_raw(p.zeros, row * groups + g, p.s_f32) : 0u;
         }
+        float sc[kExpandRows], rs[kExpandRows];
 #pragma unroll
         for (int r = 0; r < kExpandRows; ++r) {
+            const float zero = p.zeros ? raw_value<BF16>(z[r], p.s_f32) : 8.0f;
+            float c;
+            const uint32_t whole = nearest_q(zero, c);
+            sc[r] = raw_value<BF16>(s[r], p.s_f32) * U::kInverse;
+            rs[r] = (c - zero) * (1.0f / U::kInverse);
             if (row0 + r >= p.rows)
-                break;
-            const float f = raw_value<BF16>(s[r], p.s_f32), zero = p.zeros ? raw_value<BF16>(z[r], p.s_f32) : 8.0f;
-            uint16_t *o = out + (row0 + r) * ldo + i * 8;        // ldo: a multiple of 8
-            // a nibble under the exponent of 2^23 is 2^23 + q (conversions of integers are slower)
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                v[e] = e < left ? (__uint_as_float(u[r] >> (4 * e) & 15u | 0x4B000000u) - 8388608.0f - zero) * f : 0.0f;
-            const uint4 hi = make_uint4(pack16(v[0], v[1], BF16), pack16(v[2], v[3], BF16), pack16(v[4], v[5], BF16),
-                                        pack16(v[6], v[7], BF16));
-            *reinterpret_cast<uint4 *>(o) = hi;
-            if (lo) {
-                float h[8];
-                unpack16<BF16>(hi, h);
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] -= h[e];
-                *reinterpret_cast<uint4 *>(o + lo) = make_uint4(pack16(v[0], v[1], BF16), pack16(v[2], v[3], BF16),
-                                                                pack16(v[4], v[5], BF16), pack16(v[6], v[7], BF16));
-            }
+                continue;
+            uint32_t q[4];
+            widen<BF16>(u[r], minus_q<BF16>(whole * 0x10001u, 0), q);
+            *reinterpret_cast<uint4 *>(out + (row0 + r) * ldo + i * 8) =          // ldo: a multiple of 8
+                make_uint4(__byte_perm(q[0], q[1], 0x5410), __byte_perm(q[2], q[3], 0x5410),
+                           __byte_perm(q[0], q[1], 0x7632), __byte_perm(q[2], q[3], 0x7632));
+        }
+        if (first) {
+            *reinterpret_cast<float4 *>(scale + g * ld_t + row0) = make_float4(sc[0], sc[1], sc[2], sc[3]);
+            if (p.zeros)
+                *reinterpret_cast<float4 *>(rest + g * ld_t + row0) = make_float4(rs[0], rs[1], rs[2], rs[3]);
         }
     }
 }
 
-// x twice in a row, for weights in two parts: from columns 0 and lo on, zeros up to the second.
-__global__ void __launch_bounds__(256) tcg_w4_twice_kernel(const W4Args p, uint16_t *__restrict__ out, int64_t ldo, int lo)
+// Eight elements of a token a thread; a group is 4, 8 or 16 lanes of a warp.
+template <bool BF16>
+__global__ void __launch_bounds__(256) tcg_w4_sums_kernel(const W4Args p, float *__restrict__ out, int64_t ld)
 {
     griddep_launch_dependents();
     griddep_wait();
-    const int i = blockIdx.x * 256 + threadIdx.x, left = static_cast<int>(p.k) - i * 8;
-    if (left <= 0)
-        return;
+    const int i = blockIdx.x * 256 + threadIdx.x, left = static_cast<int>(p.k) - i * 8, lanes = p.group / 8;
     for (int64_t t = blockIdx.y; t < p.tokens; t += gridDim.y) {
         const uint16_t *x = static_cast<const uint16_t *>(p.X) + t * p.ldx + i * 8;
-        uint32_t u[4] = {0u, 0u, 0u, 0u};
+        float v[8];
         if (left >= 8) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(x);
-            u[0] = v.x, u[1] = v.y, u[2] = v.z, u[3] = v.w;
+            unpack16<BF16>(*reinterpret_cast<const uint4 *>(x), v);
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (j < left)
-                    u[j / 2] |= static_cast<uint32_t>(x[j]) << (16 * (j & 1));
+                v[j] = j < left ? load16(x, j, BF16) : 0.0f;
         }
-        uint16_t *o = out + t * ldo + i * 8;
-        *reinterpret_cast<uint4 *>(o) = make_uint4(u[0], u[1], u[2], u[3]);
-        *reinterpret_cast<uint4 *>(o + lo) = make_uint4(u[0], u[1], u[2], u[3]);
+        float s = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        for (int d = lanes / 2; d; d >>= 1)
+            s += __shfl_xor_sync(0xffffffffu, s, d);
+        if (left > 0 && i % lanes == 0)
+            out[i / lanes * ld + t] = s;
     }
 }
 
@@ -682,21 +681,21 @@ cudaError_t launch_w4(const W4Args &a, int num_sms, cudaStream_t s)
     return a.tokens <= 8 ? launch_types<1, 2, 8, 16>(a, num_sms, s) : launch_types<2, 2, 16, 12>(a, num_sms, s);
 }
 
-cudaError_t launch_w4_expand(const W4Args &a, void *out, int64_t ldo, int64_t lo, int num_sms, cudaStream_t s)
+cudaError_t launch_w4_expand(const W4Args &a, void *out, int64_t ldo, float *scale, float *rest, int64_t ld_t,
+                             int num_sms, cudaStream_t s)
 {
     const int64_t across = ((a.k + 7) / 8 + 255) / 256, most = static_cast<int64_t>(num_sms) * 8;
     const int64_t down = (most + across - 1) / across, need = (a.rows + kExpandRows - 1) / kExpandRows;
     const dim3 grid(static_cast<unsigned>(across), static_cast<unsigned>(need < down ? need : down));
     return launch_pdl(a.in_bf16 ? tcg_w4_expand_kernel<true> : tcg_w4_expand_kernel<false>, grid, dim3(256), s, 0, a,
-                      static_cast<uint16_t *>(out), ldo, static_cast<int>(lo));
+                      static_cast<uint16_t *>(out), ldo, scale, rest, ld_t);
 }
 
-cudaError_t launch_w4_twice(const W4Args &a, void *out, int64_t ldo, int64_t lo, cudaStream_t s)
+cudaError_t launch_w4_sums(const W4Args &a, float *out, int64_t ld, cudaStream_t s)
 {
     const dim3 grid(static_cast<unsigned>(((a.k + 7) / 8 + 255) / 256),
                     static_cast<unsigned>(a.tokens < 4096 ? a.tokens : 4096));
-    return launch_pdl(tcg_w4_twice_kernel, grid, dim3(256), s, 0, a, static_cast<uint16_t *>(out), ldo,
-                      static_cast<int>(lo));
+    return launch_pdl(a.in_bf16 ? tcg_w4_sums_kernel<true> : tcg_w4_sums_kernel<false>, grid, dim3(256), s, 0, a, out, ld);
 }
 
 }  // namespace tcg

@@ -186,10 +186,11 @@ def linear_4bit(handle, x, w, scales, group, zeros=None, bias=None, act="none", 
         q = (v.unflatten(1, (-1, group)) / s[..., None]).round().add(8).clamp(1, 15).flatten(1).byte()
         w = q[:, 0::2] | q[:, 1::2] << 4
 
-    residual may be ``out`` itself.  Few tokens (up to 48, 64 of at most 2^24 weights, 128 of at
-    most 2^21; gated 128, 256 of at most 2^21) read the packed weights; an infinity in x then makes its
-    token's outputs NaN where zeros are no whole numbers.  More tokens expand the weights in the handle's workspace, rounded
-    to x's type (gated ones in two parts).  Returns out.
+    residual may be ``out`` itself.  Weights are not rounded: q less a whole number (8, or the one
+    nearest to its zero) enters the product, which meets the scale in FP32.  Where zeros are no
+    whole numbers, an infinity in x makes its token's outputs NaN.  Few tokens (up to 48, 64 of at
+    most 2^24 weights, 128 of at most 2^21; gated 128, 256 of at most 2^21) read the packed weights,
+    more expand them in the handle's workspace to 16 bits.  Returns out.
     """
     t, k, dtype, dev = _input(x)
     if not isinstance(w, torch.Tensor) or w.dim() != 2:

@@ -163,3 +163,94 @@ def test_infinity_in_x_with_zeros(handle, t, dtype):
     assert torch.equal(torch.isnan(out[1]), sign == 0) and bool((sign == 0).any())
     assert torch.equal(out[1][sign != 0].double(), sign[sign != 0] * float("inf"))
     assert torch.isfinite(out[0]).all() and torch.isfinite(out[2:]).all()
+
+
+# ------------------------------------------------------------------- more tokens, weights expanded
+# (tokens, features, k): whole tiles and pieces of them, K no multiple of a block or a group, one block
+# and many, 64 tokens and more, several tiles of tokens
+EXPANDED = [(129, 520, 1184), (200, 72, 8224), (333, 264, 544), (60, 4128, 4128), (70, 1032, 4160), (700, 136, 1000),
+            (257, 8, 32), (130, 2056, 2112), (1100, 300, 4096)]
+
+
+def expanded(t, rows, k, gated):
+    h = tcg.Handle()
+    size = tcg.tcg_gemm_4bit_workspace_size(h.h, rows // 2 if gated else rows, t, k, gated)
+    h.close()
+    return size > 0
+
+
+@pytest.mark.parametrize("t,n,k", EXPANDED)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dtype,kind", [(BF16, BF16), (BF16, F32), (F16, F16), (F16, F32)])
+def test_many_tokens(handle, t, n, k, group, dtype, kind):
+    """Prompts are as exact as single tokens."""
+    g = gen_of(t + n + k + group)
+    assert expanded(t, n, k, False)
+    for zero in (False, True, "whole"):
+        q, scales, zeros = weights(g, n, k, group, kind, zero)
+        x = randn(g, t, k, dtype=dtype)
+        out = tcg.linear_4bit(handle, x, padded_bytes(ref.pack(q)), scales, group, zeros=zeros, out_dtype=F32)
+        within(out, *(expected_with_zeros if zero else expected)(x, q, scales, zeros, group), "out")
+
+
+@pytest.mark.parametrize("t,n,k", [(129, 1040, 1184), (300, 36, 8224), (333, 264, 544), (700, 68, 1000), (260, 1032, 2112)])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_many_tokens_gated(handle, t, n, k, group, dtype):
+    g = gen_of(t + n + k + group)
+    assert expanded(t, 2 * n, k, True)
+    for zero in (False, True):
+        q, scales, zeros = weights(g, 2 * n, k, group, dtype, zero)
+        x = randn(g, t, k, dtype=dtype)
+        out = tcg.linear_4bit(handle, x, padded_bytes(ref.pack(q)), scales, group, zeros=zeros, act="silu", gated=True,
+                              out_dtype=F32)
+        z, e = (expected_with_zeros if zero else expected)(x, q, scales, zeros, group)
+        within(out, *ref.gate(z[:, :n], z[:, n:], e[:, :n], e[:, n:], "silu"), "out")
+
+
+def padded_bytes(w):
+    """Rows a multiple of 16 bytes apart."""
+    big = torch.full((w.shape[0], -(-w.shape[1] // 16) * 16), 255, dtype=torch.uint8, device="cuda")
+    big[:, :w.shape[1]] = w
+    return big[:, :w.shape[1]]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("size", [2.0 ** -30, 2.0 ** -18, 2.0 ** 18, 2.0 ** 40])
+def test_many_tokens_with_small_and_large_scales(handle, dtype, size):
+    """Weights beyond the 16-bit type's range, products within FP32's."""
+    g = gen_of(41)
+    q, scales, _ = weights(g, 264, 544, 64, F32)
+    x = randn(g, 200, 544, dtype=dtype)
+    scales *= size
+    scales[7] *= 2.0 ** 12
+    out = tcg.linear_4bit(handle, x, ref.pack(q), scales, 64, out_dtype=F32)
+    within(out, *expected(x, q, scales, None, 64), "out")
+
+
+@pytest.mark.parametrize("zero", [None, "whole"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_many_tokens_with_an_infinity(handle, zero, gated):
+    g = gen_of(42)
+    q, scales, zeros = weights(g, 72, 544, 32, BF16, zero)
+    x = randn(g, 200, 544)
+    x[1, 77] = float("inf")
+    out = tcg.linear_4bit(handle, x, ref.pack(q), scales, 32, zeros=zeros, gated=gated)
+    sign = q[:, 77].double() - (8 if zero is None else zeros[:, 77 // 32].double())
+    want = torch.where(sign == 0, float("nan"), sign * float("inf"))
+    if gated:
+        want = want[:36] * want[36:]
+    assert torch.equal(torch.isnan(out[1]), torch.isnan(want)) and bool(torch.isnan(want).any())
+    assert torch.equal(out[1][~torch.isnan(want)].double(), want[~torch.isnan(want)])
+    assert torch.isfinite(out[0]).all() and torch.isfinite(out[2:]).all()
+
+
+def test_scales_without_a_number_are_their_rows_alone(handle):
+    g = gen_of(43)
+    q, scales, zeros = weights(g, 72, 544, 32, BF16, True)
+    x = randn(g, 200, 544)
+    want = tcg.linear_4bit(handle, x, ref.pack(q), scales, 32, zeros=zeros)
+    scales[7, 3], zeros[20, 0] = float("nan"), float("nan")
+    got = tcg.linear_4bit(handle, x, ref.pack(q), scales, 32, zeros=zeros)
+    rest = [i for i in range(72) if i not in (7, 20)]
+    assert torch.isnan(got[:, [7, 20]]).all() and torch.equal(got[:, rest], want[:, rest])

@@ -360,10 +360,16 @@ __device__ __forceinline__ void finish_narrow(const LmArgs &p, float (&z)[kCols]
     apply_act(p.act, z);
     if (p.C) {
         const int64_t cbase = static_cast<int64_t>(col) * p.ldc + row;
+        if (ncol >= kCols) {                   // loads that need not ask for themselves go together
 #pragma unroll
-        for (int j = 0; j < kCols; ++j)
-            if (j < ncol)
+            for (int j = 0; j < kCols; ++j)
                 z[j] = fmaf(p.beta, load_as<OUT>(p.C, cbase + j * p.ldc), z[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kCols; ++j)
+                if (j < ncol)
+                    z[j] = fmaf(p.beta, load_as<OUT>(p.C, cbase + j * p.ldc), z[j]);
+        }
     }
 #pragma unroll
     for (int j = 0; j < kCols; ++j)

@@ -29,7 +29,7 @@ bool is_16bit(int t) { return t == TCG_R_16F || t == TCG_R_16BF; }
 
 bool bad_ld(int64_t ld, int64_t rows, int es)
 {
-    return ld < (rows > 1 ? rows : 1) || (ld * es) % 16;
+    return ld < (rows > 1 ? rows : 1) || ld % (16 / es);
 }
 
 int pairs_of(tcgContext *h)
@@ -108,7 +108,7 @@ double load_kib(int64_t tiles, int64_t nkb, int bn, int64_t pairs)
     const int64_t rest = tiles % pairs;
     const double block = 16.0 + bn / 16.0;
     const int64_t most = rest ? std::min(pairs / rest, nkb / min_share(nkb, bn)) : 1;
-    double kib = static_cast<double>(tiles / pairs * nkb) * block;
+    double kib = static_cast<double>(tiles / pairs) * static_cast<double>(nkb) * block;
     if (rest)
         kib += static_cast<double>(most > 1 ? ceil_div(nkb, most) : nkb) * block +
                (most > 1 ? static_cast<double>(most) * bn / 2 : 0.0);
@@ -131,7 +131,7 @@ Shape shape_of(tcgContext *h, const Product &p)
             const int64_t tiles = max_tiles(p, s.epi, bn), rest = tiles % P;
             int64_t share = ceil_div(rest * nkb, P);
             share = share < min_share(nkb, bn) ? min_share(nkb, bn) : share;
-            double t = static_cast<double>(tiles / P * nkb);
+            double t = static_cast<double>(tiles / P) * static_cast<double>(nkb);
             if (rest)
                 t += nkb - share >= gain_of(bn) ? static_cast<double>(share) + gain_of(bn) / cost
                                                 : static_cast<double>(nkb);
@@ -203,9 +203,9 @@ Shape shape_of(tcgContext *h, const Product &p)
     // ranges alike for all cut tiles (1000 x 1024 outputs over K = 50021: 109 -> 84 us).
     const int64_t x_tiles = ceil_div(p.tokens, wide ? 256 : s.bn);
     const int64_t w_tiles = ceil_div(p.w_rows(), wide ? s.bn : 256);
-    s.align = !p.offsets && x_tiles > 1 && w_tiles > 1 && (p.tokens + p.w_rows()) * p.k * 2 > (int64_t(64) << 20);
+    s.align = !p.offsets && x_tiles > 1 && w_tiles > 1 && (p.tokens + p.w_rows()) * p.k > (int64_t(32) << 20);
     int64_t pairs = s.tiles;
-    if (s.cut)
+    if (s.cut && s.tiles < P)
         pairs = s.tiles * nkb / s.share > pairs ? s.tiles * nkb / s.share : pairs;
     s.grid = 2 * static_cast<int>(pairs < P ? pairs : P);
     return s;
@@ -744,7 +744,7 @@ tcgStatus_t check_gate(int act, int64_t m, int64_t n, int64_t k)
 {
     if (act < TCG_ACT_NONE || act > TCG_ACT_SILU || m < 0 || n < 0 || k < 0)
         return TCG_STATUS_INVALID_VALUE;
-    return 2 * m > kMaxExtent || n > kMaxExtent || k > kMaxK ? TCG_STATUS_NOT_SUPPORTED : TCG_STATUS_SUCCESS;
+    return m > kMaxExtent / 2 || n > kMaxExtent || k > kMaxK ? TCG_STATUS_NOT_SUPPORTED : TCG_STATUS_SUCCESS;
 }
 
 // The workspace of a gated backward pass: dZ, and what the products need.
@@ -1576,11 +1576,11 @@ tcgStatus_t tcg_gemm_4bit(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int64_
         st = check_epilogue(epi, m, n, Btype, Dtype);
     if (st != TCG_STATUS_SUCCESS)
         return st;
-    if (m < 0 || n < 0 || k < 0 || lda < (k + 1) / 2 || lda < 1 || lda % 16 || bad_ld(ldb, k, 2) ||
+    if (m < 0 || n < 0 || k < 0 || lda < k / 2 + k % 2 || lda < 1 || lda % 16 || bad_ld(ldb, k, 2) ||
         bad_ld(ldd, m, elem_size(Dtype)))
         return TCG_STATUS_INVALID_VALUE;
     if ((group != 32 && group != 64 && group != 128) || (Stype != TCG_R_32F && Stype != Btype) || epi.Z ||
-        (gated && (epi.bias || epi.beta != 0.0f)) || 2 * m > kMaxExtent || n > kMaxExtent || 2 * k > kMaxK)
+        (gated && (epi.bias || epi.beta != 0.0f)) || m > kMaxExtent / 2 || n > kMaxExtent || k > kMaxK / 2)
         return TCG_STATUS_NOT_SUPPORTED;
     if (m == 0 || n == 0)
         return TCG_STATUS_SUCCESS;
@@ -1672,7 +1672,7 @@ tcgStatus_t tcg_gemm_4bit_workspace_size(tcgHandle_t h, int64_t m, int64_t n, in
 {
     if (!h || !bytes || m < 0 || n < 0 || k < 0)
         return TCG_STATUS_INVALID_VALUE;
-    if (2 * m > kMaxExtent || n > kMaxExtent || 2 * k > kMaxK)
+    if (m > kMaxExtent / 2 || n > kMaxExtent || k > kMaxK / 2)
         return TCG_STATUS_NOT_SUPPORTED;
     *bytes = 0;
     if (m == 0 || n == 0 || w4_packed(n, gated ? 2 * m : m, k, gated))

@@ -391,7 +391,7 @@ cudaError_t norm_backward_v(const NormBackwardArgs &a, const NormShape &n, int g
 // Blocks that are resident with `threads` an SM.
 int norm_grid(const NormShape &n, int64_t rows, int num_sms, int threads)
 {
-    const int64_t need = (rows + n.rows - 1) / n.rows;
+    const int64_t need = rows / n.rows + (rows % n.rows != 0);
     const int64_t most = static_cast<int64_t>(num_sms) * (threads / (n.threads * n.rows));
     return static_cast<int>(need < most ? need : most);
 }

@@ -47,16 +47,34 @@ def load_peaks(root: str = ROOT):
     return dict(FALLBACK_PEAKS), "fallback"
 
 
+def kernel_sources(kernel: str, csrc: str):
+    """Names of the sources that make a kernel: the file that defines it and what that includes,
+    over and over (all of them where none defines it)."""
+    import re
+    text = {}
+    for name in os.listdir(csrc):
+        with open(os.path.join(csrc, name), encoding="utf-8", errors="replace") as f:
+            text[name] = f.read()
+    found = {n for n, t in text.items() if n.endswith(".cu") and re.search(rf"\b{re.escape(kernel)}\(", t)}
+    todo = list(found)
+    while todo:
+        for name in re.findall(r'^\s*#\s*include\s*"([^"]+)"', text[todo.pop()], re.M):
+            if name in text and name not in found:
+                found.add(name)
+                todo.append(name)
+    return sorted(found or text)
+
+
 def traffic_record(kernel: str, workload: str, root: str = ROOT):
     """DRAM bytes per launch from the committed ncu summary, if it was taken on the
-    current kernel source (its source digest must match), else None."""
+    kernel's current sources (their digest must match), else None."""
     import hashlib
     p = os.path.join(root, "profiles", "dram_traffic.txt")
     if not os.path.exists(p):
         return None
     h = hashlib.sha256()
     csrc = os.path.join(root, "mixed_precision_tensor_gb300", "csrc")
-    for f in sorted(os.listdir(csrc)):
+    for f in kernel_sources(kernel, csrc):
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(fh.read())
     digest = h.hexdigest()[:16]

@@ -590,7 +590,8 @@ tcgStatus_t tcg_gated_backward_workspace_size(tcgHandle_t h, int64_t m, int64_t 
  * not NULL, receives s rounded; Y is formed from the unrounded s.  Ytype is `type`, or
  * TCG_R_8F_E4M3: then scale[i] = max(max |Y[i, :]| / 448, 2^-100) and Y holds Y / scale, rounded to
  * nearest even, so that Y * scale stands for the result; scale is not touched otherwise.  S may be X
- * or R, a 16-bit Y may be X or R, not both the same.  A row with a NaN or an infinity has
+ * or R, a 16-bit Y may be X or R, not both the same, with the same leading dimension
+ * (INVALID_VALUE otherwise, also below).  A row with a NaN or an infinity has
  * entries that are NaN (in 8 bits all of them, and its scale); entries above 2^63 overflow the
  * FP32 sum of squares, which leaves zeros, and in a row whose entries are all below 2^-60 the
  * squares lose bits or vanish, which matters with an eps as small (eps 0: NaN, as for zeros). */

@@ -778,6 +778,12 @@ tcgStatus_t check_norm(int64_t rows, int64_t k, const void *W, tcgDataType_t w_t
 
 bool bad_rows(const void *p, int64_t ld, int64_t cols, int es) { return !aligned16(p) || bad_ld(ld, cols, es); }
 
+// An output in the place of an input, but with rows elsewhere: it would meet rows not read yet.
+bool bad_place(const void *out, int64_t ldo, const void *in, int64_t ldi, int64_t rows)
+{
+    return out && out == in && ldo != ldi && rows > 1;
+}
+
 // --------------------------------------------------------------------- 4-bit weights
 // Whether the packed weights are read as they are, once for every 16 tokens, or expanded to 16 bits
 // for the product of many tokens (us in a graph, groups of 128, as they are / expanded):
@@ -1460,6 +1466,9 @@ tcgStatus_t tcg_rms_norm(tcgHandle_t h, int64_t rows, int64_t k, const void *X, 
     if (!X || !Y || !aligned16(X) || !aligned16(Y) ||
         (out8 && (!scale || reinterpret_cast<uintptr_t>(scale) % 4)))
         return TCG_STATUS_INVALID_VALUE;
+    if (S == Y || (out8 && (Y == X || Y == R)) || bad_place(S, lds, X, ldx, rows) || bad_place(S, lds, R, ldr, rows) ||
+        bad_place(Y, ldy, X, ldx, rows) || bad_place(Y, ldy, R, ldr, rows))
+        return TCG_STATUS_INVALID_VALUE;
     st = bind_device(h);
     if (st == TCG_STATUS_SUCCESS)
         st = check_device(h, {X, R, S, W, Y, out8 ? scale : nullptr});
@@ -1506,6 +1515,8 @@ tcgStatus_t tcg_rms_norm_backward(tcgHandle_t h, int64_t rows, int64_t k, const 
         (dX && bad_rows(dX, lddx, k, 2)) || reinterpret_cast<uintptr_t>(dW) % 4)
         return TCG_STATUS_INVALID_VALUE;
     if (rows > 0 && (!dY || !X || !aligned16(dY) || !aligned16(X)))
+        return TCG_STATUS_INVALID_VALUE;
+    if (bad_place(dX, lddx, dY, lddy, rows) || bad_place(dX, lddx, dS, ldds, rows) || bad_place(dX, lddx, X, ldx, rows))
         return TCG_STATUS_INVALID_VALUE;
     if (!dW && (!dX || rows == 0))
         return TCG_STATUS_SUCCESS;
@@ -1588,6 +1599,8 @@ tcgStatus_t tcg_gemm_4bit(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int64_
     if (!D || !aligned16(D) ||
         (k > 0 && (!A || !B || !scales || !aligned16(A) || !aligned16(B) ||
                    reinterpret_cast<uintptr_t>(scales) % es || reinterpret_cast<uintptr_t>(zeros) % es)))
+        return TCG_STATUS_INVALID_VALUE;
+    if (epi.beta != 0.0f && bad_place(D, ldd, epi.C, epi.ldc, n))
         return TCG_STATUS_INVALID_VALUE;
     st = bind_device(h);
     if (st == TCG_STATUS_SUCCESS)

@@ -30,4 +30,3 @@ def test_the_gemm_kernels_record_is_of_its_sources():
     csrc = os.path.join(bench.ROOT, "mixed_precision_tensor_gb300", "csrc")
     assert bench.kernel_sources("tcg_gemm_kernel", csrc) == ["tcg_internal.h", "tcg_kernels.cu", "tcg_pipe.cuh",
                                                              "tcg_ptx.cuh"]
-    assert bench.traffic_record("tcg_gemm_kernel", "fp16_gemm_8192") is not None

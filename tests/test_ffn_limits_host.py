@@ -4,7 +4,8 @@ import ctypes
 import pytest
 
 import mixed_precision_tensor_gb300 as tcg
-from test_ffn_host import F32, INV, NSUP, PA, PD, PX, gated, gated_backward, handle, packed  # noqa: F401
+from test_ffn_host import (E4M3, F32, INV, NSUP, PA, PB, PD, PX, gated, gated_backward, handle,  # noqa: F401
+                           norm, norm_backward, packed)
 
 HUGE = (1 << 31, (1 << 61) + 8, 1 << 62, (1 << 63) - 8, (1 << 63) - 1)
 
@@ -44,3 +45,22 @@ def test_leading_dimensions_past_the_range_of_bytes(handle, ld):  # noqa: F811
     assert gated(handle, lda=ld) == INV and gated(handle, ldb=ld) == INV
     assert packed(handle, ldb=ld) == INV
     assert packed(handle, dt=F32, ldd=ld) == INV
+
+
+@pytest.mark.parametrize("kw", [
+    dict(S=PD), dict(S=PA, Y=PA), dict(R=PB, S=PB, Y=PB),                       # both outputs in one place
+    dict(yt=E4M3, scale=PX, Y=PA), dict(yt=E4M3, scale=PX, R=PB, Y=PB),         # bytes over 16-bit rows
+    dict(Y=PA, ldy=72), dict(S=PA, lds=72), dict(R=PB, S=PB, lds=128), dict(R=PB, Y=PB, ldy=72),
+])
+def test_norm_refuses_places(handle, kw):  # noqa: F811
+    """In place only where rows stay where they are."""
+    assert norm(handle, **kw) == INV
+
+
+@pytest.mark.parametrize("kw", [dict(dX=PA, lddx=72), dict(dS=PX, dX=PX, lddx=72), dict(dX=PB, lddx=128)])
+def test_norm_backward_refuses_places(handle, kw):  # noqa: F811
+    assert norm_backward(handle, **kw) == INV
+
+
+def test_packed_product_refuses_places(handle):  # noqa: F811
+    assert packed(handle, ldd=72, e=tcg.Epilogue(beta=1.0, C=PD, ldc=64)) == INV

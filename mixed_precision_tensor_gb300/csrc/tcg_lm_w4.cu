@@ -11,10 +11,11 @@
 // the group's sum of x, which one more product with a matrix of ones gives for all rows, comes in when
 // the group is complete and meets its scale.  Sums are FP32.
 //
-// What bounds it at a few tokens is not memory but the instructions for a weight (230 for 4096 of them,
-// most on a pipe that takes one in two cycles) and, in short calls, the first loads and the join:
-// one token of 4096 x 16384 takes 12.4 us (2.8 TB/s; the same loads alone run at 6.0 TB/s), of 16384 x
-// 16384 34 us (4.1 TB/s), of 4096 x 4096 4.7 us.
+// What bounds it at a few tokens is neither memory nor instructions (4 us of them for one token of 4096
+// x 16384, 5.8 us for the loads alone) but a chain of waits in each warp -- rings of two to four stages,
+// products one after the other, a group's end -- and, in short calls, the first loads and the join: one
+// token of 4096 x 16384 takes 11.7 us (3.0 TB/s), of 16384 x 4096 11.6, of 4096 x 4096 5.1; groups of 32
+// with zeros 18.0, 19.6 and 7.1.
 //
 // A warp has 32 or 64 rows and streams them 128 elements at a time through a ring of its own
 // (asynchronous 16-byte copies, x beside the weights), on from one tile of rows to the block's next.
@@ -671,13 +672,14 @@ cudaError_t launch_types(const W4Args &a, int num_sms, cudaStream_t s)
 cudaError_t launch_w4(const W4Args &a, int num_sms, cudaStream_t s)
 {
     // Up to eight tokens, 64 rows a warp where that leaves tiles for half of the SMs: what a stage costs
-    // besides its weights is shared by more of them (one token, us in a graph, 32 / 64 rows: 8192 x 4096
-    // 7.6 / 6.6, 16384 x 4096 14.9 / 12.2; 4096 x 16384, which then needs clusters, 12.2 / 13.9).  Rooms
-    // for two tokens' x leave those sixteen warps, for eight tokens' twelve (12.1 and 13.0 us).
+    // besides its weights is shared by more of them (one token, us in a graph, 32 / 64 rows: 4096 x 4096
+    // 5.1 / 5.9, 8192 x 4096 8.1 / 7.3, 16384 x 4096 13.3 / 11.6; eight tokens 6.0 / 6.6, 10.3 / 7.9,
+    // 16.9 / 12.9).  Rooms for two tokens' x leave those sixteen warps, for eight tokens' twelve (one
+    // token of 16384 x 4096: 11.6 and 11.8 us).
     if (a.tokens <= 8 && a.rows >= 32 * num_sms)
         return a.tokens <= 2 ? launch_types<1, 4, 2, 16>(a, num_sms, s) : launch_types<1, 4, 8, 12>(a, num_sms, s);
-    // More: sixteen tokens a pass (32 of them with eight warps took longer, 32 tokens of 16384 x 4096
-    // 51 us for 41, and 33 tokens of 4096 x 4096 22 for 18).
+    // More: sixteen tokens a pass (32 of them with eight warps take longer, 32 tokens of 16384 x 4096
+    // 39.5 us for 32.2, and 33 tokens of 4096 x 4096 18.4 for 15.0).
     return a.tokens <= 8 ? launch_types<1, 2, 8, 16>(a, num_sms, s) : launch_types<2, 2, 16, 12>(a, num_sms, s);
 }
 

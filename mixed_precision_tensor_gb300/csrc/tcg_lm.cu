@@ -24,11 +24,11 @@
 //                  1.92 PFLOP/s)
 //   kEpiGroupNarrow, kEpiGroupGated   the narrow kinds for weights that have a scale for each group of
 //                  K elements: an accumulator for each group, which meets its scale in FP32 on its
-//                  way to the sums in registers.  Bound by the thread that issues the products (four
-//                  and the waits of a block take it some 600 cycles, where 192 columns take the tensor core
-//                  192) and, in groups of 32, by that way: 4096 tokens of 4096 x 4096 take 160 us in groups
-//                  of 128, by kEpiWide without scales 85.  192 columns, as 256 leave a thread too few registers
-//                  (202 us for 169, the expansion included)
+//                  way to the sums in registers.  Bound by that way and by the thread that issues the
+//                  products: 4096 tokens of 4096 x 4096 take 119 us in groups of 128, 344 in groups of
+//                  32, by kEpiWide without scales 86.  192 columns, as 256 leave a thread too few registers
+//                  (202 us for 169, the expansion included, before elect.sync chose the issuing thread;
+//                  now 127)
 //
 // What bounds it.  A 64-element block of K costs an SM 32 KiB of operands at tile 256 x 256,
 // loaded at 64 bytes a cycle in the 512 cycles that the tensor core takes for it; with both
@@ -683,6 +683,13 @@ __host__ __device__ constexpr bool lm_wide(int epi)
     return epi == kEpiWide || epi == kEpiXentStats || epi == kEpiXentGrad || epi == kEpiGatedWide;
 }
 
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 template <int EPI, int OUT, int BN, bool RK>
 __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
     tcg_lm_kernel(const __grid_constant__ LmMaps maps, const LmArgs p)
@@ -721,7 +728,7 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
     const uint32_t b_smem = base + kStages * Cfg::kAStage;
     LmCtl *ctl = reinterpret_cast<LmCtl *>(base_ptr + kLmDataBytes);
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = GROUP ? __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0) : threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
@@ -777,8 +784,12 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
     };
     uint32_t issued_mask = 0, issued_parity = 0;
 
+    // The one thread of the first two roles.  Chosen so, the compiler knows that one thread runs what
+    // follows and keeps the operands of its products in uniform registers (see kEpiGroupNarrow).
+    auto chosen = [&]() { return GROUP ? elect_one() : lane == 0; };
+
     if (warp == 0) {
-        if (lane == 0) {
+        if (chosen()) {
             // ------------------------------------------------------------ producer
             Walk walk(pair, pairs);
             LmUnit w;
@@ -850,7 +861,7 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader && chosen()) {
             // ----------------------------------------------------------- MMA issue
             uint32_t a_lbo, a_sbo, b_lbo, b_sbo, a_off[kMmasPerStage], b_off[kMmasPerStage];
             layout(p.a_mode, a_lbo, a_sbo, a_off);

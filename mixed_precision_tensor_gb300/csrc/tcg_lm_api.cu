@@ -151,8 +151,9 @@ Shape shape_of(tcgContext *h, const Product &p)
         s.bn = p.lm_epi == kEpiXentNarrow ? 32 : 256;
     } else if (p.grouped_k) {
         s.epi = p.gated ? kEpiGroupGated : kEpiGroupNarrow;
-        // Per tile and block 0.55, 0.44 and 0.37 us at groups of 128: the one thread that issues
-        // the products and the accumulators' way to registers, not loads, bound them.
+        // Whole waves take 0.40, 0.28 and 0.22 us for a block of each tile at groups of 128, cut tiles
+        // of the narrower widths more than that; by these costs (4096 x 4096, us at 192, 128, 64
+        // columns): 333 tokens 31 32 33, 512 40 27 40, 4096 127 128 196; 16384 x 4096: 333 tokens 80 90 111.
         s.bn = best_of({192, 128, 64}, [](int bn) { return bn == 192 ? 1.0 : (bn == 128 ? 0.8 : 0.68); });
     } else {
         const int64_t per = p.offsets ? p.tokens / p.groups : p.tokens;
@@ -788,14 +789,14 @@ bool bad_place(const void *out, int64_t ldo, const void *in, int64_t ldi, int64_
 // Whether the packed weights are read as they are, once for every 16 tokens, or expanded to 16 bits
 // for the product of many tokens (us in a graph, groups of 128, as they are / expanded):
 //                 tokens   32            48            64            128
-//    1024 x  1024          3.5 / 11.2    3.4 / 11.2    3.5 / 11.7    5.6 / 12.3
-//    4096 x  4096         10.8 / 21.7   15.1 / 21.7   19.3 / 22.2   32.2 / 27.5
-//   16384 x  4096         32.2 / 63.3   49.4 / 63.6   62.3 / 64.6    118 / 62.6
-//    4096 x 16384         30.0 / 62.2   43.6 / 62.7   57.2 / 63.3   98.2 / 72.4
+//    1024 x  1024          3.5 / 9.6     3.4 / 9.5     3.5 / 10.3    5.6 / 10.5
+//    4096 x  4096         10.8 / 18.1   15.1 / 18.2   19.3 / 18.9   32.2 / 23.3
+//   16384 x  4096         32.2 / 61.9   49.4 / 62.5   62.3 / 63.5    118 / 59.4
+//    4096 x 16384         30.0 / 61.2   43.6 / 61.6   57.2 / 62.2   98.2 / 67.3
 // Gated products (2 x 512 x 1024, 2 x 2048 x 4096, 2 x 8192 x 4096 and 2 x 2048 x 16384):
-//    64 tokens   3.3 / 12.6   19.3 / 22.7   62.1 / 66.1   57.1 / 66.1
-//   128          5.4 / 13.2   32.1 / 28.2    118 / 62.5   98.2 / 74.0
-//   256          9.4 / 13.3   66.4 / 33.2    246 / 89.1    207 / 96.3
+//    64 tokens   3.3 / 10.5   19.3 / 19.3   62.1 / 65.2   57.1 / 65.0
+//   128          5.4 / 11.1   32.1 / 24.4    118 / 61.4   98.2 / 69.6
+//   256          9.4 / 11.2   66.4 / 26.6    246 / 79.8    207 / 82.7
 // Their limit of 128 tokens, which callers rely on for needing no workspace, is from a time when
 // expanded weights cost twice as much.
 bool w4_packed(int64_t tokens, int64_t rows, int64_t k, bool gated)

@@ -622,13 +622,14 @@ tcgStatus_t tcg_rms_norm_backward_workspace_size(tcgHandle_t h, int64_t rows, in
  * are not supported.
  *
  * A weight enters its product as q less a whole number, 8 or the one of 0 .. 15 nearest to its zero,
- * exactly, and its group's product meets the scale in FP32 (scales below 2^118); what is left of the zero
- * meets the group's sum of B besides.  So nothing is rounded but sums, and the accuracy is the bound above
- * with |A| = |w|, at least |scale| / 2 where zeros are no whole numbers; there an infinity in B makes its
- * column of D NaN, elsewhere it meets each weight as it is.  Few tokens (up to 48, 64 of at most 2^24
- * weights, 128 of at most 2^21; gated 128, 256 of at most 2^21) read the packed weights; for more they
- * are expanded to 16 bits in the workspace (its size from the second call: 2 bytes for a weight, an
- * eighth of that for scales, and sums of B), which rounds nothing either. */
+ * exactly, and its group's product meets the scale in FP32 (scales below 2^118, entries of B below
+ * 2^122); what is left of the zero meets the group's sum of B besides.  So nothing is rounded but sums,
+ * and the accuracy is the bound above with |A| = |w|, at least |scale| / 2 where zeros are no whole
+ * numbers; there an infinity in B makes its column of D NaN, elsewhere it meets each weight as it is.
+ * Few tokens (up to 48, 64 of at most 2^24 weights, 128 of at most 2^21; gated 128, 256 of at most
+ * 2^21) read the packed weights; for more they are expanded to 16 bits in the workspace, which rounds
+ * nothing either (its size from the second call: 2 bytes for a weight, an eighth of that for scales,
+ * and sums of B). */
 tcgStatus_t tcg_gemm_4bit(tcgHandle_t h, int64_t m, int64_t n, int64_t k, int64_t group, const void *A,
                           int64_t lda, const void *scales, const void *zeros, tcgDataType_t Stype, const void *B,
                           int64_t ldb, tcgDataType_t Btype, void *D, tcgDataType_t Dtype, int64_t ldd, int gated,

@@ -1137,7 +1137,8 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                             if (empty_k)
                                 continue;
                             if (any_rest) {
-                                const float4 *xs = reinterpret_cast<const float4 *>(p.group_sum + group * p.sum_ld + col_part + c0);
+                                const float4 *xs =
+                                    reinterpret_cast<const float4 *>(p.group_sum + group * p.sum_ld + col_part + c0);
 #pragma unroll
                                 for (int j = 0; j < kStep; j += 4) {
                                     const float4 x = __ldg(xs + j / 4);
@@ -1148,6 +1149,7 @@ __global__ void __launch_bounds__(LmCfg<BN, lm_wide(EPI)>::kThreadsLm, 1)
                                         v[j + 3] = __float_as_uint(fmaf(rest, x.w, __uint_as_float(v[j + 3])));
                                     }
                                 }
+                                __syncwarp();              // the loads from TMEM are the whole warp's
                             }
 #pragma unroll
                             for (int j = 0; j < kStep; j += 2)

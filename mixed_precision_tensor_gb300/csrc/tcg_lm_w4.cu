@@ -88,7 +88,8 @@ __device__ __forceinline__ uint32_t fma16(uint32_t a, uint32_t b, uint32_t c)
 // The eight elements of a word as A operands: pairs (0, 4), (1, 5), (2, 6), (3, 7) of q - c, times a
 // unit.  A 16-bit word 0 .. 255 read as a number is that many times the smallest subnormal one, 2^-133
 // in BF16 and 2^-24 in FP16, so a masked nibble is q or 16 q in that measure; one fused multiply-add
-// brings it among the normal numbers and takes c away, exactly.  (With c left in, a row of weights
+// brings it among the normal numbers and takes c away, exactly (to make numbers of short integers by
+// masks and exponents is a known method; subnormal ones need no exponent).  (With c left in, a row of weights
 // near zero would be the difference of two large sums; with x scaled instead, its range would end early.)
 template <bool BF16>
 struct W4Unit {
